@@ -404,6 +404,180 @@ int mlpblk_moe_backward_overwrite(const mlpblk_moe_desc *desc,
                                   void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Tokens sorted by expert and back ("Kernel 4: Routed ReLU2 MoE": select, execute,
+ * weight and combine), for programs that bring expert networks of their own; the
+ * routed block above does the same inside mlpblk_moe_forward.  The dispatch is given.
+ *
+ * Entry i = t * top_k + j is slot j of token t.  Expert e's entries, in increasing
+ * i, take the rows seg[e] .. seg[e] + count[e] of the sorted order; segments
+ * follow one another in expert order and each is padded to a multiple of
+ * desc->pad rows.  An id outside [0, experts) selects nothing; a token may name an
+ * expert more than once.
+ *
+ * mlpblk_moe_sort_rows: R, the number of rows that the sorted buffers hold, an upper
+ *   bound of seg[experts] for any ids: T*k + min(experts, T*k) * (pad - 1), rounded
+ *   up to a multiple of pad.  -1 for an invalid descriptor, 0 for tokens = 0.
+ * mlpblk_moe_sort: the plan, one launch, no workspace.
+ *     in : expert_idx[T,k]
+ *     out: count[E], seg[E+1], pos[T,k] = the entry's row or -1,
+ *          row_map[R] = the row's entry i, or -1 for padding and for the rows at
+ *          or behind seg[E]                                          (all written)
+ * mlpblk_moe_permute: rows[pos[t,j]] = x[t]; padding rows inside the segments are
+ *   zero.  Rows at or behind seg[E] are left as they were.
+ * mlpblk_moe_permute_backward: dx[t] = sum_j d_rows[pos[t,j]], in slot order
+ *   (slots that select nothing add nothing; the padding rows are not read).
+ * mlpblk_moe_unpermute: y[t] = residual[t] + sum_j weights[t,j] * rows[pos[t,j]], in
+ *   slot order; residual NULL adds nothing, weights NULL weighs each slot by 1; y
+ *   may be residual itself.
+ * mlpblk_moe_unpermute_backward: d_rows[pos[t,j]] = weights[t,j] * dy[t] (padding
+ *   rows zero, rows at or behind seg[E] left as they were) and
+ *   d_weights[t,j] = <dy[t], rows[pos[t,j]]> (0 for a slot that selects nothing).
+ *   The gradient of residual is dy.  weights NULL weighs by 1; with d_weights NULL
+ *   rows is not read and may be NULL.
+ *
+ * x, y, dx, dy, residual [T, width] and rows, d_rows [R, width] are in
+ * desc->dtype, weights and d_weights float32, the rest int32.  Sums are held in
+ * float32 and rounded once; their order is fixed.  Any width; rows of a multiple
+ * of 16 bytes move in 16-byte accesses.  pos, count and seg are those that
+ * mlpblk_moe_sort wrote for the same descriptor.  Limits: experts 1..256, top_k
+ * 1..256, pad 1..1024, R < 2^31.  Pointers are device pointers, 16-byte aligned.
+ * Outputs alias no input (MLPBLK_EINVAL) but where stated.  Each returns an
+ * MLPBLK_* code; tokens = 0 returns MLPBLK_OK and touches nothing, except that
+ * mlpblk_moe_sort still writes count and seg (zeros).
+ */
+typedef struct {
+    int64_t tokens;   /* T >= 0                                       */
+    int64_t width;    /* elements of a row, >= 1                       */
+    int32_t experts;  /* E                                             */
+    int32_t top_k;    /* k                                             */
+    int32_t pad;      /* segments are padded to a multiple of this      */
+    int32_t dtype;    /* of the rows: MLPBLK_BF16 or MLPBLK_FP32        */
+} mlpblk_sort_desc;
+
+int64_t mlpblk_moe_sort_rows(const mlpblk_sort_desc *desc);
+
+int mlpblk_moe_sort(const mlpblk_sort_desc *desc, const int32_t *expert_idx, int32_t *count, int32_t *seg,
+                    int32_t *pos, int32_t *row_map, void *stream);
+
+int mlpblk_moe_permute(const mlpblk_sort_desc *desc, const void *x, const int32_t *pos, const int32_t *count,
+                       const int32_t *seg, void *rows, void *stream);
+
+int mlpblk_moe_permute_backward(const mlpblk_sort_desc *desc, const void *d_rows, const int32_t *pos, void *dx,
+                                void *stream);
+
+int mlpblk_moe_unpermute(const mlpblk_sort_desc *desc, const void *rows, const int32_t *pos, const float *weights,
+                         const void *residual, void *y, void *stream);
+
+int mlpblk_moe_unpermute_backward(const mlpblk_sort_desc *desc, const void *dy, const void *rows,
+                                  const int32_t *pos, const int32_t *count, const int32_t *seg,
+                                  const float *weights, void *d_rows, float *d_weights, void *stream);
+
+/*
+ * MXFP4: microscaled 4-bit matrices and their product ("Where Quantization Fits";
+ * the format is the OCP Microscaling Formats specification's MXFP4).  32
+ * consecutive values of a row share one power-of-two scale (E8M0, a byte: the
+ * exponent plus 127) and are kept as E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives).
+ *
+ * Rounding: scale exponent = floor(log2(max |v| of the block)) - 2, at least -127;
+ * codes are v / scale rounded to nearest even and saturated at 6.  A block that
+ * holds an infinity or a NaN gets the scale byte 255 and reads back as NaN.  A
+ * block of zeros has scale byte 0.
+ *
+ * A quantised matrix Q[rows, cols] is two buffers, `batch` matrices back to back
+ * in each (every expert's weights, say):
+ *   codes : rows of ceil(cols / 32) * 16 bytes, two values a byte, the even column in
+ *           the low half; columns behind cols are zero codes
+ *   scales: tiles of 128 rows x 4 blocks (128 columns), 512 bytes each; the byte of
+ *           row r, block b inside a tile is (r % 32) * 16 + (r / 32) * 4 + b (the
+ *           order in which the tensor core's scale copies want them); the tiles of
+ *           128 rows follow one another along the columns, 2 * ceil(cols / 256) of
+ *           them (an even count; bytes of rows and blocks that do not exist are 0)
+ *
+ * mlpblk_fp4_codes_size, mlpblk_fp4_scales_size: their bytes; 0 for an invalid
+ *   descriptor.
+ * mlpblk_fp4_quantize: Q = x, or with desc->transposed Q = x^T of a source stored
+ *   [cols, rows] (blocks of 32 along the source's columns; the operands of a
+ *   weight gradient).  desc->act = MLPBLK_FP4_ACT_RELU2 quantises relu(x)^2
+ *   (computed in float32).  desc->dtype is x's type.  row_map (NULL: none; a
+ *   device array of one int per source row, e.g. the one mlpblk_moe_sort wrote)
+ *   maps the source's rows: where row_map[r] < 0 row r is zeros and x is not read
+ *   there, otherwise it is x's row row_map[r] / map_div for map_div > 0, and
+ *   x's row r for map_div = 0.  With transposed the mapped rows are Q's columns.
+ *   row_map needs batch = 1.  Every byte of codes and scales is written.
+ * mlpblk_fp4_dequantize: y[batch, rows, cols] in desc->dtype (exact in both types).
+ *   transposed and act must be 0.
+ * Limits: rows, cols >= 0 (with either 0: MLPBLK_OK, nothing is touched),
+ * rows * batch and cols < 2^31; pointers 16-byte aligned.
+ */
+#define MLPBLK_FP4_ACT_NONE   0
+#define MLPBLK_FP4_ACT_RELU2  1
+
+typedef struct {
+    int64_t rows, cols;   /* of Q                                         */
+    int32_t batch;        /* matrices, >= 1                               */
+    int32_t dtype;        /* of x or y: MLPBLK_BF16 or MLPBLK_FP32         */
+    int32_t transposed;   /* 1: the source is stored [cols, rows]          */
+    int32_t act;          /* MLPBLK_FP4_ACT_*                              */
+} mlpblk_fp4_desc;
+
+size_t mlpblk_fp4_codes_size(const mlpblk_fp4_desc *desc);
+size_t mlpblk_fp4_scales_size(const mlpblk_fp4_desc *desc);
+
+int mlpblk_fp4_quantize(const mlpblk_fp4_desc *desc, const void *x, const int32_t *row_map, int32_t map_div,
+                        void *codes, void *scales, void *stream);
+
+int mlpblk_fp4_dequantize(const mlpblk_fp4_desc *desc, const void *codes, const void *scales, void *y,
+                          void *stream);
+
+/*
+ * Products of MXFP4 matrices on the tensor cores (tcgen05 kind::mxf4, float32
+ * accumulators), no workspace.  C is dense, row-major, in out_dtype;
+ * accumulate = 1 (float32 only) adds into C, the gradient rule of this library, 0
+ * sets it.  Each output has one fixed order of summation.
+ *
+ * mlpblk_fp4_matmul: C[m,n] = A[m,k] . B[n,k]^T (k: the quantised columns).  The
+ *   three products of a linear layer y = x W^T: y from Q(x), Q(W); dx from
+ *   Q(dy), Q(W^T); dW from Q(dy^T), Q(x^T).
+ * mlpblk_fp4_matmul_grouped: the experts' products in sorted order.  A [m = R, k]
+ *   holds the sorted rows, B is a batch of `experts` matrices [n, k]; for every
+ *   row r of expert e's rows, C[r] = A[r] . B[e]^T.  Padding rows of a segment are
+ *   either left as they were or get A's padding row times B[e]^T; rows at or
+ *   behind seg[E] are left as they were.  pad (that of the sort) is a multiple of 128.
+ * mlpblk_fp4_wgrad_grouped: the experts' weight gradients.  A [m, k = R] and B
+ *   [n, k = R] are quantised along the sorted order (transposed, with the
+ *   row_map, so that padding is zero); C[e][m,n] = the sum over expert e's
+ *   segment, zero (or nothing added) for an expert without rows.  pad is a
+ *   multiple of 256.
+ * count and seg are those of mlpblk_moe_sort.  With m = 0 (wgrad_grouped: k = 0, not
+ * accumulating: C is still set to zero) nothing is touched.  Limits: m, n, k and
+ * experts * n (wgrad: experts * m) < 2^31, experts 1..256; experts and pad are 0 for
+ * mlpblk_fp4_matmul.  Pointers are device pointers, 16-byte aligned; C aliases no
+ * operand.  Returns an MLPBLK_* code.
+ */
+typedef struct {
+    int64_t m, n, k;
+    int32_t out_dtype;    /* MLPBLK_BF16 or MLPBLK_FP32                   */
+    int32_t accumulate;   /* 1: C += (MLPBLK_FP32 only)                    */
+    int32_t experts;      /* grouped forms: 1..256; else 0                */
+    int32_t pad;          /* grouped forms: the sort's pad; else 0        */
+    int64_t max_rows;     /* matmul_grouped: no expert has more rows than this
+                             (e.g. T * top_k), rows beyond it are not computed;
+                             0: no bound known, and in the other forms      */
+} mlpblk_fp4_matmul_desc;
+
+int mlpblk_fp4_matmul(const mlpblk_fp4_matmul_desc *desc, const void *a_codes, const void *a_scales,
+                      const void *b_codes, const void *b_scales, void *c, void *stream);
+
+int mlpblk_fp4_matmul_grouped(const mlpblk_fp4_matmul_desc *desc, const void *a_codes, const void *a_scales,
+                              const void *b_codes, const void *b_scales, const int32_t *count,
+                              const int32_t *seg, void *c, void *stream);
+
+int mlpblk_fp4_wgrad_grouped(const mlpblk_fp4_matmul_desc *desc, const void *a_codes, const void *a_scales,
+                             const void *b_codes, const void *b_scales, const int32_t *seg, void *c,
+                             void *stream);
+
+/*
  * zero_grads() of the accumulation loop ("grow_a_language_model_backprop" --
  * accumulation across microbatches): dgamma[d], dw1[F,d], dw2[d,F] = 0 (float32).
  * desc->tokens is ignored.  Returns an MLPBLK_* code.
@@ -499,6 +673,13 @@ int mlpblk_rmsnorm_backward_noalloc(const mlpblk_desc *desc, const void *x, cons
 #define MLPBLK_KERNEL_MOE_COMBINE    23  /* experts: y = x + weighted outputs         */
 #define MLPBLK_KERNEL_MOE_DP         24  /* experts: d_routing_weights and p * dy     */
 #define MLPBLK_KERNEL_MOE_SCATTER    25  /* reserved (dn's slot sum is in NORM_BWD)   */
+#define MLPBLK_KERNEL_SORT           26  /* mlpblk_moe_sort: the plan                 */
+#define MLPBLK_KERNEL_PERMUTE        27  /* rows into sorted order                    */
+#define MLPBLK_KERNEL_UNPERMUTE      28  /* rows back per token (and permute's dx)    */
+#define MLPBLK_KERNEL_UNPERMUTE_BWD  29  /* d_rows, d_weights                         */
+#define MLPBLK_KERNEL_FP4_QUANT      30  /* MXFP4: v -> codes and scales              */
+#define MLPBLK_KERNEL_FP4_DEQUANT    31  /* MXFP4: codes and scales -> v              */
+#define MLPBLK_KERNEL_FP4_GEMM       32  /* MXFP4 product, dense or grouped           */
 
 /*
  * mlpblk_trace_begin: from now on, launch i of this library records

@@ -38,7 +38,13 @@ EXPORTED = ("mlpblk_workspace_size", "mlpblk_forward", "mlpblk_backward", "mlpbl
             "mlpblk_moe_saved_size", "mlpblk_moe_workspace_size", "mlpblk_moe_forward", "mlpblk_moe_backward",
             "mlpblk_fold_weights", "mlpblk_forward_prefolded", "mlpblk_backward_overwrite",
             "mlpblk_moe_backward_overwrite", "mlpblk_backward_fp8_overwrite",
-            "mlpblk_backward_fp8_prequant_overwrite")
+            "mlpblk_backward_fp8_prequant_overwrite",
+            "mlpblk_moe_sort_rows", "mlpblk_moe_sort", "mlpblk_moe_permute", "mlpblk_moe_permute_backward",
+            "mlpblk_moe_unpermute", "mlpblk_moe_unpermute_backward",
+            "mlpblk_fp4_codes_size", "mlpblk_fp4_scales_size", "mlpblk_fp4_quantize", "mlpblk_fp4_dequantize",
+            "mlpblk_fp4_matmul", "mlpblk_fp4_matmul_grouped", "mlpblk_fp4_wgrad_grouped")
+MLPBLK_FP4_ACT_NONE = 0
+MLPBLK_FP4_ACT_RELU2 = 1
 MLPBLK_RMSNORM_STATS_PASS = 0
 MLPBLK_RMSNORM_IN_W1_PROLOGUE = 1
 MLPBLK_TEST_FAULT_NONE = 0
@@ -49,7 +55,9 @@ KERNEL_NAMES = {1: "fold_gamma", 2: "gemm_fwd_w1", 3: "gemm_fwd_w2", 4: "gemm_dg
                 9: "dgamma_reduce", 10: "zero_grads", 11: "scale_grads", 12: "rstd",
                 13: "grad_norm", 14: "clip_grads", 15: "adamw", 16: "grad_norm_final",
                 17: "quant_amax", 18: "quant_scale", 19: "quant_apply", 20: "norm_quant",
-                21: "moe_route", 22: "moe_gather", 23: "moe_combine", 24: "moe_dp", 25: "moe_scatter"}
+                21: "moe_route", 22: "moe_gather", 23: "moe_combine", 24: "moe_dp", 25: "moe_scatter",
+                26: "sort", 27: "permute", 28: "unpermute", 29: "unpermute_bwd",
+                30: "fp4_quant", 31: "fp4_dequant", 32: "fp4_gemm"}
 
 
 class MlpBlkError(RuntimeError):
@@ -70,6 +78,25 @@ class Desc(ctypes.Structure):
 class MoeDesc(ctypes.Structure):
     """mlpblk_moe_desc: the dense descriptor plus the expert count and top-k."""
     _fields_ = [("base", Desc), ("experts", ctypes.c_int32), ("top_k", ctypes.c_int32)]
+
+
+class SortDesc(ctypes.Structure):
+    """mlpblk_sort_desc: tokens sorted by expert."""
+    _fields_ = [("tokens", ctypes.c_int64), ("width", ctypes.c_int64), ("experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("pad", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class Fp4Desc(ctypes.Structure):
+    """mlpblk_fp4_desc: an MXFP4 matrix (a batch of them) and what it is made from."""
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("batch", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("transposed", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+class Fp4MatmulDesc(ctypes.Structure):
+    """mlpblk_fp4_matmul_desc: a product of MXFP4 matrices."""
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("out_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32), ("experts", ctypes.c_int32),
+                ("pad", ctypes.c_int32), ("max_rows", ctypes.c_int64)]
 
 
 class Param(ctypes.Structure):
@@ -144,6 +171,33 @@ def _load():
     lib.mlpblk_moe_backward.restype = i32
     lib.mlpblk_moe_backward_overwrite.argtypes = lib.mlpblk_moe_backward.argtypes
     lib.mlpblk_moe_backward_overwrite.restype = i32
+    ps, pf, pp, i64 = ctypes.POINTER(SortDesc), ctypes.POINTER(Fp4Desc), ctypes.POINTER(Fp4MatmulDesc), ctypes.c_int64
+    lib.mlpblk_moe_sort_rows.argtypes = [ps]
+    lib.mlpblk_moe_sort_rows.restype = i64
+    lib.mlpblk_moe_sort.argtypes = [ps] + [vp] * 6
+    lib.mlpblk_moe_sort.restype = i32
+    lib.mlpblk_moe_permute.argtypes = [ps] + [vp] * 6
+    lib.mlpblk_moe_permute.restype = i32
+    lib.mlpblk_moe_permute_backward.argtypes = [ps] + [vp] * 4
+    lib.mlpblk_moe_permute_backward.restype = i32
+    lib.mlpblk_moe_unpermute.argtypes = [ps] + [vp] * 6
+    lib.mlpblk_moe_unpermute.restype = i32
+    lib.mlpblk_moe_unpermute_backward.argtypes = [ps] + [vp] * 9
+    lib.mlpblk_moe_unpermute_backward.restype = i32
+    lib.mlpblk_fp4_codes_size.argtypes = [pf]
+    lib.mlpblk_fp4_codes_size.restype = sz
+    lib.mlpblk_fp4_scales_size.argtypes = [pf]
+    lib.mlpblk_fp4_scales_size.restype = sz
+    lib.mlpblk_fp4_quantize.argtypes = [pf, vp, vp, i32, vp, vp, vp]
+    lib.mlpblk_fp4_quantize.restype = i32
+    lib.mlpblk_fp4_dequantize.argtypes = [pf] + [vp] * 4
+    lib.mlpblk_fp4_dequantize.restype = i32
+    lib.mlpblk_fp4_matmul.argtypes = [pp] + [vp] * 6
+    lib.mlpblk_fp4_matmul.restype = i32
+    lib.mlpblk_fp4_matmul_grouped.argtypes = [pp] + [vp] * 8
+    lib.mlpblk_fp4_matmul_grouped.restype = i32
+    lib.mlpblk_fp4_wgrad_grouped.argtypes = [pp] + [vp] * 7
+    lib.mlpblk_fp4_wgrad_grouped.restype = i32
     lib.mlpblk_zero_grads.argtypes = [pd, vp, vp, vp, vp]
     lib.mlpblk_zero_grads.restype = i32
     lib.mlpblk_scale_grads.argtypes = [pd, vp, vp, vp, f32, vp]
@@ -416,6 +470,305 @@ class MoeBuffers:
         d = self.desc
         flat = make_desc(0, d.base.d_model, d.base.ffn * d.experts)
         mlpblk_zero_grads(flat, self.dgamma, self.dw1s, self.dw2s, stream=stream)
+
+
+def _operand(t, where, name, dtypes, numel, device=None):
+    """Device address of tensor argument `name` of `where`, checked: a contiguous CUDA
+    tensor of one of `dtypes` with at least `numel` elements, on the current device.
+    A call goes to the current device's stream, so a tensor of another one is
+    refused.  Integers (raw addresses) and None pass unchecked: the library checks
+    what it can of those."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda or not t.is_contiguous() or t.dtype not in dtypes or t.numel() < numel:
+        raise MlpBlkError(MLPBLK_EINVAL, f"{where}: {name} must be a contiguous CUDA tensor of "
+                          f"{' or '.join(str(d) for d in dtypes)} with at least {numel} elements")
+    if device is not None and t.device.index != device:
+        raise MlpBlkError(MLPBLK_EINVAL, f"{where}: {name} is on cuda:{t.device.index}, the call on cuda:{device}")
+    return t.data_ptr()
+
+
+def _call_site():
+    """(current device index, torch's int32, float32, byte types) for the checks."""
+    import torch
+    return torch.cuda.current_device(), (torch.int32,), (torch.float32,), (torch.uint8,)
+
+
+def _row_types(dtype):
+    import torch
+    return (torch.bfloat16,) if dtype == MLPBLK_BF16 else (torch.float32,)
+
+
+def _dtype_code(dtype):
+    """MLPBLK_BF16 / MLPBLK_FP32 of "bf16", "f32", a torch dtype or the code itself."""
+    if isinstance(dtype, int):
+        return dtype
+    name = str(dtype)
+    if name in ("bf16", "torch.bfloat16"):
+        return MLPBLK_BF16
+    if name in ("f32", "torch.float32"):
+        return MLPBLK_FP32
+    raise MlpBlkError(MLPBLK_ENOTSUP, f"element type {dtype}")
+
+
+def make_sort_desc(tokens, width, experts, top_k, pad=128, dtype=MLPBLK_BF16) -> SortDesc:
+    return SortDesc(int(tokens), int(width), int(experts), int(top_k), int(pad), _dtype_code(dtype))
+
+
+def mlpblk_moe_sort_rows(desc: SortDesc) -> int:
+    return int(lib.mlpblk_moe_sort_rows(ctypes.byref(desc)))
+
+
+def mlpblk_moe_sort(desc, expert_idx, count, seg, pos, row_map, stream=None):
+    where = "mlpblk_moe_sort"
+    dev, i32, _, _ = _call_site()
+    n = desc.tokens * desc.top_k
+    rc = lib.mlpblk_moe_sort(
+        ctypes.byref(desc), _operand(expert_idx, where, "expert_idx", i32, n, dev),
+        _operand(count, where, "count", i32, desc.experts, dev), _operand(seg, where, "seg", i32, desc.experts + 1, dev),
+        _operand(pos, where, "pos", i32, n, dev),
+        _operand(row_map, where, "row_map", i32, mlpblk_moe_sort_rows(desc), dev), _stream(stream))
+    _check(rc, where)
+
+
+def mlpblk_moe_permute(desc, x, pos, count, seg, rows, stream=None):
+    where = "mlpblk_moe_permute"
+    dev, i32, _, _ = _call_site()
+    dt = _row_types(desc.dtype)
+    rc = lib.mlpblk_moe_permute(
+        ctypes.byref(desc), _operand(x, where, "x", dt, desc.tokens * desc.width, dev),
+        _operand(pos, where, "pos", i32, desc.tokens * desc.top_k, dev),
+        _operand(count, where, "count", i32, desc.experts, dev), _operand(seg, where, "seg", i32, desc.experts + 1, dev),
+        _operand(rows, where, "rows", dt, mlpblk_moe_sort_rows(desc) * desc.width, dev), _stream(stream))
+    _check(rc, where)
+
+
+def mlpblk_moe_permute_backward(desc, d_rows, pos, dx, stream=None):
+    where = "mlpblk_moe_permute_backward"
+    dev, i32, _, _ = _call_site()
+    dt = _row_types(desc.dtype)
+    rc = lib.mlpblk_moe_permute_backward(
+        ctypes.byref(desc), _operand(d_rows, where, "d_rows", dt, mlpblk_moe_sort_rows(desc) * desc.width, dev),
+        _operand(pos, where, "pos", i32, desc.tokens * desc.top_k, dev),
+        _operand(dx, where, "dx", dt, desc.tokens * desc.width, dev), _stream(stream))
+    _check(rc, where)
+
+
+def mlpblk_moe_unpermute(desc, rows, pos, weights, residual, y, stream=None):
+    where = "mlpblk_moe_unpermute"
+    dev, i32, f32, _ = _call_site()
+    dt = _row_types(desc.dtype)
+    n = desc.tokens * desc.width
+    rc = lib.mlpblk_moe_unpermute(
+        ctypes.byref(desc), _operand(rows, where, "rows", dt, mlpblk_moe_sort_rows(desc) * desc.width, dev),
+        _operand(pos, where, "pos", i32, desc.tokens * desc.top_k, dev),
+        _operand(weights, where, "weights", f32, desc.tokens * desc.top_k, dev),
+        _operand(residual, where, "residual", dt, n, dev), _operand(y, where, "y", dt, n, dev), _stream(stream))
+    _check(rc, where)
+
+
+def mlpblk_moe_unpermute_backward(desc, dy, rows, pos, count, seg, weights, d_rows, d_weights, stream=None):
+    where = "mlpblk_moe_unpermute_backward"
+    dev, i32, f32, _ = _call_site()
+    dt = _row_types(desc.dtype)
+    n, r = desc.tokens * desc.top_k, mlpblk_moe_sort_rows(desc) * desc.width
+    rc = lib.mlpblk_moe_unpermute_backward(
+        ctypes.byref(desc), _operand(dy, where, "dy", dt, desc.tokens * desc.width, dev),
+        _operand(rows, where, "rows", dt, r, dev), _operand(pos, where, "pos", i32, n, dev),
+        _operand(count, where, "count", i32, desc.experts, dev), _operand(seg, where, "seg", i32, desc.experts + 1, dev),
+        _operand(weights, where, "weights", f32, n, dev), _operand(d_rows, where, "d_rows", dt, r, dev),
+        _operand(d_weights, where, "d_weights", f32, n, dev), _stream(stream))
+    _check(rc, where)
+
+
+class MoeSort:
+    """The plan of one batch's routing and its buffers: `sort` fills count, seg, pos
+    and row_map from the expert ids, the other methods move rows by it.  `rows` is R,
+    the row count of the sorted buffers."""
+
+    def __init__(self, tokens, width, experts, top_k, pad=128, dtype="bf16", device="cuda"):
+        import torch
+        self.desc = make_sort_desc(tokens, width, experts, top_k, pad, dtype)
+        self.rows = mlpblk_moe_sort_rows(self.desc)
+        if self.rows < 0:
+            raise MlpBlkError(MLPBLK_EINVAL, "mlpblk_moe_sort_rows")
+        e = dict(dtype=torch.int32, device=device)
+        self.count = torch.zeros(experts, **e)
+        self.seg = torch.zeros(experts + 1, **e)
+        self.pos = torch.empty(tokens, top_k, **e)
+        self.row_map = torch.empty(self.rows, **e)
+
+    def sort(self, expert_idx, stream=None):
+        mlpblk_moe_sort(self.desc, expert_idx, self.count, self.seg, self.pos, self.row_map, stream=stream)
+
+    def permute(self, x, rows, stream=None):
+        mlpblk_moe_permute(self.desc, x, self.pos, self.count, self.seg, rows, stream=stream)
+
+    def permute_backward(self, d_rows, dx, stream=None):
+        mlpblk_moe_permute_backward(self.desc, d_rows, self.pos, dx, stream=stream)
+
+    def unpermute(self, rows, y, weights=None, residual=None, stream=None):
+        mlpblk_moe_unpermute(self.desc, rows, self.pos, weights, residual, y, stream=stream)
+
+    def unpermute_backward(self, dy, rows, weights, d_rows, d_weights, stream=None):
+        mlpblk_moe_unpermute_backward(self.desc, dy, rows, self.pos, self.count, self.seg, weights, d_rows, d_weights,
+                                      stream=stream)
+
+
+def make_fp4_desc(rows, cols, batch=1, dtype=MLPBLK_BF16, transposed=False, act=MLPBLK_FP4_ACT_NONE) -> Fp4Desc:
+    return Fp4Desc(int(rows), int(cols), int(batch), _dtype_code(dtype), int(bool(transposed)), int(act))
+
+
+def mlpblk_fp4_codes_size(desc: Fp4Desc) -> int:
+    return int(lib.mlpblk_fp4_codes_size(ctypes.byref(desc)))
+
+
+def mlpblk_fp4_scales_size(desc: Fp4Desc) -> int:
+    return int(lib.mlpblk_fp4_scales_size(ctypes.byref(desc)))
+
+
+def mlpblk_fp4_quantize(desc, x, codes, scales, row_map=None, map_div=0, stream=None):
+    """x holds the whole source, unless a row_map gathers its rows (map_div > 0): its
+    row count is then the caller's business."""
+    where = "mlpblk_fp4_quantize"
+    dev, i32, _, u8 = _call_site()
+    mapped = desc.cols if desc.transposed else desc.rows  # the source's rows
+    n = 0 if row_map is not None and map_div > 0 else desc.rows * desc.cols * desc.batch
+    rc = lib.mlpblk_fp4_quantize(
+        ctypes.byref(desc), _operand(x, where, "x", _row_types(desc.dtype), n, dev),
+        _operand(row_map, where, "row_map", i32, mapped, dev), int(map_div),
+        _operand(codes, where, "codes", u8, mlpblk_fp4_codes_size(desc), dev),
+        _operand(scales, where, "scales", u8, mlpblk_fp4_scales_size(desc), dev), _stream(stream))
+    _check(rc, where)
+
+
+def mlpblk_fp4_dequantize(desc, codes, scales, y, stream=None):
+    where = "mlpblk_fp4_dequantize"
+    dev, _, _, u8 = _call_site()
+    rc = lib.mlpblk_fp4_dequantize(
+        ctypes.byref(desc), _operand(codes, where, "codes", u8, mlpblk_fp4_codes_size(desc), dev),
+        _operand(scales, where, "scales", u8, mlpblk_fp4_scales_size(desc), dev),
+        _operand(y, where, "y", _row_types(desc.dtype), desc.rows * desc.cols * desc.batch, dev), _stream(stream))
+    _check(rc, where)
+
+
+def make_fp4_matmul_desc(m, n, k, out_dtype=MLPBLK_BF16, accumulate=False, experts=0, pad=0,
+                         max_rows=0) -> Fp4MatmulDesc:
+    return Fp4MatmulDesc(int(m), int(n), int(k), _dtype_code(out_dtype), int(bool(accumulate)), int(experts), int(pad),
+                         int(max_rows))
+
+
+def _fp4_operands(where, a, a_rows, b, b_rows, b_batch, k, dev, u8):
+    """Addresses of (codes, scales) of A and B, sizes checked."""
+    out = []
+    for name, (codes, scales), rows, batch in (("a", a, a_rows, 1), ("b", b, b_rows, b_batch)):
+        d = Fp4Desc(rows, k, batch, MLPBLK_BF16, 0, 0)
+        out.append(_operand(codes, where, name + "_codes", u8, mlpblk_fp4_codes_size(d), dev))
+        out.append(_operand(scales, where, name + "_scales", u8, mlpblk_fp4_scales_size(d), dev))
+    return out
+
+
+def mlpblk_fp4_matmul(desc, a_codes, a_scales, b_codes, b_scales, c, stream=None):
+    where = "mlpblk_fp4_matmul"
+    dev, _, _, u8 = _call_site()
+    ops = _fp4_operands(where, (a_codes, a_scales), desc.m, (b_codes, b_scales), desc.n, 1, desc.k, dev, u8)
+    rc = lib.mlpblk_fp4_matmul(ctypes.byref(desc), *ops,
+                               _operand(c, where, "c", _row_types(desc.out_dtype), desc.m * desc.n, dev), _stream(stream))
+    _check(rc, where)
+
+
+def mlpblk_fp4_matmul_grouped(desc, a_codes, a_scales, b_codes, b_scales, count, seg, c, stream=None):
+    where = "mlpblk_fp4_matmul_grouped"
+    dev, i32, _, u8 = _call_site()
+    ops = _fp4_operands(where, (a_codes, a_scales), desc.m, (b_codes, b_scales), desc.n, max(desc.experts, 1), desc.k,
+                        dev, u8)
+    rc = lib.mlpblk_fp4_matmul_grouped(
+        ctypes.byref(desc), *ops, _operand(count, where, "count", i32, desc.experts, dev),
+        _operand(seg, where, "seg", i32, desc.experts + 1, dev),
+        _operand(c, where, "c", _row_types(desc.out_dtype), desc.m * desc.n, dev), _stream(stream))
+    _check(rc, where)
+
+
+def mlpblk_fp4_wgrad_grouped(desc, a_codes, a_scales, b_codes, b_scales, seg, c, stream=None):
+    where = "mlpblk_fp4_wgrad_grouped"
+    dev, i32, _, u8 = _call_site()
+    ops = _fp4_operands(where, (a_codes, a_scales), desc.m, (b_codes, b_scales), desc.n, 1, desc.k, dev, u8)
+    rc = lib.mlpblk_fp4_wgrad_grouped(
+        ctypes.byref(desc), *ops, _operand(seg, where, "seg", i32, desc.experts + 1, dev),
+        _operand(c, where, "c", _row_types(desc.out_dtype), desc.experts * desc.m * desc.n, dev), _stream(stream))
+    _check(rc, where)
+
+
+class Fp4Matrix:
+    """An MXFP4 matrix [rows, cols] (or a batch of them): its codes and scales, and
+    the products that take it as A.  `codes` and `scales` given: buffers that hold a
+    quantised matrix already (uint8)."""
+
+    def __init__(self, rows, cols, batch=1, codes=None, scales=None, device="cuda"):
+        import torch
+        self.rows, self.cols, self.batch = int(rows), int(cols), int(batch)
+        d = make_fp4_desc(rows, cols, batch)
+        nc, ns = mlpblk_fp4_codes_size(d), mlpblk_fp4_scales_size(d)
+        if (nc == 0 or ns == 0) and rows != 0 and cols != 0:
+            raise MlpBlkError(MLPBLK_EINVAL, "mlpblk_fp4_codes_size")
+        u8 = dict(dtype=torch.uint8, device=device)
+        self.codes = torch.empty(nc, **u8) if codes is None else codes
+        self.scales = torch.empty(ns, **u8) if scales is None else scales
+        if self.codes.numel() != nc or self.scales.numel() != ns:
+            raise MlpBlkError(MLPBLK_EINVAL, f"Fp4Matrix: {nc} bytes of codes and {ns} of scales")
+
+    def quantize(self, x, transposed=False, act="none", sort=None, gather=False, stream=None):
+        """From x (bf16 or float32; stored [cols, rows] when transposed).  sort: a
+        MoeSort whose row_map says which source rows are live; gather=True reads
+        them from x's tokens, otherwise x is already in sorted order."""
+        acts = {"none": MLPBLK_FP4_ACT_NONE, "relu2": MLPBLK_FP4_ACT_RELU2}
+        if act not in acts:
+            raise MlpBlkError(MLPBLK_ENOTSUP, f"Fp4Matrix.quantize: act {act!r}")
+        if gather and sort is None:
+            raise MlpBlkError(MLPBLK_EINVAL, "Fp4Matrix.quantize: gather needs a sort")
+        d = Fp4Desc(self.rows, self.cols, self.batch, _dtype_code(x.dtype), int(bool(transposed)), acts[act])
+        if sort is not None:
+            width = self.rows if transposed else self.cols
+            if gather and x.numel() != sort.desc.tokens * width:
+                raise MlpBlkError(MLPBLK_EINVAL, "Fp4Matrix.quantize: x is not [tokens, width] of the sort")
+            mlpblk_fp4_quantize(d, x, self.codes, self.scales, sort.row_map, sort.desc.top_k if gather else 0,
+                                stream=stream)
+        else:
+            mlpblk_fp4_quantize(d, x, self.codes, self.scales, stream=stream)
+
+    def dequantize(self, y, stream=None):
+        d = Fp4Desc(self.rows, self.cols, self.batch, _dtype_code(y.dtype), 0, 0)
+        mlpblk_fp4_dequantize(d, self.codes, self.scales, y, stream=stream)
+
+    def _common_k(self, b, where):
+        if self.batch != 1 or b.cols != self.cols:
+            raise MlpBlkError(MLPBLK_EINVAL, f"{where}: A [{self.rows}, {self.cols}] x {self.batch}, B [{b.rows}, {b.cols}]")
+
+    def matmul(self, b, c, accumulate=False, stream=None):
+        """c[rows, b.rows] = self . b^T (or += with accumulate, float32)."""
+        self._common_k(b, "Fp4Matrix.matmul")
+        if b.batch != 1:
+            raise MlpBlkError(MLPBLK_EINVAL, "Fp4Matrix.matmul: b is a batch")
+        d = Fp4MatmulDesc(self.rows, b.rows, self.cols, _dtype_code(c.dtype), int(bool(accumulate)), 0, 0, 0)
+        mlpblk_fp4_matmul(d, self.codes, self.scales, b.codes, b.scales, c, stream=stream)
+
+    def matmul_grouped(self, b, sort, c, accumulate=False, stream=None):
+        """c[R, b.rows]: expert e's rows of self times the batch's matrix e."""
+        self._common_k(b, "Fp4Matrix.matmul_grouped")
+        if b.batch != sort.desc.experts or self.rows != sort.rows:
+            raise MlpBlkError(MLPBLK_EINVAL, "Fp4Matrix.matmul_grouped: b is not the experts' batch or self not the sorted rows")
+        d = Fp4MatmulDesc(self.rows, b.rows, self.cols, _dtype_code(c.dtype), int(bool(accumulate)), b.batch,
+                          sort.desc.pad, sort.desc.tokens * sort.desc.top_k)
+        mlpblk_fp4_matmul_grouped(d, self.codes, self.scales, b.codes, b.scales, sort.count, sort.seg, c, stream=stream)
+
+    def wgrad_grouped(self, b, sort, c, accumulate=False, stream=None):
+        """c[experts, rows, b.rows]: self . b^T over each expert's segment."""
+        self._common_k(b, "Fp4Matrix.wgrad_grouped")
+        if b.batch != 1 or self.cols != sort.rows:
+            raise MlpBlkError(MLPBLK_EINVAL, "Fp4Matrix.wgrad_grouped: the columns are not the sorted rows")
+        d = Fp4MatmulDesc(self.rows, b.rows, self.cols, _dtype_code(c.dtype), int(bool(accumulate)), sort.desc.experts,
+                          sort.desc.pad, 0)
+        mlpblk_fp4_wgrad_grouped(d, self.codes, self.scales, b.codes, b.scales, sort.seg, c, stream=stream)
 
 
 def mlpblk_zero_grads(desc, dgamma, dw1, dw2, stream=None):

@@ -14,6 +14,7 @@
 
 #include <new>
 
+#include "fp4_layout.h"
 #include "mlpblk_internal.h"
 
 namespace mlpblk {
@@ -1275,6 +1276,236 @@ int moe_backward_entry(const mlpblk_moe_desc *desc, const void *dy, const void *
 
 }  // namespace
 
+namespace {
+
+// ----------------------------------------------- tokens sorted by expert and back
+
+int check_sort_desc(const mlpblk_sort_desc *d) {
+    if (!d) return MLPBLK_EINVAL;
+    if (d->dtype != MLPBLK_BF16 && d->dtype != MLPBLK_FP32) return MLPBLK_ENOTSUP;
+    if (d->tokens < 0 || d->width < 1 || d->experts < 1 || d->experts > 256 || d->top_k < 1 || d->top_k > 256 ||
+        d->pad < 1 || d->pad > 1024)
+        return MLPBLK_EINVAL;
+    const int64_t lim = static_cast<int64_t>(1) << 31;
+    if (d->width >= lim || d->tokens >= lim / d->top_k) return MLPBLK_EINVAL;
+    if (d->tokens * d->top_k + static_cast<int64_t>(d->experts + 1) * d->pad >= lim) return MLPBLK_EINVAL;
+    return MLPBLK_OK;
+}
+
+int64_t sort_rows(const mlpblk_sort_desc *d) {
+    const int64_t n = d->tokens * d->top_k, used = n < d->experts ? n : d->experts;
+    return (n + used * (d->pad - 1) + d->pad - 1) / d->pad * d->pad;
+}
+
+// ------------------------------------------------------------------------ MXFP4
+
+constexpr int64_t kFp4Lim = static_cast<int64_t>(1) << 31;
+
+int check_fp4_desc(const mlpblk_fp4_desc *d) {
+    if (!d) return MLPBLK_EINVAL;
+    if (d->dtype != MLPBLK_BF16 && d->dtype != MLPBLK_FP32) return MLPBLK_ENOTSUP;
+    if (d->act != MLPBLK_FP4_ACT_NONE && d->act != MLPBLK_FP4_ACT_RELU2) return MLPBLK_ENOTSUP;
+    if (d->transposed != 0 && d->transposed != 1) return MLPBLK_EINVAL;
+    if (d->rows < 0 || d->cols < 0 || d->batch < 1 || d->cols >= kFp4Lim) return MLPBLK_EINVAL;
+    if (d->rows > 0 && d->batch >= kFp4Lim / d->rows) return MLPBLK_EINVAL;
+    return MLPBLK_OK;
+}
+
+int check_fp4_matmul(const mlpblk_fp4_matmul_desc *d, int mode) {
+    if (!d) return MLPBLK_EINVAL;
+    if (d->out_dtype != MLPBLK_BF16 && d->out_dtype != MLPBLK_FP32) return MLPBLK_ENOTSUP;
+    if (d->accumulate != 0 && d->accumulate != 1) return MLPBLK_EINVAL;
+    if (d->accumulate && d->out_dtype != MLPBLK_FP32) return MLPBLK_ENOTSUP;
+    if (d->m < 0 || d->n < 1 || d->k < (mode == kFp4GroupK ? 0 : 1)) return MLPBLK_EINVAL;
+    if (d->m >= kFp4Lim || d->n >= kFp4Lim || d->k >= kFp4Lim) return MLPBLK_EINVAL;
+    if (d->max_rows < 0 || (d->max_rows > 0 && mode != kFp4GroupRows)) return MLPBLK_EINVAL;
+    int64_t tiles = ((d->m + 31) / 32) * ((d->n + 127) / 128);
+    if (mode == kFp4Dense) {
+        if (d->experts != 0 || d->pad != 0) return MLPBLK_EINVAL;
+    } else {
+        if (d->experts < 1 || d->experts > 256 || d->pad < 1) return MLPBLK_EINVAL;
+        if (d->pad % (mode == kFp4GroupRows ? 128 : 256) != 0) return MLPBLK_ENOTSUP;
+        if ((mode == kFp4GroupRows ? d->n : d->m) >= kFp4Lim / d->experts) return MLPBLK_EINVAL;
+        tiles *= mode == kFp4GroupK ? d->experts : 1;
+    }
+    return tiles < kFp4Lim / 2 ? MLPBLK_OK : MLPBLK_EINVAL;
+}
+
+int fp4_product(const mlpblk_fp4_matmul_desc *desc, int mode, const void *a_codes, const void *a_scales,
+                const void *b_codes, const void *b_scales, const int32_t *count, const int32_t *seg, void *c,
+                void *stream) {
+    MLPBLK_TRY(check_fp4_matmul(desc, mode));
+    if (desc->m == 0) return MLPBLK_OK;
+    if (desc->k == 0) {  // weight gradients of no rows at all
+        if (!aligned16(c)) return MLPBLK_EINVAL;
+        if (desc->accumulate) return MLPBLK_OK;
+        const size_t bytes = static_cast<size_t>(desc->experts) * desc->m * desc->n * (desc->out_dtype == MLPBLK_BF16 ? 2 : 4);
+        return cuda_status(cudaMemsetAsync(c, 0, bytes, static_cast<cudaStream_t>(stream)));
+    }
+    if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(b_codes) || !aligned16(b_scales) || !aligned16(c))
+        return MLPBLK_EINVAL;
+    if ((mode != kFp4Dense && !aligned16(seg)) || (mode == kFp4GroupRows && !aligned16(count))) return MLPBLK_EINVAL;
+    if (c == a_codes || c == a_scales || c == b_codes || c == b_scales || c == seg || c == count) return MLPBLK_EINVAL;
+    int sms = 0;
+    MLPBLK_TRY(device_sms(&sms));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Fp4Product p = {};
+    p.mode = mode;
+    p.m = desc->m;
+    p.n = desc->n;
+    p.k = desc->k;
+    p.experts = desc->experts;
+    p.max_rows = desc->max_rows;
+    p.a = static_cast<const uint8_t *>(a_codes);
+    p.sa = static_cast<const uint8_t *>(a_scales);
+    p.b = static_cast<const uint8_t *>(b_codes);
+    p.sb = static_cast<const uint8_t *>(b_scales);
+    p.count = count;
+    p.seg = seg;
+    p.c = c;
+    p.out_dtype = desc->out_dtype;
+    p.accumulate = desc->accumulate;
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_FP4_GEMM, s, launch_fp4_matmul(p, sms, s));
+    return MLPBLK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t mlpblk_moe_sort_rows(const mlpblk_sort_desc *desc) {
+    return check_sort_desc(desc) != MLPBLK_OK ? -1 : sort_rows(desc);
+}
+
+int mlpblk_moe_sort(const mlpblk_sort_desc *desc, const int32_t *expert_idx, int32_t *count, int32_t *seg,
+                    int32_t *pos, int32_t *row_map, void *stream) {
+    MLPBLK_TRY(check_sort_desc(desc));
+    const int64_t n = desc->tokens * desc->top_k;
+    if (!aligned16(count) || !aligned16(seg)) return MLPBLK_EINVAL;
+    if (n > 0 && (!aligned16(expert_idx) || !aligned16(pos) || !aligned16(row_map))) return MLPBLK_EINVAL;
+    if (n > 0 && (pos == expert_idx || row_map == expert_idx)) return MLPBLK_EINVAL;
+    int sms = 0;
+    MLPBLK_TRY(device_sms(&sms));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_SORT, s,
+                  launch_sort(expert_idx, n, desc->experts, desc->pad, sort_rows(desc), count, seg, pos, row_map, s));
+    return MLPBLK_OK;
+}
+
+int mlpblk_moe_permute(const mlpblk_sort_desc *desc, const void *x, const int32_t *pos, const int32_t *count,
+                       const int32_t *seg, void *rows, void *stream) {
+    MLPBLK_TRY(check_sort_desc(desc));
+    if (desc->tokens == 0) return MLPBLK_OK;
+    if (!aligned16(x) || !aligned16(pos) || !aligned16(count) || !aligned16(seg) || !aligned16(rows)) return MLPBLK_EINVAL;
+    if (rows == x) return MLPBLK_EINVAL;
+    int sms = 0;
+    MLPBLK_TRY(device_sms(&sms));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_PERMUTE, s,
+                  launch_permute(x, pos, count, seg, desc->tokens, desc->width, desc->dtype, desc->top_k, desc->experts,
+                                 desc->pad, rows, s));
+    return MLPBLK_OK;
+}
+
+int mlpblk_moe_unpermute(const mlpblk_sort_desc *desc, const void *rows, const int32_t *pos, const float *weights,
+                         const void *residual, void *y, void *stream) {
+    MLPBLK_TRY(check_sort_desc(desc));
+    if (desc->tokens == 0) return MLPBLK_OK;
+    if (!aligned16(rows) || !aligned16(pos) || !aligned16(y)) return MLPBLK_EINVAL;
+    if ((weights && !aligned16(weights)) || (residual && !aligned16(residual))) return MLPBLK_EINVAL;
+    if (y == rows) return MLPBLK_EINVAL;
+    int sms = 0;
+    MLPBLK_TRY(device_sms(&sms));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_UNPERMUTE, s,
+                  launch_unpermute(rows, pos, weights, residual, desc->tokens, desc->width, desc->dtype, desc->top_k, y, s));
+    return MLPBLK_OK;
+}
+
+int mlpblk_moe_permute_backward(const mlpblk_sort_desc *desc, const void *d_rows, const int32_t *pos, void *dx,
+                                void *stream) {
+    return mlpblk_moe_unpermute(desc, d_rows, pos, nullptr, nullptr, dx, stream);
+}
+
+int mlpblk_moe_unpermute_backward(const mlpblk_sort_desc *desc, const void *dy, const void *rows,
+                                  const int32_t *pos, const int32_t *count, const int32_t *seg,
+                                  const float *weights, void *d_rows, float *d_weights, void *stream) {
+    MLPBLK_TRY(check_sort_desc(desc));
+    if (desc->tokens == 0) return MLPBLK_OK;
+    if (!aligned16(dy) || !aligned16(pos) || !aligned16(count) || !aligned16(seg) || !aligned16(d_rows)) return MLPBLK_EINVAL;
+    if ((weights && !aligned16(weights)) || (d_weights && (!aligned16(d_weights) || !aligned16(rows)))) return MLPBLK_EINVAL;
+    if (d_rows == dy || d_rows == rows || (d_weights && d_weights == weights)) return MLPBLK_EINVAL;
+    int sms = 0;
+    MLPBLK_TRY(device_sms(&sms));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_UNPERMUTE_BWD, s,
+                  launch_unpermute_bwd(dy, rows, pos, count, seg, weights, desc->tokens, desc->width, desc->dtype,
+                                       desc->top_k, desc->experts, desc->pad, d_rows, d_weights, s));
+    return MLPBLK_OK;
+}
+
+size_t mlpblk_fp4_codes_size(const mlpblk_fp4_desc *desc) {
+    if (check_fp4_desc(desc) != MLPBLK_OK) return 0;
+    return static_cast<size_t>(desc->rows * fp4_row_bytes(desc->cols) * desc->batch);
+}
+
+size_t mlpblk_fp4_scales_size(const mlpblk_fp4_desc *desc) {
+    if (check_fp4_desc(desc) != MLPBLK_OK) return 0;
+    return static_cast<size_t>(fp4_scales_bytes(desc->rows, desc->cols) * desc->batch);
+}
+
+int mlpblk_fp4_quantize(const mlpblk_fp4_desc *desc, const void *x, const int32_t *row_map, int32_t map_div,
+                        void *codes, void *scales, void *stream) {
+    MLPBLK_TRY(check_fp4_desc(desc));
+    if (map_div < 0 || (row_map && desc->batch != 1)) return MLPBLK_EINVAL;
+    if (desc->rows == 0 || desc->cols == 0) return MLPBLK_OK;
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || (row_map && !aligned16(row_map))) return MLPBLK_EINVAL;
+    if (codes == x || scales == x || codes == scales) return MLPBLK_EINVAL;
+    int sms = 0;
+    MLPBLK_TRY(device_sms(&sms));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_FP4_QUANT, s,
+                  launch_fp4_quantize(desc->dtype, x, row_map, map_div, desc->rows, desc->cols, desc->batch,
+                                      desc->transposed != 0, desc->act == MLPBLK_FP4_ACT_RELU2,
+                                      static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales), s));
+    return MLPBLK_OK;
+}
+
+int mlpblk_fp4_dequantize(const mlpblk_fp4_desc *desc, const void *codes, const void *scales, void *y,
+                          void *stream) {
+    MLPBLK_TRY(check_fp4_desc(desc));
+    if (desc->transposed != 0 || desc->act != MLPBLK_FP4_ACT_NONE) return MLPBLK_ENOTSUP;
+    if (desc->rows == 0 || desc->cols == 0) return MLPBLK_OK;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(y)) return MLPBLK_EINVAL;
+    if (y == codes || y == scales) return MLPBLK_EINVAL;
+    int sms = 0;
+    MLPBLK_TRY(device_sms(&sms));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_FP4_DEQUANT, s,
+                  launch_fp4_dequantize(desc->dtype, static_cast<const uint8_t *>(codes),
+                                        static_cast<const uint8_t *>(scales), desc->rows, desc->cols, desc->batch, y, s));
+    return MLPBLK_OK;
+}
+
+int mlpblk_fp4_matmul(const mlpblk_fp4_matmul_desc *desc, const void *a_codes, const void *a_scales,
+                      const void *b_codes, const void *b_scales, void *c, void *stream) {
+    return fp4_product(desc, kFp4Dense, a_codes, a_scales, b_codes, b_scales, nullptr, nullptr, c, stream);
+}
+
+int mlpblk_fp4_matmul_grouped(const mlpblk_fp4_matmul_desc *desc, const void *a_codes, const void *a_scales,
+                              const void *b_codes, const void *b_scales, const int32_t *count,
+                              const int32_t *seg, void *c, void *stream) {
+    return fp4_product(desc, kFp4GroupRows, a_codes, a_scales, b_codes, b_scales, count, seg, c, stream);
+}
+
+int mlpblk_fp4_wgrad_grouped(const mlpblk_fp4_matmul_desc *desc, const void *a_codes, const void *a_scales,
+                             const void *b_codes, const void *b_scales, const int32_t *seg, void *c,
+                             void *stream) {
+    return fp4_product(desc, kFp4GroupK, a_codes, a_scales, b_codes, b_scales, nullptr, seg, c, stream);
+}
+
+}  // extern "C"
+
 extern "C" {
 
 int mlpblk_moe_backward(const mlpblk_moe_desc *desc, const void *dy, const void *x, const void *gamma,
@@ -1352,8 +1583,9 @@ int mlpblk_last_error(void) {
     const int a = take_device_error_gemm_fwd();
     const int b = take_device_error_gemm_bwd();
     const int c = take_device_error_gemm_f8();
+    const int f = take_device_error_gemm_f4();
     const int r = take_device_error_rowops();
-    return a != MLPBLK_OK ? a : (b != MLPBLK_OK ? b : (c != MLPBLK_OK ? c : r));
+    return a != MLPBLK_OK ? a : (b != MLPBLK_OK ? b : (c != MLPBLK_OK ? c : (f != MLPBLK_OK ? f : r)));
 }
 
 }  // extern "C"

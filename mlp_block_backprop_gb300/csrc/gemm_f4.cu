@@ -1,0 +1,544 @@
+// gemm_f4.cu -- products of MXFP4 matrices, C[m,n] = A[m,k] . B[n,k]^T, on the tensor
+// cores' block-scaled path (tcgen05.mma kind::mxf4: E2M1 operands, one E8M0 scale
+// per 32 values of K, fp32 accumulator in TMEM).
+//
+// A stage row is 128 bytes, 256 values of K, in the 128-byte swizzle; one MMA takes
+// 32 bytes (64 values) of it.  The scales lie in global memory in the order in which
+// tcgen05.cp wants them (include/mlpblk.h: 512-byte tiles of 128 rows x 128 values
+// of K), so a stage's scales are one untiled copy of 1 KB per 128 rows, and one
+// tcgen05.cp (32 lanes x 16 bytes, repeated over the four lane quarters) a tile puts
+// them into four TMEM columns.  The same thread issues the copies and the MMAs,
+// which the tensor core takes in order.
+//
+// f4_small: one CTA computes a 128 x BN tile with B's rows (C's columns) on the 128
+//   lanes and A's rows (tokens) on the columns, so that few tokens cost few
+//   columns: at one token the kernel streams the weights.  C leaves straight from
+//   registers: 32 lanes are 32 consecutive elements of a row of C, whatever n is.
+//   K can be split over a cluster; the parts meet in distributed shared memory and
+//   are added in rank order.
+#include "fp4_layout.h"
+#include "gemm_tc.cuh"
+
+namespace mlpblk {
+
+namespace {
+
+constexpr int kF4MaxExperts = 256;
+constexpr int kF4KB = 256;              // K values of a stage
+
+struct F4Args {
+    int mode;                           // Fp4Mode
+    int64_t m, n;                       // C (per expert when K-grouped)
+    int kblocks;                        // stages along all of K
+    int experts;
+    int64_t max_rows;
+    const uint8_t *sa, *sb;             // scales
+    int64_t row_tile_bytes;             // of one 128-row strip of scale tiles (A and B share K)
+    int64_t sb_expert_bytes;            // one expert's B scales
+    const int *count, *seg;
+    void *c;
+    int accumulate;
+};
+
+// ------------------------------------------------------------------------- PTX
+
+// Instruction descriptor of kind::mxf4: E2M1 A and B (code 1), E8M0 scales, K = 64;
+// the scale ids (0 or 2) say which two of a TMEM word's four scale bytes an MMA reads.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int sf) {
+    return (static_cast<uint32_t>(sf) << 4)           // B scale id
+           | (1u << 7) | (1u << 10)                    // A, B: E2M1
+           | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
+           | (1u << 23)                                // scales: E8M0
+           | (static_cast<uint32_t>(M >> 7) << 27)     // M / 128
+           | (static_cast<uint32_t>(sf) << 29);        // A scale id
+}
+
+__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  setp.ne.b32 p, %6, 0;\n"
+        "  tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n"
+        "}\n"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// One scale tile (32 rows of 16 bytes in shared memory) into four TMEM columns,
+// repeated over the four lane quarters.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t s_desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+}
+
+// Shared-memory descriptor of a scale tile: no swizzle, 8-row groups of 16-byte rows
+// 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
+           (static_cast<uint64_t>(1) << 46);
+}
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "  selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// mbar_wait for a barrier that other CTAs of the cluster arrive on.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (*abort) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            record_device_error(MLPBLK_ETIMEOUT);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+// ------------------------------------------------------------------- the work
+
+// The experts' segments in shared memory and the tiles before each expert.
+struct F4Groups {
+    int seg[kF4MaxExperts + 1];
+    int count[kF4MaxExperts];
+    int before[kF4MaxExperts + 1];
+};
+
+// One output tile: rows m0 .. m0 + m_valid of A, columns n0 .. n0 + n_valid of C.
+struct F4Tile {
+    int a_row, b_row;          // rows of the code matrices (TMA coordinates)
+    const uint8_t *sa, *sb;    // scale tiles of those rows at k-block 0
+    int kb0, kb1;              // k-blocks
+    int64_t c_row;             // C's row of the tile's first A row
+    int n0, m_valid, n_valid;
+};
+
+// Fills `g` (one warp; lane l takes experts l, l + 32, ...) for tiles of TM rows and
+// TN columns; returns the number of tiles.  Values that a plan of another shape would
+// give are cut to the arrays, so no access leaves them.
+template <int TM, int TN>
+__device__ int f4_groups(const F4Args &a, F4Groups *g, int lane) {
+    const int64_t limit = a.mode == kFp4GroupRows ? a.m : static_cast<int64_t>(a.kblocks) * kF4KB;
+    const int nt = static_cast<int>((a.n + TN - 1) / TN);
+    const int mt = static_cast<int>((a.m + TM - 1) / TM);
+    int run = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += 32) {
+        const int e = e0 + lane;
+        int tiles = 0;
+        if (e < a.experts) {
+            const int s0 = static_cast<int>(min(max(static_cast<int64_t>(a.seg[e]), int64_t(0)), limit));
+            const int s1 = static_cast<int>(min(max(static_cast<int64_t>(a.seg[e + 1]), int64_t(0)), limit));
+            g->seg[e] = s0;
+            if (e == a.experts - 1) g->seg[a.experts] = s1;
+            if (a.mode == kFp4GroupRows) {
+                int64_t c = min(static_cast<int64_t>(a.count[e]), static_cast<int64_t>(s1 - s0));
+                if (a.max_rows > 0) c = min(c, a.max_rows);
+                g->count[e] = static_cast<int>(max(c, int64_t(0)));
+                tiles = (g->count[e] + TM - 1) / TM * nt;
+            } else {
+                tiles = mt * nt;
+            }
+        }
+        int incl = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (e < a.experts) g->before[e] = run + incl - tiles;
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) g->before[a.experts] = run;
+    return run;
+}
+
+// Tile t.  Dense tiles are rastered with A's tiles fastest within a group of
+// group_m (raster_tile); an expert's likewise over its own rows.
+template <int TM, int TN>
+__device__ __forceinline__ F4Tile f4_tile(const F4Args &a, const F4Groups *g, int t, int group_m) {
+    F4Tile w;
+    int e = 0;
+    if (a.mode != kFp4Dense) {
+        int lo = 0, hi = a.experts;  // before[lo] <= t < before[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (g->before[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        e = lo;
+        t -= g->before[e];
+    }
+    const int nt = static_cast<int>((a.n + TN - 1) / TN);
+    const int rows = a.mode == kFp4GroupRows ? g->count[e] : static_cast<int>(a.m);
+    const int mt = (rows + TM - 1) / TM;
+    int mi = 0, ni = 0;
+    raster_tile(t, mt, nt, group_m, mi, ni);
+    const int first = a.mode == kFp4GroupRows ? g->seg[e] : 0;
+    w.a_row = first + mi * TM;
+    w.n0 = ni * TN;
+    w.b_row = (a.mode == kFp4GroupRows ? e * static_cast<int>(a.n) : 0) + w.n0;
+    w.sa = a.sa + (w.a_row / 128) * a.row_tile_bytes;
+    w.sb = a.sb + (a.mode == kFp4GroupRows ? e * a.sb_expert_bytes : 0) + (w.n0 / 128) * a.row_tile_bytes;
+    w.kb0 = 0;
+    w.kb1 = a.kblocks;
+    w.c_row = w.a_row;
+    if (a.mode == kFp4GroupK) {
+        w.kb0 = g->seg[e] / kF4KB;
+        w.kb1 = g->seg[e + 1] / kF4KB;
+        w.c_row += e * a.m;
+    }
+    w.m_valid = min(TM, rows - mi * TM);
+    w.n_valid = static_cast<int>(min(static_cast<int64_t>(TN), a.n - w.n0));
+    return w;
+}
+
+template <bool F32>
+__device__ __forceinline__ void store_c(void *c, int64_t at, float v, int accumulate) {
+    if (F32) {
+        float *p = static_cast<float *>(c) + at;
+        *p = accumulate ? *p + v : v;
+    } else {
+        static_cast<uint16_t *>(c)[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+    }
+}
+
+// ------------------------------------------------------------------- f4_small
+
+// BN columns: 32 for up to 32 tokens, 128 beyond.  A's scale tile holds 128 rows, so
+// a tile of 32 tokens starts at a multiple of 128 (there is only one).
+template <int BN_>
+struct F4Small {
+    static constexpr int BN = BN_;
+    static constexpr int kThreads = 192;           // TMA, MMA, four epilogue warps
+    static constexpr int kLBytes = 128 * 128;      // B's rows, on the lanes
+    static constexpr int kRBytes = BN * 128;       // A's rows, on the columns
+    static constexpr int kSfBytes = 1024;          // scales of 128 rows and a stage of K
+    static constexpr int kStageBytes = kLBytes + kRBytes + 2 * kSfBytes;
+    static constexpr int kDumpBytes = BN * 128 * 4;  // an fp32 tile, for the cluster's sum
+    static constexpr int kCtrlBytes = 4096;
+    static constexpr int kStages = (kSmemLimit - 1024 - kCtrlBytes - kDumpBytes) / kStageBytes;
+    static constexpr int kSmemBytes = 1024 + kCtrlBytes + kDumpBytes + kStages * kStageBytes;
+    // TMEM: two accumulators, then two sets of scales (8 columns each operand)
+    static constexpr int kSfCol = 2 * BN;
+    static constexpr int kSfSet = 16;
+    static constexpr uint32_t kTmemCols = kSfCol + 2 * kSfSet <= 128 ? 128u : 512u;
+    static_assert(kStages >= 3, "pipeline");
+    static_assert(sizeof(F4Groups) + 512 <= kCtrlBytes, "control block");
+};
+
+template <class C, bool F32>
+__global__ void __launch_bounds__(C::kThreads, 1)
+f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const F4Args args) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    constexpr int S = C::kStages;
+    uint8_t *lanes_s = smem;                                   // [S][128 rows][128 B]
+    uint8_t *cols_s = lanes_s + S * C::kLBytes;                // [S][BN rows][128 B]
+    uint8_t *sf_s = cols_s + S * C::kRBytes;                   // [S][2][1 KB]
+    float *dump = reinterpret_cast<float *>(sf_s + S * 2 * C::kSfBytes);  // [BN][128]
+    uint8_t *ctrl = reinterpret_cast<uint8_t *>(dump) + C::kDumpBytes;
+    uint64_t *full_bar = reinterpret_cast<uint64_t *>(ctrl);
+    uint64_t *empty_bar = full_bar + S;
+    uint64_t *accf_bar = empty_bar + S;
+    uint64_t *acce_bar = accf_bar + 2;
+    uint64_t *part_full = acce_bar + 2;   // every CTA of the cluster has its part in `dump`
+    uint64_t *part_empty = part_full + 1; // every CTA has read this CTA's part
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctrl + 384);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 388);
+    int *tiles_s = reinterpret_cast<int *>(ctrl + 392);
+    F4Groups *groups = reinterpret_cast<F4Groups *>(ctrl + 512);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cs = static_cast<int>(cluster_nctarank());
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int worker = static_cast<int>(blockIdx.x) / cs, workers = static_cast<int>(gridDim.x) / cs;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full_bar[s], 1);
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&accf_bar[b], 1);
+            mbar_init(&acce_bar[b], 4);
+        }
+        mbar_init(part_full, cs);
+        mbar_init(part_empty, cs);
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, C::kTmemCols);
+        tmem_relinquish_alloc_permit();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (cs > 1) cluster_sync();  // the peers' barriers exist before anyone arrives on them
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    griddep_enter();
+    if (warp == 0) {
+        int tiles;
+        if (args.mode == kFp4Dense)
+            tiles = static_cast<int>((args.m + C::BN - 1) / C::BN) * static_cast<int>((args.n + 127) / 128);
+        else
+            tiles = f4_groups<C::BN, 128>(args, groups, lane);
+        if (lane == 0) *tiles_s = tiles;
+    }
+    __syncthreads();
+    const int tiles = *tiles_s;
+    constexpr int kGroupM = 8;
+
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = worker; ok && t < tiles; t += workers) {
+                const F4Tile w = f4_tile<C::BN, 128>(args, groups, t, kGroupM);
+                const int nk = w.kb1 - w.kb0;
+                const int k0 = w.kb0 + nk * rank / cs, k1 = w.kb0 + nk * (rank + 1) / cs;
+                for (int kb = k0; kb < k1; ++kb) {
+                    ok = mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag);
+                    if (!ok) break;
+                    uint64_t *bar = &full_bar[stage];
+                    mbar_arrive_expect_tx(bar, C::kStageBytes);
+                    tma_load_2d(&tmB, bar, lanes_s + stage * C::kLBytes, kb * 128, w.b_row);
+                    tma_load_2d(&tmA, bar, cols_s + stage * C::kRBytes, kb * 128, w.a_row);
+                    uint8_t *sf = sf_s + stage * 2 * C::kSfBytes;
+                    bulk_copy_g2s(sf, w.sb + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes, bar);
+                    bulk_copy_g2s(sf + C::kSfBytes, w.sa + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes, bar);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            int stage = 0, it = 0, set = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = worker; ok && t < tiles; t += workers, ++it) {
+                const F4Tile w = f4_tile<C::BN, 128>(args, groups, t, kGroupM);
+                const int nk = w.kb1 - w.kb0;
+                const int k0 = w.kb0 + nk * rank / cs, k1 = w.kb0 + nk * (rank + 1) / cs;
+                const int buf = it & 1;
+                ok = mbar_wait(&acce_bar[buf], ((it >> 1) & 1) ^ 1u, abort_flag);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint32_t d = tmem_base + buf * C::BN;
+                for (int kb = k0; kb < k1; ++kb) {
+                    ok = mbar_wait(&full_bar[stage], phase, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint32_t la = smem_u32(lanes_s + stage * C::kLBytes);
+                    const uint32_t ca = smem_u32(cols_s + stage * C::kRBytes);
+                    const uint32_t sf = smem_u32(sf_s + stage * 2 * C::kSfBytes);
+                    const uint32_t sl = tmem_base + C::kSfCol + set * C::kSfSet, sc = sl + 8;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        tmem_copy_scales(sl + 4 * g, smem_desc_scales(sf + g * kFp4TileBytes));
+                        tmem_copy_scales(sc + 4 * g, smem_desc_scales(sf + C::kSfBytes + g * kFp4TileBytes));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        umma_mxf4(d, smem_desc_sw128(la + 32 * j, 16, 1024), smem_desc_sw128(ca + 32 * j, 16, 1024),
+                                  (j & 1) ? idesc_mxf4(128, C::BN, 2) : idesc_mxf4(128, C::BN, 0), sl + 4 * (j >> 1),
+                                  sc + 4 * (j >> 1), (kb > k0 || j > 0) ? 1u : 0u);
+                    umma_commit(&empty_bar[stage]);
+                    set ^= 1;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                umma_commit(&accf_bar[buf]);
+            }
+        }
+        __syncwarp();
+    } else {
+        // --------------------------------------------------------- epilogue
+        // A warp that gave up on a wait keeps walking (its waits then return at
+        // once), so that the barriers of the cluster's sum stay in step.
+        const int q = warp & 3;
+        const int i = 32 * q + lane;  // lane of the tile: C's column n0 + i
+        int it = 0;
+        for (int t = worker; t < tiles; t += workers, ++it) {
+            const F4Tile w = f4_tile<C::BN, 128>(args, groups, t, kGroupM);
+            const int nk = w.kb1 - w.kb0;
+            const bool some = nk * (rank + 1) / cs > nk * rank / cs;  // this CTA has a part of K
+            const int buf = it & 1;
+            bool ok = mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after_sync();
+            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * C::BN;
+            if (cs > 1) ok = mbar_wait_cluster(part_empty, (it & 1) ^ 1u, abort_flag) && ok;
+            ok = __all_sync(0xffffffffu, ok);
+            for (int c0 = 0; c0 < w.m_valid; c0 += 32) {
+                float v[32];
+                if (some && ok) {
+                    tmem_load_32cols(t_row + c0, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                }
+                if (cs > 1) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) dump[(c0 + j) * 128 + i] = v[j];
+                } else if (i < w.n_valid && ok) {
+                    const int64_t at = w.c_row * args.n + w.n0 + i;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c0 + j < w.m_valid) store_c<F32>(args.c, at + (c0 + j) * args.n, v[j], args.accumulate);
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_relaxed(&acce_bar[buf]);
+            if (cs > 1) {
+                named_barrier_sync(1, 128);
+                if (threadIdx.x >= 64 && threadIdx.x < 64 + cs)
+                    mbar_arrive_cluster(mapa_shared(smem_u32(part_full), threadIdx.x - 64));
+                ok = mbar_wait_cluster(part_full, it & 1, abort_flag) && ok;
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok && i < w.n_valid) {
+                    for (int c = rank; c < w.m_valid; c += cs) {
+                        float s = 0.0f;
+                        for (int r = 0; r < cs; ++r)
+                            s += ld_cluster_f32(mapa_shared(smem_u32(dump + c * 128 + i), r));
+                        store_c<F32>(args.c, (w.c_row + c) * args.n + w.n0 + i, s, args.accumulate);
+                    }
+                }
+                named_barrier_sync(1, 128);
+                if (threadIdx.x >= 64 && threadIdx.x < 64 + cs)
+                    mbar_arrive_cluster(mapa_shared(smem_u32(part_empty), threadIdx.x - 64));
+            }
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (cs > 1) cluster_sync();  // no CTA leaves while its part may be read
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem_base, C::kTmemCols);
+    }
+}
+
+// A code matrix as a 2-D byte array: box of 128 bytes (a stage of K) x `box_rows` rows.
+bool make_map_codes(CUtensorMap *m, const void *codes, int64_t rows, int64_t k, uint32_t box_rows) {
+    return make_map_2d(m, codes, kMapU8, static_cast<uint64_t>(fp4_row_bytes(k)), static_cast<uint64_t>(rows), 128, box_rows);
+}
+
+template <class C, bool F32>
+int run_small(const F4Args &a, const Fp4Product &p, int cs, int workers, cudaStream_t s) {
+    CUtensorMap mA, mB;
+    const int64_t a_rows = p.m, b_rows = p.mode == kFp4GroupRows ? p.n * p.experts : p.n;
+    if (!make_map_codes(&mA, p.a, a_rows, p.k, C::BN) || !make_map_codes(&mB, p.b, b_rows, p.k, 128)) return MLPBLK_ECUDA;
+    static int attr_set[64] = {0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return MLPBLK_ECUDA;
+    if (!attr_set[dev]) {
+        const int rc = cuda_status(cudaFuncSetAttribute(f4_small_kernel<C, F32>,
+                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes));
+        if (rc != MLPBLK_OK) return rc;
+        attr_set[dev] = 1;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(workers) * cs);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cs;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cs > 1 ? 2 : 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, f4_small_kernel<C, F32>, mA, mB, a));
+}
+
+}  // namespace
+
+int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s) {
+    F4Args a = {};
+    a.mode = p.mode;
+    a.m = p.m;
+    a.n = p.n;
+    a.kblocks = static_cast<int>((p.k + kF4KB - 1) / kF4KB);
+    a.experts = p.experts;
+    a.max_rows = p.max_rows;
+    a.sa = p.sa;
+    a.sb = p.sb;
+    a.row_tile_bytes = fp4_col_tiles(p.k) * kFp4TileBytes;
+    a.sb_expert_bytes = fp4_scales_bytes(p.n, p.k);
+    a.count = p.count;
+    a.seg = p.seg;
+    a.c = p.c;
+    a.accumulate = p.accumulate;
+    const bool f32 = p.out_dtype == MLPBLK_FP32;
+    int64_t rows = p.m;  // rows of one product, at most
+    int64_t groups = 1;
+    if (p.mode == kFp4GroupRows) {
+        if (p.max_rows > 0 && p.max_rows < rows) rows = p.max_rows;
+        groups = p.experts;
+    } else if (p.mode == kFp4GroupK) {
+        groups = p.experts;
+    }
+    const bool few = rows <= 32;
+    const int64_t bn = few ? 32 : 128;
+    const int64_t tiles = (rows + bn - 1) / bn * ((p.n + 127) / 128) * groups;
+    int cs = 1;
+    while (cs < 8 && tiles * cs * 2 <= num_sms && a.kblocks >= 4 * cs) cs *= 2;
+    int64_t workers = num_sms / cs;
+    if (workers < 1) workers = 1;
+    if (p.mode != kFp4GroupRows && tiles < workers) workers = tiles;
+    const int w = static_cast<int>(workers);
+    if (few) return f32 ? run_small<F4Small<32>, true>(a, p, cs, w, s) : run_small<F4Small<32>, false>(a, p, cs, w, s);
+    return f32 ? run_small<F4Small<128>, true>(a, p, cs, w, s) : run_small<F4Small<128>, false>(a, p, cs, w, s);
+}
+
+int take_device_error_gemm_f4() {
+    int v = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof(int)) != cudaSuccess) return MLPBLK_ECUDA;
+    if (v != 0) cudaMemcpyToSymbol(g_device_error, &z, sizeof(int));
+    return v;
+}
+
+}  // namespace mlpblk

@@ -1,0 +1,504 @@
+// sort.cu -- tokens sorted by expert and back ("Nemotron Kernels From Inference To
+// Backpropagation" -- "Kernel 4: Routed ReLU2 MoE": select, execute, weight and
+// combine), as operators of their own: the plan, the two moves and their gradients.
+//
+//   plan       rank of entry i among the entries of its expert; pos[i] = seg + rank
+//   permute    rows[pos[t,j]] = x[t]                dx[t] = sum_j d_rows[pos[t,j]]
+//   unpermute  y[t] = residual[t] + sum_j w[t,j] * rows[pos[t,j]]
+//              d_rows[pos[t,j]] = w[t,j] * dy[t],   dw[t,j] = <dy[t], rows[pos[t,j]]>
+//
+// The moves are bound by HBM.  All of them walk the tokens, not the sorted rows: a
+// token's row is then read (or written) once for all of its slots.
+#include "mlpblk_internal.h"
+
+namespace mlpblk {
+
+namespace {
+
+// ------------------------------------------------------------------- the plan
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortExperts = 256;
+constexpr int kSortCluster = 8;        // CTAs of a large plan (the portable cluster size)
+constexpr int64_t kSortOneCta = 4096;  // entries up to which one CTA makes the plan
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ int ld_cluster(const int *local, unsigned rank) {
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(local)), r;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(r) : "memory");
+    return v;
+}
+
+// One cluster makes the whole plan in one launch: CTA c of C takes a contiguous
+// range of the entries, warp w a contiguous part of that, so ranks follow entry
+// order.  Pass 1 counts per warp and expert (lanes with the same expert find each
+// other by match_any); the counts' prefixes run over warps in shared memory and over
+// the CTAs through distributed shared memory; pass 2 reads the ids again (from L1 or
+// L2) and places.  Bound by latency: two passes and two cluster barriers.
+__global__ void __launch_bounds__(kSortThreads)
+sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_t R, int64_t per_warp,
+            int *__restrict__ count, int *__restrict__ seg, int *__restrict__ pos, int *__restrict__ row_map) {
+    __shared__ int wcnt[kSortWarps][kSortExperts];
+    __shared__ int ctot[kSortExperts];       // this CTA's entries per expert (read by the cluster)
+    __shared__ int segs[kSortExperts + 1];
+    __shared__ int live[kSortExperts];       // every CTA's entries per expert
+    __shared__ int scan[kSortExperts / 32];
+    griddep_enter();
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int C = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+    const unsigned lt = (1u << lane) - 1u;
+    for (int e = tid; e < kSortWarps * kSortExperts; e += kSortThreads) (&wcnt[0][0])[e] = 0;
+    __syncthreads();
+    const int64_t w0 = (static_cast<int64_t>(c) * kSortWarps + wid) * per_warp;
+    const int64_t w1 = min(n, w0 + per_warp);
+    for (int64_t g = w0; g < w1; g += 32) {
+        const int64_t i = g + lane;
+        int e = i < w1 ? idx[i] : -1;
+        if (e < 0 || e >= experts) e = -1;
+        const unsigned peers = __match_any_sync(0xffffffffu, e);
+        if (e >= 0 && (peers & lt) == 0) wcnt[wid][e] += __popc(peers);
+        __syncwarp();
+    }
+    __syncthreads();
+    if (tid < kSortExperts) {
+        int run = 0;
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int v = wcnt[w][tid];
+            wcnt[w][tid] = run;
+            run += v;
+        }
+        ctot[tid] = run;
+    }
+    if (C > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    int before = 0, all = 0, padded = 0, incl = 0;
+    if (tid < kSortExperts) {
+        if (C > 1) {
+#pragma unroll
+            for (int r = 0; r < kSortCluster; ++r) {
+                const int v = r < C ? ld_cluster(&ctot[tid], r) : 0;
+                before += r < c ? v : 0;
+                all += v;
+            }
+        } else {
+            all = ctot[tid];
+        }
+        live[tid] = all;
+        padded = (all + pad - 1) / pad * pad;
+        incl = padded;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) scan[wid] = incl;
+    }
+    if (C > 1) cluster_arrive();  // this CTA has read the others' counts
+    __syncthreads();
+    if (tid < kSortExperts) {
+        int off = 0;
+        for (int w = 0; w < wid; ++w) off += scan[w];
+        segs[tid + 1] = off + incl;
+        if (tid == 0) segs[0] = 0;
+        // the first row of each warp's entries
+        for (int w = 0; w < kSortWarps; ++w) wcnt[w][tid] += off + incl - padded + before;
+    }
+    __syncthreads();
+    if (c == 0) {
+        if (tid < experts) count[tid] = live[tid];
+        if (tid <= experts) seg[tid] = segs[tid];
+    }
+    for (int64_t g = w0; g < w1; g += 32) {
+        const int64_t i = g + lane;
+        int e = i < w1 ? idx[i] : -1;
+        if (e < 0 || e >= experts) e = -1;
+        const unsigned peers = __match_any_sync(0xffffffffu, e);
+        const int base = e >= 0 ? wcnt[wid][e] : 0;
+        __syncwarp();
+        if (e >= 0 && (peers & lt) == 0) wcnt[wid][e] = base + __popc(peers);
+        __syncwarp();
+        if (i < w1) {
+            const int p = e < 0 ? -1 : base + __popc(peers & lt);
+            pos[i] = p;
+            if (p >= 0) row_map[p] = static_cast<int>(i);
+        }
+    }
+    // rows without an entry: the segments' padding and what lies behind them
+    if (pad > 1)
+        for (int e = c * kSortWarps + wid; e < experts; e += C * kSortWarps)
+            for (int r = segs[e] + live[e] + lane; r < segs[e + 1]; r += 32) row_map[r] = -1;
+    for (int64_t r = static_cast<int64_t>(segs[experts]) + c * kSortThreads + tid; r < R; r += C * kSortThreads)
+        row_map[r] = -1;
+    if (C > 1) cluster_wait();  // no CTA leaves while its counts are being read
+}
+
+// ------------------------------------------------------------------ the moves
+
+// A row is `units` accesses of type U (16, 4 or 2 bytes: the widest that divides
+// a row).  blockDim = (threads of a row, rows of a block); a thread holds kPer units
+// at a time, so a row of 4096 bf16 values is two 16-byte accesses for each of 256
+// threads.
+constexpr int kMoveThreads = 256;
+constexpr int kPer = 4;
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+// The float values of one access, and back.
+template <class U, bool BF16>
+struct Vals;
+template <>
+struct Vals<uint4, true> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void get(uint4 u, float (&v)[8]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 put(const float (&v)[8]) {
+        return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+    }
+};
+template <>
+struct Vals<uint32_t, true> {
+    static constexpr int N = 2;
+    static __device__ __forceinline__ void get(uint32_t u, float (&v)[2]) {
+        v[0] = __uint_as_float(u << 16);
+        v[1] = __uint_as_float(u & 0xFFFF0000u);
+    }
+    static __device__ __forceinline__ uint32_t put(const float (&v)[2]) { return pack2(v[0], v[1]); }
+};
+template <>
+struct Vals<uint16_t, true> {
+    static constexpr int N = 1;
+    static __device__ __forceinline__ void get(uint16_t u, float (&v)[1]) {
+        v[0] = __uint_as_float(static_cast<uint32_t>(u) << 16);
+    }
+    static __device__ __forceinline__ uint16_t put(const float (&v)[1]) {
+        return static_cast<uint16_t>(pack2(v[0], 0.0f) & 0xFFFFu);
+    }
+};
+template <>
+struct Vals<uint4, false> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void get(uint4 u, float (&v)[4]) {
+        v[0] = __uint_as_float(u.x);
+        v[1] = __uint_as_float(u.y);
+        v[2] = __uint_as_float(u.z);
+        v[3] = __uint_as_float(u.w);
+    }
+    static __device__ __forceinline__ uint4 put(const float (&v)[4]) {
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    }
+};
+template <>
+struct Vals<uint32_t, false> {
+    static constexpr int N = 1;
+    static __device__ __forceinline__ void get(uint32_t u, float (&v)[1]) { v[0] = __uint_as_float(u); }
+    static __device__ __forceinline__ uint32_t put(const float (&v)[1]) { return __float_as_uint(v[0]); }
+};
+
+template <class U>
+__device__ __forceinline__ U zero_unit() {
+    U z;
+    memset(&z, 0, sizeof(U));
+    return z;
+}
+
+// Padding row number q of the plan (q / pad = expert, q % pad = which): its row, or -1.
+__device__ __forceinline__ int64_t padding_row(int64_t q, int pad, int experts, const int *count, const int *seg) {
+    const int64_t e = q / pad;
+    if (e >= experts) return -1;
+    const int64_t r = static_cast<int64_t>(seg[e]) + count[e] + q % pad;
+    return r < seg[e + 1] ? r : -1;
+}
+
+template <class U>
+__device__ __forceinline__ void zero_row(U *row, int64_t units) {
+    for (int64_t c = threadIdx.x; c < units; c += blockDim.x) row[c] = zero_unit<U>();
+}
+
+// rows[pos[t,j]] = x[t]; the blocks behind the tokens' zero the padding rows.
+template <class U>
+__global__ void __launch_bounds__(kMoveThreads)
+permute_kernel(const U *__restrict__ x, const int *__restrict__ pos, const int *__restrict__ count,
+               const int *__restrict__ seg, int64_t T, int k, int experts, int pad, int64_t units, int64_t token_blocks,
+               U *__restrict__ rows) {
+    griddep_enter();
+    const int64_t b = blockIdx.x;
+    if (b >= token_blocks) {
+        const int64_t r = padding_row((b - token_blocks) * blockDim.y + threadIdx.y, pad, experts, count, seg);
+        if (r >= 0) zero_row(rows + r * units, units);
+        return;
+    }
+    const int64_t t = b * blockDim.y + threadIdx.y;
+    if (t >= T) return;
+    const U *src = x + t * units;
+    const int *pt = pos + t * k;
+    for (int64_t c0 = threadIdx.x; c0 < units; c0 += kPer * blockDim.x) {
+        U v[kPer];
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int64_t c = c0 + u * blockDim.x;
+            v[u] = c < units ? __ldg(src + c) : zero_unit<U>();
+        }
+        for (int j = 0; j < k; ++j) {
+            const int64_t r = pt[j];
+            if (r < 0) continue;
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) {
+                const int64_t c = c0 + u * blockDim.x;
+                if (c < units) rows[r * units + c] = v[u];
+            }
+        }
+    }
+}
+
+// y[t] = residual[t] + sum_j w[t,j] * rows[pos[t,j]], slot order, float32, rounded
+// once.  residual and y may be the same array: an element is read and written by
+// the same thread.
+template <class U, bool BF16>
+__global__ void __launch_bounds__(kMoveThreads)
+unpermute_kernel(const U *__restrict__ rows, const int *__restrict__ pos, const float *__restrict__ weights,
+                 const U *residual, int64_t T, int k, int64_t units, U *y) {
+    using V = Vals<U, BF16>;
+    griddep_enter();
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (t >= T) return;
+    const int *pt = pos + t * k;
+    for (int64_t c0 = threadIdx.x; c0 < units; c0 += kPer * blockDim.x) {
+        float acc[kPer][V::N];
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int64_t c = c0 + u * blockDim.x;
+            if (residual && c < units) {
+                V::get(residual[t * units + c], acc[u]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V::N; ++i) acc[u][i] = 0.0f;
+            }
+        }
+        for (int j = 0; j < k; ++j) {
+            const int64_t r = pt[j];
+            if (r < 0) continue;
+            const float w = weights ? weights[t * k + j] : 1.0f;
+            U o[kPer];
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) {
+                const int64_t c = c0 + u * blockDim.x;
+                o[u] = c < units ? __ldg(rows + r * units + c) : zero_unit<U>();
+            }
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) {
+                float f[V::N];
+                V::get(o[u], f);
+#pragma unroll
+                for (int i = 0; i < V::N; ++i) acc[u][i] += w * f[i];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int64_t c = c0 + u * blockDim.x;
+            if (c < units) y[t * units + c] = V::put(acc[u]);
+        }
+    }
+}
+
+// d_rows[pos[t,j]] = w[t,j] * dy[t] and dw[t,j] = <dy[t], rows[pos[t,j]]>.  Slots go
+// in groups of kSlots whose dot products are held together, so dy is read from
+// HBM once; a dot product is summed over the row's threads by shuffles, then over
+// its warps in warp order.  d_weights NULL skips the products and rows.
+constexpr int kSlots = 4;
+
+template <class U, bool BF16>
+__global__ void __launch_bounds__(kMoveThreads)
+unpermute_bwd_kernel(const U *__restrict__ dy, const U *__restrict__ rows, const int *__restrict__ pos,
+                     const int *__restrict__ count, const int *__restrict__ seg, const float *__restrict__ weights,
+                     int64_t T, int k, int experts, int pad, int64_t units, int64_t token_blocks,
+                     U *__restrict__ d_rows, float *__restrict__ d_weights) {
+    using V = Vals<U, BF16>;
+    __shared__ float part[kSlots][kMoveThreads / 32];
+    griddep_enter();
+    const int64_t b = blockIdx.x;
+    if (b >= token_blocks) {
+        const int64_t r = padding_row((b - token_blocks) * blockDim.y + threadIdx.y, pad, experts, count, seg);
+        if (r >= 0) zero_row(d_rows + r * units, units);
+        return;
+    }
+    const int64_t t = b * blockDim.y + threadIdx.y;
+    const bool in = t < T;
+    const int warps = blockDim.x / 32;  // of a row
+    const int w0 = threadIdx.y * warps;
+    for (int j0 = 0; j0 < k; j0 += kSlots) {
+        float s[kSlots];
+        int r[kSlots];
+        float w[kSlots];
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+            const bool on = in && j0 + j < k;
+            s[j] = 0.0f;
+            r[j] = on ? pos[t * k + j0 + j] : -1;
+            w[j] = on && weights ? weights[t * k + j0 + j] : 1.0f;
+        }
+        for (int64_t c0 = threadIdx.x; in && c0 < units; c0 += kPer * blockDim.x) {
+            U g[kPer];
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) {
+                const int64_t c = c0 + u * blockDim.x;
+                g[u] = c < units ? __ldg(dy + t * units + c) : zero_unit<U>();
+            }
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j) {
+                if (r[j] < 0) continue;
+                U o[kPer];
+                if (d_weights) {
+#pragma unroll
+                    for (int u = 0; u < kPer; ++u) {
+                        const int64_t c = c0 + u * blockDim.x;
+                        o[u] = c < units ? __ldg(rows + r[j] * units + c) : zero_unit<U>();
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kPer; ++u) {
+                    const int64_t c = c0 + u * blockDim.x;
+                    if (c >= units) continue;
+                    float a[V::N];
+                    V::get(g[u], a);
+                    if (d_weights) {
+                        float f[V::N];
+                        V::get(o[u], f);
+#pragma unroll
+                        for (int i = 0; i < V::N; ++i) s[j] += a[i] * f[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < V::N; ++i) a[i] *= w[j];
+                    d_rows[r[j] * units + c] = V::put(a);
+                }
+            }
+        }
+        if (!d_weights) continue;
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+            if ((threadIdx.x & 31) == 0) part[j][w0 + threadIdx.x / 32] = s[j];
+        }
+        __syncthreads();
+        if (in && threadIdx.x < kSlots && j0 + threadIdx.x < k) {
+            float d = 0.0f;
+            for (int q = 0; q < warps; ++q) d += part[threadIdx.x][w0 + q];
+            d_weights[t * k + j0 + threadIdx.x] = d;
+        }
+        __syncthreads();
+    }
+}
+
+// The shape of a move: bytes of an access, accesses of a row, threads of a row.
+struct MoveShape {
+    int unit;
+    int64_t units;
+    dim3 block;
+    int64_t token_blocks, pad_blocks;
+};
+
+MoveShape move_shape(int64_t T, int64_t width, int dtype, int experts, int pad) {
+    MoveShape m;
+    const int64_t bytes = width * (dtype == MLPBLK_BF16 ? 2 : 4);
+    m.unit = bytes % 16 == 0 ? 16 : (bytes % 4 == 0 ? 4 : 2);
+    m.units = bytes / m.unit;
+    unsigned tx = 32;
+    while (tx < static_cast<unsigned>(kMoveThreads) && tx * 2 < m.units) tx *= 2;
+    m.block = dim3(tx, kMoveThreads / tx, 1);
+    m.token_blocks = (T + m.block.y - 1) / m.block.y;
+    m.pad_blocks = pad > 1 ? (static_cast<int64_t>(experts) * pad + m.block.y - 1) / m.block.y : 0;
+    return m;
+}
+
+}  // namespace
+
+int launch_sort(const int *idx, int64_t n, int experts, int pad, int64_t R, int *count, int *seg, int *pos,
+                int *row_map, cudaStream_t s) {
+    const int C = n <= kSortOneCta ? 1 : kSortCluster;
+    int64_t per_warp = (n + static_cast<int64_t>(C) * kSortWarps - 1) / (static_cast<int64_t>(C) * kSortWarps);
+    per_warp = (per_warp + 31) / 32 * 32;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 2 : 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, sort_kernel, idx, n, experts, pad, R, per_warp, count, seg, pos, row_map));
+}
+
+int launch_permute(const void *x, const int *pos, const int *count, const int *seg, int64_t T, int64_t width,
+                   int dtype, int k, int experts, int pad, void *rows, cudaStream_t s) {
+    const MoveShape m = move_shape(T, width, dtype, experts, pad);
+    const dim3 grid(static_cast<unsigned>(m.token_blocks + m.pad_blocks));
+#define MLPBLK_PERMUTE(U)                                                                                      \
+    return launch_pdl(permute_kernel<U>, grid, m.block, 0, s, static_cast<const U *>(x), pos, count, seg, T, k, \
+                      experts, pad, m.units, m.token_blocks, static_cast<U *>(rows))
+    if (m.unit == 16) MLPBLK_PERMUTE(uint4);
+    if (m.unit == 4) MLPBLK_PERMUTE(uint32_t);
+    MLPBLK_PERMUTE(uint16_t);
+#undef MLPBLK_PERMUTE
+}
+
+int launch_unpermute(const void *rows, const int *pos, const float *weights, const void *residual, int64_t T,
+                     int64_t width, int dtype, int k, void *y, cudaStream_t s) {
+    const MoveShape m = move_shape(T, width, dtype, 1, 1);
+    const dim3 grid(static_cast<unsigned>(m.token_blocks));
+#define MLPBLK_UNPERMUTE(U, B)                                                                              \
+    return launch_pdl(unpermute_kernel<U, B>, grid, m.block, 0, s, static_cast<const U *>(rows), pos, weights, \
+                      static_cast<const U *>(residual), T, k, m.units, static_cast<U *>(y))
+    if (dtype == MLPBLK_BF16) {
+        if (m.unit == 16) MLPBLK_UNPERMUTE(uint4, true);
+        if (m.unit == 4) MLPBLK_UNPERMUTE(uint32_t, true);
+        MLPBLK_UNPERMUTE(uint16_t, true);
+    }
+    if (m.unit == 16) MLPBLK_UNPERMUTE(uint4, false);
+    MLPBLK_UNPERMUTE(uint32_t, false);
+#undef MLPBLK_UNPERMUTE
+}
+
+int launch_unpermute_bwd(const void *dy, const void *rows, const int *pos, const int *count, const int *seg,
+                         const float *weights, int64_t T, int64_t width, int dtype, int k, int experts, int pad,
+                         void *d_rows, float *d_weights, cudaStream_t s) {
+    const MoveShape m = move_shape(T, width, dtype, experts, pad);
+    const dim3 grid(static_cast<unsigned>(m.token_blocks + m.pad_blocks));
+#define MLPBLK_UNPERMUTE_BWD(U, B)                                                                               \
+    return launch_pdl(unpermute_bwd_kernel<U, B>, grid, m.block, 0, s, static_cast<const U *>(dy),                 \
+                      static_cast<const U *>(rows), pos, count, seg, weights, T, k, experts, pad, m.units,        \
+                      m.token_blocks, static_cast<U *>(d_rows), d_weights)
+    if (dtype == MLPBLK_BF16) {
+        if (m.unit == 16) MLPBLK_UNPERMUTE_BWD(uint4, true);
+        if (m.unit == 4) MLPBLK_UNPERMUTE_BWD(uint32_t, true);
+        MLPBLK_UNPERMUTE_BWD(uint16_t, true);
+    }
+    if (m.unit == 16) MLPBLK_UNPERMUTE_BWD(uint4, false);
+    MLPBLK_UNPERMUTE_BWD(uint32_t, false);
+#undef MLPBLK_UNPERMUTE_BWD
+}
+
+}  // namespace mlpblk

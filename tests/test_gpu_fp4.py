@@ -1,0 +1,493 @@
+"""MXFP4 quantisation, reading back and products against the float64 oracle
+(oracle.fp4), GB300 only.
+
+Codes, scales and values read back are compared exactly: the scaling is by a power
+of two and an element is rounded once.
+
+Products: the operands' values are multiples of half their scale with at most 3
+bits, so a block's 32 products add exactly; the K/32 scaled block sums are added in
+float32.  Bound of an output: acc * sum|a||b| with acc = (K/32 + 2) * 2^-23 (one
+float32 step, truncation included, an addition), plus half a step of the output
+type (bf16 2^-8 relative to its value).  With all scales equal and small integers
+every partial sum is a multiple of 1/4 below 2^22, so those products are exact.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import fp4, sort
+from helpers import to_np
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mb():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import mlp_block_backprop_gb300 as mb
+    yield mb
+    assert mb.mlpblk_last_error() == mb.MLPBLK_OK
+
+
+def _dt(name):
+    import torch
+    return {"bf16": torch.bfloat16, "f32": torch.float32}[name]
+
+
+def _dev(a, dtype):
+    import torch
+    return torch.from_numpy(np.array(a, dtype=np.float32)).cuda().to(_dt(dtype))
+
+
+def _draw(rng, shape, dtype):
+    """Normal values with blocks of very different sizes, some of them zero."""
+    v = rng.standard_normal(shape) * np.exp2(rng.integers(-20, 20, size=(shape[0], 1)))
+    v[rng.random(shape) < 0.05] = 0.0
+    if shape[0] > 3:
+        v[2] = 0.0
+    t = _dev(v, dtype)
+    return t, to_np(t)
+
+
+def _bytes(t):
+    return t.cpu().numpy()
+
+
+# ------------------------------------------------------- quantise and read back
+
+SHAPES = [(1, 1), (1, 32), (3, 31), (5, 33), (8, 4096), (31, 256), (127, 257), (128, 128), (129, 1000), (300, 520)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_quantize_rows(mb, shape, dtype):
+    import torch
+    x, v = _draw(np.random.default_rng(sum(shape)), shape, dtype)
+    q = mb.Fp4Matrix(*shape)
+    q.codes.fill_(0xAA)
+    q.scales.fill_(0xAA)
+    q.quantize(x)
+    codes, scales = fp4.quantize(v)
+    packed, tiled = fp4.pack(codes, scales)
+    np.testing.assert_array_equal(_bytes(q.scales), tiled)
+    np.testing.assert_array_equal(_bytes(q.codes), packed)
+    for out in ("bf16", "f32"):
+        y = torch.full(shape, float("nan"), dtype=_dt(out), device="cuda")
+        q.dequantize(y)
+        np.testing.assert_array_equal(to_np(y), fp4.values(codes, scales, shape[1]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_quantize_transposed(mb, shape, dtype):
+    x, v = _draw(np.random.default_rng(sum(shape) + 1), shape[::-1], dtype)
+    q = mb.Fp4Matrix(*shape)
+    q.codes.fill_(0xAA)
+    q.scales.fill_(0xAA)
+    q.quantize(x, transposed=True)
+    packed, tiled = fp4.pack(*fp4.quantize(v.T))
+    np.testing.assert_array_equal(_bytes(q.scales), tiled)
+    np.testing.assert_array_equal(_bytes(q.codes), packed)
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+def test_quantize_relu2_and_special_values(mb, transposed):
+    rng = np.random.default_rng(3)
+    v = rng.standard_normal((70, 100))
+    v[4, 5], v[40, 70], v[69, 99], v[10, 10] = np.inf, np.nan, -np.inf, 3e38
+    v[20, :] = 1e-39                                        # float32 subnormals
+    x = _dev(v, "f32")
+    w = to_np(x).T if transposed else to_np(x)
+    for act in ("none", "relu2"):
+        a = w
+        if act == "relu2":
+            a = np.where(w < 0, 0.0, w).astype(np.float32)
+            with np.errstate(over="ignore"):
+                a = (a * a).astype(np.float64)             # float32 squares: the largest becomes infinite
+        q = mb.Fp4Matrix(*w.shape)
+        q.quantize(x, transposed=transposed, act=act)
+        packed, tiled = fp4.pack(*fp4.quantize(a))
+        np.testing.assert_array_equal(_bytes(q.scales), tiled)
+        np.testing.assert_array_equal(_bytes(q.codes) & 0x77, packed & 0x77)
+        import torch
+        y = torch.empty(w.shape, dtype=torch.float32, device="cuda")
+        q.dequantize(y)
+        np.testing.assert_array_equal(to_np(y), fp4.rounded(a))
+
+
+def test_quantize_batch(mb):
+    import torch
+    x, v = _draw(np.random.default_rng(4), (3 * 130, 72), "bf16")
+    q = mb.Fp4Matrix(130, 72, batch=3)
+    q.quantize(x)
+    packs = [fp4.pack(*fp4.quantize(v[130 * i:130 * i + 130])) for i in range(3)]
+    np.testing.assert_array_equal(_bytes(q.codes), np.concatenate([p[0] for p in packs]))
+    np.testing.assert_array_equal(_bytes(q.scales), np.concatenate([p[1] for p in packs]))
+    y = torch.empty(3, 130, 72, dtype=torch.float32, device="cuda")
+    q.dequantize(y)
+    np.testing.assert_array_equal(to_np(y), np.stack([fp4.rounded(v[130 * i:130 * i + 130]) for i in range(3)]))
+    qt = mb.Fp4Matrix(72, 130, batch=3)
+    qt.quantize(x, transposed=True)
+    packs = [fp4.pack(*fp4.quantize(v[130 * i:130 * i + 130].T)) for i in range(3)]
+    np.testing.assert_array_equal(_bytes(qt.codes), np.concatenate([p[0] for p in packs]))
+    np.testing.assert_array_equal(_bytes(qt.scales), np.concatenate([p[1] for p in packs]))
+
+
+def _routed(mb, T, width, E, k, pad, seed, dead=()):
+    import torch
+    rng = np.random.default_rng(seed)
+    idx = rng.integers(0, E, (T, k)).astype(np.int32)
+    for e in dead:
+        idx[idx == e] = (e + 1) % E
+    if T > 2 and k > 1:
+        idx[1, 0] = -1
+        idx[2, :] = idx[2, 0]                               # an expert named k times
+    s = mb.MoeSort(T, width, E, k, pad)
+    s.sort(torch.from_numpy(idx).cuda())
+    return s, sort.plan(idx, E, pad)
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("gather", [False, True])
+def test_quantize_through_a_sort(mb, transposed, gather):
+    import torch
+    T, d, E, k, pad = 45, 90, 5, 2, 128
+    s, (count, seg, pos, row_map) = _routed(mb, T, d, E, k, pad, 5)
+    R = s.rows
+    x, v = _draw(np.random.default_rng(6), (T if gather else R, d), "bf16")
+    live = row_map >= 0
+    src = np.where(live[:, None], v[np.maximum(row_map, 0) // k] if gather else v, 0.0)
+    if not gather:                                          # what no entry owns is not read
+        x[torch.from_numpy(~live).cuda()] = float("nan")
+    shape = (d, R) if transposed else (R, d)
+    q = mb.Fp4Matrix(*shape)
+    q.quantize(x, sort=s, gather=gather, transposed=transposed)
+    packed, tiled = fp4.pack(*fp4.quantize(src.T if transposed else src))
+    np.testing.assert_array_equal(_bytes(q.scales), tiled)
+    np.testing.assert_array_equal(_bytes(q.codes), packed)
+
+
+# ---------------------------------------------------------------------- products
+
+def _check(got, a, b, out, k, base=None):
+    ref, mag = fp4.product(a, b)
+    if base is not None:
+        ref, mag = ref + base, mag + np.abs(base)
+    tol = (-(-k // 32) + 2 + (base is not None)) * 2.0 ** -23 * mag + (2.0 ** -8 * np.abs(ref) if out == "bf16" else 0.0)
+    bad = ~(np.abs(got - ref) <= tol)
+    assert not bad.any(), (int(bad.sum()), got[bad][:4], ref[bad][:4])
+
+
+def _quantized(mb, rng, rows, cols, batch=1, wide=True):
+    import torch
+    v = rng.standard_normal((batch * rows, cols))
+    if wide:
+        v *= np.exp2(rng.integers(-6, 6, size=(batch * rows, 1)))
+    x = torch.from_numpy(v.astype(np.float32)).cuda()
+    q = mb.Fp4Matrix(rows, cols, batch=batch)
+    q.quantize(x)
+    vals = np.stack([fp4.rounded(to_np(x)[i * rows:(i + 1) * rows]) for i in range(batch)])
+    return q, vals if batch > 1 else vals[0]
+
+
+@pytest.mark.parametrize("shape", [(1, 128, 256), (32, 128, 64), (128, 128, 1024), (256, 512, 512)])
+def test_product_exact(mb, shape):
+    """Codes of every value with scale 1, each row its own pattern: sums are exact,
+    and a wrong lane, column, K order or scale would show."""
+    import torch
+    m, n, k = shape
+    rng = np.random.default_rng(k)
+    a = rng.choice(np.concatenate([fp4.VALUES, -fp4.VALUES]), size=(m, k))
+    b = rng.choice(np.concatenate([fp4.VALUES, -fp4.VALUES]), size=(n, k))
+    a[:, ::32], b[:, ::32] = 6.0, -6.0                       # every block's scale is 1
+    qa, qb = mb.Fp4Matrix(m, k), mb.Fp4Matrix(n, k)
+    qa.quantize(torch.from_numpy(a.astype(np.float32)).cuda())
+    qb.quantize(torch.from_numpy(b.astype(np.float32)).cuda())
+    c = torch.full((m, n), float("nan"), device="cuda")
+    qa.matmul(qb, c)
+    np.testing.assert_array_equal(to_np(c), a @ b.T)
+
+
+@pytest.mark.parametrize("m", [1, 32, 128])
+def test_product_scales(mb, m):
+    """One non-zero element a row, scales that differ by row and block: each output is
+    one exact product, so every scale must reach its own row and block of K."""
+    import torch
+    n, k = 256, 1024
+    rng = np.random.default_rng(m)
+    a, b = np.zeros((m, k)), np.exp2(rng.integers(-8, 8, size=(n, k // 32))).repeat(32, axis=1)
+    a[np.arange(m), rng.integers(0, k, m)] = np.exp2(rng.integers(-8, 8, m))
+    qa, qb = mb.Fp4Matrix(m, k), mb.Fp4Matrix(n, k)
+    qa.quantize(torch.from_numpy(a.astype(np.float32)).cuda())
+    qb.quantize(torch.from_numpy(b.astype(np.float32)).cuda())
+    c = torch.full((m, n), float("nan"), device="cuda")
+    qa.matmul(qb, c)
+    np.testing.assert_array_equal(to_np(c), a @ b.T)
+
+
+PRODUCTS = [
+    (1, 1, 1), (1, 130, 32), (2, 64, 100), (8, 1000, 2049), (31, 257, 4096), (33, 129, 255), (40, 4096, 300),
+    (128, 256, 256), (129, 127, 512), (333, 1000, 1031), (257, 384, 8200), (1, 300, 16384), (1000, 70, 640),
+    (512, 1024, 768), (1025, 2050, 1000), (2048, 2048, 512), (2305, 1536, 288), (4, 16384, 4096),
+]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", PRODUCTS)
+def test_product(mb, shape, out):
+    import torch
+    m, n, k = shape
+    rng = np.random.default_rng(m + n + k)
+    qa, a = _quantized(mb, rng, m, k)
+    qb, b = _quantized(mb, rng, n, k)
+    c = torch.full((m, n), float("nan"), dtype=_dt(out), device="cuda")
+    qa.matmul(qb, c)
+    _check(to_np(c), a, b, out, k)
+
+
+@pytest.mark.parametrize("shape", [(1, 130, 64), (33, 129, 300), (200, 256, 2048), (1030, 1100, 520), (2048, 2304, 300)])
+def test_product_accumulates(mb, shape):
+    import torch
+    m, n, k = shape
+    rng = np.random.default_rng(m)
+    qa, a = _quantized(mb, rng, m, k)
+    qb, b = _quantized(mb, rng, n, k)
+    c = torch.from_numpy(rng.standard_normal((m, n)).astype(np.float32)).cuda()
+    base = to_np(c)
+    qa.matmul(qb, c, accumulate=True)
+    _check(to_np(c), a, b, "f32", k, base)
+
+
+def test_product_leaves_the_neighbours_alone(mb):
+    """C in the middle of a larger buffer: nothing before or behind it is touched."""
+    import torch
+    rng = np.random.default_rng(8)
+    for m, n, k in ((5, 100, 64), (300, 333, 96), (700, 1000, 64)):
+        for out in ("bf16", "f32"):
+            qa, a = _quantized(mb, rng, m, k)
+            qb, b = _quantized(mb, rng, n, k)
+            whole = torch.full((m * n + 2048,), 7.0, dtype=_dt(out), device="cuda")
+            c = whole[1024:1024 + m * n]
+            mb.mlpblk_fp4_matmul(mb.make_fp4_matmul_desc(m, n, k, out), qa.codes, qa.scales, qb.codes, qb.scales, c)
+            _check(to_np(c).reshape(m, n), a, b, out, k)
+            assert bool((whole[:1024] == 7.0).all()) and bool((whole[1024 + m * n:] == 7.0).all())
+
+
+@pytest.mark.parametrize("m", [3, 200, 600])
+def test_product_nan_rows_stay_in_their_row(mb, m):
+    import torch
+    n, k = 300, 512
+    rng = np.random.default_rng(9)
+    va, vb = rng.standard_normal((m, k)), rng.standard_normal((n, k))
+    va[1, 40], vb[70, 300] = np.nan, np.inf
+    qa, qb = mb.Fp4Matrix(m, k), mb.Fp4Matrix(n, k)
+    qa.quantize(_dev(va, "f32"))
+    qb.quantize(_dev(vb, "f32"))
+    c = torch.zeros(m, n, device="cuda")
+    qa.matmul(qb, c)
+    got = to_np(c)
+    nan = np.zeros((m, n), dtype=bool)
+    nan[1], nan[:, 70] = True, True
+    assert np.array_equal(np.isnan(got), nan)
+    a, b = fp4.rounded(_np32(va)), fp4.rounded(_np32(vb))
+    keep_r, keep_c = np.arange(m) != 1, np.arange(n) != 70
+    _check(got[keep_r][:, keep_c], a[keep_r], b[keep_c], "f32", k)
+
+
+def _np32(v):
+    return np.asarray(v, dtype=np.float32).astype(np.float64)
+
+
+# (T, d, n, E, k, pad)
+GROUPED = [(1, 64, 130, 3, 2, 128), (8, 256, 512, 8, 2, 128), (40, 300, 200, 5, 2, 128), (300, 96, 333, 7, 3, 256),
+           (700, 520, 640, 4, 2, 128), (2000, 256, 1024, 3, 2, 256), (513, 128, 64, 200, 4, 128)]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("case", GROUPED)
+def test_grouped_product(mb, case, out):
+    import torch
+    T, d, n, E, k, pad = case
+    rng = np.random.default_rng(T + n)
+    s, (count, seg, pos, row_map) = _routed(mb, T, d, E, k, pad, T, dead=(1,))
+    x, v = _draw(rng, (T, d), "bf16")
+    qx = mb.Fp4Matrix(s.rows, d)
+    qx.quantize(x, sort=s, gather=True)
+    qw, w = _quantized(mb, rng, n, d, batch=E)
+    c = torch.full((s.rows, n), 7.0, dtype=_dt(out), device="cuda")
+    qx.matmul_grouped(qw, s, c)
+    got = to_np(c)
+    a = fp4.rounded(np.where((row_map >= 0)[:, None], v[np.maximum(row_map, 0) // k], 0.0))
+    for e in range(E):
+        r = slice(seg[e], seg[e] + count[e])
+        if count[e]:
+            _check(got[r], a[r], w[e], out, d)
+        pad_rows = got[seg[e] + count[e]:seg[e + 1]]
+        assert np.all((pad_rows == 0.0) | (pad_rows == 7.0))
+    assert np.all(got[seg[E]:] == 7.0)
+    if out == "f32":
+        base = torch.from_numpy(rng.standard_normal((s.rows, n)).astype(np.float32)).cuda()
+        b0 = to_np(base)
+        qx.matmul_grouped(qw, s, base, accumulate=True)
+        got = to_np(base)
+        for e in range(E):
+            r = slice(seg[e], seg[e] + count[e])
+            if count[e]:
+                _check(got[r], a[r], w[e], out, d, b0[r])
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("case", [(1, 64, 130, 3, 2), (40, 300, 200, 5, 2), (300, 96, 333, 7, 3), (2000, 256, 520, 4, 2)])
+def test_grouped_wgrad(mb, case, accumulate):
+    import torch
+    T, d, n, E, k = case
+    rng = np.random.default_rng(T + n + 1)
+    s, (count, seg, pos, row_map) = _routed(mb, T, d, E, k, 256, T, dead=(0,))
+    live = (row_map >= 0)[:, None]
+    x, v = _draw(rng, (T, d), "bf16")
+    dy, g = _draw(rng, (s.rows, n), "bf16")
+    qx, qg = mb.Fp4Matrix(d, s.rows), mb.Fp4Matrix(n, s.rows)
+    qx.quantize(x, sort=s, gather=True, transposed=True)
+    qg.quantize(dy, sort=s, transposed=True)
+    a = fp4.rounded(np.where(live, g, 0.0).T)
+    b = fp4.rounded(np.where(live, v[np.maximum(row_map, 0) // k], 0.0).T)
+    c = torch.from_numpy(rng.standard_normal((E, n, d)).astype(np.float32)).cuda()
+    base = to_np(c)
+    qg.wgrad_grouped(qx, s, c, accumulate=accumulate)
+    got = to_np(c)
+    for e in range(E):
+        r = slice(seg[e], seg[e + 1])
+        _check(got[e], a[:, r], b[:, r], "f32", seg[e + 1] - seg[e], base[e] if accumulate else None)
+    assert count[0] == 0 and np.array_equal(got[0], base[0] if accumulate else np.zeros((n, d)))
+
+
+def test_experts_together(mb):
+    """The routed ReLU^2 experts at 4 bits as a program runs them: sort, quantise the
+    gathered tokens, up product, ReLU^2 and quantise, down product, weighted sum with
+    the residual; each stage against the oracle on the stage's own input."""
+    import torch
+    T, d, F, E, k, pad = 150, 160, 288, 5, 2, 128
+    rng = np.random.default_rng(10)
+    s, (count, seg, pos, row_map) = _routed(mb, T, d, E, k, pad, 11)
+    live = (row_map >= 0)[:, None]
+    x = _dev(rng.standard_normal((T, d)), "bf16")
+    v = to_np(x)
+    w1, b1 = _quantized(mb, rng, F, d, batch=E, wide=False)
+    w2, b2 = _quantized(mb, rng, d, F, batch=E, wide=False)
+    p = torch.rand(T, k, device="cuda")
+    qx, qh = mb.Fp4Matrix(s.rows, d), mb.Fp4Matrix(s.rows, F)
+    h = torch.full((s.rows, F), float("nan"), dtype=torch.bfloat16, device="cuda")
+    o = torch.full((s.rows, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    y = torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+    qx.quantize(x, sort=s, gather=True)
+    qx.matmul_grouped(w1, s, h)
+    qh.quantize(h, sort=s, act="relu2")
+    qh.matmul_grouped(w2, s, o)
+    s.unpermute(o, y, weights=p, residual=x)
+    a = fp4.rounded(np.where(live, v[np.maximum(row_map, 0) // k], 0.0))
+    hq = np.where(live, to_np(h), 0.0)
+    aq = fp4.rounded(np.square(np.maximum(hq, 0.0)))
+    for e in range(E):
+        r = slice(seg[e], seg[e] + count[e])
+        _check(to_np(h)[r], a[r], b1[e], "bf16", d)
+        _check(to_np(o)[r], aq[r], b2[e], "bf16", F)
+    ref, mag = sort.unpermute(np.where(live, to_np(o), 0.0), pos, to_np(p), v)
+    assert np.all(np.abs(to_np(y) - ref) <= 2.0 ** -8 * np.abs(ref) + (k + 2) * 2.0 ** -24 * mag)
+
+
+def test_linear_gradients_against_differences(mb):
+    """dx and dW of y = Q(x) Q(W)^T as the three products give them, for a loss that is
+    linear in y, against differences of the exact product: with x, W and dy already
+    MXFP4 values along both axes (small integers, scale 1), quantisation changes
+    nothing and the gradients are exact."""
+    import torch
+    m, n, k = 64, 96, 160
+    rng = np.random.default_rng(12)
+    draw = lambda r, c: rng.choice([-6.0, -3.0, -1.0, 0.5, 2.0, 4.0, 6.0], size=(r, c))
+    x, w, dy = draw(m, k), draw(n, k), draw(m, n)
+    for t in (x, w, dy):
+        t[::32, :], t[:, ::32] = 6.0, 6.0
+    q = lambda a, tr=False: _q(mb, a, tr)
+    dx, dw = torch.empty(m, k, device="cuda"), torch.empty(n, k, device="cuda")
+    q(dy).matmul(q(w, True), dx)
+    q(dy, True).matmul(q(x, True), dw)
+    loss = lambda x, w: float(np.sum((x @ w.T) * dy))
+    for i, j in ((0, 0), (63, 159), (17, 31)):
+        e = np.zeros_like(x)
+        e[i, j] = 1.0
+        assert to_np(dx)[i, j] == (loss(x + e, w) - loss(x - e, w)) / 2
+    for i, j in ((0, 0), (95, 159), (33, 64)):
+        e = np.zeros_like(w)
+        e[i, j] = 1.0
+        assert to_np(dw)[i, j] == (loss(x, w + e) - loss(x, w - e)) / 2
+
+
+def _q(mb, a, transposed):
+    rows, cols = a.shape[::-1] if transposed else a.shape
+    m = mb.Fp4Matrix(rows, cols)
+    m.quantize(_dev(a, "f32"), transposed=transposed)
+    return m
+
+
+def test_streams_and_graph(mb):
+    """Two streams at once with their own buffers, then a captured graph replayed on
+    new inputs."""
+    import torch
+    m, n, k = 64, 512, 1024
+    rng = np.random.default_rng(13)
+    qw, w = _quantized(mb, rng, n, k)
+    xs = [torch.from_numpy(rng.standard_normal((m, k)).astype(np.float32)).cuda() for _ in range(2)]
+    qs = [mb.Fp4Matrix(m, k) for _ in range(2)]
+    cs = [torch.empty(m, n, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                qs[i].quantize(xs[i])
+                qs[i].matmul(qw, cs[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        _check(to_np(cs[i]), fp4.rounded(to_np(xs[i])), w, "f32", k)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qs[0].quantize(xs[0])
+        qs[0].matmul(qw, cs[0])
+    for _ in range(2):
+        xs[0].normal_()
+        cs[0].zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        _check(to_np(cs[0]), fp4.rounded(to_np(xs[0])), w, "f32", k)
+
+
+def test_binding_checks(mb):
+    import torch
+    q = mb.Fp4Matrix(8, 64)
+    x = torch.zeros(8, 128, device="cuda")
+    for bad in (x[:, ::2], x[:, :64], torch.zeros(8, 63, device="cuda"), torch.zeros(8, 64)):
+        with pytest.raises(mb.MlpBlkError):
+            q.quantize(bad)
+    with pytest.raises(mb.MlpBlkError):
+        q.quantize(torch.zeros(8, 64, device="cuda", dtype=torch.float16))
+    with pytest.raises(mb.MlpBlkError):
+        q.matmul(mb.Fp4Matrix(8, 96), torch.zeros(8, 8, device="cuda"))
+    with pytest.raises(mb.MlpBlkError):
+        q.matmul(q, torch.zeros(8, 7, device="cuda"))
+    with pytest.raises(mb.MlpBlkError):
+        q.matmul(q, torch.zeros(8, 8, device="cuda", dtype=torch.bfloat16), accumulate=True)
+
+
+def test_wgrad_of_no_rows(mb):
+    import torch
+    s = mb.MoeSort(0, 64, 4, 2, 256)
+    s.sort(torch.empty(0, 2, dtype=torch.int32, device="cuda"))
+    assert s.rows == 0 and not s.count.any() and not s.seg.any()
+    a, b = mb.Fp4Matrix(32, 0), mb.Fp4Matrix(64, 0)
+    c = torch.full((4, 32, 64), 3.0, device="cuda")
+    a.wgrad_grouped(b, s, c, accumulate=True)
+    assert bool((c == 3.0).all())
+    a.wgrad_grouped(b, s, c)
+    assert not c.any()

@@ -1,0 +1,208 @@
+"""Pins of the token-sorting and MXFP4 oracles (CPU): values that the definitions
+fix, the rounding's error bound, the byte layout spelled out, gradients against
+central differences, and the refusals of the entry points."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import fp4, sort
+
+
+# ---------------------------------------------------------------------- MXFP4
+
+def test_e2m1_values_and_ties():
+    cases = {0.0: 0.0, 0.25: 0.0, 0.26: 0.5, 0.75: 1.0, 0.74: 0.5, 1.25: 1.0, 1.26: 1.5, 1.75: 2.0, 2.5: 2.0,
+             2.51: 3.0, 3.5: 4.0, 5.0: 4.0, 5.01: 6.0, 6.0: 6.0, 7.9: 6.0}
+    for v, q in cases.items():
+        assert fp4.decode(fp4.e2m1(np.array([v])))[0] == q, v
+        assert fp4.decode(fp4.e2m1(np.array([-v])))[0] == -q, -v
+
+
+@pytest.mark.parametrize("top,byte", [(6.0, 127), (4.0, 127), (3.99, 126), (1.0, 125), (8.0, 128), (0.0, 0),
+                                      (2.0 ** -126, 0), (2.0 ** -124, 1), (2.0 ** 127, 252), (np.inf, 255), (np.nan, 255)])
+def test_scale_byte(top, byte):
+    v = np.zeros((1, 32))
+    v[0, 7] = -top
+    assert fp4.quantize(v)[1][0, 0] == byte
+
+
+def test_rounding_error_bound():
+    v = np.random.default_rng(0).standard_normal((64, 256)) * 3.0
+    c, s = fp4.quantize(v)
+    q = fp4.values(c, s, 256)
+    scale = np.repeat(np.ldexp(1.0, s.astype(int) - 127), 32, axis=1)
+    # half a step: 1/4, 1/2 or 1 scale by binade; saturation cuts [6, 8) scales down to 6
+    assert np.all(np.abs(q - v) <= np.where(np.abs(v) < 2 * scale, 0.25, np.where(np.abs(v) < 4 * scale, 0.5, 2.0)) * scale)
+
+
+def test_layout_byte_by_byte():
+    rng = np.random.default_rng(1)
+    rows, cols = 200, 300
+    codes, sb = fp4.quantize(rng.standard_normal((rows, cols)))
+    packed, tiled = fp4.pack(codes, sb)
+    assert packed.size == rows * 10 * 16 and tiled.size == 2 * 4 * 512
+    for r, c in ((0, 0), (199, 299), (130, 131), (64, 33)):
+        assert packed[r * 160 + c // 2] >> (4 * (c % 2)) & 15 == codes[r, c]
+        b = c // 32
+        assert tiled[(r // 128 * 4 + b // 4) * 512 + r % 32 * 16 + r % 128 // 32 * 4 + b % 4] == sb[r, b]
+
+
+# -------------------------------------------------------------------- sorting
+
+def test_plan_by_hand():
+    idx = np.array([[1, 0], [1, -1], [2, 1], [1, 1]])
+    count, seg, pos, row_map = sort.plan(idx, 4, 4)
+    assert count.tolist() == [1, 5, 1, 0] and seg.tolist() == [0, 4, 12, 16, 16]
+    assert pos.tolist() == [[4, 0], [5, -1], [12, 6], [7, 8]]
+    assert row_map[:16].tolist() == [1, -1, -1, -1, 0, 2, 5, 6, 7, -1, -1, -1, 4, -1, -1, -1]
+    assert len(row_map) == 8 + 4 * 3 and np.all(row_map[16:] == -1)
+
+
+def test_gradients_against_differences():
+    rng = np.random.default_rng(2)
+    T, d, E, k = 5, 6, 3, 2
+    idx = rng.integers(-1, E, (T, k))
+    _, _, pos, row_map = sort.plan(idx, E, 2)
+    R = len(row_map)
+    rows, w = rng.standard_normal((R, d)), rng.uniform(0.1, 1, (T, k))
+    x, dy, g = rng.standard_normal((T, d)), rng.standard_normal((T, d)), rng.standard_normal((R, d))
+    live = row_map >= 0
+    d_rows, dw, _ = sort.unpermute_backward(dy, rows, pos, row_map, w)
+    dx = sort.permute_backward(np.where(live[:, None], g, 0.0), pos)
+    h = 1e-6
+
+    def check(f, at, grad):
+        for ij in np.ndindex(at.shape):
+            keep = at[ij]
+            at[ij] = keep + h
+            up = f()
+            at[ij] = keep - h
+            down = f()
+            at[ij] = keep
+            assert abs((up - down) / (2 * h) - grad[ij]) < 1e-7
+
+    check(lambda: float(np.sum(sort.unpermute(rows, pos, w, x)[0] * dy)), rows, d_rows)
+    check(lambda: float(np.sum(sort.unpermute(rows, pos, w, x)[0] * dy)), w, dw)
+    check(lambda: float(np.sum(sort.permute(x, row_map, k)[live] * g[live])), x, dx)
+
+
+# ------------------------------------------------------------------- refusals
+
+@pytest.fixture(scope="module")
+def mb():
+    import __graft_entry__
+    __graft_entry__.build()
+    import mlp_block_backprop_gb300
+    return mlp_block_backprop_gb300
+
+
+def _addresses(n):
+    return [0x10000 * (i + 1) for i in range(n)]  # aligned, never dereferenced
+
+
+@pytest.mark.parametrize("kw", [dict(tokens=-1), dict(width=0), dict(experts=0), dict(experts=257), dict(top_k=0),
+                                dict(top_k=257), dict(pad=0), dict(pad=1025), dict(tokens=1 << 31)])
+def test_sort_desc_refusals(mb, kw):
+    base = dict(tokens=10, width=64, experts=4, top_k=2, pad=128)
+    assert mb.mlpblk_moe_sort_rows(mb.make_sort_desc(**base)) == sort.rows_bound(10, 2, 4, 128)
+    bad = mb.make_sort_desc(**{**base, **kw})
+    assert mb.mlpblk_moe_sort_rows(bad) == -1
+    p = _addresses(9)
+    b = ctypes.byref(bad)
+    assert mb.lib.mlpblk_moe_sort(b, *p[:5], None) == mb.MLPBLK_EINVAL
+    assert mb.lib.mlpblk_moe_permute(b, *p[:5], None) == mb.MLPBLK_EINVAL
+    assert mb.lib.mlpblk_moe_unpermute_backward(b, *p[:8], None) == mb.MLPBLK_EINVAL
+
+
+def test_sort_argument_refusals(mb):
+    d = mb.make_sort_desc(10, 64, 4, 2, 128)
+    b = ctypes.byref(d)
+    assert mb.mlpblk_moe_sort_rows(mb.SortDesc(10, 64, 4, 2, 128, 7)) == -1
+    assert mb.lib.mlpblk_moe_permute(ctypes.byref(mb.SortDesc(10, 64, 4, 2, 128, 7)), *_addresses(5), None) == mb.MLPBLK_ENOTSUP
+    for name, n, out, ins in (("mlpblk_moe_permute", 5, 4, (0,)), ("mlpblk_moe_permute_backward", 3, 2, (0,)),
+                              ("mlpblk_moe_unpermute", 5, 4, (0,)), ("mlpblk_moe_unpermute_backward", 8, 6, (0, 1)),
+                              ("mlpblk_moe_sort", 5, 3, (0,))):
+        f = getattr(mb.lib, name)
+        p = _addresses(n)
+        for i in range(n):
+            q = list(p)
+            q[i] += 8
+            assert f(b, *q, None) == mb.MLPBLK_EINVAL, (name, i)  # misaligned
+        q = list(p)
+        q[0] = None
+        assert f(b, *q, None) == mb.MLPBLK_EINVAL
+        for i in ins:
+            q = list(p)
+            q[out] = q[i]
+            assert f(b, *q, None) == mb.MLPBLK_EINVAL, (name, "alias", i)
+    empty = ctypes.byref(mb.make_sort_desc(0, 64, 4, 2, 128))
+    assert mb.mlpblk_moe_sort_rows(mb.make_sort_desc(0, 64, 4, 2, 128)) == 0
+    assert mb.lib.mlpblk_moe_permute(empty, *[None] * 5, None) == mb.MLPBLK_OK
+    assert mb.lib.mlpblk_moe_unpermute(empty, *[None] * 5, None) == mb.MLPBLK_OK
+    assert mb.lib.mlpblk_moe_unpermute_backward(empty, *[None] * 8, None) == mb.MLPBLK_OK
+
+
+def test_fp4_sizes_and_refusals(mb):
+    size = lambda r, c, b=1: (mb.mlpblk_fp4_codes_size(mb.make_fp4_desc(r, c, b)),
+                              mb.mlpblk_fp4_scales_size(mb.make_fp4_desc(r, c, b)))
+    assert size(1, 1) == (16, 1024)
+    assert size(129, 257, 3) == (3 * 129 * 144, 3 * 2 * 4 * 512)
+    assert size(0, 64) == (0, 0)
+    q = lambda d, x=0x10000, rm=None, div=0, c=0x20000, s=0x30000: mb.lib.mlpblk_fp4_quantize(ctypes.byref(d), x, rm, div, c, s, None)
+    good = mb.make_fp4_desc(8, 64)
+    for bad in (mb.make_fp4_desc(-1, 64), mb.make_fp4_desc(8, -1), mb.make_fp4_desc(8, 64, 0), mb.make_fp4_desc(1 << 30, 64, 2),
+                mb.make_fp4_desc(8, 1 << 31)):
+        assert q(bad) == mb.MLPBLK_EINVAL
+    assert q(mb.Fp4Desc(8, 64, 1, 3, 0, 0)) == mb.MLPBLK_ENOTSUP
+    assert q(mb.make_fp4_desc(8, 64, act=2)) == mb.MLPBLK_ENOTSUP
+    assert q(mb.Fp4Desc(8, 64, 1, mb.MLPBLK_BF16, 2, 0)) == mb.MLPBLK_EINVAL
+    assert q(good, x=None) == q(good, x=0x10008) == q(good, rm=0x40004) == q(good, c=0x10000) == mb.MLPBLK_EINVAL
+    assert q(good, div=-1) == mb.MLPBLK_EINVAL
+    assert q(mb.make_fp4_desc(8, 64, 2), rm=0x40000) == mb.MLPBLK_EINVAL          # a row map takes one matrix
+    assert q(mb.make_fp4_desc(0, 64), x=None) == q(mb.make_fp4_desc(8, 0), x=None) == mb.MLPBLK_OK
+    dq = lambda d, y=0x30000: mb.lib.mlpblk_fp4_dequantize(ctypes.byref(d), 0x10000, 0x20000, y, None)
+    assert dq(mb.make_fp4_desc(8, 64, transposed=True)) == dq(mb.make_fp4_desc(8, 64, act=1)) == mb.MLPBLK_ENOTSUP
+    assert dq(good, 0x10000) == dq(good, 0x30004) == mb.MLPBLK_EINVAL
+
+
+def test_fp4_product_refusals(mb):
+    p = _addresses(5)
+    mm = lambda d, a=p: mb.lib.mlpblk_fp4_matmul(ctypes.byref(d), *a, None)
+    D = mb.make_fp4_matmul_desc
+    for bad in (D(-1, 8, 8), D(8, 0, 8), D(8, 8, 0), D(1 << 31, 8, 8), D(8, 8, 8, experts=2), D(8, 8, 8, pad=128),
+                D(8, 8, 8, max_rows=4), mb.Fp4MatmulDesc(8, 8, 8, mb.MLPBLK_FP32, 2, 0, 0, 0), D((1 << 31) - 1, (1 << 31) - 1, 8)):
+        assert mm(bad) == mb.MLPBLK_EINVAL
+    assert mm(D(8, 8, 8, accumulate=True)) == mb.MLPBLK_ENOTSUP                   # bf16 sums are not kept
+    assert mm(mb.Fp4MatmulDesc(8, 8, 8, 9, 0, 0, 0, 0)) == mb.MLPBLK_ENOTSUP
+    for i in range(5):
+        q = list(p)
+        q[i] += 8
+        assert mm(D(8, 8, 8), q) == mb.MLPBLK_EINVAL
+    for i in range(4):
+        q = list(p)
+        q[4] = q[i]
+        assert mm(D(8, 8, 8), q) == mb.MLPBLK_EINVAL
+    assert mm(D(0, 8, 8), [None] * 5) == mb.MLPBLK_OK
+    g = _addresses(7)
+    gr = lambda d, a=g: mb.lib.mlpblk_fp4_matmul_grouped(ctypes.byref(d), *a, None)
+    assert gr(D(256, 8, 8, experts=0, pad=128)) == gr(D(256, 8, 8, experts=257, pad=128)) == mb.MLPBLK_EINVAL
+    assert gr(D(256, 8, 8, experts=2, pad=64)) == mb.MLPBLK_ENOTSUP
+    assert gr(D(256, 1 << 30, 8, experts=2, pad=128)) == mb.MLPBLK_EINVAL
+    assert gr(D(256, 8, 8, experts=2, pad=128), g[:5] + [None, g[6]]) == mb.MLPBLK_EINVAL   # seg
+    wg = lambda d: mb.lib.mlpblk_fp4_wgrad_grouped(ctypes.byref(d), *_addresses(6), None)
+    assert wg(D(8, 8, 256, experts=2, pad=128)) == mb.MLPBLK_ENOTSUP
+    assert wg(D(1 << 30, 8, 256, experts=2, pad=256)) == mb.MLPBLK_EINVAL
+    assert wg(D(8, 8, 256, experts=2, pad=256, max_rows=3)) == mb.MLPBLK_EINVAL
+
+
+def test_binding_refuses_wrong_tensors(mb):
+    torch = pytest.importorskip("torch")
+    with pytest.raises(mb.MlpBlkError):                       # not a CUDA tensor
+        mb._operand(torch.zeros(4), "f", "x", (torch.float32,), 4)
+    assert mb._operand(None, "f", "x", (torch.float32,), 4) is None
+    with pytest.raises(mb.MlpBlkError):
+        mb.make_sort_desc(1, 1, 1, 1, dtype="f16")
+    with pytest.raises(mb.MlpBlkError):
+        mb.Fp4Matrix(4, 64, codes=torch.zeros(3, dtype=torch.uint8), scales=torch.zeros(1024, dtype=torch.uint8), device="cpu")
