@@ -234,6 +234,28 @@ def make_desc(tokens: int, d_model: int, ffn: int, eps: float = 1e-6, dtype: int
     return Desc(int(tokens), int(d_model), int(ffn), float(eps), int(dtype))
 
 
+class _Torch:
+    """What the calls need of torch, looked up once (torch is imported with the first
+    call, not with this package)."""
+    _one = None
+
+    @staticmethod
+    def get():
+        if _Torch._one is None:
+            import torch
+            o = _Torch()
+            o.device = torch.cuda.current_device
+            # the handle of a device's current stream; without the raw getter, through
+            # the Stream object (3 us a call instead of 0.2 on a Grace core)
+            o.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                   lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+            o.int32, o.uint8, o.float32, o.bfloat16 = torch.int32, torch.uint8, torch.float32, torch.bfloat16
+            o.row = {MLPBLK_BF16: torch.bfloat16, MLPBLK_FP32: torch.float32}
+            o.code = {torch.bfloat16: MLPBLK_BF16, torch.float32: MLPBLK_FP32, "bf16": MLPBLK_BF16, "f32": MLPBLK_FP32}
+            _Torch._one = o
+        return _Torch._one
+
+
 def _ptr(t):
     """Device address of a tensor, an int address, or None (NULL)."""
     if t is None:
@@ -245,8 +267,8 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        t = _Torch.get()
+        return t.raw_stream(t.device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -472,43 +494,26 @@ class MoeBuffers:
         mlpblk_zero_grads(flat, self.dgamma, self.dw1s, self.dw2s, stream=stream)
 
 
-def _operand(t, where, name, dtypes, numel, device=None):
+def _operand(t, where, name, dtype, numel, dev):
     """Device address of tensor argument `name` of `where`, checked: a contiguous CUDA
-    tensor of one of `dtypes` with at least `numel` elements, on the current device.
-    A call goes to the current device's stream, so a tensor of another one is
-    refused.  Integers (raw addresses) and None pass unchecked: the library checks
+    tensor of `dtype` with at least `numel` elements, on the current device `dev` (a
+    call goes to the current device's stream, so a tensor of another one is
+    refused).  Integers (raw addresses) and None pass unchecked: the library checks
     what it can of those."""
     if t is None or isinstance(t, int):
         return t
-    if not t.is_cuda or not t.is_contiguous() or t.dtype not in dtypes or t.numel() < numel:
-        raise MlpBlkError(MLPBLK_EINVAL, f"{where}: {name} must be a contiguous CUDA tensor of "
-                          f"{' or '.join(str(d) for d in dtypes)} with at least {numel} elements")
-    if device is not None and t.device.index != device:
-        raise MlpBlkError(MLPBLK_EINVAL, f"{where}: {name} is on cuda:{t.device.index}, the call on cuda:{device}")
-    return t.data_ptr()
-
-
-def _call_site():
-    """(current device index, torch's int32, float32, byte types) for the checks."""
-    import torch
-    return torch.cuda.current_device(), (torch.int32,), (torch.float32,), (torch.uint8,)
-
-
-def _row_types(dtype):
-    import torch
-    return (torch.bfloat16,) if dtype == MLPBLK_BF16 else (torch.float32,)
+    if t.get_device() == dev and t.dtype is dtype and t.numel() >= numel and t.is_contiguous():
+        return t.data_ptr()
+    raise MlpBlkError(MLPBLK_EINVAL, f"{where}: {name} must be a contiguous {dtype} tensor of at least {numel} "
+                      f"elements on cuda:{dev}, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
 def _dtype_code(dtype):
     """MLPBLK_BF16 / MLPBLK_FP32 of "bf16", "f32", a torch dtype or the code itself."""
-    if isinstance(dtype, int):
-        return dtype
-    name = str(dtype)
-    if name in ("bf16", "torch.bfloat16"):
-        return MLPBLK_BF16
-    if name in ("f32", "torch.float32"):
-        return MLPBLK_FP32
-    raise MlpBlkError(MLPBLK_ENOTSUP, f"element type {dtype}")
+    code = dtype if isinstance(dtype, int) else _Torch.get().code.get(dtype)
+    if code is None:
+        raise MlpBlkError(MLPBLK_ENOTSUP, f"element type {dtype}")
+    return code
 
 
 def make_sort_desc(tokens, width, experts, top_k, pad=128, dtype=MLPBLK_BF16) -> SortDesc:
@@ -521,7 +526,8 @@ def mlpblk_moe_sort_rows(desc: SortDesc) -> int:
 
 def mlpblk_moe_sort(desc, expert_idx, count, seg, pos, row_map, stream=None):
     where = "mlpblk_moe_sort"
-    dev, i32, _, _ = _call_site()
+    t = _Torch.get()
+    dev, i32 = t.device(), t.int32
     n = desc.tokens * desc.top_k
     rc = lib.mlpblk_moe_sort(
         ctypes.byref(desc), _operand(expert_idx, where, "expert_idx", i32, n, dev),
@@ -533,8 +539,9 @@ def mlpblk_moe_sort(desc, expert_idx, count, seg, pos, row_map, stream=None):
 
 def mlpblk_moe_permute(desc, x, pos, count, seg, rows, stream=None):
     where = "mlpblk_moe_permute"
-    dev, i32, _, _ = _call_site()
-    dt = _row_types(desc.dtype)
+    t = _Torch.get()
+    dev, i32 = t.device(), t.int32
+    dt = t.row.get(desc.dtype)
     rc = lib.mlpblk_moe_permute(
         ctypes.byref(desc), _operand(x, where, "x", dt, desc.tokens * desc.width, dev),
         _operand(pos, where, "pos", i32, desc.tokens * desc.top_k, dev),
@@ -545,8 +552,9 @@ def mlpblk_moe_permute(desc, x, pos, count, seg, rows, stream=None):
 
 def mlpblk_moe_permute_backward(desc, d_rows, pos, dx, stream=None):
     where = "mlpblk_moe_permute_backward"
-    dev, i32, _, _ = _call_site()
-    dt = _row_types(desc.dtype)
+    t = _Torch.get()
+    dev, i32 = t.device(), t.int32
+    dt = t.row.get(desc.dtype)
     rc = lib.mlpblk_moe_permute_backward(
         ctypes.byref(desc), _operand(d_rows, where, "d_rows", dt, mlpblk_moe_sort_rows(desc) * desc.width, dev),
         _operand(pos, where, "pos", i32, desc.tokens * desc.top_k, dev),
@@ -556,8 +564,9 @@ def mlpblk_moe_permute_backward(desc, d_rows, pos, dx, stream=None):
 
 def mlpblk_moe_unpermute(desc, rows, pos, weights, residual, y, stream=None):
     where = "mlpblk_moe_unpermute"
-    dev, i32, f32, _ = _call_site()
-    dt = _row_types(desc.dtype)
+    t = _Torch.get()
+    dev, i32, f32 = t.device(), t.int32, t.float32
+    dt = t.row.get(desc.dtype)
     n = desc.tokens * desc.width
     rc = lib.mlpblk_moe_unpermute(
         ctypes.byref(desc), _operand(rows, where, "rows", dt, mlpblk_moe_sort_rows(desc) * desc.width, dev),
@@ -569,8 +578,9 @@ def mlpblk_moe_unpermute(desc, rows, pos, weights, residual, y, stream=None):
 
 def mlpblk_moe_unpermute_backward(desc, dy, rows, pos, count, seg, weights, d_rows, d_weights, stream=None):
     where = "mlpblk_moe_unpermute_backward"
-    dev, i32, f32, _ = _call_site()
-    dt = _row_types(desc.dtype)
+    t = _Torch.get()
+    dev, i32, f32 = t.device(), t.int32, t.float32
+    dt = t.row.get(desc.dtype)
     n, r = desc.tokens * desc.top_k, mlpblk_moe_sort_rows(desc) * desc.width
     rc = lib.mlpblk_moe_unpermute_backward(
         ctypes.byref(desc), _operand(dy, where, "dy", dt, desc.tokens * desc.width, dev),
@@ -581,10 +591,24 @@ def mlpblk_moe_unpermute_backward(desc, dy, rows, pos, count, seg, weights, d_ro
     _check(rc, where)
 
 
-class MoeSort:
+class _Kept:
+    """Base of the classes that keep device buffers of their own: the buffers cannot
+    be replaced, so their addresses are taken once and a call checks only what it is
+    given."""
+
+    def _device(self, where):
+        """The current device, which has to be the buffers' own."""
+        dev = _Torch.get().device()
+        if dev != self._dev:
+            raise MlpBlkError(MLPBLK_EINVAL, f"{where}: the buffers are on cuda:{self._dev}, the call on cuda:{dev}")
+        return dev
+
+
+class MoeSort(_Kept):
     """The plan of one batch's routing and its buffers: `sort` fills count, seg, pos
-    and row_map from the expert ids, the other methods move rows by it.  `rows` is R,
-    the row count of the sorted buffers."""
+    and row_map from the expert ids, the other methods move rows by it (the
+    mlpblk_moe_* calls of the same names).  `rows` is R, the row count of the sorted
+    buffers."""
 
     def __init__(self, tokens, width, experts, top_k, pad=128, dtype="bf16", device="cuda"):
         import torch
@@ -593,26 +617,58 @@ class MoeSort:
         if self.rows < 0:
             raise MlpBlkError(MLPBLK_EINVAL, "mlpblk_moe_sort_rows")
         e = dict(dtype=torch.int32, device=device)
-        self.count = torch.zeros(experts, **e)
-        self.seg = torch.zeros(experts + 1, **e)
-        self.pos = torch.empty(tokens, top_k, **e)
-        self.row_map = torch.empty(self.rows, **e)
+        self._count = torch.zeros(experts, **e)
+        self._seg = torch.zeros(experts + 1, **e)
+        self._pos = torch.empty(tokens, top_k, **e)
+        self._row_map = torch.empty(self.rows, **e)
+        self._dev = self._count.get_device()
+        self._d = ctypes.byref(self.desc)
+        self._at = tuple(t.data_ptr() for t in (self._count, self._seg, self._pos, self._row_map))
+        self._entries, self._x_n, self._r_n = tokens * top_k, tokens * width, self.rows * width
+        self._type = _Torch.get().row[self.desc.dtype]
+
+    count = property(lambda self: self._count)
+    seg = property(lambda self: self._seg)
+    pos = property(lambda self: self._pos)
+    row_map = property(lambda self: self._row_map)
 
     def sort(self, expert_idx, stream=None):
-        mlpblk_moe_sort(self.desc, expert_idx, self.count, self.seg, self.pos, self.row_map, stream=stream)
+        where = "MoeSort.sort"
+        dev = self._device(where)
+        count, seg, pos, row_map = self._at
+        _check(lib.mlpblk_moe_sort(self._d, _operand(expert_idx, where, "expert_idx", _Torch.get().int32, self._entries, dev),
+                                   count, seg, pos, row_map, _stream(stream)), where)
 
     def permute(self, x, rows, stream=None):
-        mlpblk_moe_permute(self.desc, x, self.pos, self.count, self.seg, rows, stream=stream)
+        where = "MoeSort.permute"
+        dev, dt = self._device(where), self._type
+        count, seg, pos, _ = self._at
+        _check(lib.mlpblk_moe_permute(self._d, _operand(x, where, "x", dt, self._x_n, dev), pos, count, seg,
+                                      _operand(rows, where, "rows", dt, self._r_n, dev), _stream(stream)), where)
 
     def permute_backward(self, d_rows, dx, stream=None):
-        mlpblk_moe_permute_backward(self.desc, d_rows, self.pos, dx, stream=stream)
+        where = "MoeSort.permute_backward"
+        dev, dt = self._device(where), self._type
+        _check(lib.mlpblk_moe_permute_backward(self._d, _operand(d_rows, where, "d_rows", dt, self._r_n, dev), self._at[2],
+                                               _operand(dx, where, "dx", dt, self._x_n, dev), _stream(stream)), where)
 
     def unpermute(self, rows, y, weights=None, residual=None, stream=None):
-        mlpblk_moe_unpermute(self.desc, rows, self.pos, weights, residual, y, stream=stream)
+        where = "MoeSort.unpermute"
+        dev, dt = self._device(where), self._type
+        _check(lib.mlpblk_moe_unpermute(self._d, _operand(rows, where, "rows", dt, self._r_n, dev), self._at[2],
+                                        _operand(weights, where, "weights", _Torch.get().float32, self._entries, dev),
+                                        _operand(residual, where, "residual", dt, self._x_n, dev),
+                                        _operand(y, where, "y", dt, self._x_n, dev), _stream(stream)), where)
 
     def unpermute_backward(self, dy, rows, weights, d_rows, d_weights, stream=None):
-        mlpblk_moe_unpermute_backward(self.desc, dy, rows, self.pos, self.count, self.seg, weights, d_rows, d_weights,
-                                      stream=stream)
+        where = "MoeSort.unpermute_backward"
+        dev, dt, f32 = self._device(where), self._type, _Torch.get().float32
+        count, seg, pos, _ = self._at
+        _check(lib.mlpblk_moe_unpermute_backward(
+            self._d, _operand(dy, where, "dy", dt, self._x_n, dev), _operand(rows, where, "rows", dt, self._r_n, dev),
+            pos, count, seg, _operand(weights, where, "weights", f32, self._entries, dev),
+            _operand(d_rows, where, "d_rows", dt, self._r_n, dev),
+            _operand(d_weights, where, "d_weights", f32, self._entries, dev), _stream(stream)), where)
 
 
 def make_fp4_desc(rows, cols, batch=1, dtype=MLPBLK_BF16, transposed=False, act=MLPBLK_FP4_ACT_NONE) -> Fp4Desc:
@@ -631,11 +687,12 @@ def mlpblk_fp4_quantize(desc, x, codes, scales, row_map=None, map_div=0, stream=
     """x holds the whole source, unless a row_map gathers its rows (map_div > 0): its
     row count is then the caller's business."""
     where = "mlpblk_fp4_quantize"
-    dev, i32, _, u8 = _call_site()
+    t = _Torch.get()
+    dev, i32, u8 = t.device(), t.int32, t.uint8
     mapped = desc.cols if desc.transposed else desc.rows  # the source's rows
     n = 0 if row_map is not None and map_div > 0 else desc.rows * desc.cols * desc.batch
     rc = lib.mlpblk_fp4_quantize(
-        ctypes.byref(desc), _operand(x, where, "x", _row_types(desc.dtype), n, dev),
+        ctypes.byref(desc), _operand(x, where, "x", t.row.get(desc.dtype), n, dev),
         _operand(row_map, where, "row_map", i32, mapped, dev), int(map_div),
         _operand(codes, where, "codes", u8, mlpblk_fp4_codes_size(desc), dev),
         _operand(scales, where, "scales", u8, mlpblk_fp4_scales_size(desc), dev), _stream(stream))
@@ -644,11 +701,12 @@ def mlpblk_fp4_quantize(desc, x, codes, scales, row_map=None, map_div=0, stream=
 
 def mlpblk_fp4_dequantize(desc, codes, scales, y, stream=None):
     where = "mlpblk_fp4_dequantize"
-    dev, _, _, u8 = _call_site()
+    t = _Torch.get()
+    dev, u8 = t.device(), t.uint8
     rc = lib.mlpblk_fp4_dequantize(
         ctypes.byref(desc), _operand(codes, where, "codes", u8, mlpblk_fp4_codes_size(desc), dev),
         _operand(scales, where, "scales", u8, mlpblk_fp4_scales_size(desc), dev),
-        _operand(y, where, "y", _row_types(desc.dtype), desc.rows * desc.cols * desc.batch, dev), _stream(stream))
+        _operand(y, where, "y", t.row.get(desc.dtype), desc.rows * desc.cols * desc.batch, dev), _stream(stream))
     _check(rc, where)
 
 
@@ -670,39 +728,43 @@ def _fp4_operands(where, a, a_rows, b, b_rows, b_batch, k, dev, u8):
 
 def mlpblk_fp4_matmul(desc, a_codes, a_scales, b_codes, b_scales, c, stream=None):
     where = "mlpblk_fp4_matmul"
-    dev, _, _, u8 = _call_site()
+    t = _Torch.get()
+    dev, u8 = t.device(), t.uint8
     ops = _fp4_operands(where, (a_codes, a_scales), desc.m, (b_codes, b_scales), desc.n, 1, desc.k, dev, u8)
     rc = lib.mlpblk_fp4_matmul(ctypes.byref(desc), *ops,
-                               _operand(c, where, "c", _row_types(desc.out_dtype), desc.m * desc.n, dev), _stream(stream))
+                               _operand(c, where, "c", t.row.get(desc.out_dtype), desc.m * desc.n, dev), _stream(stream))
     _check(rc, where)
 
 
 def mlpblk_fp4_matmul_grouped(desc, a_codes, a_scales, b_codes, b_scales, count, seg, c, stream=None):
     where = "mlpblk_fp4_matmul_grouped"
-    dev, i32, _, u8 = _call_site()
+    t = _Torch.get()
+    dev, i32, u8 = t.device(), t.int32, t.uint8
     ops = _fp4_operands(where, (a_codes, a_scales), desc.m, (b_codes, b_scales), desc.n, max(desc.experts, 1), desc.k,
                         dev, u8)
     rc = lib.mlpblk_fp4_matmul_grouped(
         ctypes.byref(desc), *ops, _operand(count, where, "count", i32, desc.experts, dev),
         _operand(seg, where, "seg", i32, desc.experts + 1, dev),
-        _operand(c, where, "c", _row_types(desc.out_dtype), desc.m * desc.n, dev), _stream(stream))
+        _operand(c, where, "c", t.row.get(desc.out_dtype), desc.m * desc.n, dev), _stream(stream))
     _check(rc, where)
 
 
 def mlpblk_fp4_wgrad_grouped(desc, a_codes, a_scales, b_codes, b_scales, seg, c, stream=None):
     where = "mlpblk_fp4_wgrad_grouped"
-    dev, i32, _, u8 = _call_site()
+    t = _Torch.get()
+    dev, i32, u8 = t.device(), t.int32, t.uint8
     ops = _fp4_operands(where, (a_codes, a_scales), desc.m, (b_codes, b_scales), desc.n, 1, desc.k, dev, u8)
     rc = lib.mlpblk_fp4_wgrad_grouped(
         ctypes.byref(desc), *ops, _operand(seg, where, "seg", i32, desc.experts + 1, dev),
-        _operand(c, where, "c", _row_types(desc.out_dtype), desc.experts * desc.m * desc.n, dev), _stream(stream))
+        _operand(c, where, "c", t.row.get(desc.out_dtype), desc.experts * desc.m * desc.n, dev), _stream(stream))
     _check(rc, where)
 
 
-class Fp4Matrix:
+class Fp4Matrix(_Kept):
     """An MXFP4 matrix [rows, cols] (or a batch of them): its codes and scales, and
     the products that take it as A.  `codes` and `scales` given: buffers that hold a
     quantised matrix already (uint8)."""
+    _ACTS = {"none": MLPBLK_FP4_ACT_NONE, "relu2": MLPBLK_FP4_ACT_RELU2}
 
     def __init__(self, rows, cols, batch=1, codes=None, scales=None, device="cuda"):
         import torch
@@ -712,63 +774,103 @@ class Fp4Matrix:
         if (nc == 0 or ns == 0) and rows != 0 and cols != 0:
             raise MlpBlkError(MLPBLK_EINVAL, "mlpblk_fp4_codes_size")
         u8 = dict(dtype=torch.uint8, device=device)
-        self.codes = torch.empty(nc, **u8) if codes is None else codes
-        self.scales = torch.empty(ns, **u8) if scales is None else scales
-        if self.codes.numel() != nc or self.scales.numel() != ns:
-            raise MlpBlkError(MLPBLK_EINVAL, f"Fp4Matrix: {nc} bytes of codes and {ns} of scales")
+        self._codes = torch.empty(nc, **u8) if codes is None else codes
+        self._scales = torch.empty(ns, **u8) if scales is None else scales
+        for t, n in ((self._codes, nc), (self._scales, ns)):
+            if t.dtype is not torch.uint8 or t.numel() != n or not t.is_contiguous() or t.device != self._codes.device:
+                raise MlpBlkError(MLPBLK_EINVAL, f"Fp4Matrix: {nc} bytes of codes and {ns} of scales, contiguous uint8 "
+                                  "tensors of one device")
+        self._dev = self._codes.get_device()
+        self._at = (self._codes.data_ptr(), self._scales.data_ptr())
+        self._n = self.rows * self.cols * self.batch
+        self._descs = {}
+
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+
+    def _desc(self, dtype, transposed, act):
+        """byref of the descriptor for these options, made once."""
+        key = (dtype, transposed, act)
+        d = self._descs.get(key)
+        if d is None:
+            if act not in self._ACTS:
+                raise MlpBlkError(MLPBLK_ENOTSUP, f"Fp4Matrix.quantize: act {act!r}")
+            d = self._descs[key] = ctypes.byref(make_fp4_desc(self.rows, self.cols, self.batch, dtype, transposed,
+                                                              self._ACTS[act]))
+        return d
 
     def quantize(self, x, transposed=False, act="none", sort=None, gather=False, stream=None):
         """From x (bf16 or float32; stored [cols, rows] when transposed).  sort: a
         MoeSort whose row_map says which source rows are live; gather=True reads
         them from x's tokens, otherwise x is already in sorted order."""
-        acts = {"none": MLPBLK_FP4_ACT_NONE, "relu2": MLPBLK_FP4_ACT_RELU2}
-        if act not in acts:
-            raise MlpBlkError(MLPBLK_ENOTSUP, f"Fp4Matrix.quantize: act {act!r}")
-        if gather and sort is None:
-            raise MlpBlkError(MLPBLK_EINVAL, "Fp4Matrix.quantize: gather needs a sort")
-        d = Fp4Desc(self.rows, self.cols, self.batch, _dtype_code(x.dtype), int(bool(transposed)), acts[act])
+        where = "Fp4Matrix.quantize"
+        dev = self._device(where)
+        d = self._desc(x.dtype, transposed, act)
+        n, row_map, div = self._n, None, 0
         if sort is not None:
-            width = self.rows if transposed else self.cols
-            if gather and x.numel() != sort.desc.tokens * width:
-                raise MlpBlkError(MLPBLK_EINVAL, "Fp4Matrix.quantize: x is not [tokens, width] of the sort")
-            mlpblk_fp4_quantize(d, x, self.codes, self.scales, sort.row_map, sort.desc.top_k if gather else 0,
-                                stream=stream)
-        else:
-            mlpblk_fp4_quantize(d, x, self.codes, self.scales, stream=stream)
+            width, mapped = (self.rows, self.cols) if transposed else (self.cols, self.rows)
+            if mapped != sort.rows or (gather and width != sort.desc.width):
+                raise MlpBlkError(MLPBLK_EINVAL, f"{where}: [{self.rows}, {self.cols}] is not made of the sort's "
+                                  f"{sort.rows} rows of {sort.desc.width}")
+            sort._device(where)
+            row_map = sort._at[3]
+            if gather:
+                n, div = sort._x_n, sort.desc.top_k
+        elif gather:
+            raise MlpBlkError(MLPBLK_EINVAL, f"{where}: gather needs a sort")
+        _check(lib.mlpblk_fp4_quantize(d, _operand(x, where, "x", x.dtype, n, dev), row_map, div, *self._at,
+                                       _stream(stream)), where)
 
     def dequantize(self, y, stream=None):
-        d = Fp4Desc(self.rows, self.cols, self.batch, _dtype_code(y.dtype), 0, 0)
-        mlpblk_fp4_dequantize(d, self.codes, self.scales, y, stream=stream)
+        where = "Fp4Matrix.dequantize"
+        dev = self._device(where)
+        _check(lib.mlpblk_fp4_dequantize(self._desc(y.dtype, False, "none"), *self._at,
+                                         _operand(y, where, "y", y.dtype, self._n, dev), _stream(stream)), where)
 
-    def _common_k(self, b, where):
+    def _product(self, where, b, c, accumulate, key, make):
+        """byref of the product's descriptor (made once for each key) and C's address."""
+        dev = self._device(where)
+        b._device(where)
         if self.batch != 1 or b.cols != self.cols:
             raise MlpBlkError(MLPBLK_EINVAL, f"{where}: A [{self.rows}, {self.cols}] x {self.batch}, B [{b.rows}, {b.cols}]")
+        key = (where, c.dtype, accumulate, b.rows) + key
+        e = self._descs.get(key)
+        if e is None:
+            d, n = make(_dtype_code(c.dtype))
+            e = self._descs[key] = (ctypes.byref(d), n)
+        return e[0], _operand(c, where, "c", c.dtype, e[1], dev)
 
     def matmul(self, b, c, accumulate=False, stream=None):
         """c[rows, b.rows] = self . b^T (or += with accumulate, float32)."""
-        self._common_k(b, "Fp4Matrix.matmul")
+        where = "Fp4Matrix.matmul"
         if b.batch != 1:
-            raise MlpBlkError(MLPBLK_EINVAL, "Fp4Matrix.matmul: b is a batch")
-        d = Fp4MatmulDesc(self.rows, b.rows, self.cols, _dtype_code(c.dtype), int(bool(accumulate)), 0, 0, 0)
-        mlpblk_fp4_matmul(d, self.codes, self.scales, b.codes, b.scales, c, stream=stream)
+            raise MlpBlkError(MLPBLK_EINVAL, f"{where}: b is a batch")
+        d, at = self._product(where, b, c, accumulate, (), lambda dt: (
+            make_fp4_matmul_desc(self.rows, b.rows, self.cols, dt, accumulate), self.rows * b.rows))
+        _check(lib.mlpblk_fp4_matmul(d, *self._at, *b._at, at, _stream(stream)), where)
 
     def matmul_grouped(self, b, sort, c, accumulate=False, stream=None):
         """c[R, b.rows]: expert e's rows of self times the batch's matrix e."""
-        self._common_k(b, "Fp4Matrix.matmul_grouped")
+        where = "Fp4Matrix.matmul_grouped"
+        sort._device(where)
         if b.batch != sort.desc.experts or self.rows != sort.rows:
-            raise MlpBlkError(MLPBLK_EINVAL, "Fp4Matrix.matmul_grouped: b is not the experts' batch or self not the sorted rows")
-        d = Fp4MatmulDesc(self.rows, b.rows, self.cols, _dtype_code(c.dtype), int(bool(accumulate)), b.batch,
-                          sort.desc.pad, sort.desc.tokens * sort.desc.top_k)
-        mlpblk_fp4_matmul_grouped(d, self.codes, self.scales, b.codes, b.scales, sort.count, sort.seg, c, stream=stream)
+            raise MlpBlkError(MLPBLK_EINVAL, f"{where}: b is not the experts' batch or self not the sorted rows")
+        d, at = self._product(where, b, c, accumulate, (b.batch, sort.desc.pad, sort._entries), lambda dt: (
+            make_fp4_matmul_desc(self.rows, b.rows, self.cols, dt, accumulate, b.batch, sort.desc.pad, sort._entries),
+            self.rows * b.rows))
+        _check(lib.mlpblk_fp4_matmul_grouped(d, *self._at, *b._at, sort._at[0], sort._at[1], at, _stream(stream)), where)
 
     def wgrad_grouped(self, b, sort, c, accumulate=False, stream=None):
         """c[experts, rows, b.rows]: self . b^T over each expert's segment."""
-        self._common_k(b, "Fp4Matrix.wgrad_grouped")
+        where = "Fp4Matrix.wgrad_grouped"
+        sort._device(where)
         if b.batch != 1 or self.cols != sort.rows:
-            raise MlpBlkError(MLPBLK_EINVAL, "Fp4Matrix.wgrad_grouped: the columns are not the sorted rows")
-        d = Fp4MatmulDesc(self.rows, b.rows, self.cols, _dtype_code(c.dtype), int(bool(accumulate)), sort.desc.experts,
-                          sort.desc.pad, 0)
-        mlpblk_fp4_wgrad_grouped(d, self.codes, self.scales, b.codes, b.scales, sort.seg, c, stream=stream)
+            raise MlpBlkError(MLPBLK_EINVAL, f"{where}: the columns are not the sorted rows")
+        E = sort.desc.experts
+        d, at = self._product(where, b, c, accumulate, (E, sort.desc.pad), lambda dt: (
+            make_fp4_matmul_desc(self.rows, b.rows, self.cols, dt, accumulate, E, sort.desc.pad),
+            E * self.rows * b.rows))
+        _check(lib.mlpblk_fp4_wgrad_grouped(d, *self._at, *b._at, sort._at[1], at, _stream(stream)), where)
 
 
 def mlpblk_zero_grads(desc, dgamma, dw1, dw2, stream=None):

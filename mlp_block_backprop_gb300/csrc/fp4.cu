@@ -9,6 +9,8 @@
 // The scaling is by a power of two, so a code is rounded once and is the same
 // whatever precision computes it.  Both directions are bound by HBM: x is read once,
 // 17 bytes a block of 32 written.
+#include <type_traits>
+
 #include "fp4_layout.h"
 
 namespace mlpblk {
@@ -48,107 +50,169 @@ __device__ __forceinline__ float scale_inverse(uint32_t byte) {
     return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
 }
 
-template <bool RELU2>
-__device__ __forceinline__ float act(float v) {
-    if (!RELU2) return v;
-    const float r = v < 0.0f ? 0.0f : v;  // keeps a NaN
+// relu(v)^2, which keeps a NaN.
+__device__ __forceinline__ float relu2(float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
     return r * r;
 }
 
-template <class T>
-__device__ __forceinline__ float to_float(T v);
-template <>
-__device__ __forceinline__ float to_float<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_float<uint16_t>(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+// max(m, |v|), a NaN once there is one.
+__device__ __forceinline__ float max_abs(float m, float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t v) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(v & 0x7FFF7FFFu));
+    return r;
+}
 
-// The 8 values x[0..8) of a row from column c on (0 at and behind cols).  VEC: the
-// row is 16-byte aligned and cols a multiple of a 16-byte access.
-template <class T, bool VEC>
-__device__ __forceinline__ void load8(const T *row, int64_t c, int64_t cols, float (&v)[8]) {
-    if (VEC && sizeof(T) == 2) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (c < cols) u = __ldg(reinterpret_cast<const uint4 *>(row + c));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+// The source row of Q's row (or, transposed, column) r under a row map, or -1 for zeros.
+__device__ __forceinline__ int source_row(const int *row_map, int map_div, int64_t r) {
+    const int m = row_map[r];
+    return m < 0 ? -1 : (map_div > 0 ? m / map_div : static_cast<int>(r));
+}
+
+// 8 consecutive values of a row from column c on (0 at and behind cols), as loaded:
+// 4 words of bf16 pairs or 8 floats.  VEC: the row is 16-byte aligned and a multiple
+// of 16 bytes.
+template <bool BF16>
+struct Oct;
+template <>
+struct Oct<true> {
+    uint32_t w[4];
+    template <bool VEC>
+    __device__ __forceinline__ void load(const uint16_t *row, int64_t c, int64_t cols) {
+        if (VEC) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (c < cols) u = __ldg(reinterpret_cast<const uint4 *>(row + c));
+            w[0] = u.x;
+            w[1] = u.y;
+            w[2] = u.z;
+            w[3] = u.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = c + 2 * i < cols ? __ldg(row + c + 2 * i) : 0u;
+                const uint32_t hi = c + 2 * i + 1 < cols ? __ldg(row + c + 2 * i + 1) : 0u;
+                w[i] = lo | (hi << 16);
+            }
+        }
+    }
+    __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
+    __device__ __forceinline__ void floats(float (&v)[8]) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            v[2 * i] = bf16_lo(w[i]);
+            v[2 * i + 1] = bf16_hi(w[i]);
         }
-    } else if (VEC) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (c + 4 * h < cols) u = __ldg(reinterpret_cast<const float4 *>(row + c + 4 * h));
-            v[4 * h] = u.x;
-            v[4 * h + 1] = u.y;
-            v[4 * h + 2] = u.z;
-            v[4 * h + 3] = u.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? to_float<T>(__ldg(row + c + i)) : 0.0f;
     }
-}
+    // bits of max |v| as a float
+    __device__ __forceinline__ uint32_t top() const {
+        const uint32_t m = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(w[0] & 0x7FFF7FFFu, w[1]), w[2]), w[3]);
+        return max(m << 16, m & 0xFFFF0000u);
+    }
+};
+template <>
+struct Oct<false> {
+    float f[8];
+    template <bool VEC>
+    __device__ __forceinline__ void load(const float *row, int64_t c, int64_t cols) {
+        if (VEC) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (c + 4 * h < cols) u = __ldg(reinterpret_cast<const float4 *>(row + c + 4 * h));
+                f[4 * h] = u.x;
+                f[4 * h + 1] = u.y;
+                f[4 * h + 2] = u.z;
+                f[4 * h + 3] = u.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? __ldg(row + c + i) : 0.0f;
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+    }
+    __device__ __forceinline__ void floats(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = f[i];
+    }
+    __device__ __forceinline__ uint32_t top() const { return top8(f); }
+    static __device__ __forceinline__ uint32_t top8(const float (&v)[8]) {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max_abs(m, v[i]);
+        return __float_as_uint(m);
+    }
+};
 
-// Q's row r of x under a row map (Fp4Args): the source row, or -1 for a row of zeros.
-__device__ __forceinline__ int64_t source_row(const int *row_map, int map_div, int64_t r) {
-    if (!row_map) return r;
-    const int m = row_map[r];
-    return m < 0 ? -1 : (map_div > 0 ? m / map_div : r);
-}
-
-// Blocks along the source's rows.  An item is the rows r, r + 32, r + 64, r + 96 of a
-// 128-row scale tile over 256 columns: a lane holds 8 consecutive values of each, a
-// block is four lanes, and the four rows' scales of 4 blocks are 16 consecutive
-// bytes of a tile (one store), with the rows' neighbours filling the rest of a
-// sector.  The four rows' loads are in flight together.
-template <class T, bool VEC, bool RELU2>
+// Blocks along the source's rows.  A CTA takes 8 values of r % 32 of one 128-row scale
+// tile, a warp the rows r, r + 32, r + 64, r + 96, 256 columns at a time: a lane holds
+// 8 consecutive values of each row, a block is four lanes, and the four rows'
+// scales of 4 blocks are 16 consecutive bytes of a tile (one store), with the next
+// row's beside them.  The four rows' loads are in flight together.
+template <bool BF16, bool VEC, bool RELU2, bool MAP>
 __global__ void __launch_bounds__(kThreads)
-quantize_rows_kernel(const T *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows, int64_t cols,
-                     int64_t row_tiles, int64_t chunks, int64_t items, uint8_t *__restrict__ codes,
+quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
+                     int64_t cols, int row_tiles, int chunks, uint8_t *__restrict__ codes,
                      uint8_t *__restrict__ scales) {
+    using T = typename std::conditional<BF16, uint16_t, float>::type;
     griddep_enter();
     const int lane = threadIdx.x & 31;
     const int64_t ld = fp4_row_bytes(cols);
-    for (int64_t it = blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5); it < items;
-         it += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int64_t chunk = it % chunks;
-        const int64_t q = it / chunks;
-        const int64_t tile = q / 32;  // of the whole batch
-        const int64_t mat = tile / row_tiles;
-        const int64_t r0 = (tile - mat * row_tiles) * 128 + q % 32;
-        const int64_t c = chunk * 256 + lane * 8;
-        float v[4][8];
+    const int tile = static_cast<int>(blockIdx.x >> 2);  // of the whole batch
+    const int mat = tile / row_tiles;
+    const int rr = static_cast<int>(blockIdx.x & 3) * 8 + (threadIdx.x >> 5);
+    const int64_t r0 = static_cast<int64_t>(tile - mat * row_tiles) * 128 + rr;
+    const T *src[4];
+    bool live[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t r = r0 + 32 * j;
+        int64_t at = r < rows ? r : -1;
+        if (MAP && r < rows) at = source_row(row_map, map_div, r);
+        live[j] = at >= 0;
+        src[j] = static_cast<const T *>(x) + (mat * rows + (at < 0 ? 0 : at)) * cols;
+    }
+    uint8_t *out = codes + (mat * rows + r0) * ld;
+    for (int chunk = blockIdx.y; chunk < chunks; chunk += gridDim.y) {
+        const int64_t c = static_cast<int64_t>(chunk) * 256 + lane * 8;
+        Oct<BF16> o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int64_t r = r0 + 32 * j;
-            const int64_t src = r < rows ? source_row(row_map, map_div, r) : -1;
-            if (src >= 0) {
-                load8<T, VEC>(x + (mat * rows + src) * cols, c, cols, v[j]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-            }
+            if (live[j]) o[j].template load<VEC>(src[j], c, cols);
+            else o[j].zero();
         }
         uint32_t word[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            uint32_t m = 0;
+            float v[8];
+            o[j].floats(v);
+            uint32_t m;
+            if (RELU2) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[j][i] = act<RELU2>(v[j][i]);
-                m = max(m, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+                for (int i = 0; i < 8; ++i) v[i] = relu2(v[i]);
+                m = Oct<false>::top8(v);
+            } else {
+                m = o[j].top();
             }
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
             const uint32_t sb = scale_byte(m);
             const float inv = scale_inverse(sb);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[j][i] = sb == 255u ? 0.0f : v[j][i] * inv;
-            const int64_t r = r0 + 32 * j;
-            if (r < rows && c < 2 * ld)
-                *reinterpret_cast<uint32_t *>(codes + (mat * rows + r) * ld + c / 2) = e2m1x8(v[j]);
+            for (int i = 0; i < 8; ++i) v[i] *= inv;
+            const uint32_t q = sb == 255u ? 0u : e2m1x8(v);
+            if (r0 + 32 * j < rows && c < 2 * ld) *reinterpret_cast<uint32_t *>(out + 32 * j * ld + c / 2) = q;
             // the four blocks' bytes of this half warp
             uint32_t w = sb << (8 * ((lane >> 2) & 3));
             w |= __shfl_xor_sync(0xffffffffu, w, 4);
@@ -156,107 +220,132 @@ quantize_rows_kernel(const T *__restrict__ x, const int *__restrict__ row_map, i
             word[j] = w;
         }
         if ((lane & 15) == 0) {
-            uint8_t *st = scales + ((tile * chunks + chunk) * 2 + (lane >> 4)) * 512 + (q % 32) * 16;
+            uint8_t *st = scales + ((static_cast<int64_t>(tile) * chunks + chunk) * 2 + (lane >> 4)) * 512 + rr * 16;
             *reinterpret_cast<uint4 *>(st) = make_uint4(word[0], word[1], word[2], word[3]);
         }
     }
 }
 
 // Two neighbouring values of a source row, columns c and c + 1 (0 at and behind
-// `width`).  VEC: width is even, so a pair is one aligned access.
-template <class T, bool VEC>
-__device__ __forceinline__ float2 load2(const T *row, int64_t c, int64_t width) {
-    float2 f = make_float2(0.0f, 0.0f);
-    if (VEC) {
-        if (c < width) {
-            if (sizeof(T) == 2) {
-                const uint32_t u = __ldg(reinterpret_cast<const uint32_t *>(row + c));
-                f = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
-            } else {
-                f = __ldg(reinterpret_cast<const float2 *>(row + c));
-            }
+// `width`), as loaded.  VEC: width is even, so a pair is one aligned access.
+template <bool BF16>
+struct Pair;
+template <>
+struct Pair<true> {
+    uint32_t w;
+    template <bool VEC>
+    __device__ __forceinline__ void load(const uint16_t *row, int64_t c, int64_t width) {
+        if (VEC) {
+            w = c < width ? __ldg(reinterpret_cast<const uint32_t *>(row + c)) : 0u;
+        } else {
+            const uint32_t lo = c < width ? __ldg(row + c) : 0u, hi = c + 1 < width ? __ldg(row + c + 1) : 0u;
+            w = lo | (hi << 16);
         }
-    } else {
-        if (c < width) f.x = to_float<T>(__ldg(row + c));
-        if (c + 1 < width) f.y = to_float<T>(__ldg(row + c + 1));
     }
-    return f;
+    __device__ __forceinline__ void zero() { w = 0u; }
+    __device__ __forceinline__ float lo() const { return bf16_lo(w); }
+    __device__ __forceinline__ float hi() const { return bf16_hi(w); }
+};
+template <>
+struct Pair<false> {
+    float2 f;
+    template <bool VEC>
+    __device__ __forceinline__ void load(const float *row, int64_t c, int64_t width) {
+        f = make_float2(0.0f, 0.0f);
+        if (VEC) {
+            if (c < width) f = __ldg(reinterpret_cast<const float2 *>(row + c));
+        } else {
+            if (c < width) f.x = __ldg(row + c);
+            if (c + 1 < width) f.y = __ldg(row + c + 1);
+        }
+    }
+    __device__ __forceinline__ void zero() { f = make_float2(0.0f, 0.0f); }
+    __device__ __forceinline__ float lo() const { return f.x; }
+    __device__ __forceinline__ float hi() const { return f.y; }
+};
+
+// The 32 values of one block, every one from `get(i)`: their codes and scale byte.
+template <bool RELU2, class F>
+__device__ __forceinline__ uint4 quantize_block(F get, uint32_t &sb) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m = max_abs(m, RELU2 ? relu2(get(i)) : get(i));
+    sb = scale_byte(__float_as_uint(m));
+    const float inv = scale_inverse(sb);
+    uint32_t q[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (RELU2 ? relu2(get(8 * g + i)) : get(8 * g + i)) * inv;
+        q[g] = sb == 255u ? 0u : e2m1x8(v);
+    }
+    return make_uint4(q[0], q[1], q[2], q[3]);
 }
 
 // Blocks along the source's columns: Q = x^T, Q's rows are x's columns.  A CTA
 // takes 64 columns and 256 rows of x; warp w holds rows 32w .. 32w + 31 of it, two
-// columns a lane, so a block is one lane's 32 registers.  The codes cross shared
-// memory to leave as 128 consecutive bytes a row of Q.
+// columns a lane, so a block is one lane's 32 values, kept as they were loaded (pairs of
+// bf16 in one register).  The codes cross shared memory to leave as 128 consecutive
+// bytes a row of Q.
 constexpr int kTCols = 64;              // x's columns of a CTA (Q's rows)
 constexpr int kTPitch = 128 + 16;       // bytes of a Q row in shared memory
 
-template <class T, bool VEC, bool RELU2>
-__global__ void __launch_bounds__(kThreads)
-quantize_cols_kernel(const T *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows, int64_t cols,
-                     int64_t row_tiles, int64_t chunks, int64_t items, uint8_t *__restrict__ codes,
+template <bool BF16, bool VEC, bool RELU2, bool MAP>
+__global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2)
+quantize_cols_kernel(const void *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
+                     int64_t cols, int row_tiles, int chunks, uint8_t *__restrict__ codes,
                      uint8_t *__restrict__ scales) {
+    using T = typename std::conditional<BF16, uint16_t, float>::type;
     __shared__ __align__(16) uint8_t sc[kTCols][kTPitch];
     __shared__ __align__(8) uint8_t ss[kTCols][8];
     griddep_enter();
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int64_t ld = fp4_row_bytes(cols);
-    const int64_t halves = row_tiles * 2;  // 64-row parts of the scale tiles of one matrix
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int64_t half = it % halves;
-        const int64_t q = it / halves;
-        const int64_t chunk = q % chunks, mat = q / chunks;
-        const int64_t r0 = half * kTCols;             // Q's first row
-        const int64_t c0 = chunk * 256 + wid * 32;    // Q's first column of this warp: x's row
-        const T *base = x + mat * rows * cols;
-        const int64_t own = c0 + lane;
-        const int64_t mine = own < cols ? source_row(row_map, map_div, own) : -1;
-        float a[32], b[32];
-        uint32_t ma = 0, mb = 0;
+    const int halves = row_tiles * 2;  // 64-row parts of the scale tiles of one matrix
+    const int mat = static_cast<int>(blockIdx.x) / halves;
+    const int half = static_cast<int>(blockIdx.x) - mat * halves;
+    const int64_t r0 = static_cast<int64_t>(half) * kTCols;  // Q's first row
+    const int64_t col = r0 + 2 * lane;                       // x's column
+    const T *base = static_cast<const T *>(x) + mat * rows * cols;
+    for (int chunk = blockIdx.y; chunk < chunks; chunk += gridDim.y) {
+        const int64_t c0 = static_cast<int64_t>(chunk) * 256 + wid * 32;  // Q's first column of this warp: x's row
+        Pair<BF16> p[32];
+        if (MAP) {
+            const int64_t own = c0 + lane;
+            const int mine = own < cols ? source_row(row_map, map_div, own) : -1;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const int64_t src = __shfl_sync(0xffffffffu, mine, i);
-            float2 f = make_float2(0.0f, 0.0f);
-            if (src >= 0) f = load2<T, VEC>(base + src * rows, r0 + 2 * lane, rows);
-            a[i] = f.x;
-            b[i] = f.y;
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            a[i] = act<RELU2>(a[i]);
-            b[i] = act<RELU2>(b[i]);
-            ma = max(ma, __float_as_uint(a[i]) & 0x7FFFFFFFu);
-            mb = max(mb, __float_as_uint(b[i]) & 0x7FFFFFFFu);
-        }
-        const uint32_t sa = scale_byte(ma), sb = scale_byte(mb);
-        const float ia = scale_inverse(sa), ib = scale_inverse(sb);
-        uint32_t wa[4], wb[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            float va[8], vb[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                va[i] = sa == 255u ? 0.0f : a[8 * g + i] * ia;
-                vb[i] = sb == 255u ? 0.0f : b[8 * g + i] * ib;
+            for (int i = 0; i < 32; ++i) {
+                const int src = __shfl_sync(0xffffffffu, mine, i);
+                p[i].template load<VEC>(base + (src < 0 ? 0 : src) * rows, src < 0 ? rows : col, rows);
             }
-            wa[g] = e2m1x8(va);
-            wb[g] = e2m1x8(vb);
+        } else {
+            const T *row = base + c0 * rows;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const bool in = c0 + i < cols;
+                p[i].template load<VEC>(in ? row + i * rows : base, in ? col : rows, rows);
+            }
         }
-        *reinterpret_cast<uint4 *>(&sc[2 * lane][wid * 16]) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
-        *reinterpret_cast<uint4 *>(&sc[2 * lane + 1][wid * 16]) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+        uint32_t sa, sb;
+        *reinterpret_cast<uint4 *>(&sc[2 * lane][wid * 16]) = quantize_block<RELU2>([&](int i) { return p[i].lo(); }, sa);
+        *reinterpret_cast<uint4 *>(&sc[2 * lane + 1][wid * 16]) = quantize_block<RELU2>([&](int i) { return p[i].hi(); }, sb);
         ss[2 * lane][wid] = static_cast<uint8_t>(sa);
         ss[2 * lane + 1][wid] = static_cast<uint8_t>(sb);
         __syncthreads();
-        for (int p = threadIdx.x; p < kTCols * 8; p += kThreads) {
-            const int r = p >> 3, blk = p & 7;
-            const int64_t at = chunk * 128 + blk * 16;
+#pragma unroll
+        for (int h = 0; h < kTCols * 8 / kThreads; ++h) {
+            const int q = threadIdx.x + h * kThreads;
+            const int r = q >> 3, blk = q & 7;
+            const int64_t at = static_cast<int64_t>(chunk) * 128 + blk * 16;
             if (r0 + r < rows && at < ld)
                 *reinterpret_cast<uint4 *>(codes + (mat * rows + r0 + r) * ld + at) =
                     *reinterpret_cast<const uint4 *>(&sc[r][blk * 16]);
         }
         if (threadIdx.x < kTCols * 2) {
             const int r = threadIdx.x >> 1, g = threadIdx.x & 1;  // row, 4-block group
-            const int64_t tile = mat * row_tiles + half / 2;
-            const int rt = static_cast<int>((half & 1) * 64) + r;  // row of the scale tile
+            const int64_t tile = static_cast<int64_t>(mat) * row_tiles + half / 2;
+            const int rt = (half & 1) * 64 + r;  // row of the scale tile
             *reinterpret_cast<uint32_t *>(scales + ((tile * chunks + chunk) * 2 + g) * 512 + (rt % 32) * 16 + (rt / 32) * 4) =
                 *reinterpret_cast<const uint32_t *>(&ss[r][g * 4]);
         }
@@ -296,91 +385,126 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return r;
 }
 
-// One thread per 8 values: 4 bytes of codes and their block's scale byte.
-template <class T, bool VEC>
+// A warp per row, 1024 columns at a time: a lane takes 8 values of each 256, 4 bytes of
+// codes and their block's scale byte, with four of them in flight.
+constexpr int kDeqChunks = 4;
+
+template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows, int64_t cols,
-                  int64_t row_tiles, int64_t chunks, int64_t items, int64_t per_row, T *__restrict__ y) {
+                  int64_t all_rows, int row_tiles, int chunks, void *__restrict__ y) {
+    using T = typename std::conditional<BF16, uint16_t, float>::type;
     griddep_enter();
-    const int64_t ld = fp4_row_bytes(cols);
-    for (int64_t it = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; it < items;
-         it += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int64_t row = it / per_row, c = (it - row * per_row) * 8;
-        const int64_t mat = row / rows, r = row - mat * rows;
-        const uint32_t u = __ldg(reinterpret_cast<const uint32_t *>(codes + row * ld + c / 2));
-        const int64_t tile = (mat * row_tiles + r / 128) * chunks * 2 + c / 128;
-        const uint32_t sb = __ldg(scales + tile * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + (c / 32) % 4);
-        float v[8];
-        decode8(u, scale_value(sb), v);
-        T *out = y + row * cols + c;
-        if (VEC && sizeof(T) == 2) {
-            *reinterpret_cast<uint4 *>(out) =
-                make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-        } else if (VEC) {
-            *reinterpret_cast<float4 *>(out) = make_float4(v[0], v[1], v[2], v[3]);
-            if (c + 4 < cols) *(reinterpret_cast<float4 *>(out) + 1) = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    if (row >= all_rows) return;
+    const int64_t mat = row / rows, r = row - mat * rows, ld = fp4_row_bytes(cols);
+    const uint8_t *in = codes + row * ld + lane * 4;
+    const uint8_t *sc = scales + (mat * row_tiles + r / 128) * chunks * 1024 + (lane >> 4) * 512 + (r % 32) * 16 +
+                        (r % 128) / 32 * 4 + ((lane >> 2) & 3);
+    T *out = static_cast<T *>(y) + row * cols;
+    for (int g = blockIdx.y * kDeqChunks; g < chunks; g += gridDim.y * kDeqChunks) {
+        uint32_t u[kDeqChunks], sb[kDeqChunks];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (c + i < cols) {
-                    if (sizeof(T) == 2) reinterpret_cast<uint16_t *>(out)[i] = static_cast<uint16_t>(pack2(v[i], 0.0f) & 0xFFFFu);
-                    else reinterpret_cast<float *>(out)[i] = v[i];
-                }
+        for (int j = 0; j < kDeqChunks; ++j) {
+            const int64_t c = static_cast<int64_t>(g + j) * 256 + lane * 8;
+            u[j] = sb[j] = 0u;
+            if (c < cols) {
+                u[j] = __ldg(reinterpret_cast<const uint32_t *>(in + static_cast<int64_t>(g + j) * 128));
+                sb[j] = __ldg(sc + static_cast<int64_t>(g + j) * 1024);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kDeqChunks; ++j) {
+            const int64_t c = static_cast<int64_t>(g + j) * 256 + lane * 8;
+            if (c >= cols) continue;
+            float v[8];
+            decode8(u[j], scale_value(sb[j]), v);
+            if (VEC && BF16) {
+                *reinterpret_cast<uint4 *>(out + c) =
+                    make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+            } else if (VEC) {
+                *reinterpret_cast<float4 *>(out + c) = make_float4(v[0], v[1], v[2], v[3]);
+                if (c + 4 < cols) *reinterpret_cast<float4 *>(out + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c + i < cols) {
+                        if (BF16) reinterpret_cast<uint16_t *>(out)[c + i] = static_cast<uint16_t>(pack2(v[i], 0.0f) & 0xFFFFu);
+                        else reinterpret_cast<float *>(out)[c + i] = v[i];
+                    }
+            }
         }
     }
 }
 
-unsigned grid_for(int64_t blocks, int per_sm) {
+int sm_total() {
     int dev = 0, n = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t cap = static_cast<int64_t>(n > 0 ? n : 1) * per_sm;
-    return static_cast<unsigned>(blocks < 1 ? 1 : (blocks < cap ? blocks : cap));
+    return n > 0 ? n : 1;
 }
 
-template <class T, bool RELU2>
+// CTAs along the second axis (up to `most` pieces of work) beside x CTAs along the
+// first: about 32 CTAs an SM in all.
+dim3 grid_for(int64_t x, int64_t most) {
+    int64_t y = (static_cast<int64_t>(sm_total()) * 32 + x - 1) / x;
+    if (y > most) y = most;
+    if (y > 65535) y = 65535;
+    return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y < 1 ? 1 : y));
+}
+
+template <bool BF16, bool RELU2, bool MAP>
 int quantize_typed(const void *x, const int *row_map, int map_div, int64_t rows, int64_t cols, int batch,
                    bool transposed, uint8_t *codes, uint8_t *scales, cudaStream_t s) {
-    const int64_t row_tiles = (rows + 127) / 128, chunks = (cols + 255) / 256;
-    const T *xt = static_cast<const T *>(x);
+    const int row_tiles = static_cast<int>((rows + 127) / 128), chunks = static_cast<int>((cols + 255) / 256);
     if (transposed) {
-        const int64_t items = row_tiles * 2 * chunks * batch;
-        auto kern = rows % 2 == 0 ? quantize_cols_kernel<T, true, RELU2> : quantize_cols_kernel<T, false, RELU2>;
-        return launch_pdl(kern, dim3(grid_for(items, 16)), dim3(kThreads), 0, s, xt, row_map, map_div, rows, cols,
-                          row_tiles, chunks, items, codes, scales);
+        auto kern = rows % 2 == 0 ? quantize_cols_kernel<BF16, true, RELU2, MAP> : quantize_cols_kernel<BF16, false, RELU2, MAP>;
+        return launch_pdl(kern, grid_for(static_cast<int64_t>(row_tiles) * 2 * batch, chunks), dim3(kThreads), 0, s, x,
+                          row_map, map_div, rows, cols, row_tiles, chunks, codes, scales);
     }
-    const int64_t items = row_tiles * 32 * chunks * batch;
-    auto kern = cols * sizeof(T) % 16 == 0 ? quantize_rows_kernel<T, true, RELU2> : quantize_rows_kernel<T, false, RELU2>;
-    return launch_pdl(kern, dim3(grid_for((items + kWarps - 1) / kWarps, 16)), dim3(kThreads), 0, s, xt, row_map,
-                      map_div, rows, cols, row_tiles, chunks, items, codes, scales);
+    auto kern = cols * (BF16 ? 2 : 4) % 16 == 0 ? quantize_rows_kernel<BF16, true, RELU2, MAP>
+                                                : quantize_rows_kernel<BF16, false, RELU2, MAP>;
+    return launch_pdl(kern, grid_for(static_cast<int64_t>(row_tiles) * 4 * batch, chunks), dim3(kThreads), 0, s, x,
+                      row_map, map_div, rows, cols, row_tiles, chunks, codes, scales);
 }
 
-template <class T>
+template <bool BF16>
+int quantize_dtype(const void *x, const int *row_map, int map_div, int64_t rows, int64_t cols, int batch,
+                   bool transposed, bool relu2, uint8_t *codes, uint8_t *scales, cudaStream_t s) {
+#define MLPBLK_Q(R, M) return quantize_typed<BF16, R, M>(x, row_map, map_div, rows, cols, batch, transposed, codes, scales, s)
+    if (relu2) {
+        if (row_map) MLPBLK_Q(true, true);
+        MLPBLK_Q(true, false);
+    }
+    if (row_map) MLPBLK_Q(false, true);
+    MLPBLK_Q(false, false);
+#undef MLPBLK_Q
+}
+
+template <bool BF16>
 int dequantize_typed(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, int batch, void *y,
                      cudaStream_t s) {
-    const int64_t row_tiles = (rows + 127) / 128, chunks = (cols + 255) / 256;
-    const int64_t per_row = (cols + 7) / 8, items = per_row * rows * batch;
-    auto kern = cols * sizeof(T) % 16 == 0 ? dequantize_kernel<T, true> : dequantize_kernel<T, false>;
-    return launch_pdl(kern, dim3(grid_for((items + kThreads - 1) / kThreads, 16)), dim3(kThreads), 0, s, codes, scales,
-                      rows, cols, row_tiles, chunks, items, per_row, static_cast<T *>(y));
+    const int row_tiles = static_cast<int>((rows + 127) / 128), chunks = static_cast<int>((cols + 255) / 256);
+    const int64_t all = rows * batch;
+    auto kern = cols * (BF16 ? 2 : 4) % 16 == 0 ? dequantize_kernel<BF16, true> : dequantize_kernel<BF16, false>;
+    return launch_pdl(kern, grid_for((all + kWarps - 1) / kWarps, (chunks + kDeqChunks - 1) / kDeqChunks), dim3(kThreads), 0,
+                      s, codes, scales, rows, cols, all, row_tiles, chunks, y);
 }
 
 }  // namespace
 
 int launch_fp4_quantize(int dtype, const void *x, const int *row_map, int map_div, int64_t rows, int64_t cols,
                         int batch, bool transposed, bool relu2, uint8_t *codes, uint8_t *scales, cudaStream_t s) {
-    if (dtype == MLPBLK_BF16) {
-        if (relu2) return quantize_typed<uint16_t, true>(x, row_map, map_div, rows, cols, batch, transposed, codes, scales, s);
-        return quantize_typed<uint16_t, false>(x, row_map, map_div, rows, cols, batch, transposed, codes, scales, s);
-    }
-    if (relu2) return quantize_typed<float, true>(x, row_map, map_div, rows, cols, batch, transposed, codes, scales, s);
-    return quantize_typed<float, false>(x, row_map, map_div, rows, cols, batch, transposed, codes, scales, s);
+    return dtype == MLPBLK_BF16
+               ? quantize_dtype<true>(x, row_map, map_div, rows, cols, batch, transposed, relu2, codes, scales, s)
+               : quantize_dtype<false>(x, row_map, map_div, rows, cols, batch, transposed, relu2, codes, scales, s);
 }
 
 int launch_fp4_dequantize(int dtype, const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols,
                           int batch, void *y, cudaStream_t s) {
-    if (dtype == MLPBLK_BF16) return dequantize_typed<uint16_t>(codes, scales, rows, cols, batch, y, s);
-    return dequantize_typed<float>(codes, scales, rows, cols, batch, y, s);
+    return dtype == MLPBLK_BF16 ? dequantize_typed<true>(codes, scales, rows, cols, batch, y, s)
+                                : dequantize_typed<false>(codes, scales, rows, cols, batch, y, s);
 }
 
 }  // namespace mlpblk

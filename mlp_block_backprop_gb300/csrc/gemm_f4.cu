@@ -16,6 +16,9 @@
 //   registers: 32 lanes are 32 consecutive elements of a row of C, whatever n is.
 //   K can be split over a cluster; the parts meet in distributed shared memory and
 //   are added in rank order.
+// f4_pair: two CTAs on two SMs compute a 256 x 256 tile (cta_group::2), A's rows on the
+//   lanes; each CTA stages 128 rows of A and of B, and the scales of its A rows and
+//   of all 256 columns.
 #include "fp4_layout.h"
 #include "gemm_tc.cuh"
 
@@ -34,7 +37,7 @@ struct F4Args {
     int64_t max_rows;
     const uint8_t *sa, *sb;             // scales
     int64_t row_tile_bytes;             // of one 128-row strip of scale tiles (A and B share K)
-    int64_t sb_expert_bytes;            // one expert's B scales
+    int group_m;                        // raster: this many tiles of A sweep B together
     const int *count, *seg;
     void *c;
     int accumulate;
@@ -133,7 +136,9 @@ struct F4Tile {
     int a_row, b_row;          // rows of the code matrices (TMA coordinates)
     const uint8_t *sa, *sb;    // scale tiles of those rows at k-block 0
     int kb0, kb1;              // k-blocks
-    int64_t c_row;             // C's row of the tile's first A row
+    int sa_tile, sb_tile;      // the same as row indices of the scale arrays
+    int64_t c_row;             // C's row of the tile's first A row, counted through all of C
+    int c_local, c_mat;        // the same as a row of one matrix of C, and which
     int n0, m_valid, n_valid;
 };
 
@@ -201,12 +206,16 @@ __device__ __forceinline__ F4Tile f4_tile(const F4Args &a, const F4Groups *g, in
     w.a_row = first + mi * TM;
     w.n0 = ni * TN;
     w.b_row = (a.mode == kFp4GroupRows ? e * static_cast<int>(a.n) : 0) + w.n0;
-    w.sa = a.sa + (w.a_row / 128) * a.row_tile_bytes;
-    w.sb = a.sb + (a.mode == kFp4GroupRows ? e * a.sb_expert_bytes : 0) + (w.n0 / 128) * a.row_tile_bytes;
+    w.sa_tile = w.a_row / 128;
+    w.sb_tile = (a.mode == kFp4GroupRows ? e * static_cast<int>((a.n + 127) / 128) : 0) + w.n0 / 128;
+    w.sa = a.sa + w.sa_tile * a.row_tile_bytes;
+    w.sb = a.sb + w.sb_tile * a.row_tile_bytes;
     w.kb0 = 0;
     w.kb1 = a.kblocks;
-    w.c_row = w.a_row;
+    w.c_row = w.c_local = w.a_row;
+    w.c_mat = 0;
     if (a.mode == kFp4GroupK) {
+        w.c_mat = e;
         w.kb0 = g->seg[e] / kF4KB;
         w.kb1 = g->seg[e + 1] / kF4KB;
         w.c_row += e * a.m;
@@ -313,7 +322,6 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     }
     __syncthreads();
     const int tiles = *tiles_s;
-    constexpr int kGroupM = 8;
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
@@ -322,7 +330,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             uint32_t phase = 0;
             bool ok = true;
             for (int t = worker; ok && t < tiles; t += workers) {
-                const F4Tile w = f4_tile<C::BN, 128>(args, groups, t, kGroupM);
+                const F4Tile w = f4_tile<C::BN, 128>(args, groups, t, args.group_m);
                 const int nk = w.kb1 - w.kb0;
                 const int k0 = w.kb0 + nk * rank / cs, k1 = w.kb0 + nk * (rank + 1) / cs;
                 for (int kb = k0; kb < k1; ++kb) {
@@ -350,7 +358,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             uint32_t phase = 0;
             bool ok = true;
             for (int t = worker; ok && t < tiles; t += workers, ++it) {
-                const F4Tile w = f4_tile<C::BN, 128>(args, groups, t, kGroupM);
+                const F4Tile w = f4_tile<C::BN, 128>(args, groups, t, args.group_m);
                 const int nk = w.kb1 - w.kb0;
                 const int k0 = w.kb0 + nk * rank / cs, k1 = w.kb0 + nk * (rank + 1) / cs;
                 const int buf = it & 1;
@@ -396,7 +404,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         const int i = 32 * q + lane;  // lane of the tile: C's column n0 + i
         int it = 0;
         for (int t = worker; t < tiles; t += workers, ++it) {
-            const F4Tile w = f4_tile<C::BN, 128>(args, groups, t, kGroupM);
+            const F4Tile w = f4_tile<C::BN, 128>(args, groups, t, args.group_m);
             const int nk = w.kb1 - w.kb0;
             const bool some = nk * (rank + 1) / cs > nk * rank / cs;  // this CTA has a part of K
             const int buf = it & 1;
@@ -457,6 +465,326 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     }
 }
 
+// --------------------------------------------------------------------- f4_pair
+
+__device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  setp.ne.b32 p, %6, 0;\n"
+        "  tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n"
+        "}\n"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// tmem_copy_scales in both CTAs of the pair, each from its own shared memory.
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t s_desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int32_t c0, int32_t c1, int32_t c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap *map, const void *src, int32_t c0, int32_t c1,
+                                                  int32_t c2) {
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
+// TMEM of a pair tile: the two accumulators overlap in 64 columns, which leaves 64
+// for the scales: accumulator 0 at 0, accumulator 1 at 192, two sets of scales (A: 8
+// columns, B: 16) at 448.  The epilogue drains the shared columns first and tells the
+// MMA so; only then may the next tile start, and it does while the rest drains.
+struct F4Pair {
+    static constexpr int kThreads = 320;           // TMA, MMA, eight epilogue warps
+    static constexpr int kOpBytes = 128 * 128;     // 128 rows of A or B
+    static constexpr int kSfABytes = 1024, kSfBBytes = 2048;
+    static constexpr int kStageBytes = 2 * kOpBytes + kSfABytes + kSfBBytes;
+    static constexpr int kStagingBytes = 8 * 4096; // 32 rows x 128 B an epilogue warp
+    static constexpr int kCtrlBytes = 4096;
+    static constexpr int kStages = (kSmemLimit - 1024 - kCtrlBytes - kStagingBytes) / kStageBytes;
+    static constexpr int kSmemBytes = 1024 + kCtrlBytes + kStagingBytes + kStages * kStageBytes;
+    static constexpr int kAcc1 = 192, kSfCol = 448, kSfSet = 24;
+    static_assert(kStages >= 4 && kSfCol + 2 * kSfSet <= 512, "shared memory or TMEM over budget");
+};
+
+// OUT: 0 bf16, 1 float32, 2 float32 +=.  TMA_OUT: rows of C are a multiple of 16 bytes.
+template <int OUT, bool TMA_OUT>
+__global__ void __launch_bounds__(F4Pair::kThreads, 1)
+f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+               const __grid_constant__ CUtensorMap tmC, const F4Args args) {
+    using P = F4Pair;
+    constexpr int S = P::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *a_s = smem;                             // [S][128 rows][128 B]
+    uint8_t *b_s = a_s + S * P::kOpBytes;            // [S][128 rows][128 B]
+    uint8_t *staging = b_s + S * P::kOpBytes;        // [8 warps][32 rows][128 B]
+    uint8_t *sf_s = staging + P::kStagingBytes;      // [S][A 1 KB, B 2 KB]
+    uint8_t *ctrl = sf_s + S * (P::kSfABytes + P::kSfBBytes);
+    uint64_t *full_bar = reinterpret_cast<uint64_t *>(ctrl);
+    uint64_t *empty_bar = full_bar + S;
+    uint64_t *accf_bar = empty_bar + S;
+    uint64_t *acce_bar = accf_bar + 2;   // accumulator drained
+    uint64_t *ovl_bar = acce_bar + 2;    // the columns shared with the other accumulator drained
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctrl + 384);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 388);
+    int *tiles_s = reinterpret_cast<int *>(ctrl + 392);
+    F4Groups *groups = reinterpret_cast<F4Groups *>(ctrl + 512);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int worker = static_cast<int>(blockIdx.x >> 1), workers = static_cast<int>(gridDim.x >> 1);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full_bar[s], 1);
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&accf_bar[b], 1);
+            mbar_init(&acce_bar[b], 16);  // both CTAs' epilogue warps (the leader's barrier counts)
+        }
+        mbar_init(ovl_bar, 8);            // the four warps of each CTA that drain those columns
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+        prefetch_tensormap(&tmSA);
+        prefetch_tensormap(&tmSB);
+        if (TMA_OUT) prefetch_tensormap(&tmC);
+    }
+    cluster_sync();
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_alloc_permit_pair();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    griddep_enter();
+    if (warp == 0) {
+        int tiles;
+        if (args.mode == kFp4Dense)
+            tiles = static_cast<int>((args.m + 255) / 256) * static_cast<int>((args.n + 255) / 256);
+        else
+            tiles = f4_groups<256, 256>(args, groups, lane);
+        if (lane == 0) *tiles_s = tiles;
+    }
+    __syncthreads();
+    const int tiles = *tiles_s;
+
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = worker; ok && t < tiles; t += workers) {
+                const F4Tile w = f4_tile<256, 256>(args, groups, t, args.group_m);
+                const int a_row = w.a_row + static_cast<int>(rank) * 128, b_row = w.b_row + static_cast<int>(rank) * 128;
+                for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                    ok = mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag);
+                    if (!ok) break;
+                    uint8_t *da = a_s + stage * P::kOpBytes, *db = b_s + stage * P::kOpBytes;
+                    uint8_t *sf = sf_s + stage * (P::kSfABytes + P::kSfBBytes);
+                    if (leader) {
+                        // the leader's barrier collects both CTAs' bytes
+                        uint64_t *bar = &full_bar[stage];
+                        mbar_arrive_expect_tx(bar, 2 * P::kStageBytes);
+                        tma_load_2d(&tmA, bar, da, kb * 128, a_row);
+                        tma_load_2d(&tmB, bar, db, kb * 128, b_row);
+                        tma_load_2d(&tmSA, bar, sf, kb * 256, w.sa_tile);
+                        tma_load_2d(&tmSB, bar, sf + P::kSfABytes, kb * 256, w.sb_tile);
+                    } else {
+                        const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
+                        tma_load_2d_pair(&tmA, bar, da, kb * 128, a_row);
+                        tma_load_2d_pair(&tmB, bar, db, kb * 128, b_row);
+                        tma_load_2d_pair(&tmSA, bar, sf, kb * 256, w.sa_tile + 1);
+                        tma_load_2d_pair(&tmSB, bar, sf + P::kSfABytes, kb * 256, w.sb_tile);
+                    }
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------- MMA issuer
+        if (lane == 0 && leader) {
+            int stage = 0, it = 0, set = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = worker; ok && t < tiles; t += workers) {
+                const F4Tile w = f4_tile<256, 256>(args, groups, t, args.group_m);
+                if (w.kb0 == w.kb1) continue;
+                const int buf = it & 1;
+                ok = mbar_wait(&acce_bar[buf], ((it >> 1) & 1) ^ 1u, abort_flag);
+                if (ok && it > 0) ok = mbar_wait(ovl_bar, (it - 1) & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint32_t d = tmem_base + (buf ? P::kAcc1 : 0);
+                for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                    ok = mbar_wait(&full_bar[stage], phase, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint32_t aa = smem_u32(a_s + stage * P::kOpBytes), ba = smem_u32(b_s + stage * P::kOpBytes);
+                    const uint32_t sf = smem_u32(sf_s + stage * (P::kSfABytes + P::kSfBBytes));
+                    const uint32_t sa = tmem_base + P::kSfCol + set * P::kSfSet, sb = sa + 8;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        tmem_copy_scales_pair(sa + 4 * g, smem_desc_scales(sf + g * kFp4TileBytes));
+                        tmem_copy_scales_pair(sb + 8 * g, smem_desc_scales(sf + P::kSfABytes + g * kFp4TileBytes));
+                        tmem_copy_scales_pair(sb + 8 * g + 4, smem_desc_scales(sf + P::kSfABytes + 1024 + g * kFp4TileBytes));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        umma_mxf4_pair(d, smem_desc_sw128(aa + 32 * j, 16, 1024), smem_desc_sw128(ba + 32 * j, 16, 1024),
+                                       (j & 1) ? idesc_mxf4(256, 256, 2) : idesc_mxf4(256, 256, 0), sa + 4 * (j >> 1),
+                                       sb + 8 * (j >> 1), (kb > w.kb0 || j > 0) ? 1u : 0u);
+                    umma_commit_pair(&empty_bar[stage], 3);
+                    set ^= 1;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                umma_commit_pair(&accf_bar[buf], 3);
+                ++it;
+            }
+        }
+        __syncwarp();
+    } else {
+        // --------------------------------------------------------- epilogue
+        // Two warps a lane quarter.  The first drains the 64 columns that the other
+        // accumulator shares, then 64 more; the second the remaining 128.
+        const int q = warp & 3, ew = warp - 2;
+        const bool first = ew < 4;
+        uint8_t *st = staging + ew * 4096;
+        const uint32_t srow = smem_u32(st) + lane * 128;
+        const uint32_t sw = static_cast<uint32_t>(lane & 7);
+        const uint32_t ovl0 = mapa_shared(smem_u32(ovl_bar), 0), acce0 = mapa_shared(smem_u32(&acce_bar[0]), 0);
+        int it = 0;
+        for (int t = worker; t < tiles; t += workers) {
+            const F4Tile w = f4_tile<256, 256>(args, groups, t, args.group_m);
+            const bool some = w.kb0 < w.kb1;
+            const int buf = it & 1;
+            if (some) {
+                const bool ok = mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc_fence_after_sync();
+            }
+            const int rt = static_cast<int>(rank) * 128 + 32 * q;  // the warp's first row of the tile
+            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + (buf ? P::kAcc1 : 0);
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                const int chunk = buf ? (first ? i : 2 + i) : (first ? 3 - i : i);
+                float v[2][32];
+                if (some) {
+                    tmem_load_64cols(t_row + 64 * chunk, v[0], v[1]);
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        // the leader's MMA may overwrite what every warp has now read
+                        if (i == 0 && first) {
+                            if (leader) mbar_arrive_relaxed(ovl_bar);
+                            else mbar_arrive_cluster_relaxed(ovl0);
+                        }
+                        if (i == 1) {
+                            if (leader) mbar_arrive_relaxed(&acce_bar[buf]);
+                            else mbar_arrive_cluster_relaxed(acce0 + buf * 8);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[0][j] = v[1][j] = 0.0f;
+                }
+                const int col = w.n0 + 64 * chunk;
+                if (rt >= w.m_valid || col >= args.n) continue;
+                constexpr int kParts = OUT == 0 ? 1 : 2;  // 128-byte pieces of a row of the chunk
+#pragma unroll
+                for (int h = 0; h < kParts; ++h) {
+                    constexpr int kCols = OUT == 0 ? 64 : 32;
+                    const int c0 = col + h * kCols;
+                    if (TMA_OUT) {
+                        if (lane == 0) bulk_wait_group_read<0>();  // the staging rows are free again
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t at = srow + ((static_cast<uint32_t>(j) ^ sw) << 4);
+                        if (OUT == 0) {
+                            const float *e = j < 4 ? &v[0][8 * j] : &v[1][8 * (j - 4)];
+                            st_shared_v4(at, pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
+                                         pack_bf16x2(e[6], e[7]));
+                        } else {
+                            const float *e = &v[h][4 * j];
+                            st_shared_v4(at, __float_as_uint(e[0]), __float_as_uint(e[1]), __float_as_uint(e[2]),
+                                         __float_as_uint(e[3]));
+                        }
+                    }
+                    if (TMA_OUT) {
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0 && c0 < args.n) {
+                            const int r = w.c_local + rt;
+                            if (OUT == 2) tma_reduce_add_3d(&tmC, st, c0, r, w.c_mat);
+                            else tma_store_3d(&tmC, st, c0, r, w.c_mat);
+                            bulk_commit_group();
+                        }
+                    } else {
+                        // rows of any length: a row at a time, neighbouring lanes neighbouring columns
+                        __syncwarp();
+                        const int n_rows = min(32, w.m_valid - rt);
+                        for (int r = 0; r < n_rows; ++r) {
+                            const int64_t at = (w.c_row + rt + r) * args.n;
+                            const uint8_t *row = st + r * 128;
+#pragma unroll
+                            for (int u = 0; u < kCols / 32; ++u) {
+                                const int c = lane + 32 * u;
+                                if (c0 + c >= args.n) continue;
+                                const int byte = c * (OUT == 0 ? 2 : 4);
+                                const uint8_t *p = row + ((((byte >> 4) ^ (r & 7)) << 4) | (byte & 15));
+                                if (OUT == 0) {
+                                    static_cast<uint16_t *>(args.c)[at + c0 + c] = *reinterpret_cast<const uint16_t *>(p);
+                                } else {
+                                    float *o = static_cast<float *>(args.c) + at + c0 + c;
+                                    const float f = *reinterpret_cast<const float *>(p);
+                                    *o = OUT == 2 ? *o + f : f;
+                                }
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (some) ++it;
+        }
+        if (TMA_OUT && lane == 0) bulk_wait_group<0>();
+        __syncwarp();
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the pair's MMAs may touch it
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
 // A code matrix as a 2-D byte array: box of 128 bytes (a stage of K) x `box_rows` rows.
 bool make_map_codes(CUtensorMap *m, const void *codes, int64_t rows, int64_t k, uint32_t box_rows) {
     return make_map_2d(m, codes, kMapU8, static_cast<uint64_t>(fp4_row_bytes(k)), static_cast<uint64_t>(rows), 128, box_rows);
@@ -494,6 +822,75 @@ int run_small(const F4Args &a, const Fp4Product &p, int cs, int workers, cudaStr
     return cuda_status(cudaLaunchKernelEx(&cfg, f4_small_kernel<C, F32>, mA, mB, a));
 }
 
+// Scales as a 2-D array of words: a row is the tiles of 128 rows of the matrix, a
+// stage's part of it 256 words.
+bool make_map_scales(CUtensorMap *m, const void *scales, int64_t row_tiles, int64_t k, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint64_t words = static_cast<cuuint64_t>(fp4_col_tiles(k)) * (kFp4TileBytes / 4);
+    cuuint64_t dims[2] = {words, static_cast<cuuint64_t>(row_tiles)};
+    cuuint64_t strides[1] = {words * 4};
+    cuuint32_t box[2] = {256, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(scales), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// C as matrices of [m, n]: boxes of 32 rows x 128 bytes, 128-byte swizzle.
+bool make_map_c(CUtensorMap *m, void *c, bool f32, int64_t mats, int64_t rows, int64_t cols) {
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint64_t esz = f32 ? 4 : 2;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(mats)};
+    cuuint64_t strides[2] = {dims[0] * esz, dims[0] * dims[1] * esz};
+    cuuint32_t box[3] = {f32 ? 32u : 64u, 32u, 1u};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c, dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int OUT, bool TMA_OUT>
+int run_pair(const F4Args &a, const Fp4Product &p, int workers, cudaStream_t s) {
+    CUtensorMap mA, mB, mSA, mSB, mC;
+    const bool rows_grouped = p.mode == kFp4GroupRows;
+    const int64_t a_tiles = (p.m + 127) / 128, b_tiles = (p.n + 127) / 128 * (rows_grouped ? p.experts : 1);
+    if (!make_map_codes(&mA, p.a, p.m, p.k, 128) || !make_map_codes(&mB, p.b, rows_grouped ? p.n * p.experts : p.n, p.k, 128) ||
+        !make_map_scales(&mSA, p.sa, a_tiles, p.k, 1) || !make_map_scales(&mSB, p.sb, b_tiles, p.k, 2))
+        return MLPBLK_ECUDA;
+    if (TMA_OUT) {
+        if (!make_map_c(&mC, p.c, OUT != 0, p.mode == kFp4GroupK ? p.experts : 1, p.m, p.n)) return MLPBLK_ECUDA;
+    } else {
+        mC = mA;
+    }
+    static int attr_set[64] = {0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return MLPBLK_ECUDA;
+    if (!attr_set[dev]) {
+        const int rc = cuda_status(cudaFuncSetAttribute(f4_pair_kernel<OUT, TMA_OUT>,
+                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, F4Pair::kSmemBytes));
+        if (rc != MLPBLK_OK) return rc;
+        attr_set[dev] = 1;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * static_cast<unsigned>(workers));
+    cfg.blockDim = dim3(F4Pair::kThreads);
+    cfg.dynamicSmemBytes = F4Pair::kSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, f4_pair_kernel<OUT, TMA_OUT>, mA, mB, mSA, mSB, mC, a));
+}
+
 }  // namespace
 
 int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s) {
@@ -507,7 +904,7 @@ int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s) {
     a.sa = p.sa;
     a.sb = p.sb;
     a.row_tile_bytes = fp4_col_tiles(p.k) * kFp4TileBytes;
-    a.sb_expert_bytes = fp4_scales_bytes(p.n, p.k);
+    a.group_m = 8;
     a.count = p.count;
     a.seg = p.seg;
     a.c = p.c;
@@ -520,6 +917,16 @@ int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s) {
         groups = p.experts;
     } else if (p.mode == kFp4GroupK) {
         groups = p.experts;
+    }
+    // 256 x 256 pair tiles where they occupy most of the SM pairs
+    const int pairs = num_sms / 2;
+    const int64_t pair_tiles = (p.mode == kFp4GroupRows ? (p.m + 255) / 256 : (rows + 255) / 256 * groups) * ((p.n + 255) / 256);
+    if (pairs >= 1 && rows > 128 && 2 * pair_tiles >= pairs) {
+        const bool tma = p.n * (f32 ? 4 : 2) % 16 == 0;
+        const int w = static_cast<int>(p.mode != kFp4GroupRows && pair_tiles < pairs ? pair_tiles : pairs);
+        if (!f32) return tma ? run_pair<0, true>(a, p, w, s) : run_pair<0, false>(a, p, w, s);
+        if (!p.accumulate) return tma ? run_pair<1, true>(a, p, w, s) : run_pair<1, false>(a, p, w, s);
+        return tma ? run_pair<2, true>(a, p, w, s) : run_pair<2, false>(a, p, w, s);
     }
     const bool few = rows <= 32;
     const int64_t bn = few ? 32 : 128;

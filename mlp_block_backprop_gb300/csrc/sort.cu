@@ -145,7 +145,7 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
 
 // A row is `units` accesses of type U (16, 4 or 2 bytes: the widest that divides
 // a row).  blockDim = (threads of a row, rows of a block); a thread holds kPer units
-// at a time, so a row of 4096 bf16 values is two 16-byte accesses for each of 256
+// at a time, so a row of 4096 bf16 values is four 16-byte accesses for each of 128
 // threads.
 constexpr int kMoveThreads = 256;
 constexpr int kPer = 4;
@@ -270,8 +270,9 @@ permute_kernel(const U *__restrict__ x, const int *__restrict__ pos, const int *
 }
 
 // y[t] = residual[t] + sum_j w[t,j] * rows[pos[t,j]], slot order, float32, rounded
-// once.  residual and y may be the same array: an element is read and written by
-// the same thread.
+// once.  Two slots' rows are loaded together, so that a thread has 3 * kPer accesses
+// in flight.  residual and y may be the same array: an element is read and written
+// by the same thread.
 template <class U, bool BF16>
 __global__ void __launch_bounds__(kMoveThreads)
 unpermute_kernel(const U *__restrict__ rows, const int *__restrict__ pos, const float *__restrict__ weights,
@@ -283,32 +284,44 @@ unpermute_kernel(const U *__restrict__ rows, const int *__restrict__ pos, const 
     const int *pt = pos + t * k;
     for (int64_t c0 = threadIdx.x; c0 < units; c0 += kPer * blockDim.x) {
         float acc[kPer][V::N];
+        U res[kPer];
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
             const int64_t c = c0 + u * blockDim.x;
-            if (residual && c < units) {
-                V::get(residual[t * units + c], acc[u]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < V::N; ++i) acc[u][i] = 0.0f;
-            }
+            res[u] = residual && c < units ? residual[t * units + c] : zero_unit<U>();
         }
-        for (int j = 0; j < k; ++j) {
-            const int64_t r = pt[j];
-            if (r < 0) continue;
-            const float w = weights ? weights[t * k + j] : 1.0f;
-            U o[kPer];
+        for (int j = 0; j < k; j += 2) {
+            const int64_t ra = pt[j], rb = j + 1 < k ? pt[j + 1] : -1;
+            const float wa = weights ? weights[t * k + j] : 1.0f;
+            const float wb = weights && j + 1 < k ? weights[t * k + j + 1] : 1.0f;
+            U oa[kPer], ob[kPer];
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
                 const int64_t c = c0 + u * blockDim.x;
-                o[u] = c < units ? __ldg(rows + r * units + c) : zero_unit<U>();
+                oa[u] = c < units && ra >= 0 ? __ldg(rows + ra * units + c) : zero_unit<U>();
+                ob[u] = c < units && rb >= 0 ? __ldg(rows + rb * units + c) : zero_unit<U>();
             }
+            if (j == 0) {
 #pragma unroll
-            for (int u = 0; u < kPer; ++u) {
-                float f[V::N];
-                V::get(o[u], f);
+                for (int u = 0; u < kPer; ++u) V::get(res[u], acc[u]);
+            }
+            if (ra >= 0) {
 #pragma unroll
-                for (int i = 0; i < V::N; ++i) acc[u][i] += w * f[i];
+                for (int u = 0; u < kPer; ++u) {
+                    float f[V::N];
+                    V::get(oa[u], f);
+#pragma unroll
+                    for (int i = 0; i < V::N; ++i) acc[u][i] += wa * f[i];
+                }
+            }
+            if (rb >= 0) {
+#pragma unroll
+                for (int u = 0; u < kPer; ++u) {
+                    float f[V::N];
+                    V::get(ob[u], f);
+#pragma unroll
+                    for (int i = 0; i < V::N; ++i) acc[u][i] += wb * f[i];
+                }
             }
         }
 #pragma unroll
@@ -320,10 +333,10 @@ unpermute_kernel(const U *__restrict__ rows, const int *__restrict__ pos, const 
 }
 
 // d_rows[pos[t,j]] = w[t,j] * dy[t] and dw[t,j] = <dy[t], rows[pos[t,j]]>.  Slots go
-// in groups of kSlots whose dot products are held together, so dy is read from
-// HBM once; a dot product is summed over the row's threads by shuffles, then over
-// its warps in warp order.  d_weights NULL skips the products and rows.
-constexpr int kSlots = 4;
+// in pairs whose rows are loaded together with dy; a dot product is summed over the
+// row's threads by shuffles, then over its warps in warp order.  d_weights NULL skips
+// the products and rows.
+constexpr int kSlots = 2;
 
 template <class U, bool BF16>
 __global__ void __launch_bounds__(kMoveThreads)
@@ -332,7 +345,7 @@ unpermute_bwd_kernel(const U *__restrict__ dy, const U *__restrict__ rows, const
                      int64_t T, int k, int experts, int pad, int64_t units, int64_t token_blocks,
                      U *__restrict__ d_rows, float *__restrict__ d_weights) {
     using V = Vals<U, BF16>;
-    __shared__ float part[kSlots][kMoveThreads / 32];
+    __shared__ float part[2][kSlots][kMoveThreads / 32];
     griddep_enter();
     const int64_t b = blockIdx.x;
     if (b >= token_blocks) {
@@ -346,7 +359,7 @@ unpermute_bwd_kernel(const U *__restrict__ dy, const U *__restrict__ rows, const
     const int w0 = threadIdx.y * warps;
     for (int j0 = 0; j0 < k; j0 += kSlots) {
         float s[kSlots];
-        int r[kSlots];
+        int64_t r[kSlots];
         float w[kSlots];
 #pragma unroll
         for (int j = 0; j < kSlots; ++j) {
@@ -356,55 +369,49 @@ unpermute_bwd_kernel(const U *__restrict__ dy, const U *__restrict__ rows, const
             w[j] = on && weights ? weights[t * k + j0 + j] : 1.0f;
         }
         for (int64_t c0 = threadIdx.x; in && c0 < units; c0 += kPer * blockDim.x) {
-            U g[kPer];
+            U g[kPer], o[kSlots][kPer];
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
                 const int64_t c = c0 + u * blockDim.x;
                 g[u] = c < units ? __ldg(dy + t * units + c) : zero_unit<U>();
+#pragma unroll
+                for (int j = 0; j < kSlots; ++j)
+                    o[j][u] = d_weights && c < units && r[j] >= 0 ? __ldg(rows + r[j] * units + c) : zero_unit<U>();
             }
 #pragma unroll
-            for (int j = 0; j < kSlots; ++j) {
-                if (r[j] < 0) continue;
-                U o[kPer];
-                if (d_weights) {
+            for (int u = 0; u < kPer; ++u) {
+                const int64_t c = c0 + u * blockDim.x;
+                if (c >= units) continue;
+                float a[V::N];
+                V::get(g[u], a);
 #pragma unroll
-                    for (int u = 0; u < kPer; ++u) {
-                        const int64_t c = c0 + u * blockDim.x;
-                        o[u] = c < units ? __ldg(rows + r[j] * units + c) : zero_unit<U>();
+                for (int j = 0; j < kSlots; ++j) {
+                    if (r[j] < 0) continue;
+                    float f[V::N];
+                    V::get(o[j][u], f);
+#pragma unroll
+                    for (int i = 0; i < V::N; ++i) {
+                        s[j] += a[i] * f[i];
+                        f[i] = a[i] * w[j];
                     }
-                }
-#pragma unroll
-                for (int u = 0; u < kPer; ++u) {
-                    const int64_t c = c0 + u * blockDim.x;
-                    if (c >= units) continue;
-                    float a[V::N];
-                    V::get(g[u], a);
-                    if (d_weights) {
-                        float f[V::N];
-                        V::get(o[u], f);
-#pragma unroll
-                        for (int i = 0; i < V::N; ++i) s[j] += a[i] * f[i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < V::N; ++i) a[i] *= w[j];
-                    d_rows[r[j] * units + c] = V::put(a);
+                    d_rows[r[j] * units + c] = V::put(f);
                 }
             }
         }
         if (!d_weights) continue;
+        const int buf = (j0 / kSlots) & 1;
 #pragma unroll
         for (int j = 0; j < kSlots; ++j) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
-            if ((threadIdx.x & 31) == 0) part[j][w0 + threadIdx.x / 32] = s[j];
+            if ((threadIdx.x & 31) == 0) part[buf][j][w0 + threadIdx.x / 32] = s[j];
         }
-        __syncthreads();
+        __syncthreads();  // one barrier a pair of slots: the next pair writes the other half of `part`
         if (in && threadIdx.x < kSlots && j0 + threadIdx.x < k) {
             float d = 0.0f;
-            for (int q = 0; q < warps; ++q) d += part[threadIdx.x][w0 + q];
+            for (int q = 0; q < warps; ++q) d += part[buf][threadIdx.x][w0 + q];
             d_weights[t * k + j0 + threadIdx.x] = d;
         }
-        __syncthreads();
     }
 }
 
@@ -422,7 +429,7 @@ MoveShape move_shape(int64_t T, int64_t width, int dtype, int experts, int pad) 
     m.unit = bytes % 16 == 0 ? 16 : (bytes % 4 == 0 ? 4 : 2);
     m.units = bytes / m.unit;
     unsigned tx = 32;
-    while (tx < static_cast<unsigned>(kMoveThreads) && tx * 2 < m.units) tx *= 2;
+    while (tx < static_cast<unsigned>(kMoveThreads) && tx * kPer < m.units) tx *= 2;
     m.block = dim3(tx, kMoveThreads / tx, 1);
     m.token_blocks = (T + m.block.y - 1) / m.block.y;
     m.pad_blocks = pad > 1 ? (static_cast<int64_t>(experts) * pad + m.block.y - 1) / m.block.y : 0;

@@ -192,7 +192,7 @@ def _quantized(mb, rng, rows, cols, batch=1, wide=True):
     return q, vals if batch > 1 else vals[0]
 
 
-@pytest.mark.parametrize("shape", [(1, 128, 256), (32, 128, 64), (128, 128, 1024), (256, 512, 512)])
+@pytest.mark.parametrize("shape", [(1, 128, 256), (32, 128, 64), (128, 128, 1024), (256, 512, 512), (2560, 2048, 1024)])
 def test_product_exact(mb, shape):
     """Codes of every value with scale 1, each row its own pattern: sums are exact,
     and a wrong lane, column, K order or scale would show."""
@@ -210,12 +210,12 @@ def test_product_exact(mb, shape):
     np.testing.assert_array_equal(to_np(c), a @ b.T)
 
 
-@pytest.mark.parametrize("m", [1, 32, 128])
-def test_product_scales(mb, m):
+@pytest.mark.parametrize("m,n", [(1, 256), (32, 256), (128, 256), (2560, 2048)])
+def test_product_scales(mb, m, n):
     """One non-zero element a row, scales that differ by row and block: each output is
     one exact product, so every scale must reach its own row and block of K."""
     import torch
-    n, k = 256, 1024
+    k = 1024
     rng = np.random.default_rng(m)
     a, b = np.zeros((m, k)), np.exp2(rng.integers(-8, 8, size=(n, k // 32))).repeat(32, axis=1)
     a[np.arange(m), rng.integers(0, k, m)] = np.exp2(rng.integers(-8, 8, m))
@@ -302,7 +302,8 @@ def _np32(v):
 
 # (T, d, n, E, k, pad)
 GROUPED = [(1, 64, 130, 3, 2, 128), (8, 256, 512, 8, 2, 128), (40, 300, 200, 5, 2, 128), (300, 96, 333, 7, 3, 256),
-           (700, 520, 640, 4, 2, 128), (2000, 256, 1024, 3, 2, 256), (513, 128, 64, 200, 4, 128)]
+           (700, 520, 640, 4, 2, 128), (2000, 256, 1024, 3, 2, 256), (513, 128, 64, 200, 4, 128),
+           (3000, 200, 1000, 5, 2, 128), (3000, 136, 1001, 5, 2, 128)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
@@ -339,7 +340,8 @@ def test_grouped_product(mb, case, out):
 
 
 @pytest.mark.parametrize("accumulate", [False, True])
-@pytest.mark.parametrize("case", [(1, 64, 130, 3, 2), (40, 300, 200, 5, 2), (300, 96, 333, 7, 3), (2000, 256, 520, 4, 2)])
+@pytest.mark.parametrize("case", [(1, 64, 130, 3, 2), (40, 300, 200, 5, 2), (300, 96, 333, 7, 3), (2000, 256, 520, 4, 2),
+                                  (1000, 1024, 1200, 6, 2), (1000, 1023, 1200, 6, 2)])
 def test_grouped_wgrad(mb, case, accumulate):
     import torch
     T, d, n, E, k = case

@@ -200,8 +200,8 @@ def test_fp4_product_refusals(mb):
 def test_binding_refuses_wrong_tensors(mb):
     torch = pytest.importorskip("torch")
     with pytest.raises(mb.MlpBlkError):                       # not a CUDA tensor
-        mb._operand(torch.zeros(4), "f", "x", (torch.float32,), 4)
-    assert mb._operand(None, "f", "x", (torch.float32,), 4) is None
+        mb._operand(torch.zeros(4), "f", "x", torch.float32, 4, 0)
+    assert mb._operand(None, "f", "x", torch.float32, 4, 0) is None
     with pytest.raises(mb.MlpBlkError):
         mb.make_sort_desc(1, 1, 1, 1, dtype="f16")
     with pytest.raises(mb.MlpBlkError):
