@@ -479,11 +479,6 @@ __device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc,
         : "memory");
 }
 
-// tmem_copy_scales in both CTAs of the pair, each from its own shared memory.
-__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t s_desc) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
-}
-
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int32_t c0, int32_t c1, int32_t c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
                  ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
@@ -497,21 +492,36 @@ __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap *map, const 
                  : "memory");
 }
 
-// TMEM of a pair tile: the two accumulators overlap in 64 columns, which leaves 64
-// for the scales: accumulator 0 at 0, accumulator 1 at 192, two sets of scales (A: 8
-// columns, B: 16) at 448.  The epilogue drains the shared columns first and tells the
-// MMA so; only then may the next tile start, and it does while the rest drains.
+// Four columns of scales of this warp's lane quarter from registers.
+__device__ __forceinline__ void tmem_store_4cols(uint32_t taddr, uint4 v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// TMEM of a pair tile: the two accumulators overlap in 128 columns, which leaves 128
+// for the scales: accumulator 0 at 0, accumulator 1 at 128, the scales of each of the
+// five stages (A: 8 columns, B: 16) from 384 on.  The epilogue drains the shared
+// columns first and tells the MMA so; only then may the next tile start, and it does
+// while the rest drains.
+//
+// Four warps of each CTA put a stage's scales into TMEM (tcgen05.st, one lane quarter
+// each).  tcgen05.cp would do it without them, but it runs in the MMAs' pipe: its six
+// copies a stage cost some 300 of a stage's 512 MMA cycles (8192 x 16384 x 4096: 236
+// us with the copies, 189 without them).
 struct F4Pair {
-    static constexpr int kThreads = 320;           // TMA, MMA, eight epilogue warps
+    static constexpr int kThreads = 448;           // TMA, MMA, eight epilogue warps, four scale warps
     static constexpr int kOpBytes = 128 * 128;     // 128 rows of A or B
     static constexpr int kSfABytes = 1024, kSfBBytes = 2048;
-    static constexpr int kStageBytes = 2 * kOpBytes + kSfABytes + kSfBBytes;
+    static constexpr int kSfBytes = kSfABytes + kSfBBytes;
+    static constexpr int kStageBytes = 2 * kOpBytes + kSfBytes;
     static constexpr int kStagingBytes = 8 * 4096; // 32 rows x 128 B an epilogue warp
     static constexpr int kCtrlBytes = 4096;
     static constexpr int kStages = (kSmemLimit - 1024 - kCtrlBytes - kStagingBytes) / kStageBytes;
     static constexpr int kSmemBytes = 1024 + kCtrlBytes + kStagingBytes + kStages * kStageBytes;
-    static constexpr int kAcc1 = 192, kSfCol = 448, kSfSet = 24;
-    static_assert(kStages >= 4 && kSfCol + 2 * kSfSet <= 512, "shared memory or TMEM over budget");
+    static constexpr int kAcc1 = 128, kSfCol = 384, kSfSet = 24;
+    static_assert(kStages >= 4 && kSfCol + kStages * kSfSet <= 512, "shared memory or TMEM over budget");
 };
 
 // OUT: 0 bf16, 1 float32, 2 float32 +=.  TMA_OUT: rows of C are a multiple of 16 bytes.
@@ -528,12 +538,13 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     uint8_t *b_s = a_s + S * P::kOpBytes;            // [S][128 rows][128 B]
     uint8_t *staging = b_s + S * P::kOpBytes;        // [8 warps][32 rows][128 B]
     uint8_t *sf_s = staging + P::kStagingBytes;      // [S][A 1 KB, B 2 KB]
-    uint8_t *ctrl = sf_s + S * (P::kSfABytes + P::kSfBBytes);
+    uint8_t *ctrl = sf_s + S * P::kSfBytes;
     uint64_t *full_bar = reinterpret_cast<uint64_t *>(ctrl);
     uint64_t *empty_bar = full_bar + S;
     uint64_t *accf_bar = empty_bar + S;
     uint64_t *acce_bar = accf_bar + 2;   // accumulator drained
     uint64_t *ovl_bar = acce_bar + 2;    // the columns shared with the other accumulator drained
+    uint64_t *sf_bar = ovl_bar + 1;      // this CTA's scales of a stage are in shared memory
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctrl + 384);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 388);
     int *tiles_s = reinterpret_cast<int *>(ctrl + 392);
@@ -546,14 +557,15 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full_bar[s], 1);
+            mbar_init(&full_bar[s], 1 + 8);  // both CTAs' operands, and their scale warps
             mbar_init(&empty_bar[s], 1);
+            mbar_init(&sf_bar[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accf_bar[b], 1);
             mbar_init(&acce_bar[b], 16);  // both CTAs' epilogue warps (the leader's barrier counts)
         }
-        mbar_init(ovl_bar, 8);            // the four warps of each CTA that drain those columns
+        mbar_init(ovl_bar, 16);
         *abort_flag = 0;
         fence_barrier_init();
         prefetch_tensormap(&tmA);
@@ -596,21 +608,20 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     ok = mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag);
                     if (!ok) break;
                     uint8_t *da = a_s + stage * P::kOpBytes, *db = b_s + stage * P::kOpBytes;
-                    uint8_t *sf = sf_s + stage * (P::kSfABytes + P::kSfBBytes);
+                    uint8_t *sf = sf_s + stage * P::kSfBytes;
+                    mbar_arrive_expect_tx(&sf_bar[stage], P::kSfBytes);
+                    tma_load_2d(&tmSA, &sf_bar[stage], sf, kb * 256, w.sa_tile + static_cast<int>(rank));
+                    tma_load_2d(&tmSB, &sf_bar[stage], sf + P::kSfABytes, kb * 256, w.sb_tile);
                     if (leader) {
-                        // the leader's barrier collects both CTAs' bytes
+                        // the leader's barrier collects both CTAs' operand bytes
                         uint64_t *bar = &full_bar[stage];
-                        mbar_arrive_expect_tx(bar, 2 * P::kStageBytes);
+                        mbar_arrive_expect_tx(bar, 4 * P::kOpBytes);
                         tma_load_2d(&tmA, bar, da, kb * 128, a_row);
                         tma_load_2d(&tmB, bar, db, kb * 128, b_row);
-                        tma_load_2d(&tmSA, bar, sf, kb * 256, w.sa_tile);
-                        tma_load_2d(&tmSB, bar, sf + P::kSfABytes, kb * 256, w.sb_tile);
                     } else {
                         const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
                         tma_load_2d_pair(&tmA, bar, da, kb * 128, a_row);
                         tma_load_2d_pair(&tmB, bar, db, kb * 128, b_row);
-                        tma_load_2d_pair(&tmSA, bar, sf, kb * 256, w.sa_tile + 1);
-                        tma_load_2d_pair(&tmSB, bar, sf + P::kSfABytes, kb * 256, w.sb_tile);
                     }
                     if (++stage == S) {
                         stage = 0;
@@ -623,7 +634,7 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     } else if (warp == 1) {
         // ------------------------------------------------------- MMA issuer
         if (lane == 0 && leader) {
-            int stage = 0, it = 0, set = 0;
+            int stage = 0, it = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int t = worker; ok && t < tiles; t += workers) {
@@ -640,21 +651,13 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     if (!ok) break;
                     tc_fence_after_sync();
                     const uint32_t aa = smem_u32(a_s + stage * P::kOpBytes), ba = smem_u32(b_s + stage * P::kOpBytes);
-                    const uint32_t sf = smem_u32(sf_s + stage * (P::kSfABytes + P::kSfBBytes));
-                    const uint32_t sa = tmem_base + P::kSfCol + set * P::kSfSet, sb = sa + 8;
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        tmem_copy_scales_pair(sa + 4 * g, smem_desc_scales(sf + g * kFp4TileBytes));
-                        tmem_copy_scales_pair(sb + 8 * g, smem_desc_scales(sf + P::kSfABytes + g * kFp4TileBytes));
-                        tmem_copy_scales_pair(sb + 8 * g + 4, smem_desc_scales(sf + P::kSfABytes + 1024 + g * kFp4TileBytes));
-                    }
+                    const uint32_t sa = tmem_base + P::kSfCol + stage * P::kSfSet, sb = sa + 8;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         umma_mxf4_pair(d, smem_desc_sw128(aa + 32 * j, 16, 1024), smem_desc_sw128(ba + 32 * j, 16, 1024),
                                        (j & 1) ? idesc_mxf4(256, 256, 2) : idesc_mxf4(256, 256, 0), sa + 4 * (j >> 1),
                                        sb + 8 * (j >> 1), (kb > w.kb0 || j > 0) ? 1u : 0u);
                     umma_commit_pair(&empty_bar[stage], 3);
-                    set ^= 1;
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
@@ -666,10 +669,52 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             }
         }
         __syncwarp();
+    } else if (warp >= 10) {
+        // ------------------------------------------------------ scale warps
+        // Shared memory to TMEM.  A stage's TMEM columns are free again once its shared
+        // memory is (its MMAs have completed), so sf_bar's phase covers both.
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t full0 = mapa_shared(smem_u32(&full_bar[0]), 0);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = worker; ok && t < tiles; t += workers) {
+            const F4Tile w = f4_tile<256, 256>(args, groups, t, args.group_m);
+            for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                ok = mbar_wait(&sf_bar[stage], phase, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after_sync();
+                // word 4l + j of a tile is row 32j + l's four scales: column j, lane l
+                const uint32_t sf = smem_u32(sf_s + stage * P::kSfBytes) + lane * 16;
+                const uint32_t to = tmem_base + lanes + P::kSfCol + stage * P::kSfSet;
+                uint4 v[6];
+#pragma unroll
+                for (int i = 0; i < 6; ++i) v[i] = ld_shared_v4(sf + i * kFp4TileBytes);
+                tmem_store_4cols(to, v[0]);       // A, K values 0-127 of the stage
+                tmem_store_4cols(to + 4, v[1]);   // A, 128-255
+                tmem_store_4cols(to + 8, v[2]);   // B rows 0-127, K 0-127
+                tmem_store_4cols(to + 12, v[4]);  // B rows 128-255, K 0-127
+                tmem_store_4cols(to + 16, v[3]);
+                tmem_store_4cols(to + 20, v[5]);
+                tmem_wait_store();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    // no memory access to release: wait::st has completed the TMEM writes
+                    if (leader) mbar_arrive_relaxed(&full_bar[stage]);
+                    else mbar_arrive_cluster_relaxed(full0 + stage * 8);
+                }
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
     } else {
         // --------------------------------------------------------- epilogue
-        // Two warps a lane quarter.  The first drains the 64 columns that the other
-        // accumulator shares, then 64 more; the second the remaining 128.
+        // Two warps a lane quarter; each drains 64 of the 128 columns that the other
+        // accumulator shares, then 64 more.
         const int q = warp & 3, ew = warp - 2;
         const bool first = ew < 4;
         uint8_t *st = staging + ew * 4096;
@@ -690,7 +735,7 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + (buf ? P::kAcc1 : 0);
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
-                const int chunk = buf ? (first ? i : 2 + i) : (first ? 3 - i : i);
+                const int chunk = buf ? (first ? 0 : 1) + 2 * i : (first ? 2 : 3) - 2 * i;
                 float v[2][32];
                 if (some) {
                     tmem_load_64cols(t_row + 64 * chunk, v[0], v[1]);
@@ -698,7 +743,7 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     __syncwarp();
                     if (lane == 0) {
                         // the leader's MMA may overwrite what every warp has now read
-                        if (i == 0 && first) {
+                        if (i == 0) {
                             if (leader) mbar_arrive_relaxed(ovl_bar);
                             else mbar_arrive_cluster_relaxed(ovl0);
                         }
