@@ -32,6 +32,7 @@ constexpr int kF4KB = 256;              // K values of a stage
 struct F4Args {
     int mode;                           // Fp4Mode
     int64_t m, n;                       // C (per expert when K-grouped)
+    int mt, nt;                         // tiles along m (but when grouped by rows) and n
     int kblocks;                        // stages along all of K
     int experts;
     int64_t max_rows;
@@ -148,8 +149,7 @@ struct F4Tile {
 template <int TM, int TN>
 __device__ int f4_groups(const F4Args &a, F4Groups *g, int lane) {
     const int64_t limit = a.mode == kFp4GroupRows ? a.m : static_cast<int64_t>(a.kblocks) * kF4KB;
-    const int nt = static_cast<int>((a.n + TN - 1) / TN);
-    const int mt = static_cast<int>((a.m + TM - 1) / TM);
+    const int nt = a.nt, mt = a.mt;
     int run = 0;
     for (int e0 = 0; e0 < a.experts; e0 += 32) {
         const int e = e0 + lane;
@@ -197,11 +197,9 @@ __device__ __forceinline__ F4Tile f4_tile(const F4Args &a, const F4Groups *g, in
         e = lo;
         t -= g->before[e];
     }
-    const int nt = static_cast<int>((a.n + TN - 1) / TN);
     const int rows = a.mode == kFp4GroupRows ? g->count[e] : static_cast<int>(a.m);
-    const int mt = (rows + TM - 1) / TM;
     int mi = 0, ni = 0;
-    raster_tile(t, mt, nt, group_m, mi, ni);
+    raster_tile(t, (rows + TM - 1) / TM, a.nt, group_m, mi, ni);
     const int first = a.mode == kFp4GroupRows ? g->seg[e] : 0;
     w.a_row = first + mi * TM;
     w.n0 = ni * TN;
@@ -315,7 +313,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     if (warp == 0) {
         int tiles;
         if (args.mode == kFp4Dense)
-            tiles = static_cast<int>((args.m + C::BN - 1) / C::BN) * static_cast<int>((args.n + 127) / 128);
+            tiles = args.mt * args.nt;
         else
             tiles = f4_groups<C::BN, 128>(args, groups, lane);
         if (lane == 0) *tiles_s = tiles;
@@ -587,7 +585,7 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     if (warp == 0) {
         int tiles;
         if (args.mode == kFp4Dense)
-            tiles = static_cast<int>((args.m + 255) / 256) * static_cast<int>((args.n + 255) / 256);
+            tiles = args.mt * args.nt;
         else
             tiles = f4_groups<256, 256>(args, groups, lane);
         if (lane == 0) *tiles_s = tiles;
@@ -637,16 +635,24 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             int stage = 0, it = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int t = worker; ok && t < tiles; t += workers) {
-                const F4Tile w = f4_tile<256, 256>(args, groups, t, args.group_m);
-                if (w.kb0 == w.kb1) continue;
+            int t = worker;
+            auto next_k = [&]() {  // stages of the next tile that has any, found ahead of its start
+                for (; t < tiles; t += workers) {
+                    const F4Tile w = f4_tile<256, 256>(args, groups, t, args.group_m);
+                    if (w.kb0 < w.kb1) return w.kb1 - w.kb0;
+                }
+                return 0;
+            };
+            int nk = next_k();
+            while (ok && nk > 0) {
+                const int now = nk;
                 const int buf = it & 1;
                 ok = mbar_wait(&acce_bar[buf], ((it >> 1) & 1) ^ 1u, abort_flag);
                 if (ok && it > 0) ok = mbar_wait(ovl_bar, (it - 1) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after_sync();
                 const uint32_t d = tmem_base + (buf ? P::kAcc1 : 0);
-                for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                for (int kb = 0; kb < now; ++kb) {
                     ok = mbar_wait(&full_bar[stage], phase, abort_flag);
                     if (!ok) break;
                     tc_fence_after_sync();
@@ -656,11 +662,15 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     for (int j = 0; j < 4; ++j)
                         umma_mxf4_pair(d, smem_desc_sw128(aa + 32 * j, 16, 1024), smem_desc_sw128(ba + 32 * j, 16, 1024),
                                        (j & 1) ? idesc_mxf4(256, 256, 2) : idesc_mxf4(256, 256, 0), sa + 4 * (j >> 1),
-                                       sb + 8 * (j >> 1), (kb > w.kb0 || j > 0) ? 1u : 0u);
+                                       sb + 8 * (j >> 1), (kb > 0 || j > 0) ? 1u : 0u);
                     umma_commit_pair(&empty_bar[stage], 3);
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
+                    }
+                    if (kb == 0) {  // while the first stage's MMAs run
+                        t += workers;
+                        nk = next_k();
                     }
                 }
                 if (!ok) break;
@@ -836,7 +846,9 @@ bool make_map_codes(CUtensorMap *m, const void *codes, int64_t rows, int64_t k, 
 }
 
 template <class C, bool F32>
-int run_small(const F4Args &a, const Fp4Product &p, int cs, int workers, cudaStream_t s) {
+int run_small(F4Args a, const Fp4Product &p, int cs, int workers, cudaStream_t s) {
+    a.mt = static_cast<int>((p.m + C::BN - 1) / C::BN);
+    a.nt = static_cast<int>((p.n + 127) / 128);
     CUtensorMap mA, mB;
     const int64_t a_rows = p.m, b_rows = p.mode == kFp4GroupRows ? p.n * p.experts : p.n;
     if (!make_map_codes(&mA, p.a, a_rows, p.k, C::BN) || !make_map_codes(&mB, p.b, b_rows, p.k, 128)) return MLPBLK_ECUDA;
@@ -897,7 +909,9 @@ bool make_map_c(CUtensorMap *m, void *c, bool f32, int64_t mats, int64_t rows, i
 }
 
 template <int OUT, bool TMA_OUT>
-int run_pair(const F4Args &a, const Fp4Product &p, int workers, cudaStream_t s) {
+int run_pair(F4Args a, const Fp4Product &p, int workers, cudaStream_t s) {
+    a.mt = static_cast<int>((p.m + 255) / 256);
+    a.nt = static_cast<int>((p.n + 255) / 256);
     CUtensorMap mA, mB, mSA, mSB, mC;
     const bool rows_grouped = p.mode == kFp4GroupRows;
     const int64_t a_tiles = (p.m + 127) / 128, b_tiles = (p.n + 127) / 128 * (rows_grouped ? p.experts : 1);
