@@ -57,7 +57,8 @@ __device__ __forceinline__ float relu2(float v) {
     return r * r;
 }
 
-// max(m, |v|), a NaN once there is one.
+// max(|m|, |v|), a NaN once there is one (the bf16 form's signs are of no meaning: one
+// instruction fewer than clearing them first, in kernels bound by the integer pipe).
 __device__ __forceinline__ float max_abs(float m, float v) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
@@ -65,7 +66,15 @@ __device__ __forceinline__ float max_abs(float m, float v) {
 }
 __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t v) {
     uint32_t r;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(v & 0x7FFF7FFFu));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(v));
+    return r;
+}
+
+// Both bf16 values of v times those of m.  Exact for powers of two in m, but for
+// results below bf16's normal range, whose code is 0 either way.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t v, uint32_t m) {
+    uint32_t r;
+    asm("mul.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(m));
     return r;
 }
 
@@ -78,31 +87,27 @@ __device__ __forceinline__ int source_row(const int *row_map, int map_div, int64
     return m < 0 ? -1 : (map_div > 0 ? m / map_div : static_cast<int>(r));
 }
 
-// 8 consecutive values of a row from column c on (0 at and behind cols), as loaded:
-// 4 words of bf16 pairs or 8 floats.  VEC: the row is 16-byte aligned and a multiple
-// of 16 bytes.
+// 8 consecutive values of a row, as loaded: 4 words of bf16 pairs or 8 floats.
 template <bool BF16>
 struct Oct;
 template <>
 struct Oct<true> {
     uint32_t w[4];
-    template <bool VEC>
+    // columns c .. c + 7, 16-byte aligned, all of them below cols or none
     __device__ __forceinline__ void load(const uint16_t *row, int64_t c, int64_t cols) {
-        if (VEC) {
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (c < cols) u = __ldg(reinterpret_cast<const uint4 *>(row + c));
-            w[0] = u.x;
-            w[1] = u.y;
-            w[2] = u.z;
-            w[3] = u.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t lo = c + 2 * i < cols ? __ldg(row + c + 2 * i) : 0u;
-                const uint32_t hi = c + 2 * i + 1 < cols ? __ldg(row + c + 2 * i + 1) : 0u;
-                w[i] = lo | (hi << 16);
-            }
-        }
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (c < cols) u = __ldg(reinterpret_cast<const uint4 *>(row + c));
+        w[0] = u.x;
+        w[1] = u.y;
+        w[2] = u.z;
+        w[3] = u.w;
+    }
+    __device__ __forceinline__ void load_shared(const uint16_t *p) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        w[0] = u.x;
+        w[1] = u.y;
+        w[2] = u.z;
+        w[3] = u.w;
     }
     __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
     __device__ __forceinline__ void floats(float (&v)[8]) const {
@@ -112,30 +117,44 @@ struct Oct<true> {
             v[2 * i + 1] = bf16_hi(w[i]);
         }
     }
+    // the values times inv, a power of two: in bf16, two at a time
+    __device__ __forceinline__ void scaled(float inv, float (&v)[8]) const {
+        const uint32_t m = __float_as_uint(inv) >> 16, m2 = m | (m << 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t u = mul_bf16x2(w[i], m2);
+            v[2 * i] = bf16_lo(u);
+            v[2 * i + 1] = bf16_hi(u);
+        }
+    }
     // bits of max |v| as a float
     __device__ __forceinline__ uint32_t top() const {
-        const uint32_t m = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(w[0] & 0x7FFF7FFFu, w[1]), w[2]), w[3]);
+        const uint32_t m = max_abs_bf16x2(max_abs_bf16x2(w[0], w[1]), max_abs_bf16x2(w[2], w[3])) & 0x7FFF7FFFu;
         return max(m << 16, m & 0xFFFF0000u);
     }
 };
 template <>
 struct Oct<false> {
     float f[8];
-    template <bool VEC>
     __device__ __forceinline__ void load(const float *row, int64_t c, int64_t cols) {
-        if (VEC) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (c + 4 * h < cols) u = __ldg(reinterpret_cast<const float4 *>(row + c + 4 * h));
-                f[4 * h] = u.x;
-                f[4 * h + 1] = u.y;
-                f[4 * h + 2] = u.z;
-                f[4 * h + 3] = u.w;
-            }
-        } else {
+        for (int h = 0; h < 2; ++h) {
+            float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (c + 4 * h < cols) u = __ldg(reinterpret_cast<const float4 *>(row + c + 4 * h));
+            f[4 * h] = u.x;
+            f[4 * h + 1] = u.y;
+            f[4 * h + 2] = u.z;
+            f[4 * h + 3] = u.w;
+        }
+    }
+    __device__ __forceinline__ void load_shared(const float *p) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? __ldg(row + c + i) : 0.0f;
+        for (int h = 0; h < 2; ++h) {
+            const float4 u = *reinterpret_cast<const float4 *>(p + 4 * h);
+            f[4 * h] = u.x;
+            f[4 * h + 1] = u.y;
+            f[4 * h + 2] = u.z;
+            f[4 * h + 3] = u.w;
         }
     }
     __device__ __forceinline__ void zero() {
@@ -145,6 +164,10 @@ struct Oct<false> {
     __device__ __forceinline__ void floats(float (&v)[8]) const {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = f[i];
+    }
+    __device__ __forceinline__ void scaled(float inv, float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = f[i] * inv;
     }
     __device__ __forceinline__ uint32_t top() const { return top8(f); }
     static __device__ __forceinline__ uint32_t top8(const float (&v)[8]) {
@@ -161,11 +184,12 @@ struct Oct<false> {
 // scales of 4 blocks are 16 consecutive bytes of a tile (one store), with the next
 // row's beside them.  The four rows' loads are in flight together.
 template <bool BF16, bool VEC, bool RELU2, bool MAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, BF16 && VEC && !RELU2 ? 5 : 3)
 quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
                      int64_t cols, int row_tiles, int chunks, uint8_t *__restrict__ codes,
                      uint8_t *__restrict__ scales) {
     using T = typename std::conditional<BF16, uint16_t, float>::type;
+    __shared__ __align__(16) T turn[VEC ? 1 : kWarps][4][VEC ? 8 : 256];
     griddep_enter();
     const int lane = threadIdx.x & 31;
     const int64_t ld = fp4_row_bytes(cols);
@@ -187,18 +211,31 @@ quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map
     for (int chunk = blockIdx.y; chunk < chunks; chunk += gridDim.y) {
         const int64_t c = static_cast<int64_t>(chunk) * 256 + lane * 8;
         Oct<BF16> o[4];
+        if (VEC) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (live[j]) o[j].template load<VEC>(src[j], c, cols);
-            else o[j].zero();
+            for (int j = 0; j < 4; ++j) {
+                if (live[j]) o[j].load(src[j], c, cols);
+                else o[j].zero();
+            }
+        } else {
+            T *mine = &turn[VEC ? 0 : threadIdx.x >> 5][0][0];
+            const int64_t c0 = static_cast<int64_t>(chunk) * 256 + lane;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mine[j * 256 + 32 * i + lane] = live[j] && c0 + 32 * i < cols ? __ldg(src[j] + c0 + 32 * i) : T(0);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j].load_shared(mine + j * 256 + lane * 8);
+            __syncwarp();
         }
         uint32_t word[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float v[8];
-            o[j].floats(v);
             uint32_t m;
             if (RELU2) {
+                o[j].floats(v);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = relu2(v[i]);
                 m = Oct<false>::top8(v);
@@ -209,8 +246,12 @@ quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
             const uint32_t sb = scale_byte(m);
             const float inv = scale_inverse(sb);
+            if (RELU2) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= inv;
+                for (int i = 0; i < 8; ++i) v[i] *= inv;
+            } else {
+                o[j].scaled(inv, v);
+            }
             const uint32_t q = sb == 255u ? 0u : e2m1x8(v);
             if (r0 + 32 * j < rows && c < 2 * ld) *reinterpret_cast<uint32_t *>(out + 32 * j * ld + c / 2) = q;
             // the four blocks' bytes of this half warp
@@ -264,23 +305,50 @@ struct Pair<false> {
     __device__ __forceinline__ float hi() const { return f.y; }
 };
 
-// The 32 values of one block, every one from `get(i)`: their codes and scale byte.
-template <bool RELU2, class F>
-__device__ __forceinline__ uint4 quantize_block(F get, uint32_t &sb) {
-    float m = 0.0f;
+// The two columns' blocks of 32 values: their codes and scale bytes.
+template <bool BF16, bool RELU2>
+__device__ __forceinline__ void quantize_pairs(const Pair<BF16> (&p)[32], uint4 &qa, uint4 &qb, uint32_t &sa, uint32_t &sb) {
+    uint32_t ta, tb;  // bits of the columns' max |v|
+    if constexpr (BF16 && !RELU2) {
+        uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) m = max_abs(m, RELU2 ? relu2(get(i)) : get(i));
-    sb = scale_byte(__float_as_uint(m));
-    const float inv = scale_inverse(sb);
-    uint32_t q[4];
+        for (int i = 0; i < 32; ++i) m = max_abs_bf16x2(m, p[i].w);
+        m &= 0x7FFF7FFFu;
+        ta = m << 16;
+        tb = m & 0xFFFF0000u;
+    } else {
+        float ma = 0.0f, mb = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            ma = max_abs(ma, RELU2 ? relu2(p[i].lo()) : p[i].lo());
+            mb = max_abs(mb, RELU2 ? relu2(p[i].hi()) : p[i].hi());
+        }
+        ta = __float_as_uint(ma);
+        tb = __float_as_uint(mb);
+    }
+    sa = scale_byte(ta);
+    sb = scale_byte(tb);
+    const float ia = scale_inverse(sa), ib = scale_inverse(sb);
+    uint32_t wa[4], wb[4];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-        float v[8];
+        float va[8], vb[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = (RELU2 ? relu2(get(8 * g + i)) : get(8 * g + i)) * inv;
-        q[g] = sb == 255u ? 0u : e2m1x8(v);
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (BF16 && !RELU2) {
+                const uint32_t u = mul_bf16x2(p[8 * g + i].w, (__float_as_uint(ia) >> 16) | (__float_as_uint(ib) & 0xFFFF0000u));
+                va[i] = bf16_lo(u);
+                vb[i] = bf16_hi(u);
+            } else {
+                va[i] = (RELU2 ? relu2(p[8 * g + i].lo()) : p[8 * g + i].lo()) * ia;
+                vb[i] = (RELU2 ? relu2(p[8 * g + i].hi()) : p[8 * g + i].hi()) * ib;
+            }
+        }
+        wa[g] = sa == 255u ? 0u : e2m1x8(va);
+        wb[g] = sb == 255u ? 0u : e2m1x8(vb);
     }
-    return make_uint4(q[0], q[1], q[2], q[3]);
+    qa = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+    qb = make_uint4(wb[0], wb[1], wb[2], wb[3]);
 }
 
 // Blocks along the source's columns: Q = x^T, Q's rows are x's columns.  A CTA
@@ -319,6 +387,10 @@ quantize_cols_kernel(const void *__restrict__ x, const int *__restrict__ row_map
                 const int src = __shfl_sync(0xffffffffu, mine, i);
                 p[i].template load<VEC>(base + (src < 0 ? 0 : src) * rows, src < 0 ? rows : col, rows);
             }
+        } else if (c0 + 32 <= cols) {
+            const T *row = base + c0 * rows;
+#pragma unroll
+            for (int i = 0; i < 32; ++i, row += rows) p[i].template load<VEC>(row, col, rows);
         } else {
             const T *row = base + c0 * rows;
 #pragma unroll
@@ -328,8 +400,10 @@ quantize_cols_kernel(const void *__restrict__ x, const int *__restrict__ row_map
             }
         }
         uint32_t sa, sb;
-        *reinterpret_cast<uint4 *>(&sc[2 * lane][wid * 16]) = quantize_block<RELU2>([&](int i) { return p[i].lo(); }, sa);
-        *reinterpret_cast<uint4 *>(&sc[2 * lane + 1][wid * 16]) = quantize_block<RELU2>([&](int i) { return p[i].hi(); }, sb);
+        uint4 qa, qb;
+        quantize_pairs<BF16, RELU2>(p, qa, qb, sa, sb);
+        *reinterpret_cast<uint4 *>(&sc[2 * lane][wid * 16]) = qa;
+        *reinterpret_cast<uint4 *>(&sc[2 * lane + 1][wid * 16]) = qb;
         ss[2 * lane][wid] = static_cast<uint8_t>(sa);
         ss[2 * lane + 1][wid] = static_cast<uint8_t>(sb);
         __syncthreads();
@@ -372,6 +446,23 @@ __device__ __forceinline__ void decode8(uint32_t u, float scale, float (&v)[8]) 
         v[2 * i] = lo * scale;
         v[2 * i + 1] = hi * scale;
     }
+}
+
+// The value of the code in the lowest four bits.
+__device__ __forceinline__ float decode1(uint32_t u) {
+    float f;
+    asm("{\n"
+        "  .reg .b8 a, b, c, d;\n"
+        "  .reg .b32 h;\n"
+        "  .reg .f16 l, m;\n"
+        "  mov.b32 {a, b, c, d}, %1;\n"
+        "  cvt.rn.f16x2.e2m1x2 h, a;\n"
+        "  mov.b32 {l, m}, h;\n"
+        "  cvt.f32.f16 %0, l;\n"
+        "}\n"
+        : "=f"(f)
+        : "r"(u));
+    return f;
 }
 
 __device__ __forceinline__ float scale_value(uint32_t byte) {
@@ -417,22 +508,31 @@ dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__
 #pragma unroll
         for (int j = 0; j < kDeqChunks; ++j) {
             const int64_t c = static_cast<int64_t>(g + j) * 256 + lane * 8;
+            if (!VEC) {
+                // rows of any length: neighbouring lanes store neighbouring columns, whose
+                // codes and scales other lanes hold
+                const float sv = scale_value(sb[j]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int64_t ci = static_cast<int64_t>(g + j) * 256 + 32 * i + lane;
+                    const uint32_t word = __shfl_sync(0xffffffffu, u[j], 4 * i + (lane >> 3));
+                    const float f = decode1(word >> (4 * (lane & 7))) * __shfl_sync(0xffffffffu, sv, 4 * i);
+                    if (ci < cols) {
+                        if (BF16) reinterpret_cast<uint16_t *>(out)[ci] = static_cast<uint16_t>(pack2(f, 0.0f) & 0xFFFFu);
+                        else reinterpret_cast<float *>(out)[ci] = f;
+                    }
+                }
+                continue;
+            }
             if (c >= cols) continue;
             float v[8];
             decode8(u[j], scale_value(sb[j]), v);
-            if (VEC && BF16) {
+            if (BF16) {
                 *reinterpret_cast<uint4 *>(out + c) =
                     make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-            } else if (VEC) {
+            } else {
                 *reinterpret_cast<float4 *>(out + c) = make_float4(v[0], v[1], v[2], v[3]);
                 if (c + 4 < cols) *reinterpret_cast<float4 *>(out + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (c + i < cols) {
-                        if (BF16) reinterpret_cast<uint16_t *>(out)[c + i] = static_cast<uint16_t>(pack2(v[i], 0.0f) & 0xFFFFu);
-                        else reinterpret_cast<float *>(out)[c + i] = v[i];
-                    }
             }
         }
     }

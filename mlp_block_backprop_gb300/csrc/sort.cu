@@ -148,7 +148,8 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
 // at a time, so a row of 4096 bf16 values is four 16-byte accesses for each of 128
 // threads.
 constexpr int kMoveThreads = 256;
-constexpr int kPer = 4;
+constexpr int kPer = 4;      // permute, unpermute
+constexpr int kPerBwd = 2;   // unpermute's gradient (16384 x 4096, top-2: 105 us; 114 with 4)
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
@@ -368,10 +369,10 @@ unpermute_bwd_kernel(const U *__restrict__ dy, const U *__restrict__ rows, const
             r[j] = on ? pos[t * k + j0 + j] : -1;
             w[j] = on && weights ? weights[t * k + j0 + j] : 1.0f;
         }
-        for (int64_t c0 = threadIdx.x; in && c0 < units; c0 += kPer * blockDim.x) {
-            U g[kPer], o[kSlots][kPer];
+        for (int64_t c0 = threadIdx.x; in && c0 < units; c0 += kPerBwd * blockDim.x) {
+            U g[kPerBwd], o[kSlots][kPerBwd];
 #pragma unroll
-            for (int u = 0; u < kPer; ++u) {
+            for (int u = 0; u < kPerBwd; ++u) {
                 const int64_t c = c0 + u * blockDim.x;
                 g[u] = c < units ? __ldg(dy + t * units + c) : zero_unit<U>();
 #pragma unroll
@@ -379,7 +380,7 @@ unpermute_bwd_kernel(const U *__restrict__ dy, const U *__restrict__ rows, const
                     o[j][u] = d_weights && c < units && r[j] >= 0 ? __ldg(rows + r[j] * units + c) : zero_unit<U>();
             }
 #pragma unroll
-            for (int u = 0; u < kPer; ++u) {
+            for (int u = 0; u < kPerBwd; ++u) {
                 const int64_t c = c0 + u * blockDim.x;
                 if (c >= units) continue;
                 float a[V::N];
@@ -423,13 +424,13 @@ struct MoveShape {
     int64_t token_blocks, pad_blocks;
 };
 
-MoveShape move_shape(int64_t T, int64_t width, int dtype, int experts, int pad) {
+MoveShape move_shape(int64_t T, int64_t width, int dtype, int experts, int pad, int per) {
     MoveShape m;
     const int64_t bytes = width * (dtype == MLPBLK_BF16 ? 2 : 4);
     m.unit = bytes % 16 == 0 ? 16 : (bytes % 4 == 0 ? 4 : 2);
     m.units = bytes / m.unit;
     unsigned tx = 32;
-    while (tx < static_cast<unsigned>(kMoveThreads) && tx * kPer < m.units) tx *= 2;
+    while (tx < static_cast<unsigned>(kMoveThreads) && tx * per < m.units) tx *= 2;
     m.block = dim3(tx, kMoveThreads / tx, 1);
     m.token_blocks = (T + m.block.y - 1) / m.block.y;
     m.pad_blocks = pad > 1 ? (static_cast<int64_t>(experts) * pad + m.block.y - 1) / m.block.y : 0;
@@ -461,7 +462,7 @@ int launch_sort(const int *idx, int64_t n, int experts, int pad, int64_t R, int 
 
 int launch_permute(const void *x, const int *pos, const int *count, const int *seg, int64_t T, int64_t width,
                    int dtype, int k, int experts, int pad, void *rows, cudaStream_t s) {
-    const MoveShape m = move_shape(T, width, dtype, experts, pad);
+    const MoveShape m = move_shape(T, width, dtype, experts, pad, kPer);
     const dim3 grid(static_cast<unsigned>(m.token_blocks + m.pad_blocks));
 #define MLPBLK_PERMUTE(U)                                                                                      \
     return launch_pdl(permute_kernel<U>, grid, m.block, 0, s, static_cast<const U *>(x), pos, count, seg, T, k, \
@@ -474,7 +475,7 @@ int launch_permute(const void *x, const int *pos, const int *count, const int *s
 
 int launch_unpermute(const void *rows, const int *pos, const float *weights, const void *residual, int64_t T,
                      int64_t width, int dtype, int k, void *y, cudaStream_t s) {
-    const MoveShape m = move_shape(T, width, dtype, 1, 1);
+    const MoveShape m = move_shape(T, width, dtype, 1, 1, kPer);
     const dim3 grid(static_cast<unsigned>(m.token_blocks));
 #define MLPBLK_UNPERMUTE(U, B)                                                                              \
     return launch_pdl(unpermute_kernel<U, B>, grid, m.block, 0, s, static_cast<const U *>(rows), pos, weights, \
@@ -492,7 +493,7 @@ int launch_unpermute(const void *rows, const int *pos, const float *weights, con
 int launch_unpermute_bwd(const void *dy, const void *rows, const int *pos, const int *count, const int *seg,
                          const float *weights, int64_t T, int64_t width, int dtype, int k, int experts, int pad,
                          void *d_rows, float *d_weights, cudaStream_t s) {
-    const MoveShape m = move_shape(T, width, dtype, experts, pad);
+    const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerBwd);
     const dim3 grid(static_cast<unsigned>(m.token_blocks + m.pad_blocks));
 #define MLPBLK_UNPERMUTE_BWD(U, B)                                                                               \
     return launch_pdl(unpermute_bwd_kernel<U, B>, grid, m.block, 0, s, static_cast<const U *>(dy),                 \
