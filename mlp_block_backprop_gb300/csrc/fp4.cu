@@ -184,7 +184,7 @@ struct Oct<false> {
 // scales of 4 blocks are 16 consecutive bytes of a tile (one store), with the next
 // row's beside them.  The four rows' loads are in flight together.
 template <bool BF16, bool VEC, bool RELU2, bool MAP>
-__global__ void __launch_bounds__(kThreads, BF16 && VEC && !RELU2 ? 5 : 3)
+__global__ void __launch_bounds__(kThreads, BF16 && VEC ? (RELU2 ? 4 : 5) : 3)
 quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
                      int64_t cols, int row_tiles, int chunks, uint8_t *__restrict__ codes,
                      uint8_t *__restrict__ scales) {

@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kF4MaxExperts = 256;
 constexpr int kF4KB = 256;              // K values of a stage
+constexpr int kF4PrefetchStages = 32;   // stages of B that f4_small asks into L2 ahead (544 KB a CTA)
 
 struct F4Args {
     int mode;                           // Fp4Mode
@@ -80,6 +81,13 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t s_desc
 __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
     return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
            (static_cast<uint64_t>(1) << 46);
+}
+
+// Asks L2 to fetch a box of a 2-D tensor map.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1)
+                 : "memory");
 }
 
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
@@ -309,7 +317,20 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     if (cs > 1) cluster_sync();  // the peers' barriers exist before anyone arrives on them
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
-    griddep_enter();
+    griddep_launch_dependents();
+    if (args.mode == kFp4Dense && warp == 0 && lane == 0 && worker < args.mt * args.nt) {
+        // B is asked into L2 while the previous kernel (A's quantisation, as a rule) still
+        // runs: no data reaches this kernel before griddep_wait.  At one token the
+        // weights' way from HBM is most of the time.
+        const F4Tile w = f4_tile<C::BN, 128>(args, groups, worker, args.group_m);
+        const int k0 = w.kb1 * rank / cs, k1 = w.kb1 * (rank + 1) / cs;
+        for (int kb = k0; kb < k1 && kb < k0 + kF4PrefetchStages; ++kb) {
+            tma_prefetch_2d(&tmB, kb * 128, w.b_row);
+            bulk_prefetch_l2(w.sb + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes);
+        }
+    }
+    __syncwarp();
+    griddep_wait();
     if (warp == 0) {
         int tiles;
         if (args.mode == kFp4Dense)
@@ -439,12 +460,27 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     mbar_arrive_cluster(mapa_shared(smem_u32(part_full), threadIdx.x - 64));
                 ok = mbar_wait_cluster(part_full, it & 1, abort_flag) && ok;
                 ok = __all_sync(0xffffffffu, ok);
-                if (ok && i < w.n_valid) {
-                    for (int c = rank; c < w.m_valid; c += cs) {
-                        float s = 0.0f;
-                        for (int r = 0; r < cs; ++r)
-                            s += ld_cluster_f32(mapa_shared(smem_u32(dump + c * 128 + i), r));
-                        store_c<F32>(args.c, (w.c_row + c) * args.n + w.n0 + i, s, args.accumulate);
+                if (ok) {
+                    // columns rank, rank + cs, ...: eight at a time, their remote loads in flight together
+                    constexpr int kCols = 8;
+                    for (int c0 = rank; c0 < w.m_valid; c0 += kCols * cs) {
+                        float sum[kCols];
+#pragma unroll
+                        for (int u = 0; u < kCols; ++u) sum[u] = 0.0f;
+                        for (int r = 0; r < cs; ++r) {
+                            const uint32_t from = mapa_shared(smem_u32(dump + i), r);
+                            float part[kCols];
+#pragma unroll
+                            for (int u = 0; u < kCols; ++u)  // past the tile: column 0 instead, not stored
+                                part[u] = ld_cluster_f32(from + (c0 + u * cs < w.m_valid ? c0 + u * cs : 0) * 512);
+#pragma unroll
+                            for (int u = 0; u < kCols; ++u) sum[u] += part[u];
+                        }
+                        const int64_t at = w.c_row * args.n + w.n0 + i;
+#pragma unroll
+                        for (int u = 0; u < kCols; ++u)
+                            if (i < w.n_valid && c0 + u * cs < w.m_valid)
+                                store_c<F32>(args.c, at + (c0 + u * cs) * args.n, sum[u], args.accumulate);
                     }
                 }
                 named_barrier_sync(1, 128);
@@ -991,7 +1027,7 @@ int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s) {
     const int64_t bn = few ? 32 : 128;
     const int64_t tiles = (rows + bn - 1) / bn * ((p.n + 127) / 128) * groups;
     int cs = 1;
-    while (cs < 8 && tiles * cs * 2 <= num_sms && a.kblocks >= 4 * cs) cs *= 2;
+    while (cs < 8 && tiles * cs * 2 <= num_sms && a.kblocks >= 8 * cs) cs *= 2;
     int64_t workers = num_sms / cs;
     if (workers < 1) workers = 1;
     if (p.mode != kFp4GroupRows && tiles < workers) workers = tiles;

@@ -52,10 +52,14 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int C = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
     const unsigned lt = (1u << lane) - 1u;
-    for (int e = tid; e < kSortWarps * kSortExperts; e += kSortThreads) (&wcnt[0][0])[e] = 0;
-    __syncthreads();
+    // warps of this CTA that have entries
+    const int64_t left = n - static_cast<int64_t>(c) * kSortWarps * per_warp;
+    const int nw = left <= 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(kSortWarps), (left + per_warp - 1) / per_warp));
     const int64_t w0 = (static_cast<int64_t>(c) * kSortWarps + wid) * per_warp;
     const int64_t w1 = min(n, w0 + per_warp);
+    if (wid < nw)
+        for (int e = lane; e < kSortExperts; e += 32) wcnt[wid][e] = 0;
+    __syncwarp();
     for (int64_t g = w0; g < w1; g += 32) {
         const int64_t i = g + lane;
         int e = i < w1 ? idx[i] : -1;
@@ -67,7 +71,7 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
     __syncthreads();
     if (tid < kSortExperts) {
         int run = 0;
-        for (int w = 0; w < kSortWarps; ++w) {
+        for (int w = 0; w < nw; ++w) {
             const int v = wcnt[w][tid];
             wcnt[w][tid] = run;
             run += v;
@@ -110,7 +114,7 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
         segs[tid + 1] = off + incl;
         if (tid == 0) segs[0] = 0;
         // the first row of each warp's entries
-        for (int w = 0; w < kSortWarps; ++w) wcnt[w][tid] += off + incl - padded + before;
+        for (int w = 0; w < nw; ++w) wcnt[w][tid] += off + incl - padded + before;
     }
     __syncthreads();
     if (c == 0) {
