@@ -5,10 +5,11 @@
 // A stage row is 128 bytes, 256 values of K, in the 128-byte swizzle; one MMA takes
 // 32 bytes (64 values) of it.  The scales lie in global memory in the order in which
 // tcgen05.cp wants them (include/mlpblk.h: 512-byte tiles of 128 rows x 128 values
-// of K), so a stage's scales are one untiled copy of 1 KB per 128 rows, and one
-// tcgen05.cp (32 lanes x 16 bytes, repeated over the four lane quarters) a tile puts
-// them into four TMEM columns.  The same thread issues the copies and the MMAs,
-// which the tensor core takes in order.
+// of K).  In TMEM a tile is four columns, lane l of column j holding the scales of row
+// 32j + l, the same in all four lane quarters: four warps read a stage's tiles from
+// shared memory, 16 bytes a lane, and store them with tcgen05.st, one quarter each.
+// tcgen05.cp would do it without them, but it runs in the MMAs' pipe (8192 x 16384 x
+// 4096: 226 us with it, 172 without; one token x 16384 x 4096: 10.5 us and 8.9).
 //
 // f4_small: one CTA computes a 128 x BN tile with B's rows (C's columns) on the 128
 //   lanes and A's rows (tokens) on the columns, so that few tokens cost few
@@ -42,7 +43,6 @@ struct F4Args {
     int group_m;                        // raster: this many tiles of A sweep B together
     const int *count, *seg;
     void *c;
-    int accumulate;
 };
 
 // ------------------------------------------------------------------------- PTX
@@ -70,18 +70,13 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
-// One scale tile (32 rows of 16 bytes in shared memory) into four TMEM columns,
-// repeated over the four lane quarters.
-__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t s_desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+// Four columns of scales of this warp's lane quarter from registers.
+__device__ __forceinline__ void tmem_store_4cols(uint32_t taddr, uint4 v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
 }
-
-// Shared-memory descriptor of a scale tile: no swizzle, 8-row groups of 16-byte rows
-// 128 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
-           (static_cast<uint64_t>(1) << 46);
-}
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Asks L2 to fetch a box of a 2-D tensor map.
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int32_t c0, int32_t c1) {
@@ -231,16 +226,6 @@ __device__ __forceinline__ F4Tile f4_tile(const F4Args &a, const F4Groups *g, in
     return w;
 }
 
-template <bool F32>
-__device__ __forceinline__ void store_c(void *c, int64_t at, float v, int accumulate) {
-    if (F32) {
-        float *p = static_cast<float *>(c) + at;
-        *p = accumulate ? *p + v : v;
-    } else {
-        static_cast<uint16_t *>(c)[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
-    }
-}
-
 // ------------------------------------------------------------------- f4_small
 
 // BN columns: 32 for up to 32 tokens, 128 beyond.  A's scale tile holds 128 rows, so
@@ -248,7 +233,9 @@ __device__ __forceinline__ void store_c(void *c, int64_t at, float v, int accumu
 template <int BN_>
 struct F4Small {
     static constexpr int BN = BN_;
-    static constexpr int kThreads = 192;           // TMA, MMA, four epilogue warps
+    static constexpr int kEpiWarps = BN == 128 ? 8 : 4;  // two a lane quarter: 64 columns each
+    static constexpr int kEpiCols = BN == 128 ? 64 : 32;
+    static constexpr int kThreads = 64 + 32 * kEpiWarps + 128;  // TMA, MMA, epilogue, four scale warps
     static constexpr int kLBytes = 128 * 128;      // B's rows, on the lanes
     static constexpr int kRBytes = BN * 128;       // A's rows, on the columns
     static constexpr int kSfBytes = 1024;          // scales of 128 rows and a stage of K
@@ -257,15 +244,55 @@ struct F4Small {
     static constexpr int kCtrlBytes = 4096;
     static constexpr int kStages = (kSmemLimit - 1024 - kCtrlBytes - kDumpBytes) / kStageBytes;
     static constexpr int kSmemBytes = 1024 + kCtrlBytes + kDumpBytes + kStages * kStageBytes;
-    // TMEM: two accumulators, then two sets of scales (8 columns each operand)
+    // TMEM: two accumulators, then each stage's scales (8 columns each operand)
     static constexpr int kSfCol = 2 * BN;
     static constexpr int kSfSet = 16;
-    static constexpr uint32_t kTmemCols = kSfCol + 2 * kSfSet <= 128 ? 128u : 512u;
-    static_assert(kStages >= 3, "pipeline");
+    static constexpr uint32_t kTmemCols = kSfCol + kStages * kSfSet <= 256 ? 256u : 512u;
+    static_assert(kStages >= 3 && kSfCol + kStages * kSfSet <= 512, "pipeline");
     static_assert(sizeof(F4Groups) + 512 <= kCtrlBytes, "control block");
 };
 
-template <class C, bool F32>
+// 32 columns of a tile out of a lane's registers: column j goes to C's row row0 + j,
+// lane i to its column col0 + i; `rows` of the columns and the lanes with `on` are stored.
+// OUT: 0 bf16, 1 float32, 2 float32 +=.  bf16 with an even n: neighbouring lanes swap
+// every other value, so that a store is a pair of columns.
+template <int OUT>
+__device__ __forceinline__ void store_columns(void *c, int64_t row0, int64_t n, int64_t col, const float (&v)[32], int rows,
+                                              bool on) {
+    const int lane = threadIdx.x & 31;
+    if (OUT == 0 && (n & 1) == 0) {
+        const int odd = lane & 1;
+        uint16_t *p = static_cast<uint16_t *>(c) + (row0 + odd) * n + (col - odd);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+            const uint32_t w = odd ? pack_bf16x2(got, v[j + 1]) : pack_bf16x2(v[j], got);
+            if (on && j + odd < rows) *reinterpret_cast<uint32_t *>(p) = w;
+            p += 2 * n;
+        }
+    } else if (OUT == 0) {
+        uint16_t *p = static_cast<uint16_t *>(c) + row0 * n + col;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (on && j < rows) *p = static_cast<uint16_t>(pack_bf16x2(v[j], 0.0f) & 0xFFFFu);
+            p += n;
+        }
+    } else {
+        float *p = static_cast<float *>(c) + row0 * n + col;
+        float old[32];
+        if (OUT == 2) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) old[j] = on && j < rows ? p[j * n] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (on && j < rows) *p = OUT == 2 ? old[j] + v[j] : v[j];
+            p += n;
+        }
+    }
+}
+
+template <class C, int OUT>
 __global__ void __launch_bounds__(C::kThreads, 1)
 f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const F4Args args) {
     extern __shared__ uint8_t smem_raw[];
@@ -278,7 +305,8 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     uint8_t *ctrl = reinterpret_cast<uint8_t *>(dump) + C::kDumpBytes;
     uint64_t *full_bar = reinterpret_cast<uint64_t *>(ctrl);
     uint64_t *empty_bar = full_bar + S;
-    uint64_t *accf_bar = empty_bar + S;
+    uint64_t *sf_bar = empty_bar + S;     // the stage's scales are in shared memory
+    uint64_t *accf_bar = sf_bar + S;
     uint64_t *acce_bar = accf_bar + 2;
     uint64_t *part_full = acce_bar + 2;   // every CTA of the cluster has its part in `dump`
     uint64_t *part_empty = part_full + 1; // every CTA has read this CTA's part
@@ -286,6 +314,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 388);
     int *tiles_s = reinterpret_cast<int *>(ctrl + 392);
     F4Groups *groups = reinterpret_cast<F4Groups *>(ctrl + 512);
+    static_assert((3 * S + 6) * 8 <= 384, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cs = static_cast<int>(cluster_nctarank());
@@ -294,12 +323,13 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full_bar[s], 1);
+            mbar_init(&full_bar[s], 1 + 4);  // the operands, and the scale warps
             mbar_init(&empty_bar[s], 1);
+            mbar_init(&sf_bar[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accf_bar[b], 1);
-            mbar_init(&acce_bar[b], 4);
+            mbar_init(&acce_bar[b], C::kEpiWarps);
         }
         mbar_init(part_full, cs);
         mbar_init(part_empty, cs);
@@ -318,7 +348,8 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
     griddep_launch_dependents();
-    if (args.mode == kFp4Dense && warp == 0 && lane == 0 && worker < args.mt * args.nt) {
+    int tiles = args.mt * args.nt;  // dense; grouped: from the segments, below
+    if (args.mode == kFp4Dense && warp == 0 && lane == 0 && worker < tiles) {
         // B is asked into L2 while the previous kernel (A's quantisation, as a rule) still
         // runs: no data reaches this kernel before griddep_wait.  At one token the
         // weights' way from HBM is most of the time.
@@ -331,16 +362,14 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     }
     __syncwarp();
     griddep_wait();
-    if (warp == 0) {
-        int tiles;
-        if (args.mode == kFp4Dense)
-            tiles = args.mt * args.nt;
-        else
-            tiles = f4_groups<C::BN, 128>(args, groups, lane);
-        if (lane == 0) *tiles_s = tiles;
+    if (args.mode != kFp4Dense) {
+        if (warp == 0) {
+            const int total = f4_groups<C::BN, 128>(args, groups, lane);
+            if (lane == 0) *tiles_s = total;
+        }
+        __syncthreads();
+        tiles = *tiles_s;
     }
-    __syncthreads();
-    const int tiles = *tiles_s;
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
@@ -356,12 +385,13 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     ok = mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag);
                     if (!ok) break;
                     uint64_t *bar = &full_bar[stage];
-                    mbar_arrive_expect_tx(bar, C::kStageBytes);
-                    tma_load_2d(&tmB, bar, lanes_s + stage * C::kLBytes, kb * 128, w.b_row);
-                    tma_load_2d(&tmA, bar, cols_s + stage * C::kRBytes, kb * 128, w.a_row);
                     uint8_t *sf = sf_s + stage * 2 * C::kSfBytes;
-                    bulk_copy_g2s(sf, w.sb + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes, bar);
-                    bulk_copy_g2s(sf + C::kSfBytes, w.sa + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes, bar);
+                    mbar_arrive_expect_tx(bar, C::kLBytes + C::kRBytes);
+                    tma_load_2d(&tmB, bar, lanes_s + stage * C::kLBytes, kb * 128, w.b_row);
+                    mbar_arrive_expect_tx(&sf_bar[stage], 2 * C::kSfBytes);
+                    bulk_copy_g2s(sf, w.sb + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes, &sf_bar[stage]);
+                    bulk_copy_g2s(sf + C::kSfBytes, w.sa + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes, &sf_bar[stage]);
+                    tma_load_2d(&tmA, bar, cols_s + stage * C::kRBytes, kb * 128, w.a_row);
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
@@ -373,7 +403,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     } else if (warp == 1) {
         // ------------------------------------------------------- MMA issuer
         if (lane == 0) {
-            int stage = 0, it = 0, set = 0;
+            int stage = 0, it = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int t = worker; ok && t < tiles; t += workers, ++it) {
@@ -391,20 +421,13 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     tc_fence_after_sync();
                     const uint32_t la = smem_u32(lanes_s + stage * C::kLBytes);
                     const uint32_t ca = smem_u32(cols_s + stage * C::kRBytes);
-                    const uint32_t sf = smem_u32(sf_s + stage * 2 * C::kSfBytes);
-                    const uint32_t sl = tmem_base + C::kSfCol + set * C::kSfSet, sc = sl + 8;
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        tmem_copy_scales(sl + 4 * g, smem_desc_scales(sf + g * kFp4TileBytes));
-                        tmem_copy_scales(sc + 4 * g, smem_desc_scales(sf + C::kSfBytes + g * kFp4TileBytes));
-                    }
+                    const uint32_t sl = tmem_base + C::kSfCol + stage * C::kSfSet, sc = sl + 8;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         umma_mxf4(d, smem_desc_sw128(la + 32 * j, 16, 1024), smem_desc_sw128(ca + 32 * j, 16, 1024),
                                   (j & 1) ? idesc_mxf4(128, C::BN, 2) : idesc_mxf4(128, C::BN, 0), sl + 4 * (j >> 1),
                                   sc + 4 * (j >> 1), (kb > k0 || j > 0) ? 1u : 0u);
                     umma_commit(&empty_bar[stage]);
-                    set ^= 1;
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
@@ -415,12 +438,47 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             }
         }
         __syncwarp();
+    } else if (warp >= 2 + C::kEpiWarps) {
+        // ------------------------------------------------------ scale warps
+        // Shared memory to TMEM, as in f4_pair.
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = worker; ok && t < tiles; t += workers) {
+            const F4Tile w = f4_tile<C::BN, 128>(args, groups, t, args.group_m);
+            const int nk = w.kb1 - w.kb0;
+            const int k0 = w.kb0 + nk * rank / cs, k1 = w.kb0 + nk * (rank + 1) / cs;
+            for (int kb = k0; kb < k1; ++kb) {
+                ok = mbar_wait(&sf_bar[stage], phase, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint32_t sf = smem_u32(sf_s + stage * 2 * C::kSfBytes) + lane * 16;
+                const uint32_t to = tmem_base + lanes + C::kSfCol + stage * C::kSfSet;
+                uint4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = ld_shared_v4(sf + i * kFp4TileBytes);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_store_4cols(to + 4 * i, v[i]);
+                tmem_wait_store();
+                tc_fence_before_sync();
+                __syncwarp();
+                // no memory access to release: wait::st has completed the TMEM writes
+                if (lane == 0) mbar_arrive_relaxed(&full_bar[stage]);
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
     } else {
         // --------------------------------------------------------- epilogue
         // A warp that gave up on a wait keeps walking (its waits then return at
         // once), so that the barriers of the cluster's sum stay in step.
-        const int q = warp & 3;
+        const int q = warp & 3, half = (warp - 2) >> 2;
         const int i = 32 * q + lane;  // lane of the tile: C's column n0 + i
+        constexpr int kEpiThreads = 32 * C::kEpiWarps;
         int it = 0;
         for (int t = worker; t < tiles; t += workers, ++it) {
             const F4Tile w = f4_tile<C::BN, 128>(args, groups, t, args.group_m);
@@ -433,7 +491,8 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * C::BN;
             if (cs > 1) ok = mbar_wait_cluster(part_empty, (it & 1) ^ 1u, abort_flag) && ok;
             ok = __all_sync(0xffffffffu, ok);
-            for (int c0 = 0; c0 < w.m_valid; c0 += 32) {
+            const int c_end = min(w.m_valid, (half + 1) * C::kEpiCols);
+            for (int c0 = half * C::kEpiCols; c0 < c_end; c0 += 32) {
                 float v[32];
                 if (some && ok) {
                     tmem_load_32cols(t_row + c0, v);
@@ -444,18 +503,15 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 if (cs > 1) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) dump[(c0 + j) * 128 + i] = v[j];
-                } else if (i < w.n_valid && ok) {
-                    const int64_t at = w.c_row * args.n + w.n0 + i;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (c0 + j < w.m_valid) store_c<F32>(args.c, at + (c0 + j) * args.n, v[j], args.accumulate);
+                } else {
+                    store_columns<OUT>(args.c, w.c_row + c0, args.n, w.n0 + i, v, w.m_valid - c0, ok && i < w.n_valid);
                 }
             }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive_relaxed(&acce_bar[buf]);
             if (cs > 1) {
-                named_barrier_sync(1, 128);
+                named_barrier_sync(1, kEpiThreads);
                 if (threadIdx.x >= 64 && threadIdx.x < 64 + cs)
                     mbar_arrive_cluster(mapa_shared(smem_u32(part_full), threadIdx.x - 64));
                 ok = mbar_wait_cluster(part_full, it & 1, abort_flag) && ok;
@@ -463,8 +519,10 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 if (ok) {
                     // columns rank, rank + cs, ...: eight at a time, their remote loads in flight together
                     constexpr int kCols = 8;
-                    for (int c0 = rank; c0 < w.m_valid; c0 += kCols * cs) {
+                    constexpr int kHalves = C::kEpiWarps / 4;
+                    for (int c0 = rank + half * kCols * cs; c0 < w.m_valid; c0 += kHalves * kCols * cs) {
                         float sum[kCols];
+                        const int64_t at = (w.c_row + c0) * args.n + w.n0 + i;
 #pragma unroll
                         for (int u = 0; u < kCols; ++u) sum[u] = 0.0f;
                         for (int r = 0; r < cs; ++r) {
@@ -476,14 +534,20 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
                             for (int u = 0; u < kCols; ++u) sum[u] += part[u];
                         }
-                        const int64_t at = w.c_row * args.n + w.n0 + i;
 #pragma unroll
-                        for (int u = 0; u < kCols; ++u)
-                            if (i < w.n_valid && c0 + u * cs < w.m_valid)
-                                store_c<F32>(args.c, at + (c0 + u * cs) * args.n, sum[u], args.accumulate);
+                        for (int u = 0; u < kCols; ++u) {
+                            if (i >= w.n_valid || c0 + u * cs >= w.m_valid) continue;
+                            const int64_t o = at + static_cast<int64_t>(u * cs) * args.n;
+                            if (OUT == 0) {
+                                static_cast<uint16_t *>(args.c)[o] = static_cast<uint16_t>(pack_bf16x2(sum[u], 0.0f) & 0xFFFFu);
+                            } else {
+                                float *p = static_cast<float *>(args.c) + o;
+                                *p = OUT == 2 ? *p + sum[u] : sum[u];
+                            }
+                        }
                     }
                 }
-                named_barrier_sync(1, 128);
+                named_barrier_sync(1, kEpiThreads);
                 if (threadIdx.x >= 64 && threadIdx.x < 64 + cs)
                     mbar_arrive_cluster(mapa_shared(smem_u32(part_empty), threadIdx.x - 64));
             }
@@ -526,24 +590,11 @@ __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap *map, const 
                  : "memory");
 }
 
-// Four columns of scales of this warp's lane quarter from registers.
-__device__ __forceinline__ void tmem_store_4cols(uint32_t taddr, uint4 v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v.x), "r"(v.y), "r"(v.z),
-                 "r"(v.w)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
 // TMEM of a pair tile: the two accumulators overlap in 128 columns, which leaves 128
 // for the scales: accumulator 0 at 0, accumulator 1 at 128, the scales of each of the
 // five stages (A: 8 columns, B: 16) from 384 on.  The epilogue drains the shared
 // columns first and tells the MMA so; only then may the next tile start, and it does
 // while the rest drains.
-//
-// Four warps of each CTA put a stage's scales into TMEM (tcgen05.st, one lane quarter
-// each).  tcgen05.cp would do it without them, but it runs in the MMAs' pipe: its six
-// copies a stage cost some 300 of a stage's 512 MMA cycles (8192 x 16384 x 4096: 236
-// us with the copies, 189 without them).
 struct F4Pair {
     static constexpr int kThreads = 448;           // TMA, MMA, eight epilogue warps, four scale warps
     static constexpr int kOpBytes = 128 * 128;     // 128 rows of A or B
@@ -881,7 +932,7 @@ bool make_map_codes(CUtensorMap *m, const void *codes, int64_t rows, int64_t k, 
     return make_map_2d(m, codes, kMapU8, static_cast<uint64_t>(fp4_row_bytes(k)), static_cast<uint64_t>(rows), 128, box_rows);
 }
 
-template <class C, bool F32>
+template <class C, int OUT>
 int run_small(F4Args a, const Fp4Product &p, int cs, int workers, cudaStream_t s) {
     a.mt = static_cast<int>((p.m + C::BN - 1) / C::BN);
     a.nt = static_cast<int>((p.n + 127) / 128);
@@ -893,7 +944,7 @@ int run_small(F4Args a, const Fp4Product &p, int cs, int workers, cudaStream_t s
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) return MLPBLK_ECUDA;
     if (!attr_set[dev]) {
-        const int rc = cuda_status(cudaFuncSetAttribute(f4_small_kernel<C, F32>,
+        const int rc = cuda_status(cudaFuncSetAttribute(f4_small_kernel<C, OUT>,
                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes));
         if (rc != MLPBLK_OK) return rc;
         attr_set[dev] = 1;
@@ -912,7 +963,7 @@ int run_small(F4Args a, const Fp4Product &p, int cs, int workers, cudaStream_t s
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cs > 1 ? 2 : 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, f4_small_kernel<C, F32>, mA, mB, a));
+    return cuda_status(cudaLaunchKernelEx(&cfg, f4_small_kernel<C, OUT>, mA, mB, a));
 }
 
 // Scales as a 2-D array of words: a row is the tiles of 128 rows of the matrix, a
@@ -1003,7 +1054,6 @@ int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s) {
     a.count = p.count;
     a.seg = p.seg;
     a.c = p.c;
-    a.accumulate = p.accumulate;
     const bool f32 = p.out_dtype == MLPBLK_FP32;
     int64_t rows = p.m;  // rows of one product, at most
     int64_t groups = 1;
@@ -1032,8 +1082,15 @@ int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s) {
     if (workers < 1) workers = 1;
     if (p.mode != kFp4GroupRows && tiles < workers) workers = tiles;
     const int w = static_cast<int>(workers);
-    if (few) return f32 ? run_small<F4Small<32>, true>(a, p, cs, w, s) : run_small<F4Small<32>, false>(a, p, cs, w, s);
-    return f32 ? run_small<F4Small<128>, true>(a, p, cs, w, s) : run_small<F4Small<128>, false>(a, p, cs, w, s);
+#define MLPBLK_SMALL(BN)                                             \
+    {                                                                \
+        if (!f32) return run_small<F4Small<BN>, 0>(a, p, cs, w, s);    \
+        if (!p.accumulate) return run_small<F4Small<BN>, 1>(a, p, cs, w, s); \
+        return run_small<F4Small<BN>, 2>(a, p, cs, w, s);              \
+    }
+    if (few) MLPBLK_SMALL(32)
+    MLPBLK_SMALL(128)
+#undef MLPBLK_SMALL
 }
 
 int take_device_error_gemm_f4() {
