@@ -232,6 +232,12 @@ quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map
         uint32_t word[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            const bool out_row = r0 + 32 * j < rows;
+            if (!live[j]) {  // a row of zeros, or none
+                if (out_row && c < 2 * ld) *reinterpret_cast<uint32_t *>(out + 32 * j * ld + c / 2) = 0u;
+                word[j] = 0u;
+                continue;
+            }
             float v[8];
             uint32_t m;
             if (RELU2) {
@@ -253,7 +259,7 @@ quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map
                 o[j].scaled(inv, v);
             }
             const uint32_t q = sb == 255u ? 0u : e2m1x8(v);
-            if (r0 + 32 * j < rows && c < 2 * ld) *reinterpret_cast<uint32_t *>(out + 32 * j * ld + c / 2) = q;
+            if (c < 2 * ld) *reinterpret_cast<uint32_t *>(out + 32 * j * ld + c / 2) = q;
             // the four blocks' bytes of this half warp
             uint32_t w = sb << (8 * ((lane >> 2) & 3));
             w |= __shfl_xor_sync(0xffffffffu, w, 4);

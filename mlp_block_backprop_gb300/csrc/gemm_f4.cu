@@ -40,6 +40,7 @@ struct F4Args {
     int64_t max_rows;
     const uint8_t *sa, *sb;             // scales
     int64_t row_tile_bytes;             // of one 128-row strip of scale tiles (A and B share K)
+    int prefetch;                       // f4_small: ask B into L2 ahead
     int group_m;                        // raster: this many tiles of A sweep B together
     const int *count, *seg;
     void *c;
@@ -77,6 +78,13 @@ __device__ __forceinline__ void tmem_store_4cols(uint32_t taddr, uint4 v) {
                  : "memory");
 }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// mbar_arrive_expect_tx without its release: the producer's own accesses need no
+// ordering (the copies it issues signal the barrier by themselves).
+__device__ __forceinline__ void mbar_expect_relaxed(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+                 : "memory");
+}
 
 // Asks L2 to fetch a box of a 2-D tensor map.
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int32_t c0, int32_t c1) {
@@ -229,20 +237,27 @@ __device__ __forceinline__ F4Tile f4_tile(const F4Args &a, const F4Groups *g, in
 // ------------------------------------------------------------------- f4_small
 
 // BN columns: 32 for up to 32 tokens, 128 beyond.  A's scale tile holds 128 rows, so
-// a tile of 32 tokens starts at a multiple of 128 (there is only one).
-template <int BN_>
+// a tile of 32 tokens starts at a multiple of 128 (there is only one).  A tile of the
+// 128-column kernel that has 32 or 64 rows at most loads and multiplies no more (the
+// experts of a batch of a few hundred tokens).  SPLIT: K may be split over a cluster.
+// With 32 columns two CTAs fit an SM, so the next product's set-up and prefetch run
+// beside this one's end.
+template <int BN_, bool SPLIT_>
 struct F4Small {
     static constexpr int BN = BN_;
+    static constexpr bool SPLIT = SPLIT_;
     static constexpr int kEpiWarps = BN == 128 ? 8 : 4;  // two a lane quarter: 64 columns each
     static constexpr int kEpiCols = BN == 128 ? 64 : 32;
-    static constexpr int kThreads = 64 + 32 * kEpiWarps + 128;  // TMA, MMA, epilogue, four scale warps
+    static constexpr int kThreads = 64 + 32 * kEpiWarps + 128 + 32;  // codes, MMA, epilogue, four scale warps, scale loads
+    static constexpr int kScaleLoadWarp = kThreads / 32 - 1;
     static constexpr int kLBytes = 128 * 128;      // B's rows, on the lanes
     static constexpr int kRBytes = BN * 128;       // A's rows, on the columns
     static constexpr int kSfBytes = 1024;          // scales of 128 rows and a stage of K
     static constexpr int kStageBytes = kLBytes + kRBytes + 2 * kSfBytes;
-    static constexpr int kDumpBytes = BN * 128 * 4;  // an fp32 tile, for the cluster's sum
+    static constexpr int kDumpBytes = SPLIT ? BN * 128 * 4 : 0;  // an fp32 tile, for the cluster's sum
     static constexpr int kCtrlBytes = 4096;
-    static constexpr int kStages = (kSmemLimit - 1024 - kCtrlBytes - kDumpBytes) / kStageBytes;
+    static constexpr int kBudget = BN == 128 ? kSmemLimit : 112 * 1024;
+    static constexpr int kStages = (kBudget - 1024 - kCtrlBytes - kDumpBytes) / kStageBytes;
     static constexpr int kSmemBytes = 1024 + kCtrlBytes + kDumpBytes + kStages * kStageBytes;
     // TMEM: two accumulators, then each stage's scales (8 columns each operand)
     static constexpr int kSfCol = 2 * BN;
@@ -251,6 +266,12 @@ struct F4Small {
     static_assert(kStages >= 3 && kSfCol + kStages * kSfSet <= 512, "pipeline");
     static_assert(sizeof(F4Groups) + 512 <= kCtrlBytes, "control block");
 };
+
+// Columns that a tile's loads and MMAs cover.
+template <int BN>
+__device__ __forceinline__ int f4_width(const F4Tile &w) {
+    return w.m_valid <= 32 ? 32 : (w.m_valid <= 64 ? 64 : BN);
+}
 
 // 32 columns of a tile out of a lane's registers: column j goes to C's row row0 + j,
 // lane i to its column col0 + i; `rows` of the columns and the lanes with `on` are stored.
@@ -292,9 +313,37 @@ __device__ __forceinline__ void store_columns(void *c, int64_t row0, int64_t n, 
     }
 }
 
+// Asks the first tiles of a worker's B into L2 while the previous kernels (A's
+// quantisation, as a rule) still run: no data reaches this kernel before
+// griddep_wait.  With few tokens the weights' way from HBM is most of the time.  Grouped,
+// the tiles are not known yet: every expert is taken to have one tile of rows (the host
+// asks for it only where most experts do).
+template <class C>
+__device__ __forceinline__ void f4_prefetch(const F4Args &a, const CUtensorMap *map, int tiles, int worker, int workers,
+                                            int rank, int cs) {
+    int left = kF4PrefetchStages;
+    const int all = a.mode == kFp4Dense ? tiles : a.experts * a.nt;
+    for (int t = worker; t < all && left > 0; t += workers) {
+        int e = 0, mi = 0, ni = t;
+        if (a.mode == kFp4Dense) {
+            raster_tile(t, a.mt, a.nt, a.group_m, mi, ni);
+        } else {
+            e = t / a.nt;
+            ni = t - e * a.nt;
+        }
+        const uint8_t *sb = a.sb + (static_cast<int64_t>(e) * ((a.n + 127) / 128) + ni) * a.row_tile_bytes;
+        const int k1 = a.kblocks * (rank + 1) / cs;
+        for (int kb = a.kblocks * rank / cs; kb < k1 && left > 0; ++kb, --left) {
+            tma_prefetch_2d(map, kb * 128, e * static_cast<int>(a.n) + ni * 128);
+            bulk_prefetch_l2(sb + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes);
+        }
+    }
+}
+
 template <class C, int OUT>
 __global__ void __launch_bounds__(C::kThreads, 1)
-f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const F4Args args) {
+f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
+                const __grid_constant__ CUtensorMap tmB, const F4Args args) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     constexpr int S = C::kStages;
@@ -317,8 +366,8 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     static_assert((3 * S + 6) * 8 <= 384, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cs = static_cast<int>(cluster_nctarank());
-    const int rank = static_cast<int>(cluster_ctarank());
+    const int cs = C::SPLIT ? static_cast<int>(cluster_nctarank()) : 1;
+    const int rank = C::SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
     const int worker = static_cast<int>(blockIdx.x) / cs, workers = static_cast<int>(gridDim.x) / cs;
 
     if (threadIdx.x == 0) {
@@ -336,6 +385,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         *abort_flag = 0;
         fence_barrier_init();
         prefetch_tensormap(&tmA);
+        if (C::BN > 32) prefetch_tensormap(&tmA32);
         prefetch_tensormap(&tmB);
     }
     if (warp == 1) {
@@ -348,50 +398,62 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
     griddep_launch_dependents();
+    const bool dense = args.mode == kFp4Dense;
     int tiles = args.mt * args.nt;  // dense; grouped: from the segments, below
-    if (args.mode == kFp4Dense && warp == 0 && lane == 0 && worker < tiles) {
-        // B is asked into L2 while the previous kernel (A's quantisation, as a rule) still
-        // runs: no data reaches this kernel before griddep_wait.  At one token the
-        // weights' way from HBM is most of the time.
-        const F4Tile w = f4_tile<C::BN, 128>(args, groups, worker, args.group_m);
-        const int k0 = w.kb1 * rank / cs, k1 = w.kb1 * (rank + 1) / cs;
-        for (int kb = k0; kb < k1 && kb < k0 + kF4PrefetchStages; ++kb) {
-            tma_prefetch_2d(&tmB, kb * 128, w.b_row);
-            bulk_prefetch_l2(w.sb + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes);
-        }
-    }
+    int t = worker;                 // the tile at hand, the same walk in every role
+    F4Tile w;
+    if (dense && t < tiles) w = f4_tile<C::BN, 128>(args, groups, t, args.group_m);
+    if (args.prefetch && warp == 2 && lane == 0) f4_prefetch<C>(args, &tmB, tiles, worker, workers, rank, cs);
     __syncwarp();
     griddep_wait();
-    if (args.mode != kFp4Dense) {
+    if (!dense) {
         if (warp == 0) {
             const int total = f4_groups<C::BN, 128>(args, groups, lane);
             if (lane == 0) *tiles_s = total;
         }
         __syncthreads();
         tiles = *tiles_s;
+        if (t < tiles) w = f4_tile<C::BN, 128>(args, groups, t, args.group_m);
     }
+    auto next = [&]() {
+        t += workers;
+        if (t < tiles) w = f4_tile<C::BN, 128>(args, groups, t, args.group_m);
+    };
 
-    if (warp == 0) {
-        // ------------------------------------------------------ TMA producer
+    if (warp == 0 || warp == C::kScaleLoadWarp) {
+        // ----------------------------------------------------- TMA producers
+        // One warp for the codes, one for the scales: a thread issues a copy in some 70
+        // ns, and four a stage from one thread took longer than the stage (340 ns a
+        // stage at one token x 16384 x 4096).
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int t = worker; ok && t < tiles; t += workers) {
-                const F4Tile w = f4_tile<C::BN, 128>(args, groups, t, args.group_m);
+            for (; ok && t < tiles; next()) {
                 const int nk = w.kb1 - w.kb0;
                 const int k0 = w.kb0 + nk * rank / cs, k1 = w.kb0 + nk * (rank + 1) / cs;
+                const int wide = f4_width<C::BN>(w);
                 for (int kb = k0; kb < k1; ++kb) {
                     ok = mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag);
                     if (!ok) break;
-                    uint64_t *bar = &full_bar[stage];
-                    uint8_t *sf = sf_s + stage * 2 * C::kSfBytes;
-                    mbar_arrive_expect_tx(bar, C::kLBytes + C::kRBytes);
-                    tma_load_2d(&tmB, bar, lanes_s + stage * C::kLBytes, kb * 128, w.b_row);
-                    mbar_arrive_expect_tx(&sf_bar[stage], 2 * C::kSfBytes);
-                    bulk_copy_g2s(sf, w.sb + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes, &sf_bar[stage]);
-                    bulk_copy_g2s(sf + C::kSfBytes, w.sa + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes, &sf_bar[stage]);
-                    tma_load_2d(&tmA, bar, cols_s + stage * C::kRBytes, kb * 128, w.a_row);
+                    if (warp == 0) {
+                        uint64_t *bar = &full_bar[stage];
+                        uint8_t *cols = cols_s + stage * C::kRBytes;
+                        mbar_expect_relaxed(bar, C::kLBytes + wide * 128);
+                        tma_load_2d(&tmB, bar, lanes_s + stage * C::kLBytes, kb * 128, w.b_row);
+                        if (wide == C::BN) {
+                            tma_load_2d(&tmA, bar, cols, kb * 128, w.a_row);
+                        } else {
+                            tma_load_2d(&tmA32, bar, cols, kb * 128, w.a_row);
+                            if (wide > 32) tma_load_2d(&tmA32, bar, cols + 32 * 128, kb * 128, w.a_row + 32);
+                        }
+                    } else {
+                        uint64_t *bar = &sf_bar[stage];
+                        uint8_t *sf = sf_s + stage * 2 * C::kSfBytes;
+                        mbar_expect_relaxed(bar, 2 * C::kSfBytes);
+                        bulk_copy_g2s(sf, w.sb + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes, bar);
+                        bulk_copy_g2s(sf + C::kSfBytes, w.sa + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes, bar);
+                    }
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
@@ -406,8 +468,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             int stage = 0, it = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int t = worker; ok && t < tiles; t += workers, ++it) {
-                const F4Tile w = f4_tile<C::BN, 128>(args, groups, t, args.group_m);
+            for (; ok && t < tiles; next(), ++it) {
                 const int nk = w.kb1 - w.kb0;
                 const int k0 = w.kb0 + nk * rank / cs, k1 = w.kb0 + nk * (rank + 1) / cs;
                 const int buf = it & 1;
@@ -415,6 +476,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 if (!ok) break;
                 tc_fence_after_sync();
                 const uint32_t d = tmem_base + buf * C::BN;
+                const uint32_t idesc = idesc_mxf4(128, f4_width<C::BN>(w), 0);
                 for (int kb = k0; kb < k1; ++kb) {
                     ok = mbar_wait(&full_bar[stage], phase, abort_flag);
                     if (!ok) break;
@@ -425,7 +487,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         umma_mxf4(d, smem_desc_sw128(la + 32 * j, 16, 1024), smem_desc_sw128(ca + 32 * j, 16, 1024),
-                                  (j & 1) ? idesc_mxf4(128, C::BN, 2) : idesc_mxf4(128, C::BN, 0), sl + 4 * (j >> 1),
+                                  (j & 1) ? idesc | idesc_mxf4(0, 0, 2) : idesc, sl + 4 * (j >> 1),
                                   sc + 4 * (j >> 1), (kb > k0 || j > 0) ? 1u : 0u);
                     umma_commit(&empty_bar[stage]);
                     if (++stage == S) {
@@ -445,8 +507,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int t = worker; ok && t < tiles; t += workers) {
-            const F4Tile w = f4_tile<C::BN, 128>(args, groups, t, args.group_m);
+        for (; ok && t < tiles; next()) {
             const int nk = w.kb1 - w.kb0;
             const int k0 = w.kb0 + nk * rank / cs, k1 = w.kb0 + nk * (rank + 1) / cs;
             for (int kb = k0; kb < k1; ++kb) {
@@ -480,8 +541,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         const int i = 32 * q + lane;  // lane of the tile: C's column n0 + i
         constexpr int kEpiThreads = 32 * C::kEpiWarps;
         int it = 0;
-        for (int t = worker; t < tiles; t += workers, ++it) {
-            const F4Tile w = f4_tile<C::BN, 128>(args, groups, t, args.group_m);
+        for (; t < tiles; next(), ++it) {
             const int nk = w.kb1 - w.kb0;
             const bool some = nk * (rank + 1) / cs > nk * rank / cs;  // this CTA has a part of K
             const int buf = it & 1;
@@ -596,7 +656,8 @@ __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap *map, const 
 // columns first and tells the MMA so; only then may the next tile start, and it does
 // while the rest drains.
 struct F4Pair {
-    static constexpr int kThreads = 448;           // TMA, MMA, eight epilogue warps, four scale warps
+    static constexpr int kThreads = 480;           // codes, MMA, eight epilogue warps, four scale warps, scale loads
+    static constexpr int kScaleLoadWarp = kThreads / 32 - 1;
     static constexpr int kOpBytes = 128 * 128;     // 128 rows of A or B
     static constexpr int kSfABytes = 1024, kSfBBytes = 2048;
     static constexpr int kSfBytes = kSfABytes + kSfBBytes;
@@ -668,45 +729,55 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
-    griddep_enter();
-    if (warp == 0) {
-        int tiles;
-        if (args.mode == kFp4Dense)
-            tiles = args.mt * args.nt;
-        else
-            tiles = f4_groups<256, 256>(args, groups, lane);
-        if (lane == 0) *tiles_s = tiles;
+    griddep_launch_dependents();
+    int tiles = args.mt * args.nt;  // dense; grouped: from the segments, below
+    int t = worker;                 // the tile at hand, the same walk in every role
+    F4Tile w;
+    if (args.mode == kFp4Dense && t < tiles) w = f4_tile<256, 256>(args, groups, t, args.group_m);
+    griddep_wait();
+    if (args.mode != kFp4Dense) {
+        if (warp == 0) {
+            const int total = f4_groups<256, 256>(args, groups, lane);
+            if (lane == 0) *tiles_s = total;
+        }
+        __syncthreads();
+        tiles = *tiles_s;
+        if (t < tiles) w = f4_tile<256, 256>(args, groups, t, args.group_m);
     }
-    __syncthreads();
-    const int tiles = *tiles_s;
+    auto next = [&]() {
+        t += workers;
+        if (t < tiles) w = f4_tile<256, 256>(args, groups, t, args.group_m);
+    };
 
-    if (warp == 0) {
-        // ------------------------------------------------------ TMA producer
+    if (warp == 0 || warp == P::kScaleLoadWarp) {
+        // ------------------------------- TMA producers: the codes, the scales
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int t = worker; ok && t < tiles; t += workers) {
-                const F4Tile w = f4_tile<256, 256>(args, groups, t, args.group_m);
+            for (; ok && t < tiles; next()) {
                 const int a_row = w.a_row + static_cast<int>(rank) * 128, b_row = w.b_row + static_cast<int>(rank) * 128;
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     ok = mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag);
                     if (!ok) break;
-                    uint8_t *da = a_s + stage * P::kOpBytes, *db = b_s + stage * P::kOpBytes;
-                    uint8_t *sf = sf_s + stage * P::kSfBytes;
-                    mbar_arrive_expect_tx(&sf_bar[stage], P::kSfBytes);
-                    tma_load_2d(&tmSA, &sf_bar[stage], sf, kb * 256, w.sa_tile + static_cast<int>(rank));
-                    tma_load_2d(&tmSB, &sf_bar[stage], sf + P::kSfABytes, kb * 256, w.sb_tile);
-                    if (leader) {
-                        // the leader's barrier collects both CTAs' operand bytes
-                        uint64_t *bar = &full_bar[stage];
-                        mbar_arrive_expect_tx(bar, 4 * P::kOpBytes);
-                        tma_load_2d(&tmA, bar, da, kb * 128, a_row);
-                        tma_load_2d(&tmB, bar, db, kb * 128, b_row);
+                    if (warp != 0) {
+                        uint8_t *sf = sf_s + stage * P::kSfBytes;
+                        mbar_expect_relaxed(&sf_bar[stage], P::kSfBytes);
+                        tma_load_2d(&tmSA, &sf_bar[stage], sf, kb * 256, w.sa_tile + static_cast<int>(rank));
+                        tma_load_2d(&tmSB, &sf_bar[stage], sf + P::kSfABytes, kb * 256, w.sb_tile);
                     } else {
-                        const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
-                        tma_load_2d_pair(&tmA, bar, da, kb * 128, a_row);
-                        tma_load_2d_pair(&tmB, bar, db, kb * 128, b_row);
+                        uint8_t *da = a_s + stage * P::kOpBytes, *db = b_s + stage * P::kOpBytes;
+                        if (leader) {
+                            // the leader's barrier collects both CTAs' operand bytes
+                            uint64_t *bar = &full_bar[stage];
+                            mbar_expect_relaxed(bar, 4 * P::kOpBytes);
+                            tma_load_2d(&tmA, bar, da, kb * 128, a_row);
+                            tma_load_2d(&tmB, bar, db, kb * 128, b_row);
+                        } else {
+                            const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
+                            tma_load_2d_pair(&tmA, bar, da, kb * 128, a_row);
+                            tma_load_2d_pair(&tmB, bar, db, kb * 128, b_row);
+                        }
                     }
                     if (++stage == S) {
                         stage = 0;
@@ -722,12 +793,9 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             int stage = 0, it = 0;
             uint32_t phase = 0;
             bool ok = true;
-            int t = worker;
-            auto next_k = [&]() {  // stages of the next tile that has any, found ahead of its start
-                for (; t < tiles; t += workers) {
-                    const F4Tile w = f4_tile<256, 256>(args, groups, t, args.group_m);
+            auto next_k = [&]() {  // stages of the tile at hand, or of the next that has any
+                for (; t < tiles; next())
                     if (w.kb0 < w.kb1) return w.kb1 - w.kb0;
-                }
                 return 0;
             };
             int nk = next_k();
@@ -756,7 +824,7 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         phase ^= 1u;
                     }
                     if (kb == 0) {  // while the first stage's MMAs run
-                        t += workers;
+                        next();
                         nk = next_k();
                     }
                 }
@@ -775,8 +843,7 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int t = worker; ok && t < tiles; t += workers) {
-            const F4Tile w = f4_tile<256, 256>(args, groups, t, args.group_m);
+        for (; ok && t < tiles; next()) {
             for (int kb = w.kb0; kb < w.kb1; ++kb) {
                 ok = mbar_wait(&sf_bar[stage], phase, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
@@ -819,8 +886,7 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const uint32_t sw = static_cast<uint32_t>(lane & 7);
         const uint32_t ovl0 = mapa_shared(smem_u32(ovl_bar), 0), acce0 = mapa_shared(smem_u32(&acce_bar[0]), 0);
         int it = 0;
-        for (int t = worker; t < tiles; t += workers) {
-            const F4Tile w = f4_tile<256, 256>(args, groups, t, args.group_m);
+        for (; t < tiles; next()) {
             const bool some = w.kb0 < w.kb1;
             const int buf = it & 1;
             if (some) {
@@ -936,9 +1002,11 @@ template <class C, int OUT>
 int run_small(F4Args a, const Fp4Product &p, int cs, int workers, cudaStream_t s) {
     a.mt = static_cast<int>((p.m + C::BN - 1) / C::BN);
     a.nt = static_cast<int>((p.n + 127) / 128);
-    CUtensorMap mA, mB;
+    CUtensorMap mA, mA32, mB;
     const int64_t a_rows = p.m, b_rows = p.mode == kFp4GroupRows ? p.n * p.experts : p.n;
     if (!make_map_codes(&mA, p.a, a_rows, p.k, C::BN) || !make_map_codes(&mB, p.b, b_rows, p.k, 128)) return MLPBLK_ECUDA;
+    mA32 = mA;
+    if (C::BN > 32 && !make_map_codes(&mA32, p.a, a_rows, p.k, 32)) return MLPBLK_ECUDA;
     static int attr_set[64] = {0};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -962,8 +1030,8 @@ int run_small(F4Args a, const Fp4Product &p, int cs, int workers, cudaStream_t s
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = cs > 1 ? 2 : 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, f4_small_kernel<C, OUT>, mA, mB, a));
+    cfg.numAttrs = C::SPLIT ? 2 : 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, f4_small_kernel<C, OUT>, mA, mA32, mB, a));
 }
 
 // Scales as a 2-D array of words: a row is the tiles of 128 rows of the matrix, a
@@ -1082,14 +1150,19 @@ int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s) {
     if (workers < 1) workers = 1;
     if (p.mode != kFp4GroupRows && tiles < workers) workers = tiles;
     const int w = static_cast<int>(workers);
-#define MLPBLK_SMALL(BN)                                             \
-    {                                                                \
-        if (!f32) return run_small<F4Small<BN>, 0>(a, p, cs, w, s);    \
-        if (!p.accumulate) return run_small<F4Small<BN>, 1>(a, p, cs, w, s); \
-        return run_small<F4Small<BN>, 2>(a, p, cs, w, s);              \
+    // B ahead into L2 (see the kernel): dense, or grouped where most experts have rows
+    // (T * k >= 2 E: 86 % of them if the ids are even) and all of B fits the half of L2
+    const int64_t b_bytes = p.n * fp4_row_bytes(p.k) * groups;
+    a.prefetch = p.mode == kFp4Dense || (p.mode == kFp4GroupRows && p.max_rows >= 2 * p.experts && b_bytes <= (64ll << 20)) ? 1 : 0;
+#define MLPBLK_SMALL(BN, SPLIT)                                               \
+    {                                                                         \
+        if (!f32) return run_small<F4Small<BN, SPLIT>, 0>(a, p, cs, w, s);    \
+        if (!p.accumulate) return run_small<F4Small<BN, SPLIT>, 1>(a, p, cs, w, s); \
+        return run_small<F4Small<BN, SPLIT>, 2>(a, p, cs, w, s);              \
     }
-    if (few) MLPBLK_SMALL(32)
-    MLPBLK_SMALL(128)
+    if (few) MLPBLK_SMALL(32, true)
+    if (cs > 1) MLPBLK_SMALL(128, true)
+    MLPBLK_SMALL(128, false)
 #undef MLPBLK_SMALL
 }
 
