@@ -79,6 +79,23 @@ __device__ __forceinline__ void tmem_store_4cols(uint32_t taddr, uint4 v) {
 }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// One lane of the warp, the same one each time.  The roles that issue copies and MMAs
+// run their loops with the whole warp and let this lane issue: addresses and
+// descriptors are then warp-uniform and live in uniform registers.  With the loop
+// inside `if (lane == 0)` every operand crosses from vector registers, and a stage cost
+// the issuing thread some 680 cycles, more than its MMAs take.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t p;
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  elect.sync _|p, 0xffffffff;\n"
+        "  selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
 // mbar_arrive_expect_tx without its release: the producer's own accesses need no
 // ordering (the copies it issues signal the barrier by themselves).
 __device__ __forceinline__ void mbar_expect_relaxed(uint64_t *bar, uint32_t bytes) {
@@ -365,7 +382,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     F4Groups *groups = reinterpret_cast<F4Groups *>(ctrl + 512);
     static_assert((3 * S + 6) * 8 <= 384, "barriers");
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int cs = C::SPLIT ? static_cast<int>(cluster_nctarank()) : 1;
     const int rank = C::SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
     const int worker = static_cast<int>(blockIdx.x) / cs, workers = static_cast<int>(gridDim.x) / cs;
@@ -425,17 +442,18 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         // One warp for the codes, one for the scales: a thread issues a copy in some 70
         // ns, and four a stage from one thread took longer than the stage (340 ns a
         // stage at one token x 16384 x 4096).
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (; ok && t < tiles; next()) {
-                const int nk = w.kb1 - w.kb0;
-                const int k0 = w.kb0 + nk * rank / cs, k1 = w.kb0 + nk * (rank + 1) / cs;
-                const int wide = f4_width<C::BN>(w);
-                for (int kb = k0; kb < k1; ++kb) {
-                    ok = mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag);
-                    if (!ok) break;
+        const bool issue = elect_lane();
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (; ok && t < tiles; next()) {
+            const int nk = w.kb1 - w.kb0;
+            const int k0 = w.kb0 + nk * rank / cs, k1 = w.kb0 + nk * (rank + 1) / cs;
+            const int wide = f4_width<C::BN>(w);
+            for (int kb = k0; kb < k1; ++kb) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag));
+                if (!ok) break;
+                if (issue) {
                     if (warp == 0) {
                         uint64_t *bar = &full_bar[stage];
                         uint8_t *cols = cols_s + stage * C::kRBytes;
@@ -454,50 +472,53 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         bulk_copy_g2s(sf, w.sb + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes, bar);
                         bulk_copy_g2s(sf + C::kSfBytes, w.sa + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes, bar);
                     }
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                }
+                __syncwarp();
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            int stage = 0, it = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (; ok && t < tiles; next(), ++it) {
-                const int nk = w.kb1 - w.kb0;
-                const int k0 = w.kb0 + nk * rank / cs, k1 = w.kb0 + nk * (rank + 1) / cs;
-                const int buf = it & 1;
-                ok = mbar_wait(&acce_bar[buf], ((it >> 1) & 1) ^ 1u, abort_flag);
+        const bool issue = elect_lane();
+        const uint64_t l0 = smem_desc_sw128(smem_u32(lanes_s), 16, 1024), c0 = smem_desc_sw128(smem_u32(cols_s), 16, 1024);
+        int stage = 0, it = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (; ok && t < tiles; next(), ++it) {
+            const int nk = w.kb1 - w.kb0;
+            const int k0 = w.kb0 + nk * rank / cs, k1 = w.kb0 + nk * (rank + 1) / cs;
+            const int buf = it & 1;
+            ok = __all_sync(0xffffffffu, mbar_wait(&acce_bar[buf], ((it >> 1) & 1) ^ 1u, abort_flag));
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t d = tmem_base + buf * C::BN;
+            const uint32_t idesc = idesc_mxf4(128, f4_width<C::BN>(w), 0);
+            for (int kb = k0; kb < k1; ++kb) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort_flag));
                 if (!ok) break;
                 tc_fence_after_sync();
-                const uint32_t d = tmem_base + buf * C::BN;
-                const uint32_t idesc = idesc_mxf4(128, f4_width<C::BN>(w), 0);
-                for (int kb = k0; kb < k1; ++kb) {
-                    ok = mbar_wait(&full_bar[stage], phase, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint32_t la = smem_u32(lanes_s + stage * C::kLBytes);
-                    const uint32_t ca = smem_u32(cols_s + stage * C::kRBytes);
-                    const uint32_t sl = tmem_base + C::kSfCol + stage * C::kSfSet, sc = sl + 8;
+                const uint64_t ld = l0 + stage * (C::kLBytes >> 4), cd = c0 + stage * (C::kRBytes >> 4);
+                const uint32_t sl = tmem_base + C::kSfCol + stage * C::kSfSet, sc = sl + 8;
+                if (issue) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        umma_mxf4(d, smem_desc_sw128(la + 32 * j, 16, 1024), smem_desc_sw128(ca + 32 * j, 16, 1024),
-                                  (j & 1) ? idesc | idesc_mxf4(0, 0, 2) : idesc, sl + 4 * (j >> 1),
+                        umma_mxf4(d, ld + 2 * j, cd + 2 * j, (j & 1) ? idesc | idesc_mxf4(0, 0, 2) : idesc, sl + 4 * (j >> 1),
                                   sc + 4 * (j >> 1), (kb > k0 || j > 0) ? 1u : 0u);
                     umma_commit(&empty_bar[stage]);
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
                 }
-                if (!ok) break;
-                umma_commit(&accf_bar[buf]);
+                __syncwarp();
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
+            if (!ok) break;
+            if (issue) umma_commit(&accf_bar[buf]);
+            __syncwarp();
         }
         __syncwarp();
     } else if (warp >= 2 + C::kEpiWarps) {
@@ -696,7 +717,7 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     int *tiles_s = reinterpret_cast<int *>(ctrl + 392);
     F4Groups *groups = reinterpret_cast<F4Groups *>(ctrl + 512);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int worker = static_cast<int>(blockIdx.x >> 1), workers = static_cast<int>(gridDim.x >> 1);
@@ -751,15 +772,17 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
     if (warp == 0 || warp == P::kScaleLoadWarp) {
         // ------------------------------- TMA producers: the codes, the scales
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (; ok && t < tiles; next()) {
-                const int a_row = w.a_row + static_cast<int>(rank) * 128, b_row = w.b_row + static_cast<int>(rank) * 128;
-                for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                    ok = mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag);
-                    if (!ok) break;
+        const bool issue = elect_lane();
+        const uint32_t full0 = mapa_shared(smem_u32(&full_bar[0]), 0);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (; ok && t < tiles; next()) {
+            const int a_row = w.a_row + static_cast<int>(rank) * 128, b_row = w.b_row + static_cast<int>(rank) * 128;
+            for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag));
+                if (!ok) break;
+                if (issue) {
                     if (warp != 0) {
                         uint8_t *sf = sf_s + stage * P::kSfBytes;
                         mbar_expect_relaxed(&sf_bar[stage], P::kSfBytes);
@@ -774,22 +797,24 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                             tma_load_2d(&tmA, bar, da, kb * 128, a_row);
                             tma_load_2d(&tmB, bar, db, kb * 128, b_row);
                         } else {
-                            const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
-                            tma_load_2d_pair(&tmA, bar, da, kb * 128, a_row);
-                            tma_load_2d_pair(&tmB, bar, db, kb * 128, b_row);
+                            tma_load_2d_pair(&tmA, full0 + stage * 8, da, kb * 128, a_row);
+                            tma_load_2d_pair(&tmB, full0 + stage * 8, db, kb * 128, b_row);
                         }
                     }
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                }
+                __syncwarp();
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------- MMA issuer
-        if (lane == 0 && leader) {
+        if (leader) {
+            const bool issue = elect_lane();
+            const uint64_t a0 = smem_desc_sw128(smem_u32(a_s), 16, 1024), b0 = smem_desc_sw128(smem_u32(b_s), 16, 1024);
             int stage = 0, it = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -804,21 +829,24 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 const int buf = it & 1;
                 ok = mbar_wait(&acce_bar[buf], ((it >> 1) & 1) ^ 1u, abort_flag);
                 if (ok && it > 0) ok = mbar_wait(ovl_bar, (it - 1) & 1, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after_sync();
                 const uint32_t d = tmem_base + (buf ? P::kAcc1 : 0);
                 for (int kb = 0; kb < now; ++kb) {
-                    ok = mbar_wait(&full_bar[stage], phase, abort_flag);
+                    ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort_flag));
                     if (!ok) break;
                     tc_fence_after_sync();
-                    const uint32_t aa = smem_u32(a_s + stage * P::kOpBytes), ba = smem_u32(b_s + stage * P::kOpBytes);
+                    const uint64_t ad = a0 + stage * (P::kOpBytes >> 4), bd = b0 + stage * (P::kOpBytes >> 4);
                     const uint32_t sa = tmem_base + P::kSfCol + stage * P::kSfSet, sb = sa + 8;
+                    if (issue) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        umma_mxf4_pair(d, smem_desc_sw128(aa + 32 * j, 16, 1024), smem_desc_sw128(ba + 32 * j, 16, 1024),
-                                       (j & 1) ? idesc_mxf4(256, 256, 2) : idesc_mxf4(256, 256, 0), sa + 4 * (j >> 1),
-                                       sb + 8 * (j >> 1), (kb > 0 || j > 0) ? 1u : 0u);
-                    umma_commit_pair(&empty_bar[stage], 3);
+                        for (int j = 0; j < 4; ++j)
+                            umma_mxf4_pair(d, ad + 2 * j, bd + 2 * j, (j & 1) ? idesc_mxf4(256, 256, 2) : idesc_mxf4(256, 256, 0),
+                                           sa + 4 * (j >> 1), sb + 8 * (j >> 1), (kb > 0 || j > 0) ? 1u : 0u);
+                        umma_commit_pair(&empty_bar[stage], 3);
+                    }
+                    __syncwarp();
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
@@ -829,7 +857,8 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     }
                 }
                 if (!ok) break;
-                umma_commit_pair(&accf_bar[buf], 3);
+                if (issue) umma_commit_pair(&accf_bar[buf], 3);
+                __syncwarp();
                 ++it;
             }
         }
