@@ -158,6 +158,7 @@ struct F4Groups {
     int seg[kF4MaxExperts + 1];
     int count[kF4MaxExperts];
     int before[kF4MaxExperts + 1];
+    int warp_tiles[kF4MaxExperts / 32];
 };
 
 // One output tile: rows m0 .. m0 + m_valid of A, columns n0 .. n0 + n_valid of C.
@@ -171,42 +172,46 @@ struct F4Tile {
     int n0, m_valid, n_valid;
 };
 
-// Fills `g` (one warp; lane l takes experts l, l + 32, ...) for tiles of TM rows and
-// TN columns; returns the number of tiles.  Values that a plan of another shape would
-// give are cut to the arrays, so no access leaves them.
-template <int TM, int TN>
-__device__ int f4_groups(const F4Args &a, F4Groups *g, int lane) {
-    const int64_t limit = a.mode == kFp4GroupRows ? a.m : static_cast<int64_t>(a.kblocks) * kF4KB;
-    const int nt = a.nt, mt = a.mt;
-    int run = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += 32) {
-        const int e = e0 + lane;
-        int tiles = 0;
-        if (e < a.experts) {
-            const int s0 = static_cast<int>(min(max(static_cast<int64_t>(a.seg[e]), int64_t(0)), limit));
-            const int s1 = static_cast<int>(min(max(static_cast<int64_t>(a.seg[e + 1]), int64_t(0)), limit));
-            g->seg[e] = s0;
-            if (e == a.experts - 1) g->seg[a.experts] = s1;
-            if (a.mode == kFp4GroupRows) {
-                int64_t c = min(static_cast<int64_t>(a.count[e]), static_cast<int64_t>(s1 - s0));
-                if (a.max_rows > 0) c = min(c, a.max_rows);
-                g->count[e] = static_cast<int>(max(c, int64_t(0)));
-                tiles = (g->count[e] + TM - 1) / TM * nt;
-            } else {
-                tiles = mt * nt;
-            }
+// Fills `g` (the whole CTA, a thread an expert) for tiles of TM rows; returns the number
+// of tiles.  Values that a plan of another shape would give are cut to the arrays, so
+// no access leaves them.
+template <int TM>
+__device__ __forceinline__ int f4_groups(const F4Args &a, F4Groups *g) {
+    const int e = static_cast<int>(threadIdx.x), lane = e & 31, warp = e >> 5;
+    const int limit = static_cast<int>(a.mode == kFp4GroupRows ? a.m : static_cast<int64_t>(a.kblocks) * kF4KB);
+    int tiles = 0;
+    if (e < a.experts) {
+        const int s0 = min(max(a.seg[e], 0), limit), s1 = min(max(a.seg[e + 1], 0), limit);
+        g->seg[e] = s0;
+        if (e == a.experts - 1) g->seg[a.experts] = s1;
+        if (a.mode == kFp4GroupRows) {
+            int c = max(min(a.count[e], s1 - s0), 0);
+            if (a.max_rows > 0) c = static_cast<int>(min(static_cast<int64_t>(c), a.max_rows));
+            g->count[e] = c;
+            tiles = (c + TM - 1) / TM * a.nt;
+        } else {
+            tiles = a.mt * a.nt;
         }
-        int incl = tiles;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (e < a.experts) g->before[e] = run + incl - tiles;
-        run += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) g->before[a.experts] = run;
-    return run;
+    int incl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (warp < kF4MaxExperts / 32 && lane == 31) g->warp_tiles[warp] = incl;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int v = 0; v < kF4MaxExperts / 32; ++v) {
+        const int c = v * 32 < a.experts ? g->warp_tiles[v] : 0;
+        before += v < warp ? c : 0;
+        all += c;
+    }
+    if (e < a.experts) g->before[e] = before + incl - tiles;
+    if (e == 0) g->before[a.experts] = all;
+    __syncthreads();
+    return all;
 }
 
 // Tile t.  Dense tiles are rastered with A's tiles fastest within a group of
@@ -227,7 +232,9 @@ __device__ __forceinline__ F4Tile f4_tile(const F4Args &a, const F4Groups *g, in
     }
     const int rows = a.mode == kFp4GroupRows ? g->count[e] : static_cast<int>(a.m);
     int mi = 0, ni = 0;
-    raster_tile(t, (rows + TM - 1) / TM, a.nt, group_m, mi, ni);
+    const int mt = (rows + TM - 1) / TM;
+    if (mt == 1) ni = t;
+    else raster_tile(t, mt, a.nt, group_m, mi, ni);
     const int first = a.mode == kFp4GroupRows ? g->seg[e] : 0;
     w.a_row = first + mi * TM;
     w.n0 = ni * TN;
@@ -332,9 +339,11 @@ __device__ __forceinline__ void store_columns(void *c, int64_t row0, int64_t n, 
 
 // Asks the first tiles of a worker's B into L2 while the previous kernels (A's
 // quantisation, as a rule) still run: no data reaches this kernel before
-// griddep_wait.  With few tokens the weights' way from HBM is most of the time.  Grouped,
-// the tiles are not known yet: every expert is taken to have one tile of rows (the host
-// asks for it only where most experts do).
+// griddep_wait.  With few tokens the weights' way from HBM is most of the time (one token x
+// 16384 x 4096 with the quantisation before it: 10.6 -> 10.0 us; a request of a row
+// each from 128 lanes instead of a box each: 12.2 us).  Grouped, the tiles are not
+// known yet: every expert is taken to have one tile of rows (the host asks for it
+// only where most experts do).
 template <class C>
 __device__ __forceinline__ void f4_prefetch(const F4Args &a, const CUtensorMap *map, int tiles, int worker, int workers,
                                             int rank, int cs) {
@@ -378,7 +387,6 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     uint64_t *part_empty = part_full + 1; // every CTA has read this CTA's part
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctrl + 384);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 388);
-    int *tiles_s = reinterpret_cast<int *>(ctrl + 392);
     F4Groups *groups = reinterpret_cast<F4Groups *>(ctrl + 512);
     static_assert((3 * S + 6) * 8 <= 384, "barriers");
 
@@ -424,12 +432,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     __syncwarp();
     griddep_wait();
     if (!dense) {
-        if (warp == 0) {
-            const int total = f4_groups<C::BN, 128>(args, groups, lane);
-            if (lane == 0) *tiles_s = total;
-        }
-        __syncthreads();
-        tiles = *tiles_s;
+        tiles = f4_groups<C::BN>(args, groups);
         if (t < tiles) w = f4_tile<C::BN, 128>(args, groups, t, args.group_m);
     }
     auto next = [&]() {
@@ -714,7 +717,6 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     uint64_t *sf_bar = ovl_bar + 1;      // this CTA's scales of a stage are in shared memory
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctrl + 384);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 388);
-    int *tiles_s = reinterpret_cast<int *>(ctrl + 392);
     F4Groups *groups = reinterpret_cast<F4Groups *>(ctrl + 512);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -757,12 +759,7 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     if (args.mode == kFp4Dense && t < tiles) w = f4_tile<256, 256>(args, groups, t, args.group_m);
     griddep_wait();
     if (args.mode != kFp4Dense) {
-        if (warp == 0) {
-            const int total = f4_groups<256, 256>(args, groups, lane);
-            if (lane == 0) *tiles_s = total;
-        }
-        __syncthreads();
-        tiles = *tiles_s;
+        tiles = f4_groups<256>(args, groups);
         if (t < tiles) w = f4_tile<256, 256>(args, groups, t, args.group_m);
     }
     auto next = [&]() {
@@ -1160,10 +1157,14 @@ int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s) {
     } else if (p.mode == kFp4GroupK) {
         groups = p.experts;
     }
-    // 256 x 256 pair tiles where they occupy most of the SM pairs
+    // 256 x 256 pair tiles where they occupy half of the SM pairs and, grouped by rows, an
+    // expert has more than one 128-row tile on average (1500 tokens, top-4 of 60 experts
+    // of 776 x 1000: 13.8 us in pair tiles)
     const int pairs = num_sms / 2;
-    const int64_t pair_tiles = (p.mode == kFp4GroupRows ? (p.m + 255) / 256 : (rows + 255) / 256 * groups) * ((p.n + 255) / 256);
-    if (pairs >= 1 && rows > 128 && 2 * pair_tiles >= pairs) {
+    const int64_t mean_rows = p.mode == kFp4GroupRows ? rows / p.experts : rows;
+    const int64_t pair_tiles = p.mode == kFp4GroupRows ? ((mean_rows + 255) / 256) * p.experts * ((p.n + 255) / 256)
+                                                       : (rows + 255) / 256 * groups * ((p.n + 255) / 256);
+    if (pairs >= 1 && mean_rows > 128 && 2 * pair_tiles >= pairs) {
         const bool tma = p.n * (f32 ? 4 : 2) % 16 == 0;
         const int w = static_cast<int>(p.mode != kFp4GroupRows && pair_tiles < pairs ? pair_tiles : pairs);
         if (!f32) return tma ? run_pair<0, true>(a, p, w, s) : run_pair<0, false>(a, p, w, s);
