@@ -439,8 +439,8 @@ int mlpblk_moe_backward_overwrite(const mlpblk_moe_desc *desc,
  * desc->dtype, weights and d_weights float32, the rest int32.  Sums are held in
  * float32 and rounded once; their order is fixed.  Any width; rows of a multiple
  * of 16 bytes move in 16-byte accesses.  pos, count and seg are those that
- * mlpblk_moe_sort wrote for the same descriptor.  Limits: experts 1..256, top_k
- * 1..256, pad 1..1024, R < 2^31.  Pointers are device pointers, 16-byte aligned.
+ * mlpblk_moe_sort wrote for the same descriptor.  Limits: width < 2^30, experts
+ * 1..256, top_k 1..256, pad 1..1024, R < 2^31.  Pointers are device pointers, 16-byte aligned.
  * Outputs alias no input (MLPBLK_EINVAL) but where stated.  Each returns an
  * MLPBLK_* code; tokens = 0 returns MLPBLK_OK and touches nothing, except that
  * mlpblk_moe_sort still writes count and seg (zeros).

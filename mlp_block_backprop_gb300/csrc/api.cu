@@ -1287,7 +1287,7 @@ int check_sort_desc(const mlpblk_sort_desc *d) {
         d->pad < 1 || d->pad > 1024)
         return MLPBLK_EINVAL;
     const int64_t lim = static_cast<int64_t>(1) << 31;
-    if (d->width >= lim || d->tokens >= lim / d->top_k) return MLPBLK_EINVAL;
+    if (d->width >= lim / 2 || d->tokens >= lim / d->top_k) return MLPBLK_EINVAL;
     if (d->tokens * d->top_k + static_cast<int64_t>(d->experts + 1) * d->pad >= lim) return MLPBLK_EINVAL;
     return MLPBLK_OK;
 }

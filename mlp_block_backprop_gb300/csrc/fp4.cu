@@ -21,19 +21,24 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
 // 8 floats -> 8 E2M1 codes (first value in the lowest four bits), nearest-even,
-// saturating.
+// saturating; RELU: negative values become 0.
+template <bool RELU>
 __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
     uint32_t r;
-    asm("{\n"
-        "  .reg .b8 a, b, c, d;\n"
-        "  cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
-        "  cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
-        "  cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
-        "  cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
-        "  mov.b32 %0, {a, b, c, d};\n"
-        "}\n"
-        : "=r"(r)
-        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+#define MLPBLK_E2M1(RELU_)                                                   \
+    asm("{\n"                                                                \
+        "  .reg .b8 a, b, c, d;\n"                                           \
+        "  cvt.rn.satfinite" RELU_ ".e2m1x2.f32 a, %2, %1;\n"                \
+        "  cvt.rn.satfinite" RELU_ ".e2m1x2.f32 b, %4, %3;\n"                \
+        "  cvt.rn.satfinite" RELU_ ".e2m1x2.f32 c, %6, %5;\n"                \
+        "  cvt.rn.satfinite" RELU_ ".e2m1x2.f32 d, %8, %7;\n"                \
+        "  mov.b32 %0, {a, b, c, d};\n"                                      \
+        "}\n"                                                                \
+        : "=r"(r)                                                            \
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]))
+    if (RELU) MLPBLK_E2M1(".relu");
+    else MLPBLK_E2M1("");
+#undef MLPBLK_E2M1
     return r;
 }
 
@@ -50,11 +55,18 @@ __device__ __forceinline__ float scale_inverse(uint32_t byte) {
     return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
 }
 
-// relu(v)^2, which keeps a NaN.
-__device__ __forceinline__ float relu2(float v) {
+// ReLU^2 needs no clamp of its own: the block's maximum is the square of the largest
+// v (0 at least), and v |v| has v^2's size and a sign that the conversion's .relu
+// reads.  max(m, v), a NaN once there is one:
+__device__ __forceinline__ float max_signed(float m, float v) {
     float r;
-    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
-    return r * r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_signed_bf16x2(uint32_t m, uint32_t v) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(v));
+    return r;
 }
 
 // max(|m|, |v|), a NaN once there is one (the bf16 form's signs are of no meaning: one
@@ -87,6 +99,22 @@ __device__ __forceinline__ int source_row(const int *row_map, int map_div, int64
     return m < 0 ? -1 : (map_div > 0 ? m / map_div : static_cast<int>(r));
 }
 
+// The bits of a block's largest |value| (or largest value, squared) from its maxima:
+// `m` packed bf16, or a float.
+template <bool RELU2>
+__device__ __forceinline__ uint32_t top_bits(uint32_t m) {
+    if (!RELU2) {
+        m &= 0x7FFF7FFFu;
+        return max(m << 16, m & 0xFFFF0000u);
+    }
+    const float t = max_signed(bf16_lo(m), bf16_hi(m));
+    return __float_as_uint(t * t);
+}
+template <bool RELU2>
+__device__ __forceinline__ uint32_t top_bits(float m) {
+    return __float_as_uint(RELU2 ? m * m : m);
+}
+
 // 8 consecutive values of a row, as loaded: 4 words of bf16 pairs or 8 floats.
 template <bool BF16>
 struct Oct;
@@ -117,8 +145,16 @@ struct Oct<true> {
             v[2 * i + 1] = bf16_hi(w[i]);
         }
     }
-    // the values times inv, a power of two: in bf16, two at a time
+    // what is rounded: the values times inv, a power of two (in bf16, two at a time), or
+    // their signed squares times inv
+    template <bool RELU2>
     __device__ __forceinline__ void scaled(float inv, float (&v)[8]) const {
+        if (RELU2) {
+            floats(v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = v[i] * fabsf(v[i]) * inv;
+            return;
+        }
         const uint32_t m = __float_as_uint(inv) >> 16, m2 = m | (m << 16);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -127,10 +163,12 @@ struct Oct<true> {
             v[2 * i + 1] = bf16_hi(u);
         }
     }
-    // bits of max |v| as a float
-    __device__ __forceinline__ uint32_t top() const {
-        const uint32_t m = max_abs_bf16x2(max_abs_bf16x2(w[0], w[1]), max_abs_bf16x2(w[2], w[3])) & 0x7FFF7FFFu;
-        return max(m << 16, m & 0xFFFF0000u);
+    using Max = uint32_t;
+    static constexpr Max kNone = 0u;
+    template <bool RELU2>
+    __device__ __forceinline__ void top(Max &m) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = RELU2 ? max_signed_bf16x2(m, w[i]) : max_abs_bf16x2(m, w[i]);
     }
 };
 template <>
@@ -165,16 +203,17 @@ struct Oct<false> {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = f[i];
     }
+    template <bool RELU2>
     __device__ __forceinline__ void scaled(float inv, float (&v)[8]) const {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = f[i] * inv;
+        for (int i = 0; i < 8; ++i) v[i] = (RELU2 ? f[i] * fabsf(f[i]) : f[i]) * inv;
     }
-    __device__ __forceinline__ uint32_t top() const { return top8(f); }
-    static __device__ __forceinline__ uint32_t top8(const float (&v)[8]) {
-        float m = 0.0f;
+    using Max = float;
+    static constexpr Max kNone = 0.0f;
+    template <bool RELU2>
+    __device__ __forceinline__ void top(Max &m) const {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max_abs(m, v[i]);
-        return __float_as_uint(m);
+        for (int i = 0; i < 8; ++i) m = RELU2 ? max_signed(m, f[i]) : max_abs(m, f[i]);
     }
 };
 
@@ -239,26 +278,14 @@ quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map
                 continue;
             }
             float v[8];
-            uint32_t m;
-            if (RELU2) {
-                o[j].floats(v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = relu2(v[i]);
-                m = Oct<false>::top8(v);
-            } else {
-                m = o[j].top();
-            }
+            typename Oct<BF16>::Max top = Oct<BF16>::kNone;
+            o[j].template top<RELU2>(top);
+            uint32_t m = top_bits<RELU2>(top);
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
             const uint32_t sb = scale_byte(m);
-            const float inv = scale_inverse(sb);
-            if (RELU2) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= inv;
-            } else {
-                o[j].scaled(inv, v);
-            }
-            const uint32_t q = sb == 255u ? 0u : e2m1x8(v);
+            o[j].template scaled<RELU2>(scale_inverse(sb), v);
+            const uint32_t q = sb == 255u ? 0u : e2m1x8<RELU2>(v);
             if (c < 2 * ld) *reinterpret_cast<uint32_t *>(out + 32 * j * ld + c / 2) = q;
             // the four blocks' bytes of this half warp
             uint32_t w = sb << (8 * ((lane >> 2) & 3));
@@ -270,6 +297,86 @@ quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map
             uint8_t *st = scales + ((static_cast<int64_t>(tile) * chunks + chunk) * 2 + (lane >> 4)) * 512 + rr * 16;
             *reinterpret_cast<uint4 *>(st) = make_uint4(word[0], word[1], word[2], word[3]);
         }
+    }
+}
+
+// Blocks along the source's rows, rows of 1024 columns and more in 16-byte accesses: a
+// lane holds a whole block (its 16-byte loads 64 or 128 bytes from its neighbour's; the
+// sectors' other halves come from L1), so a block's maximum needs no shuffle and its
+// codes are one 16-byte store.  A warp takes 1024 columns of the rows r, r + 32, r + 64,
+// r + 96 of a scale tile, two rows in flight; four lanes then transpose their 4 x 4
+// scale bytes and store 16 consecutive bytes of a tile.  8192 x 16384 bf16: 61 us with the
+// kernel above, 56 with this one (6.06 TB/s).
+template <bool BF16, bool RELU2, bool MAP>
+__global__ void __launch_bounds__(kThreads, BF16 && !RELU2 ? 3 : 2)
+quantize_blocks_kernel(const void *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
+                       int64_t cols, int row_tiles, int chunks, uint8_t *__restrict__ codes,
+                       uint8_t *__restrict__ scales) {
+    using T = typename std::conditional<BF16, uint16_t, float>::type;
+    constexpr int kParts = 4;                    // Octs of a block
+    constexpr int kRows = BF16 ? 2 : 1;          // rows in flight
+    griddep_enter();
+    const int lane = threadIdx.x & 31;
+    const int64_t ld = fp4_row_bytes(cols);
+    const int col_tiles = chunks * 2;
+    const int tile = static_cast<int>(blockIdx.x >> 2);  // of the whole batch
+    const int mat = tile / row_tiles;
+    const int rr = static_cast<int>(blockIdx.x & 3) * 8 + (threadIdx.x >> 5);
+    const int64_t r0 = static_cast<int64_t>(tile - mat * row_tiles) * 128 + rr;
+    int64_t src[4];  // source rows, -1: zeros
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t r = r0 + 32 * j;
+        src[j] = r < rows ? r : -1;
+        if (MAP && r < rows) src[j] = source_row(row_map, map_div, r);
+    }
+    const T *base = static_cast<const T *>(x) + static_cast<int64_t>(mat) * rows * cols;
+    uint8_t *out = codes + (mat * rows + r0) * ld;
+    uint8_t *st = scales + static_cast<int64_t>(tile) * col_tiles * 512 + rr * 16 + (lane & 3) * 4;
+    for (int64_t blk = static_cast<int64_t>(blockIdx.y) * 32 + lane; blk - lane < col_tiles * 4;
+         blk += static_cast<int64_t>(gridDim.y) * 32) {
+        const int64_t c = blk * 32;
+        uint32_t bytes = 0;  // of the four rows
+#pragma unroll
+        for (int j0 = 0; j0 < 4; j0 += kRows) {
+            Oct<BF16> o[kRows][kParts];
+#pragma unroll
+            for (int u = 0; u < kRows; ++u)
+#pragma unroll
+                for (int q = 0; q < kParts; ++q) {
+                    if (src[j0 + u] >= 0) o[u][q].load(base + src[j0 + u] * cols, c + 8 * q, cols);
+                    else o[u][q].zero();
+                }
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const int j = j0 + u;
+                const bool row = r0 + 32 * j < rows && c < 2 * ld;
+                if (src[j] < 0) {  // a row of zeros, or none
+                    if (row) *reinterpret_cast<uint4 *>(out + 32 * j * ld + c / 2) = make_uint4(0u, 0u, 0u, 0u);
+                    continue;
+                }
+                typename Oct<BF16>::Max top = Oct<BF16>::kNone;
+#pragma unroll
+                for (int q = 0; q < kParts; ++q) o[u][q].template top<RELU2>(top);
+                const uint32_t sb = scale_byte(top_bits<RELU2>(top));
+                const float inv = scale_inverse(sb);
+                uint32_t w[kParts];
+#pragma unroll
+                for (int q = 0; q < kParts; ++q) {
+                    float v[8];
+                    o[u][q].template scaled<RELU2>(inv, v);
+                    w[q] = sb == 255u ? 0u : e2m1x8<RELU2>(v);
+                }
+                if (row) *reinterpret_cast<uint4 *>(out + 32 * j * ld + c / 2) = make_uint4(w[0], w[1], w[2], w[3]);
+                bytes |= sb << (8 * j);
+            }
+        }
+        // byte j of lane b -> byte b of lane j, within four lanes
+        uint32_t t = __shfl_xor_sync(0xffffffffu, bytes, 1);
+        bytes = (lane & 1) ? __byte_perm(bytes, t, 0x3715) : __byte_perm(bytes, t, 0x6240);
+        t = __shfl_xor_sync(0xffffffffu, bytes, 2);
+        bytes = (lane & 2) ? __byte_perm(bytes, t, 0x3276) : __byte_perm(bytes, t, 0x5410);
+        if (blk < col_tiles * 4) *reinterpret_cast<uint32_t *>(st + (blk >> 2) * 512) = bytes;
     }
 }
 
@@ -314,23 +421,22 @@ struct Pair<false> {
 // The two columns' blocks of 32 values: their codes and scale bytes.
 template <bool BF16, bool RELU2>
 __device__ __forceinline__ void quantize_pairs(const Pair<BF16> (&p)[32], uint4 &qa, uint4 &qb, uint32_t &sa, uint32_t &sb) {
-    uint32_t ta, tb;  // bits of the columns' max |v|
-    if constexpr (BF16 && !RELU2) {
+    uint32_t ta, tb;  // bits of the columns' largest |v|, or squared
+    if constexpr (BF16) {
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) m = max_abs_bf16x2(m, p[i].w);
-        m &= 0x7FFF7FFFu;
-        ta = m << 16;
-        tb = m & 0xFFFF0000u;
+        for (int i = 0; i < 32; ++i) m = RELU2 ? max_signed_bf16x2(m, p[i].w) : max_abs_bf16x2(m, p[i].w);
+        ta = top_bits<RELU2>(bf16_lo(RELU2 ? m : m & 0x7FFF7FFFu));
+        tb = top_bits<RELU2>(bf16_hi(RELU2 ? m : m & 0x7FFF7FFFu));
     } else {
         float ma = 0.0f, mb = 0.0f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            ma = max_abs(ma, RELU2 ? relu2(p[i].lo()) : p[i].lo());
-            mb = max_abs(mb, RELU2 ? relu2(p[i].hi()) : p[i].hi());
+            ma = RELU2 ? max_signed(ma, p[i].lo()) : max_abs(ma, p[i].lo());
+            mb = RELU2 ? max_signed(mb, p[i].hi()) : max_abs(mb, p[i].hi());
         }
-        ta = __float_as_uint(ma);
-        tb = __float_as_uint(mb);
+        ta = top_bits<RELU2>(ma);
+        tb = top_bits<RELU2>(mb);
     }
     sa = scale_byte(ta);
     sb = scale_byte(tb);
@@ -346,12 +452,13 @@ __device__ __forceinline__ void quantize_pairs(const Pair<BF16> (&p)[32], uint4 
                 va[i] = bf16_lo(u);
                 vb[i] = bf16_hi(u);
             } else {
-                va[i] = (RELU2 ? relu2(p[8 * g + i].lo()) : p[8 * g + i].lo()) * ia;
-                vb[i] = (RELU2 ? relu2(p[8 * g + i].hi()) : p[8 * g + i].hi()) * ib;
+                const float a = p[8 * g + i].lo(), b = p[8 * g + i].hi();
+                va[i] = (RELU2 ? a * fabsf(a) : a) * ia;
+                vb[i] = (RELU2 ? b * fabsf(b) : b) * ib;
             }
         }
-        wa[g] = sa == 255u ? 0u : e2m1x8(va);
-        wb[g] = sb == 255u ? 0u : e2m1x8(vb);
+        wa[g] = sa == 255u ? 0u : e2m1x8<RELU2>(va);
+        wb[g] = sb == 255u ? 0u : e2m1x8<RELU2>(vb);
     }
     qa = make_uint4(wa[0], wa[1], wa[2], wa[3]);
     qb = make_uint4(wb[0], wb[1], wb[2], wb[3]);
@@ -365,7 +472,8 @@ __device__ __forceinline__ void quantize_pairs(const Pair<BF16> (&p)[32], uint4 
 constexpr int kTCols = 64;              // x's columns of a CTA (Q's rows)
 constexpr int kTPitch = 128 + 16;       // bytes of a Q row in shared memory
 
-template <bool BF16, bool VEC, bool RELU2, bool MAP>
+// MAP: 0 no row map, 1 a map that only says which rows are live, 2 one that gathers.
+template <bool BF16, bool VEC, bool RELU2, int MAP>
 __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2)
 quantize_cols_kernel(const void *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
                      int64_t cols, int row_tiles, int chunks, uint8_t *__restrict__ codes,
@@ -385,13 +493,27 @@ quantize_cols_kernel(const void *__restrict__ x, const int *__restrict__ row_map
     for (int chunk = blockIdx.y; chunk < chunks; chunk += gridDim.y) {
         const int64_t c0 = static_cast<int64_t>(chunk) * 256 + wid * 32;  // Q's first column of this warp: x's row
         Pair<BF16> p[32];
-        if (MAP) {
+        if (MAP == 2) {
             const int64_t own = c0 + lane;
             const int mine = own < cols ? source_row(row_map, map_div, own) : -1;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
                 const int src = __shfl_sync(0xffffffffu, mine, i);
                 p[i].template load<VEC>(base + (src < 0 ? 0 : src) * rows, src < 0 ? rows : col, rows);
+            }
+        } else if (MAP == 1) {
+            const int64_t own = c0 + lane;
+            const unsigned live = __ballot_sync(0xffffffffu, own < cols && row_map[own < cols ? own : 0] >= 0);
+            const T *row = base + c0 * rows;
+            if (live == 0xffffffffu) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i, row += rows) p[i].template load<VEC>(row, col, rows);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const bool in = live >> i & 1u;
+                    p[i].template load<VEC>(in ? row + i * rows : base, in ? col : rows, rows);
+                }
             }
         } else if (c0 + 32 <= cols) {
             const T *row = base + c0 * rows;
@@ -560,7 +682,7 @@ dim3 grid_for(int64_t x, int64_t most) {
     return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y < 1 ? 1 : y));
 }
 
-template <bool BF16, bool RELU2, bool MAP>
+template <bool BF16, bool RELU2, int MAP>
 int quantize_typed(const void *x, const int *row_map, int map_div, int64_t rows, int64_t cols, int batch,
                    bool transposed, uint8_t *codes, uint8_t *scales, cudaStream_t s) {
     const int row_tiles = static_cast<int>((rows + 127) / 128), chunks = static_cast<int>((cols + 255) / 256);
@@ -569,8 +691,12 @@ int quantize_typed(const void *x, const int *row_map, int map_div, int64_t rows,
         return launch_pdl(kern, grid_for(static_cast<int64_t>(row_tiles) * 2 * batch, chunks), dim3(kThreads), 0, s, x,
                           row_map, map_div, rows, cols, row_tiles, chunks, codes, scales);
     }
-    auto kern = cols * (BF16 ? 2 : 4) % 16 == 0 ? quantize_rows_kernel<BF16, true, RELU2, MAP>
-                                                : quantize_rows_kernel<BF16, false, RELU2, MAP>;
+    if (cols * (BF16 ? 2 : 4) % 16 == 0 && cols >= 1024)
+        return launch_pdl(quantize_blocks_kernel<BF16, RELU2, MAP != 0>,
+                          grid_for(static_cast<int64_t>(row_tiles) * 4 * batch, (chunks + 3) / 4), dim3(kThreads), 0, s, x, row_map,
+                          map_div, rows, cols, row_tiles, chunks, codes, scales);
+    auto kern = cols * (BF16 ? 2 : 4) % 16 == 0 ? quantize_rows_kernel<BF16, true, RELU2, MAP != 0>
+                                                : quantize_rows_kernel<BF16, false, RELU2, MAP != 0>;
     return launch_pdl(kern, grid_for(static_cast<int64_t>(row_tiles) * 4 * batch, chunks), dim3(kThreads), 0, s, x,
                       row_map, map_div, rows, cols, row_tiles, chunks, codes, scales);
 }
@@ -579,12 +705,15 @@ template <bool BF16>
 int quantize_dtype(const void *x, const int *row_map, int map_div, int64_t rows, int64_t cols, int batch,
                    bool transposed, bool relu2, uint8_t *codes, uint8_t *scales, cudaStream_t s) {
 #define MLPBLK_Q(R, M) return quantize_typed<BF16, R, M>(x, row_map, map_div, rows, cols, batch, transposed, codes, scales, s)
-    if (relu2) {
-        if (row_map) MLPBLK_Q(true, true);
-        MLPBLK_Q(true, false);
+#define MLPBLK_QM(R)                          \
+    {                                         \
+        if (!row_map) MLPBLK_Q(R, 0);         \
+        if (map_div == 0) MLPBLK_Q(R, 1);     \
+        MLPBLK_Q(R, 2);                       \
     }
-    if (row_map) MLPBLK_Q(false, true);
-    MLPBLK_Q(false, false);
+    if (relu2) MLPBLK_QM(true)
+    MLPBLK_QM(false)
+#undef MLPBLK_QM
 #undef MLPBLK_Q
 }
 

@@ -36,47 +36,77 @@ __device__ __forceinline__ int ld_cluster(const int *local, unsigned rank) {
 
 // One cluster makes the whole plan in one launch: CTA c of C takes a contiguous
 // range of the entries, warp w a contiguous part of that, so ranks follow entry
-// order.  Pass 1 counts per warp and expert (lanes with the same expert find each
-// other by match_any); the counts' prefixes run over warps in shared memory and over
-// the CTAs through distributed shared memory; pass 2 reads the ids again (from L1 or
-// L2) and places.  Bound by latency: two passes and two cluster barriers.
+// order.  A warp walks its part once: lanes with the same expert find each other by
+// match_any and take the next ranks within the warp.  The counts' prefixes then run over
+// the warps (a lane a warp) and over the CTAs through distributed shared memory, and an
+// entry's row is its expert's first row, plus the entries before its CTA, its warp,
+// and itself.  An entry's expert and rank stay in a register for parts of up to
+// 32 * kSortKeep entries; longer parts leave the rank in pos and read the id again.
+// Bound by latency: one pass over the ids, two cluster barriers.
+constexpr int kSortKeep = 16;
+
 __global__ void __launch_bounds__(kSortThreads)
 sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_t R, int64_t per_warp,
             int *__restrict__ count, int *__restrict__ seg, int *__restrict__ pos, int *__restrict__ row_map) {
-    __shared__ int wcnt[kSortWarps][kSortExperts];
+    __shared__ int wcnt[kSortExperts][kSortWarps + 1];  // entries of an expert in a warp, then in the warps before it
     __shared__ int ctot[kSortExperts];       // this CTA's entries per expert (read by the cluster)
     __shared__ int segs[kSortExperts + 1];
+    __shared__ int first[kSortExperts];      // the row of this CTA's first entry of an expert
     __shared__ int live[kSortExperts];       // every CTA's entries per expert
     __shared__ int scan[kSortExperts / 32];
-    griddep_enter();
+    griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int C = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
     const unsigned lt = (1u << lane) - 1u;
-    // warps of this CTA that have entries
-    const int64_t left = n - static_cast<int64_t>(c) * kSortWarps * per_warp;
-    const int nw = left <= 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(kSortWarps), (left + per_warp - 1) / per_warp));
+    for (int e = lane; e < experts; e += 32) wcnt[e][wid] = 0;
+    __syncwarp();
     const int64_t w0 = (static_cast<int64_t>(c) * kSortWarps + wid) * per_warp;
     const int64_t w1 = min(n, w0 + per_warp);
-    if (wid < nw)
-        for (int e = lane; e < kSortExperts; e += 32) wcnt[wid][e] = 0;
-    __syncwarp();
-    for (int64_t g = w0; g < w1; g += 32) {
-        const int64_t i = g + lane;
-        int e = i < w1 ? idx[i] : -1;
-        if (e < 0 || e >= experts) e = -1;
+    const bool keep = per_warp <= 32 * kSortKeep;
+    uint32_t kept[kSortKeep];  // rank in the warp << 9 | expert (511: none)
+    griddep_wait();
+    // the next rank of expert e within the warp, for the 32 lanes' entries in order
+    auto rank_of = [&](int e) {
         const unsigned peers = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && (peers & lt) == 0) wcnt[wid][e] += __popc(peers);
+        const int base = e >= 0 ? wcnt[e][wid] : 0;
         __syncwarp();
+        if (e >= 0 && (peers & lt) == 0) wcnt[e][wid] = base + __popc(peers);
+        __syncwarp();
+        return base + __popc(peers & lt);
+    };
+    auto valid = [&](int e) { return e >= 0 && e < experts ? e : -1; };
+    if (keep) {
+#pragma unroll
+        for (int g = 0; g < kSortKeep; ++g) {
+            const int64_t i = w0 + 32 * g + lane;
+            kept[g] = static_cast<uint32_t>(i < w1 ? valid(idx[i]) : -1);
+        }
+#pragma unroll
+        for (int g = 0; g < kSortKeep; ++g) {
+            if (w0 + 32 * g >= w1) break;
+            const int e = static_cast<int>(kept[g]);
+            const int r = rank_of(e);
+            kept[g] = (static_cast<uint32_t>(r) << 9) | (e < 0 ? 511u : static_cast<uint32_t>(e));
+        }
+    } else {
+        for (int64_t g = w0; g < w1; g += 32) {
+            const int64_t i = g + lane;
+            const int r = rank_of(i < w1 ? valid(idx[i]) : -1);
+            if (i < w1) pos[i] = r;
+        }
     }
     __syncthreads();
-    if (tid < kSortExperts) {
-        int run = 0;
-        for (int w = 0; w < nw; ++w) {
-            const int v = wcnt[w][tid];
-            wcnt[w][tid] = run;
-            run += v;
+    // the warps before each warp: warp w takes experts w, w + 32, ..., a lane a warp
+    for (int e = wid; e < experts; e += kSortWarps) {
+        const int own = wcnt[e][lane];
+        int incl = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
         }
-        ctot[tid] = run;
+        wcnt[e][lane] = incl - own;
+        if (lane == 31) ctot[e] = incl;
     }
     if (C > 1) {
         cluster_arrive();
@@ -86,15 +116,17 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
     }
     int before = 0, all = 0, padded = 0, incl = 0;
     if (tid < kSortExperts) {
-        if (C > 1) {
+        if (tid < experts) {
+            if (C > 1) {
 #pragma unroll
-            for (int r = 0; r < kSortCluster; ++r) {
-                const int v = r < C ? ld_cluster(&ctot[tid], r) : 0;
-                before += r < c ? v : 0;
-                all += v;
+                for (int r = 0; r < kSortCluster; ++r) {
+                    const int v = r < C ? ld_cluster(&ctot[tid], r) : 0;
+                    before += r < c ? v : 0;
+                    all += v;
+                }
+            } else {
+                all = ctot[tid];
             }
-        } else {
-            all = ctot[tid];
         }
         live[tid] = all;
         padded = (all + pad - 1) / pad * pad;
@@ -110,31 +142,31 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
     __syncthreads();
     if (tid < kSortExperts) {
         int off = 0;
-        for (int w = 0; w < wid; ++w) off += scan[w];
+#pragma unroll
+        for (int w = 0; w < kSortExperts / 32; ++w) off += w < wid ? scan[w] : 0;
         segs[tid + 1] = off + incl;
         if (tid == 0) segs[0] = 0;
-        // the first row of each warp's entries
-        for (int w = 0; w < nw; ++w) wcnt[w][tid] += off + incl - padded + before;
+        first[tid] = off + incl - padded + before;
     }
     __syncthreads();
     if (c == 0) {
         if (tid < experts) count[tid] = live[tid];
         if (tid <= experts) seg[tid] = segs[tid];
     }
-    for (int64_t g = w0; g < w1; g += 32) {
-        const int64_t i = g + lane;
-        int e = i < w1 ? idx[i] : -1;
-        if (e < 0 || e >= experts) e = -1;
-        const unsigned peers = __match_any_sync(0xffffffffu, e);
-        const int base = e >= 0 ? wcnt[wid][e] : 0;
-        __syncwarp();
-        if (e >= 0 && (peers & lt) == 0) wcnt[wid][e] = base + __popc(peers);
-        __syncwarp();
-        if (i < w1) {
-            const int p = e < 0 ? -1 : base + __popc(peers & lt);
-            pos[i] = p;
-            if (p >= 0) row_map[p] = static_cast<int>(i);
+    auto place = [&](int64_t i, int e, int r) {
+        const int p = e < 0 ? -1 : first[e] + wcnt[e][wid] + r;
+        pos[i] = p;
+        if (p >= 0) row_map[p] = static_cast<int>(i);
+    };
+    if (keep) {
+#pragma unroll
+        for (int g = 0; g < kSortKeep; ++g) {
+            const int64_t i = w0 + 32 * g + lane;
+            const uint32_t e = kept[g] & 511u;
+            if (i < w1) place(i, e == 511u ? -1 : static_cast<int>(e), static_cast<int>(kept[g] >> 9));
         }
+    } else {
+        for (int64_t i = w0 + lane; i < w1; i += 32) place(i, valid(idx[i]), pos[i]);
     }
     // rows without an entry: the segments' padding and what lies behind them
     if (pad > 1)
@@ -148,12 +180,18 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
 // ------------------------------------------------------------------ the moves
 
 // A row is `units` accesses of type U (16, 4 or 2 bytes: the widest that divides
-// a row).  blockDim = (threads of a row, rows of a block); a thread holds kPer units
-// at a time, so a row of 4096 bf16 values is four 16-byte accesses for each of 128
-// threads.
+// a row), a CTA kMoveThreads / TX rows of TX threads.  A thread holds several accesses
+// at a time, TX apart: enough bytes in flight where they are short.  TX is a constant,
+// so a row's addresses are one pointer and immediate offsets (the plan, both moves and
+// both gradients of 4097 x 1001 float32, top-6: 140 us with 64-bit indices throughout, 122
+// so; 16384 x 4096 bf16, top-2: 342 and 325).
 constexpr int kMoveThreads = 256;
-constexpr int kPer = 4;      // permute, unpermute
-constexpr int kPerBwd = 2;   // unpermute's gradient (16384 x 4096, top-2: 105 us; 114 with 4)
+template <class U>
+constexpr int kPerOf = sizeof(U) == 16 ? 4 : 8;      // permute, unpermute
+template <class U>
+constexpr int kSlotsOf = sizeof(U) == 16 ? 2 : 4;    // slots whose rows the gradient loads together
+template <class U>
+constexpr int kPerBwdOf = sizeof(U) == 16 ? 2 : 4;   // unpermute's gradient (16384 x 4096 bf16, top-2: 98 us)
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
@@ -227,84 +265,85 @@ __device__ __forceinline__ U zero_unit() {
 
 // Padding row number q of the plan (q / pad = expert, q % pad = which): its row, or -1.
 __device__ __forceinline__ int64_t padding_row(int64_t q, int pad, int experts, const int *count, const int *seg) {
-    const int64_t e = q / pad;
+    const int e = static_cast<int>(q / pad);
     if (e >= experts) return -1;
     const int64_t r = static_cast<int64_t>(seg[e]) + count[e] + q % pad;
     return r < seg[e + 1] ? r : -1;
 }
 
-template <class U>
-__device__ __forceinline__ void zero_row(U *row, int64_t units) {
-    for (int64_t c = threadIdx.x; c < units; c += blockDim.x) row[c] = zero_unit<U>();
+template <int TX, class U>
+__device__ __forceinline__ void zero_row(U *row, int units) {
+    for (int c = threadIdx.x; c < units; c += TX) row[c] = zero_unit<U>();
 }
 
 // rows[pos[t,j]] = x[t]; the blocks behind the tokens' zero the padding rows.
-template <class U>
+template <int TX, class U>
 __global__ void __launch_bounds__(kMoveThreads)
 permute_kernel(const U *__restrict__ x, const int *__restrict__ pos, const int *__restrict__ count,
-               const int *__restrict__ seg, int64_t T, int k, int experts, int pad, int64_t units, int64_t token_blocks,
+               const int *__restrict__ seg, int64_t T, int k, int experts, int pad, int units, int64_t token_blocks,
                U *__restrict__ rows) {
+    constexpr int kPer = kPerOf<U>;
     griddep_enter();
     const int64_t b = blockIdx.x;
     if (b >= token_blocks) {
         const int64_t r = padding_row((b - token_blocks) * blockDim.y + threadIdx.y, pad, experts, count, seg);
-        if (r >= 0) zero_row(rows + r * units, units);
+        if (r >= 0) zero_row<TX>(rows + r * units, units);
         return;
     }
     const int64_t t = b * blockDim.y + threadIdx.y;
     if (t >= T) return;
-    const U *src = x + t * units;
     const int *pt = pos + t * k;
-    for (int64_t c0 = threadIdx.x; c0 < units; c0 += kPer * blockDim.x) {
+    for (int c = threadIdx.x; c < units; c += kPer * TX) {
+        const U *src = x + t * units + c;
         U v[kPer];
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int64_t c = c0 + u * blockDim.x;
-            v[u] = c < units ? __ldg(src + c) : zero_unit<U>();
-        }
+        for (int u = 0; u < kPer; ++u) v[u] = c + u * TX < units ? __ldg(src + u * TX) : zero_unit<U>();
         for (int j = 0; j < k; ++j) {
             const int64_t r = pt[j];
             if (r < 0) continue;
+            U *dst = rows + r * units + c;
 #pragma unroll
-            for (int u = 0; u < kPer; ++u) {
-                const int64_t c = c0 + u * blockDim.x;
-                if (c < units) rows[r * units + c] = v[u];
-            }
+            for (int u = 0; u < kPer; ++u)
+                if (c + u * TX < units) dst[u * TX] = v[u];
         }
     }
 }
 
 // y[t] = residual[t] + sum_j w[t,j] * rows[pos[t,j]], slot order, float32, rounded
 // once.  Two slots' rows are loaded together, so that a thread has 3 * kPer accesses
-// in flight.  residual and y may be the same array: an element is read and written
-// by the same thread.
-template <class U, bool BF16>
+// in flight (four slots' at a time take it to one CTA an SM: 90 -> 153 us at 16384 x
+// 4096 bf16, top-2; rows that arrive by bulk copies in a ring of shared-memory stages
+// were no faster there, 91 us, and half as fast on 1001-float rows).
+// residual and y may be the same array: an element is read and written by the same
+// thread.
+template <int TX, class U, bool BF16>
 __global__ void __launch_bounds__(kMoveThreads)
 unpermute_kernel(const U *__restrict__ rows, const int *__restrict__ pos, const float *__restrict__ weights,
-                 const U *residual, int64_t T, int k, int64_t units, U *y) {
+                 const U *residual, int64_t T, int k, int units, U *y) {
     using V = Vals<U, BF16>;
+    constexpr int kPer = kPerOf<U>;
     griddep_enter();
     const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (t >= T) return;
     const int *pt = pos + t * k;
-    for (int64_t c0 = threadIdx.x; c0 < units; c0 += kPer * blockDim.x) {
+    const float *wt = weights + t * k;
+    for (int c = threadIdx.x; c < units; c += kPer * TX) {
         float acc[kPer][V::N];
         U res[kPer];
+        const U *rp = residual + t * units + c;
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int64_t c = c0 + u * blockDim.x;
-            res[u] = residual && c < units ? residual[t * units + c] : zero_unit<U>();
-        }
+        for (int u = 0; u < kPer; ++u) res[u] = residual && c + u * TX < units ? rp[u * TX] : zero_unit<U>();
         for (int j = 0; j < k; j += 2) {
-            const int64_t ra = pt[j], rb = j + 1 < k ? pt[j + 1] : -1;
-            const float wa = weights ? weights[t * k + j] : 1.0f;
-            const float wb = weights && j + 1 < k ? weights[t * k + j + 1] : 1.0f;
+            const int ra = pt[j], rb = j + 1 < k ? pt[j + 1] : -1;
+            const float wa = weights ? wt[j] : 1.0f;
+            const float wb = weights && j + 1 < k ? wt[j + 1] : 1.0f;
+            const U *pa = rows + static_cast<int64_t>(ra < 0 ? 0 : ra) * units + c;
+            const U *pb = rows + static_cast<int64_t>(rb < 0 ? 0 : rb) * units + c;
             U oa[kPer], ob[kPer];
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
-                const int64_t c = c0 + u * blockDim.x;
-                oa[u] = c < units && ra >= 0 ? __ldg(rows + ra * units + c) : zero_unit<U>();
-                ob[u] = c < units && rb >= 0 ? __ldg(rows + rb * units + c) : zero_unit<U>();
+                oa[u] = c + u * TX < units && ra >= 0 ? __ldg(pa + u * TX) : zero_unit<U>();
+                ob[u] = c + u * TX < units && rb >= 0 ? __ldg(pb + u * TX) : zero_unit<U>();
             }
             if (j == 0) {
 #pragma unroll
@@ -329,42 +368,40 @@ unpermute_kernel(const U *__restrict__ rows, const int *__restrict__ pos, const 
                 }
             }
         }
+        U *yp = y + t * units + c;
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int64_t c = c0 + u * blockDim.x;
-            if (c < units) y[t * units + c] = V::put(acc[u]);
-        }
+        for (int u = 0; u < kPer; ++u)
+            if (c + u * TX < units) yp[u * TX] = V::put(acc[u]);
     }
 }
 
-// d_rows[pos[t,j]] = w[t,j] * dy[t] and dw[t,j] = <dy[t], rows[pos[t,j]]>.  Slots go
-// in pairs whose rows are loaded together with dy; a dot product is summed over the
-// row's threads by shuffles, then over its warps in warp order.  d_weights NULL skips
-// the products and rows.
-constexpr int kSlots = 2;
-
-template <class U, bool BF16>
+// d_rows[pos[t,j]] = w[t,j] * dy[t] and dw[t,j] = <dy[t], rows[pos[t,j]]>.  The rows of
+// kSlotsOf slots are loaded together with dy; a dot product is summed over the row's
+// threads by shuffles, then over its warps in warp order.  d_weights NULL skips the
+// products and rows.
+template <int TX, class U, bool BF16>
 __global__ void __launch_bounds__(kMoveThreads)
 unpermute_bwd_kernel(const U *__restrict__ dy, const U *__restrict__ rows, const int *__restrict__ pos,
                      const int *__restrict__ count, const int *__restrict__ seg, const float *__restrict__ weights,
-                     int64_t T, int k, int experts, int pad, int64_t units, int64_t token_blocks,
+                     int64_t T, int k, int experts, int pad, int units, int64_t token_blocks,
                      U *__restrict__ d_rows, float *__restrict__ d_weights) {
     using V = Vals<U, BF16>;
+    constexpr int kPerBwd = kPerBwdOf<U>, kSlots = kSlotsOf<U>;
+    constexpr int kWarps = TX / 32;  // of a row
     __shared__ float part[2][kSlots][kMoveThreads / 32];
     griddep_enter();
     const int64_t b = blockIdx.x;
     if (b >= token_blocks) {
         const int64_t r = padding_row((b - token_blocks) * blockDim.y + threadIdx.y, pad, experts, count, seg);
-        if (r >= 0) zero_row(d_rows + r * units, units);
+        if (r >= 0) zero_row<TX>(d_rows + r * units, units);
         return;
     }
     const int64_t t = b * blockDim.y + threadIdx.y;
     const bool in = t < T;
-    const int warps = blockDim.x / 32;  // of a row
-    const int w0 = threadIdx.y * warps;
+    const int w0 = threadIdx.y * kWarps;
     for (int j0 = 0; j0 < k; j0 += kSlots) {
         float s[kSlots];
-        int64_t r[kSlots];
+        int r[kSlots];
         float w[kSlots];
 #pragma unroll
         for (int j = 0; j < kSlots; ++j) {
@@ -373,33 +410,33 @@ unpermute_bwd_kernel(const U *__restrict__ dy, const U *__restrict__ rows, const
             r[j] = on ? pos[t * k + j0 + j] : -1;
             w[j] = on && weights ? weights[t * k + j0 + j] : 1.0f;
         }
-        for (int64_t c0 = threadIdx.x; in && c0 < units; c0 += kPerBwd * blockDim.x) {
+        for (int c = threadIdx.x; in && c < units; c += kPerBwd * TX) {
+            const U *gp = dy + t * units + c;
             U g[kPerBwd], o[kSlots][kPerBwd];
 #pragma unroll
-            for (int u = 0; u < kPerBwd; ++u) {
-                const int64_t c = c0 + u * blockDim.x;
-                g[u] = c < units ? __ldg(dy + t * units + c) : zero_unit<U>();
+            for (int u = 0; u < kPerBwd; ++u) g[u] = c + u * TX < units ? __ldg(gp + u * TX) : zero_unit<U>();
 #pragma unroll
-                for (int j = 0; j < kSlots; ++j)
-                    o[j][u] = d_weights && c < units && r[j] >= 0 ? __ldg(rows + r[j] * units + c) : zero_unit<U>();
+            for (int j = 0; j < kSlots; ++j) {
+                const U *rp = rows + static_cast<int64_t>(r[j] < 0 ? 0 : r[j]) * units + c;
+                const bool use = d_weights && r[j] >= 0;
+#pragma unroll
+                for (int u = 0; u < kPerBwd; ++u) o[j][u] = use && c + u * TX < units ? __ldg(rp + u * TX) : zero_unit<U>();
             }
 #pragma unroll
-            for (int u = 0; u < kPerBwd; ++u) {
-                const int64_t c = c0 + u * blockDim.x;
-                if (c >= units) continue;
-                float a[V::N];
-                V::get(g[u], a);
+            for (int j = 0; j < kSlots; ++j) {
+                if (r[j] < 0) continue;
+                U *dp = d_rows + static_cast<int64_t>(r[j]) * units + c;
 #pragma unroll
-                for (int j = 0; j < kSlots; ++j) {
-                    if (r[j] < 0) continue;
-                    float f[V::N];
+                for (int u = 0; u < kPerBwd; ++u) {
+                    float a[V::N], f[V::N];
+                    V::get(g[u], a);
                     V::get(o[j][u], f);
 #pragma unroll
                     for (int i = 0; i < V::N; ++i) {
                         s[j] += a[i] * f[i];
                         f[i] = a[i] * w[j];
                     }
-                    d_rows[r[j] * units + c] = V::put(f);
+                    if (c + u * TX < units) dp[u * TX] = V::put(f);
                 }
             }
         }
@@ -411,10 +448,11 @@ unpermute_bwd_kernel(const U *__restrict__ dy, const U *__restrict__ rows, const
             for (int o = 16; o > 0; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
             if ((threadIdx.x & 31) == 0) part[buf][j][w0 + threadIdx.x / 32] = s[j];
         }
-        __syncthreads();  // one barrier a pair of slots: the next pair writes the other half of `part`
+        __syncthreads();  // one barrier a group of slots: the next group writes the other half of `part`
         if (in && threadIdx.x < kSlots && j0 + threadIdx.x < k) {
             float d = 0.0f;
-            for (int q = 0; q < warps; ++q) d += part[buf][threadIdx.x][w0 + q];
+#pragma unroll
+            for (int q = 0; q < kWarps; ++q) d += part[buf][threadIdx.x][w0 + q];
             d_weights[t * k + j0 + threadIdx.x] = d;
         }
     }
@@ -422,20 +460,19 @@ unpermute_bwd_kernel(const U *__restrict__ dy, const U *__restrict__ rows, const
 
 // The shape of a move: bytes of an access, accesses of a row, threads of a row.
 struct MoveShape {
-    int unit;
-    int64_t units;
+    int unit, units;
+    int tx;
     dim3 block;
     int64_t token_blocks, pad_blocks;
 };
 
-MoveShape move_shape(int64_t T, int64_t width, int dtype, int experts, int pad, int per) {
+MoveShape move_shape(int64_t T, int64_t width, int dtype, int experts, int pad, int per16, int per) {
     MoveShape m;
     const int64_t bytes = width * (dtype == MLPBLK_BF16 ? 2 : 4);
     m.unit = bytes % 16 == 0 ? 16 : (bytes % 4 == 0 ? 4 : 2);
-    m.units = bytes / m.unit;
-    unsigned tx = 32;
-    while (tx < static_cast<unsigned>(kMoveThreads) && tx * per < m.units) tx *= 2;
-    m.block = dim3(tx, kMoveThreads / tx, 1);
+    m.units = static_cast<int>(bytes / m.unit);
+    m.tx = m.units <= 32 * (m.unit == 16 ? per16 : per) ? 32 : 128;
+    m.block = dim3(m.tx, kMoveThreads / m.tx, 1);
     m.token_blocks = (T + m.block.y - 1) / m.block.y;
     m.pad_blocks = pad > 1 ? (static_cast<int64_t>(experts) * pad + m.block.y - 1) / m.block.y : 0;
     return m;
@@ -466,10 +503,10 @@ int launch_sort(const int *idx, int64_t n, int experts, int pad, int64_t R, int 
 
 int launch_permute(const void *x, const int *pos, const int *count, const int *seg, int64_t T, int64_t width,
                    int dtype, int k, int experts, int pad, void *rows, cudaStream_t s) {
-    const MoveShape m = move_shape(T, width, dtype, experts, pad, kPer);
+    const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerOf<uint4>, kPerOf<uint32_t>);
     const dim3 grid(static_cast<unsigned>(m.token_blocks + m.pad_blocks));
 #define MLPBLK_PERMUTE(U)                                                                                      \
-    return launch_pdl(permute_kernel<U>, grid, m.block, 0, s, static_cast<const U *>(x), pos, count, seg, T, k, \
+    return launch_pdl(m.tx == 32 ? permute_kernel<32, U> : permute_kernel<128, U>, grid, m.block, 0, s, static_cast<const U *>(x), pos, count, seg, T, k, \
                       experts, pad, m.units, m.token_blocks, static_cast<U *>(rows))
     if (m.unit == 16) MLPBLK_PERMUTE(uint4);
     if (m.unit == 4) MLPBLK_PERMUTE(uint32_t);
@@ -479,10 +516,10 @@ int launch_permute(const void *x, const int *pos, const int *count, const int *s
 
 int launch_unpermute(const void *rows, const int *pos, const float *weights, const void *residual, int64_t T,
                      int64_t width, int dtype, int k, void *y, cudaStream_t s) {
-    const MoveShape m = move_shape(T, width, dtype, 1, 1, kPer);
+    const MoveShape m = move_shape(T, width, dtype, 1, 1, kPerOf<uint4>, kPerOf<uint32_t>);
     const dim3 grid(static_cast<unsigned>(m.token_blocks));
 #define MLPBLK_UNPERMUTE(U, B)                                                                              \
-    return launch_pdl(unpermute_kernel<U, B>, grid, m.block, 0, s, static_cast<const U *>(rows), pos, weights, \
+    return launch_pdl(m.tx == 32 ? unpermute_kernel<32, U, B> : unpermute_kernel<128, U, B>, grid, m.block, 0, s, static_cast<const U *>(rows), pos, weights, \
                       static_cast<const U *>(residual), T, k, m.units, static_cast<U *>(y))
     if (dtype == MLPBLK_BF16) {
         if (m.unit == 16) MLPBLK_UNPERMUTE(uint4, true);
@@ -497,10 +534,10 @@ int launch_unpermute(const void *rows, const int *pos, const float *weights, con
 int launch_unpermute_bwd(const void *dy, const void *rows, const int *pos, const int *count, const int *seg,
                          const float *weights, int64_t T, int64_t width, int dtype, int k, int experts, int pad,
                          void *d_rows, float *d_weights, cudaStream_t s) {
-    const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerBwd);
+    const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerBwdOf<uint4>, kPerBwdOf<uint32_t>);
     const dim3 grid(static_cast<unsigned>(m.token_blocks + m.pad_blocks));
 #define MLPBLK_UNPERMUTE_BWD(U, B)                                                                               \
-    return launch_pdl(unpermute_bwd_kernel<U, B>, grid, m.block, 0, s, static_cast<const U *>(dy),                 \
+    return launch_pdl(m.tx == 32 ? unpermute_bwd_kernel<32, U, B> : unpermute_bwd_kernel<128, U, B>, grid, m.block, 0, s, static_cast<const U *>(dy),                 \
                       static_cast<const U *>(rows), pos, count, seg, weights, T, k, experts, pad, m.units,        \
                       m.token_blocks, static_cast<U *>(d_rows), d_weights)
     if (dtype == MLPBLK_BF16) {

@@ -103,7 +103,7 @@ def _addresses(n):
 
 
 @pytest.mark.parametrize("kw", [dict(tokens=-1), dict(width=0), dict(experts=0), dict(experts=257), dict(top_k=0),
-                                dict(top_k=257), dict(pad=0), dict(pad=1025), dict(tokens=1 << 31)])
+                                dict(top_k=257), dict(pad=0), dict(pad=1025), dict(tokens=1 << 31), dict(width=1 << 30)])
 def test_sort_desc_refusals(mb, kw):
     base = dict(tokens=10, width=64, experts=4, top_k=2, pad=128)
     assert mb.mlpblk_moe_sort_rows(mb.make_sort_desc(**base)) == sort.rows_bound(10, 2, 4, 128)
