@@ -300,13 +300,13 @@ quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map
     }
 }
 
-// Blocks along the source's rows, rows of 1024 columns and more in 16-byte accesses: a
+// Blocks along the source's rows, rows of 768 columns and more in 16-byte accesses: a
 // lane holds a whole block (its 16-byte loads 64 or 128 bytes from its neighbour's; the
 // sectors' other halves come from L1), so a block's maximum needs no shuffle and its
 // codes are one 16-byte store.  A warp takes 1024 columns of the rows r, r + 32, r + 64,
 // r + 96 of a scale tile, two rows in flight; four lanes then transpose their 4 x 4
 // scale bytes and store 16 consecutive bytes of a tile.  8192 x 16384 bf16: 61 us with the
-// kernel above, 56 with this one (6.06 TB/s).
+// kernel above, 56 with this one (6.06 TB/s); below 24 blocks a row too many lanes idle.
 template <bool BF16, bool RELU2, bool MAP>
 __global__ void __launch_bounds__(kThreads, BF16 && !RELU2 ? 3 : 2)
 quantize_blocks_kernel(const void *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
@@ -576,23 +576,6 @@ __device__ __forceinline__ void decode8(uint32_t u, float scale, float (&v)[8]) 
     }
 }
 
-// The value of the code in the lowest four bits.
-__device__ __forceinline__ float decode1(uint32_t u) {
-    float f;
-    asm("{\n"
-        "  .reg .b8 a, b, c, d;\n"
-        "  .reg .b32 h;\n"
-        "  .reg .f16 l, m;\n"
-        "  mov.b32 {a, b, c, d}, %1;\n"
-        "  cvt.rn.f16x2.e2m1x2 h, a;\n"
-        "  mov.b32 {l, m}, h;\n"
-        "  cvt.f32.f16 %0, l;\n"
-        "}\n"
-        : "=f"(f)
-        : "r"(u));
-    return f;
-}
-
 __device__ __forceinline__ float scale_value(uint32_t byte) {
     if (byte == 255u) return __uint_as_float(0x7FC00000u);
     return byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
@@ -613,6 +596,7 @@ __global__ void __launch_bounds__(kThreads)
 dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows, int64_t cols,
                   int64_t all_rows, int row_tiles, int chunks, void *__restrict__ y) {
     using T = typename std::conditional<BF16, uint16_t, float>::type;
+    __shared__ __align__(16) float turn[VEC ? 1 : kWarps][VEC ? 4 : 256];
     griddep_enter();
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
@@ -636,20 +620,26 @@ dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__
 #pragma unroll
         for (int j = 0; j < kDeqChunks; ++j) {
             const int64_t c = static_cast<int64_t>(g + j) * 256 + lane * 8;
+            if (g + j >= chunks) break;
             if (!VEC) {
-                // rows of any length: neighbouring lanes store neighbouring columns, whose
-                // codes and scales other lanes hold
-                const float sv = scale_value(sb[j]);
+                // rows of any length: through shared memory, so that neighbouring lanes
+                // store neighbouring columns
+                float v[8];
+                decode8(u[j], scale_value(sb[j]), v);
+                float *mine = &turn[VEC ? 0 : threadIdx.x >> 5][0];
+                *reinterpret_cast<float4 *>(mine + lane * 8) = make_float4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<float4 *>(mine + lane * 8 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                __syncwarp();
+                const int64_t c0 = static_cast<int64_t>(g + j) * 256 + lane;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int64_t ci = static_cast<int64_t>(g + j) * 256 + 32 * i + lane;
-                    const uint32_t word = __shfl_sync(0xffffffffu, u[j], 4 * i + (lane >> 3));
-                    const float f = decode1(word >> (4 * (lane & 7))) * __shfl_sync(0xffffffffu, sv, 4 * i);
-                    if (ci < cols) {
-                        if (BF16) reinterpret_cast<uint16_t *>(out)[ci] = static_cast<uint16_t>(pack2(f, 0.0f) & 0xFFFFu);
-                        else reinterpret_cast<float *>(out)[ci] = f;
+                    const float f = mine[32 * i + lane];
+                    if (c0 + 32 * i < cols) {
+                        if (BF16) reinterpret_cast<uint16_t *>(out)[c0 + 32 * i] = static_cast<uint16_t>(pack2(f, 0.0f) & 0xFFFFu);
+                        else reinterpret_cast<float *>(out)[c0 + 32 * i] = f;
                     }
                 }
+                __syncwarp();
                 continue;
             }
             if (c >= cols) continue;
@@ -691,7 +681,7 @@ int quantize_typed(const void *x, const int *row_map, int map_div, int64_t rows,
         return launch_pdl(kern, grid_for(static_cast<int64_t>(row_tiles) * 2 * batch, chunks), dim3(kThreads), 0, s, x,
                           row_map, map_div, rows, cols, row_tiles, chunks, codes, scales);
     }
-    if (cols * (BF16 ? 2 : 4) % 16 == 0 && cols >= 1024)
+    if (cols * (BF16 ? 2 : 4) % 16 == 0 && cols >= 768)
         return launch_pdl(quantize_blocks_kernel<BF16, RELU2, MAP != 0>,
                           grid_for(static_cast<int64_t>(row_tiles) * 4 * batch, (chunks + 3) / 4), dim3(kThreads), 0, s, x, row_map,
                           map_div, rows, cols, row_tiles, chunks, codes, scales);
