@@ -594,14 +594,14 @@ def mlpblk_moe_unpermute_backward(desc, dy, rows, pos, count, seg, weights, d_ro
 class _Kept:
     """Base of the classes that keep device buffers of their own: the buffers cannot
     be replaced, so their addresses are taken once and a call checks only what it is
-    given."""
+    given.  A call of these classes costs about 4 us of host time on a Grace core, 2.5 of
+    them in the library (launches included): the checks of the common case stand in
+    the methods themselves, _operand only words the refusal."""
 
-    def _device(self, where):
-        """The current device, which has to be the buffers' own."""
-        dev = _Torch.get().device()
+    def _where(self, dev, where):
+        """Refuses a call whose device is not the buffers' own."""
         if dev != self._dev:
             raise MlpBlkError(MLPBLK_EINVAL, f"{where}: the buffers are on cuda:{self._dev}, the call on cuda:{dev}")
-        return dev
 
 
 class MoeSort(_Kept):
@@ -632,43 +632,71 @@ class MoeSort(_Kept):
     pos = property(lambda self: self._pos)
     row_map = property(lambda self: self._row_map)
 
+    def _check_all(self, where, tensors):
+        """The addresses of (tensor or None, name, dtype, elements), or a refusal; then
+        the device, which is the tensors' own."""
+        t = _Torch.get()
+        dev = t.device()
+        if dev != self._dev:
+            self._where(dev, where)
+        out = []
+        for x, name, dt, n in tensors:
+            if x is None:
+                out.append(None)
+            elif x.dtype is dt and x.numel() >= n and x.get_device() == dev and x.is_contiguous():
+                out.append(x.data_ptr())
+            else:
+                out.append(_operand(x, where, name, dt, n, dev))
+        out.append(t.raw_stream(dev))
+        return out
+
     def sort(self, expert_idx, stream=None):
         where = "MoeSort.sort"
-        dev = self._device(where)
+        idx, st = self._check_all(where, ((expert_idx, "expert_idx", _Torch.get().int32, self._entries),))
         count, seg, pos, row_map = self._at
-        _check(lib.mlpblk_moe_sort(self._d, _operand(expert_idx, where, "expert_idx", _Torch.get().int32, self._entries, dev),
-                                   count, seg, pos, row_map, _stream(stream)), where)
+        rc = lib.mlpblk_moe_sort(self._d, idx, count, seg, pos, row_map, st if stream is None else _stream(stream))
+        if rc:
+            _check(rc, where)
 
     def permute(self, x, rows, stream=None):
         where = "MoeSort.permute"
-        dev, dt = self._device(where), self._type
+        dt = self._type
+        x, rows, st = self._check_all(where, ((x, "x", dt, self._x_n), (rows, "rows", dt, self._r_n)))
         count, seg, pos, _ = self._at
-        _check(lib.mlpblk_moe_permute(self._d, _operand(x, where, "x", dt, self._x_n, dev), pos, count, seg,
-                                      _operand(rows, where, "rows", dt, self._r_n, dev), _stream(stream)), where)
+        rc = lib.mlpblk_moe_permute(self._d, x, pos, count, seg, rows, st if stream is None else _stream(stream))
+        if rc:
+            _check(rc, where)
 
     def permute_backward(self, d_rows, dx, stream=None):
         where = "MoeSort.permute_backward"
-        dev, dt = self._device(where), self._type
-        _check(lib.mlpblk_moe_permute_backward(self._d, _operand(d_rows, where, "d_rows", dt, self._r_n, dev), self._at[2],
-                                               _operand(dx, where, "dx", dt, self._x_n, dev), _stream(stream)), where)
+        dt = self._type
+        d_rows, dx, st = self._check_all(where, ((d_rows, "d_rows", dt, self._r_n), (dx, "dx", dt, self._x_n)))
+        rc = lib.mlpblk_moe_permute_backward(self._d, d_rows, self._at[2], dx, st if stream is None else _stream(stream))
+        if rc:
+            _check(rc, where)
 
     def unpermute(self, rows, y, weights=None, residual=None, stream=None):
         where = "MoeSort.unpermute"
-        dev, dt = self._device(where), self._type
-        _check(lib.mlpblk_moe_unpermute(self._d, _operand(rows, where, "rows", dt, self._r_n, dev), self._at[2],
-                                        _operand(weights, where, "weights", _Torch.get().float32, self._entries, dev),
-                                        _operand(residual, where, "residual", dt, self._x_n, dev),
-                                        _operand(y, where, "y", dt, self._x_n, dev), _stream(stream)), where)
+        dt = self._type
+        rows, weights, residual, y, st = self._check_all(where, (
+            (rows, "rows", dt, self._r_n), (weights, "weights", _Torch.get().float32, self._entries),
+            (residual, "residual", dt, self._x_n), (y, "y", dt, self._x_n)))
+        rc = lib.mlpblk_moe_unpermute(self._d, rows, self._at[2], weights, residual, y,
+                                      st if stream is None else _stream(stream))
+        if rc:
+            _check(rc, where)
 
     def unpermute_backward(self, dy, rows, weights, d_rows, d_weights, stream=None):
         where = "MoeSort.unpermute_backward"
-        dev, dt, f32 = self._device(where), self._type, _Torch.get().float32
+        dt, f32 = self._type, _Torch.get().float32
+        dy, rows, weights, d_rows, d_weights, st = self._check_all(where, (
+            (dy, "dy", dt, self._x_n), (rows, "rows", dt, self._r_n), (weights, "weights", f32, self._entries),
+            (d_rows, "d_rows", dt, self._r_n), (d_weights, "d_weights", f32, self._entries)))
         count, seg, pos, _ = self._at
-        _check(lib.mlpblk_moe_unpermute_backward(
-            self._d, _operand(dy, where, "dy", dt, self._x_n, dev), _operand(rows, where, "rows", dt, self._r_n, dev),
-            pos, count, seg, _operand(weights, where, "weights", f32, self._entries, dev),
-            _operand(d_rows, where, "d_rows", dt, self._r_n, dev),
-            _operand(d_weights, where, "d_weights", f32, self._entries, dev), _stream(stream)), where)
+        rc = lib.mlpblk_moe_unpermute_backward(self._d, dy, rows, pos, count, seg, weights, d_rows, d_weights,
+                                               st if stream is None else _stream(stream))
+        if rc:
+            _check(rc, where)
 
 
 def make_fp4_desc(rows, cols, batch=1, dtype=MLPBLK_BF16, transposed=False, act=MLPBLK_FP4_ACT_NONE) -> Fp4Desc:
@@ -804,73 +832,102 @@ class Fp4Matrix(_Kept):
         MoeSort whose row_map says which source rows are live; gather=True reads
         them from x's tokens, otherwise x is already in sorted order."""
         where = "Fp4Matrix.quantize"
-        dev = self._device(where)
-        d = self._desc(x.dtype, transposed, act)
+        t = _Torch.get()
+        dev = t.device()
+        if dev != self._dev:
+            self._where(dev, where)
+        d = self._descs.get((x.dtype, transposed, act)) or self._desc(x.dtype, transposed, act)
         n, row_map, div = self._n, None, 0
         if sort is not None:
             width, mapped = (self.rows, self.cols) if transposed else (self.cols, self.rows)
             if mapped != sort.rows or (gather and width != sort.desc.width):
                 raise MlpBlkError(MLPBLK_EINVAL, f"{where}: [{self.rows}, {self.cols}] is not made of the sort's "
                                   f"{sort.rows} rows of {sort.desc.width}")
-            sort._device(where)
+            sort._where(dev, where)
             row_map = sort._at[3]
             if gather:
                 n, div = sort._x_n, sort.desc.top_k
         elif gather:
             raise MlpBlkError(MLPBLK_EINVAL, f"{where}: gather needs a sort")
-        _check(lib.mlpblk_fp4_quantize(d, _operand(x, where, "x", x.dtype, n, dev), row_map, div, *self._at,
-                                       _stream(stream)), where)
+        if x.numel() < n or x.get_device() != dev or not x.is_contiguous():
+            _operand(x, where, "x", x.dtype, n, dev)
+        codes, scales = self._at
+        rc = lib.mlpblk_fp4_quantize(d, x.data_ptr(), row_map, div, codes, scales,
+                                     t.raw_stream(dev) if stream is None else _stream(stream))
+        if rc:
+            _check(rc, where)
 
     def dequantize(self, y, stream=None):
         where = "Fp4Matrix.dequantize"
-        dev = self._device(where)
-        _check(lib.mlpblk_fp4_dequantize(self._desc(y.dtype, False, "none"), *self._at,
-                                         _operand(y, where, "y", y.dtype, self._n, dev), _stream(stream)), where)
+        t = _Torch.get()
+        dev = t.device()
+        if dev != self._dev:
+            self._where(dev, where)
+        d = self._descs.get((y.dtype, False, "none")) or self._desc(y.dtype, False, "none")
+        if y.numel() < self._n or y.get_device() != dev or not y.is_contiguous():
+            _operand(y, where, "y", y.dtype, self._n, dev)
+        codes, scales = self._at
+        rc = lib.mlpblk_fp4_dequantize(d, codes, scales, y.data_ptr(), t.raw_stream(dev) if stream is None else _stream(stream))
+        if rc:
+            _check(rc, where)
 
     def _product(self, where, b, c, accumulate, key, make):
-        """byref of the product's descriptor (made once for each key) and C's address."""
-        dev = self._device(where)
-        b._device(where)
+        """byref of the product's descriptor (made once for each key), C's address and
+        the current stream."""
+        t = _Torch.get()
+        dev = t.device()
+        if dev != self._dev or dev != b._dev:
+            self._where(dev, where)
+            b._where(dev, where)
         if self.batch != 1 or b.cols != self.cols:
             raise MlpBlkError(MLPBLK_EINVAL, f"{where}: A [{self.rows}, {self.cols}] x {self.batch}, B [{b.rows}, {b.cols}]")
-        key = (where, c.dtype, accumulate, b.rows) + key
+        key = (where, c.dtype, accumulate, b.rows, key)
         e = self._descs.get(key)
         if e is None:
             d, n = make(_dtype_code(c.dtype))
             e = self._descs[key] = (ctypes.byref(d), n)
-        return e[0], _operand(c, where, "c", c.dtype, e[1], dev)
+        if c.numel() < e[1] or c.get_device() != dev or not c.is_contiguous():
+            _operand(c, where, "c", c.dtype, e[1], dev)
+        return e[0], c.data_ptr(), t.raw_stream(dev)
 
     def matmul(self, b, c, accumulate=False, stream=None):
         """c[rows, b.rows] = self . b^T (or += with accumulate, float32)."""
         where = "Fp4Matrix.matmul"
         if b.batch != 1:
             raise MlpBlkError(MLPBLK_EINVAL, f"{where}: b is a batch")
-        d, at = self._product(where, b, c, accumulate, (), lambda dt: (
+        d, at, st = self._product(where, b, c, accumulate, None, lambda dt: (
             make_fp4_matmul_desc(self.rows, b.rows, self.cols, dt, accumulate), self.rows * b.rows))
-        _check(lib.mlpblk_fp4_matmul(d, *self._at, *b._at, at, _stream(stream)), where)
+        rc = lib.mlpblk_fp4_matmul(d, *self._at, *b._at, at, st if stream is None else _stream(stream))
+        if rc:
+            _check(rc, where)
 
     def matmul_grouped(self, b, sort, c, accumulate=False, stream=None):
         """c[R, b.rows]: expert e's rows of self times the batch's matrix e."""
         where = "Fp4Matrix.matmul_grouped"
-        sort._device(where)
         if b.batch != sort.desc.experts or self.rows != sort.rows:
             raise MlpBlkError(MLPBLK_EINVAL, f"{where}: b is not the experts' batch or self not the sorted rows")
-        d, at = self._product(where, b, c, accumulate, (b.batch, sort.desc.pad, sort._entries), lambda dt: (
+        d, at, st = self._product(where, b, c, accumulate, (b.batch, sort.desc.pad, sort._entries), lambda dt: (
             make_fp4_matmul_desc(self.rows, b.rows, self.cols, dt, accumulate, b.batch, sort.desc.pad, sort._entries),
             self.rows * b.rows))
-        _check(lib.mlpblk_fp4_matmul_grouped(d, *self._at, *b._at, sort._at[0], sort._at[1], at, _stream(stream)), where)
+        sort._where(self._dev, where)
+        rc = lib.mlpblk_fp4_matmul_grouped(d, *self._at, *b._at, sort._at[0], sort._at[1], at,
+                                           st if stream is None else _stream(stream))
+        if rc:
+            _check(rc, where)
 
     def wgrad_grouped(self, b, sort, c, accumulate=False, stream=None):
         """c[experts, rows, b.rows]: self . b^T over each expert's segment."""
         where = "Fp4Matrix.wgrad_grouped"
-        sort._device(where)
         if b.batch != 1 or self.cols != sort.rows:
             raise MlpBlkError(MLPBLK_EINVAL, f"{where}: the columns are not the sorted rows")
         E = sort.desc.experts
-        d, at = self._product(where, b, c, accumulate, (E, sort.desc.pad), lambda dt: (
+        d, at, st = self._product(where, b, c, accumulate, (E, sort.desc.pad), lambda dt: (
             make_fp4_matmul_desc(self.rows, b.rows, self.cols, dt, accumulate, E, sort.desc.pad),
             E * self.rows * b.rows))
-        _check(lib.mlpblk_fp4_wgrad_grouped(d, *self._at, *b._at, sort._at[1], at, _stream(stream)), where)
+        sort._where(self._dev, where)
+        rc = lib.mlpblk_fp4_wgrad_grouped(d, *self._at, *b._at, sort._at[1], at, st if stream is None else _stream(stream))
+        if rc:
+            _check(rc, where)
 
 
 def mlpblk_zero_grads(desc, dgamma, dw1, dw2, stream=None):
