@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kF4MaxExperts = 256;
 constexpr int kF4KB = 256;              // K values of a stage
-constexpr int kF4PrefetchStages = 32;   // stages of B that f4_small asks into L2 ahead (544 KB a CTA)
+constexpr int kF4PrefetchStages = 8;    // stages of B that f4_small asks into L2 ahead (136 KB a CTA)
 
 struct F4Args {
     int mode;                           // Fp4Mode
@@ -40,7 +40,6 @@ struct F4Args {
     int64_t max_rows;
     const uint8_t *sa, *sb;             // scales
     int64_t row_tile_bytes;             // of one 128-row strip of scale tiles (A and B share K)
-    int prefetch;                       // f4_small: ask B into L2 ahead
     int group_m;                        // raster: this many tiles of A sweep B together
     const int *count, *seg;
     void *c;
@@ -337,32 +336,18 @@ __device__ __forceinline__ void store_columns(void *c, int64_t row0, int64_t n, 
     }
 }
 
-// Asks the first tiles of a worker's B into L2 while the previous kernels (A's
-// quantisation, as a rule) still run: no data reaches this kernel before
-// griddep_wait.  With few tokens the weights' way from HBM is most of the time (one token x
-// 16384 x 4096 with the quantisation before it: 10.6 -> 10.0 us; a request of a row
-// each from 128 lanes instead of a box each: 12.2 us).  Grouped, the tiles are not
-// known yet: every expert is taken to have one tile of rows (the host asks for it
-// only where most experts do).
+// Asks the first stages of a worker's B into L2 while the previous kernel (A's
+// quantisation, as a rule) still runs: no data reaches this kernel before
+// griddep_wait.  With few tokens the weights' way from HBM is most of the time: one token x
+// 16384 x 4096 with the quantisation before it takes 10.9 us without, 9.3 with eight
+// stages asked ahead and no less with more (L2 drops requests that come faster than
+// it fetches).  Where the experts' segments decide the tiles it gained nothing.
 template <class C>
-__device__ __forceinline__ void f4_prefetch(const F4Args &a, const CUtensorMap *map, int tiles, int worker, int workers,
-                                            int rank, int cs) {
-    int left = kF4PrefetchStages;
-    const int all = a.mode == kFp4Dense ? tiles : a.experts * a.nt;
-    for (int t = worker; t < all && left > 0; t += workers) {
-        int e = 0, mi = 0, ni = t;
-        if (a.mode == kFp4Dense) {
-            raster_tile(t, a.mt, a.nt, a.group_m, mi, ni);
-        } else {
-            e = t / a.nt;
-            ni = t - e * a.nt;
-        }
-        const uint8_t *sb = a.sb + (static_cast<int64_t>(e) * ((a.n + 127) / 128) + ni) * a.row_tile_bytes;
-        const int k1 = a.kblocks * (rank + 1) / cs;
-        for (int kb = a.kblocks * rank / cs; kb < k1 && left > 0; ++kb, --left) {
-            tma_prefetch_2d(map, kb * 128, e * static_cast<int>(a.n) + ni * 128);
-            bulk_prefetch_l2(sb + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes);
-        }
+__device__ __forceinline__ void f4_prefetch(const F4Args &a, const CUtensorMap *map, const F4Tile &w, int rank, int cs) {
+    const int k0 = w.kb1 * rank / cs, k1 = min(w.kb1 * (rank + 1) / cs, k0 + kF4PrefetchStages);
+    for (int kb = k0; kb < k1; ++kb) {
+        tma_prefetch_2d(map, kb * 128, w.b_row);
+        bulk_prefetch_l2(w.sb + static_cast<int64_t>(kb) * C::kSfBytes, C::kSfBytes);
     }
 }
 
@@ -428,7 +413,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     int t = worker;                 // the tile at hand, the same walk in every role
     F4Tile w;
     if (dense && t < tiles) w = f4_tile<C::BN, 128>(args, groups, t, args.group_m);
-    if (args.prefetch && warp == 2 && lane == 0) f4_prefetch<C>(args, &tmB, tiles, worker, workers, rank, cs);
+    if (dense && t < tiles && warp == 2 && lane == 0) f4_prefetch<C>(args, &tmB, w, rank, cs);
     __syncwarp();
     griddep_wait();
     if (!dense) {
@@ -1180,10 +1165,6 @@ int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s) {
     if (workers < 1) workers = 1;
     if (p.mode != kFp4GroupRows && tiles < workers) workers = tiles;
     const int w = static_cast<int>(workers);
-    // B ahead into L2 (see the kernel): dense, or grouped where most experts have rows
-    // (T * k >= 2 E: 86 % of them if the ids are even) and all of B fits the half of L2
-    const int64_t b_bytes = p.n * fp4_row_bytes(p.k) * groups;
-    a.prefetch = p.mode == kFp4Dense || (p.mode == kFp4GroupRows && p.max_rows >= 2 * p.experts && b_bytes <= (64ll << 20)) ? 1 : 0;
 #define MLPBLK_SMALL(BN, SPLIT)                                               \
     {                                                                         \
         if (!f32) return run_small<F4Small<BN, SPLIT>, 0>(a, p, cs, w, s);    \

@@ -17,11 +17,11 @@ namespace {
 
 // ------------------------------------------------------------------- the plan
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortExperts = 256;
 constexpr int kSortCluster = 8;        // CTAs of a large plan (the portable cluster size)
 constexpr int64_t kSortOneCta = 4096;  // entries up to which one CTA makes the plan
+constexpr int64_t kSortSmall = 64;     // entries up to which that CTA has 8 warps, not 32 (16 entries: 3.6 us and 4.1;
+                                       // 384 of 64 experts, whose padding is most of the work: 6.2 and 5.2)
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -45,9 +45,11 @@ __device__ __forceinline__ int ld_cluster(const int *local, unsigned rank) {
 // Bound by latency: one pass over the ids, two cluster barriers.
 constexpr int kSortKeep = 16;
 
-__global__ void __launch_bounds__(kSortThreads)
+template <int kSortWarps>
+__global__ void __launch_bounds__(32 * kSortWarps)
 sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_t R, int64_t per_warp,
             int *__restrict__ count, int *__restrict__ seg, int *__restrict__ pos, int *__restrict__ row_map) {
+    constexpr int kSortThreads = 32 * kSortWarps;
     __shared__ int wcnt[kSortExperts][kSortWarps + 1];  // entries of an expert in a warp, then in the warps before it
     __shared__ int ctot[kSortExperts];       // this CTA's entries per expert (read by the cluster)
     __shared__ int segs[kSortExperts + 1];
@@ -98,14 +100,14 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
     __syncthreads();
     // the warps before each warp: warp w takes experts w, w + 32, ..., a lane a warp
     for (int e = wid; e < experts; e += kSortWarps) {
-        const int own = wcnt[e][lane];
+        const int own = lane < kSortWarps ? wcnt[e][lane] : 0;
         int incl = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
         }
-        wcnt[e][lane] = incl - own;
+        if (lane < kSortWarps) wcnt[e][lane] = incl - own;
         if (lane == 31) ctot[e] = incl;
     }
     if (C > 1) {
@@ -151,7 +153,7 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
     __syncthreads();
     if (c == 0) {
         if (tid < experts) count[tid] = live[tid];
-        if (tid <= experts) seg[tid] = segs[tid];
+        for (int e = tid; e <= experts; e += kSortThreads) seg[e] = segs[e];
     }
     auto place = [&](int64_t i, int e, int r) {
         const int p = e < 0 ? -1 : first[e] + wcnt[e][wid] + r;
@@ -483,11 +485,12 @@ MoveShape move_shape(int64_t T, int64_t width, int dtype, int experts, int pad, 
 int launch_sort(const int *idx, int64_t n, int experts, int pad, int64_t R, int *count, int *seg, int *pos,
                 int *row_map, cudaStream_t s) {
     const int C = n <= kSortOneCta ? 1 : kSortCluster;
-    int64_t per_warp = (n + static_cast<int64_t>(C) * kSortWarps - 1) / (static_cast<int64_t>(C) * kSortWarps);
+    const int warps = n <= kSortSmall ? 8 : 32;
+    int64_t per_warp = (n + static_cast<int64_t>(C) * warps - 1) / (static_cast<int64_t>(C) * warps);
     per_warp = (per_warp + 31) / 32 * 32;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(C);
-    cfg.blockDim = dim3(kSortThreads);
+    cfg.blockDim = dim3(32 * warps);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -498,7 +501,8 @@ int launch_sort(const int *idx, int64_t n, int experts, int pad, int64_t R, int 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = C > 1 ? 2 : 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, sort_kernel, idx, n, experts, pad, R, per_warp, count, seg, pos, row_map));
+    auto kern = warps == 8 ? sort_kernel<8> : sort_kernel<32>;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kern, idx, n, experts, pad, R, per_warp, count, seg, pos, row_map));
 }
 
 int launch_permute(const void *x, const int *pos, const int *count, const int *seg, int64_t T, int64_t width,
