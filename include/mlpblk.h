@@ -508,7 +508,8 @@ int mlpblk_moe_unpermute_backward(const mlpblk_sort_desc *desc, const void *dy, 
  * mlpblk_fp4_dequantize: y[batch, rows, cols] in desc->dtype (exact in both types).
  *   transposed and act must be 0.
  * Limits: rows, cols >= 0 (with either 0: MLPBLK_OK, nothing is touched),
- * rows * batch and cols < 2^31; pointers 16-byte aligned.
+ * rows * batch and cols < 2^31, ceil(rows / 128) * batch < 2^29; pointers 16-byte
+ * aligned.
  */
 #define MLPBLK_FP4_ACT_NONE   0
 #define MLPBLK_FP4_ACT_RELU2  1

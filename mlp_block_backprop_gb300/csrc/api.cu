@@ -1308,6 +1308,7 @@ int check_fp4_desc(const mlpblk_fp4_desc *d) {
     if (d->transposed != 0 && d->transposed != 1) return MLPBLK_EINVAL;
     if (d->rows < 0 || d->cols < 0 || d->batch < 1 || d->cols >= kFp4Lim) return MLPBLK_EINVAL;
     if (d->rows > 0 && d->batch >= kFp4Lim / d->rows) return MLPBLK_EINVAL;
+    if ((d->rows + 127) / 128 * d->batch >= kFp4Lim / 4) return MLPBLK_EINVAL;  // CTAs of a launch
     return MLPBLK_OK;
 }
 
@@ -1403,7 +1404,7 @@ int mlpblk_moe_permute(const mlpblk_sort_desc *desc, const void *x, const int32_
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     MLPBLK_LAUNCH(MLPBLK_KERNEL_PERMUTE, s,
                   launch_permute(x, pos, count, seg, desc->tokens, desc->width, desc->dtype, desc->top_k, desc->experts,
-                                 desc->pad, rows, s));
+                                 desc->pad, sort_rows(desc), rows, s));
     return MLPBLK_OK;
 }
 
@@ -1418,7 +1419,8 @@ int mlpblk_moe_unpermute(const mlpblk_sort_desc *desc, const void *rows, const i
     MLPBLK_TRY(device_sms(&sms));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     MLPBLK_LAUNCH(MLPBLK_KERNEL_UNPERMUTE, s,
-                  launch_unpermute(rows, pos, weights, residual, desc->tokens, desc->width, desc->dtype, desc->top_k, y, s));
+                  launch_unpermute(rows, pos, weights, residual, desc->tokens, desc->width, desc->dtype, desc->top_k,
+                                   sort_rows(desc), y, s));
     return MLPBLK_OK;
 }
 
@@ -1440,7 +1442,7 @@ int mlpblk_moe_unpermute_backward(const mlpblk_sort_desc *desc, const void *dy, 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     MLPBLK_LAUNCH(MLPBLK_KERNEL_UNPERMUTE_BWD, s,
                   launch_unpermute_bwd(dy, rows, pos, count, seg, weights, desc->tokens, desc->width, desc->dtype,
-                                       desc->top_k, desc->experts, desc->pad, d_rows, d_weights, s));
+                                       desc->top_k, desc->experts, desc->pad, sort_rows(desc), d_rows, d_weights, s));
     return MLPBLK_OK;
 }
 

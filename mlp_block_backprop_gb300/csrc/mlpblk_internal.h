@@ -311,11 +311,11 @@ int launch_moe_dout(const void *dy, const void *o_perm, const float *p, const in
 int launch_sort(const int *idx, int64_t n, int experts, int pad, int64_t R, int *count, int *seg, int *pos,
                 int *row_map, cudaStream_t s);
 int launch_permute(const void *x, const int *pos, const int *count, const int *seg, int64_t T, int64_t width,
-                   int dtype, int k, int experts, int pad, void *rows, cudaStream_t s);
+                   int dtype, int k, int experts, int pad, int64_t R, void *rows, cudaStream_t s);
 int launch_unpermute(const void *rows, const int *pos, const float *weights, const void *residual, int64_t T,
-                     int64_t width, int dtype, int k, void *y, cudaStream_t s);
+                     int64_t width, int dtype, int k, int64_t R, void *y, cudaStream_t s);
 int launch_unpermute_bwd(const void *dy, const void *rows, const int *pos, const int *count, const int *seg,
-                         const float *weights, int64_t T, int64_t width, int dtype, int k, int experts, int pad,
+                         const float *weights, int64_t T, int64_t width, int dtype, int k, int experts, int pad, int64_t R,
                          void *d_rows, float *d_weights, cudaStream_t s);
 
 // Host: fp32 CUDA-core GEMM path (simt_f32.cu).  Strides are in elements:

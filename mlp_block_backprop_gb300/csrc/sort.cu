@@ -265,12 +265,19 @@ __device__ __forceinline__ U zero_unit() {
     return z;
 }
 
+// An entry's row, -1 where it has none.  Positions of another plan than this shape's
+// are taken as none, so no access leaves the R rows.
+__device__ __forceinline__ int entry_row(const int *pos, int64_t i, int R) {
+    const int r = pos[i];
+    return static_cast<unsigned>(r) < static_cast<unsigned>(R) ? r : -1;
+}
+
 // Padding row number q of the plan (q / pad = expert, q % pad = which): its row, or -1.
-__device__ __forceinline__ int64_t padding_row(int64_t q, int pad, int experts, const int *count, const int *seg) {
+__device__ __forceinline__ int64_t padding_row(int64_t q, int pad, int experts, const int *count, const int *seg, int R) {
     const int e = static_cast<int>(q / pad);
     if (e >= experts) return -1;
     const int64_t r = static_cast<int64_t>(seg[e]) + count[e] + q % pad;
-    return r < seg[e + 1] ? r : -1;
+    return r >= 0 && r < seg[e + 1] && r < R ? r : -1;
 }
 
 template <int TX, class U>
@@ -282,26 +289,25 @@ __device__ __forceinline__ void zero_row(U *row, int units) {
 template <int TX, class U>
 __global__ void __launch_bounds__(kMoveThreads)
 permute_kernel(const U *__restrict__ x, const int *__restrict__ pos, const int *__restrict__ count,
-               const int *__restrict__ seg, int64_t T, int k, int experts, int pad, int units, int64_t token_blocks,
+               const int *__restrict__ seg, int64_t T, int k, int experts, int pad, int R, int units, int64_t token_blocks,
                U *__restrict__ rows) {
     constexpr int kPer = kPerOf<U>;
     griddep_enter();
     const int64_t b = blockIdx.x;
     if (b >= token_blocks) {
-        const int64_t r = padding_row((b - token_blocks) * blockDim.y + threadIdx.y, pad, experts, count, seg);
+        const int64_t r = padding_row((b - token_blocks) * blockDim.y + threadIdx.y, pad, experts, count, seg, R);
         if (r >= 0) zero_row<TX>(rows + r * units, units);
         return;
     }
     const int64_t t = b * blockDim.y + threadIdx.y;
     if (t >= T) return;
-    const int *pt = pos + t * k;
     for (int c = threadIdx.x; c < units; c += kPer * TX) {
         const U *src = x + t * units + c;
         U v[kPer];
 #pragma unroll
         for (int u = 0; u < kPer; ++u) v[u] = c + u * TX < units ? __ldg(src + u * TX) : zero_unit<U>();
         for (int j = 0; j < k; ++j) {
-            const int64_t r = pt[j];
+            const int64_t r = entry_row(pos, t * k + j, R);
             if (r < 0) continue;
             U *dst = rows + r * units + c;
 #pragma unroll
@@ -321,13 +327,12 @@ permute_kernel(const U *__restrict__ x, const int *__restrict__ pos, const int *
 template <int TX, class U, bool BF16>
 __global__ void __launch_bounds__(kMoveThreads)
 unpermute_kernel(const U *__restrict__ rows, const int *__restrict__ pos, const float *__restrict__ weights,
-                 const U *residual, int64_t T, int k, int units, U *y) {
+                 const U *residual, int64_t T, int k, int R, int units, U *y) {
     using V = Vals<U, BF16>;
     constexpr int kPer = kPerOf<U>;
     griddep_enter();
     const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (t >= T) return;
-    const int *pt = pos + t * k;
     const float *wt = weights + t * k;
     for (int c = threadIdx.x; c < units; c += kPer * TX) {
         float acc[kPer][V::N];
@@ -336,7 +341,7 @@ unpermute_kernel(const U *__restrict__ rows, const int *__restrict__ pos, const 
 #pragma unroll
         for (int u = 0; u < kPer; ++u) res[u] = residual && c + u * TX < units ? rp[u * TX] : zero_unit<U>();
         for (int j = 0; j < k; j += 2) {
-            const int ra = pt[j], rb = j + 1 < k ? pt[j + 1] : -1;
+            const int ra = entry_row(pos, t * k + j, R), rb = j + 1 < k ? entry_row(pos, t * k + j + 1, R) : -1;
             const float wa = weights ? wt[j] : 1.0f;
             const float wb = weights && j + 1 < k ? wt[j + 1] : 1.0f;
             const U *pa = rows + static_cast<int64_t>(ra < 0 ? 0 : ra) * units + c;
@@ -385,7 +390,7 @@ template <int TX, class U, bool BF16>
 __global__ void __launch_bounds__(kMoveThreads)
 unpermute_bwd_kernel(const U *__restrict__ dy, const U *__restrict__ rows, const int *__restrict__ pos,
                      const int *__restrict__ count, const int *__restrict__ seg, const float *__restrict__ weights,
-                     int64_t T, int k, int experts, int pad, int units, int64_t token_blocks,
+                     int64_t T, int k, int experts, int pad, int R, int units, int64_t token_blocks,
                      U *__restrict__ d_rows, float *__restrict__ d_weights) {
     using V = Vals<U, BF16>;
     constexpr int kPerBwd = kPerBwdOf<U>, kSlots = kSlotsOf<U>;
@@ -394,7 +399,7 @@ unpermute_bwd_kernel(const U *__restrict__ dy, const U *__restrict__ rows, const
     griddep_enter();
     const int64_t b = blockIdx.x;
     if (b >= token_blocks) {
-        const int64_t r = padding_row((b - token_blocks) * blockDim.y + threadIdx.y, pad, experts, count, seg);
+        const int64_t r = padding_row((b - token_blocks) * blockDim.y + threadIdx.y, pad, experts, count, seg, R);
         if (r >= 0) zero_row<TX>(d_rows + r * units, units);
         return;
     }
@@ -409,7 +414,7 @@ unpermute_bwd_kernel(const U *__restrict__ dy, const U *__restrict__ rows, const
         for (int j = 0; j < kSlots; ++j) {
             const bool on = in && j0 + j < k;
             s[j] = 0.0f;
-            r[j] = on ? pos[t * k + j0 + j] : -1;
+            r[j] = on ? entry_row(pos, t * k + j0 + j, R) : -1;
             w[j] = on && weights ? weights[t * k + j0 + j] : 1.0f;
         }
         for (int c = threadIdx.x; in && c < units; c += kPerBwd * TX) {
@@ -506,12 +511,13 @@ int launch_sort(const int *idx, int64_t n, int experts, int pad, int64_t R, int 
 }
 
 int launch_permute(const void *x, const int *pos, const int *count, const int *seg, int64_t T, int64_t width,
-                   int dtype, int k, int experts, int pad, void *rows, cudaStream_t s) {
+                   int dtype, int k, int experts, int pad, int64_t R, void *rows, cudaStream_t s) {
     const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerOf<uint4>, kPerOf<uint32_t>);
     const dim3 grid(static_cast<unsigned>(m.token_blocks + m.pad_blocks));
 #define MLPBLK_PERMUTE(U)                                                                                      \
-    return launch_pdl(m.tx == 32 ? permute_kernel<32, U> : permute_kernel<128, U>, grid, m.block, 0, s, static_cast<const U *>(x), pos, count, seg, T, k, \
-                      experts, pad, m.units, m.token_blocks, static_cast<U *>(rows))
+    return launch_pdl(m.tx == 32 ? permute_kernel<32, U> : permute_kernel<128, U>, grid, m.block, 0, s,         \
+                      static_cast<const U *>(x), pos, count, seg, T, k,                                        \
+                      experts, pad, static_cast<int>(R), m.units, m.token_blocks, static_cast<U *>(rows))
     if (m.unit == 16) MLPBLK_PERMUTE(uint4);
     if (m.unit == 4) MLPBLK_PERMUTE(uint32_t);
     MLPBLK_PERMUTE(uint16_t);
@@ -519,12 +525,12 @@ int launch_permute(const void *x, const int *pos, const int *count, const int *s
 }
 
 int launch_unpermute(const void *rows, const int *pos, const float *weights, const void *residual, int64_t T,
-                     int64_t width, int dtype, int k, void *y, cudaStream_t s) {
+                     int64_t width, int dtype, int k, int64_t R, void *y, cudaStream_t s) {
     const MoveShape m = move_shape(T, width, dtype, 1, 1, kPerOf<uint4>, kPerOf<uint32_t>);
     const dim3 grid(static_cast<unsigned>(m.token_blocks));
 #define MLPBLK_UNPERMUTE(U, B)                                                                              \
     return launch_pdl(m.tx == 32 ? unpermute_kernel<32, U, B> : unpermute_kernel<128, U, B>, grid, m.block, 0, s, static_cast<const U *>(rows), pos, weights, \
-                      static_cast<const U *>(residual), T, k, m.units, static_cast<U *>(y))
+                      static_cast<const U *>(residual), T, k, static_cast<int>(R), m.units, static_cast<U *>(y))
     if (dtype == MLPBLK_BF16) {
         if (m.unit == 16) MLPBLK_UNPERMUTE(uint4, true);
         if (m.unit == 4) MLPBLK_UNPERMUTE(uint32_t, true);
@@ -536,13 +542,13 @@ int launch_unpermute(const void *rows, const int *pos, const float *weights, con
 }
 
 int launch_unpermute_bwd(const void *dy, const void *rows, const int *pos, const int *count, const int *seg,
-                         const float *weights, int64_t T, int64_t width, int dtype, int k, int experts, int pad,
+                         const float *weights, int64_t T, int64_t width, int dtype, int k, int experts, int pad, int64_t R,
                          void *d_rows, float *d_weights, cudaStream_t s) {
     const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerBwdOf<uint4>, kPerBwdOf<uint32_t>);
     const dim3 grid(static_cast<unsigned>(m.token_blocks + m.pad_blocks));
 #define MLPBLK_UNPERMUTE_BWD(U, B)                                                                               \
     return launch_pdl(m.tx == 32 ? unpermute_bwd_kernel<32, U, B> : unpermute_bwd_kernel<128, U, B>, grid, m.block, 0, s, static_cast<const U *>(dy),                 \
-                      static_cast<const U *>(rows), pos, count, seg, weights, T, k, experts, pad, m.units,        \
+                      static_cast<const U *>(rows), pos, count, seg, weights, T, k, experts, pad, static_cast<int>(R), m.units,        \
                       m.token_blocks, static_cast<U *>(d_rows), d_weights)
     if (dtype == MLPBLK_BF16) {
         if (m.unit == 16) MLPBLK_UNPERMUTE_BWD(uint4, true);

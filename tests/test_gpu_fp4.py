@@ -493,3 +493,69 @@ def test_wgrad_of_no_rows(mb):
     assert bool((c == 3.0).all())
     a.wgrad_grouped(b, s, c)
     assert not c.any()
+
+
+def test_no_row_chosen(mb):
+    """Every id invalid: no tile at all, C as it was; weight gradients zero."""
+    import torch
+    for T, E in ((5, 4), (3000, 6)):
+        s = mb.MoeSort(T, 64, E, 2, 256)
+        s.sort(torch.full((T, 2), -1, dtype=torch.int32, device="cuda"))
+        x = torch.randn(T, 64, device="cuda")
+        q, qt, w = mb.Fp4Matrix(s.rows, 64), mb.Fp4Matrix(64, s.rows), mb.Fp4Matrix(96, 64, batch=E)
+        q.quantize(x, sort=s, gather=True)
+        qt.quantize(x, sort=s, gather=True, transposed=True)
+        w.quantize(torch.randn(E * 96, 64, device="cuda"))
+        c = torch.full((s.rows, 96), 5.0, device="cuda")
+        q.matmul_grouped(w, s, c)
+        assert bool((c == 5.0).all())
+        dw = torch.full((E, 64, 64), 5.0, device="cuda")
+        qt.wgrad_grouped(qt, s, dw)
+        assert not dw.any()
+
+
+def test_repeats_are_bitwise_equal(mb):
+    import torch
+    rng = np.random.default_rng(14)
+    for m, n, k in ((3, 4096, 8192), (200, 600, 4000), (2300, 2304, 1000)):
+        qa, _ = _quantized(mb, rng, m, k)
+        qb, _ = _quantized(mb, rng, n, k)
+        outs = []
+        for _ in range(3):
+            c = torch.full((m, n), 1.0, device="cuda")
+            qa.matmul(qb, c, accumulate=True)
+            outs.append(c)
+        assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+def test_matrices_beyond_two_billion_elements(mb):
+    """A source and a C of more than 2^31 elements, at their far ends."""
+    import torch
+    rows, cols = 70000, 32768
+    x = torch.randn(256, cols, device="cuda").bfloat16().repeat(rows // 256 + 1, 1)[:rows].contiguous()
+    assert x.numel() > 1 << 31
+    tail = x[rows - 300:].contiguous()
+    for tr in (False, True):
+        if tr:
+            x, tail = x.view(cols, rows), x.view(cols, rows)[:, rows - 300:].contiguous()
+        q, qs = mb.Fp4Matrix(rows, cols), mb.Fp4Matrix(300, cols)
+        q.quantize(x, transposed=tr)
+        qs.quantize(tail, transposed=tr)
+        assert torch.equal(q.codes.view(rows, -1)[rows - 300:], qs.codes.view(300, -1))
+    y = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    q.dequantize(y)
+    ys = torch.empty(300, cols, dtype=torch.bfloat16, device="cuda")
+    qs.dequantize(ys)
+    assert torch.equal(y[rows - 300:], ys)
+    del x, y, q, qs, ys, tail
+    for m, n in ((46400, 46400), (30, 75_000_000)):
+        a, b = torch.randn(m, 64, device="cuda"), torch.randn(n, 64, device="cuda")
+        qa, qb = mb.Fp4Matrix(m, 64), mb.Fp4Matrix(n, 64)
+        qa.quantize(a)
+        qb.quantize(b)
+        c = torch.zeros(m, n, dtype=torch.bfloat16, device="cuda")
+        assert c.numel() > 1 << 31
+        qa.matmul(qb, c)
+        i, j = slice(m - 20, m), slice(n - 200, n)
+        _check(to_np(c[i, j]), fp4.rounded(to_np(a[i])), fp4.rounded(to_np(b[j])), "bf16", 64)
+        _check(to_np(c[:20, j]), fp4.rounded(to_np(a[:20])), fp4.rounded(to_np(b[j])), "bf16", 64)

@@ -49,7 +49,7 @@ def _plan(mb, idx, width, E, pad, dtype="bf16"):
 
 @pytest.mark.parametrize("kind", ["any", "one", "none", "mixed"])
 @pytest.mark.parametrize("shape", [(1, 1, 1, 1), (1, 256, 8, 128), (33, 7, 3, 16), (500, 256, 8, 256), (513, 60, 8, 1),
-                                   (4097, 3, 1, 1024), (5000, 130, 2, 100), (20011, 17, 6, 128)])
+                                   (4097, 3, 1, 1024), (5000, 130, 2, 100), (20011, 17, 6, 128), (70001, 40, 2, 16)])
 def test_plan(mb, shape, kind):
     T, E, k, pad = shape
     idx = _ids(np.random.default_rng(T), T, E, k, kind)
@@ -184,3 +184,45 @@ def test_binding_checks(mb):
     x = torch.zeros(s.rows, 8, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(mb.MlpBlkError):
         s.permute(x, x)
+
+
+def test_positions_of_another_plan_stay_inside(mb):
+    """pos of a larger batch handed to a smaller one's calls: entries beyond its rows
+    count as none, and nothing outside the buffers is read or written."""
+    import torch
+    s = mb.MoeSort(4, 64, 3, 2, 16)
+    pos = torch.tensor([[0, 1 << 20], [-7, 1], [s.rows, 2], [3, 2147483647]], dtype=torch.int32, device="cuda")
+    count, seg = torch.tensor([5, 1 << 20, 0], dtype=torch.int32, device="cuda"), torch.tensor(
+        [0, 16, 1 << 21, 1 << 22], dtype=torch.int32, device="cuda")
+    whole = torch.full((s.rows * 64 + 4096,), 7.0, dtype=torch.bfloat16, device="cuda")
+    rows = whole[2048:2048 + s.rows * 64]
+    x = torch.randn(4, 64, device="cuda").bfloat16()
+    mb.mlpblk_moe_permute(s.desc, x, pos, count, seg, rows)
+    got = rows.view(s.rows, 64)
+    assert torch.equal(got[0], x[0]) and torch.equal(got[1], x[1]) and torch.equal(got[2], x[2]) and torch.equal(got[3], x[3])
+    assert bool((whole[:2048] == 7).all()) and bool((whole[-2048:] == 7).all())
+    y = torch.empty_like(x)
+    mb.mlpblk_moe_unpermute(s.desc, rows, pos, None, None, y)
+    assert torch.equal(y, x)
+
+
+def test_rows_beyond_two_billion_elements(mb):
+    """Sorted rows of more than 2^31 elements: both moves at their far end."""
+    import torch
+    T, d, E, k = 270000, 4096, 2, 2
+    s = mb.MoeSort(T, d, E, k, 1)
+    idx = torch.stack((torch.zeros(T), torch.ones(T)), 1).int().cuda()
+    s.sort(idx)
+    x = torch.arange(T, device="cuda", dtype=torch.float32)[:, None].remainder(251).expand(T, d).bfloat16().contiguous()
+    rows = torch.zeros(s.rows, d, dtype=torch.bfloat16, device="cuda")
+    assert rows.numel() > 1 << 31
+    s.permute(x, rows)
+    for t in (0, 1, T // 2, T - 1):
+        assert torch.equal(rows[t], x[t]) and torch.equal(rows[T + t], x[t])
+    y = torch.empty_like(x)
+    s.permute_backward(rows, y)
+    assert torch.equal(y, (2 * x.float()).bfloat16())
+    dw = torch.empty(T, k, device="cuda")
+    s.unpermute_backward(x, rows, None, y.new_zeros(s.rows, d), dw)
+    ref = x[:, 0].float() ** 2 * d
+    assert bool(((dw - ref[:, None]).abs() <= 2.0 ** -20 * ref[:, None]).all())
