@@ -646,9 +646,13 @@ __device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc,
         : "memory");
 }
 
+// C's lines are the first to leave L2, so that the operands' stay (16384 x 8192 x 2048
+// bf16: 91 -> 87 us).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int32_t c0, int32_t c1, int32_t c2) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
-                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], %5;"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2), "l"(pol)
                  : "memory");
 }
 
@@ -1011,6 +1015,7 @@ bool make_map_codes(CUtensorMap *m, const void *codes, int64_t rows, int64_t k, 
 
 template <class C, int OUT>
 int run_small(F4Args a, const Fp4Product &p, int cs, int workers, cudaStream_t s) {
+    a.group_m = 8;
     a.mt = static_cast<int>((p.m + C::BN - 1) / C::BN);
     a.nt = static_cast<int>((p.n + 127) / 128);
     CUtensorMap mA, mA32, mB;
@@ -1076,6 +1081,7 @@ bool make_map_c(CUtensorMap *m, void *c, bool f32, int64_t mats, int64_t rows, i
 
 template <int OUT, bool TMA_OUT>
 int run_pair(F4Args a, const Fp4Product &p, int workers, cudaStream_t s) {
+    a.group_m = 4;  // 8192 x 16384 x 4096: 157 us; 160 with 8, 162 with 16
     a.mt = static_cast<int>((p.m + 255) / 256);
     a.nt = static_cast<int>((p.n + 255) / 256);
     CUtensorMap mA, mB, mSA, mSB, mC;
@@ -1129,7 +1135,6 @@ int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s) {
     a.sa = p.sa;
     a.sb = p.sb;
     a.row_tile_bytes = fp4_col_tiles(p.k) * kFp4TileBytes;
-    a.group_m = 8;
     a.count = p.count;
     a.seg = p.seg;
     a.c = p.c;

@@ -231,6 +231,7 @@ PRODUCTS = [
     (1, 1, 1), (1, 130, 32), (2, 64, 100), (8, 1000, 2049), (31, 257, 4096), (33, 129, 255), (40, 4096, 300),
     (128, 256, 256), (129, 127, 512), (333, 1000, 1031), (257, 384, 8200), (1, 300, 16384), (1000, 70, 640),
     (512, 1024, 768), (1025, 2050, 1000), (2048, 2048, 512), (2305, 1536, 288), (4, 16384, 4096),
+    (2100, 2056, 320), (2100, 2052, 320),
 ]
 
 
