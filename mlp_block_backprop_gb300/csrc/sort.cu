@@ -321,11 +321,12 @@ permute_kernel(const U *__restrict__ x, const int *__restrict__ pos, const int *
 // once.  Two slots' rows are loaded together, so that a thread has 3 * kPer accesses
 // in flight (four slots' at a time take it to one CTA an SM: 90 -> 153 us at 16384 x
 // 4096 bf16, top-2; rows that arrive by bulk copies in a ring of shared-memory stages
-// were no faster there, 91 us, and half as fast on 1001-float rows).
+// were no faster there, 91 us, and half as fast on 1001-float rows; 4- and 2-byte
+// accesses gain from a third CTA, 34 -> 30 us at 4097 x 1001 float32, top-6).
 // residual and y may be the same array: an element is read and written by the same
 // thread.
 template <int TX, class U, bool BF16>
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kMoveThreads, sizeof(U) == 16 ? 1 : 3)
 unpermute_kernel(const U *__restrict__ rows, const int *__restrict__ pos, const float *__restrict__ weights,
                  const U *residual, int64_t T, int k, int R, int units, U *y) {
     using V = Vals<U, BF16>;
