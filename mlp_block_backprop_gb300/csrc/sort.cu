@@ -36,8 +36,10 @@ __device__ __forceinline__ int ld_cluster(const int *local, unsigned rank) {
 
 // One cluster makes the whole plan in one launch: CTA c of C takes a contiguous
 // range of the entries, warp w a contiguous part of that, so ranks follow entry
-// order.  A warp walks its part once: lanes with the same expert find each other by
-// match_any and take the next ranks within the warp.  The counts' prefixes then run over
+// order.  A warp walks its part once: lanes with the same expert find each other by a
+// ballot for each bit of the id (match_any does the same at one instruction in some 80
+// cycles an SM: 24582 entries of 60 experts, 3.8 us for the ranks alone) and take the
+// next ranks within the warp.  The counts' prefixes then run over
 // the warps (a lane a warp) and over the CTAs through distributed shared memory, and an
 // entry's row is its expert's first row, plus the entries before its CTA, its warp,
 // and itself.  An entry's expert and rank stay in a register for parts of up to
@@ -65,11 +67,17 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
     const int64_t w0 = (static_cast<int64_t>(c) * kSortWarps + wid) * per_warp;
     const int64_t w1 = min(n, w0 + per_warp);
     const bool keep = per_warp <= 32 * kSortKeep;
+    const int bits = 32 - __clz(experts);  // of the ids 0 .. experts - 1 and of -1
     uint32_t kept[kSortKeep];  // rank in the warp << 9 | expert (511: none)
     griddep_wait();
     // the next rank of expert e within the warp, for the 32 lanes' entries in order
     auto rank_of = [&](int e) {
-        const unsigned peers = __match_any_sync(0xffffffffu, e);
+        unsigned peers = 0xffffffffu;  // lanes with the same id (-1 has every bit set)
+        for (int b = 0; b < bits; ++b) {
+            const bool set = e >> b & 1;
+            const unsigned m = __ballot_sync(0xffffffffu, set);
+            peers &= set ? m : ~m;
+        }
         const int base = e >= 0 ? wcnt[e][wid] : 0;
         __syncwarp();
         if (e >= 0 && (peers & lt) == 0) wcnt[e][wid] = base + __popc(peers);
