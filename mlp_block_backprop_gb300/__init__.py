@@ -226,6 +226,31 @@ def _load():
 lib = _load()
 
 
+class _Calls:
+    """The latency-bound entry points for the classes below, descriptors and tensors by
+    address: csrc/pycalls.c where it was built (it needs Python's headers), else the
+    same functions through ctypes."""
+
+    def __init__(self):
+        try:
+            from . import _mlpblk_calls as native
+        except ImportError:
+            native = None
+        for name in ("moe_sort", "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
+                     "fp4_quantize", "fp4_dequantize", "fp4_matmul", "fp4_matmul_grouped", "fp4_wgrad_grouped"):
+            setattr(self, name, getattr(native, "mlpblk_" + name) if native else self._ctypes("mlpblk_" + name))
+        self.native = native is not None
+
+    @staticmethod
+    def _ctypes(name):
+        f = getattr(lib, name)
+        desc = f.argtypes[0]
+        return lambda d, *a: f(ctypes.cast(d, desc), *a)
+
+
+_calls = _Calls()
+
+
 def strerror(code: int) -> str:
     return lib.mlpblk_strerror(int(code)).decode()
 
@@ -244,7 +269,7 @@ class _Torch:
         if _Torch._one is None:
             import torch
             o = _Torch()
-            o.device = torch.cuda.current_device
+            o.device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
             # the handle of a device's current stream; without the raw getter, through
             # the Stream object (3 us a call instead of 0.2 on a Grace core)
             o.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
@@ -594,9 +619,9 @@ def mlpblk_moe_unpermute_backward(desc, dy, rows, pos, count, seg, weights, d_ro
 class _Kept:
     """Base of the classes that keep device buffers of their own: the buffers cannot
     be replaced, so their addresses are taken once and a call checks only what it is
-    given.  A call of these classes costs about 4 us of host time on a Grace core, 2.5 of
-    them in the library (launches included): the checks of the common case stand in
-    the methods themselves, _operand only words the refusal."""
+    given.  A call of these classes costs about 3 us of host time on a Grace core, 2 of them
+    in the library (launches included): the checks of the common case stand in the
+    methods themselves, _operand only words the refusal."""
 
     def _where(self, dev, where):
         """Refuses a call whose device is not the buffers' own."""
@@ -622,7 +647,7 @@ class MoeSort(_Kept):
         self._pos = torch.empty(tokens, top_k, **e)
         self._row_map = torch.empty(self.rows, **e)
         self._dev = self._count.get_device()
-        self._d = ctypes.byref(self.desc)
+        self._d = ctypes.addressof(self.desc)
         self._at = tuple(t.data_ptr() for t in (self._count, self._seg, self._pos, self._row_map))
         self._entries, self._x_n, self._r_n = tokens * top_k, tokens * width, self.rows * width
         self._type = _Torch.get().row[self.desc.dtype]
@@ -639,14 +664,9 @@ class MoeSort(_Kept):
         dev = t.device()
         if dev != self._dev:
             self._where(dev, where)
-        out = []
-        for x, name, dt, n in tensors:
-            if x is None:
-                out.append(None)
-            elif x.dtype is dt and x.numel() >= n and x.get_device() == dev and x.is_contiguous():
-                out.append(x.data_ptr())
-            else:
-                out.append(_operand(x, where, name, dt, n, dev))
+        out = [None if x is None else x.data_ptr()
+               if x.dtype is dt and x.numel() >= n and x.get_device() == dev and x.is_contiguous()
+               else _operand(x, where, name, dt, n, dev) for x, name, dt, n in tensors]
         out.append(t.raw_stream(dev))
         return out
 
@@ -654,7 +674,7 @@ class MoeSort(_Kept):
         where = "MoeSort.sort"
         idx, st = self._check_all(where, ((expert_idx, "expert_idx", _Torch.get().int32, self._entries),))
         count, seg, pos, row_map = self._at
-        rc = lib.mlpblk_moe_sort(self._d, idx, count, seg, pos, row_map, st if stream is None else _stream(stream))
+        rc = _calls.moe_sort(self._d, idx, count, seg, pos, row_map, st if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
 
@@ -663,7 +683,7 @@ class MoeSort(_Kept):
         dt = self._type
         x, rows, st = self._check_all(where, ((x, "x", dt, self._x_n), (rows, "rows", dt, self._r_n)))
         count, seg, pos, _ = self._at
-        rc = lib.mlpblk_moe_permute(self._d, x, pos, count, seg, rows, st if stream is None else _stream(stream))
+        rc = _calls.moe_permute(self._d, x, pos, count, seg, rows, st if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
 
@@ -671,7 +691,7 @@ class MoeSort(_Kept):
         where = "MoeSort.permute_backward"
         dt = self._type
         d_rows, dx, st = self._check_all(where, ((d_rows, "d_rows", dt, self._r_n), (dx, "dx", dt, self._x_n)))
-        rc = lib.mlpblk_moe_permute_backward(self._d, d_rows, self._at[2], dx, st if stream is None else _stream(stream))
+        rc = _calls.moe_permute_backward(self._d, d_rows, self._at[2], dx, st if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
 
@@ -681,7 +701,7 @@ class MoeSort(_Kept):
         rows, weights, residual, y, st = self._check_all(where, (
             (rows, "rows", dt, self._r_n), (weights, "weights", _Torch.get().float32, self._entries),
             (residual, "residual", dt, self._x_n), (y, "y", dt, self._x_n)))
-        rc = lib.mlpblk_moe_unpermute(self._d, rows, self._at[2], weights, residual, y,
+        rc = _calls.moe_unpermute(self._d, rows, self._at[2], weights, residual, y,
                                       st if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
@@ -693,7 +713,7 @@ class MoeSort(_Kept):
             (dy, "dy", dt, self._x_n), (rows, "rows", dt, self._r_n), (weights, "weights", f32, self._entries),
             (d_rows, "d_rows", dt, self._r_n), (d_weights, "d_weights", f32, self._entries)))
         count, seg, pos, _ = self._at
-        rc = lib.mlpblk_moe_unpermute_backward(self._d, dy, rows, pos, count, seg, weights, d_rows, d_weights,
+        rc = _calls.moe_unpermute_backward(self._d, dy, rows, pos, count, seg, weights, d_rows, d_weights,
                                                st if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
@@ -811,20 +831,20 @@ class Fp4Matrix(_Kept):
         self._dev = self._codes.get_device()
         self._at = (self._codes.data_ptr(), self._scales.data_ptr())
         self._n = self.rows * self.cols * self.batch
-        self._descs = {}
+        self._descs, self._kept = {}, []   # addresses of descriptors, and the descriptors
 
     codes = property(lambda self: self._codes)
     scales = property(lambda self: self._scales)
 
     def _desc(self, dtype, transposed, act):
-        """byref of the descriptor for these options, made once."""
+        """Address of the descriptor for these options, made once."""
         key = (dtype, transposed, act)
         d = self._descs.get(key)
         if d is None:
             if act not in self._ACTS:
                 raise MlpBlkError(MLPBLK_ENOTSUP, f"Fp4Matrix.quantize: act {act!r}")
-            d = self._descs[key] = ctypes.byref(make_fp4_desc(self.rows, self.cols, self.batch, dtype, transposed,
-                                                              self._ACTS[act]))
+            self._kept.append(make_fp4_desc(self.rows, self.cols, self.batch, dtype, transposed, self._ACTS[act]))
+            d = self._descs[key] = ctypes.addressof(self._kept[-1])
         return d
 
     def quantize(self, x, transposed=False, act="none", sort=None, gather=False, stream=None):
@@ -852,7 +872,7 @@ class Fp4Matrix(_Kept):
         if x.numel() < n or x.get_device() != dev or not x.is_contiguous():
             _operand(x, where, "x", x.dtype, n, dev)
         codes, scales = self._at
-        rc = lib.mlpblk_fp4_quantize(d, x.data_ptr(), row_map, div, codes, scales,
+        rc = _calls.fp4_quantize(d, x.data_ptr(), row_map, div, codes, scales,
                                      t.raw_stream(dev) if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
@@ -867,12 +887,12 @@ class Fp4Matrix(_Kept):
         if y.numel() < self._n or y.get_device() != dev or not y.is_contiguous():
             _operand(y, where, "y", y.dtype, self._n, dev)
         codes, scales = self._at
-        rc = lib.mlpblk_fp4_dequantize(d, codes, scales, y.data_ptr(), t.raw_stream(dev) if stream is None else _stream(stream))
+        rc = _calls.fp4_dequantize(d, codes, scales, y.data_ptr(), t.raw_stream(dev) if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
 
     def _product(self, where, b, c, accumulate, key, make):
-        """byref of the product's descriptor (made once for each key), C's address and
+        """Address of the product's descriptor (made once for each key), C's address and
         the current stream."""
         t = _Torch.get()
         dev = t.device()
@@ -885,7 +905,8 @@ class Fp4Matrix(_Kept):
         e = self._descs.get(key)
         if e is None:
             d, n = make(_dtype_code(c.dtype))
-            e = self._descs[key] = (ctypes.byref(d), n)
+            self._kept.append(d)
+            e = self._descs[key] = (ctypes.addressof(d), n)
         if c.numel() < e[1] or c.get_device() != dev or not c.is_contiguous():
             _operand(c, where, "c", c.dtype, e[1], dev)
         return e[0], c.data_ptr(), t.raw_stream(dev)
@@ -897,7 +918,7 @@ class Fp4Matrix(_Kept):
             raise MlpBlkError(MLPBLK_EINVAL, f"{where}: b is a batch")
         d, at, st = self._product(where, b, c, accumulate, None, lambda dt: (
             make_fp4_matmul_desc(self.rows, b.rows, self.cols, dt, accumulate), self.rows * b.rows))
-        rc = lib.mlpblk_fp4_matmul(d, *self._at, *b._at, at, st if stream is None else _stream(stream))
+        rc = _calls.fp4_matmul(d, *self._at, *b._at, at, st if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
 
@@ -910,7 +931,7 @@ class Fp4Matrix(_Kept):
             make_fp4_matmul_desc(self.rows, b.rows, self.cols, dt, accumulate, b.batch, sort.desc.pad, sort._entries),
             self.rows * b.rows))
         sort._where(self._dev, where)
-        rc = lib.mlpblk_fp4_matmul_grouped(d, *self._at, *b._at, sort._at[0], sort._at[1], at,
+        rc = _calls.fp4_matmul_grouped(d, *self._at, *b._at, sort._at[0], sort._at[1], at,
                                            st if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
@@ -925,7 +946,7 @@ class Fp4Matrix(_Kept):
             make_fp4_matmul_desc(self.rows, b.rows, self.cols, dt, accumulate, E, sort.desc.pad),
             E * self.rows * b.rows))
         sort._where(self._dev, where)
-        rc = lib.mlpblk_fp4_wgrad_grouped(d, *self._at, *b._at, sort._at[1], at, st if stream is None else _stream(stream))
+        rc = _calls.fp4_wgrad_grouped(d, *self._at, *b._at, sort._at[1], at, st if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
 

@@ -11,12 +11,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmlpblk.so")
+CALLS = os.path.join(HERE, "_mlpblk_calls.so")   # csrc/pycalls.c: CPython entry to the latency-bound calls
 SOURCES = ["api.cu", "gemm_fwd.cu", "gemm_bwd.cu", "rowops.cu", "simt_f32.cu", "noalloc.cu", "optim.cu", "fp8.cu", "gemm_f8.cu", "moe.cu",
            "sort.cu", "fp4.cu", "gemm_f4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -38,7 +40,29 @@ def _newest_input_mtime() -> float:
 
 
 def up_to_date() -> bool:
-    return os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input_mtime()
+    outputs = [LIB] + ([CALLS] if _python_headers() else [])
+    return all(os.path.exists(p) and os.path.getmtime(p) >= _newest_input_mtime() for p in outputs)
+
+
+def _python_headers():
+    """The directory of Python.h, or None: without it the binding makes every call
+    through ctypes."""
+    inc = sysconfig.get_paths()["include"]
+    return inc if os.path.exists(os.path.join(inc, "Python.h")) else None
+
+
+def _build_calls() -> None:
+    """csrc/pycalls.c against the library just linked (found beside it at run time)."""
+    inc = _python_headers()
+    if inc is None:
+        return
+    tmp = CALLS + ".tmp"
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-shared", "-fPIC", "-Wall", "-I", inc, os.path.join(CSRC, "pycalls.c"), "-o", tmp,
+           "-L", HERE, "-l:libmlpblk.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"pycalls.c failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
@@ -67,6 +91,7 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_calls()
     return LIB
 
 

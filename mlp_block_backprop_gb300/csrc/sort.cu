@@ -334,7 +334,7 @@ permute_kernel(const U *__restrict__ x, const int *__restrict__ pos, const int *
 // residual and y may be the same array: an element is read and written by the same
 // thread.
 template <int TX, class U, bool BF16>
-__global__ void __launch_bounds__(kMoveThreads, sizeof(U) == 16 ? 1 : 3)
+__global__ void __launch_bounds__(kMoveThreads, sizeof(U) == 16 ? 2 : 3)
 unpermute_kernel(const U *__restrict__ rows, const int *__restrict__ pos, const float *__restrict__ weights,
                  const U *residual, int64_t T, int k, int R, int units, U *y) {
     using V = Vals<U, BF16>;

@@ -560,3 +560,14 @@ def test_matrices_beyond_two_billion_elements(mb):
         i, j = slice(m - 20, m), slice(n - 200, n)
         _check(to_np(c[i, j]), fp4.rounded(to_np(a[i])), fp4.rounded(to_np(b[j])), "bf16", 64)
         _check(to_np(c[:20, j]), fp4.rounded(to_np(a[:20])), fp4.rounded(to_np(b[j])), "bf16", 64)
+
+
+def test_without_the_native_calls(mb, monkeypatch):
+    """The classes through ctypes, as on a machine without Python's headers."""
+    import types
+    names = ("moe_sort", "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
+             "fp4_quantize", "fp4_dequantize", "fp4_matmul", "fp4_matmul_grouped", "fp4_wgrad_grouped")
+    monkeypatch.setattr(mb, "_calls", types.SimpleNamespace(**{n: mb._Calls._ctypes("mlpblk_" + n) for n in names}))
+    test_experts_together(mb)
+    test_grouped_wgrad(mb, (40, 300, 200, 5, 2), True)
+    test_quantize_rows(mb, (5, 33), "f32")

@@ -206,3 +206,26 @@ def test_binding_refuses_wrong_tensors(mb):
         mb.make_sort_desc(1, 1, 1, 1, dtype="f16")
     with pytest.raises(mb.MlpBlkError):
         mb.Fp4Matrix(4, 64, codes=torch.zeros(3, dtype=torch.uint8), scales=torch.zeros(1024, dtype=torch.uint8), device="cpu")
+
+
+def test_both_ways_into_the_library_agree(mb):
+    """The CPython entry points (where built) and ctypes give the same refusals, and the
+    former check their argument count and types before they call."""
+    slow = {n: mb._Calls._ctypes("mlpblk_" + n) for n in ("moe_sort", "fp4_quantize", "fp4_matmul", "fp4_wgrad_grouped")}
+    sort, fp4, mm = mb.make_sort_desc(10, 64, 4, 2), mb.make_fp4_desc(8, 64), mb.make_fp4_matmul_desc(8, 8, 256, experts=2, pad=128)
+    at = ctypes.addressof
+    cases = [("moe_sort", (at(sort), None, 0x10000, 0x20000, 0x30000, 0x40000, None)),
+             ("moe_sort", (at(sort), 0x10000, 0x20008, 0x30000, 0x40000, 0x50000, None)),
+             ("fp4_quantize", (at(fp4), 0x10000, None, -1, 0x20000, 0x30000, None)),
+             ("fp4_quantize", (at(fp4), 0x10000, None, 0, 0x10000, 0x30000, None)),
+             ("fp4_matmul", (at(mm),) + tuple(_addresses(5)) + (None,)),
+             ("fp4_wgrad_grouped", (at(mm),) + tuple(_addresses(6)) + (None,))]
+    for name, args in cases:
+        rc = slow[name](*args)
+        assert rc in (mb.MLPBLK_EINVAL, mb.MLPBLK_ENOTSUP)
+        assert getattr(mb._calls, name)(*args) == rc, name
+    if mb._calls.native:
+        with pytest.raises(TypeError):
+            mb._calls.fp4_quantize(at(fp4), 0x10000)
+        with pytest.raises(TypeError):
+            mb._calls.fp4_quantize(at(fp4), "x", None, 0, 0x20000, 0x30000, None)
