@@ -130,13 +130,6 @@ struct Oct<true> {
         w[2] = u.z;
         w[3] = u.w;
     }
-    __device__ __forceinline__ void load_shared(const uint16_t *p) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        w[0] = u.x;
-        w[1] = u.y;
-        w[2] = u.z;
-        w[3] = u.w;
-    }
     __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
     __device__ __forceinline__ void floats(float (&v)[8]) const {
 #pragma unroll
@@ -217,18 +210,30 @@ struct Oct<false> {
     }
 };
 
-// Blocks along the source's rows.  A CTA takes 8 values of r % 32 of one 128-row scale
+// Four rows of zeros (`out`, each 32 rows behind the one before; those below `left`) and their
+// 16 bytes of every scale tile: padding between sorted segments, which is whole tiles of
+// a warp's rows where the experts' rows are few.
+__device__ __forceinline__ void zero_rows(uint8_t *out, int64_t ld, int64_t left, uint8_t *tile_scales, int col_tiles) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t u = static_cast<int64_t>(blockIdx.y) * 32 + lane; u < ld / 16; u += static_cast<int64_t>(gridDim.y) * 32)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (32 * j < left) *reinterpret_cast<uint4 *>(out + 32 * j * ld + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+    for (int g = blockIdx.y * 32 + lane; g < col_tiles; g += gridDim.y * 32)
+        *reinterpret_cast<uint4 *>(tile_scales + static_cast<int64_t>(g) * 512) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Blocks along the source's rows, float32.  A CTA takes 8 values of r % 32 of one 128-row scale
 // tile, a warp the rows r, r + 32, r + 64, r + 96, 256 columns at a time: a lane holds
 // 8 consecutive values of each row, a block is four lanes, and the four rows'
 // scales of 4 blocks are 16 consecutive bytes of a tile (one store), with the next
 // row's beside them.  The four rows' loads are in flight together.
-template <bool BF16, bool VEC, bool RELU2, bool MAP>
-__global__ void __launch_bounds__(kThreads, BF16 && VEC ? (RELU2 ? 4 : 5) : 3)
-quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
+template <bool VEC, bool RELU2, bool MAP>
+__global__ void __launch_bounds__(kThreads, 3)
+quantize_rows_kernel(const float *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
                      int64_t cols, int row_tiles, int chunks, uint8_t *__restrict__ codes,
                      uint8_t *__restrict__ scales) {
-    using T = typename std::conditional<BF16, uint16_t, float>::type;
-    __shared__ __align__(16) T turn[VEC ? 1 : kWarps][4][VEC ? 8 : 256];
+    __shared__ __align__(16) float turn[VEC ? 1 : kWarps][4][VEC ? 8 : 256];
     griddep_enter();
     const int lane = threadIdx.x & 31;
     const int64_t ld = fp4_row_bytes(cols);
@@ -236,7 +241,7 @@ quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map
     const int mat = tile / row_tiles;
     const int rr = static_cast<int>(blockIdx.x & 3) * 8 + (threadIdx.x >> 5);
     const int64_t r0 = static_cast<int64_t>(tile - mat * row_tiles) * 128 + rr;
-    const T *src[4];
+    const float *src[4];
     bool live[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -244,12 +249,16 @@ quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map
         int64_t at = r < rows ? r : -1;
         if (MAP && r < rows) at = source_row(row_map, map_div, r);
         live[j] = at >= 0;
-        src[j] = static_cast<const T *>(x) + (mat * rows + (at < 0 ? 0 : at)) * cols;
+        src[j] = x + (mat * rows + (at < 0 ? 0 : at)) * cols;
     }
     uint8_t *out = codes + (mat * rows + r0) * ld;
+    if (MAP && !(live[0] || live[1] || live[2] || live[3])) {
+        zero_rows(out, ld, rows - r0, scales + static_cast<int64_t>(tile) * chunks * 1024 + rr * 16, chunks * 2);
+        return;
+    }
     for (int chunk = blockIdx.y; chunk < chunks; chunk += gridDim.y) {
         const int64_t c = static_cast<int64_t>(chunk) * 256 + lane * 8;
-        Oct<BF16> o[4];
+        Oct<false> o[4];
         if (VEC) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -257,12 +266,12 @@ quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map
                 else o[j].zero();
             }
         } else {
-            T *mine = &turn[VEC ? 0 : threadIdx.x >> 5][0][0];
+            float *mine = &turn[VEC ? 0 : threadIdx.x >> 5][0][0];
             const int64_t c0 = static_cast<int64_t>(chunk) * 256 + lane;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) mine[j * 256 + 32 * i + lane] = live[j] && c0 + 32 * i < cols ? __ldg(src[j] + c0 + 32 * i) : T(0);
+                for (int i = 0; i < 8; ++i) mine[j * 256 + 32 * i + lane] = live[j] && c0 + 32 * i < cols ? __ldg(src[j] + c0 + 32 * i) : 0.0f;
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[j].load_shared(mine + j * 256 + lane * 8);
@@ -278,13 +287,13 @@ quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map
                 continue;
             }
             float v[8];
-            typename Oct<BF16>::Max top = Oct<BF16>::kNone;
-            o[j].template top<RELU2>(top);
+            Oct<false>::Max top = Oct<false>::kNone;
+            o[j].top<RELU2>(top);
             uint32_t m = top_bits<RELU2>(top);
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
             const uint32_t sb = scale_byte(m);
-            o[j].template scaled<RELU2>(scale_inverse(sb), v);
+            o[j].scaled<RELU2>(scale_inverse(sb), v);
             const uint32_t q = sb == 255u ? 0u : e2m1x8<RELU2>(v);
             if (c < 2 * ld) *reinterpret_cast<uint32_t *>(out + 32 * j * ld + c / 2) = q;
             // the four blocks' bytes of this half warp
@@ -300,29 +309,81 @@ quantize_rows_kernel(const void *__restrict__ x, const int *__restrict__ row_map
     }
 }
 
-// Blocks along the source's rows, rows of 768 columns and more in 16-byte accesses: a
-// lane holds a whole block (its 16-byte loads 64 or 128 bytes from its neighbour's; the
-// sectors' other halves come from L1), so a block's maximum needs no shuffle and its
-// codes are one 16-byte store.  A warp takes 1024 columns of the rows r, r + 32, r + 64,
-// r + 96 of a scale tile, two rows in flight; four lanes then transpose their 4 x 4
-// scale bytes and store 16 consecutive bytes of a tile.  8192 x 16384 bf16: 61 us with the
-// kernel above, 56 with this one (6.06 TB/s); below 24 blocks a row too many lanes idle.
-template <bool BF16, bool RELU2, bool MAP>
-__global__ void __launch_bounds__(kThreads, BF16 && !RELU2 ? 3 : 2)
-quantize_blocks_kernel(const void *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
-                       int64_t cols, int row_tiles, int chunks, uint8_t *__restrict__ codes,
+// 32 bf16 values at p, of which `left` lie before the row's end (0 behind it).  Rows that do
+// not begin on 16-byte boundaries are read in aligned 16-byte accesses all the same and
+// shifted into place by two words, one word, half a word; the access that the row's end cuts
+// is read by elements, so nothing behind the row is read.
+__device__ __forceinline__ void load_block(const uint16_t *__restrict__ p, int left, Oct<true> (&o)[4]) {
+    const int phase = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) / 2;
+    const uint16_t *a = p - phase;
+    left += phase;
+    uint32_t w[20];
+#pragma unroll
+    for (int u = 0; u < 5; ++u) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (8 * u + 8 <= left && (u < 4 || phase != 0)) v = __ldg(reinterpret_cast<const uint4 *>(a + 8 * u));
+        w[4 * u] = v.x;
+        w[4 * u + 1] = v.y;
+        w[4 * u + 2] = v.z;
+        w[4 * u + 3] = v.w;
+    }
+    if (left < 40) {
+        uint32_t t[4] = {0u, 0u, 0u, 0u};
+        const int n = left > 0 ? left & 7 : 0, at = left >> 3;
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (i < n) t[i >> 1] |= static_cast<uint32_t>(__ldg(a + 8 * at + i)) << (16 * (i & 1));
+#pragma unroll
+        for (int u = 0; u < 5; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (u == at && n > 0) w[4 * u + i] = t[i];
+    }
+    if (phase & 4) {
+#pragma unroll
+        for (int i = 0; i < 18; ++i) w[i] = w[i + 2];
+    }
+    if (phase & 2) {
+#pragma unroll
+        for (int i = 0; i < 17; ++i) w[i] = w[i + 1];
+    }
+    const int sh = (phase & 1) * 16;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i >> 2].w[i & 3] = __funnelshift_r(w[i], w[i + 1], sh);
+}
+
+// Blocks along the source's rows, bf16 rows in 16-byte accesses: a lane holds a whole
+// block (its 16-byte loads 64 bytes from its neighbour's; the sectors' other halves
+// come from L1), so a block's maximum needs no shuffle and its codes are one 16-byte
+// store.  A warp takes one column tile (128 columns) of the rows r, r + 32, r + 64, r + 96
+// of a scale tile for eight neighbouring r, two rows in flight; four lanes then transpose
+// their 4 x 4 scale bytes, and the warp stores 128 consecutive bytes of the tile.  Warps
+// are numbered along a row's tiles first, so a CTA's eight cover 2048 bytes of a row
+// and no lane idles but in a row's last 256 columns.  8192 x
+// 16384: 51 us (6.6 TB/s), ReLU^2 52, where a lane with 8 values and shuffles takes 67;
+// 192 MB in rows of 1056: 44 and 63, of 1031: 57 and 88.  (float32 gains nothing: four rows'
+// loads of 8 values take 38 us for 192 MB, blocks of 128 bytes a lane 51.)
+template <bool RELU2, bool MAP, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads, RELU2 ? 2 : 3)
+quantize_blocks_kernel(const uint16_t *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
+                       int64_t cols, int row_tiles, int col_tiles, uint32_t warps, uint8_t *__restrict__ codes,
                        uint8_t *__restrict__ scales) {
-    using T = typename std::conditional<BF16, uint16_t, float>::type;
-    constexpr int kParts = 4;                    // Octs of a block
-    constexpr int kRows = BF16 ? 2 : 1;          // rows in flight
+    constexpr int kParts = 4;  // Octs of a block
+    constexpr int kRows = 2;   // rows in flight
     griddep_enter();
     const int lane = threadIdx.x & 31;
-    const int64_t ld = fp4_row_bytes(cols);
-    const int col_tiles = chunks * 2;
-    const int tile = static_cast<int>(blockIdx.x >> 2);  // of the whole batch
+    const uint32_t w = blockIdx.x * static_cast<uint32_t>(kWarps) + (threadIdx.x >> 5);
+    if (w >= warps) return;
+    const uint32_t eight = w / col_tiles;  // rows r .. r + 7, of the whole batch
+    const int col_tile = static_cast<int>(w - eight * col_tiles);
+    const int tile = static_cast<int>(eight >> 2);
     const int mat = tile / row_tiles;
-    const int rr = static_cast<int>(blockIdx.x & 3) * 8 + (threadIdx.x >> 5);
+    const int rr = static_cast<int>(eight & 3) * 8 + (lane >> 2);
+    const int64_t ld = fp4_row_bytes(cols);
     const int64_t r0 = static_cast<int64_t>(tile - mat * row_tiles) * 128 + rr;
+    const int64_t c = static_cast<int64_t>(col_tile) * 128 + (lane & 3) * 32;
+    const uint16_t *base = x + mat * rows * cols;
+    uint8_t *out = codes + (mat * rows + r0) * ld + c / 2;
     int64_t src[4];  // source rows, -1: zeros
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -330,54 +391,53 @@ quantize_blocks_kernel(const void *__restrict__ x, const int *__restrict__ row_m
         src[j] = r < rows ? r : -1;
         if (MAP && r < rows) src[j] = source_row(row_map, map_div, r);
     }
-    const T *base = static_cast<const T *>(x) + static_cast<int64_t>(mat) * rows * cols;
-    uint8_t *out = codes + (mat * rows + r0) * ld;
-    uint8_t *st = scales + static_cast<int64_t>(tile) * col_tiles * 512 + rr * 16 + (lane & 3) * 4;
-    for (int64_t blk = static_cast<int64_t>(blockIdx.y) * 32 + lane; blk - lane < col_tiles * 4;
-         blk += static_cast<int64_t>(gridDim.y) * 32) {
-        const int64_t c = blk * 32;
-        uint32_t bytes = 0;  // of the four rows
+    uint32_t bytes = 0;  // of the four rows
 #pragma unroll
-        for (int j0 = 0; j0 < 4; j0 += kRows) {
-            Oct<BF16> o[kRows][kParts];
+    for (int j0 = 0; j0 < 4; j0 += kRows) {
+        Oct<true> o[kRows][kParts];
 #pragma unroll
-            for (int u = 0; u < kRows; ++u)
+        for (int u = 0; u < kRows; ++u) {
+            if constexpr (ALIGNED) {
 #pragma unroll
                 for (int q = 0; q < kParts; ++q) {
                     if (src[j0 + u] >= 0) o[u][q].load(base + src[j0 + u] * cols, c + 8 * q, cols);
                     else o[u][q].zero();
                 }
-#pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-                const int j = j0 + u;
-                const bool row = r0 + 32 * j < rows && c < 2 * ld;
-                if (src[j] < 0) {  // a row of zeros, or none
-                    if (row) *reinterpret_cast<uint4 *>(out + 32 * j * ld + c / 2) = make_uint4(0u, 0u, 0u, 0u);
-                    continue;
-                }
-                typename Oct<BF16>::Max top = Oct<BF16>::kNone;
-#pragma unroll
-                for (int q = 0; q < kParts; ++q) o[u][q].template top<RELU2>(top);
-                const uint32_t sb = scale_byte(top_bits<RELU2>(top));
-                const float inv = scale_inverse(sb);
-                uint32_t w[kParts];
-#pragma unroll
-                for (int q = 0; q < kParts; ++q) {
-                    float v[8];
-                    o[u][q].template scaled<RELU2>(inv, v);
-                    w[q] = sb == 255u ? 0u : e2m1x8<RELU2>(v);
-                }
-                if (row) *reinterpret_cast<uint4 *>(out + 32 * j * ld + c / 2) = make_uint4(w[0], w[1], w[2], w[3]);
-                bytes |= sb << (8 * j);
+            } else if (src[j0 + u] >= 0) {
+                load_block(base + src[j0 + u] * cols + c, static_cast<int>(min(cols - c, static_cast<int64_t>(64))), o[u]);
             }
         }
-        // byte j of lane b -> byte b of lane j, within four lanes
-        uint32_t t = __shfl_xor_sync(0xffffffffu, bytes, 1);
-        bytes = (lane & 1) ? __byte_perm(bytes, t, 0x3715) : __byte_perm(bytes, t, 0x6240);
-        t = __shfl_xor_sync(0xffffffffu, bytes, 2);
-        bytes = (lane & 2) ? __byte_perm(bytes, t, 0x3276) : __byte_perm(bytes, t, 0x5410);
-        if (blk < col_tiles * 4) *reinterpret_cast<uint32_t *>(st + (blk >> 2) * 512) = bytes;
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int j = j0 + u;
+            const bool row = r0 + 32 * j < rows && c < 2 * ld;
+            if (src[j] < 0) {  // a row of zeros, or none
+                if (row) *reinterpret_cast<uint4 *>(out + 32 * j * ld) = make_uint4(0u, 0u, 0u, 0u);
+                continue;
+            }
+            Oct<true>::Max top = Oct<true>::kNone;
+#pragma unroll
+            for (int q = 0; q < kParts; ++q) o[u][q].template top<RELU2>(top);
+            const uint32_t sb = scale_byte(top_bits<RELU2>(top));
+            const float inv = scale_inverse(sb);
+            uint32_t v4[kParts];
+#pragma unroll
+            for (int q = 0; q < kParts; ++q) {
+                float v[8];
+                o[u][q].template scaled<RELU2>(inv, v);
+                v4[q] = sb == 255u ? 0u : e2m1x8<RELU2>(v);
+            }
+            if (row) *reinterpret_cast<uint4 *>(out + 32 * j * ld) = make_uint4(v4[0], v4[1], v4[2], v4[3]);
+            bytes |= sb << (8 * j);
+        }
     }
+    // byte j of lane b -> byte b of lane j, within four lanes
+    uint32_t t = __shfl_xor_sync(0xffffffffu, bytes, 1);
+    bytes = (lane & 1) ? __byte_perm(bytes, t, 0x3715) : __byte_perm(bytes, t, 0x6240);
+    t = __shfl_xor_sync(0xffffffffu, bytes, 2);
+    bytes = (lane & 2) ? __byte_perm(bytes, t, 0x3276) : __byte_perm(bytes, t, 0x5410);
+    *reinterpret_cast<uint32_t *>(scales + (static_cast<int64_t>(tile) * col_tiles + col_tile) * 512 + rr * 16 +
+                                  (lane & 3) * 4) = bytes;
 }
 
 // Two neighbouring values of a source row, columns c and c + 1 (0 at and behind
@@ -493,22 +553,27 @@ quantize_cols_kernel(const void *__restrict__ x, const int *__restrict__ row_map
     for (int chunk = blockIdx.y; chunk < chunks; chunk += gridDim.y) {
         const int64_t c0 = static_cast<int64_t>(chunk) * 256 + wid * 32;  // Q's first column of this warp: x's row
         Pair<BF16> p[32];
+        bool none = false;  // no row of x is live: zeros without the arithmetic
         if (MAP == 2) {
             const int64_t own = c0 + lane;
             const int mine = own < cols ? source_row(row_map, map_div, own) : -1;
+            none = !__any_sync(0xffffffffu, mine >= 0);
+            if (!none) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int src = __shfl_sync(0xffffffffu, mine, i);
-                p[i].template load<VEC>(base + (src < 0 ? 0 : src) * rows, src < 0 ? rows : col, rows);
+                for (int i = 0; i < 32; ++i) {
+                    const int src = __shfl_sync(0xffffffffu, mine, i);
+                    p[i].template load<VEC>(base + (src < 0 ? 0 : src) * rows, src < 0 ? rows : col, rows);
+                }
             }
         } else if (MAP == 1) {
             const int64_t own = c0 + lane;
             const unsigned live = __ballot_sync(0xffffffffu, own < cols && row_map[own < cols ? own : 0] >= 0);
             const T *row = base + c0 * rows;
+            none = live == 0u;
             if (live == 0xffffffffu) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i, row += rows) p[i].template load<VEC>(row, col, rows);
-            } else {
+            } else if (!none) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const bool in = live >> i & 1u;
@@ -527,9 +592,9 @@ quantize_cols_kernel(const void *__restrict__ x, const int *__restrict__ row_map
                 p[i].template load<VEC>(in ? row + i * rows : base, in ? col : rows, rows);
             }
         }
-        uint32_t sa, sb;
-        uint4 qa, qb;
-        quantize_pairs<BF16, RELU2>(p, qa, qb, sa, sb);
+        uint32_t sa = 0, sb = 0;
+        uint4 qa = make_uint4(0u, 0u, 0u, 0u), qb = qa;
+        if (MAP == 0 || !none) quantize_pairs<BF16, RELU2>(p, qa, qb, sa, sb);
         *reinterpret_cast<uint4 *>(&sc[2 * lane][wid * 16]) = qa;
         *reinterpret_cast<uint4 *>(&sc[2 * lane + 1][wid * 16]) = qb;
         ss[2 * lane][wid] = static_cast<uint8_t>(sa);
@@ -555,104 +620,130 @@ quantize_cols_kernel(const void *__restrict__ x, const int *__restrict__ row_map
     }
 }
 
-// 8 codes -> 8 values (exact), times the block's scale.
-__device__ __forceinline__ void decode8(uint32_t u, float scale, float (&v)[8]) {
+// 8 codes -> their values in bf16 (exact), the first in the lowest half.  A code's three low
+// bits select the two bytes of its size from tables (four codes a byte permutation); the
+// fourth, that permutation's sign mode, makes a byte of ones of a set sign byte.
+__device__ __forceinline__ void decode8(uint32_t u, uint32_t (&v)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t h;
-        asm("{\n"
-            "  .reg .b8 a, b, c, d;\n"
-            "  mov.b32 {a, b, c, d}, %1;\n"
-            "  cvt.rn.f16x2.e2m1x2 %0, a;\n"
-            "}\n"
-            : "=r"(h)
-            : "r"(u >> (8 * i)));
-        float lo, hi;
-        asm("{\n .reg .f16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}\n"
-            : "=f"(lo), "=f"(hi)
-            : "r"(h));
-        v[2 * i] = lo * scale;
-        v[2 * i + 1] = hi * scale;
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t c = h == 0 ? u : u >> 16, size = c & 0x7777u;
+        const uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, size);  // 0 .5 1 1.5 | 2 3 4 6
+        uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, size);
+        uint32_t sign;  // 0x80 or, of a negative code, 0xFF
+        asm("prmt.b32 %0, %1, %1, %2;" : "=r"(sign) : "r"(0x80808080u), "r"(c));
+        hi |= (sign << 7) & 0x80808080u;
+        v[2 * h] = __byte_perm(lo, hi, 0x5140);
+        v[2 * h + 1] = __byte_perm(lo, hi, 0x7362);
     }
 }
 
-__device__ __forceinline__ float scale_value(uint32_t byte) {
-    if (byte == 255u) return __uint_as_float(0x7FC00000u);
-    return byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
+// A scale in bf16, in both halves.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
+    const uint32_t m = byte == 255u ? 0x7FC0u : (byte == 0u ? 0x0040u : byte << 7);
+    return m | (m << 16);
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-
-// A warp per row, 1024 columns at a time: a lane takes 8 values of each 256, 4 bytes of
-// codes and their block's scale byte, with four of them in flight.
+// A warp takes kDeqChunks pieces of 256 values, numbered along the rows, with the
+// pieces' loads in flight together: a lane 8 values of each, 4 bytes of codes and their
+// block's scale byte.  bf16 rows of whole 16-byte accesses are stored from registers.
+// float32 values, and rows of any length, cross shared memory, so that neighbouring
+// lanes store neighbouring words (two float4 stores 32 bytes apart take 51 us where this
+// takes 36, 192 MB of values; bf16 rows of 4097: 66, instruction issue).
 constexpr int kDeqChunks = 4;
 
-template <bool BF16, bool VEC>
+template <bool BF16, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads)
 dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows, int64_t cols,
-                  int64_t all_rows, int row_tiles, int chunks, void *__restrict__ y) {
+                  int row_tiles, int pieces, uint32_t all_pieces, void *__restrict__ y) {
     using T = typename std::conditional<BF16, uint16_t, float>::type;
-    __shared__ __align__(16) float turn[VEC ? 1 : kWarps][VEC ? 4 : 256];
+    constexpr bool kTurn = !(BF16 && ALIGNED);
+    __shared__ __align__(16) T turn[kTurn ? kWarps : 1][kTurn ? 256 : 8];
     griddep_enter();
     const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (row >= all_rows) return;
-    const int64_t mat = row / rows, r = row - mat * rows, ld = fp4_row_bytes(cols);
-    const uint8_t *in = codes + row * ld + lane * 4;
-    const uint8_t *sc = scales + (mat * row_tiles + r / 128) * chunks * 1024 + (lane >> 4) * 512 + (r % 32) * 16 +
-                        (r % 128) / 32 * 4 + ((lane >> 2) & 3);
-    T *out = static_cast<T *>(y) + row * cols;
-    for (int g = blockIdx.y * kDeqChunks; g < chunks; g += gridDim.y * kDeqChunks) {
-        uint32_t u[kDeqChunks], sb[kDeqChunks];
+    const uint32_t p0 = (blockIdx.x * static_cast<uint32_t>(kWarps) + (threadIdx.x >> 5)) * kDeqChunks;
+    if (p0 >= all_pieces) return;
+    const int64_t ld = fp4_row_bytes(cols);
+    const int64_t tile_row = fp4_col_tiles(cols) * kFp4TileBytes;  // bytes of a row of scale tiles
+    uint32_t row = p0 / pieces;
+    uint32_t piece = p0 - row * pieces;
+    uint32_t mat = row / static_cast<uint32_t>(rows), r = row - mat * static_cast<uint32_t>(rows);
+    const uint8_t *in, *sc;  // of the row, this lane's
+    T *out;                  // the row's
+    auto start_row = [&]() {
+        in = codes + row * ld + lane * 4;
+        sc = scales + (static_cast<int64_t>(mat) * row_tiles + (r >> 7)) * tile_row + (lane >> 4) * kFp4TileBytes +
+             (r & 31) * 16 + (r >> 5 & 3) * 4 + ((lane >> 2) & 3);
+        out = static_cast<T *>(y) + row * cols;
+    };
+    start_row();
+    T *to[kDeqChunks];      // the piece's first value
+    int count[kDeqChunks];  // of its values
+    uint32_t u[kDeqChunks], sb[kDeqChunks];
 #pragma unroll
-        for (int j = 0; j < kDeqChunks; ++j) {
-            const int64_t c = static_cast<int64_t>(g + j) * 256 + lane * 8;
-            u[j] = sb[j] = 0u;
-            if (c < cols) {
-                u[j] = __ldg(reinterpret_cast<const uint32_t *>(in + static_cast<int64_t>(g + j) * 128));
-                sb[j] = __ldg(sc + static_cast<int64_t>(g + j) * 1024);
-            }
+    for (int j = 0; j < kDeqChunks; ++j) {
+        to[j] = out + static_cast<int64_t>(piece) * 256;
+        count[j] = p0 + j < all_pieces ? static_cast<int>(min(cols - static_cast<int64_t>(piece) * 256, static_cast<int64_t>(256))) : 0;
+        u[j] = sb[j] = 0u;
+        if (lane * 8 < count[j]) {
+            u[j] = __ldg(reinterpret_cast<const uint32_t *>(in + static_cast<int64_t>(piece) * 128));
+            sb[j] = __ldg(sc + static_cast<int64_t>(piece) * (2 * kFp4TileBytes));
         }
-#pragma unroll
-        for (int j = 0; j < kDeqChunks; ++j) {
-            const int64_t c = static_cast<int64_t>(g + j) * 256 + lane * 8;
-            if (g + j >= chunks) break;
-            if (!VEC) {
-                // rows of any length: through shared memory, so that neighbouring lanes
-                // store neighbouring columns
-                float v[8];
-                decode8(u[j], scale_value(sb[j]), v);
-                float *mine = &turn[VEC ? 0 : threadIdx.x >> 5][0];
-                *reinterpret_cast<float4 *>(mine + lane * 8) = make_float4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<float4 *>(mine + lane * 8 + 4) = make_float4(v[4], v[5], v[6], v[7]);
-                __syncwarp();
-                const int64_t c0 = static_cast<int64_t>(g + j) * 256 + lane;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float f = mine[32 * i + lane];
-                    if (c0 + 32 * i < cols) {
-                        if (BF16) reinterpret_cast<uint16_t *>(out)[c0 + 32 * i] = static_cast<uint16_t>(pack2(f, 0.0f) & 0xFFFFu);
-                        else reinterpret_cast<float *>(out)[c0 + 32 * i] = f;
-                    }
-                }
-                __syncwarp();
-                continue;
+        if (++piece == static_cast<uint32_t>(pieces)) {
+            piece = 0;
+            ++row;
+            if (++r == static_cast<uint32_t>(rows)) {
+                r = 0;
+                ++mat;
             }
-            if (c >= cols) continue;
-            float v[8];
-            decode8(u[j], scale_value(sb[j]), v);
-            if (BF16) {
-                *reinterpret_cast<uint4 *>(out + c) =
-                    make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-            } else {
-                *reinterpret_cast<float4 *>(out + c) = make_float4(v[0], v[1], v[2], v[3]);
-                if (c + 4 < cols) *reinterpret_cast<float4 *>(out + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
-            }
+            start_row();
         }
+    }
+#pragma unroll
+    for (int j = 0; j < kDeqChunks; ++j) {
+        const int n = count[j];
+        if (n == 0) break;
+        // the products are exact: a power of two times at most two bits, down to 2^-128
+        uint32_t v[4];
+        decode8(u[j], v);
+        const uint32_t scale = scale_pair(sb[j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = mul_bf16x2(v[i], scale);
+        if (!kTurn) {
+            if (lane * 8 < n) *reinterpret_cast<uint4 *>(to[j] + lane * 8) = make_uint4(v[0], v[1], v[2], v[3]);
+            continue;
+        }
+        T *mine = turn[kTurn ? threadIdx.x >> 5 : 0];
+        if constexpr (BF16) {
+            *reinterpret_cast<uint4 *>(mine + lane * 8) = make_uint4(v[0], v[1], v[2], v[3]);
+        } else {
+            *reinterpret_cast<float4 *>(mine + lane * 8) = make_float4(bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1]));
+            *reinterpret_cast<float4 *>(mine + lane * 8 + 4) = make_float4(bf16_lo(v[2]), bf16_hi(v[2]), bf16_lo(v[3]), bf16_hi(v[3]));
+        }
+        __syncwarp();
+        if constexpr (BF16) {
+            // pairs from the first 4-byte boundary on
+            const uint32_t *words = reinterpret_cast<const uint32_t *>(mine);
+            const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(to[j]) >> 1 & 1);
+            if (odd && lane == 0) to[j][0] = mine[0];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = 32 * i + lane, c = 2 * k + odd;
+                uint32_t w = words[k];
+                if (odd) w = __funnelshift_r(w, words[k < 127 ? k + 1 : k], 16);
+                if (c + 1 < n) *reinterpret_cast<uint32_t *>(to[j] + c) = w;
+                else if (c < n) to[j][c] = static_cast<uint16_t>(w & 0xFFFFu);
+            }
+        } else if (ALIGNED) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (128 * i + lane * 4 < n)
+                    *reinterpret_cast<float4 *>(to[j] + 128 * i + lane * 4) = *reinterpret_cast<const float4 *>(mine + 128 * i + lane * 4);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (32 * i + lane < n) to[j][32 * i + lane] = mine[32 * i + lane];
+        }
+        __syncwarp();
     }
 }
 
@@ -681,14 +772,18 @@ int quantize_typed(const void *x, const int *row_map, int map_div, int64_t rows,
         return launch_pdl(kern, grid_for(static_cast<int64_t>(row_tiles) * 2 * batch, chunks), dim3(kThreads), 0, s, x,
                           row_map, map_div, rows, cols, row_tiles, chunks, codes, scales);
     }
-    if (cols * (BF16 ? 2 : 4) % 16 == 0 && cols >= 768)
-        return launch_pdl(quantize_blocks_kernel<BF16, RELU2, MAP != 0>,
-                          grid_for(static_cast<int64_t>(row_tiles) * 4 * batch, (chunks + 3) / 4), dim3(kThreads), 0, s, x, row_map,
-                          map_div, rows, cols, row_tiles, chunks, codes, scales);
-    auto kern = cols * (BF16 ? 2 : 4) % 16 == 0 ? quantize_rows_kernel<BF16, true, RELU2, MAP != 0>
-                                                : quantize_rows_kernel<BF16, false, RELU2, MAP != 0>;
-    return launch_pdl(kern, grid_for(static_cast<int64_t>(row_tiles) * 4 * batch, chunks), dim3(kThreads), 0, s, x,
-                      row_map, map_div, rows, cols, row_tiles, chunks, codes, scales);
+    if constexpr (BF16) {
+        const int64_t warps = static_cast<int64_t>(row_tiles) * batch * 4 * chunks * 2;
+        if (warps >= static_cast<int64_t>(1) << 31) return MLPBLK_EINVAL;  // of 4096 values: larger than the device's memory
+        return launch_pdl(cols % 8 == 0 ? quantize_blocks_kernel<RELU2, MAP != 0, true> : quantize_blocks_kernel<RELU2, MAP != 0, false>,
+                          dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), dim3(kThreads), 0, s,
+                          static_cast<const uint16_t *>(x), row_map, map_div, rows, cols, row_tiles, chunks * 2,
+                          static_cast<uint32_t>(warps), codes, scales);
+    } else {
+        auto kern = cols % 4 == 0 ? quantize_rows_kernel<true, RELU2, MAP != 0> : quantize_rows_kernel<false, RELU2, MAP != 0>;
+        return launch_pdl(kern, grid_for(static_cast<int64_t>(row_tiles) * 4 * batch, chunks), dim3(kThreads), 0, s,
+                          static_cast<const float *>(x), row_map, map_div, rows, cols, row_tiles, chunks, codes, scales);
+    }
 }
 
 template <bool BF16>
@@ -710,11 +805,15 @@ int quantize_dtype(const void *x, const int *row_map, int map_div, int64_t rows,
 template <bool BF16>
 int dequantize_typed(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, int batch, void *y,
                      cudaStream_t s) {
-    const int row_tiles = static_cast<int>((rows + 127) / 128), chunks = static_cast<int>((cols + 255) / 256);
-    const int64_t all = rows * batch;
-    auto kern = cols * (BF16 ? 2 : 4) % 16 == 0 ? dequantize_kernel<BF16, true> : dequantize_kernel<BF16, false>;
-    return launch_pdl(kern, grid_for((all + kWarps - 1) / kWarps, (chunks + kDeqChunks - 1) / kDeqChunks), dim3(kThreads), 0,
-                      s, codes, scales, rows, cols, all, row_tiles, chunks, y);
+    const int row_tiles = static_cast<int>((rows + 127) / 128);
+    const bool aligned = cols * (BF16 ? 2 : 4) % 16 == 0;
+    const int pieces = static_cast<int>((cols + 255) / 256);
+    const int64_t all = rows * batch * pieces;
+    if (all >= static_cast<int64_t>(1) << 31) return MLPBLK_EINVAL;  // more than 2^38 codes: larger than the device's memory
+    constexpr int kCta = kWarps * kDeqChunks;
+    return launch_pdl(aligned ? dequantize_kernel<BF16, true> : dequantize_kernel<BF16, false>,
+                      dim3(static_cast<unsigned>((all + kCta - 1) / kCta)), dim3(kThreads), 0, s, codes, scales, rows, cols,
+                      row_tiles, pieces, static_cast<uint32_t>(all), y);
 }
 
 }  // namespace

@@ -117,6 +117,58 @@ def test_quantize_relu2_and_special_values(mb, transposed):
         np.testing.assert_array_equal(to_np(y), fp4.rounded(a))
 
 
+@pytest.mark.parametrize("act", ["none", "relu2"])
+@pytest.mark.parametrize("shape", [(9, 33), (40, 31), (130, 7), (33, 258), (64, 289), (70, 1031), (17, 2049), (5, 1028)])
+def test_rows_that_begin_anywhere(mb, shape, act):
+    """bf16 rows of every alignment, with NaN right behind the matrix: what is not the
+    row's reaches no code; values read back stop at the matrix's end."""
+    import torch
+    rows, cols = shape
+    buf = torch.full((rows * cols + 64,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    x, v = _draw(np.random.default_rng(cols), shape, "bf16")
+    v[rows // 2, cols // 2:] = np.inf
+    buf[:rows * cols] = torch.from_numpy(v.astype(np.float32)).cuda().to(torch.bfloat16).reshape(-1)
+    a = v if act == "none" else np.where(v < 0, 0.0, v * v)
+    q = mb.Fp4Matrix(rows, cols)
+    q.codes.fill_(0xAA)
+    q.scales.fill_(0xAA)
+    q.quantize(buf[:rows * cols].view(rows, cols), act=act)
+    packed, tiled = fp4.pack(*fp4.quantize(a))
+    np.testing.assert_array_equal(_bytes(q.scales), tiled)
+    mask = 0xFF if act == "none" else 0x77
+    np.testing.assert_array_equal(_bytes(q.codes) & mask, packed & mask)
+    for dt in ("bf16", "f32"):
+        y = torch.full((rows * cols + 64,), 7.0, dtype=_dt(dt), device="cuda")
+        q.dequantize(y[:rows * cols].view(rows, cols))
+        np.testing.assert_array_equal(to_np(y[:rows * cols]).reshape(shape), fp4.rounded(a))
+        assert (y[rows * cols:] == 7.0).all()
+
+
+@pytest.mark.parametrize("cols", [32, 31, 64])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_read_back_every_code_and_scale(mb, dtype, cols):
+    import torch
+    q = mb.Fp4Matrix(256, cols)
+    r = np.arange(256)
+    scales = np.zeros((2, 2, 512), dtype=np.uint8)          # row r has the scale byte r in each of its blocks
+    for b in range(4):
+        scales[r // 128, 0, r % 32 * 16 + r % 128 // 32 * 4 + b] = r
+    nib = np.arange(cols + 32) % 16
+    q.scales.copy_(torch.from_numpy(scales.reshape(-1)).cuda())
+    ld = (cols + 31) // 32 * 16
+    row = (nib[0:2 * ld:2] | nib[1:2 * ld:2] << 4).astype(np.uint8)
+    q.codes.copy_(torch.from_numpy(np.tile(row, (256, 1))).cuda().reshape(q.codes.shape))
+    y = torch.empty(256, cols, dtype=_dt(dtype), device="cuda")
+    q.dequantize(y)
+    size = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+    ref = (np.where(nib[:cols] < 8, 1.0, -1.0) * size[nib[:cols] % 8])[None, :] * np.exp2(r - 127.0)[:, None]
+    ref[255] = np.nan
+    with np.errstate(over="ignore"):
+        ref = ref.astype(np.float32)                        # beyond 2^128: infinite
+    np.testing.assert_array_equal(to_np(y), ref)
+    np.testing.assert_array_equal(np.signbit(to_np(y)[:255]), np.signbit(ref[:255]))
+
+
 def test_quantize_batch(mb):
     import torch
     x, v = _draw(np.random.default_rng(4), (3 * 130, 72), "bf16")
@@ -151,9 +203,10 @@ def _routed(mb, T, width, E, k, pad, seed, dead=()):
 
 @pytest.mark.parametrize("transposed", [False, True])
 @pytest.mark.parametrize("gather", [False, True])
-def test_quantize_through_a_sort(mb, transposed, gather):
+@pytest.mark.parametrize("shape", [(45, 90, 5, 2, 128), (6, 301, 40, 2, 256), (37, 1032, 9, 3, 128)])
+def test_quantize_through_a_sort(mb, shape, transposed, gather):
     import torch
-    T, d, E, k, pad = 45, 90, 5, 2, 128
+    T, d, E, k, pad = shape
     s, (count, seg, pos, row_map) = _routed(mb, T, d, E, k, pad, 5)
     R = s.rows
     x, v = _draw(np.random.default_rng(6), (T if gather else R, d), "bf16")
