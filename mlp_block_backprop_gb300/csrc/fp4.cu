@@ -356,14 +356,14 @@ __device__ __forceinline__ void load_block(const uint16_t *__restrict__ p, int l
 // block (its 16-byte loads 64 bytes from its neighbour's; the sectors' other halves
 // come from L1), so a block's maximum needs no shuffle and its codes are one 16-byte
 // store.  A warp takes one column tile (128 columns) of the rows r, r + 32, r + 64, r + 96
-// of a scale tile for eight neighbouring r, two rows in flight; four lanes then transpose
-// their 4 x 4 scale bytes, and the warp stores 128 consecutive bytes of the tile.  Warps
-// are numbered along a row's tiles first, so a CTA's eight cover 2048 bytes of a row
-// and no lane idles but in a row's last 256 columns.  8192 x
-// 16384: 51 us (6.6 TB/s), ReLU^2 52, where a lane with 8 values and shuffles takes 67;
-// 192 MB in rows of 1056: 44 and 63, of 1031: 57 and 88.  (float32 gains nothing: four rows'
+// of a scale tile for eight neighbouring r, two rows in flight (HALVES 2: two of the four
+// rows alone); four lanes then transpose their 4 x 4 scale bytes, and the warp stores 128
+// consecutive bytes of the tile.  Warps are numbered along a row's tiles first, so a
+// CTA's eight cover 2048 bytes of a row and no lane idles but in a row's last 256
+// columns.  8192 x 16384: 51 us (6.6 TB/s), ReLU^2 52, where a lane with 8 values and
+// shuffles takes 67; 192 MB in rows of 1056: 44 and 63, of 1031: 57 and 88.  (float32 gains nothing: four rows'
 // loads of 8 values take 38 us for 192 MB, blocks of 128 bytes a lane 51.)
-template <bool RELU2, bool MAP, bool ALIGNED>
+template <bool RELU2, bool MAP, bool ALIGNED, int HALVES>
 __global__ void __launch_bounds__(kThreads, RELU2 ? 2 : 3)
 quantize_blocks_kernel(const uint16_t *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
                        int64_t cols, int row_tiles, int col_tiles, uint32_t warps, uint8_t *__restrict__ codes,
@@ -372,8 +372,10 @@ quantize_blocks_kernel(const uint16_t *__restrict__ x, const int *__restrict__ r
     constexpr int kRows = 2;   // rows in flight
     griddep_enter();
     const int lane = threadIdx.x & 31;
-    const uint32_t w = blockIdx.x * static_cast<uint32_t>(kWarps) + (threadIdx.x >> 5);
+    uint32_t w = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     if (w >= warps) return;
+    const int own = HALVES == 2 ? static_cast<int>(w & 1u) : -1;  // the half of the four rows, -1: both
+    w /= HALVES;
     const uint32_t eight = w / col_tiles;  // rows r .. r + 7, of the whole batch
     const int col_tile = static_cast<int>(w - eight * col_tiles);
     const int tile = static_cast<int>(eight >> 2);
@@ -394,6 +396,7 @@ quantize_blocks_kernel(const uint16_t *__restrict__ x, const int *__restrict__ r
     uint32_t bytes = 0;  // of the four rows
 #pragma unroll
     for (int j0 = 0; j0 < 4; j0 += kRows) {
+        if (own >= 0 && own != j0 / kRows) continue;
         Oct<true> o[kRows][kParts];
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
@@ -436,8 +439,9 @@ quantize_blocks_kernel(const uint16_t *__restrict__ x, const int *__restrict__ r
     bytes = (lane & 1) ? __byte_perm(bytes, t, 0x3715) : __byte_perm(bytes, t, 0x6240);
     t = __shfl_xor_sync(0xffffffffu, bytes, 2);
     bytes = (lane & 2) ? __byte_perm(bytes, t, 0x3276) : __byte_perm(bytes, t, 0x5410);
-    *reinterpret_cast<uint32_t *>(scales + (static_cast<int64_t>(tile) * col_tiles + col_tile) * 512 + rr * 16 +
-                                  (lane & 3) * 4) = bytes;
+    if (own < 0 || own == (lane & 3) / kRows)
+        *reinterpret_cast<uint32_t *>(scales + (static_cast<int64_t>(tile) * col_tiles + col_tile) * 512 + rr * 16 +
+                                      (lane & 3) * 4) = bytes;
 }
 
 // Two neighbouring values of a source row, columns c and c + 1 (0 at and behind
@@ -660,7 +664,7 @@ dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__
     __shared__ __align__(16) T turn[kTurn ? kWarps : 1][kTurn ? 256 : 8];
     griddep_enter();
     const int lane = threadIdx.x & 31;
-    const uint32_t p0 = (blockIdx.x * static_cast<uint32_t>(kWarps) + (threadIdx.x >> 5)) * kDeqChunks;
+    const uint32_t p0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kDeqChunks;
     if (p0 >= all_pieces) return;
     const int64_t ld = fp4_row_bytes(cols);
     const int64_t tile_row = fp4_col_tiles(cols) * kFp4TileBytes;  // bytes of a row of scale tiles
@@ -763,6 +767,20 @@ dim3 grid_for(int64_t x, int64_t most) {
     return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y < 1 ? 1 : y));
 }
 
+// Where there are at most this many warps an SM, quantize_blocks_kernel deals a warp's four
+// rows out to two (bf16 from L2, 2048 x 2048: 5.8 us with one warp and 3.5 with two, 4096 x
+// 4096: 6.8 and 6.4; 8192 x 16384 from HBM, ReLU^2: 53 and 57).
+constexpr int64_t kHalfWarps = 32;
+
+// Warps of a CTA for kernels whose warps are independent: fewer than kWarps where that
+// spreads few warps over the SMs (118 x 6624: 2.7 us, with CTAs of eight 3.5).
+int warps_per_cta(int64_t warps) {
+    const int sms = sm_total();
+    int w = 1;
+    while (w < kWarps && warps > static_cast<int64_t>(sms) * w) w *= 2;
+    return w;
+}
+
 template <bool BF16, bool RELU2, int MAP>
 int quantize_typed(const void *x, const int *row_map, int map_div, int64_t rows, int64_t cols, int batch,
                    bool transposed, uint8_t *codes, uint8_t *scales, cudaStream_t s) {
@@ -773,10 +791,14 @@ int quantize_typed(const void *x, const int *row_map, int map_div, int64_t rows,
                           row_map, map_div, rows, cols, row_tiles, chunks, codes, scales);
     }
     if constexpr (BF16) {
-        const int64_t warps = static_cast<int64_t>(row_tiles) * batch * 4 * chunks * 2;
+        int64_t warps = static_cast<int64_t>(row_tiles) * batch * 4 * chunks * 2;
         if (warps >= static_cast<int64_t>(1) << 31) return MLPBLK_EINVAL;  // of 4096 values: larger than the device's memory
-        return launch_pdl(cols % 8 == 0 ? quantize_blocks_kernel<RELU2, MAP != 0, true> : quantize_blocks_kernel<RELU2, MAP != 0, false>,
-                          dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), dim3(kThreads), 0, s,
+        const int halves = warps <= static_cast<int64_t>(sm_total()) * kHalfWarps ? 2 : 1;
+        warps *= halves;
+        const int w = warps_per_cta(warps);
+        auto kern = halves == 2 ? (cols % 8 == 0 ? quantize_blocks_kernel<RELU2, MAP != 0, true, 2> : quantize_blocks_kernel<RELU2, MAP != 0, false, 2>)
+                                : (cols % 8 == 0 ? quantize_blocks_kernel<RELU2, MAP != 0, true, 1> : quantize_blocks_kernel<RELU2, MAP != 0, false, 1>);
+        return launch_pdl(kern, dim3(static_cast<unsigned>((warps + w - 1) / w)), dim3(32 * w), 0, s,
                           static_cast<const uint16_t *>(x), row_map, map_div, rows, cols, row_tiles, chunks * 2,
                           static_cast<uint32_t>(warps), codes, scales);
     } else {
@@ -810,9 +832,10 @@ int dequantize_typed(const uint8_t *codes, const uint8_t *scales, int64_t rows, 
     const int pieces = static_cast<int>((cols + 255) / 256);
     const int64_t all = rows * batch * pieces;
     if (all >= static_cast<int64_t>(1) << 31) return MLPBLK_EINVAL;  // more than 2^38 codes: larger than the device's memory
-    constexpr int kCta = kWarps * kDeqChunks;
+    const int w = warps_per_cta((all + kDeqChunks - 1) / kDeqChunks);
+    const int64_t per_cta = static_cast<int64_t>(w) * kDeqChunks;
     return launch_pdl(aligned ? dequantize_kernel<BF16, true> : dequantize_kernel<BF16, false>,
-                      dim3(static_cast<unsigned>((all + kCta - 1) / kCta)), dim3(kThreads), 0, s, codes, scales, rows, cols,
+                      dim3(static_cast<unsigned>((all + per_cta - 1) / per_cta)), dim3(32 * w), 0, s, codes, scales, rows, cols,
                       row_tiles, pieces, static_cast<uint32_t>(all), y);
 }
 
