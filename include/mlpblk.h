@@ -490,7 +490,7 @@ int mlpblk_moe_unpermute_backward(const mlpblk_sort_desc *desc, const void *dy, 
  *           the low half; columns behind cols are zero codes
  *   scales: tiles of 128 rows x 4 blocks (128 columns), 512 bytes each; the byte of
  *           row r, block b inside a tile is (r % 32) * 16 + (r / 32) * 4 + b (the
- *           order in which the tensor core's scale copies want them); the tiles of
+ *           order in which tensor memory holds them); the tiles of
  *           128 rows follow one another along the columns, 2 * ceil(cols / 256) of
  *           them (an even count; bytes of rows and blocks that do not exist are 0)
  *
@@ -508,8 +508,9 @@ int mlpblk_moe_unpermute_backward(const mlpblk_sort_desc *desc, const void *dy, 
  * mlpblk_fp4_dequantize: y[batch, rows, cols] in desc->dtype (exact in both types).
  *   transposed and act must be 0.
  * Limits: rows, cols >= 0 (with either 0: MLPBLK_OK, nothing is touched),
- * rows * batch and cols < 2^31, ceil(rows / 128) * batch < 2^29; pointers 16-byte
- * aligned.
+ * rows * batch and cols < 2^31, ceil(rows / 128) * batch < 2^29, ceil(rows / 128) *
+ * batch * ceil(cols / 256) < 2^28 (275 GB of scales), rows * batch * ceil(cols / 256)
+ * < 2^31; pointers 16-byte aligned.
  */
 #define MLPBLK_FP4_ACT_NONE   0
 #define MLPBLK_FP4_ACT_RELU2  1

@@ -1309,6 +1309,8 @@ int check_fp4_desc(const mlpblk_fp4_desc *d) {
     if (d->rows < 0 || d->cols < 0 || d->batch < 1 || d->cols >= kFp4Lim) return MLPBLK_EINVAL;
     if (d->rows > 0 && d->batch >= kFp4Lim / d->rows) return MLPBLK_EINVAL;
     if ((d->rows + 127) / 128 * d->batch >= kFp4Lim / 4) return MLPBLK_EINVAL;  // CTAs of a launch
+    const int64_t pieces = (d->cols + 255) / 256;  // of a row: warps of a launch
+    if ((d->rows + 127) / 128 * d->batch * pieces >= kFp4Lim / 8 || d->rows * d->batch * pieces >= kFp4Lim) return MLPBLK_EINVAL;
     return MLPBLK_OK;
 }
 

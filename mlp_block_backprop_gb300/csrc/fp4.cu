@@ -792,7 +792,6 @@ int quantize_typed(const void *x, const int *row_map, int map_div, int64_t rows,
     }
     if constexpr (BF16) {
         int64_t warps = static_cast<int64_t>(row_tiles) * batch * 4 * chunks * 2;
-        if (warps >= static_cast<int64_t>(1) << 31) return MLPBLK_EINVAL;  // of 4096 values: larger than the device's memory
         const int halves = warps <= static_cast<int64_t>(sm_total()) * kHalfWarps ? 2 : 1;
         warps *= halves;
         const int w = warps_per_cta(warps);
@@ -831,7 +830,6 @@ int dequantize_typed(const uint8_t *codes, const uint8_t *scales, int64_t rows, 
     const bool aligned = cols * (BF16 ? 2 : 4) % 16 == 0;
     const int pieces = static_cast<int>((cols + 255) / 256);
     const int64_t all = rows * batch * pieces;
-    if (all >= static_cast<int64_t>(1) << 31) return MLPBLK_EINVAL;  // more than 2^38 codes: larger than the device's memory
     const int w = warps_per_cta((all + kDeqChunks - 1) / kDeqChunks);
     const int64_t per_cta = static_cast<int64_t>(w) * kDeqChunks;
     return launch_pdl(aligned ? dequantize_kernel<BF16, true> : dequantize_kernel<BF16, false>,

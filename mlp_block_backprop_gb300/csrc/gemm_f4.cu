@@ -573,7 +573,8 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
                     for (int j = 0; j < 32; ++j) dump[(c0 + j) * 128 + i] = v[j];
                 } else {
-                    store_columns<OUT>(args.c, w.c_row + c0, args.n, w.n0 + i, v, w.m_valid - c0, ok && i < w.n_valid);
+                    store_columns<OUT>(args.c, w.c_row + c0, args.n, w.n0 + i, v, w.m_valid - c0,
+                                       ok && i < w.n_valid && (OUT != 2 || some));
                 }
             }
             tc_fence_before_sync();
@@ -589,7 +590,8 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     // columns rank, rank + cs, ...: eight at a time, their remote loads in flight together
                     constexpr int kCols = 8;
                     constexpr int kHalves = C::kEpiWarps / 4;
-                    for (int c0 = rank + half * kCols * cs; c0 < w.m_valid; c0 += kHalves * kCols * cs) {
+                    const int c_all = OUT == 2 && nk == 0 ? 0 : w.m_valid;  // 0: nothing to add
+                    for (int c0 = rank + half * kCols * cs; c0 < c_all; c0 += kHalves * kCols * cs) {
                         float sum[kCols];
                         const int64_t at = (w.c_row + c0) * args.n + w.n0 + i;
 #pragma unroll
@@ -903,6 +905,7 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         int it = 0;
         for (; t < tiles; next()) {
             const bool some = w.kb0 < w.kb1;
+            if (OUT == 2 && !some) continue;  // nothing to add
             const int buf = it & 1;
             if (some) {
                 const bool ok = mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort_flag);

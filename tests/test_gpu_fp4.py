@@ -127,6 +127,7 @@ def test_rows_that_begin_anywhere(mb, shape, act):
     buf = torch.full((rows * cols + 64,), float("nan"), dtype=torch.bfloat16, device="cuda")
     x, v = _draw(np.random.default_rng(cols), shape, "bf16")
     v[rows // 2, cols // 2:] = np.inf
+    v[rows - 1, 0] = np.nan
     buf[:rows * cols] = torch.from_numpy(v.astype(np.float32)).cuda().to(torch.bfloat16).reshape(-1)
     a = v if act == "none" else np.where(v < 0, 0.0, v * v)
     q = mb.Fp4Matrix(rows, cols)

@@ -153,7 +153,7 @@ def test_fp4_sizes_and_refusals(mb):
     q = lambda d, x=0x10000, rm=None, div=0, c=0x20000, s=0x30000: mb.lib.mlpblk_fp4_quantize(ctypes.byref(d), x, rm, div, c, s, None)
     good = mb.make_fp4_desc(8, 64)
     for bad in (mb.make_fp4_desc(-1, 64), mb.make_fp4_desc(8, -1), mb.make_fp4_desc(8, 64, 0), mb.make_fp4_desc(1 << 30, 64, 2),
-                mb.make_fp4_desc(8, 1 << 31)):
+                mb.make_fp4_desc(8, 1 << 31), mb.make_fp4_desc(1 << 16, (1 << 31) - 1), mb.make_fp4_desc(1, 257, 1 << 28)):
         assert q(bad) == mb.MLPBLK_EINVAL
     assert q(mb.Fp4Desc(8, 64, 1, 3, 0, 0)) == mb.MLPBLK_ENOTSUP
     assert q(mb.make_fp4_desc(8, 64, act=2)) == mb.MLPBLK_ENOTSUP
