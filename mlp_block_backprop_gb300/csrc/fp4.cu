@@ -554,8 +554,36 @@ quantize_cols_kernel(const void *__restrict__ x, const int *__restrict__ row_map
     const int64_t r0 = static_cast<int64_t>(half) * kTCols;  // Q's first row
     const int64_t col = r0 + 2 * lane;                       // x's column
     const T *base = static_cast<const T *>(x) + mat * rows * cols;
+    auto live_at = [&](int64_t chunk) {  // this thread's row of x of a chunk
+        const int64_t own = chunk * 256 + threadIdx.x;
+        return own < cols && row_map[own] >= 0;
+    };
+    bool live_here = MAP != 0 && live_at(blockIdx.y);
     for (int chunk = blockIdx.y; chunk < chunks; chunk += gridDim.y) {
         const int64_t c0 = static_cast<int64_t>(chunk) * 256 + wid * 32;  // Q's first column of this warp: x's row
+        if (MAP != 0) {
+            // padding alone (an expert's segment is mostly that where its rows are few):
+            // zeros without the way through shared memory.  The barrier is also the one
+            // between the chunk before and the writes below.
+            const bool any = __syncthreads_or(live_here);
+            live_here = live_at(chunk + static_cast<int64_t>(gridDim.y));
+            if (!any) {
+#pragma unroll
+                for (int h = 0; h < kTCols * 8 / kThreads; ++h) {
+                    const int q = threadIdx.x + h * kThreads;
+                    const int64_t at = static_cast<int64_t>(chunk) * 128 + (q & 7) * 16;
+                    if (r0 + (q >> 3) < rows && at < ld)
+                        *reinterpret_cast<uint4 *>(codes + (mat * rows + r0 + (q >> 3)) * ld + at) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                if (threadIdx.x < kTCols * 2) {
+                    const int rt = (half & 1) * 64 + (threadIdx.x >> 1);
+                    const int64_t tile = static_cast<int64_t>(mat) * row_tiles + half / 2;
+                    *reinterpret_cast<uint32_t *>(scales + ((tile * chunks + chunk) * 2 + (threadIdx.x & 1)) * 512 + (rt % 32) * 16 +
+                                                  (rt / 32) * 4) = 0u;
+                }
+                continue;
+            }
+        }
         Pair<BF16> p[32];
         bool none = false;  // no row of x is live: zeros without the arithmetic
         if (MAP == 2) {
@@ -620,7 +648,7 @@ quantize_cols_kernel(const void *__restrict__ x, const int *__restrict__ row_map
             *reinterpret_cast<uint32_t *>(scales + ((tile * chunks + chunk) * 2 + g) * 512 + (rt % 32) * 16 + (rt / 32) * 4) =
                 *reinterpret_cast<const uint32_t *>(&ss[r][g * 4]);
         }
-        __syncthreads();
+        if (MAP == 0) __syncthreads();
     }
 }
 

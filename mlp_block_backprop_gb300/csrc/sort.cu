@@ -22,6 +22,9 @@ namespace {
 constexpr int kSortExperts = 256;
 constexpr int kSortCluster = 8;        // CTAs of a large plan (the portable cluster size)
 constexpr int64_t kSortOneCta = 4096;  // entries up to which one CTA makes the plan
+constexpr int64_t kSortOneRows = 9216; // and sorted rows, most of which it only marks as empty (4096 entries of 128 experts
+                                       // padded to 256: 10.3 us, with a cluster 6.2; 384 of 64 padded to 128: 4.6 and 5.0)
+constexpr int64_t kSortSmallRows = 4096;
 constexpr int64_t kSortSmall = 64;     // entries up to which that CTA has 8 warps, not 32 (16 entries: 3.6 us and 4.1;
                                        // 384 of 64 experts, whose padding is most of the work: 6.2 and 5.2)
 
@@ -525,8 +528,8 @@ MoveShape move_shape(int64_t T, int64_t width, int dtype, int experts, int pad, 
 
 int launch_sort(const int *idx, int64_t n, int experts, int pad, int64_t R, int *count, int *seg, int *pos,
                 int *row_map, cudaStream_t s) {
-    const int C = n <= kSortOneCta ? 1 : kSortCluster;
-    const int warps = n <= kSortSmall ? 8 : 32;
+    const int C = n <= kSortOneCta && R <= kSortOneRows ? 1 : kSortCluster;
+    const int warps = n <= kSortSmall && R <= kSortSmallRows ? 8 : 32;
     int64_t per_warp = (n + static_cast<int64_t>(C) * warps - 1) / (static_cast<int64_t>(C) * warps);
     per_warp = (per_warp + 31) / 32 * 32;
     cudaLaunchConfig_t cfg = {};
