@@ -196,7 +196,9 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
 
 // A row is `units` accesses of type U (16, 4 or 2 bytes: the widest that divides
 // a row), a CTA kMoveThreads / TX rows of TX threads.  A thread holds several accesses
-// at a time, TX apart: enough bytes in flight where they are short.  TX is a constant,
+// at a time, TX apart: enough bytes in flight where they are short; TX (32, 64 or 128) is
+// the least that covers a row so, that no thread's accesses lie behind it (16384 x 2048
+// bf16, top-2, unpermute: 68 us with 128 threads, 46 with 64).  TX is a constant,
 // so a row's addresses are one pointer and immediate offsets (the plan, both moves and
 // both gradients of 4097 x 1001 float32, top-6: 140 us with 64-bit indices throughout, 122
 // so; 16384 x 4096 bf16, top-2: 342 and 325).
@@ -513,7 +515,7 @@ MoveShape move_shape(int64_t T, int64_t width, int dtype, int experts, int pad, 
     m.unit = bytes % 16 == 0 ? 16 : (bytes % 4 == 0 ? 4 : 2);
     m.units = static_cast<int>(bytes / m.unit);
     const int p = m.unit == 16 ? per16 : per;
-    m.tx = m.units <= 32 * p ? 32 : 128;
+    m.tx = m.units <= 32 * p ? 32 : (m.units <= 64 * p ? 64 : 128);
     m.block = dim3(m.tx, kMoveThreads / m.tx, 1);
     const int64_t blocks = (T + m.block.y - 1) / m.block.y;
     const int64_t steps = slots ? slots : (m.units + m.tx * p - 1) / (m.tx * p);
@@ -554,7 +556,7 @@ int launch_permute(const void *x, const int *pos, const int *count, const int *s
     const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerOf<uint4>, kPerOf<uint32_t>, 0);
     const dim3 grid(static_cast<unsigned>(m.token_blocks + m.pad_blocks));
 #define MLPBLK_PERMUTE(U)                                                                                      \
-    return launch_pdl(m.tx == 32 ? permute_kernel<32, U> : permute_kernel<128, U>, grid, m.block, 0, s,         \
+    return launch_pdl(m.tx == 32 ? permute_kernel<32, U> : m.tx == 64 ? permute_kernel<64, U> : permute_kernel<128, U>, grid, m.block, 0, s,         \
                       static_cast<const U *>(x), pos, count, seg, T, k,                                        \
                       experts, m.slices, static_cast<int>(R), m.units, m.parts, m.token_blocks, static_cast<U *>(rows))
     if (m.unit == 16) MLPBLK_PERMUTE(uint4);
@@ -568,7 +570,9 @@ int launch_unpermute(const void *rows, const int *pos, const float *weights, con
     const MoveShape m = move_shape(T, width, dtype, 1, 1, kPerOf<uint4>, kPerOf<uint32_t>, 0);
     const dim3 grid(static_cast<unsigned>(m.token_blocks));
 #define MLPBLK_UNPERMUTE(U, B)                                                                              \
-    return launch_pdl(m.tx == 32 ? unpermute_kernel<32, U, B> : unpermute_kernel<128, U, B>, grid, m.block, 0, s, static_cast<const U *>(rows), pos, weights, \
+    return launch_pdl(m.tx == 32 ? unpermute_kernel<32, U, B>                                               \
+                      : m.tx == 64 ? unpermute_kernel<64, U, B> : unpermute_kernel<128, U, B>,              \
+                      grid, m.block, 0, s, static_cast<const U *>(rows), pos, weights,                      \
                       static_cast<const U *>(residual), T, k, static_cast<int>(R), m.units, m.parts, static_cast<U *>(y))
     if (dtype == MLPBLK_BF16) {
         if (m.unit == 16) MLPBLK_UNPERMUTE(uint4, true);
@@ -588,7 +592,9 @@ int launch_unpermute_bwd(const void *dy, const void *rows, const int *pos, const
                                    (k + slots - 1) / slots);
     const dim3 grid(static_cast<unsigned>(m.token_blocks + m.pad_blocks));
 #define MLPBLK_UNPERMUTE_BWD(U, B)                                                                               \
-    return launch_pdl(m.tx == 32 ? unpermute_bwd_kernel<32, U, B> : unpermute_bwd_kernel<128, U, B>, grid, m.block, 0, s, static_cast<const U *>(dy),                 \
+    return launch_pdl(m.tx == 32 ? unpermute_bwd_kernel<32, U, B>                                                \
+                      : m.tx == 64 ? unpermute_bwd_kernel<64, U, B> : unpermute_bwd_kernel<128, U, B>,           \
+                      grid, m.block, 0, s, static_cast<const U *>(dy),                                           \
                       static_cast<const U *>(rows), pos, count, seg, weights, T, k, experts, m.slices, static_cast<int>(R), m.units,  \
                       m.parts, m.token_blocks, static_cast<U *>(d_rows), d_weights)
     if (dtype == MLPBLK_BF16) {
