@@ -11,9 +11,9 @@
 // tcgen05.cp would do it without them, but it runs in the MMAs' pipe (8192 x 16384 x
 // 4096: 226 us with it, 172 without; one token x 16384 x 4096: 10.5 us and 8.9).
 //
-// f4_small: one CTA computes a 128 x BN tile with B's rows (C's columns) on the 128
+// f4_small: one CTA computes a 128 x 128 tile with B's rows (C's columns) on the 128
 //   lanes and A's rows (tokens) on the columns, so that few tokens cost few
-//   columns: at one token the kernel streams the weights.  C leaves straight from
+//   columns (32 or 64): at one token the kernel streams the weights.  C leaves straight from
 //   registers: 32 lanes are 32 consecutive elements of a row of C, whatever n is.
 //   K can be split over a cluster; the parts meet in distributed shared memory and
 //   are added in rank order.
@@ -259,18 +259,16 @@ __device__ __forceinline__ F4Tile f4_tile(const F4Args &a, const F4Groups *g, in
 
 // ------------------------------------------------------------------- f4_small
 
-// BN columns: 32 for up to 32 tokens, 128 beyond.  A's scale tile holds 128 rows, so
-// a tile of 32 tokens starts at a multiple of 128 (there is only one).  A tile of the
-// 128-column kernel that has 32 or 64 rows at most loads and multiplies no more (the
-// experts of a batch of a few hundred tokens).  SPLIT: K may be split over a cluster.
-// With 32 columns two CTAs fit an SM, so the next product's set-up and prefetch run
-// beside this one's end.
-template <int BN_, bool SPLIT_>
+// 128 columns: a tile that has 32 or 64 rows of A at most loads and multiplies no more (a
+// kernel with 32 columns and two CTAs an SM, four stages each, was slower everywhere: one
+// token x 16384 x 4096 7.8 us and 6.1, 8 x 2048 x 2048 4.6 and 3.2).  SPLIT: K is split
+// over a cluster, whose sum takes shared memory from the stages.
+template <bool SPLIT_>
 struct F4Small {
-    static constexpr int BN = BN_;
+    static constexpr int BN = 128;
     static constexpr bool SPLIT = SPLIT_;
-    static constexpr int kEpiWarps = BN == 128 ? 8 : 4;  // two a lane quarter: 64 columns each
-    static constexpr int kEpiCols = BN == 128 ? 64 : 32;
+    static constexpr int kEpiWarps = 8;            // two a lane quarter: 64 columns each
+    static constexpr int kEpiCols = 64;
     static constexpr int kThreads = 64 + 32 * kEpiWarps + 128 + 32;  // codes, MMA, epilogue, four scale warps, scale loads
     static constexpr int kScaleLoadWarp = kThreads / 32 - 1;
     static constexpr int kLBytes = 128 * 128;      // B's rows, on the lanes
@@ -279,22 +277,18 @@ struct F4Small {
     static constexpr int kStageBytes = kLBytes + kRBytes + 2 * kSfBytes;
     static constexpr int kDumpBytes = SPLIT ? BN * 128 * 4 : 0;  // an fp32 tile, for the cluster's sum
     static constexpr int kCtrlBytes = 4096;
-    static constexpr int kBudget = BN == 128 ? kSmemLimit : 112 * 1024;
-    static constexpr int kStages = (kBudget - 1024 - kCtrlBytes - kDumpBytes) / kStageBytes;
+    static constexpr int kStages = (kSmemLimit - 1024 - kCtrlBytes - kDumpBytes) / kStageBytes;
     static constexpr int kSmemBytes = 1024 + kCtrlBytes + kDumpBytes + kStages * kStageBytes;
     // TMEM: two accumulators, then each stage's scales (8 columns each operand)
     static constexpr int kSfCol = 2 * BN;
     static constexpr int kSfSet = 16;
-    static constexpr uint32_t kTmemCols = kSfCol + kStages * kSfSet <= 256 ? 256u : 512u;
+    static constexpr uint32_t kTmemCols = 512;
     static_assert(kStages >= 3 && kSfCol + kStages * kSfSet <= 512, "pipeline");
     static_assert(sizeof(F4Groups) + 512 <= kCtrlBytes, "control block");
 };
 
 // Columns that a tile's loads and MMAs cover.
-template <int BN>
-__device__ __forceinline__ int f4_width(const F4Tile &w) {
-    return w.m_valid <= 32 ? 32 : (w.m_valid <= 64 ? 64 : BN);
-}
+__device__ __forceinline__ int f4_width(const F4Tile &w) { return w.m_valid <= 32 ? 32 : (w.m_valid <= 64 ? 64 : 128); }
 
 // 32 columns of a tile out of a lane's registers: column j goes to C's row row0 + j,
 // lane i to its column col0 + i; `rows` of the columns and the lanes with `on` are stored.
@@ -395,7 +389,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         *abort_flag = 0;
         fence_barrier_init();
         prefetch_tensormap(&tmA);
-        if (C::BN > 32) prefetch_tensormap(&tmA32);
+        prefetch_tensormap(&tmA32);
         prefetch_tensormap(&tmB);
     }
     if (warp == 1) {
@@ -437,7 +431,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         for (; ok && t < tiles; next()) {
             const int nk = w.kb1 - w.kb0;
             const int k0 = w.kb0 + nk * rank / cs, k1 = w.kb0 + nk * (rank + 1) / cs;
-            const int wide = f4_width<C::BN>(w);
+            const int wide = f4_width(w);
             for (int kb = k0; kb < k1; ++kb) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag));
                 if (!ok) break;
@@ -484,7 +478,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t d = tmem_base + buf * C::BN;
-            const uint32_t idesc = idesc_mxf4(128, f4_width<C::BN>(w), 0);
+            const uint32_t idesc = idesc_mxf4(128, f4_width(w), 0);
             for (int kb = k0; kb < k1; ++kb) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort_flag));
                 if (!ok) break;
@@ -1024,8 +1018,7 @@ int run_small(F4Args a, const Fp4Product &p, int cs, int workers, cudaStream_t s
     CUtensorMap mA, mA32, mB;
     const int64_t a_rows = p.m, b_rows = p.mode == kFp4GroupRows ? p.n * p.experts : p.n;
     if (!make_map_codes(&mA, p.a, a_rows, p.k, C::BN) || !make_map_codes(&mB, p.b, b_rows, p.k, 128)) return MLPBLK_ECUDA;
-    mA32 = mA;
-    if (C::BN > 32 && !make_map_codes(&mA32, p.a, a_rows, p.k, 32)) return MLPBLK_ECUDA;
+    if (!make_map_codes(&mA32, p.a, a_rows, p.k, 32)) return MLPBLK_ECUDA;
     static int attr_set[64] = {0};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1164,24 +1157,28 @@ int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s) {
         if (!p.accumulate) return tma ? run_pair<1, true>(a, p, w, s) : run_pair<1, false>(a, p, w, s);
         return tma ? run_pair<2, true>(a, p, w, s) : run_pair<2, false>(a, p, w, s);
     }
-    const bool few = rows <= 32;
-    const int64_t bn = few ? 32 : 128;
-    const int64_t tiles = (rows + bn - 1) / bn * ((p.n + 127) / 128) * groups;
+    // K is split where that saves more of its stages than the cluster's sum costs: 4 us for
+    // 128 columns, 1.5 for up to 32.  A stage takes 0.15 us, twice that where rows of codes
+    // begin at no 128-byte line (each of its 256 rows is then two requests of the copies):
+    // 128 x 128 x 8192 7.3 us whole and 7.8 split, x 16384 12.3 and 8.4; 118 x 192 x 6624
+    // 11.3 and 8.9; one token x 1024 x 4096 4.3 and 4.7, x 8192 6.6 and 5.2.
+    const int64_t tiles = (rows + 127) / 128 * ((p.n + 127) / 128) * groups;
+    const int64_t stages = a.kblocks * (fp4_row_bytes(p.k) % 128 != 0 ? 2 : 1);
     int cs = 1;
-    while (cs < 8 && tiles * cs * 2 <= num_sms && a.kblocks >= 8 * cs) cs *= 2;
+    if (stages >= (rows <= 32 ? 32 : 40))
+        while (cs < 8 && tiles * cs * 2 <= num_sms && stages >= 8 * cs) cs *= 2;
     int64_t workers = num_sms / cs;
     if (workers < 1) workers = 1;
     if (p.mode != kFp4GroupRows && tiles < workers) workers = tiles;
     const int w = static_cast<int>(workers);
-#define MLPBLK_SMALL(BN, SPLIT)                                               \
-    {                                                                         \
-        if (!f32) return run_small<F4Small<BN, SPLIT>, 0>(a, p, cs, w, s);    \
-        if (!p.accumulate) return run_small<F4Small<BN, SPLIT>, 1>(a, p, cs, w, s); \
-        return run_small<F4Small<BN, SPLIT>, 2>(a, p, cs, w, s);              \
+#define MLPBLK_SMALL(SPLIT)                                                     \
+    {                                                                           \
+        if (!f32) return run_small<F4Small<SPLIT>, 0>(a, p, cs, w, s);          \
+        if (!p.accumulate) return run_small<F4Small<SPLIT>, 1>(a, p, cs, w, s); \
+        return run_small<F4Small<SPLIT>, 2>(a, p, cs, w, s);                    \
     }
-    if (few) MLPBLK_SMALL(32, true)
-    if (cs > 1) MLPBLK_SMALL(128, true)
-    MLPBLK_SMALL(128, false)
+    if (cs > 1) MLPBLK_SMALL(true)
+    MLPBLK_SMALL(false)
 #undef MLPBLK_SMALL
 }
 
