@@ -20,6 +20,8 @@
 // f4_pair: two CTAs on two SMs compute a 256 x 256 tile (cta_group::2), A's rows on the
 //   lanes; each CTA stages 128 rows of A and of B, and the scales of its A rows and
 //   of all 256 columns.
+#include <type_traits>
+
 #include "fp4_layout.h"
 #include "gemm_tc.cuh"
 
@@ -965,26 +967,34 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                             bulk_commit_group();
                         }
                     } else {
-                        // rows of any length: a row at a time, neighbouring lanes neighbouring columns
+                        // rows of any length: eight rows at a time, neighbouring lanes neighbouring
+                        // columns
                         __syncwarp();
                         const int n_rows = min(32, w.m_valid - rt);
-                        for (int r = 0; r < n_rows; ++r) {
-                            const int64_t at = (w.c_row + rt + r) * args.n;
-                            const uint8_t *row = st + r * 128;
+                        using E = typename std::conditional<OUT == 0, uint16_t, float>::type;
+                        E *out = static_cast<E *>(args.c) + (w.c_row + rt) * args.n + c0 + lane;
+#pragma unroll 1
+                        for (int r0 = 0; r0 < n_rows; r0 += 8, out += 8 * args.n) {
+                            E e[8][kCols / 32];
+                            float old[8];
 #pragma unroll
-                            for (int u = 0; u < kCols / 32; ++u) {
-                                const int c = lane + 32 * u;
-                                if (c0 + c >= args.n) continue;
-                                const int byte = c * (OUT == 0 ? 2 : 4);
-                                const uint8_t *p = row + ((((byte >> 4) ^ (r & 7)) << 4) | (byte & 15));
-                                if (OUT == 0) {
-                                    static_cast<uint16_t *>(args.c)[at + c0 + c] = *reinterpret_cast<const uint16_t *>(p);
-                                } else {
-                                    float *o = static_cast<float *>(args.c) + at + c0 + c;
-                                    const float f = *reinterpret_cast<const float *>(p);
-                                    *o = OUT == 2 ? *o + f : f;
+                            for (int r = 0; r < 8; ++r)
+#pragma unroll
+                                for (int u = 0; u < kCols / 32; ++u) {
+                                    const int byte = (lane + 32 * u) * static_cast<int>(sizeof(E));
+                                    e[r][u] = *reinterpret_cast<const E *>(st + (r0 + r) * 128 + ((((byte >> 4) ^ r) << 4) | (byte & 15)));
                                 }
+                            if (OUT == 2) {
+#pragma unroll
+                                for (int r = 0; r < 8; ++r)
+                                    old[r] = r0 + r < n_rows && c0 + lane < args.n ? static_cast<float>(out[r * args.n]) : 0.0f;
                             }
+#pragma unroll
+                            for (int r = 0; r < 8; ++r)
+#pragma unroll
+                                for (int u = 0; u < kCols / 32; ++u)
+                                    if (r0 + r < n_rows && c0 + lane + 32 * u < args.n)
+                                        out[r * args.n + 32 * u] = OUT == 2 ? static_cast<E>(old[r] + static_cast<float>(e[r][u])) : e[r][u];
                         }
                         __syncwarp();
                     }
@@ -1145,13 +1155,19 @@ int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s) {
     }
     // 256 x 256 pair tiles where they occupy half of the SM pairs and, grouped by rows, an
     // expert has more than one 128-row tile on average (1500 tokens, top-4 of 60 experts
-    // of 776 x 1000: 13.8 us in pair tiles)
+    // of 776 x 1000: 13.8 us in pair tiles, 8.4 in small ones).  A single round of them
+    // needs 16 stages to make up for its longer start and end (2048 x 2048 x 1024 4.8 us
+    // in small tiles, 5.8 in pair tiles; x 4096 9.3 and 9.3; x 8192 15.1 and 13.8), and
+    // float32 rows that are not whole 16-byte pieces 6 (8192 x 4095 x 1024 33 and 41 us,
+    // x 4096 63 and 55).
     const int pairs = num_sms / 2;
     const int64_t mean_rows = p.mode == kFp4GroupRows ? rows / p.experts : rows;
     const int64_t pair_tiles = p.mode == kFp4GroupRows ? ((mean_rows + 255) / 256) * p.experts * ((p.n + 255) / 256)
                                                        : (rows + 255) / 256 * groups * ((p.n + 255) / 256);
-    if (pairs >= 1 && mean_rows > 128 && 2 * pair_tiles >= pairs) {
-        const bool tma = p.n * (f32 ? 4 : 2) % 16 == 0;
+    const bool tma = p.n * (f32 ? 4 : 2) % 16 == 0;
+    const int stages_of_tile = p.mode == kFp4GroupK ? a.kblocks / p.experts : a.kblocks;
+    const int least = pair_tiles <= pairs ? 16 : (f32 && !tma ? 6 : 0);
+    if (pairs >= 1 && mean_rows > 128 && 2 * pair_tiles >= pairs && stages_of_tile >= least) {
         const int w = static_cast<int>(p.mode != kFp4GroupRows && pair_tiles < pairs ? pair_tiles : pairs);
         if (!f32) return tma ? run_pair<0, true>(a, p, w, s) : run_pair<0, false>(a, p, w, s);
         if (!p.accumulate) return tma ? run_pair<1, true>(a, p, w, s) : run_pair<1, false>(a, p, w, s);
