@@ -206,9 +206,10 @@ constexpr int kMoveThreads = 256;
 template <class U>
 constexpr int kPerOf = sizeof(U) == 16 ? 4 : 8;      // permute, unpermute
 template <class U>
-constexpr int kSlotsOf = sizeof(U) == 16 ? 2 : 4;    // slots whose rows the gradient loads together
+constexpr int kSlotsOf = sizeof(U) == 4 ? 4 : 2;     // slots whose rows the gradient loads together
 template <class U>
-constexpr int kPerBwdOf = sizeof(U) == 16 ? 2 : 4;   // unpermute's gradient (16384 x 4096 bf16, top-2: 98 us)
+constexpr int kPerBwdOf = sizeof(U) == 16 ? 2 : (sizeof(U) == 4 ? 4 : 8);  // unpermute's gradient (16384 x 4096 bf16,
+                                                                           // top-2: 98 us; x 2049: 134, 181 with 4 and 4 slots)
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
@@ -509,12 +510,17 @@ struct MoveShape {
 constexpr int64_t kFewBlocks = 152;
 constexpr int64_t kSliceBytes = 32768;
 
-MoveShape move_shape(int64_t T, int64_t width, int dtype, int experts, int pad, int per16, int per, int slots) {
+int access_bytes(int64_t width, int dtype) {
+    const int64_t bytes = width * (dtype == MLPBLK_BF16 ? 2 : 4);
+    return bytes % 16 == 0 ? 16 : (bytes % 4 == 0 ? 4 : 2);
+}
+
+MoveShape move_shape(int64_t T, int64_t width, int dtype, int experts, int pad, int per16, int per4, int per2, int slots) {
     MoveShape m;
     const int64_t bytes = width * (dtype == MLPBLK_BF16 ? 2 : 4);
-    m.unit = bytes % 16 == 0 ? 16 : (bytes % 4 == 0 ? 4 : 2);
+    m.unit = access_bytes(width, dtype);
     m.units = static_cast<int>(bytes / m.unit);
-    const int p = m.unit == 16 ? per16 : per;
+    const int p = m.unit == 16 ? per16 : (m.unit == 4 ? per4 : per2);
     m.tx = m.units <= 32 * p ? 32 : (m.units <= 64 * p ? 64 : 128);
     m.block = dim3(m.tx, kMoveThreads / m.tx, 1);
     const int64_t blocks = (T + m.block.y - 1) / m.block.y;
@@ -553,7 +559,7 @@ int launch_sort(const int *idx, int64_t n, int experts, int pad, int64_t R, int 
 
 int launch_permute(const void *x, const int *pos, const int *count, const int *seg, int64_t T, int64_t width,
                    int dtype, int k, int experts, int pad, int64_t R, void *rows, cudaStream_t s) {
-    const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerOf<uint4>, kPerOf<uint32_t>, 0);
+    const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerOf<uint4>, kPerOf<uint32_t>, kPerOf<uint16_t>, 0);
     const dim3 grid(static_cast<unsigned>(m.token_blocks + m.pad_blocks));
 #define MLPBLK_PERMUTE(U)                                                                                      \
     return launch_pdl(m.tx == 32 ? permute_kernel<32, U> : m.tx == 64 ? permute_kernel<64, U> : permute_kernel<128, U>, grid, m.block, 0, s,         \
@@ -567,7 +573,7 @@ int launch_permute(const void *x, const int *pos, const int *count, const int *s
 
 int launch_unpermute(const void *rows, const int *pos, const float *weights, const void *residual, int64_t T,
                      int64_t width, int dtype, int k, int64_t R, void *y, cudaStream_t s) {
-    const MoveShape m = move_shape(T, width, dtype, 1, 1, kPerOf<uint4>, kPerOf<uint32_t>, 0);
+    const MoveShape m = move_shape(T, width, dtype, 1, 1, kPerOf<uint4>, kPerOf<uint32_t>, kPerOf<uint16_t>, 0);
     const dim3 grid(static_cast<unsigned>(m.token_blocks));
 #define MLPBLK_UNPERMUTE(U, B)                                                                              \
     return launch_pdl(m.tx == 32 ? unpermute_kernel<32, U, B>                                               \
@@ -587,8 +593,9 @@ int launch_unpermute(const void *rows, const int *pos, const float *weights, con
 int launch_unpermute_bwd(const void *dy, const void *rows, const int *pos, const int *count, const int *seg,
                          const float *weights, int64_t T, int64_t width, int dtype, int k, int experts, int pad, int64_t R,
                          void *d_rows, float *d_weights, cudaStream_t s) {
-    const int slots = width * (dtype == MLPBLK_BF16 ? 2 : 4) % 16 == 0 ? kSlotsOf<uint4> : kSlotsOf<uint32_t>;
-    const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerBwdOf<uint4>, kPerBwdOf<uint32_t>,
+    const int unit = access_bytes(width, dtype);
+    const int slots = unit == 16 ? kSlotsOf<uint4> : (unit == 4 ? kSlotsOf<uint32_t> : kSlotsOf<uint16_t>);
+    const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerBwdOf<uint4>, kPerBwdOf<uint32_t>, kPerBwdOf<uint16_t>,
                                    (k + slots - 1) / slots);
     const dim3 grid(static_cast<unsigned>(m.token_blocks + m.pad_blocks));
 #define MLPBLK_UNPERMUTE_BWD(U, B)                                                                               \

@@ -68,6 +68,8 @@ MOVES = [(1, 8, 2, 1, 1), (5, 1, 3, 2, 4), (37, 1002, 5, 3, 16), (64, 1001, 4, 6
          (9, 5000, 3, 9, 8), (300, 64, 60, 4, 128), (17, 12288, 2, 2, 2),
          # few tokens, whose rows are shared by CTAs, and much padding
          (20, 3051, 85, 7, 128), (3, 20001, 200, 7, 256), (1, 4097, 4, 4, 1024), (151, 9002, 4, 5, 3),
+         # the smallest rows
+         (1, 1, 1, 1, 1), (3, 1, 2, 2, 1), (2, 3, 2, 1, 1), (7, 5, 3, 2, 2),
          # many tokens, long rows, many slots
          (1300, 1024, 6, 2, 16), (1250, 1027, 5, 6, 1), (700, 6001, 3, 3, 4), (1300, 520, 20, 15, 1), (1300, 1040, 20, 16, 1)]
 
