@@ -619,8 +619,8 @@ def mlpblk_moe_unpermute_backward(desc, dy, rows, pos, count, seg, weights, d_ro
 class _Kept:
     """Base of the classes that keep device buffers of their own: the buffers cannot
     be replaced, so their addresses are taken once and a call checks only what it is
-    given.  A call of these classes costs about 3 us of host time on a Grace core, 2 of them
-    in the library (launches included): the checks of the common case stand in the
+    given.  A call of these classes costs 2.3 to 3.4 us of host time on a Grace core, 1.5 of
+    them the runtime's launch: the checks of the common case stand in the
     methods themselves, _operand only words the refusal."""
 
     def _where(self, dev, where):
@@ -650,71 +650,93 @@ class MoeSort(_Kept):
         self._d = ctypes.addressof(self.desc)
         self._at = tuple(t.data_ptr() for t in (self._count, self._seg, self._pos, self._row_map))
         self._entries, self._x_n, self._r_n = tokens * top_k, tokens * width, self.rows * width
-        self._type = _Torch.get().row[self.desc.dtype]
+        self._t = _Torch.get()
+        self._type = self._t.row[self.desc.dtype]
 
     count = property(lambda self: self._count)
     seg = property(lambda self: self._seg)
     pos = property(lambda self: self._pos)
     row_map = property(lambda self: self._row_map)
 
-    def _check_all(self, where, tensors):
-        """The addresses of (tensor or None, name, dtype, elements), or a refusal; then
-        the device, which is the tensors' own."""
-        t = _Torch.get()
-        dev = t.device()
-        if dev != self._dev:
-            self._where(dev, where)
-        out = [None if x is None else x.data_ptr()
-               if x.dtype is dt and x.numel() >= n and x.get_device() == dev and x.is_contiguous()
-               else _operand(x, where, name, dt, n, dev) for x, name, dt, n in tensors]
-        out.append(t.raw_stream(dev))
-        return out
+    def _at_of(self, x, where, name, dtype, numel, dev):
+        """The address of a tensor, or a refusal; None is None."""
+        if x is None:
+            return None
+        if x.dtype is dtype and x.numel() >= numel and x.get_device() == dev and x.is_contiguous():
+            return x.data_ptr()
+        return _operand(x, where, name, dtype, numel, dev)
 
     def sort(self, expert_idx, stream=None):
         where = "MoeSort.sort"
-        idx, st = self._check_all(where, ((expert_idx, "expert_idx", _Torch.get().int32, self._entries),))
+        t = self._t
+        dev = t.device()
+        if dev != self._dev:
+            self._where(dev, where)
+        if (expert_idx.dtype is not t.int32 or expert_idx.numel() < self._entries or expert_idx.get_device() != dev
+                or not expert_idx.is_contiguous()):
+            _operand(expert_idx, where, "expert_idx", t.int32, self._entries, dev)
         count, seg, pos, row_map = self._at
-        rc = _calls.moe_sort(self._d, idx, count, seg, pos, row_map, st if stream is None else _stream(stream))
+        rc = _calls.moe_sort(self._d, expert_idx.data_ptr(), count, seg, pos, row_map,
+                             t.raw_stream(dev) if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
 
     def permute(self, x, rows, stream=None):
         where = "MoeSort.permute"
-        dt = self._type
-        x, rows, st = self._check_all(where, ((x, "x", dt, self._x_n), (rows, "rows", dt, self._r_n)))
+        t, dt = self._t, self._type
+        dev = t.device()
+        if dev != self._dev:
+            self._where(dev, where)
+        if x.dtype is not dt or x.numel() < self._x_n or x.get_device() != dev or not x.is_contiguous():
+            _operand(x, where, "x", dt, self._x_n, dev)
+        if rows.dtype is not dt or rows.numel() < self._r_n or rows.get_device() != dev or not rows.is_contiguous():
+            _operand(rows, where, "rows", dt, self._r_n, dev)
         count, seg, pos, _ = self._at
-        rc = _calls.moe_permute(self._d, x, pos, count, seg, rows, st if stream is None else _stream(stream))
+        rc = _calls.moe_permute(self._d, x.data_ptr(), pos, count, seg, rows.data_ptr(),
+                                t.raw_stream(dev) if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
 
     def permute_backward(self, d_rows, dx, stream=None):
         where = "MoeSort.permute_backward"
-        dt = self._type
-        d_rows, dx, st = self._check_all(where, ((d_rows, "d_rows", dt, self._r_n), (dx, "dx", dt, self._x_n)))
-        rc = _calls.moe_permute_backward(self._d, d_rows, self._at[2], dx, st if stream is None else _stream(stream))
+        t, dt = self._t, self._type
+        dev = t.device()
+        if dev != self._dev:
+            self._where(dev, where)
+        if d_rows.dtype is not dt or d_rows.numel() < self._r_n or d_rows.get_device() != dev or not d_rows.is_contiguous():
+            _operand(d_rows, where, "d_rows", dt, self._r_n, dev)
+        if dx.dtype is not dt or dx.numel() < self._x_n or dx.get_device() != dev or not dx.is_contiguous():
+            _operand(dx, where, "dx", dt, self._x_n, dev)
+        rc = _calls.moe_permute_backward(self._d, d_rows.data_ptr(), self._at[2], dx.data_ptr(),
+                                         t.raw_stream(dev) if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
 
     def unpermute(self, rows, y, weights=None, residual=None, stream=None):
         where = "MoeSort.unpermute"
-        dt = self._type
-        rows, weights, residual, y, st = self._check_all(where, (
-            (rows, "rows", dt, self._r_n), (weights, "weights", _Torch.get().float32, self._entries),
-            (residual, "residual", dt, self._x_n), (y, "y", dt, self._x_n)))
-        rc = _calls.moe_unpermute(self._d, rows, self._at[2], weights, residual, y,
-                                      st if stream is None else _stream(stream))
+        t, dt, at = self._t, self._type, self._at_of
+        dev = t.device()
+        if dev != self._dev:
+            self._where(dev, where)
+        rc = _calls.moe_unpermute(self._d, at(rows, where, "rows", dt, self._r_n, dev), self._at[2],
+                                  at(weights, where, "weights", t.float32, self._entries, dev),
+                                  at(residual, where, "residual", dt, self._x_n, dev), at(y, where, "y", dt, self._x_n, dev),
+                                  t.raw_stream(dev) if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
 
     def unpermute_backward(self, dy, rows, weights, d_rows, d_weights, stream=None):
         where = "MoeSort.unpermute_backward"
-        dt, f32 = self._type, _Torch.get().float32
-        dy, rows, weights, d_rows, d_weights, st = self._check_all(where, (
-            (dy, "dy", dt, self._x_n), (rows, "rows", dt, self._r_n), (weights, "weights", f32, self._entries),
-            (d_rows, "d_rows", dt, self._r_n), (d_weights, "d_weights", f32, self._entries)))
+        t, dt, at = self._t, self._type, self._at_of
+        dev = t.device()
+        if dev != self._dev:
+            self._where(dev, where)
         count, seg, pos, _ = self._at
-        rc = _calls.moe_unpermute_backward(self._d, dy, rows, pos, count, seg, weights, d_rows, d_weights,
-                                               st if stream is None else _stream(stream))
+        rc = _calls.moe_unpermute_backward(
+            self._d, at(dy, where, "dy", dt, self._x_n, dev), at(rows, where, "rows", dt, self._r_n, dev), pos, count, seg,
+            at(weights, where, "weights", t.float32, self._entries, dev), at(d_rows, where, "d_rows", dt, self._r_n, dev),
+            at(d_weights, where, "d_weights", t.float32, self._entries, dev),
+            t.raw_stream(dev) if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
 
@@ -831,6 +853,7 @@ class Fp4Matrix(_Kept):
         self._dev = self._codes.get_device()
         self._at = (self._codes.data_ptr(), self._scales.data_ptr())
         self._n = self.rows * self.cols * self.batch
+        self._t = _Torch.get()
         self._descs, self._kept = {}, []   # addresses of descriptors, and the descriptors
 
     codes = property(lambda self: self._codes)
@@ -852,7 +875,7 @@ class Fp4Matrix(_Kept):
         MoeSort whose row_map says which source rows are live; gather=True reads
         them from x's tokens, otherwise x is already in sorted order."""
         where = "Fp4Matrix.quantize"
-        t = _Torch.get()
+        t = self._t
         dev = t.device()
         if dev != self._dev:
             self._where(dev, where)
@@ -879,7 +902,7 @@ class Fp4Matrix(_Kept):
 
     def dequantize(self, y, stream=None):
         where = "Fp4Matrix.dequantize"
-        t = _Torch.get()
+        t = self._t
         dev = t.device()
         if dev != self._dev:
             self._where(dev, where)
@@ -894,7 +917,7 @@ class Fp4Matrix(_Kept):
     def _product(self, where, b, c, accumulate, key, make):
         """Address of the product's descriptor (made once for each key), C's address and
         the current stream."""
-        t = _Torch.get()
+        t = self._t
         dev = t.device()
         if dev != self._dev or dev != b._dev:
             self._where(dev, where)

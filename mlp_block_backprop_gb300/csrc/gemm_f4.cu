@@ -335,9 +335,10 @@ __device__ __forceinline__ void store_columns(void *c, int64_t row0, int64_t n, 
 // Asks the first stages of a worker's B into L2 while the previous kernel (A's
 // quantisation, as a rule) still runs: no data reaches this kernel before
 // griddep_wait.  With few tokens the weights' way from HBM is most of the time: one token x
-// 16384 x 4096 with the quantisation before it takes 10.9 us without, 9.3 with eight
-// stages asked ahead and no less with more (L2 drops requests that come faster than
-// it fetches).  Where the experts' segments decide the tiles it gained nothing.
+// 16384 x 4096 with the quantisation before it takes 9.3 us without and 9.2 with eight
+// stages asked ahead where the weights are in L2, 25 and 22 alone with its host's calls
+// where they are not; 16 stages 9.9 and 23 (L2 drops requests that come faster than it
+// fetches).  Where the experts' segments decide the tiles it gained nothing.
 template <class C>
 __device__ __forceinline__ void f4_prefetch(const F4Args &a, const CUtensorMap *map, const F4Tile &w, int rank, int cs) {
     const int k0 = w.kb1 * rank / cs, k1 = min(w.kb1 * (rank + 1) / cs, k0 + kF4PrefetchStages);
@@ -1027,8 +1028,14 @@ int run_small(F4Args a, const Fp4Product &p, int cs, int workers, cudaStream_t s
     a.nt = static_cast<int>((p.n + 127) / 128);
     CUtensorMap mA, mA32, mB;
     const int64_t a_rows = p.m, b_rows = p.mode == kFp4GroupRows ? p.n * p.experts : p.n;
-    if (!make_map_codes(&mA, p.a, a_rows, p.k, C::BN) || !make_map_codes(&mB, p.b, b_rows, p.k, 128)) return MLPBLK_ECUDA;
-    if (!make_map_codes(&mA32, p.a, a_rows, p.k, 32)) return MLPBLK_ECUDA;
+    // a map takes 0.2 us of host time: none that no tile's rows ask for (f4_width)
+    const int64_t last = p.m % C::BN;
+    const bool narrow = p.mode != kFp4Dense || (last != 0 && last <= 64), wide = p.mode != kFp4Dense || p.m > 64;
+    if (!make_map_codes(&mB, p.b, b_rows, p.k, 128)) return MLPBLK_ECUDA;
+    if (wide && !make_map_codes(&mA, p.a, a_rows, p.k, C::BN)) return MLPBLK_ECUDA;
+    if (narrow && !make_map_codes(&mA32, p.a, a_rows, p.k, 32)) return MLPBLK_ECUDA;
+    if (!wide) mA = mA32;
+    if (!narrow) mA32 = mA;
     static int attr_set[64] = {0};
     int dev = 0;
     cudaGetDevice(&dev);

@@ -1,6 +1,6 @@
 /* pycalls.c -- the latency-bound entry points of libmlpblk.so as CPython functions:
  * the calls of a serving step take microseconds on the device, and ctypes' argument
- * conversion is a large part of a call's host time (0.7 us of 3.7 on a Grace core; 0.15
+ * conversion is a large part of a call's host time (0.7 us on a Grace core; 0.15
  * here).  Each function takes the C function's arguments in order, addresses as
  * integers (None: NULL), and returns the MLPBLK_* code.  No checks but the argument
  * count: the Python classes and the library make them. */

@@ -199,9 +199,9 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
 // at a time, TX apart: enough bytes in flight where they are short; TX (32, 64 or 128) is
 // the least that covers a row so, that no thread's accesses lie behind it (16384 x 2048
 // bf16, top-2, unpermute: 68 us with 128 threads, 46 with 64).  TX is a constant,
-// so a row's addresses are one pointer and immediate offsets (the plan, both moves and
-// both gradients of 4097 x 1001 float32, top-6: 140 us with 64-bit indices throughout, 122
-// so; 16384 x 4096 bf16, top-2: 342 and 325).
+// so a row's addresses are one pointer and immediate offsets (64-bit indices throughout
+// cost the plan, both moves and both gradients of 4097 x 1001 float32, top-6, 18 us of now
+// 110, of 16384 x 4096 bf16, top-2, 17 of now 327).
 constexpr int kMoveThreads = 256;
 template <class U>
 constexpr int kPerOf = sizeof(U) == 16 ? 4 : 8;      // permute, unpermute
