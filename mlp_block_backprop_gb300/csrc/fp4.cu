@@ -675,24 +675,22 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
     return m | (m << 16);
 }
 
-// A warp takes kDeqChunks pieces of 256 values, numbered along the rows, with the
-// pieces' loads in flight together: a lane 8 values of each, 4 bytes of codes and their
+// A warp takes CHUNKS pieces of 256 values, numbered along the rows, with the pieces'
+// loads in flight together: a lane 8 values of each, 4 bytes of codes and their
 // block's scale byte.  bf16 rows of whole 16-byte accesses are stored from registers.
 // float32 values, and rows of any length, cross shared memory, so that neighbouring
 // lanes store neighbouring words (two float4 stores 32 bytes apart take 51 us where this
 // takes 36, 192 MB of values; bf16 rows of 4097: 66, instruction issue).
-constexpr int kDeqChunks = 4;
-
-template <bool BF16, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads)
+template <bool BF16, bool ALIGNED, int WARPS, int CHUNKS>
+__global__ void __launch_bounds__(32 * WARPS)
 dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows, int64_t cols,
                   int row_tiles, int pieces, uint32_t all_pieces, void *__restrict__ y) {
     using T = typename std::conditional<BF16, uint16_t, float>::type;
     constexpr bool kTurn = !(BF16 && ALIGNED);
-    __shared__ __align__(16) T turn[kTurn ? kWarps : 1][kTurn ? 256 : 8];
+    __shared__ __align__(16) T turn[kTurn ? WARPS : 1][kTurn ? 256 : 8];
     griddep_enter();
     const int lane = threadIdx.x & 31;
-    const uint32_t p0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kDeqChunks;
+    const uint32_t p0 = (blockIdx.x * static_cast<uint32_t>(WARPS) + (threadIdx.x >> 5)) * CHUNKS;
     if (p0 >= all_pieces) return;
     const int64_t ld = fp4_row_bytes(cols);
     const int64_t tile_row = fp4_col_tiles(cols) * kFp4TileBytes;  // bytes of a row of scale tiles
@@ -708,11 +706,11 @@ dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__
         out = static_cast<T *>(y) + row * cols;
     };
     start_row();
-    T *to[kDeqChunks];      // the piece's first value
-    int count[kDeqChunks];  // of its values
-    uint32_t u[kDeqChunks], sb[kDeqChunks];
+    T *to[CHUNKS];      // the piece's first value
+    int count[CHUNKS];  // of its values
+    uint32_t u[CHUNKS], sb[CHUNKS];
 #pragma unroll
-    for (int j = 0; j < kDeqChunks; ++j) {
+    for (int j = 0; j < CHUNKS; ++j) {
         to[j] = out + static_cast<int64_t>(piece) * 256;
         count[j] = p0 + j < all_pieces ? static_cast<int>(min(cols - static_cast<int64_t>(piece) * 256, static_cast<int64_t>(256))) : 0;
         u[j] = sb[j] = 0u;
@@ -731,7 +729,7 @@ dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__
         }
     }
 #pragma unroll
-    for (int j = 0; j < kDeqChunks; ++j) {
+    for (int j = 0; j < CHUNKS; ++j) {
         const int n = count[j];
         if (n == 0) break;
         // the products are exact: a power of two times at most two bits, down to 2^-128
@@ -858,11 +856,18 @@ int dequantize_typed(const uint8_t *codes, const uint8_t *scales, int64_t rows, 
     const bool aligned = cols * (BF16 ? 2 : 4) % 16 == 0;
     const int pieces = static_cast<int>((cols + 255) / 256);
     const int64_t all = rows * batch * pieces;
-    const int w = warps_per_cta((all + kDeqChunks - 1) / kDeqChunks);
-    const int64_t per_cta = static_cast<int64_t>(w) * kDeqChunks;
-    return launch_pdl(aligned ? dequantize_kernel<BF16, true> : dequantize_kernel<BF16, false>,
-                      dim3(static_cast<unsigned>((all + per_cta - 1) / per_cta)), dim3(32 * w), 0, s, codes, scales, rows, cols,
-                      row_tiles, pieces, static_cast<uint32_t>(all), y);
+    // more pieces a warp as there are more warps than the SMs hold (float32, from L2: 8 x 4096
+    // 1.7 us with four pieces, 1.2 with one; 1031 x 4095 5.1 and 4.5 with two; 4096 x 4096
+    // 10.8, 11.5 with two)
+    const int64_t sms = sm_total();
+#define MLPBLK_DEQ(W, N)                                                                                              \
+    return launch_pdl(aligned ? dequantize_kernel<BF16, true, W, N> : dequantize_kernel<BF16, false, W, N>,           \
+                      dim3(static_cast<unsigned>((all + W * N - 1) / (W * N))), dim3(32 * W), 0, s, codes, scales,     \
+                      rows, cols, row_tiles, pieces, static_cast<uint32_t>(all), y)
+    if (all <= 8 * sms) MLPBLK_DEQ(1, 1);
+    if (all <= 192 * sms) MLPBLK_DEQ(8, 2);
+    MLPBLK_DEQ(8, 4);
+#undef MLPBLK_DEQ
 }
 
 }  // namespace
