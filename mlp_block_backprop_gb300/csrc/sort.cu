@@ -352,8 +352,8 @@ permute_kernel(const U *__restrict__ x, const int *__restrict__ pos, const int *
 // accesses gain from a third CTA, 34 -> 30 us at 4097 x 1001 float32, top-6).
 // residual and y may be the same array: an element is read and written by the same
 // thread.
-template <int TX, class U, bool BF16>
-__global__ void __launch_bounds__(kMoveThreads, sizeof(U) == 16 ? 2 : 3)
+template <int TX, class U, bool BF16, bool RES>
+__global__ void __launch_bounds__(kMoveThreads, sizeof(U) == 16 && RES ? 2 : 3)
 unpermute_kernel(const U *__restrict__ rows, const int *__restrict__ pos, const float *__restrict__ weights,
                  const U *residual, int64_t T, int k, int R, int units, int parts, U *y) {
     using V = Vals<U, BF16>;
@@ -368,7 +368,7 @@ unpermute_kernel(const U *__restrict__ rows, const int *__restrict__ pos, const 
         U res[kPer];
         const U *rp = residual + t * units + c;
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) res[u] = residual && c + u * TX < units ? rp[u * TX] : zero_unit<U>();
+        for (int u = 0; u < kPer; ++u) res[u] = RES && c + u * TX < units ? rp[u * TX] : zero_unit<U>();
         for (int j = 0; j < k; j += 2) {
             const int ra = entry_row(pos, t * k + j, R), rb = j + 1 < k ? entry_row(pos, t * k + j + 1, R) : -1;
             const float wa = weights ? wt[j] : 1.0f;
@@ -575,19 +575,29 @@ int launch_unpermute(const void *rows, const int *pos, const float *weights, con
                      int64_t width, int dtype, int k, int64_t R, void *y, cudaStream_t s) {
     const MoveShape m = move_shape(T, width, dtype, 1, 1, kPerOf<uint4>, kPerOf<uint32_t>, kPerOf<uint16_t>, 0);
     const dim3 grid(static_cast<unsigned>(m.token_blocks));
-#define MLPBLK_UNPERMUTE(U, B)                                                                              \
-    return launch_pdl(m.tx == 32 ? unpermute_kernel<32, U, B>                                               \
-                      : m.tx == 64 ? unpermute_kernel<64, U, B> : unpermute_kernel<128, U, B>,              \
-                      grid, m.block, 0, s, static_cast<const U *>(rows), pos, weights,                      \
+#define MLPBLK_UNPERMUTE_R(U, B, RES)                                                                        \
+    return launch_pdl(m.tx == 32 ? unpermute_kernel<32, U, B, RES>                                           \
+                      : m.tx == 64 ? unpermute_kernel<64, U, B, RES> : unpermute_kernel<128, U, B, RES>,     \
+                      grid, m.block, 0, s, static_cast<const U *>(rows), pos, weights,                       \
                       static_cast<const U *>(residual), T, k, static_cast<int>(R), m.units, m.parts, static_cast<U *>(y))
+#define MLPBLK_UNPERMUTE(U, B)                  \
+    if (residual) MLPBLK_UNPERMUTE_R(U, B, true); \
+    MLPBLK_UNPERMUTE_R(U, B, false)
     if (dtype == MLPBLK_BF16) {
-        if (m.unit == 16) MLPBLK_UNPERMUTE(uint4, true);
-        if (m.unit == 4) MLPBLK_UNPERMUTE(uint32_t, true);
+        if (m.unit == 16) {
+            MLPBLK_UNPERMUTE(uint4, true);
+        }
+        if (m.unit == 4) {
+            MLPBLK_UNPERMUTE(uint32_t, true);
+        }
         MLPBLK_UNPERMUTE(uint16_t, true);
     }
-    if (m.unit == 16) MLPBLK_UNPERMUTE(uint4, false);
+    if (m.unit == 16) {
+        MLPBLK_UNPERMUTE(uint4, false);
+    }
     MLPBLK_UNPERMUTE(uint32_t, false);
 #undef MLPBLK_UNPERMUTE
+#undef MLPBLK_UNPERMUTE_R
 }
 
 int launch_unpermute_bwd(const void *dy, const void *rows, const int *pos, const int *count, const int *seg,
