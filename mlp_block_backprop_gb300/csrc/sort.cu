@@ -204,7 +204,9 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
 // 110, of 16384 x 4096 bf16, top-2, 17 of now 327).
 constexpr int kMoveThreads = 256;
 template <class U>
-constexpr int kPerOf = sizeof(U) == 16 ? 4 : 8;      // permute, unpermute
+constexpr int kPerOf = sizeof(U) == 16 ? 4 : 8;      // permute
+template <class U, bool RES>
+constexpr int kPerUnOf = sizeof(U) == 16 && RES ? 2 : kPerOf<U>;  // unpermute, with and without a residual
 template <class U>
 constexpr int kSlotsOf = sizeof(U) == 4 ? 4 : 2;     // slots whose rows the gradient loads together
 template <class U>
@@ -345,19 +347,20 @@ permute_kernel(const U *__restrict__ x, const int *__restrict__ pos, const int *
 }
 
 // y[t] = residual[t] + sum_j w[t,j] * rows[pos[t,j]], slot order, float32, rounded
-// once.  Two slots' rows are loaded together, so that a thread has 3 * kPer accesses
-// in flight (four slots' at a time take it to one CTA an SM: 90 -> 153 us at 16384 x
-// 4096 bf16, top-2; rows that arrive by bulk copies in a ring of shared-memory stages
-// were no faster there, 91 us, and half as fast on 1001-float rows; 4- and 2-byte
-// accesses gain from a third CTA, 34 -> 30 us at 4097 x 1001 float32, top-6).
+// once.  Two slots' rows are loaded together, with the residual's.  What counts is loads in
+// flight over all warps of an SM: 16384 x 4096 bf16, top-2, takes 82 us with two
+// accesses of 16 bytes a thread and four CTAs an SM, 91 with four and two, 98 with four and
+// three (spills), 153 with four slots at a time and one CTA; without a residual four
+// accesses fit three CTAs (60 us, the bytes' floor).  Rows that arrive by bulk copies in a
+// ring of shared-memory stages were no faster (91 us, half as fast on 1001-float rows).
 // residual and y may be the same array: an element is read and written by the same
 // thread.
 template <int TX, class U, bool BF16, bool RES>
-__global__ void __launch_bounds__(kMoveThreads, sizeof(U) == 16 && RES ? 2 : 3)
+__global__ void __launch_bounds__(kMoveThreads, sizeof(U) == 16 && RES ? 4 : 3)
 unpermute_kernel(const U *__restrict__ rows, const int *__restrict__ pos, const float *__restrict__ weights,
                  const U *residual, int64_t T, int k, int R, int units, int parts, U *y) {
     using V = Vals<U, BF16>;
-    constexpr int kPer = kPerOf<U>;
+    constexpr int kPer = kPerUnOf<U, RES>;
     griddep_enter();
     const int64_t t = static_cast<int64_t>(blockIdx.x / parts) * blockDim.y + threadIdx.y;
     if (t >= T) return;
@@ -515,7 +518,8 @@ int access_bytes(int64_t width, int dtype) {
     return bytes % 16 == 0 ? 16 : (bytes % 4 == 0 ? 4 : 2);
 }
 
-MoveShape move_shape(int64_t T, int64_t width, int dtype, int experts, int pad, int per16, int per4, int per2, int slots) {
+MoveShape move_shape(int64_t T, int64_t width, int dtype, int experts, int pad, int per16, int per4, int per2, int step16,
+                     int slots) {
     MoveShape m;
     const int64_t bytes = width * (dtype == MLPBLK_BF16 ? 2 : 4);
     m.unit = access_bytes(width, dtype);
@@ -524,7 +528,8 @@ MoveShape move_shape(int64_t T, int64_t width, int dtype, int experts, int pad, 
     m.tx = m.units <= 32 * p ? 32 : (m.units <= 64 * p ? 64 : 128);
     m.block = dim3(m.tx, kMoveThreads / m.tx, 1);
     const int64_t blocks = (T + m.block.y - 1) / m.block.y;
-    const int64_t steps = slots ? slots : (m.units + m.tx * p - 1) / (m.tx * p);
+    const int64_t step = static_cast<int64_t>(m.tx) * (m.unit == 16 ? step16 : p);
+    const int64_t steps = slots ? slots : (m.units + step - 1) / step;
     m.parts = static_cast<int>(std::max<int64_t>(1, std::min(steps, kFewBlocks / std::max<int64_t>(1, blocks))));
     m.token_blocks = blocks * m.parts;
     m.slices = pad > 1 ? static_cast<int>(std::min<int64_t>(pad - 1, ((pad - 1) * bytes + kSliceBytes - 1) / kSliceBytes)) : 0;
@@ -559,7 +564,7 @@ int launch_sort(const int *idx, int64_t n, int experts, int pad, int64_t R, int 
 
 int launch_permute(const void *x, const int *pos, const int *count, const int *seg, int64_t T, int64_t width,
                    int dtype, int k, int experts, int pad, int64_t R, void *rows, cudaStream_t s) {
-    const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerOf<uint4>, kPerOf<uint32_t>, kPerOf<uint16_t>, 0);
+    const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerOf<uint4>, kPerOf<uint32_t>, kPerOf<uint16_t>, kPerOf<uint4>, 0);
     const dim3 grid(static_cast<unsigned>(m.token_blocks + m.pad_blocks));
 #define MLPBLK_PERMUTE(U)                                                                                      \
     return launch_pdl(m.tx == 32 ? permute_kernel<32, U> : m.tx == 64 ? permute_kernel<64, U> : permute_kernel<128, U>, grid, m.block, 0, s,         \
@@ -573,7 +578,8 @@ int launch_permute(const void *x, const int *pos, const int *count, const int *s
 
 int launch_unpermute(const void *rows, const int *pos, const float *weights, const void *residual, int64_t T,
                      int64_t width, int dtype, int k, int64_t R, void *y, cudaStream_t s) {
-    const MoveShape m = move_shape(T, width, dtype, 1, 1, kPerOf<uint4>, kPerOf<uint32_t>, kPerOf<uint16_t>, 0);
+    const MoveShape m = move_shape(T, width, dtype, 1, 1, kPerOf<uint4>, kPerOf<uint32_t>, kPerOf<uint16_t>,
+                                   residual ? kPerUnOf<uint4, true> : kPerUnOf<uint4, false>, 0);
     const dim3 grid(static_cast<unsigned>(m.token_blocks));
 #define MLPBLK_UNPERMUTE_R(U, B, RES)                                                                        \
     return launch_pdl(m.tx == 32 ? unpermute_kernel<32, U, B, RES>                                           \
@@ -605,7 +611,7 @@ int launch_unpermute_bwd(const void *dy, const void *rows, const int *pos, const
                          void *d_rows, float *d_weights, cudaStream_t s) {
     const int unit = access_bytes(width, dtype);
     const int slots = unit == 16 ? kSlotsOf<uint4> : (unit == 4 ? kSlotsOf<uint32_t> : kSlotsOf<uint16_t>);
-    const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerBwdOf<uint4>, kPerBwdOf<uint32_t>, kPerBwdOf<uint16_t>,
+    const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerBwdOf<uint4>, kPerBwdOf<uint32_t>, kPerBwdOf<uint16_t>, kPerBwdOf<uint4>,
                                    (k + slots - 1) / slots);
     const dim3 grid(static_cast<unsigned>(m.token_blocks + m.pad_blocks));
 #define MLPBLK_UNPERMUTE_BWD(U, B)                                                                               \
