@@ -201,17 +201,17 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
 // bf16, top-2, unpermute: 68 us with 128 threads, 46 with 64).  TX is a constant,
 // so a row's addresses are one pointer and immediate offsets (64-bit indices throughout
 // cost the plan, both moves and both gradients of 4097 x 1001 float32, top-6, 18 us of now
-// 110, of 16384 x 4096 bf16, top-2, 17 of now 327).
+// 109, of 16384 x 4096 bf16, top-2, 17 of now 306).
 constexpr int kMoveThreads = 256;
 template <class U>
-constexpr int kPerOf = sizeof(U) == 16 ? 4 : 8;      // permute
+constexpr int kPerOf = sizeof(U) == 16 ? 4 : 8;  // permute
 template <class U, bool RES>
 constexpr int kPerUnOf = sizeof(U) == 16 && RES ? 2 : kPerOf<U>;  // unpermute, with and without a residual
+constexpr int kSlots = 2;  // slots whose rows the gradient loads together
+// unpermute's gradient (16384 tokens, top-2, bf16: x 4096 97 us; x 4098 104, with four
+// slots of four accesses 114; x 2049 134 and 181)
 template <class U>
-constexpr int kSlotsOf = sizeof(U) == 4 ? 4 : 2;     // slots whose rows the gradient loads together
-template <class U>
-constexpr int kPerBwdOf = sizeof(U) == 16 ? 2 : (sizeof(U) == 4 ? 4 : 8);  // unpermute's gradient (16384 x 4096 bf16,
-                                                                           // top-2: 98 us; x 2049: 134, 181 with 4 and 4 slots)
+constexpr int kPerBwdOf = sizeof(U) == 16 ? 2 : 8;
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
@@ -415,7 +415,7 @@ unpermute_kernel(const U *__restrict__ rows, const int *__restrict__ pos, const 
 }
 
 // d_rows[pos[t,j]] = w[t,j] * dy[t] and dw[t,j] = <dy[t], rows[pos[t,j]]>.  The rows of
-// kSlotsOf slots are loaded together with dy; a dot product is summed over the row's
+// kSlots slots are loaded together with dy; a dot product is summed over the row's
 // threads by shuffles, then over its warps in warp order.  d_weights NULL skips the
 // products and rows.
 template <int TX, class U, bool BF16>
@@ -425,7 +425,7 @@ unpermute_bwd_kernel(const U *__restrict__ dy, const U *__restrict__ rows, const
                      int64_t T, int k, int experts, int slices, int R, int units, int parts, int64_t token_blocks,
                      U *__restrict__ d_rows, float *__restrict__ d_weights) {
     using V = Vals<U, BF16>;
-    constexpr int kPerBwd = kPerBwdOf<U>, kSlots = kSlotsOf<U>;
+    constexpr int kPerBwd = kPerBwdOf<U>;
     constexpr int kWarps = TX / 32;  // of a row
     __shared__ float part[2][kSlots][kMoveThreads / 32];
     griddep_enter();
@@ -513,16 +513,11 @@ struct MoveShape {
 constexpr int64_t kFewBlocks = 152;
 constexpr int64_t kSliceBytes = 32768;
 
-int access_bytes(int64_t width, int dtype) {
-    const int64_t bytes = width * (dtype == MLPBLK_BF16 ? 2 : 4);
-    return bytes % 16 == 0 ? 16 : (bytes % 4 == 0 ? 4 : 2);
-}
-
 MoveShape move_shape(int64_t T, int64_t width, int dtype, int experts, int pad, int per16, int per4, int per2, int step16,
                      int slots) {
     MoveShape m;
     const int64_t bytes = width * (dtype == MLPBLK_BF16 ? 2 : 4);
-    m.unit = access_bytes(width, dtype);
+    m.unit = bytes % 16 == 0 ? 16 : (bytes % 4 == 0 ? 4 : 2);
     m.units = static_cast<int>(bytes / m.unit);
     const int p = m.unit == 16 ? per16 : (m.unit == 4 ? per4 : per2);
     m.tx = m.units <= 32 * p ? 32 : (m.units <= 64 * p ? 64 : 128);
@@ -609,10 +604,8 @@ int launch_unpermute(const void *rows, const int *pos, const float *weights, con
 int launch_unpermute_bwd(const void *dy, const void *rows, const int *pos, const int *count, const int *seg,
                          const float *weights, int64_t T, int64_t width, int dtype, int k, int experts, int pad, int64_t R,
                          void *d_rows, float *d_weights, cudaStream_t s) {
-    const int unit = access_bytes(width, dtype);
-    const int slots = unit == 16 ? kSlotsOf<uint4> : (unit == 4 ? kSlotsOf<uint32_t> : kSlotsOf<uint16_t>);
     const MoveShape m = move_shape(T, width, dtype, experts, pad, kPerBwdOf<uint4>, kPerBwdOf<uint32_t>, kPerBwdOf<uint16_t>, kPerBwdOf<uint4>,
-                                   (k + slots - 1) / slots);
+                                   (k + kSlots - 1) / kSlots);
     const dim3 grid(static_cast<unsigned>(m.token_blocks + m.pad_blocks));
 #define MLPBLK_UNPERMUTE_BWD(U, B)                                                                               \
     return launch_pdl(m.tx == 32 ? unpermute_bwd_kernel<32, U, B>                                                \
