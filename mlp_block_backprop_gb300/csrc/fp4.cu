@@ -359,12 +359,14 @@ __device__ __forceinline__ void load_block(const uint16_t *__restrict__ p, int l
 // of a scale tile for eight neighbouring r, two rows in flight (HALVES 2: two of the four
 // rows alone); four lanes then transpose their 4 x 4 scale bytes, and the warp stores 128
 // consecutive bytes of the tile.  Warps are numbered along a row's tiles first, so a
-// CTA's eight cover 2048 bytes of a row and no lane idles but in a row's last 256
-// columns.  8192 x 16384: 51 us (6.6 TB/s), ReLU^2 52, where a lane with 8 values and
-// shuffles takes 67; 192 MB in rows of 1056: 44 and 63, of 1031: 57 and 88.  (float32 gains nothing: four rows'
+// CTA's cover neighbouring parts of a row and no lane idles but in a row's last 256
+// columns.  8192 x 16384: 49.5 us (6.86 TB/s), with ReLU^2 too, where a lane with 8 values
+// and shuffles takes 67; 192 MB in rows of 1056: 40 and 63, of 1031: 55 and 88.  (float32 gains nothing: four rows'
 // loads of 8 values take 38 us for 192 MB, blocks of 128 bytes a lane 51.)
+constexpr int kBlockWarps = 4;  // of a CTA (16384 x 16384: 98 us with eight, ReLU^2 100)
+
 template <bool RELU2, bool MAP, bool ALIGNED, int HALVES>
-__global__ void __launch_bounds__(kThreads, RELU2 ? 2 : 3)
+__global__ void __launch_bounds__(32 * kBlockWarps, RELU2 ? 4 : 6)
 quantize_blocks_kernel(const uint16_t *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
                        int64_t cols, int row_tiles, int col_tiles, uint32_t warps, uint8_t *__restrict__ codes,
                        uint8_t *__restrict__ scales) {
@@ -795,15 +797,15 @@ dim3 grid_for(int64_t x, int64_t most) {
 
 // Where there are at most this many warps an SM, quantize_blocks_kernel deals a warp's four
 // rows out to two (bf16 from L2, 2048 x 2048: 5.8 us with one warp and 3.5 with two, 4096 x
-// 4096: 6.8 and 6.4; 8192 x 16384 from HBM, ReLU^2: 53 and 57).
+// 4096: 6.8 and 6.2; 8192 x 16384 from HBM, ReLU^2: 53 and 57, in CTAs of eight warps).
 constexpr int64_t kHalfWarps = 32;
 
-// Warps of a CTA for kernels whose warps are independent: fewer than kWarps where that
-// spreads few warps over the SMs (118 x 6624: 2.7 us, with CTAs of eight 3.5).
+// Warps of a CTA for quantize_blocks_kernel, whose warps are independent: kBlockWarps, fewer
+// where that spreads few warps over the SMs (118 x 6624: 2.7 us, with CTAs of eight 3.5).
 int warps_per_cta(int64_t warps) {
     const int sms = sm_total();
     int w = 1;
-    while (w < kWarps && warps > static_cast<int64_t>(sms) * w) w *= 2;
+    while (w < kBlockWarps && warps > static_cast<int64_t>(sms) * w) w *= 2;
     return w;
 }
 
@@ -865,8 +867,8 @@ int dequantize_typed(const uint8_t *codes, const uint8_t *scales, int64_t rows, 
                       dim3(static_cast<unsigned>((all + W * N - 1) / (W * N))), dim3(32 * W), 0, s, codes, scales,     \
                       rows, cols, row_tiles, pieces, static_cast<uint32_t>(all), y)
     if (all <= 8 * sms) MLPBLK_DEQ(1, 1);
-    if (all <= 192 * sms) MLPBLK_DEQ(8, 2);
-    MLPBLK_DEQ(8, 4);
+    if (all <= 192 * sms) MLPBLK_DEQ(4, 2);
+    MLPBLK_DEQ(4, 4);
 #undef MLPBLK_DEQ
 }
 
