@@ -202,7 +202,7 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
 // so a row's addresses are one pointer and immediate offsets (64-bit indices throughout
 // cost the plan, both moves and both gradients of 4097 x 1001 float32, top-6, 18 us of now
 // 109, of 16384 x 4096 bf16, top-2, 17 of now 306).
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 128;  // 256: 4097 x 1001 float32 109 us, 107 so; 16384 x 2049 bf16 352 and 336
 template <class U>
 constexpr int kPerOf = sizeof(U) == 16 ? 4 : 8;  // permute
 template <class U, bool RES>
@@ -348,15 +348,15 @@ permute_kernel(const U *__restrict__ x, const int *__restrict__ pos, const int *
 
 // y[t] = residual[t] + sum_j w[t,j] * rows[pos[t,j]], slot order, float32, rounded
 // once.  Two slots' rows are loaded together, with the residual's.  What counts is loads in
-// flight over all warps of an SM: 16384 x 4096 bf16, top-2, takes 82 us with two
-// accesses of 16 bytes a thread and four CTAs an SM, 91 with four and two, 98 with four and
-// three (spills), 153 with four slots at a time and one CTA; without a residual four
-// accesses fit three CTAs (60 us, the bytes' floor).  Rows that arrive by bulk copies in a
+// flight over all warps of an SM: 16384 x 4096 bf16, top-2, takes 81 us with two
+// accesses of 16 bytes a thread and 32 warps an SM, 91 with four and 16 warps, 98 with four
+// and 24 (spills), 153 with four slots at a time and 8; without a residual four accesses
+// leave room for 24 warps (59 us, the bytes' floor).  Rows that arrive by bulk copies in a
 // ring of shared-memory stages were no faster (91 us, half as fast on 1001-float rows).
 // residual and y may be the same array: an element is read and written by the same
 // thread.
 template <int TX, class U, bool BF16, bool RES>
-__global__ void __launch_bounds__(kMoveThreads, sizeof(U) == 16 && RES ? 4 : 3)
+__global__ void __launch_bounds__(kMoveThreads, sizeof(U) == 16 && RES ? 8 : 6)
 unpermute_kernel(const U *__restrict__ rows, const int *__restrict__ pos, const float *__restrict__ weights,
                  const U *residual, int64_t T, int k, int R, int units, int parts, U *y) {
     using V = Vals<U, BF16>;
