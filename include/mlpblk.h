@@ -504,7 +504,10 @@ int mlpblk_moe_unpermute_backward(const mlpblk_sort_desc *desc, const void *dy, 
  *   maps the source's rows: where row_map[r] < 0 row r is zeros and x is not read
  *   there, otherwise it is x's row row_map[r] / map_div for map_div > 0, and
  *   x's row r for map_div = 0.  With transposed the mapped rows are Q's columns.
- *   row_map needs batch = 1.  Every byte of codes and scales is written.
+ *   A gathering map (map_div > 0) needs desc->source_rows, x's row count: a row that
+ *   it maps to source_rows or beyond (a map of a larger batch) is zeros too, so no
+ *   access leaves x.  row_map needs batch = 1.  Every byte of codes and scales is
+ *   written.
  * mlpblk_fp4_dequantize: y[batch, rows, cols] in desc->dtype (exact in both types).
  *   transposed and act must be 0.
  * Limits: rows, cols >= 0 (with either 0: MLPBLK_OK, nothing is touched),
@@ -521,6 +524,8 @@ typedef struct {
     int32_t dtype;        /* of x or y: MLPBLK_BF16 or MLPBLK_FP32         */
     int32_t transposed;   /* 1: the source is stored [cols, rows]          */
     int32_t act;          /* MLPBLK_FP4_ACT_*                              */
+    int64_t source_rows;  /* rows of x under a gathering row_map (>= 1 there,
+                             < 2^31); not used otherwise                   */
 } mlpblk_fp4_desc;
 
 size_t mlpblk_fp4_codes_size(const mlpblk_fp4_desc *desc);

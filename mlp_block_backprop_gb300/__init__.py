@@ -89,7 +89,8 @@ class SortDesc(ctypes.Structure):
 class Fp4Desc(ctypes.Structure):
     """mlpblk_fp4_desc: an MXFP4 matrix (a batch of them) and what it is made from."""
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("batch", ctypes.c_int32),
-                ("dtype", ctypes.c_int32), ("transposed", ctypes.c_int32), ("act", ctypes.c_int32)]
+                ("dtype", ctypes.c_int32), ("transposed", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("source_rows", ctypes.c_int64)]
 
 
 class Fp4MatmulDesc(ctypes.Structure):
@@ -741,8 +742,9 @@ class MoeSort(_Kept):
             _check(rc, where)
 
 
-def make_fp4_desc(rows, cols, batch=1, dtype=MLPBLK_BF16, transposed=False, act=MLPBLK_FP4_ACT_NONE) -> Fp4Desc:
-    return Fp4Desc(int(rows), int(cols), int(batch), _dtype_code(dtype), int(bool(transposed)), int(act))
+def make_fp4_desc(rows, cols, batch=1, dtype=MLPBLK_BF16, transposed=False, act=MLPBLK_FP4_ACT_NONE,
+                  source_rows=0) -> Fp4Desc:
+    return Fp4Desc(int(rows), int(cols), int(batch), _dtype_code(dtype), int(bool(transposed)), int(act), int(source_rows))
 
 
 def mlpblk_fp4_codes_size(desc: Fp4Desc) -> int:
@@ -754,13 +756,19 @@ def mlpblk_fp4_scales_size(desc: Fp4Desc) -> int:
 
 
 def mlpblk_fp4_quantize(desc, x, codes, scales, row_map=None, map_div=0, stream=None):
-    """x holds the whole source, unless a row_map gathers its rows (map_div > 0): its
-    row count is then the caller's business."""
+    """x holds the whole source; where a row_map gathers its rows (map_div > 0), that is
+    desc.source_rows of them, or, where the descriptor leaves that 0, the rows that the
+    tensor x has."""
     where = "mlpblk_fp4_quantize"
     t = _Torch.get()
     dev, i32, u8 = t.device(), t.int32, t.uint8
-    mapped = desc.cols if desc.transposed else desc.rows  # the source's rows
-    n = 0 if row_map is not None and map_div > 0 else desc.rows * desc.cols * desc.batch
+    mapped, width = (desc.cols, desc.rows) if desc.transposed else (desc.rows, desc.cols)  # the source's
+    n = desc.rows * desc.cols * desc.batch
+    if row_map is not None and map_div > 0:
+        if desc.source_rows == 0 and not isinstance(x, int) and x is not None and width > 0:
+            desc = Fp4Desc(desc.rows, desc.cols, desc.batch, desc.dtype, desc.transposed, desc.act,
+                           min(x.numel() // width, 2 ** 31 - 1))
+        n = desc.source_rows * width
     rc = lib.mlpblk_fp4_quantize(
         ctypes.byref(desc), _operand(x, where, "x", t.row.get(desc.dtype), n, dev),
         _operand(row_map, where, "row_map", i32, mapped, dev), int(map_div),
@@ -859,14 +867,15 @@ class Fp4Matrix(_Kept):
     codes = property(lambda self: self._codes)
     scales = property(lambda self: self._scales)
 
-    def _desc(self, dtype, transposed, act):
+    def _desc(self, dtype, transposed, act, source_rows=0):
         """Address of the descriptor for these options, made once."""
-        key = (dtype, transposed, act)
+        key = (dtype, transposed, act, source_rows)
         d = self._descs.get(key)
         if d is None:
             if act not in self._ACTS:
                 raise MlpBlkError(MLPBLK_ENOTSUP, f"Fp4Matrix.quantize: act {act!r}")
-            self._kept.append(make_fp4_desc(self.rows, self.cols, self.batch, dtype, transposed, self._ACTS[act]))
+            self._kept.append(make_fp4_desc(self.rows, self.cols, self.batch, dtype, transposed, self._ACTS[act],
+                                            source_rows))
             d = self._descs[key] = ctypes.addressof(self._kept[-1])
         return d
 
@@ -879,8 +888,7 @@ class Fp4Matrix(_Kept):
         dev = t.device()
         if dev != self._dev:
             self._where(dev, where)
-        d = self._descs.get((x.dtype, transposed, act)) or self._desc(x.dtype, transposed, act)
-        n, row_map, div = self._n, None, 0
+        n, row_map, div, source_rows = self._n, None, 0, 0
         if sort is not None:
             width, mapped = (self.rows, self.cols) if transposed else (self.cols, self.rows)
             if mapped != sort.rows or (gather and width != sort.desc.width):
@@ -889,11 +897,13 @@ class Fp4Matrix(_Kept):
             sort._where(dev, where)
             row_map = sort._at[3]
             if gather:
-                n, div = sort._x_n, sort.desc.top_k
+                n, div, source_rows = sort._x_n, sort.desc.top_k, sort.desc.tokens
         elif gather:
             raise MlpBlkError(MLPBLK_EINVAL, f"{where}: gather needs a sort")
         if x.numel() < n or x.get_device() != dev or not x.is_contiguous():
             _operand(x, where, "x", x.dtype, n, dev)
+        key = (x.dtype, transposed, act, source_rows)
+        d = self._descs.get(key) or self._desc(*key)
         codes, scales = self._at
         rc = _calls.fp4_quantize(d, x.data_ptr(), row_map, div, codes, scales,
                                      t.raw_stream(dev) if stream is None else _stream(stream))
@@ -906,7 +916,7 @@ class Fp4Matrix(_Kept):
         dev = t.device()
         if dev != self._dev:
             self._where(dev, where)
-        d = self._descs.get((y.dtype, False, "none")) or self._desc(y.dtype, False, "none")
+        d = self._descs.get((y.dtype, False, "none", 0)) or self._desc(y.dtype, False, "none")
         if y.numel() < self._n or y.get_device() != dev or not y.is_contiguous():
             _operand(y, where, "y", y.dtype, self._n, dev)
         codes, scales = self._at

@@ -1463,13 +1463,15 @@ int mlpblk_fp4_quantize(const mlpblk_fp4_desc *desc, const void *x, const int32_
     MLPBLK_TRY(check_fp4_desc(desc));
     if (map_div < 0 || (row_map && desc->batch != 1)) return MLPBLK_EINVAL;
     if (desc->rows == 0 || desc->cols == 0) return MLPBLK_OK;
+    const int64_t source_rows = row_map && map_div > 0 ? desc->source_rows : 1;
+    if (source_rows < 1 || source_rows >= kFp4Lim) return MLPBLK_EINVAL;
     if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || (row_map && !aligned16(row_map))) return MLPBLK_EINVAL;
     if (codes == x || scales == x || codes == scales) return MLPBLK_EINVAL;
     int sms = 0;
     MLPBLK_TRY(device_sms(&sms));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     MLPBLK_LAUNCH(MLPBLK_KERNEL_FP4_QUANT, s,
-                  launch_fp4_quantize(desc->dtype, x, row_map, map_div, desc->rows, desc->cols, desc->batch,
+                  launch_fp4_quantize(desc->dtype, x, row_map, map_div, static_cast<int>(source_rows), desc->rows, desc->cols, desc->batch,
                                       desc->transposed != 0, desc->act == MLPBLK_FP4_ACT_RELU2,
                                       static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales), s));
     return MLPBLK_OK;

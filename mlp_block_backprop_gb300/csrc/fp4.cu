@@ -94,9 +94,14 @@ __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v 
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
 // The source row of Q's row (or, transposed, column) r under a row map, or -1 for zeros.
-__device__ __forceinline__ int source_row(const int *row_map, int map_div, int64_t r) {
+// A gathered row behind the source's own (a map of another batch) is taken as none, so no
+// access leaves x.
+__device__ __forceinline__ int source_row(const int *row_map, int map_div, int source_rows, int64_t r) {
     const int m = row_map[r];
-    return m < 0 ? -1 : (map_div > 0 ? m / map_div : static_cast<int>(r));
+    if (m < 0) return -1;
+    if (map_div == 0) return static_cast<int>(r);
+    const int q = m / map_div;
+    return q < source_rows ? q : -1;
 }
 
 // The bits of a block's largest |value| (or largest value, squared) from its maxima:
@@ -230,7 +235,7 @@ __device__ __forceinline__ void zero_rows(uint8_t *out, int64_t ld, int64_t left
 // row's beside them.  The four rows' loads are in flight together.
 template <bool VEC, bool RELU2, bool MAP>
 __global__ void __launch_bounds__(kThreads, 3)
-quantize_rows_kernel(const float *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
+quantize_rows_kernel(const float *__restrict__ x, const int *__restrict__ row_map, int map_div, int source_rows, int64_t rows,
                      int64_t cols, int row_tiles, int chunks, uint8_t *__restrict__ codes,
                      uint8_t *__restrict__ scales) {
     __shared__ __align__(16) float turn[VEC ? 1 : kWarps][4][VEC ? 8 : 256];
@@ -247,7 +252,7 @@ quantize_rows_kernel(const float *__restrict__ x, const int *__restrict__ row_ma
     for (int j = 0; j < 4; ++j) {
         const int64_t r = r0 + 32 * j;
         int64_t at = r < rows ? r : -1;
-        if (MAP && r < rows) at = source_row(row_map, map_div, r);
+        if (MAP && r < rows) at = source_row(row_map, map_div, source_rows, r);
         live[j] = at >= 0;
         src[j] = x + (mat * rows + (at < 0 ? 0 : at)) * cols;
     }
@@ -367,7 +372,7 @@ constexpr int kBlockWarps = 4;  // of a CTA (16384 x 16384: 98 us with eight, Re
 
 template <bool RELU2, bool MAP, bool ALIGNED, int HALVES>
 __global__ void __launch_bounds__(32 * kBlockWarps, RELU2 ? 4 : 6)
-quantize_blocks_kernel(const uint16_t *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
+quantize_blocks_kernel(const uint16_t *__restrict__ x, const int *__restrict__ row_map, int map_div, int source_rows, int64_t rows,
                        int64_t cols, int row_tiles, int col_tiles, uint32_t warps, uint8_t *__restrict__ codes,
                        uint8_t *__restrict__ scales) {
     constexpr int kParts = 4;  // Octs of a block
@@ -393,7 +398,7 @@ quantize_blocks_kernel(const uint16_t *__restrict__ x, const int *__restrict__ r
     for (int j = 0; j < 4; ++j) {
         const int64_t r = r0 + 32 * j;
         src[j] = r < rows ? r : -1;
-        if (MAP && r < rows) src[j] = source_row(row_map, map_div, r);
+        if (MAP && r < rows) src[j] = source_row(row_map, map_div, source_rows, r);
     }
     uint32_t bytes = 0;  // of the four rows
 #pragma unroll
@@ -541,7 +546,7 @@ constexpr int kTPitch = 128 + 16;       // bytes of a Q row in shared memory
 // MAP: 0 no row map, 1 a map that only says which rows are live, 2 one that gathers.
 template <bool BF16, bool VEC, bool RELU2, int MAP>
 __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2)
-quantize_cols_kernel(const void *__restrict__ x, const int *__restrict__ row_map, int map_div, int64_t rows,
+quantize_cols_kernel(const void *__restrict__ x, const int *__restrict__ row_map, int map_div, int source_rows, int64_t rows,
                      int64_t cols, int row_tiles, int chunks, uint8_t *__restrict__ codes,
                      uint8_t *__restrict__ scales) {
     using T = typename std::conditional<BF16, uint16_t, float>::type;
@@ -590,7 +595,7 @@ quantize_cols_kernel(const void *__restrict__ x, const int *__restrict__ row_map
         bool none = false;  // no row of x is live: zeros without the arithmetic
         if (MAP == 2) {
             const int64_t own = c0 + lane;
-            const int mine = own < cols ? source_row(row_map, map_div, own) : -1;
+            const int mine = own < cols ? source_row(row_map, map_div, source_rows, own) : -1;
             none = !__any_sync(0xffffffffu, mine >= 0);
             if (!none) {
 #pragma unroll
@@ -810,13 +815,13 @@ int warps_per_cta(int64_t warps) {
 }
 
 template <bool BF16, bool RELU2, int MAP>
-int quantize_typed(const void *x, const int *row_map, int map_div, int64_t rows, int64_t cols, int batch,
+int quantize_typed(const void *x, const int *row_map, int map_div, int source_rows, int64_t rows, int64_t cols, int batch,
                    bool transposed, uint8_t *codes, uint8_t *scales, cudaStream_t s) {
     const int row_tiles = static_cast<int>((rows + 127) / 128), chunks = static_cast<int>((cols + 255) / 256);
     if (transposed) {
         auto kern = rows % 2 == 0 ? quantize_cols_kernel<BF16, true, RELU2, MAP> : quantize_cols_kernel<BF16, false, RELU2, MAP>;
         return launch_pdl(kern, grid_for(static_cast<int64_t>(row_tiles) * 2 * batch, chunks), dim3(kThreads), 0, s, x,
-                          row_map, map_div, rows, cols, row_tiles, chunks, codes, scales);
+                          row_map, map_div, source_rows, rows, cols, row_tiles, chunks, codes, scales);
     }
     if constexpr (BF16) {
         int64_t warps = static_cast<int64_t>(row_tiles) * batch * 4 * chunks * 2;
@@ -826,19 +831,19 @@ int quantize_typed(const void *x, const int *row_map, int map_div, int64_t rows,
         auto kern = halves == 2 ? (cols % 8 == 0 ? quantize_blocks_kernel<RELU2, MAP != 0, true, 2> : quantize_blocks_kernel<RELU2, MAP != 0, false, 2>)
                                 : (cols % 8 == 0 ? quantize_blocks_kernel<RELU2, MAP != 0, true, 1> : quantize_blocks_kernel<RELU2, MAP != 0, false, 1>);
         return launch_pdl(kern, dim3(static_cast<unsigned>((warps + w - 1) / w)), dim3(32 * w), 0, s,
-                          static_cast<const uint16_t *>(x), row_map, map_div, rows, cols, row_tiles, chunks * 2,
+                          static_cast<const uint16_t *>(x), row_map, map_div, source_rows, rows, cols, row_tiles, chunks * 2,
                           static_cast<uint32_t>(warps), codes, scales);
     } else {
         auto kern = cols % 4 == 0 ? quantize_rows_kernel<true, RELU2, MAP != 0> : quantize_rows_kernel<false, RELU2, MAP != 0>;
         return launch_pdl(kern, grid_for(static_cast<int64_t>(row_tiles) * 4 * batch, chunks), dim3(kThreads), 0, s,
-                          static_cast<const float *>(x), row_map, map_div, rows, cols, row_tiles, chunks, codes, scales);
+                          static_cast<const float *>(x), row_map, map_div, source_rows, rows, cols, row_tiles, chunks, codes, scales);
     }
 }
 
 template <bool BF16>
-int quantize_dtype(const void *x, const int *row_map, int map_div, int64_t rows, int64_t cols, int batch,
+int quantize_dtype(const void *x, const int *row_map, int map_div, int source_rows, int64_t rows, int64_t cols, int batch,
                    bool transposed, bool relu2, uint8_t *codes, uint8_t *scales, cudaStream_t s) {
-#define MLPBLK_Q(R, M) return quantize_typed<BF16, R, M>(x, row_map, map_div, rows, cols, batch, transposed, codes, scales, s)
+#define MLPBLK_Q(R, M) return quantize_typed<BF16, R, M>(x, row_map, map_div, source_rows, rows, cols, batch, transposed, codes, scales, s)
 #define MLPBLK_QM(R)                          \
     {                                         \
         if (!row_map) MLPBLK_Q(R, 0);         \
@@ -874,11 +879,11 @@ int dequantize_typed(const uint8_t *codes, const uint8_t *scales, int64_t rows, 
 
 }  // namespace
 
-int launch_fp4_quantize(int dtype, const void *x, const int *row_map, int map_div, int64_t rows, int64_t cols,
-                        int batch, bool transposed, bool relu2, uint8_t *codes, uint8_t *scales, cudaStream_t s) {
+int launch_fp4_quantize(int dtype, const void *x, const int *row_map, int map_div, int source_rows, int64_t rows,
+                        int64_t cols, int batch, bool transposed, bool relu2, uint8_t *codes, uint8_t *scales, cudaStream_t s) {
     return dtype == MLPBLK_BF16
-               ? quantize_dtype<true>(x, row_map, map_div, rows, cols, batch, transposed, relu2, codes, scales, s)
-               : quantize_dtype<false>(x, row_map, map_div, rows, cols, batch, transposed, relu2, codes, scales, s);
+               ? quantize_dtype<true>(x, row_map, map_div, source_rows, rows, cols, batch, transposed, relu2, codes, scales, s)
+               : quantize_dtype<false>(x, row_map, map_div, source_rows, rows, cols, batch, transposed, relu2, codes, scales, s);
 }
 
 int launch_fp4_dequantize(int dtype, const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols,

@@ -21,8 +21,8 @@ __host__ __device__ inline int64_t fp4_scales_bytes(int64_t rows, int64_t cols) 
 }
 
 // Host: MXFP4 quantisation and reading back (fp4.cu).
-int launch_fp4_quantize(int dtype, const void *x, const int *row_map, int map_div, int64_t rows, int64_t cols,
-                        int batch, bool transposed, bool relu2, uint8_t *codes, uint8_t *scales, cudaStream_t s);
+int launch_fp4_quantize(int dtype, const void *x, const int *row_map, int map_div, int source_rows, int64_t rows,
+                        int64_t cols, int batch, bool transposed, bool relu2, uint8_t *codes, uint8_t *scales, cudaStream_t s);
 int launch_fp4_dequantize(int dtype, const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols,
                           int batch, void *y, cudaStream_t s);
 

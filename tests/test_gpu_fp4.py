@@ -223,6 +223,39 @@ def test_quantize_through_a_sort(mb, shape, transposed, gather):
     np.testing.assert_array_equal(_bytes(q.codes), packed)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("d", [64, 90, 101])
+def test_rows_mapped_beyond_the_source_are_zeros(mb, d, transposed, dtype):
+    """A gathering map of a larger batch: entries at or behind the source's last row come
+    out as zero blocks, and what lies around the source (NaN here) reaches no code."""
+    import torch
+    T, R, div = 21, 300, 3
+    rng = np.random.default_rng(d)
+    row_map = rng.integers(-3, 3 * T * div, R).astype(np.int32)
+    row_map[:4] = [T * div - 1, T * div, 2 ** 31 - 1, -2 ** 31]
+    whole = torch.full((2 * 64 * d + T * d,), float("nan"), dtype=_dt(dtype), device="cuda")
+    x, v = _draw(rng, (T, d), dtype)
+    whole[64 * d:64 * d + T * d] = x.reshape(-1)
+    at = np.where(row_map >= 0, row_map // div, T)
+    src = np.where((at < T)[:, None], v[np.minimum(at, T - 1)], 0.0)
+    packed, tiled = fp4.pack(*fp4.quantize(src.T if transposed else src))
+    shape = (d, R) if transposed else (R, d)
+    rm = torch.from_numpy(row_map).cuda()
+    q = mb.Fp4Matrix(*shape)
+    # the rows stated, and (0) those that the tensor has
+    for rows, xs in ((T, whole[64 * d:]), (0, whole[64 * d:64 * d + T * d])):
+        q.codes.fill_(0xAA)
+        q.scales.fill_(0xAA)
+        mb.mlpblk_fp4_quantize(mb.make_fp4_desc(*shape, dtype=dtype, transposed=transposed, source_rows=rows), xs,
+                               q.codes, q.scales, row_map=rm, map_div=div)
+        np.testing.assert_array_equal(_bytes(q.scales), tiled)
+        np.testing.assert_array_equal(_bytes(q.codes), packed)
+    with pytest.raises(mb.MlpBlkError):                     # fewer rows than stated
+        mb.mlpblk_fp4_quantize(mb.make_fp4_desc(*shape, dtype=dtype, transposed=transposed, source_rows=T + 1),
+                               x, q.codes, q.scales, row_map=rm, map_div=div)
+
+
 # ---------------------------------------------------------------------- products
 
 def _check(got, a, b, out, k, base=None):

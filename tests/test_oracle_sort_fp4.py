@@ -167,6 +167,17 @@ def test_fp4_sizes_and_refusals(mb):
     assert dq(good, 0x10000) == dq(good, 0x30004) == mb.MLPBLK_EINVAL
 
 
+def test_fp4_gather_needs_the_sources_rows(mb):
+    """A row map that gathers is taken only with the source's row count: the map's
+    values are device data, and nothing else bounds the rows that are read."""
+    q = lambda d, rm=0x40000, div=2: mb.lib.mlpblk_fp4_quantize(ctypes.byref(d), 0x10000, rm, div, 0x20000, 0x30000, None)
+    for n in (0, -1, 1 << 31):
+        for tr in (False, True):
+            assert q(mb.make_fp4_desc(8, 64, transposed=tr, source_rows=n)) == mb.MLPBLK_EINVAL
+    assert q(mb.make_fp4_desc(0, 64)) == q(mb.make_fp4_desc(8, 0)) == mb.MLPBLK_OK    # nothing is read
+    assert mb.mlpblk_fp4_codes_size(mb.make_fp4_desc(8, 64, source_rows=-1)) == 8 * 32  # of no meaning elsewhere
+
+
 def test_fp4_product_refusals(mb):
     p = _addresses(5)
     mm = lambda d, a=p: mb.lib.mlpblk_fp4_matmul(ctypes.byref(d), *a, None)
