@@ -634,7 +634,7 @@ class MoeSort(_Kept):
     """The plan of one batch's routing and its buffers: `sort` fills count, seg, pos
     and row_map from the expert ids, the other methods move rows by it (the
     mlpblk_moe_* calls of the same names).  `rows` is R, the row count of the sorted
-    buffers."""
+    buffers.  Before the first `sort` the plan is that of ids that select nothing."""
 
     def __init__(self, tokens, width, experts, top_k, pad=128, dtype="bf16", device="cuda"):
         import torch
@@ -645,8 +645,8 @@ class MoeSort(_Kept):
         e = dict(dtype=torch.int32, device=device)
         self._count = torch.zeros(experts, **e)
         self._seg = torch.zeros(experts + 1, **e)
-        self._pos = torch.empty(tokens, top_k, **e)
-        self._row_map = torch.empty(self.rows, **e)
+        self._pos = torch.full((tokens, top_k), -1, **e)   # a plan of no entry until `sort` makes one
+        self._row_map = torch.full((self.rows,), -1, **e)
         self._dev = self._count.get_device()
         self._d = ctypes.addressof(self.desc)
         self._at = tuple(t.data_ptr() for t in (self._count, self._seg, self._pos, self._row_map))

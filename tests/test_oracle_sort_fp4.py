@@ -144,6 +144,20 @@ def test_sort_argument_refusals(mb):
     assert mb.lib.mlpblk_moe_unpermute_backward(empty, *[None] * 8, None) == mb.MLPBLK_OK
 
 
+@pytest.mark.parametrize("shape", [(10, 4, 2, 128), (5, 200, 3, 1), (0, 4, 2, 16)])
+def test_a_plan_not_made_yet_selects_nothing(mb, shape):
+    """The plan's buffers of a new MoeSort, in memory that held something else before."""
+    torch = pytest.importorskip("torch")
+    T, E, k, pad = shape
+    for _ in range(3):
+        keep = [torch.full((max(n, 1),), 7, dtype=torch.int32) for n in (T * k, sort.rows_bound(T, k, E, pad))]
+        del keep
+        s = mb.MoeSort(T, 64, E, k, pad, device="cpu")
+        ref = sort.plan(np.full((T, k), -1), E, pad)
+        for got, want in zip((s.count, s.seg, s.pos, s.row_map), ref):
+            np.testing.assert_array_equal(got.numpy(), want)
+
+
 def test_fp4_sizes_and_refusals(mb):
     size = lambda r, c, b=1: (mb.mlpblk_fp4_codes_size(mb.make_fp4_desc(r, c, b)),
                               mb.mlpblk_fp4_scales_size(mb.make_fp4_desc(r, c, b)))
