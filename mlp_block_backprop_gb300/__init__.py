@@ -870,14 +870,15 @@ class Fp4Matrix(_Kept):
     def _desc(self, dtype, transposed, act, source_rows=0):
         """Address of the descriptor for these options, made once."""
         key = (dtype, transposed, act, source_rows)
-        d = self._descs.get(key)
-        if d is None:
+        at = self._descs.get(key)
+        if at is None:
             if act not in self._ACTS:
                 raise MlpBlkError(MLPBLK_ENOTSUP, f"Fp4Matrix.quantize: act {act!r}")
-            self._kept.append(make_fp4_desc(self.rows, self.cols, self.batch, dtype, transposed, self._ACTS[act],
-                                            source_rows))
-            d = self._descs[key] = ctypes.addressof(self._kept[-1])
-        return d
+            d = make_fp4_desc(self.rows, self.cols, self.batch, dtype, transposed, self._ACTS[act], source_rows)
+            self._kept.append(d)
+            # another thread may make the same one: the first stays, each lives in _kept
+            at = self._descs.setdefault(key, ctypes.addressof(d))
+        return at
 
     def quantize(self, x, transposed=False, act="none", sort=None, gather=False, stream=None):
         """From x (bf16 or float32; stored [cols, rows] when transposed).  sort: a

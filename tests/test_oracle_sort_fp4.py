@@ -254,3 +254,42 @@ def test_both_ways_into_the_library_agree(mb):
             mb._calls.fp4_quantize(at(fp4), 0x10000)
         with pytest.raises(TypeError):
             mb._calls.fp4_quantize(at(fp4), "x", None, 0, 0x20000, 0x30000, None)
+
+
+def test_descriptors_of_first_calls_from_several_threads(mb):
+    """Threads that make the first calls with different options on one matrix: each
+    kept descriptor is its key's, also where threads change over between any two
+    steps of making one (`_kept` below yields there)."""
+    import threading
+    import time
+    torch = pytest.importorskip("torch")
+    u8 = dict(dtype=torch.uint8, device="cpu")
+
+    class Yielding(list):
+        def append(self, d):
+            super().append(d)
+            time.sleep(0.01)
+
+    for _ in range(3):
+        q = mb.Fp4Matrix(4, 64, codes=torch.zeros(4 * 32, **u8), scales=torch.zeros(1024, **u8), device="cpu")
+        q._kept = Yielding()
+        keys = [(dt, tr, act, n) for dt in (torch.bfloat16, torch.float32) for tr in (False, True)
+                for act in ("none", "relu2") for n in (0, 9)]
+        got = {}
+        start = threading.Barrier(2 * len(keys))
+
+        def first_call(i, key):
+            start.wait()
+            got[i] = q._desc(*key)
+
+        threads = [threading.Thread(target=first_call, args=(i, k)) for i, k in enumerate(keys * 2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        for i, (dt, tr, act, n) in enumerate(keys * 2):
+            assert got[i] == q._descs[(dt, tr, act, n)]
+            d = mb.Fp4Desc.from_address(got[i])
+            assert (d.rows, d.cols, d.batch) == (4, 64, 1)
+            assert (d.dtype, d.transposed, d.act, d.source_rows) == (
+                mb.MLPBLK_BF16 if dt is torch.bfloat16 else mb.MLPBLK_FP32, int(tr), int(act == "relu2"), n)
