@@ -11,18 +11,16 @@
 
 static void *ptr(PyObject *o) { return o == Py_None ? NULL : PyLong_AsVoidPtr(o); }
 
-static PyObject *result(int rc) {
-    if (PyErr_Occurred()) return NULL; /* an argument was no integer */
-    return PyLong_FromLong(rc);
-}
-
 static int count(Py_ssize_t n, Py_ssize_t want) {
     if (n == want) return 1;
     PyErr_Format(PyExc_TypeError, "%zd arguments, %zd expected", n, want);
     return 0;
 }
 
-/* Converts every argument before the call, so that a bad one calls nothing. */
+/* Converts every argument before the call, so that a bad one calls nothing.  The call
+ * runs without the interpreter's lock, as it does through ctypes: a launch can block (a
+ * full launch queue, a kernel's first load), and what it waits for may be a callback that
+ * needs the lock. */
 #define CALL(name, N, ...)                                                       \
     static PyObject *py_##name(PyObject *self, PyObject *const *o, Py_ssize_t n) { \
         void *a[N];                                                              \
@@ -30,7 +28,11 @@ static int count(Py_ssize_t n, Py_ssize_t want) {
         if (!count(n, N)) return NULL;                                           \
         for (int i = 0; i < N; ++i) a[i] = ptr(o[i]);                            \
         if (PyErr_Occurred()) return NULL;                                       \
-        return result(mlpblk_##name(__VA_ARGS__));                               \
+        int rc;                                                                  \
+        Py_BEGIN_ALLOW_THREADS                                                   \
+        rc = mlpblk_##name(__VA_ARGS__);                                         \
+        Py_END_ALLOW_THREADS                                                     \
+        return PyLong_FromLong(rc);                                              \
     }
 
 CALL(moe_sort, 7, a[0], a[1], a[2], a[3], a[4], a[5], a[6])

@@ -293,3 +293,69 @@ def test_descriptors_of_first_calls_from_several_threads(mb):
             assert (d.rows, d.cols, d.batch) == (4, 64, 1)
             assert (d.dtype, d.transposed, d.act, d.source_rows) == (
                 mb.MLPBLK_BF16 if dt is torch.bfloat16 else mb.MLPBLK_FP32, int(tr), int(act == "relu2"), n)
+
+
+_STUB = """
+#include <stdint.h>
+#include <time.h>
+#include "mlpblk.h"
+volatile int stub_entered = 0, stub_release = 0;
+/* waits up to 5 s for another thread to set stub_release: 0 where it did, else 1 */
+static int waited(void) {
+    struct timespec t0, t;
+    clock_gettime(CLOCK_MONOTONIC, &t0);
+    stub_entered = 1;
+    do clock_gettime(CLOCK_MONOTONIC, &t);
+    while (!stub_release && t.tv_sec - t0.tv_sec < 5);
+    return stub_release ? 0 : 1;
+}
+"""
+
+
+def test_native_calls_let_other_threads_run(mb, tmp_path):
+    """The CPython entry points around stand-ins that return only once another Python
+    thread has run: each is entered without the interpreter's lock."""
+    import os
+    import re
+    import subprocess
+    import sys
+    import sysconfig
+    if not mb._calls.native:
+        pytest.skip("built without Python's headers")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(mb.__file__)))
+    src = os.path.join(root, "mlp_block_backprop_gb300", "csrc", "pycalls.c")
+    names = re.findall(r"^CALL\((\w+), (\d+),", open(src).read(), flags=re.M)
+    assert len(names) >= 10
+    header = re.sub(r"/\*.*?\*/", "", open(os.path.join(root, "include", "mlpblk.h")).read(), flags=re.S)
+    stubs = ""
+    for name, _ in names:
+        params = re.search(r"int mlpblk_%s\(([^;]*?)\);" % name, header, flags=re.S).group(1)
+        stubs += "int mlpblk_%s(%s) { return waited(); }\n" % (name, params)
+    c = tmp_path / "stub.c"
+    c.write_text(_STUB + stubs)
+    inc = sysconfig.get_paths()["include"]
+    out = str(tmp_path / "_mlpblk_calls.so")
+    r = subprocess.run(["gcc", "-O1", "-shared", "-fPIC", "-I", inc, "-I", os.path.join(root, "include"), "-I", os.path.dirname(src),
+                        src, str(c), "-o", out, "-Wl,-Bsymbolic"], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    run = f"""
+import ctypes, importlib.machinery, importlib.util, threading, time
+spec = importlib.util.spec_from_file_location("_mlpblk_calls", {out!r})
+m = importlib.util.module_from_spec(spec)
+spec.loader.exec_module(m)
+stub = ctypes.CDLL({out!r})
+entered, release = ctypes.c_int.in_dll(stub, "stub_entered"), ctypes.c_int.in_dll(stub, "stub_release")
+for name, n in {[(n, int(k)) for n, k in names]!r}:
+    entered.value = release.value = 0
+    def other():
+        while not entered.value:
+            time.sleep(0.001)
+        release.value = 1
+    t = threading.Thread(target=other)
+    t.start()
+    rc = getattr(m, "mlpblk_" + name)(*[16] * n)
+    t.join()
+    assert rc == 0, name
+"""
+    r = subprocess.run([sys.executable, "-c", run], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr
