@@ -11,10 +11,14 @@ the library has not been built: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmlpblk.so")
+# csrc/pycalls.c as built for this interpreter: the name carries its ABI tag
+CALLS_PATH = os.path.join(_HERE, "_mlpblk_calls" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 MLPBLK_OK = 0
 MLPBLK_EINVAL = 1
@@ -229,18 +233,29 @@ lib = _load()
 
 class _Calls:
     """The latency-bound entry points for the classes below, descriptors and tensors by
-    address: csrc/pycalls.c where it was built (it needs Python's headers), else the
-    same functions through ctypes."""
+    address: csrc/pycalls.c where it was built for this interpreter (it needs Python's
+    headers), else the same functions through ctypes."""
 
     def __init__(self):
-        try:
-            from . import _mlpblk_calls as native
-        except ImportError:
-            native = None
+        native = self._native()
         for name in ("moe_sort", "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
                      "fp4_quantize", "fp4_dequantize", "fp4_matmul", "fp4_matmul_grouped", "fp4_wgrad_grouped"):
             setattr(self, name, getattr(native, "mlpblk_" + name) if native else self._ctypes("mlpblk_" + name))
         self.native = native is not None
+
+    @staticmethod
+    def _native():
+        """The module at CALLS_PATH, or None.  By its path: an import would also take a
+        file without an ABI tag, whichever interpreter it was built for."""
+        if not os.path.exists(CALLS_PATH):
+            return None
+        spec = importlib.util.spec_from_file_location(__name__ + "._mlpblk_calls", CALLS_PATH)
+        try:
+            native = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(native)
+        except ImportError:
+            return None
+        return native
 
     @staticmethod
     def _ctypes(name):

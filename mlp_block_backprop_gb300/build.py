@@ -7,6 +7,8 @@ extension machinery: the library has a plain C ABI (include/mlpblk.h).
 
 from __future__ import annotations
 
+import glob
+import importlib.machinery
 import os
 import shutil
 import subprocess
@@ -18,7 +20,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmlpblk.so")
-CALLS = os.path.join(HERE, "_mlpblk_calls.so")   # csrc/pycalls.c: CPython entry to the latency-bound calls
+# csrc/pycalls.c: CPython entry to the latency-bound calls, for this interpreter alone
+CALLS = os.path.join(HERE, "_mlpblk_calls" + importlib.machinery.EXTENSION_SUFFIXES[0])
 SOURCES = ["api.cu", "gemm_fwd.cu", "gemm_bwd.cu", "rowops.cu", "simt_f32.cu", "noalloc.cu", "optim.cu", "fp8.cu", "gemm_f8.cu", "moe.cu",
            "sort.cu", "fp4.cu", "gemm_f4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -65,6 +68,12 @@ def _build_calls() -> None:
     os.replace(tmp, CALLS)
 
 
+def _remove_calls() -> None:
+    """Every interpreter's module: they were built against the library before this one."""
+    for path in glob.glob(os.path.join(glob.escape(HERE), "_mlpblk_calls*.so")):
+        os.remove(path)
+
+
 def build_library(force: bool = False, verbose: bool = False) -> str:
     """Compile and link libmlpblk.so; returns its path.  Raises on failure."""
     if not force and up_to_date():
@@ -91,6 +100,7 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _remove_calls()
     _build_calls()
     return LIB
 

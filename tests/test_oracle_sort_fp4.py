@@ -359,3 +359,40 @@ for name, n in {[(n, int(k)) for n, k in names]!r}:
 """
     r = subprocess.run([sys.executable, "-c", run], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr
+
+
+def test_native_calls_belong_to_one_interpreter(mb, tmp_path):
+    """The module's file name carries the interpreter's ABI tag; one without a tag, or of
+    another interpreter, is not loaded: the calls then go through ctypes."""
+    import importlib.machinery
+    import os
+    import shutil
+    import subprocess
+    import sys
+    if not mb._calls.native:
+        pytest.skip("built without Python's headers")
+    suffix = importlib.machinery.EXTENSION_SUFFIXES[0]
+    here = os.path.dirname(os.path.abspath(mb.__file__))
+    built = os.path.join(here, "_mlpblk_calls" + suffix)
+    assert "cpython" in suffix and os.path.exists(built)
+    pkg = tmp_path / "mlp_block_backprop_gb300"
+    pkg.mkdir()
+    for name in ("__init__.py", "libmlpblk.so"):
+        shutil.copy(os.path.join(here, name), pkg / name)
+    run = "import mlp_block_backprop_gb300 as mb; print(mb.__file__, mb._calls.native)"
+    for name, native in (("_mlpblk_calls.so", False), ("_mlpblk_calls.cpython-39-none.so", False), ("_mlpblk_calls" + suffix, True)):
+        shutil.copy(built, pkg / name)
+        r = subprocess.run([sys.executable, "-c", run], capture_output=True, text=True, cwd=tmp_path,
+                           env={**os.environ, "PYTHONPATH": str(tmp_path)})
+        assert r.returncode == 0 and r.stdout.split() == [str(pkg / "__init__.py"), str(native)], (name, r)
+
+
+def test_a_new_library_leaves_no_other_interpreters_module(tmp_path, monkeypatch):
+    """A module built against the library before this one does not stay behind."""
+    import __graft_entry__
+    build = __graft_entry__._build_script()
+    monkeypatch.setattr(build, "HERE", str(tmp_path))
+    for name in ("_mlpblk_calls.so", "_mlpblk_calls.cpython-39-none.so", "libmlpblk.so", "other.so"):
+        (tmp_path / name).write_bytes(b"")
+    build._remove_calls()
+    assert sorted(f.name for f in tmp_path.iterdir()) == ["libmlpblk.so", "other.so"]
