@@ -441,7 +441,8 @@ int mlpblk_moe_backward_overwrite(const mlpblk_moe_desc *desc,
  * of 16 bytes move in 16-byte accesses.  pos, count and seg are those that
  * mlpblk_moe_sort wrote for the same descriptor.  Limits: width < 2^30, experts
  * 1..256, top_k 1..256, pad 1..1024, R < 2^31.  Pointers are device pointers, 16-byte aligned.
- * Outputs alias no input (MLPBLK_EINVAL) but where stated.  Each returns an
+ * Outputs share no byte with an input (MLPBLK_EINVAL) but where stated, nor with each
+ * other.  Each returns an
  * MLPBLK_* code; tokens = 0 returns MLPBLK_OK and touches nothing, except that
  * mlpblk_moe_sort still writes count and seg (zeros).
  */
@@ -513,7 +514,8 @@ int mlpblk_moe_unpermute_backward(const mlpblk_sort_desc *desc, const void *dy, 
  * Limits: rows, cols >= 0 (with either 0: MLPBLK_OK, nothing is touched),
  * rows * batch and cols < 2^31, ceil(rows / 128) * batch < 2^29, ceil(rows / 128) *
  * batch * ceil(cols / 256) < 2^28 (275 GB of scales), rows * batch * ceil(cols / 256)
- * < 2^31; pointers 16-byte aligned.
+ * < 2^31; pointers 16-byte aligned; outputs share no byte with an input or with each
+ * other (MLPBLK_EINVAL).
  */
 #define MLPBLK_FP4_ACT_NONE   0
 #define MLPBLK_FP4_ACT_RELU2  1
@@ -559,8 +561,8 @@ int mlpblk_fp4_dequantize(const mlpblk_fp4_desc *desc, const void *codes, const 
  * count and seg are those of mlpblk_moe_sort.  With m = 0 (wgrad_grouped: k = 0, not
  * accumulating: C is still set to zero) nothing is touched.  Limits: m, n, k and
  * experts * n (wgrad: experts * m) < 2^31, experts 1..256; experts and pad are 0 for
- * mlpblk_fp4_matmul.  Pointers are device pointers, 16-byte aligned; C aliases no
- * operand.  Returns an MLPBLK_* code.
+ * mlpblk_fp4_matmul.  Pointers are device pointers, 16-byte aligned; C shares no byte
+ * with an operand, count or seg (MLPBLK_EINVAL).  Returns an MLPBLK_* code.
  */
 typedef struct {
     int64_t m, n, k;

@@ -12,6 +12,7 @@
 #include <math.h>
 #include <stdlib.h>
 
+#include <initializer_list>
 #include <new>
 
 #include "fp4_layout.h"
@@ -1278,7 +1279,31 @@ int moe_backward_entry(const mlpblk_moe_desc *desc, const void *dy, const void *
 
 namespace {
 
+// The bytes of one argument, for the check that outputs lie apart (NULL: none).
+struct Span {
+    uintptr_t first, end;
+    Span(const void *p, int64_t n, int64_t element, int64_t more = 1) : first(reinterpret_cast<uintptr_t>(p)), end(first) {
+        const unsigned __int128 top = static_cast<unsigned __int128>(first) + static_cast<unsigned __int128>(n) * element * more;
+        if (p) end = top > UINTPTR_MAX ? UINTPTR_MAX : static_cast<uintptr_t>(top);
+    }
+    bool meets(const Span &o) const { return first < o.end && o.first < end; }
+};
+
+// No output shares a byte with an input or with another output.
+bool apart(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+    for (const Span *o = outputs.begin(); o != outputs.end(); ++o) {
+        for (const Span &i : inputs)
+            if (o->meets(i)) return false;
+        for (const Span *p = outputs.begin(); p != o; ++p)
+            if (o->meets(*p)) return false;
+    }
+    return true;
+}
+
 // ----------------------------------------------- tokens sorted by expert and back
+
+// Bytes of a row's element.
+int64_t element_bytes(int dtype) { return dtype == MLPBLK_BF16 ? 2 : 4; }
 
 int check_sort_desc(const mlpblk_sort_desc *d) {
     if (!d) return MLPBLK_EINVAL;
@@ -1348,7 +1373,12 @@ int fp4_product(const mlpblk_fp4_matmul_desc *desc, int mode, const void *a_code
     if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(b_codes) || !aligned16(b_scales) || !aligned16(c))
         return MLPBLK_EINVAL;
     if ((mode != kFp4Dense && !aligned16(seg)) || (mode == kFp4GroupRows && !aligned16(count))) return MLPBLK_EINVAL;
-    if (c == a_codes || c == a_scales || c == b_codes || c == b_scales || c == seg || c == count) return MLPBLK_EINVAL;
+    const int64_t b_mats = mode == kFp4GroupRows ? desc->experts : 1, c_mats = mode == kFp4GroupK ? desc->experts : 1;
+    if (!apart({Span(c, desc->m, desc->n * element_bytes(desc->out_dtype), c_mats)},
+               {Span(a_codes, desc->m, fp4_row_bytes(desc->k)), Span(a_scales, fp4_scales_bytes(desc->m, desc->k), 1),
+                Span(b_codes, desc->n, fp4_row_bytes(desc->k), b_mats), Span(b_scales, fp4_scales_bytes(desc->n, desc->k), b_mats),
+                Span(count, desc->experts, 4), Span(seg, desc->experts + 1, 4)}))
+        return MLPBLK_EINVAL;
     int sms = 0;
     MLPBLK_TRY(device_sms(&sms));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1386,7 +1416,9 @@ int mlpblk_moe_sort(const mlpblk_sort_desc *desc, const int32_t *expert_idx, int
     const int64_t n = desc->tokens * desc->top_k;
     if (!aligned16(count) || !aligned16(seg)) return MLPBLK_EINVAL;
     if (n > 0 && (!aligned16(expert_idx) || !aligned16(pos) || !aligned16(row_map))) return MLPBLK_EINVAL;
-    if (n > 0 && (pos == expert_idx || row_map == expert_idx)) return MLPBLK_EINVAL;
+    if (!apart({Span(count, desc->experts, 4), Span(seg, desc->experts + 1, 4), Span(pos, n, 4), Span(row_map, sort_rows(desc), 4)},
+               {Span(expert_idx, n, 4)}))
+        return MLPBLK_EINVAL;
     int sms = 0;
     MLPBLK_TRY(device_sms(&sms));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1400,7 +1432,10 @@ int mlpblk_moe_permute(const mlpblk_sort_desc *desc, const void *x, const int32_
     MLPBLK_TRY(check_sort_desc(desc));
     if (desc->tokens == 0) return MLPBLK_OK;
     if (!aligned16(x) || !aligned16(pos) || !aligned16(count) || !aligned16(seg) || !aligned16(rows)) return MLPBLK_EINVAL;
-    if (rows == x) return MLPBLK_EINVAL;
+    const int64_t row = desc->width * element_bytes(desc->dtype);
+    if (!apart({Span(rows, sort_rows(desc), row)}, {Span(x, desc->tokens, row), Span(pos, desc->tokens * desc->top_k, 4),
+                                                    Span(count, desc->experts, 4), Span(seg, desc->experts + 1, 4)}))
+        return MLPBLK_EINVAL;
     int sms = 0;
     MLPBLK_TRY(device_sms(&sms));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1416,7 +1451,10 @@ int mlpblk_moe_unpermute(const mlpblk_sort_desc *desc, const void *rows, const i
     if (desc->tokens == 0) return MLPBLK_OK;
     if (!aligned16(rows) || !aligned16(pos) || !aligned16(y)) return MLPBLK_EINVAL;
     if ((weights && !aligned16(weights)) || (residual && !aligned16(residual))) return MLPBLK_EINVAL;
-    if (y == rows) return MLPBLK_EINVAL;
+    const int64_t row = desc->width * element_bytes(desc->dtype), n = desc->tokens * desc->top_k;
+    if (!apart({Span(y, desc->tokens, row)}, {Span(rows, sort_rows(desc), row), Span(pos, n, 4), Span(weights, n, 4),
+                                              Span(residual == y ? nullptr : residual, desc->tokens, row)}))
+        return MLPBLK_EINVAL;
     int sms = 0;
     MLPBLK_TRY(device_sms(&sms));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1438,7 +1476,12 @@ int mlpblk_moe_unpermute_backward(const mlpblk_sort_desc *desc, const void *dy, 
     if (desc->tokens == 0) return MLPBLK_OK;
     if (!aligned16(dy) || !aligned16(pos) || !aligned16(count) || !aligned16(seg) || !aligned16(d_rows)) return MLPBLK_EINVAL;
     if ((weights && !aligned16(weights)) || (d_weights && (!aligned16(d_weights) || !aligned16(rows)))) return MLPBLK_EINVAL;
-    if (d_rows == dy || d_rows == rows || (d_weights && d_weights == weights)) return MLPBLK_EINVAL;
+    const int64_t row = desc->width * element_bytes(desc->dtype), n = desc->tokens * desc->top_k, r = sort_rows(desc);
+    if (d_rows == rows) return MLPBLK_EINVAL;
+    if (!apart({Span(d_rows, r, row), Span(d_weights, n, 4)},
+               {Span(dy, desc->tokens, row), Span(d_weights ? rows : nullptr, r, row), Span(pos, n, 4), Span(count, desc->experts, 4),
+                Span(seg, desc->experts + 1, 4), Span(weights, n, 4)}))
+        return MLPBLK_EINVAL;
     int sms = 0;
     MLPBLK_TRY(device_sms(&sms));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1466,7 +1509,13 @@ int mlpblk_fp4_quantize(const mlpblk_fp4_desc *desc, const void *x, const int32_
     const int64_t source_rows = row_map && map_div > 0 ? desc->source_rows : 1;
     if (source_rows < 1 || source_rows >= kFp4Lim) return MLPBLK_EINVAL;
     if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || (row_map && !aligned16(row_map))) return MLPBLK_EINVAL;
-    if (codes == x || scales == x || codes == scales) return MLPBLK_EINVAL;
+    // x's rows: Q's, or, transposed, its columns, or those that the map gathers from
+    const int64_t mapped = desc->transposed ? desc->cols : desc->rows, width = desc->transposed ? desc->rows : desc->cols;
+    const int64_t x_rows = row_map && map_div > 0 ? source_rows : mapped * desc->batch;
+    if (!apart({Span(codes, desc->rows * desc->batch, fp4_row_bytes(desc->cols)),
+                Span(scales, fp4_scales_bytes(desc->rows, desc->cols), desc->batch)},
+               {Span(x, x_rows, width * element_bytes(desc->dtype)), Span(row_map, mapped, 4)}))
+        return MLPBLK_EINVAL;
     int sms = 0;
     MLPBLK_TRY(device_sms(&sms));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1483,7 +1532,10 @@ int mlpblk_fp4_dequantize(const mlpblk_fp4_desc *desc, const void *codes, const 
     if (desc->transposed != 0 || desc->act != MLPBLK_FP4_ACT_NONE) return MLPBLK_ENOTSUP;
     if (desc->rows == 0 || desc->cols == 0) return MLPBLK_OK;
     if (!aligned16(codes) || !aligned16(scales) || !aligned16(y)) return MLPBLK_EINVAL;
-    if (y == codes || y == scales) return MLPBLK_EINVAL;
+    if (!apart({Span(y, desc->rows * desc->batch, desc->cols * element_bytes(desc->dtype))},
+               {Span(codes, desc->rows * desc->batch, fp4_row_bytes(desc->cols)),
+                Span(scales, fp4_scales_bytes(desc->rows, desc->cols), desc->batch)}))
+        return MLPBLK_EINVAL;
     int sms = 0;
     MLPBLK_TRY(device_sms(&sms));
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -658,3 +658,67 @@ def test_without_the_native_calls(mb, monkeypatch):
     test_experts_together(mb)
     test_grouped_wgrad(mb, (40, 300, 200, 5, 2), True)
     test_quantize_rows(mb, (5, 33), "f32")
+
+
+def test_buffers_that_only_touch(mb):
+    """Every buffer of a pass cut from one allocation, each directly behind the one before:
+    nothing is refused, nothing is written beyond its own bytes."""
+    import torch
+    T, d, n, E, k, pad = 40, 96, 72, 4, 2, 256
+    rng = np.random.default_rng(21)
+    s0 = mb.MoeSort(T, d, E, k, pad)
+    R = s0.rows
+    whole = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+    at = [0]
+
+    def cut(shape, dtype):
+        size = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+        assert size % 16 == 0
+        at[0] += size
+        return whole[at[0] - size:at[0]].view(dtype).view(shape)
+
+    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
+    idx, count, seg4 = cut((T, k), i32), cut((E,), i32), cut((8,), i32)
+    seg, pos, row_map = seg4[:E + 1], cut((T, k), i32), cut((R,), i32)
+    x, rows, w, y = cut((T, d), f32), cut((R, d), f32), cut((T, k), f32), cut((T, d), f32)
+    dr, dw, dx = cut((R, d), f32), cut((T, k), f32), cut((T, d), f32)
+    fp4_of = lambda r, c, b=1: (cut((r * b * -(-c // 32) * 16,), u8), cut((-(-r // 128) * -(-c // 256) * 1024 * b,), u8))
+    a, bt, at_, = fp4_of(R, d), fp4_of(n, d, E), fp4_of(d, R)
+    c, back, g = cut((R, n), f32), cut((R, d), f32), cut((E, d, d), f32)
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    idx.copy_(torch.from_numpy(ids))
+    x.normal_()
+    w.fill_(0.5)
+    wn = torch.randn(E * n, d, device="cuda")
+    desc = mb.make_sort_desc(T, d, E, k, pad, "f32")
+    mb.mlpblk_moe_sort(desc, idx, count, seg, pos, row_map)
+    mb.mlpblk_moe_permute(desc, x, pos, count, seg, rows)
+    mb.mlpblk_moe_unpermute(desc, rows, pos, w, x, y)
+    mb.mlpblk_moe_unpermute_backward(desc, y, rows, pos, count, seg, w, dr, dw)
+    mb.mlpblk_moe_permute_backward(desc, rows, pos, dx)
+    mb.mlpblk_fp4_quantize(mb.make_fp4_desc(R, d, dtype="f32", source_rows=T), x, *a, row_map=row_map, map_div=k)
+    mb.mlpblk_fp4_quantize(mb.make_fp4_desc(n, d, E, dtype="f32"), wn, *bt)
+    mb.mlpblk_fp4_quantize(mb.make_fp4_desc(d, R, dtype="f32", transposed=True, source_rows=T), x, *at_, row_map=row_map, map_div=k)
+    mb.mlpblk_fp4_matmul_grouped(mb.make_fp4_matmul_desc(R, n, d, "f32", experts=E, pad=pad), *a, *bt, count, seg, c)
+    mb.mlpblk_fp4_dequantize(mb.make_fp4_desc(R, d, dtype="f32"), *a, back)
+    mb.mlpblk_fp4_wgrad_grouped(mb.make_fp4_matmul_desc(d, d, R, "f32", experts=E, pad=pad), *at_, *at_, seg, g)
+    assert not whole[at[0]:].any()
+    cn, sn, pn, rn = sort.plan(ids, E, pad)
+    for t, ref in ((idx, ids), (count, cn), (seg, sn), (pos, pn), (row_map, rn)):
+        np.testing.assert_array_equal(t.cpu().numpy(), ref)
+    v = to_np(x)
+    src = np.where((rn >= 0)[:, None], v[np.maximum(rn, 0) // k], 0.0)
+    np.testing.assert_array_equal(to_np(rows), src)
+    # both of a token's rows are the token itself: y = x + x, d_rows = y / 2, dw = <y, x>, dx = 2 x
+    np.testing.assert_array_equal(to_np(y), 2 * v)
+    np.testing.assert_array_equal(to_np(dr), src)
+    np.testing.assert_array_equal(to_np(dx), 2 * v)
+    ref = (2 * v * v).sum(1)
+    assert np.all(np.abs(to_np(dw) - ref[:, None]) <= (d + 1) * 2.0 ** -24 * ref[:, None])
+    np.testing.assert_array_equal(to_np(back), fp4.rounded(src))
+    wv, srcT = fp4.rounded(to_np(wn)).reshape(E, n, d), fp4.rounded(src.T)
+    for e in range(E):
+        r = slice(sn[e], sn[e] + cn[e])
+        _check(to_np(c)[r], fp4.rounded(src)[r], wv[e], "f32", d)
+        r = slice(sn[e], sn[e + 1])
+        _check(to_np(g)[e], srcT[:, r], srcT[:, r], "f32", sn[e + 1] - sn[e])

@@ -144,6 +144,57 @@ def test_sort_argument_refusals(mb):
     assert mb.lib.mlpblk_moe_unpermute_backward(empty, *[None] * 8, None) == mb.MLPBLK_OK
 
 
+def _spans(mb):
+    """Every entry point with its arguments' sizes in bytes, which of them are outputs, and
+    a call of it."""
+    at = ctypes.byref
+    T, w, E, k, pad = 10, 64, 5, 2, 128
+    s = mb.make_sort_desc(T, w, E, k, pad)
+    R, n = mb.mlpblk_moe_sort_rows(s), T * k
+    x, r, c, g = 2 * T * w, 2 * R * w, 4 * E, 4 * (E + 1)
+    yield "mlpblk_moe_sort", (at(s),), [4 * n, c, g, 4 * n, 4 * R], (1, 2, 3, 4)
+    yield "mlpblk_moe_permute", (at(s),), [x, 4 * n, c, g, r], (4,)
+    yield "mlpblk_moe_permute_backward", (at(s),), [r, 4 * n, x], (2,)
+    yield "mlpblk_moe_unpermute", (at(s),), [r, 4 * n, 4 * n, x, x], (4,)
+    yield "mlpblk_moe_unpermute_backward", (at(s),), [x, r, 4 * n, c, g, 4 * n, r, 4 * n], (6, 7)
+    size = lambda rows, cols, b=1: [rows * b * -(-cols // 32) * 16, -(-rows // 128) * -(-cols // 256) * 1024 * b]
+    for tr, b in ((0, 1), (1, 1), (0, 3)):
+        q = mb.make_fp4_desc(40, 300, b, transposed=tr)
+        yield "mlpblk_fp4_quantize", (at(q),), [2 * b * 40 * 300, None, None] + size(40, 300, b), (3, 4)
+    for tr in (0, 1):
+        q = mb.make_fp4_desc(40, 300, dtype="f32", transposed=tr, source_rows=7)
+        yield "mlpblk_fp4_quantize", (at(q),), [4 * 7 * (40 if tr else 300), 4 * (300 if tr else 40), 2] + size(40, 300), (3, 4)
+        yield "mlpblk_fp4_quantize", (at(q),), [4 * 40 * 300, 4 * (300 if tr else 40), 0] + size(40, 300), (3, 4)
+    yield "mlpblk_fp4_dequantize", (at(mb.make_fp4_desc(40, 300, 2)),), size(40, 300, 2) + [2 * 2 * 40 * 300], (2,)
+    yield "mlpblk_fp4_matmul", (at(mb.make_fp4_matmul_desc(40, 50, 300, "f32")),), size(40, 300) + size(50, 300) + [4 * 40 * 50], (4,)
+    yield ("mlpblk_fp4_matmul_grouped", (at(mb.make_fp4_matmul_desc(256, 50, 300, experts=E, pad=128)),),
+           size(256, 300) + size(50, 300, E) + [c, g, 2 * 256 * 50], (6,))
+    yield ("mlpblk_fp4_wgrad_grouped", (at(mb.make_fp4_matmul_desc(40, 50, 512, "f32", experts=E, pad=256)),),
+           size(40, 512) + size(50, 512) + [g, 4 * E * 40 * 50], (5,))
+
+
+def test_outputs_that_share_bytes_are_refused(mb):
+    """Each output laid over the end and over the beginning of every other argument, and
+    inside it.  (No call here would be accepted: the addresses are never used.)"""
+    for name, desc, sizes, outs in _spans(mb):
+        f = getattr(mb.lib, name)
+        buffers = [i for i, n in enumerate(sizes) if n is not None and not (name == "mlpblk_fp4_quantize" and i == 2)]
+        base = [None if n is None else (n if i not in buffers else 0x10000000 * (i + 1)) for i, n in enumerate(sizes)]
+        if name == "mlpblk_fp4_quantize" and sizes[2] is None:
+            base[2] = 0
+        for o in outs:
+            for i in buffers:
+                if i == o:
+                    continue
+                inside = (sizes[i] - 1) // 16 * 16
+                for at in (base[i], base[i] + inside, base[i] - (sizes[o] - 1) // 16 * 16, base[i] + inside // 32 * 16):
+                    if name == "mlpblk_moe_unpermute" and i == 3 and at == base[i]:
+                        continue                           # y may be residual itself
+                    q = list(base)
+                    q[o] = at
+                    assert f(*desc, *q, None) == mb.MLPBLK_EINVAL, (name, "argument", o, "over", i, hex(at))
+
+
 @pytest.mark.parametrize("shape", [(10, 4, 2, 128), (5, 200, 3, 1), (0, 4, 2, 16)])
 def test_a_plan_not_made_yet_selects_nothing(mb, shape):
     """The plan's buffers of a new MoeSort, in memory that held something else before."""
