@@ -20,6 +20,8 @@
 // f4_pair: two CTAs on two SMs compute a 256 x 256 tile (cta_group::2), A's rows on the
 //   lanes; each CTA stages 128 rows of A and of B, and the scales of its A rows and
 //   of all 256 columns.
+#include <limits.h>
+
 #include <type_traits>
 
 #include "fp4_layout.h"
@@ -179,7 +181,8 @@ struct F4Tile {
 template <int TM>
 __device__ __forceinline__ int f4_groups(const F4Args &a, F4Groups *g) {
     const int e = static_cast<int>(threadIdx.x), lane = e & 31, warp = e >> 5;
-    const int limit = static_cast<int>(a.mode == kFp4GroupRows ? a.m : static_cast<int64_t>(a.kblocks) * kF4KB);
+    // (whole stages of the largest K end at 2^31, behind what a segment can name)
+    const int limit = static_cast<int>(a.mode == kFp4GroupRows ? a.m : min(static_cast<int64_t>(a.kblocks) * kF4KB, static_cast<int64_t>(INT_MAX)));
     int tiles = 0;
     if (e < a.experts) {
         const int s0 = min(max(a.seg[e], 0), limit), s1 = min(max(a.seg[e + 1], 0), limit);

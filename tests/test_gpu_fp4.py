@@ -722,3 +722,22 @@ def test_buffers_that_only_touch(mb):
         _check(to_np(c)[r], fp4.rounded(src)[r], wv[e], "f32", d)
         r = slice(sn[e], sn[e + 1])
         _check(to_np(g)[e], srcT[:, r], srcT[:, r], "f32", sn[e + 1] - sn[e])
+
+
+def test_wgrad_of_the_longest_k(mb):
+    """K = 2^31 - 1, the largest that the descriptor takes: segments at its beginning and
+    at its far end (2^31 is no int)."""
+    import torch
+    k = (1 << 31) - 1
+    d = mb.make_fp4_desc(1, k)
+    codes = torch.zeros(mb.mlpblk_fp4_codes_size(d), dtype=torch.uint8, device="cuda")
+    scales = torch.full((mb.mlpblk_fp4_scales_size(d),), 127, dtype=torch.uint8, device="cuda")
+    end = (1 << 31) - 256
+    codes[:128] = 0x22                                      # ones: 256 at the beginning, 64 at the end
+    codes[end // 2 - 32:end // 2] = 0x22
+    seg = torch.tensor([0, 512, 512, end], dtype=torch.int32, device="cuda")
+    c = torch.full((3, 1, 1), 7.0, device="cuda")
+    mb.mlpblk_fp4_wgrad_grouped(mb.make_fp4_matmul_desc(1, 1, k, "f32", experts=3, pad=256), codes, scales, codes, scales, seg, c)
+    assert c.flatten().tolist() == [256.0, 0.0, 64.0]
+    mb.mlpblk_fp4_wgrad_grouped(mb.make_fp4_matmul_desc(1, 1, k, "f32", True, 3, 256), codes, scales, codes, scales, seg, c)
+    assert c.flatten().tolist() == [512.0, 0.0, 128.0]
