@@ -587,6 +587,18 @@ int mlpblk_fp4_wgrad_grouped(const mlpblk_fp4_matmul_desc *desc, const void *a_c
                              void *stream);
 
 /*
+ * Test hook: the kernel that the product `desc` takes on a device of `sms` SMs (form 0:
+ * mlpblk_fp4_matmul, 1: mlpblk_fp4_matmul_grouped, 2: mlpblk_fp4_wgrad_grouped), so that
+ * tests can say which kernel they reach.  One of MLPBLK_FP4_KERNEL_PAIR_TMA and
+ * MLPBLK_FP4_KERNEL_PAIR (CTA pairs; C stored by TMA, or by threads), or the number of CTAs
+ * that share a tile's K (1, 2, 4, 8) in the kernel of single CTAs; -1 for a descriptor that
+ * is invalid or launches nothing.  Host only.
+ */
+#define MLPBLK_FP4_KERNEL_PAIR_TMA  256
+#define MLPBLK_FP4_KERNEL_PAIR      257
+int mlpblk_fp4_product_kernel(const mlpblk_fp4_matmul_desc *desc, int form, int sms);
+
+/*
  * zero_grads() of the accumulation loop ("grow_a_language_model_backprop" --
  * accumulation across microbatches): dgamma[d], dw1[F,d], dw2[d,F] = 0 (float32).
  * desc->tokens is ignored.  Returns an MLPBLK_* code.

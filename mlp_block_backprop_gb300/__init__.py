@@ -46,7 +46,10 @@ EXPORTED = ("mlpblk_workspace_size", "mlpblk_forward", "mlpblk_backward", "mlpbl
             "mlpblk_moe_sort_rows", "mlpblk_moe_sort", "mlpblk_moe_permute", "mlpblk_moe_permute_backward",
             "mlpblk_moe_unpermute", "mlpblk_moe_unpermute_backward",
             "mlpblk_fp4_codes_size", "mlpblk_fp4_scales_size", "mlpblk_fp4_quantize", "mlpblk_fp4_dequantize",
-            "mlpblk_fp4_matmul", "mlpblk_fp4_matmul_grouped", "mlpblk_fp4_wgrad_grouped")
+            "mlpblk_fp4_matmul", "mlpblk_fp4_matmul_grouped", "mlpblk_fp4_wgrad_grouped",
+            "mlpblk_fp4_product_kernel")
+MLPBLK_FP4_KERNEL_PAIR_TMA = 256
+MLPBLK_FP4_KERNEL_PAIR = 257
 MLPBLK_FP4_ACT_NONE = 0
 MLPBLK_FP4_ACT_RELU2 = 1
 MLPBLK_RMSNORM_STATS_PASS = 0
@@ -203,6 +206,8 @@ def _load():
     lib.mlpblk_fp4_matmul_grouped.restype = i32
     lib.mlpblk_fp4_wgrad_grouped.argtypes = [pp] + [vp] * 7
     lib.mlpblk_fp4_wgrad_grouped.restype = i32
+    lib.mlpblk_fp4_product_kernel.argtypes = [pp, i32, i32]
+    lib.mlpblk_fp4_product_kernel.restype = i32
     lib.mlpblk_zero_grads.argtypes = [pd, vp, vp, vp, vp]
     lib.mlpblk_zero_grads.restype = i32
     lib.mlpblk_scale_grads.argtypes = [pd, vp, vp, vp, f32, vp]
@@ -851,6 +856,10 @@ def mlpblk_fp4_wgrad_grouped(desc, a_codes, a_scales, b_codes, b_scales, seg, c,
         ctypes.byref(desc), *ops, _operand(seg, where, "seg", i32, desc.experts + 1, dev),
         _operand(c, where, "c", t.row.get(desc.out_dtype), desc.experts * desc.m * desc.n, dev), _stream(stream))
     _check(rc, where)
+
+
+def mlpblk_fp4_product_kernel(desc, form: int, sms: int) -> int:
+    return int(lib.mlpblk_fp4_product_kernel(ctypes.byref(desc), int(form), int(sms)))
 
 
 class Fp4Matrix(_Kept):

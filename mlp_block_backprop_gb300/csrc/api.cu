@@ -1359,6 +1359,20 @@ int check_fp4_matmul(const mlpblk_fp4_matmul_desc *d, int mode) {
     return tiles < kFp4Lim / 2 ? MLPBLK_OK : MLPBLK_EINVAL;
 }
 
+// A product's sizes and types; its buffers are the caller's to fill in.
+Fp4Product fp4_product_of(const mlpblk_fp4_matmul_desc *desc, int mode) {
+    Fp4Product p = {};
+    p.mode = mode;
+    p.m = desc->m;
+    p.n = desc->n;
+    p.k = desc->k;
+    p.experts = desc->experts;
+    p.max_rows = desc->max_rows;
+    p.out_dtype = desc->out_dtype;
+    p.accumulate = desc->accumulate;
+    return p;
+}
+
 int fp4_product(const mlpblk_fp4_matmul_desc *desc, int mode, const void *a_codes, const void *a_scales,
                 const void *b_codes, const void *b_scales, const int32_t *count, const int32_t *seg, void *c,
                 void *stream) {
@@ -1382,13 +1396,7 @@ int fp4_product(const mlpblk_fp4_matmul_desc *desc, int mode, const void *a_code
     int sms = 0;
     MLPBLK_TRY(device_sms(&sms));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    Fp4Product p = {};
-    p.mode = mode;
-    p.m = desc->m;
-    p.n = desc->n;
-    p.k = desc->k;
-    p.experts = desc->experts;
-    p.max_rows = desc->max_rows;
+    Fp4Product p = fp4_product_of(desc, mode);
     p.a = static_cast<const uint8_t *>(a_codes);
     p.sa = static_cast<const uint8_t *>(a_scales);
     p.b = static_cast<const uint8_t *>(b_codes);
@@ -1396,8 +1404,6 @@ int fp4_product(const mlpblk_fp4_matmul_desc *desc, int mode, const void *a_code
     p.count = count;
     p.seg = seg;
     p.c = c;
-    p.out_dtype = desc->out_dtype;
-    p.accumulate = desc->accumulate;
     MLPBLK_LAUNCH(MLPBLK_KERNEL_FP4_GEMM, s, launch_fp4_matmul(p, sms, s));
     return MLPBLK_OK;
 }
@@ -1560,6 +1566,13 @@ int mlpblk_fp4_wgrad_grouped(const mlpblk_fp4_matmul_desc *desc, const void *a_c
                              const void *b_codes, const void *b_scales, const int32_t *seg, void *c,
                              void *stream) {
     return fp4_product(desc, kFp4GroupK, a_codes, a_scales, b_codes, b_scales, nullptr, seg, c, stream);
+}
+
+int mlpblk_fp4_product_kernel(const mlpblk_fp4_matmul_desc *desc, int form, int sms) {
+    if (form < kFp4Dense || form > kFp4GroupK || sms < 1 || check_fp4_matmul(desc, form) != MLPBLK_OK) return -1;
+    if (desc->m == 0 || desc->k == 0) return -1;
+    const Fp4Choice c = choose_fp4_matmul(fp4_product_of(desc, form), sms);
+    return c.pair ? (c.tma ? MLPBLK_FP4_KERNEL_PAIR_TMA : MLPBLK_FP4_KERNEL_PAIR) : c.split;
 }
 
 }  // extern "C"

@@ -41,6 +41,15 @@ struct Fp4Product {
     int out_dtype, accumulate;
 };
 
+// The kernel that a product takes (a rule on sizes and types alone).
+struct Fp4Choice {
+    bool pair;     // f4_pair, else f4_small
+    bool tma;      // rows of C are whole 16-byte pieces: f4_pair stores them by TMA
+    int split;     // f4_small: CTAs that share a tile's K
+    int workers;   // CTAs, CTA pairs or clusters that walk the tiles
+};
+Fp4Choice choose_fp4_matmul(const Fp4Product &p, int num_sms);
+
 int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s);
 int take_device_error_gemm_f4();
 

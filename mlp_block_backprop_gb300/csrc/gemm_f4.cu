@@ -1140,6 +1140,54 @@ int run_pair(F4Args a, const Fp4Product &p, int workers, cudaStream_t s) {
 
 }  // namespace
 
+Fp4Choice choose_fp4_matmul(const Fp4Product &p, int num_sms) {
+    const bool f32 = p.out_dtype == MLPBLK_FP32;
+    const int kblocks = static_cast<int>((p.k + kF4KB - 1) / kF4KB);
+    int64_t rows = p.m;  // rows of one product, at most
+    int64_t groups = 1;
+    if (p.mode == kFp4GroupRows) {
+        if (p.max_rows > 0 && p.max_rows < rows) rows = p.max_rows;
+        groups = p.experts;
+    } else if (p.mode == kFp4GroupK) {
+        groups = p.experts;
+    }
+    Fp4Choice c = {};
+    // 256 x 256 pair tiles where they occupy half of the SM pairs and, grouped by rows, an
+    // expert has more than one 128-row tile on average (1500 tokens, top-4 of 60 experts
+    // of 776 x 1000: 13.8 us in pair tiles, 8.4 in small ones).  A single round of them
+    // needs 16 stages to make up for its longer start and end (2048 x 2048 x 1024 4.8 us
+    // in small tiles, 5.8 in pair tiles; x 4096 9.3 and 9.3; x 8192 15.1 and 13.8), and
+    // float32 rows that are not whole 16-byte pieces 6 (8192 x 4095 x 1024 33 and 41 us,
+    // x 4096 63 and 55).
+    const int pairs = num_sms / 2;
+    const int64_t mean_rows = p.mode == kFp4GroupRows ? rows / p.experts : rows;
+    const int64_t pair_tiles = p.mode == kFp4GroupRows ? ((mean_rows + 255) / 256) * p.experts * ((p.n + 255) / 256)
+                                                       : (rows + 255) / 256 * groups * ((p.n + 255) / 256);
+    c.tma = p.n * (f32 ? 4 : 2) % 16 == 0;
+    const int stages_of_tile = p.mode == kFp4GroupK ? kblocks / p.experts : kblocks;
+    const int least = pair_tiles <= pairs ? 16 : (f32 && !c.tma ? 6 : 0);
+    if (pairs >= 1 && mean_rows > 128 && 2 * pair_tiles >= pairs && stages_of_tile >= least) {
+        c.pair = true;
+        c.workers = static_cast<int>(p.mode != kFp4GroupRows && pair_tiles < pairs ? pair_tiles : pairs);
+        return c;
+    }
+    // K is split where that saves more of its stages than the cluster's sum costs: 4 us for
+    // 128 columns, 1.5 for up to 32.  A stage takes 0.15 us, twice that where rows of codes
+    // begin at no 128-byte line (each of its 256 rows is then two requests of the copies):
+    // 128 x 128 x 8192 7.3 us whole and 7.8 split, x 16384 12.3 and 8.4; 118 x 192 x 6624
+    // 11.3 and 8.9; one token x 1024 x 4096 4.3 and 4.7, x 8192 6.6 and 5.2.
+    const int64_t tiles = (rows + 127) / 128 * ((p.n + 127) / 128) * groups;
+    const int64_t stages = static_cast<int64_t>(kblocks) * (fp4_row_bytes(p.k) % 128 != 0 ? 2 : 1);
+    c.split = 1;
+    if (stages >= (rows <= 32 ? 32 : 40))
+        while (c.split < 8 && tiles * c.split * 2 <= num_sms && stages >= 8 * c.split) c.split *= 2;
+    int64_t workers = num_sms / c.split;
+    if (workers < 1) workers = 1;
+    if (p.mode != kFp4GroupRows && tiles < workers) workers = tiles;
+    c.workers = static_cast<int>(workers);
+    return c;
+}
+
 int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s) {
     F4Args a = {};
     a.mode = p.mode;
@@ -1155,55 +1203,20 @@ int launch_fp4_matmul(const Fp4Product &p, int num_sms, cudaStream_t s) {
     a.seg = p.seg;
     a.c = p.c;
     const bool f32 = p.out_dtype == MLPBLK_FP32;
-    int64_t rows = p.m;  // rows of one product, at most
-    int64_t groups = 1;
-    if (p.mode == kFp4GroupRows) {
-        if (p.max_rows > 0 && p.max_rows < rows) rows = p.max_rows;
-        groups = p.experts;
-    } else if (p.mode == kFp4GroupK) {
-        groups = p.experts;
+    const Fp4Choice ch = choose_fp4_matmul(p, num_sms);
+    const int w = ch.workers;
+    if (ch.pair) {
+        if (!f32) return ch.tma ? run_pair<0, true>(a, p, w, s) : run_pair<0, false>(a, p, w, s);
+        if (!p.accumulate) return ch.tma ? run_pair<1, true>(a, p, w, s) : run_pair<1, false>(a, p, w, s);
+        return ch.tma ? run_pair<2, true>(a, p, w, s) : run_pair<2, false>(a, p, w, s);
     }
-    // 256 x 256 pair tiles where they occupy half of the SM pairs and, grouped by rows, an
-    // expert has more than one 128-row tile on average (1500 tokens, top-4 of 60 experts
-    // of 776 x 1000: 13.8 us in pair tiles, 8.4 in small ones).  A single round of them
-    // needs 16 stages to make up for its longer start and end (2048 x 2048 x 1024 4.8 us
-    // in small tiles, 5.8 in pair tiles; x 4096 9.3 and 9.3; x 8192 15.1 and 13.8), and
-    // float32 rows that are not whole 16-byte pieces 6 (8192 x 4095 x 1024 33 and 41 us,
-    // x 4096 63 and 55).
-    const int pairs = num_sms / 2;
-    const int64_t mean_rows = p.mode == kFp4GroupRows ? rows / p.experts : rows;
-    const int64_t pair_tiles = p.mode == kFp4GroupRows ? ((mean_rows + 255) / 256) * p.experts * ((p.n + 255) / 256)
-                                                       : (rows + 255) / 256 * groups * ((p.n + 255) / 256);
-    const bool tma = p.n * (f32 ? 4 : 2) % 16 == 0;
-    const int stages_of_tile = p.mode == kFp4GroupK ? a.kblocks / p.experts : a.kblocks;
-    const int least = pair_tiles <= pairs ? 16 : (f32 && !tma ? 6 : 0);
-    if (pairs >= 1 && mean_rows > 128 && 2 * pair_tiles >= pairs && stages_of_tile >= least) {
-        const int w = static_cast<int>(p.mode != kFp4GroupRows && pair_tiles < pairs ? pair_tiles : pairs);
-        if (!f32) return tma ? run_pair<0, true>(a, p, w, s) : run_pair<0, false>(a, p, w, s);
-        if (!p.accumulate) return tma ? run_pair<1, true>(a, p, w, s) : run_pair<1, false>(a, p, w, s);
-        return tma ? run_pair<2, true>(a, p, w, s) : run_pair<2, false>(a, p, w, s);
+#define MLPBLK_SMALL(SPLIT)                                                           \
+    {                                                                                 \
+        if (!f32) return run_small<F4Small<SPLIT>, 0>(a, p, ch.split, w, s);          \
+        if (!p.accumulate) return run_small<F4Small<SPLIT>, 1>(a, p, ch.split, w, s); \
+        return run_small<F4Small<SPLIT>, 2>(a, p, ch.split, w, s);                    \
     }
-    // K is split where that saves more of its stages than the cluster's sum costs: 4 us for
-    // 128 columns, 1.5 for up to 32.  A stage takes 0.15 us, twice that where rows of codes
-    // begin at no 128-byte line (each of its 256 rows is then two requests of the copies):
-    // 128 x 128 x 8192 7.3 us whole and 7.8 split, x 16384 12.3 and 8.4; 118 x 192 x 6624
-    // 11.3 and 8.9; one token x 1024 x 4096 4.3 and 4.7, x 8192 6.6 and 5.2.
-    const int64_t tiles = (rows + 127) / 128 * ((p.n + 127) / 128) * groups;
-    const int64_t stages = a.kblocks * (fp4_row_bytes(p.k) % 128 != 0 ? 2 : 1);
-    int cs = 1;
-    if (stages >= (rows <= 32 ? 32 : 40))
-        while (cs < 8 && tiles * cs * 2 <= num_sms && stages >= 8 * cs) cs *= 2;
-    int64_t workers = num_sms / cs;
-    if (workers < 1) workers = 1;
-    if (p.mode != kFp4GroupRows && tiles < workers) workers = tiles;
-    const int w = static_cast<int>(workers);
-#define MLPBLK_SMALL(SPLIT)                                                     \
-    {                                                                           \
-        if (!f32) return run_small<F4Small<SPLIT>, 0>(a, p, cs, w, s);          \
-        if (!p.accumulate) return run_small<F4Small<SPLIT>, 1>(a, p, cs, w, s); \
-        return run_small<F4Small<SPLIT>, 2>(a, p, cs, w, s);                    \
-    }
-    if (cs > 1) MLPBLK_SMALL(true)
+    if (ch.split > 1) MLPBLK_SMALL(true)
     MLPBLK_SMALL(false)
 #undef MLPBLK_SMALL
 }

@@ -15,6 +15,7 @@ every partial sum is a multiple of 1/4 below 2^22, so those products are exact.
 import numpy as np
 import pytest
 
+import fp4_shapes
 from oracle import fp4, sort
 from helpers import to_np
 
@@ -741,3 +742,115 @@ def test_wgrad_of_the_longest_k(mb):
     assert c.flatten().tolist() == [256.0, 0.0, 64.0]
     mb.mlpblk_fp4_wgrad_grouped(mb.make_fp4_matmul_desc(1, 1, k, "f32", True, 3, 256), codes, scales, codes, scales, seg, c)
     assert c.flatten().tolist() == [512.0, 0.0, 128.0]
+
+
+# ------------------------------------- every kernel of the products, neighbours looked at
+
+def _reaches(mb, desc, form, kernel):
+    import torch
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert fp4_shapes.kernel(mb, desc, form, sms) == kernel
+
+
+def _guarded(shape, dtype, fill):
+    """A C of its own values (or NaN) in the middle of a larger buffer of sevens."""
+    import torch
+    n = int(np.prod(shape))
+    whole = torch.full((n + 4096,), 7.0, dtype=_dt(dtype), device="cuda")
+    c = whole[2048:2048 + n].view(shape)
+    if fill is None:
+        c.fill_(float("nan"))
+    else:
+        c.copy_(fill)
+    return whole, c
+
+
+def _untouched(whole):
+    assert bool((whole[:2048] == 7.0).all()) and bool((whole[-2048:] == 7.0).all())
+
+
+# A sum over a cluster adds up to eight parts, half a step each: four steps more, those of
+# 128 more columns in _check's bound.
+def _columns(k, kernel):
+    return k + (128 if kernel in (2, 4, 8) else 0)
+
+
+@pytest.mark.parametrize("shape,out,accumulate,kernel", fp4_shapes.DENSE)
+def test_product_on_each_kernel(mb, shape, out, accumulate, kernel):
+    import torch
+    m, n, k = shape
+    desc = fp4_shapes.dense_desc(mb, shape, out, accumulate)
+    _reaches(mb, desc, 0, kernel)
+    rng = np.random.default_rng(m + n + k + accumulate)
+    qa, a = _quantized(mb, rng, m, k)
+    qb, b = _quantized(mb, rng, n, k)
+    base = torch.from_numpy(rng.standard_normal((m, n)).astype(np.float32)).cuda() if accumulate else None
+    whole, c = _guarded((m, n), out, base)
+    mb.mlpblk_fp4_matmul(desc, qa.codes, qa.scales, qb.codes, qb.scales, c)
+    _check(to_np(c), a, b, out, _columns(k, kernel), to_np(base) if accumulate else None)
+    _untouched(whole)
+
+
+@pytest.mark.parametrize("case,out,accumulate,kernel", fp4_shapes.GROUPED)
+def test_grouped_product_on_each_kernel(mb, case, out, accumulate, kernel):
+    import torch
+    T, d, n, E, k, pad = case
+    desc = fp4_shapes.grouped_desc(mb, case, out, accumulate)
+    _reaches(mb, desc, 1, kernel)
+    rng = np.random.default_rng(T + d + n)
+    s, (count, seg, pos, row_map) = _routed(mb, T, d, E, k, pad, T, dead=(1,))
+    assert s.rows == desc.m and count[1] == 0
+    x, v = _draw(rng, (T, d), "bf16")
+    qx = mb.Fp4Matrix(s.rows, d)
+    qx.quantize(x, sort=s, gather=True)
+    qw, w = _quantized(mb, rng, n, d, batch=E)
+    base = torch.from_numpy(rng.standard_normal((s.rows, n)).astype(np.float32)).cuda()
+    whole, c = _guarded((s.rows, n), out, base)
+    before = to_np(c)
+    mb.mlpblk_fp4_matmul_grouped(desc, qx.codes, qx.scales, qw.codes, qw.scales, s.count, s.seg, c)
+    got = to_np(c)
+    a = fp4.rounded(np.where((row_map >= 0)[:, None], v[np.maximum(row_map, 0) // k], 0.0))
+    for e in range(E):
+        r = slice(seg[e], seg[e] + count[e])
+        if count[e]:
+            _check(got[r], a[r], w[e], out, _columns(d, kernel), before[r] if accumulate else None)
+        # padding rows: as they were, or zeros (times the weights, or added)
+        p = slice(seg[e] + count[e], seg[e + 1])
+        assert np.all((got[p] == before[p]) | (got[p] == 0.0))
+    assert np.array_equal(got[seg[E]:], before[seg[E]:])
+    _untouched(whole)
+
+
+@pytest.mark.parametrize("case,accumulate,kernel", fp4_shapes.WGRAD)
+def test_grouped_wgrad_on_each_kernel(mb, case, accumulate, kernel):
+    """Expert 0 has no rows, expert 1 one block of 256, expert 2 two; the rest have the
+    other tokens' rows."""
+    import torch
+    T, d, n, E, k = case
+    desc = fp4_shapes.wgrad_desc(mb, case, accumulate)
+    _reaches(mb, desc, 2, kernel)
+    rng = np.random.default_rng(T + d + n)
+    idx = rng.integers(3, E, (T, k)).astype(np.int32)
+    idx[:200, 0], idx[200:500, 0] = 1, 2
+    idx[rng.random((T, k)) < 0.01] = -1
+    s = mb.MoeSort(T, d, E, k, 256)
+    s.sort(torch.from_numpy(idx).cuda())
+    count, seg, pos, row_map = sort.plan(idx, E, 256)
+    assert count[0] == 0 and seg[2] - seg[1] == 256 and seg[3] - seg[2] == 512
+    live = (row_map >= 0)[:, None]
+    x, v = _draw(rng, (T, d), "bf16")
+    dy, g = _draw(rng, (s.rows, n), "bf16")
+    qx, qg = mb.Fp4Matrix(d, s.rows), mb.Fp4Matrix(n, s.rows)
+    qx.quantize(x, sort=s, gather=True, transposed=True)
+    qg.quantize(dy, sort=s, transposed=True)
+    a = fp4.rounded(np.where(live, g, 0.0).T)
+    b = fp4.rounded(np.where(live, v[np.maximum(row_map, 0) // k], 0.0).T)
+    base = torch.from_numpy(rng.standard_normal((E, n, d)).astype(np.float32)).cuda() if accumulate else None
+    whole, c = _guarded((E, n, d), "f32", base)
+    mb.mlpblk_fp4_wgrad_grouped(desc, qg.codes, qg.scales, qx.codes, qx.scales, s.seg, c)
+    got = to_np(c)
+    for e in range(E):
+        r = slice(seg[e], seg[e + 1])
+        _check(got[e], a[:, r], b[:, r], "f32", _columns(int(seg[e + 1] - seg[e]), kernel), to_np(base)[e] if accumulate else None)
+    assert np.array_equal(got[0], to_np(base)[0] if accumulate else np.zeros((n, d)))
+    _untouched(whole)

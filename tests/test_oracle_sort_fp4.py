@@ -447,3 +447,24 @@ def test_a_new_library_leaves_no_other_interpreters_module(tmp_path, monkeypatch
         (tmp_path / name).write_bytes(b"")
     build._remove_calls()
     assert sorted(f.name for f in tmp_path.iterdir()) == ["libmlpblk.so", "other.so"]
+
+
+@pytest.mark.parametrize("sms", [148, 152])
+def test_product_shapes_reach_the_kernels_they_are_for(mb, sms):
+    import fp4_shapes as f
+    got = [(c, f.kernel(mb, f.dense_desc(mb, *c[:3]), 0, sms)) for c in f.DENSE]
+    got += [(c, f.kernel(mb, f.grouped_desc(mb, *c[:3]), 1, sms)) for c in f.GROUPED]
+    got += [(c, f.kernel(mb, f.wgrad_desc(mb, *c[:2]), 2, sms)) for c in f.WGRAD]
+    assert not [(c, k) for c, k in got if k != c[-1]]
+    # every instantiation of the two kernels (output type, += and the store of C) is among them
+    kinds = {(c[1], c[2], "split" if k in (2, 4, 8) else k) for c, k in got[:len(f.DENSE)]}
+    assert {(o, a, k) for o, a in (("bf16", False), ("f32", False), ("f32", True)) for k in ("tma", "pair", "split")} <= kinds
+
+
+def test_product_kernel_refusals(mb):
+    D = mb.make_fp4_matmul_desc
+    f = mb.mlpblk_fp4_product_kernel
+    assert f(D(8, 8, 8), 0, 152) == 1
+    assert f(D(8, 8, 8), 3, 152) == f(D(8, 8, 8), -1, 152) == f(D(8, 8, 8), 0, 0) == f(D(0, 8, 8), 0, 152) == -1
+    assert f(D(8, 8, 8), 1, 152) == f(D(8, 0, 8), 0, 152) == f(D(8, 8, 0, experts=2, pad=256), 2, 152) == -1
+    assert mb.lib.mlpblk_fp4_product_kernel(None, 0, 152) == -1
