@@ -854,3 +854,146 @@ def test_grouped_wgrad_on_each_kernel(mb, case, accumulate, kernel):
         _check(got[e], a[:, r], b[:, r], "f32", _columns(int(seg[e + 1] - seg[e]), kernel), to_np(base)[e] if accumulate else None)
     assert np.array_equal(got[0], to_np(base)[0] if accumulate else np.zeros((n, d)))
     _untouched(whole)
+
+
+# ------------------------------------------------------- through a sort, and captured
+
+@pytest.mark.parametrize("act", ["none", "relu2"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("shape", [(45, 90, 5, 2, 128), (6, 301, 40, 2, 256), (37, 1032, 9, 3, 128), (70, 513, 4, 2, 1),
+                                   (300, 40, 3, 1, 7)])
+def test_quantize_through_a_sort_from_each_source(mb, shape, gather, dtype, act):
+    """Both types, along rows and columns, buffers full of other bytes before: every byte
+    of codes and scales is written, padding and unowned rows are zeros."""
+    import torch
+    T, d, E, k, pad = shape
+    s, (count, seg, pos, row_map) = _routed(mb, T, d, E, k, pad, 7, dead=(2,))
+    R = s.rows
+    live = row_map >= 0
+    x, v = _draw(np.random.default_rng(T + d), (T if gather else R, d), dtype)
+    src = np.where(live[:, None], v[np.maximum(row_map, 0) // k] if gather else v, 0.0)
+    if act == "relu2":                                      # squares in float32, as the operator says
+        src = (np.maximum(src, 0.0).astype(np.float32) ** 2).astype(np.float64)
+    if not gather:                                          # what no entry owns is not read
+        x[torch.from_numpy(~live).cuda()] = float("nan")
+    mask = 0xFF if act == "none" else 0x77                  # a square's zero has either sign
+    for transposed in (False, True):
+        q = mb.Fp4Matrix(*((d, R) if transposed else (R, d)))
+        q.codes.fill_(0xAA)
+        q.scales.fill_(0xAA)
+        q.quantize(x, sort=s, gather=gather, transposed=transposed, act=act)
+        packed, tiled = fp4.pack(*fp4.quantize(src.T if transposed else src))
+        np.testing.assert_array_equal(_bytes(q.scales), tiled)
+        np.testing.assert_array_equal(_bytes(q.codes) & mask, packed & mask)
+
+
+def test_a_plan_not_made_yet(mb):
+    """A MoeSort before its first sort: nothing is moved, gathered or multiplied."""
+    import torch
+    T, d, E, k = 33, 64, 3, 2
+    for _ in range(2):
+        junk = torch.full((1 << 20,), 5, dtype=torch.int32, device="cuda")
+        del junk
+        s = mb.MoeSort(T, d, E, k, 256)
+        x = torch.randn(T, d, device="cuda").bfloat16()
+        rows = torch.full((s.rows, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        s.permute(x, rows)
+        assert bool((rows == 7.0).all())
+        y = torch.empty_like(x)
+        s.unpermute(rows, y, residual=x)
+        assert torch.equal(y, x)
+        q, w = mb.Fp4Matrix(s.rows, d), mb.Fp4Matrix(48, d, batch=E)
+        q.codes.fill_(0xAA)
+        q.scales.fill_(0xAA)
+        q.quantize(x, sort=s, gather=True)
+        assert not q.codes.any() and not q.scales.any()
+        w.quantize(torch.randn(E * 48, d, device="cuda"))
+        c = torch.full((s.rows, 48), 7.0, device="cuda")
+        q.matmul_grouped(w, s, c)
+        assert bool((c == 7.0).all())
+
+
+def test_experts_captured_and_replayed_on_new_ids(mb):
+    """The routed experts at 4 bits with the second layer's gradients, captured once and
+    replayed on other tokens and ids: an expert loses all its rows and gains them again;
+    each stage against the oracle on the stage's own input."""
+    import torch
+    T, d, F, E, k, pad = 200, 96, 288, 4, 2, 256
+    rng = np.random.default_rng(22)
+    bf = torch.bfloat16
+    s = mb.MoeSort(T, d, E, k, pad)
+    R = s.rows
+    idx = torch.zeros(T, k, dtype=torch.int32, device="cuda")
+    x, dy = torch.zeros(T, d, dtype=bf, device="cuda"), torch.zeros(T, d, dtype=bf, device="cuda")
+    p = torch.zeros(T, k, device="cuda")
+    w1, b1 = _quantized(mb, rng, F, d, batch=E, wide=False)
+    v2 = rng.standard_normal((E, d, F))
+    pack = lambda v: _pack_batch(mb, v)
+    (w2, b2), (w2t, b2t) = pack(v2), pack(v2.transpose(0, 2, 1))
+    qx, qh, qo = mb.Fp4Matrix(R, d), mb.Fp4Matrix(R, F), mb.Fp4Matrix(R, d)
+    qot, qht = mb.Fp4Matrix(d, R), mb.Fp4Matrix(F, R)
+    h, o, do, dg = (torch.zeros(R, n, dtype=bf, device="cuda") for n in (F, d, d, F))
+    y, dp, dw = torch.empty(T, d, dtype=bf, device="cuda"), torch.empty(T, k, device="cuda"), torch.empty(E, d, F, device="cuda")
+
+    def step():
+        s.sort(idx)
+        qx.quantize(x, sort=s, gather=True)
+        qx.matmul_grouped(w1, s, h)
+        qh.quantize(h, sort=s, act="relu2")
+        qh.matmul_grouped(w2, s, o)
+        s.unpermute(o, y, weights=p, residual=x)
+        s.unpermute_backward(dy, o, p, do, dp)
+        qo.quantize(do, sort=s)
+        qo.matmul_grouped(w2t, s, dg)
+        qot.quantize(do, sort=s, transposed=True)
+        qht.quantize(h, sort=s, act="relu2", transposed=True)
+        qot.wgrad_grouped(qht, s, dw)
+
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        step()
+    for dead, eager in ((None, False), (1, False), (None, False), (3, True), (0, False)):
+        ids = rng.integers(0, E, (T, k)).astype(np.int32)
+        if dead is not None:
+            ids[ids == dead] = -1
+        idx.copy_(torch.from_numpy(ids))
+        for t in (x, dy):
+            t.copy_(torch.from_numpy(rng.standard_normal((T, d)).astype(np.float32)))
+        p.copy_(torch.from_numpy(rng.uniform(0.1, 1, (T, k)).astype(np.float32)))
+        torch.cuda.synchronize()
+        step() if eager else g.replay()
+        torch.cuda.synchronize()
+        count, seg, pos, row_map = sort.plan(ids, E, pad)
+        for got, ref in zip((s.count, s.seg, s.pos, s.row_map), (count, seg, pos, row_map)):
+            np.testing.assert_array_equal(got.cpu().numpy(), ref)
+        live = (row_map >= 0)[:, None]
+        own = lambda t: np.where(live, to_np(t), 0.0)
+        xv, dyv, pv, ov, dov = to_np(x), to_np(dy), to_np(p), own(o), own(do)
+        a = fp4.rounded(np.where(live, xv[np.maximum(row_map, 0) // k], 0.0))
+        hr = np.square(np.maximum(own(h), 0.0))
+        aq, dq = fp4.rounded(hr), fp4.rounded(dov)
+        dqt, hqt = fp4.rounded(dov.T), fp4.rounded(hr.T)
+        for e in range(E):
+            r, part = slice(seg[e], seg[e] + count[e]), slice(seg[e], seg[e + 1])
+            if count[e]:
+                _check(to_np(h)[r], a[r], b1[e], "bf16", d)
+                _check(to_np(o)[r], aq[r], b2[e], "bf16", F)
+                _check(to_np(dg)[r], dq[r], b2t[e], "bf16", d)
+            _check(to_np(dw)[e], dqt[:, part], hqt[:, part], "f32", int(seg[e + 1] - seg[e]))
+        ref, mag = sort.unpermute(ov, pos, pv, xv)
+        assert np.all(np.abs(to_np(y) - ref) <= 2.0 ** -8 * np.abs(ref) + (k + 2) * 2.0 ** -24 * mag)
+        r_do, r_dp, mag = sort.unpermute_backward(dyv, ov, pos, row_map, pv)
+        assert np.all(np.abs(dov - r_do) <= (2.0 ** -8 + 2.0 ** -24) * np.abs(r_do))
+        assert np.all(np.abs(to_np(dp) - r_dp) <= (d + 1) * 2.0 ** -24 * mag)
+
+
+def _pack_batch(mb, v):
+    """A batch of matrices quantised along their rows, and the values that they have."""
+    import torch
+    E, rows, cols = v.shape
+    x = torch.from_numpy(np.ascontiguousarray(v, dtype=np.float32)).cuda()
+    q = mb.Fp4Matrix(rows, cols, batch=E)
+    q.quantize(x)
+    return q, np.stack([fp4.rounded(to_np(x[e])) for e in range(E)])
