@@ -183,10 +183,11 @@ sort_kernel(const int *__restrict__ idx, int64_t n, int experts, int pad, int64_
     } else {
         for (int64_t i = w0 + lane; i < w1; i += 32) place(i, valid(idx[i]), pos[i]);
     }
-    // rows without an entry: the segments' padding and what lies behind them
+    // rows without an entry: the segments' padding and what lies behind them (64 bits: a
+    // lane's row may lie behind the last int)
     if (pad > 1)
         for (int e = c * kSortWarps + wid; e < experts; e += C * kSortWarps)
-            for (int r = segs[e] + live[e] + lane; r < segs[e + 1]; r += 32) row_map[r] = -1;
+            for (int64_t r = static_cast<int64_t>(segs[e]) + live[e] + lane; r < segs[e + 1]; r += 32) row_map[r] = -1;
     for (int64_t r = static_cast<int64_t>(segs[experts]) + c * kSortThreads + tid; r < R; r += C * kSortThreads)
         row_map[r] = -1;
     if (C > 1) cluster_wait();  // no CTA leaves while its counts are being read

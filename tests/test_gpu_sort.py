@@ -230,3 +230,36 @@ def test_rows_beyond_two_billion_elements(mb):
     s.unpermute_backward(x, rows, None, y.new_zeros(s.rows, d), dw)
     ref = x[:, 0].float() ** 2 * d
     assert bool(((dw - ref[:, None]).abs() <= 2.0 ** -20 * ref[:, None]).all())
+
+
+def test_plan_and_moves_of_two_billion_tokens(mb):
+    """The largest plan that the descriptor takes with padding: its rows end within a warp's
+    width of 2^31."""
+    import torch
+    T, pad = (1 << 31) - 5, 2
+    s = mb.make_sort_desc(T, 1, 1, 1, pad)
+    assert mb.mlpblk_moe_sort_rows(mb.make_sort_desc(T + 1, 1, 1, 1, pad)) == -1
+    R = mb.mlpblk_moe_sort_rows(s)
+    assert R == T + 1
+    i32 = dict(dtype=torch.int32, device="cuda")
+    idx = torch.zeros(T, **i32)
+    idx[[3, T - 2]] = 1                                     # two ids that select nothing
+    count, seg, pos, row_map = torch.zeros(1, **i32), torch.zeros(2, **i32), torch.zeros(T, **i32), torch.full((R + 64,), 7, **i32)
+    mb.mlpblk_moe_sort(s, idx, count, seg, pos, row_map)
+    assert count.item() == T - 2 and seg.tolist() == [0, T - 1]
+    live = torch.ones(T, dtype=torch.bool, device="cuda")
+    live[[3, T - 2]] = False
+    entries = torch.nonzero(live)[:, 0].int()
+    assert torch.equal(row_map[:T - 2], entries) and row_map[T - 2:R].tolist() == [-1] * 3 and bool((row_map[R:] == 7).all())
+    del entries
+    assert pos[3].item() == -1 and pos[T - 2].item() == -1
+    assert torch.equal(row_map[pos[live].long()], torch.nonzero(live)[:, 0].int())
+    del idx, row_map
+    x = torch.arange(T, **i32).remainder_(251).to(torch.bfloat16)[:, None]
+    rows = torch.full((R + 64, 1), 7.0, dtype=torch.bfloat16, device="cuda")
+    mb.mlpblk_moe_permute(s, x, pos, count, seg, rows)
+    assert torch.equal(rows[:T - 2], x[live]) and rows[T - 2:, 0].tolist() == [0.0] + [7.0] * (R + 64 - T + 1)
+    y = torch.full_like(x, 7.0)
+    mb.mlpblk_moe_unpermute(s, rows, pos, None, None, y)
+    x[~live] = 0.0
+    assert torch.equal(y, x)
