@@ -1312,7 +1312,7 @@ int check_sort_desc(const mlpblk_sort_desc *d) {
         d->pad < 1 || d->pad > 1024)
         return MLPBLK_EINVAL;
     const int64_t lim = static_cast<int64_t>(1) << 31;
-    if (d->width >= lim / 2 || d->tokens >= lim / d->top_k) return MLPBLK_EINVAL;
+    if (d->width >= lim / 2 || d->tokens >= lim) return MLPBLK_EINVAL;
     if (d->tokens * d->top_k + static_cast<int64_t>(d->experts + 1) * d->pad >= lim) return MLPBLK_EINVAL;
     return MLPBLK_OK;
 }
@@ -1332,7 +1332,7 @@ int check_fp4_desc(const mlpblk_fp4_desc *d) {
     if (d->act != MLPBLK_FP4_ACT_NONE && d->act != MLPBLK_FP4_ACT_RELU2) return MLPBLK_ENOTSUP;
     if (d->transposed != 0 && d->transposed != 1) return MLPBLK_EINVAL;
     if (d->rows < 0 || d->cols < 0 || d->batch < 1 || d->cols >= kFp4Lim) return MLPBLK_EINVAL;
-    if (d->rows > 0 && d->batch >= kFp4Lim / d->rows) return MLPBLK_EINVAL;
+    if (d->rows >= kFp4Lim || d->rows * d->batch >= kFp4Lim) return MLPBLK_EINVAL;
     if ((d->rows + 127) / 128 * d->batch >= kFp4Lim / 4) return MLPBLK_EINVAL;  // CTAs of a launch
     const int64_t pieces = (d->cols + 255) / 256;  // of a row: warps of a launch
     if ((d->rows + 127) / 128 * d->batch * pieces >= kFp4Lim / 8 || d->rows * d->batch * pieces >= kFp4Lim) return MLPBLK_EINVAL;
@@ -1353,7 +1353,7 @@ int check_fp4_matmul(const mlpblk_fp4_matmul_desc *d, int mode) {
     } else {
         if (d->experts < 1 || d->experts > 256 || d->pad < 1) return MLPBLK_EINVAL;
         if (d->pad % (mode == kFp4GroupRows ? 128 : 256) != 0) return MLPBLK_ENOTSUP;
-        if ((mode == kFp4GroupRows ? d->n : d->m) >= kFp4Lim / d->experts) return MLPBLK_EINVAL;
+        if ((mode == kFp4GroupRows ? d->n : d->m) * d->experts >= kFp4Lim) return MLPBLK_EINVAL;
         tiles *= mode == kFp4GroupK ? d->experts : 1;
     }
     return tiles < kFp4Lim / 2 ? MLPBLK_OK : MLPBLK_EINVAL;

@@ -997,3 +997,18 @@ def _pack_batch(mb, v):
     q = mb.Fp4Matrix(rows, cols, batch=E)
     q.quantize(x)
     return q, np.stack([fp4.rounded(to_np(x[e])) for e in range(E)])
+
+
+def test_two_billion_rows(mb):
+    """The most rows that a descriptor takes, quantised along rows and columns and read back."""
+    import torch
+    m = (1 << 31) - 1
+    x = torch.arange(m, dtype=torch.int32, device="cuda").remainder_(7).to(torch.bfloat16)   # 0 .. 6, all but 5 E2M1 values
+    x[x == 5] = -3.0
+    q = mb.Fp4Matrix(m, 1)
+    for transposed in (False, True):
+        q.quantize(x.view(1, m) if transposed else x.view(m, 1), transposed=transposed)
+        y = torch.full((m + 64,), 9.0, dtype=torch.bfloat16, device="cuda")
+        q.dequantize(y[:m].view(m, 1))
+        assert torch.equal(y[:m], x) and bool((y[m:] == 9.0).all())
+        q.codes[-16 * 4096:].fill_(0x77)                    # the second pass has these to mend

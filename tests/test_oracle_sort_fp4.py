@@ -468,3 +468,18 @@ def test_product_kernel_refusals(mb):
     assert f(D(8, 8, 8), 3, 152) == f(D(8, 8, 8), -1, 152) == f(D(8, 8, 8), 0, 0) == f(D(0, 8, 8), 0, 152) == -1
     assert f(D(8, 8, 8), 1, 152) == f(D(8, 0, 8), 0, 152) == f(D(8, 8, 0, experts=2, pad=256), 2, 152) == -1
     assert mb.lib.mlpblk_fp4_product_kernel(None, 0, 152) == -1
+
+
+def test_limits_as_documented(mb):
+    """rows * batch, experts * n and tokens * top_k are taken up to 2^31 - 1, whether or not
+    the factors divide 2^31."""
+    size = lambda *a: mb.mlpblk_fp4_codes_size(mb.make_fp4_desc(*a))
+    top = (1 << 31) - 1
+    for rows, batch in ((top, 1), ((1 << 30) + 1, 1), (715827882, 3), (1 << 30, 1)):
+        assert size(rows, 1, batch) == rows * batch * 16
+    assert size(1 << 31, 1) == size(715827883, 1, 3) == size(1 << 62, 1, 4) == 0
+    D, f = mb.make_fp4_matmul_desc, mb.mlpblk_fp4_product_kernel
+    assert f(D(128, 715827882, 1, experts=3, pad=128), 1, 152) > 0 and f(D(128, 715827883, 1, experts=3, pad=128), 1, 152) == -1
+    assert f(D(715827882, 1, 256, experts=3, pad=256), 2, 152) > 0 and f(D(715827883, 1, 256, experts=3, pad=256), 2, 152) == -1
+    rows = lambda t, k, pad=1: mb.mlpblk_moe_sort_rows(mb.make_sort_desc(t, 1, 1, k, pad))
+    assert rows(715827881, 3) == 715827881 * 3 and rows(715827882, 3) == rows(1 << 31, 1) == rows((1 << 31) - 1, 256) == -1
