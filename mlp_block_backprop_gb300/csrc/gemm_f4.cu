@@ -175,6 +175,12 @@ struct F4Tile {
     int n0, m_valid, n_valid;
 };
 
+// Tiles of TM rows that `rows` take (up to 2^31 - 1: the sum needs 32 unsigned bits).
+template <int TM>
+__device__ __forceinline__ int f4_row_tiles(int rows) {
+    return static_cast<int>((static_cast<unsigned>(rows) + (TM - 1)) / TM);
+}
+
 // Fills `g` (the whole CTA, a thread an expert) for tiles of TM rows; returns the number
 // of tiles.  Values that a plan of another shape would give are cut to the arrays, so
 // no access leaves them.
@@ -192,7 +198,7 @@ __device__ __forceinline__ int f4_groups(const F4Args &a, F4Groups *g) {
             int c = max(min(a.count[e], s1 - s0), 0);
             if (a.max_rows > 0) c = static_cast<int>(min(static_cast<int64_t>(c), a.max_rows));
             g->count[e] = c;
-            tiles = (c + TM - 1) / TM * a.nt;
+            tiles = f4_row_tiles<TM>(c) * a.nt;
         } else {
             tiles = a.mt * a.nt;
         }
@@ -236,7 +242,7 @@ __device__ __forceinline__ F4Tile f4_tile(const F4Args &a, const F4Groups *g, in
     }
     const int rows = a.mode == kFp4GroupRows ? g->count[e] : static_cast<int>(a.m);
     int mi = 0, ni = 0;
-    const int mt = (rows + TM - 1) / TM;
+    const int mt = f4_row_tiles<TM>(rows);
     if (mt == 1) ni = t;
     else raster_tile(t, mt, a.nt, group_m, mi, ni);
     const int first = a.mode == kFp4GroupRows ? g->seg[e] : 0;

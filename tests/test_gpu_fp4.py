@@ -1012,3 +1012,35 @@ def test_two_billion_rows(mb):
         q.dequantize(y[:m].view(m, 1))
         assert torch.equal(y[:m], x) and bool((y[m:] == 9.0).all())
         q.codes[-16 * 4096:].fill_(0x77)                    # the second pass has these to mend
+
+
+def test_products_of_two_billion_rows(mb):
+    """The most rows that a descriptor takes, by both kernels, dense and as one expert's."""
+    import torch
+    m = (1 << 31) - 1
+    x = torch.arange(m, dtype=torch.int32, device="cuda").remainder_(7).to(torch.bfloat16)
+    x[x == 5] = -3.0
+    q = mb.Fp4Matrix(m, 1)
+    q.quantize(x.view(m, 1))
+    w = mb.Fp4Matrix(1, 1)
+    w.quantize(torch.full((1, 1), 4.0, device="cuda"))
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    ref = x * 4.0
+    for out, kernel in (("bf16", "pair"), ("f32", 1)):
+        d = mb.make_fp4_matmul_desc(m, 1, 1, out)
+        assert fp4_shapes.kernel(mb, d, 0, sms) == kernel
+        c = torch.full((m + 64,), 9.0, dtype=_dt(out), device="cuda")
+        mb.mlpblk_fp4_matmul(d, q.codes, q.scales, w.codes, w.scales, c[:m])
+        assert torch.equal(c[:m].bfloat16(), ref) and bool((c[m:] == 9.0).all())
+        del c
+    R, live = m + 1 - 128, m - 137
+    count, seg = torch.tensor([live], dtype=torch.int32, device="cuda"), torch.tensor([0, R], dtype=torch.int32, device="cuda")
+    for out, kernel in (("bf16", "pair"), ("f32", 1)):
+        d = mb.make_fp4_matmul_desc(R, 1, 1, out, False, 1, 128)
+        assert fp4_shapes.kernel(mb, d, 1, sms) == kernel
+        c = torch.full((m,), 9.0, dtype=_dt(out), device="cuda")
+        mb.mlpblk_fp4_matmul_grouped(d, q.codes, q.scales, w.codes, w.scales, count, seg, c[:R])
+        assert torch.equal(c[:live].bfloat16(), ref[:live]) and bool((c[R:] == 9.0).all())
+        pad = c[live:R].bfloat16()
+        assert bool(((pad == 9.0) | (pad == ref[live:R])).all())
+        del c
