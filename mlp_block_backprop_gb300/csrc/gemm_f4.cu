@@ -142,6 +142,17 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
 }
 
+// Before a producer leaves: waits for the copies that it issued into the S stages, the next
+// of which would be `stage` in phase `phase`.  A run that went well finds them landed; one
+// that gave up must not leave while a copy may still write its shared memory.  Bounded over
+// all stages together.
+__device__ __forceinline__ void await_copies(uint64_t *bars, int S, int stage, uint32_t phase) {
+    const uint64_t t0 = global_timer_ns();
+    for (int s = 0; s < S; ++s)
+        while (!mbar_try_wait(&bars[s], s < stage ? phase : phase ^ 1u) && global_timer_ns() - t0 <= kWaitLimitNs) {
+        }
+}
+
 __device__ __forceinline__ uint32_t cluster_nctarank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
@@ -474,6 +485,7 @@ f4_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 }
             }
         }
+        await_copies(warp == 0 ? full_bar : sf_bar, S, stage, phase);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------- MMA issuer
@@ -803,6 +815,9 @@ f4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 }
             }
         }
+        // the leader's barriers collect the other CTA's operands too, which leaves no earlier
+        if (warp != 0) await_copies(sf_bar, S, stage, phase);
+        else if (leader) await_copies(full_bar, S, stage, phase);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------- MMA issuer
