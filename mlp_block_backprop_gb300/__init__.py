@@ -640,7 +640,7 @@ def mlpblk_moe_unpermute_backward(desc, dy, rows, pos, count, seg, weights, d_ro
 class _Kept:
     """Base of the classes that keep device buffers of their own: the buffers cannot
     be replaced, so their addresses are taken once and a call checks only what it is
-    given.  A call of these classes costs 2.3 to 3.4 us of host time on a Grace core, 1.5 of
+    given.  A call of these classes costs 2.4 to 3.9 us of host time on a Grace core, 1.5 of
     them the runtime's launch: the checks of the common case stand in the
     methods themselves, _operand only words the refusal."""
 
