@@ -753,7 +753,8 @@ const char *mlpblk_cuda_error_string(void);
 /* Static, NUL-terminated description of an MLPBLK_* code. */
 const char *mlpblk_strerror(int code);
 
-/* ABI version (major * 100 + minor). */
+/* ABI version (major * 100 + minor).  101: mlpblk_fp4_desc ends with source_rows, and a
+ * gathering mlpblk_fp4_quantize needs it. */
 int mlpblk_version(void);
 
 #ifdef __cplusplus

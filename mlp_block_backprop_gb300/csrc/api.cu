@@ -239,7 +239,7 @@ int traced(int kind, cudaStream_t s, F &&launch) {
 
 extern "C" {
 
-int mlpblk_version(void) { return 100; }
+int mlpblk_version(void) { return 101; }
 
 const char *mlpblk_strerror(int code) {
     switch (code) {

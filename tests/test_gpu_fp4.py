@@ -1044,3 +1044,59 @@ def test_products_of_two_billion_rows(mb):
         pad = c[live:R].bfloat16()
         assert bool(((pad == 9.0) | (pad == ref[live:R])).all())
         del c
+
+
+def test_calls_from_several_threads(mb):
+    """Threads with their own streams and buffers, and one set of weights between them, in
+    the middle of one another's calls (these run without the interpreter's lock)."""
+    import threading
+    import torch
+    T, d, n, E, k, pad = 60, 128, 96, 4, 2, 128
+    rng = np.random.default_rng(23)
+    w, b = _quantized(mb, rng, n, d, batch=E, wide=False)
+    work = []
+    for i in range(4):
+        ids = rng.integers(0, E, (T, k)).astype(np.int32)
+        s = mb.MoeSort(T, d, E, k, pad)
+        work.append(dict(ids=ids, idx=torch.from_numpy(ids).cuda(), s=s, x=_dev(rng.standard_normal((T, d)), "bf16"),
+                         q=mb.Fp4Matrix(s.rows, d), c=torch.zeros(s.rows, n, device="cuda"),
+                         back=torch.zeros(s.rows, d, device="cuda"), y=torch.zeros(T, n, dtype=torch.bfloat16, device="cuda"),
+                         o=mb.MoeSort(T, n, E, k, pad), rows=torch.zeros(s.rows, n, dtype=torch.bfloat16, device="cuda"),
+                         stream=torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    failed = []
+    start = threading.Barrier(len(work))
+
+    def run(m):
+        try:
+            start.wait()
+            with torch.cuda.stream(m["stream"]):
+                for _ in range(100):
+                    m["s"].sort(m["idx"])
+                    m["o"].sort(m["idx"])
+                    m["q"].quantize(m["x"], sort=m["s"], gather=True)
+                    m["q"].matmul_grouped(w, m["s"], m["c"])
+                    m["q"].matmul_grouped(w, m["s"], m["rows"])
+                    m["q"].dequantize(m["back"])
+                    m["o"].unpermute(m["rows"], m["y"])
+                m["stream"].synchronize()
+        except Exception as e:                              # shown by the test's own thread
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(m,)) for m in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for m in work:
+        count, seg, pos, row_map = sort.plan(m["ids"], E, pad)
+        src = np.where((row_map >= 0)[:, None], to_np(m["x"])[np.maximum(row_map, 0) // k], 0.0)
+        a = fp4.rounded(src)
+        np.testing.assert_array_equal(to_np(m["back"]), a)
+        for e in range(E):
+            r = slice(seg[e], seg[e] + count[e])
+            _check(to_np(m["c"])[r], a[r], b[e], "f32", d)
+            _check(to_np(m["rows"])[r], a[r], b[e], "bf16", d)
+        ref, mag = sort.unpermute(to_np(m["rows"]), pos)
+        assert np.all(np.abs(to_np(m["y"]) - ref) <= 2.0 ** -8 * np.abs(ref) + (k + 1) * 2.0 ** -24 * mag)

@@ -243,6 +243,10 @@ def test_fp4_gather_needs_the_sources_rows(mb):
     assert mb.mlpblk_fp4_codes_size(mb.make_fp4_desc(8, 64, source_rows=-1)) == 8 * 32  # of no meaning elsewhere
 
 
+def test_version_tells_of_the_descriptors_field(mb):
+    assert mb.mlpblk_version() >= 101 and mb.Fp4Desc._fields_[-1][0] == "source_rows" and ctypes.sizeof(mb.Fp4Desc) == 40
+
+
 def test_fp4_product_refusals(mb):
     p = _addresses(5)
     mm = lambda d, a=p: mb.lib.mlpblk_fp4_matmul(ctypes.byref(d), *a, None)
