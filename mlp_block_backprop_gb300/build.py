@@ -42,9 +42,8 @@ def _newest_input_mtime() -> float:
     return max(os.path.getmtime(p) for p in paths)
 
 
-def up_to_date() -> bool:
-    outputs = [LIB] + ([CALLS] if _python_headers() else [])
-    return all(os.path.exists(p) and os.path.getmtime(p) >= _newest_input_mtime() for p in outputs)
+def up_to_date(path: str) -> bool:
+    return os.path.exists(path) and os.path.getmtime(path) >= _newest_input_mtime()
 
 
 def _python_headers():
@@ -76,7 +75,9 @@ def _remove_calls() -> None:
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
     """Compile and link libmlpblk.so; returns its path.  Raises on failure."""
-    if not force and up_to_date():
+    if not force and up_to_date(LIB):
+        if _python_headers() and not up_to_date(CALLS):  # another interpreter than the last one's
+            _build_calls()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()

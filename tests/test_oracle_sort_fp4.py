@@ -487,3 +487,23 @@ def test_limits_as_documented(mb):
     assert f(D(715827882, 1, 256, experts=3, pad=256), 2, 152) > 0 and f(D(715827883, 1, 256, experts=3, pad=256), 2, 152) == -1
     rows = lambda t, k, pad=1: mb.mlpblk_moe_sort_rows(mb.make_sort_desc(t, 1, 1, k, pad))
     assert rows(715827881, 3) == 715827881 * 3 and rows(715827882, 3) == rows(1 << 31, 1) == rows((1 << 31) - 1, 256) == -1
+
+
+def test_two_interpreters_keep_their_modules(tmp_path, monkeypatch):
+    """A second interpreter's build beside a library that is up to date makes its own module
+    and leaves the library and the first one's alone."""
+    import __graft_entry__
+    build = __graft_entry__._build_script()
+    lib, mine, other = (tmp_path / n for n in ("libmlpblk.so", "_mlpblk_calls.mine.so", "_mlpblk_calls.cpython-39-none.so"))
+    lib.write_bytes(b"library")
+    other.write_bytes(b"other")
+    monkeypatch.setattr(build, "HERE", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", str(lib))
+    monkeypatch.setattr(build, "CALLS", str(mine))
+    monkeypatch.setattr(build, "_newest_input_mtime", lambda: 0.0)
+    monkeypatch.setattr(build, "_python_headers", lambda: str(tmp_path))
+    monkeypatch.setattr(build, "nvcc", lambda: pytest.fail("the library is up to date"))
+    monkeypatch.setattr(build, "_build_calls", lambda: mine.write_bytes(b"mine"))
+    assert build.build_library() == str(lib) and mine.read_bytes() == b"mine" and other.read_bytes() == b"other"
+    mine.write_bytes(b"kept")
+    assert build.build_library() == str(lib) and mine.read_bytes() == b"kept"
