@@ -599,6 +599,164 @@ int mlpblk_fp4_wgrad_grouped(const mlpblk_fp4_matmul_desc *desc, const void *a_c
 int mlpblk_fp4_product_kernel(const mlpblk_fp4_matmul_desc *desc, int form, int sms);
 
 /*
+ * The router of routed experts ("Kernel 4: Routed ReLU2 MoE": select): logits -> expert ids
+ * and routing weights, as mlpblk_moe_sort, mlpblk_moe_unpermute and mlpblk_moe_forward take
+ * them.
+ *   s_e   = softmax over the token's open experts, or 1 / (1 + exp(-l_e))   (desc->score)
+ *   key_e = s_e + bias_e; bias NULL: s_e.  The bias balances the experts' load; it decides
+ *           what is selected and enters nothing else
+ *   groups: the experts lie in desc->groups equal runs; a group's mark is the sum of its two
+ *           best keys (of the only one, if it has one open expert); the top_groups best marks
+ *           stay, ties to the lower group
+ *   expert_idx[t,j]      = the j-th best key's expert among those groups, ties to the lower
+ *                          expert (so a token names no expert twice); -1 where no open
+ *                          expert is left
+ *   routing_weights[t,j] = scale * s, or with desc->renorm scale * s / (sum_j s + 1e-20); 0
+ *                          beside -1
+ * A logit of -infinity or NaN closes its expert to the token; +infinity counts as the largest
+ * finite value.  A row whose experts are all closed selects nothing.  The order is that of
+ * the scores in float64 (without a bias, of the logits), whatever the arithmetic here:
+ * float32 keys that are too close to call are computed again.  bias values are finite.
+ *
+ * mlpblk_moe_route_backward: d_logits[T,E] (written) from d_routing_weights[T,k], for the
+ * ids of the same logits, held fixed ("Hard Top-K Has No Ordinary Derivative").  Ids outside
+ * 0 .. E-1 and closed experts have no gradient.  The bias has none.
+ *
+ * logits and d_logits [T,E] are in desc->dtype, the rest float32 and int32; scores, sums and
+ * quotients are float32, their order fixed.  Limits: tokens < 2^31, experts 1..256, top_k
+ * 1..16, groups 1..64 and a divisor of experts, top_groups 1..groups, top_k at most
+ * top_groups * experts / groups, scale finite.  Pointers are device pointers, 16-byte
+ * aligned; outputs share no byte with an input or with each other (MLPBLK_EINVAL).  tokens = 0 returns
+ * MLPBLK_OK and touches nothing.
+ */
+#define MLPBLK_ROUTE_SOFTMAX  0
+#define MLPBLK_ROUTE_SIGMOID  1
+#define MLPBLK_ROUTE_MAX_TOP_K 16
+
+typedef struct {
+    int64_t tokens;       /* T >= 0                                              */
+    int32_t experts;      /* E                                                   */
+    int32_t top_k;        /* k                                                   */
+    int32_t score;        /* MLPBLK_ROUTE_SOFTMAX or MLPBLK_ROUTE_SIGMOID         */
+    int32_t groups;       /* 1: none                                             */
+    int32_t top_groups;   /* groups that stay; = groups: all                      */
+    int32_t renorm;       /* 1: the weights are divided by their sum              */
+    float   scale;        /* of the weights                                      */
+    int32_t dtype;        /* of the logits: MLPBLK_BF16 or MLPBLK_FP32             */
+} mlpblk_route_desc;
+
+int mlpblk_moe_route(const mlpblk_route_desc *desc, const void *logits, const float *bias, int32_t *expert_idx,
+                     float *routing_weights, void *stream);
+
+int mlpblk_moe_route_backward(const mlpblk_route_desc *desc, const void *logits, const int32_t *expert_idx,
+                              const float *d_routing_weights, void *d_logits, void *stream);
+
+/*
+ * The residual sum and RMSNorm of the pre-norm shell, with an 8-bit output ("Setup: The
+ * Shared Transformer Shell"; "Where Quantization Fits"), for programs whose next products
+ * are their own:
+ *   sum   = x + residual, rounded to the dtype; residual NULL: sum is x itself
+ *   rstd  = 1 / sqrt(mean_k sum^2 + eps)
+ *   n     = sum * rstd * gamma                                    (optional output, dtype)
+ *   scales = max |n| / 448 over the row (desc->block = 0: [T]), or over each run of 128
+ *           columns (desc->block = 128: [T, ceil(width / 128)]), rounded to float32; 1
+ *           where that is 0
+ *   codes = E4M3(n / scale), nearest even                         [T, width], a byte each
+ * sum is written where residual is given (and only then) and may be x or residual itself.
+ * codes and scales are given together; n, codes and rstd may be NULL, n and codes not both.
+ * The codes are those of the real number n / scale, rounded once.  A row that holds an
+ * infinity or a NaN, or whose mean square exceeds float32, has a NaN rstd and NaN scales and
+ * codes.
+ *
+ * mlpblk_add_rmsnorm_backward: with dn the gradient of n (as the codes stand for it:
+ *   rounding passes it on) and d_sum that of sum (NULL: none),
+ *     dx[T,width] = d_sum + rstd * (g - xh * mean_k(g * xh)),  g = dn * gamma, xh = sum * rstd
+ *                   (written; the gradient of x and of residual)
+ *     dgamma[width] += (overwrite = 1: =) sum_t dn * xh               float32
+ *   sum and rstd are the forward's (sum is x where there was no residual).  dx may be dn or
+ *   d_sum itself.  Sums are float32 in a fixed order.  workspace: scratch,
+ *   mlpblk_add_rmsnorm_workspace_size bytes (0 for an invalid descriptor), not shared by two
+ *   calls in flight.  With tokens = 0 dgamma is set to zero when overwriting; nothing else
+ *   is touched.
+ *
+ * x, residual, gamma, sum, n, dn, d_sum, dx are in desc->dtype.  Limits: tokens < 2^31,
+ * 1 <= width <= 16384 (MLPBLK_ENOTSUP beyond), eps finite and >= 0.  Rows of a multiple of 16 bytes
+ * move in 16-byte accesses.  Pointers are device pointers, 16-byte aligned; outputs share no
+ * byte with an input but where stated, nor with each other (MLPBLK_EINVAL).  tokens = 0
+ * returns MLPBLK_OK and touches nothing but what is stated.
+ */
+typedef struct {
+    int64_t tokens;   /* T >= 0                                       */
+    int64_t width;    /* elements of a row                              */
+    float   eps;
+    int32_t dtype;    /* MLPBLK_BF16 or MLPBLK_FP32                    */
+    int32_t block;    /* columns that share a scale: 0 (a row) or 128   */
+} mlpblk_norm_desc;
+
+int mlpblk_add_rmsnorm(const mlpblk_norm_desc *desc, const void *x, const void *residual, const void *gamma,
+                       void *sum, void *n, void *codes, float *scales, float *rstd, void *stream);
+
+size_t mlpblk_add_rmsnorm_workspace_size(const mlpblk_norm_desc *desc);
+
+int mlpblk_add_rmsnorm_backward(const mlpblk_norm_desc *desc, const void *dn, const void *d_sum, const void *sum,
+                                const float *rstd, const void *gamma, void *dx, float *dgamma, int32_t overwrite,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Orthogonalised updates for matrices, beside AdamW ("optimizer state": here one moment per
+ * weight; the step is Muon's, K. Jordan et al., 2024).
+ *
+ * mlpblk_orthogonalize: o[batch, rows, cols] (bf16, written) = the result of desc->steps
+ *   Newton-Schulz steps on each u[rows, cols] (desc->dtype):
+ *     X = u / (|u| + eps),   |u| the Frobenius norm;   then for each step's (a, b, c)
+ *     X <- a X + (b G + c G^2) X,  G = X X^T
+ *   (the odd polynomial a s + b s^3 + c s^5 on the singular values; a tall u is worked on from
+ *   its right, which is the same).  u is not changed; a matrix of zeros gives zeros.
+ * mlpblk_muon_step: one update of `batch` weights (float32 master, gradient and momentum):
+ *     g <- grad * grad_scale[0] (NULL: 1),  momentum <- beta momentum + g
+ *     u = g + beta momentum (nesterov), or momentum;   X as above (not rounded to bf16)
+ *     master <- master * (1 - lr * weight_decay) - lr * scale * X
+ *   then weight = master in desc->dtype (NULL: none).
+ *
+ * Precision: products of fp16 values, whose range X's scaling fits, with float32 sums; a X
+ * takes X as two fp16 values in all but the last step.  With Muon's coefficients
+ * (3.4445, -4.7750, 2.0315), five steps, the result is within 3e-3 of the formula's in the
+ * Frobenius norm (before o's rounding to bf16).  The polynomials must keep |X|'s singular values below 16.  A NaN or an
+ * infinity in u makes its matrix NaN.  Sums have a fixed order.
+ *
+ * mlpblk_orthogonalize_workspace_size: bytes of scratch for both; 0 for an invalid
+ *   descriptor.  Not shared by two calls in flight.
+ * Limits: rows and cols 1 .. 131072, batch 1 .. 65535, rows * cols * batch < 2^40,
+ * steps 1 .. MLPBLK_ORTHO_MAX_STEPS, coefficients and hyper-parameters finite, eps >= 0, 0 <= momentum
+ * < 1, lr and weight_decay >= 0.  Pointers are device pointers, 16-byte aligned; outputs and
+ * the workspace share no byte with an input or with each other (MLPBLK_EINVAL).
+ */
+#define MLPBLK_ORTHO_MAX_STEPS 16
+
+typedef struct {
+    int64_t rows, cols;
+    int32_t batch;
+    int32_t dtype;        /* of u (orthogonalize) or weight (muon_step)        */
+    int32_t steps;
+    float   eps;
+    float   coefficients[MLPBLK_ORTHO_MAX_STEPS][3];   /* a, b, c of each step */
+} mlpblk_ortho_desc;
+
+typedef struct {
+    float lr, momentum, weight_decay, scale;
+    int32_t nesterov;
+} mlpblk_muon;
+
+size_t mlpblk_orthogonalize_workspace_size(const mlpblk_ortho_desc *desc);
+
+int mlpblk_orthogonalize(const mlpblk_ortho_desc *desc, const void *u, void *o, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+int mlpblk_muon_step(const mlpblk_ortho_desc *desc, const mlpblk_muon *hp, float *master, void *weight,
+                     const float *grad, float *momentum, const float *grad_scale, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
  * zero_grads() of the accumulation loop ("grow_a_language_model_backprop" --
  * accumulation across microbatches): dgamma[d], dw1[F,d], dw2[d,F] = 0 (float32).
  * desc->tokens is ignored.  Returns an MLPBLK_* code.
@@ -701,6 +859,17 @@ int mlpblk_rmsnorm_backward_noalloc(const mlpblk_desc *desc, const void *x, cons
 #define MLPBLK_KERNEL_FP4_QUANT      30  /* MXFP4: v -> codes and scales              */
 #define MLPBLK_KERNEL_FP4_DEQUANT    31  /* MXFP4: codes and scales -> v              */
 #define MLPBLK_KERNEL_FP4_GEMM       32  /* MXFP4 product, dense or grouped           */
+#define MLPBLK_KERNEL_ROUTE          33  /* mlpblk_moe_route                          */
+#define MLPBLK_KERNEL_ROUTE_BWD      34  /* mlpblk_moe_route_backward                 */
+#define MLPBLK_KERNEL_ADD_NORM       35  /* mlpblk_add_rmsnorm                        */
+#define MLPBLK_KERNEL_ADD_NORM_BWD   36  /* mlpblk_add_rmsnorm_backward: dx, dgamma parts */
+#define MLPBLK_KERNEL_ADD_NORM_DG    37  /* its dgamma from the parts                 */
+#define MLPBLK_KERNEL_ORTHO_NORM     38  /* |u|'s partial sums (momentum on the way)   */
+#define MLPBLK_KERNEL_ORTHO_SCALE    39  /* X = u / (|u| + eps)                       */
+#define MLPBLK_KERNEL_NS_GRAM        40  /* G = X X^T                                 */
+#define MLPBLK_KERNEL_NS_SQUARE      41  /* P = b G + c G^2                           */
+#define MLPBLK_KERNEL_NS_UPDATE      42  /* X = a X + P X                             */
+#define MLPBLK_KERNEL_MUON_APPLY     43  /* master, weight                            */
 
 /*
  * mlpblk_trace_begin: from now on, launch i of this library records
@@ -754,7 +923,7 @@ const char *mlpblk_cuda_error_string(void);
 const char *mlpblk_strerror(int code);
 
 /* ABI version (major * 100 + minor).  101: mlpblk_fp4_desc ends with source_rows, and a
- * gathering mlpblk_fp4_quantize needs it. */
+ * gathering mlpblk_fp4_quantize needs it.  102: routing, add_rmsnorm, orthogonalize, muon_step. */
 int mlpblk_version(void);
 
 #ifdef __cplusplus

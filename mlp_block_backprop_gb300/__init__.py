@@ -47,7 +47,14 @@ EXPORTED = ("mlpblk_workspace_size", "mlpblk_forward", "mlpblk_backward", "mlpbl
             "mlpblk_moe_unpermute", "mlpblk_moe_unpermute_backward",
             "mlpblk_fp4_codes_size", "mlpblk_fp4_scales_size", "mlpblk_fp4_quantize", "mlpblk_fp4_dequantize",
             "mlpblk_fp4_matmul", "mlpblk_fp4_matmul_grouped", "mlpblk_fp4_wgrad_grouped",
-            "mlpblk_fp4_product_kernel")
+            "mlpblk_fp4_product_kernel",
+            "mlpblk_moe_route", "mlpblk_moe_route_backward",
+            "mlpblk_add_rmsnorm", "mlpblk_add_rmsnorm_workspace_size", "mlpblk_add_rmsnorm_backward",
+            "mlpblk_orthogonalize_workspace_size", "mlpblk_orthogonalize", "mlpblk_muon_step")
+MLPBLK_ROUTE_SOFTMAX = 0
+MLPBLK_ROUTE_SIGMOID = 1
+MLPBLK_ROUTE_MAX_TOP_K = 16
+MLPBLK_ORTHO_MAX_STEPS = 16
 MLPBLK_FP4_KERNEL_PAIR_TMA = 256
 MLPBLK_FP4_KERNEL_PAIR = 257
 MLPBLK_FP4_ACT_NONE = 0
@@ -64,7 +71,9 @@ KERNEL_NAMES = {1: "fold_gamma", 2: "gemm_fwd_w1", 3: "gemm_fwd_w2", 4: "gemm_dg
                 17: "quant_amax", 18: "quant_scale", 19: "quant_apply", 20: "norm_quant",
                 21: "moe_route", 22: "moe_gather", 23: "moe_combine", 24: "moe_dp", 25: "moe_scatter",
                 26: "sort", 27: "permute", 28: "unpermute", 29: "unpermute_bwd",
-                30: "fp4_quant", 31: "fp4_dequant", 32: "fp4_gemm"}
+                30: "fp4_quant", 31: "fp4_dequant", 32: "fp4_gemm", 33: "route", 34: "route_bwd",
+                35: "add_norm", 36: "add_norm_bwd", 37: "add_norm_dgamma", 38: "ortho_norm", 39: "ortho_scale",
+                40: "ns_gram", 41: "ns_square", 42: "ns_update", 43: "muon_apply"}
 
 
 class MlpBlkError(RuntimeError):
@@ -105,6 +114,32 @@ class Fp4MatmulDesc(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
                 ("out_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32), ("experts", ctypes.c_int32),
                 ("pad", ctypes.c_int32), ("max_rows", ctypes.c_int64)]
+
+
+class RouteDesc(ctypes.Structure):
+    """mlpblk_route_desc: the router of routed experts."""
+    _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class NormDesc(ctypes.Structure):
+    """mlpblk_norm_desc: the residual sum with RMSNorm."""
+    _fields_ = [("tokens", ctypes.c_int64), ("width", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("dtype", ctypes.c_int32), ("block", ctypes.c_int32)]
+
+
+class OrthoDesc(ctypes.Structure):
+    """mlpblk_ortho_desc: an orthogonalised update."""
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("batch", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("steps", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("coefficients", ctypes.c_float * 3 * MLPBLK_ORTHO_MAX_STEPS)]
+
+
+class Muon(ctypes.Structure):
+    """mlpblk_muon: Muon's hyper-parameters."""
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("scale", ctypes.c_float), ("nesterov", ctypes.c_int32)]
 
 
 class Param(ctypes.Structure):
@@ -208,6 +243,23 @@ def _load():
     lib.mlpblk_fp4_wgrad_grouped.restype = i32
     lib.mlpblk_fp4_product_kernel.argtypes = [pp, i32, i32]
     lib.mlpblk_fp4_product_kernel.restype = i32
+    pr, pn, po = ctypes.POINTER(RouteDesc), ctypes.POINTER(NormDesc), ctypes.POINTER(OrthoDesc)
+    lib.mlpblk_moe_route.argtypes = [pr] + [vp] * 5
+    lib.mlpblk_moe_route.restype = i32
+    lib.mlpblk_moe_route_backward.argtypes = [pr] + [vp] * 5
+    lib.mlpblk_moe_route_backward.restype = i32
+    lib.mlpblk_add_rmsnorm.argtypes = [pn] + [vp] * 9
+    lib.mlpblk_add_rmsnorm.restype = i32
+    lib.mlpblk_add_rmsnorm_workspace_size.argtypes = [pn]
+    lib.mlpblk_add_rmsnorm_workspace_size.restype = sz
+    lib.mlpblk_add_rmsnorm_backward.argtypes = [pn] + [vp] * 7 + [i32, vp, sz, vp]
+    lib.mlpblk_add_rmsnorm_backward.restype = i32
+    lib.mlpblk_orthogonalize_workspace_size.argtypes = [po]
+    lib.mlpblk_orthogonalize_workspace_size.restype = sz
+    lib.mlpblk_orthogonalize.argtypes = [po, vp, vp, vp, sz, vp]
+    lib.mlpblk_orthogonalize.restype = i32
+    lib.mlpblk_muon_step.argtypes = [po, ctypes.POINTER(Muon)] + [vp] * 6 + [sz, vp]
+    lib.mlpblk_muon_step.restype = i32
     lib.mlpblk_zero_grads.argtypes = [pd, vp, vp, vp, vp]
     lib.mlpblk_zero_grads.restype = i32
     lib.mlpblk_scale_grads.argtypes = [pd, vp, vp, vp, f32, vp]
@@ -244,7 +296,8 @@ class _Calls:
     def __init__(self):
         native = self._native()
         for name in ("moe_sort", "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
-                     "fp4_quantize", "fp4_dequantize", "fp4_matmul", "fp4_matmul_grouped", "fp4_wgrad_grouped"):
+                     "fp4_quantize", "fp4_dequantize", "fp4_matmul", "fp4_matmul_grouped", "fp4_wgrad_grouped",
+                     "moe_route", "moe_route_backward", "add_rmsnorm", "add_rmsnorm_backward", "orthogonalize"):
             setattr(self, name, getattr(native, "mlpblk_" + name) if native else self._ctypes("mlpblk_" + name))
         self.native = native is not None
 
@@ -1007,6 +1060,302 @@ class Fp4Matrix(_Kept):
         rc = _calls.fp4_wgrad_grouped(d, *self._at, *b._at, sort._at[1], at, st if stream is None else _stream(stream))
         if rc:
             _check(rc, where)
+
+
+_SCORES = {"softmax": MLPBLK_ROUTE_SOFTMAX, "sigmoid": MLPBLK_ROUTE_SIGMOID}
+
+
+def make_route_desc(tokens, experts, top_k, score="softmax", groups=1, top_groups=None, renorm=True, scale=1.0,
+                    dtype=MLPBLK_BF16) -> RouteDesc:
+    code = score if isinstance(score, int) else _SCORES.get(score)
+    if code is None:
+        raise MlpBlkError(MLPBLK_ENOTSUP, f"score {score!r}")
+    return RouteDesc(int(tokens), int(experts), int(top_k), code, int(groups), int(groups if top_groups is None else top_groups),
+                     int(bool(renorm)), float(scale), _dtype_code(dtype))
+
+
+def mlpblk_moe_route(desc, logits, bias, expert_idx, routing_weights, stream=None):
+    where = "mlpblk_moe_route"
+    t = _Torch.get()
+    dev, n = t.device(), desc.tokens * desc.top_k
+    rc = lib.mlpblk_moe_route(
+        ctypes.byref(desc), _operand(logits, where, "logits", t.row.get(desc.dtype), desc.tokens * desc.experts, dev),
+        _operand(bias, where, "bias", t.float32, desc.experts, dev),
+        _operand(expert_idx, where, "expert_idx", t.int32, n, dev),
+        _operand(routing_weights, where, "routing_weights", t.float32, n, dev), _stream(stream))
+    _check(rc, where)
+
+
+def mlpblk_moe_route_backward(desc, logits, expert_idx, d_routing_weights, d_logits, stream=None):
+    where = "mlpblk_moe_route_backward"
+    t = _Torch.get()
+    dev, n = t.device(), desc.tokens * desc.top_k
+    dt, e = t.row.get(desc.dtype), desc.tokens * desc.experts
+    rc = lib.mlpblk_moe_route_backward(
+        ctypes.byref(desc), _operand(logits, where, "logits", dt, e, dev),
+        _operand(expert_idx, where, "expert_idx", t.int32, n, dev),
+        _operand(d_routing_weights, where, "d_routing_weights", t.float32, n, dev),
+        _operand(d_logits, where, "d_logits", dt, e, dev), _stream(stream))
+    _check(rc, where)
+
+
+class MoeRouter:
+    """The router of one batch: `route` turns logits into expert ids and weights (those that
+    MoeSort.sort and MoeSort.unpermute take), `route_backward` the weights' gradient into
+    the logits'.  It keeps no buffers: every tensor is the caller's."""
+
+    def __init__(self, tokens, experts, top_k, score="softmax", groups=1, top_groups=None, renorm=True, scale=1.0,
+                 dtype="bf16"):
+        self.desc = make_route_desc(tokens, experts, top_k, score, groups, top_groups, renorm, scale, dtype)
+        rc = lib.mlpblk_moe_route(ctypes.byref(make_route_desc(0, experts, top_k, score, groups, top_groups, renorm, scale, dtype)),
+                                  None, None, None, None, None)   # no tokens: checks the descriptor alone
+        if rc or self.desc.tokens < 0 or self.desc.tokens >= 2 ** 31:
+            raise MlpBlkError(rc or MLPBLK_EINVAL, "MoeRouter")
+        self._d = ctypes.addressof(self.desc)
+        self._n, self._l, self._e = self.desc.tokens * self.desc.top_k, self.desc.tokens * self.desc.experts, self.desc.experts
+        self._t = _Torch.get()
+        self._type = self._t.row[self.desc.dtype]
+
+    def route(self, logits, expert_idx, routing_weights, bias=None, stream=None):
+        """expert_idx [tokens, top_k] int32 and routing_weights [tokens, top_k] float32 of
+        logits [tokens, experts]; bias [experts] float32 or None."""
+        where = "MoeRouter.route"
+        t, dt, n = self._t, self._type, self._n
+        dev = t.device()
+        if logits.dtype is not dt or logits.numel() < self._l or logits.get_device() != dev or not logits.is_contiguous():
+            _operand(logits, where, "logits", dt, self._l, dev)
+        if (expert_idx.dtype is not t.int32 or expert_idx.numel() < n or expert_idx.get_device() != dev
+                or not expert_idx.is_contiguous()):
+            _operand(expert_idx, where, "expert_idx", t.int32, n, dev)
+        if (routing_weights.dtype is not t.float32 or routing_weights.numel() < n or routing_weights.get_device() != dev
+                or not routing_weights.is_contiguous()):
+            _operand(routing_weights, where, "routing_weights", t.float32, n, dev)
+        if bias is not None:
+            if bias.dtype is not t.float32 or bias.numel() < self._e or bias.get_device() != dev or not bias.is_contiguous():
+                _operand(bias, where, "bias", t.float32, self._e, dev)
+            bias = bias.data_ptr()
+        rc = _calls.moe_route(self._d, logits.data_ptr(), bias, expert_idx.data_ptr(), routing_weights.data_ptr(),
+                              t.raw_stream(dev) if stream is None else _stream(stream))
+        if rc:
+            _check(rc, where)
+
+    def route_backward(self, logits, expert_idx, d_routing_weights, d_logits, stream=None):
+        """d_logits [tokens, experts] (written) of the same logits and the ids `route` gave."""
+        where = "MoeRouter.route_backward"
+        t, dt, n = self._t, self._type, self._n
+        dev = t.device()
+        for x, name, want, least in ((logits, "logits", dt, self._l), (expert_idx, "expert_idx", t.int32, n),
+                                     (d_routing_weights, "d_routing_weights", t.float32, n), (d_logits, "d_logits", dt, self._l)):
+            if x.dtype is not want or x.numel() < least or x.get_device() != dev or not x.is_contiguous():
+                _operand(x, where, name, want, least, dev)
+        rc = _calls.moe_route_backward(self._d, logits.data_ptr(), expert_idx.data_ptr(), d_routing_weights.data_ptr(),
+                                       d_logits.data_ptr(), t.raw_stream(dev) if stream is None else _stream(stream))
+        if rc:
+            _check(rc, where)
+
+
+def make_norm_desc(tokens, width, eps=1e-6, dtype=MLPBLK_BF16, block=0) -> NormDesc:
+    return NormDesc(int(tokens), int(width), float(eps), _dtype_code(dtype), int(block))
+
+
+def _norm_scales(desc):
+    """Scales of one row."""
+    return (desc.width + 127) // 128 if desc.block else 1
+
+
+def _codes(t, where, numel, dev):
+    """Address of a tensor of codes: torch.float8_e4m3fn or uint8."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    return _operand(t, where, "codes", t.dtype if t.dtype in (torch.float8_e4m3fn, torch.uint8) else torch.float8_e4m3fn, numel, dev)
+
+
+def mlpblk_add_rmsnorm(desc, x, residual, gamma, sum, n, codes, scales, rstd, stream=None):
+    where = "mlpblk_add_rmsnorm"
+    t = _Torch.get()
+    dev, dt, e = t.device(), t.row.get(desc.dtype), desc.tokens * desc.width
+    rc = lib.mlpblk_add_rmsnorm(
+        ctypes.byref(desc), _operand(x, where, "x", dt, e, dev), _operand(residual, where, "residual", dt, e, dev),
+        _operand(gamma, where, "gamma", dt, desc.width, dev), _operand(sum, where, "sum", dt, e, dev),
+        _operand(n, where, "n", dt, e, dev), _codes(codes, where, e, dev),
+        _operand(scales, where, "scales", t.float32, desc.tokens * _norm_scales(desc), dev),
+        _operand(rstd, where, "rstd", t.float32, desc.tokens, dev), _stream(stream))
+    _check(rc, where)
+
+
+def mlpblk_add_rmsnorm_workspace_size(desc: NormDesc) -> int:
+    return int(lib.mlpblk_add_rmsnorm_workspace_size(ctypes.byref(desc)))
+
+
+def mlpblk_add_rmsnorm_backward(desc, dn, d_sum, sum, rstd, gamma, dx, dgamma, workspace, overwrite=False, stream=None):
+    where = "mlpblk_add_rmsnorm_backward"
+    t = _Torch.get()
+    dev, dt, e = t.device(), t.row.get(desc.dtype), desc.tokens * desc.width
+    rc = lib.mlpblk_add_rmsnorm_backward(
+        ctypes.byref(desc), _operand(dn, where, "dn", dt, e, dev), _operand(d_sum, where, "d_sum", dt, e, dev),
+        _operand(sum, where, "sum", dt, e, dev), _operand(rstd, where, "rstd", t.float32, desc.tokens, dev),
+        _operand(gamma, where, "gamma", dt, desc.width, dev), _operand(dx, where, "dx", dt, e, dev),
+        _operand(dgamma, where, "dgamma", t.float32, desc.width, dev), int(bool(overwrite)),
+        _operand(workspace, where, "workspace", t.uint8, 0, dev), 0 if workspace is None else workspace.numel(), _stream(stream))
+    _check(rc, where)
+
+
+class AddRmsNorm(_Kept):
+    """The residual sum and RMSNorm of one batch, with E4M3 codes and their scales: `forward`
+    and `backward`.  It keeps rstd (written by `forward`, read by `backward`) and the
+    backward's scratch; a forward whose backward is to come keeps both until then."""
+
+    def __init__(self, tokens, width, eps=1e-6, dtype="bf16", block=0, device="cuda"):
+        import torch
+        self.desc = make_norm_desc(tokens, width, eps, dtype, block)
+        size = mlpblk_add_rmsnorm_workspace_size(self.desc)
+        if size == 0:
+            raise MlpBlkError(MLPBLK_EINVAL, "mlpblk_add_rmsnorm_workspace_size")
+        self._rstd = torch.zeros(tokens, dtype=torch.float32, device=device)
+        self._ws = torch.empty(size, dtype=torch.uint8, device=device)
+        self._dev = self._ws.get_device()
+        self._d = ctypes.addressof(self.desc)
+        self._at = (self._rstd.data_ptr(), self._ws.data_ptr(), size)
+        self._n, self._s = tokens * width, tokens * _norm_scales(self.desc)
+        self._t = _Torch.get()
+        self._type = self._t.row[self.desc.dtype]
+        self._code_types = (torch.float8_e4m3fn, torch.uint8)
+
+    rstd = property(lambda self: self._rstd)
+
+    def forward(self, x, gamma, codes=None, scales=None, n=None, residual=None, sum=None, stream=None):
+        """codes [tokens, width] (torch.float8_e4m3fn, or uint8) with scales [tokens] or
+        [tokens, ceil(width / 128)] float32, and / or n; with residual, sum = x + residual
+        (x or residual itself, or another tensor)."""
+        where = "AddRmsNorm.forward"
+        t, dt, e = self._t, self._type, self._n
+        dev = t.device()
+        if dev != self._dev:
+            self._where(dev, where)
+        if x.dtype is not dt or x.numel() < e or x.get_device() != dev or not x.is_contiguous():
+            _operand(x, where, "x", dt, e, dev)
+        if gamma.dtype is not dt or gamma.numel() < self.desc.width or gamma.get_device() != dev or not gamma.is_contiguous():
+            _operand(gamma, where, "gamma", dt, self.desc.width, dev)
+        if codes is not None:
+            if codes.dtype not in self._code_types or codes.numel() < e or codes.get_device() != dev or not codes.is_contiguous():
+                _codes(codes, where, e, dev)
+            codes = codes.data_ptr()
+        if scales is not None:
+            scales = _operand(scales, where, "scales", t.float32, self._s, dev)
+        if n is not None:
+            n = _operand(n, where, "n", dt, e, dev)
+        if residual is not None:
+            residual = _operand(residual, where, "residual", dt, e, dev)
+        if sum is not None:
+            sum = _operand(sum, where, "sum", dt, e, dev)
+        rc = _calls.add_rmsnorm(self._d, x.data_ptr(), residual, gamma.data_ptr(), sum, n, codes, scales, self._at[0],
+                                t.raw_stream(dev) if stream is None else _stream(stream))
+        if rc:
+            _check(rc, where)
+
+    def backward(self, dn, sum, gamma, dx, dgamma, d_sum=None, overwrite=False, stream=None):
+        """dx and dgamma (added to, or set with overwrite) from dn and d_sum; sum is the
+        forward's (x where it had no residual)."""
+        where = "AddRmsNorm.backward"
+        t, dt, e = self._t, self._type, self._n
+        dev = t.device()
+        if dev != self._dev:
+            self._where(dev, where)
+        rstd, ws, size = self._at
+        rc = _calls.add_rmsnorm_backward(
+            self._d, _operand(dn, where, "dn", dt, e, dev), _operand(d_sum, where, "d_sum", dt, e, dev),
+            _operand(sum, where, "sum", dt, e, dev), rstd, _operand(gamma, where, "gamma", dt, self.desc.width, dev),
+            _operand(dx, where, "dx", dt, e, dev), _operand(dgamma, where, "dgamma", t.float32, self.desc.width, dev),
+            1 if overwrite else 0, ws, size, t.raw_stream(dev) if stream is None else _stream(stream))
+        if rc:
+            _check(rc, where)
+
+
+MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)   # K. Jordan et al., 2024
+
+
+def make_ortho_desc(rows, cols, batch=1, steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7, dtype=MLPBLK_FP32) -> OrthoDesc:
+    """coefficients: (a, b, c) of every step, or one such triple for each step."""
+    d = OrthoDesc(int(rows), int(cols), int(batch), _dtype_code(dtype), int(steps), float(eps))
+    each = list(coefficients)
+    if each and not hasattr(each[0], "__len__"):
+        each = [tuple(each)] * max(d.steps, 0)
+    if len(each) != d.steps or d.steps > MLPBLK_ORTHO_MAX_STEPS or any(len(e) != 3 for e in each):
+        raise MlpBlkError(MLPBLK_EINVAL, f"{len(each)} triples of coefficients for {steps} steps (at most {MLPBLK_ORTHO_MAX_STEPS})")
+    for i, e in enumerate(each):
+        for j in range(3):
+            d.coefficients[i][j] = float(e[j])
+    return d
+
+
+def mlpblk_orthogonalize_workspace_size(desc: OrthoDesc) -> int:
+    return int(lib.mlpblk_orthogonalize_workspace_size(ctypes.byref(desc)))
+
+
+def mlpblk_orthogonalize(desc, u, o, workspace, stream=None):
+    where = "mlpblk_orthogonalize"
+    t = _Torch.get()
+    dev, n = t.device(), desc.rows * desc.cols * desc.batch
+    rc = lib.mlpblk_orthogonalize(
+        ctypes.byref(desc), _operand(u, where, "u", t.row.get(desc.dtype), n, dev), _operand(o, where, "o", t.bfloat16, n, dev),
+        _operand(workspace, where, "workspace", t.uint8, 0, dev), 0 if workspace is None else workspace.numel(), _stream(stream))
+    _check(rc, where)
+
+
+def mlpblk_muon_step(desc, hp, master, weight, grad, momentum, workspace, grad_scale=None, stream=None):
+    where = "mlpblk_muon_step"
+    t = _Torch.get()
+    dev, n, f32 = t.device(), desc.rows * desc.cols * desc.batch, t.float32
+    rc = lib.mlpblk_muon_step(
+        ctypes.byref(desc), ctypes.byref(hp), _operand(master, where, "master", f32, n, dev),
+        _operand(weight, where, "weight", t.row.get(desc.dtype), n, dev), _operand(grad, where, "grad", f32, n, dev),
+        _operand(momentum, where, "momentum", f32, n, dev), _operand(grad_scale, where, "grad_scale", f32, 1, dev),
+        _operand(workspace, where, "workspace", t.uint8, 0, dev), 0 if workspace is None else workspace.numel(), _stream(stream))
+    _check(rc, where)
+
+
+class Orthogonalizer(_Kept):
+    """Orthogonalised updates of `batch` matrices [rows, cols], and the scratch they need:
+    `orthogonalize` gives the update itself, `muon_step` takes the whole optimizer step on
+    float32 masters.  One workspace serves every weight of a shape in turn."""
+
+    def __init__(self, rows, cols, batch=1, steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7, dtype="f32", device="cuda"):
+        import torch
+        self.desc = make_ortho_desc(rows, cols, batch, steps, coefficients, eps, dtype)
+        size = mlpblk_orthogonalize_workspace_size(self.desc)
+        if size == 0:
+            raise MlpBlkError(MLPBLK_EINVAL, "mlpblk_orthogonalize_workspace_size")
+        self._ws = torch.empty(size, dtype=torch.uint8, device=device)
+        self._dev = self._ws.get_device()
+        self._d = ctypes.addressof(self.desc)
+        self._at = (self._ws.data_ptr(), size)
+        self._n = rows * cols * batch
+        self._t = _Torch.get()
+
+    def orthogonalize(self, u, o, stream=None):
+        """o (bfloat16) from u, in the descriptor's dtype; both [batch, rows, cols]."""
+        where = "Orthogonalizer.orthogonalize"
+        t = self._t
+        dev = t.device()
+        if dev != self._dev:
+            self._where(dev, where)
+        ws, size = self._at
+        rc = _calls.orthogonalize(self._d, _operand(u, where, "u", t.row[self.desc.dtype], self._n, dev),
+                                  _operand(o, where, "o", t.bfloat16, self._n, dev), ws, size,
+                                  t.raw_stream(dev) if stream is None else _stream(stream))
+        if rc:
+            _check(rc, where)
+
+    def muon_step(self, master, grad, momentum, lr, beta=0.95, weight_decay=0.0, scale=1.0, nesterov=True, weight=None,
+                  grad_scale=None, stream=None):
+        """One update of master and momentum (float32); weight: a working copy in the
+        descriptor's dtype; grad_scale: a device scalar."""
+        dev = self._t.device()
+        if dev != self._dev:
+            self._where(dev, "Orthogonalizer.muon_step")
+        mlpblk_muon_step(self.desc, Muon(lr, beta, weight_decay, scale, int(bool(nesterov))), master, weight, grad, momentum,
+                         self._ws, grad_scale, stream)
 
 
 def mlpblk_zero_grads(desc, dgamma, dw1, dw2, stream=None):

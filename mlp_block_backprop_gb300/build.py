@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "libmlpblk.so")
 # csrc/pycalls.c: CPython entry to the latency-bound calls, for this interpreter alone
 CALLS = os.path.join(HERE, "_mlpblk_calls" + importlib.machinery.EXTENSION_SUFFIXES[0])
 SOURCES = ["api.cu", "gemm_fwd.cu", "gemm_bwd.cu", "rowops.cu", "simt_f32.cu", "noalloc.cu", "optim.cu", "fp8.cu", "gemm_f8.cu", "moe.cu",
-           "sort.cu", "fp4.cu", "gemm_f4.cu"]
+           "sort.cu", "fp4.cu", "gemm_f4.cu", "route.cu", "norm.cu", "ortho.cu", "gemm_ns.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v"]
 

@@ -17,6 +17,7 @@
 
 #include "fp4_layout.h"
 #include "mlpblk_internal.h"
+#include "ortho.h"
 
 namespace mlpblk {
 int launch_gemm_tc_fwd(int epi, int M, int N, int K, const void *A, const void *B, void *C0,
@@ -239,7 +240,7 @@ int traced(int kind, cudaStream_t s, F &&launch) {
 
 extern "C" {
 
-int mlpblk_version(void) { return 101; }
+int mlpblk_version(void) { return 102; }
 
 const char *mlpblk_strerror(int code) {
     switch (code) {
@@ -1579,6 +1580,276 @@ int mlpblk_fp4_product_kernel(const mlpblk_fp4_matmul_desc *desc, int form, int 
 
 extern "C" {
 
+// ------------------------------------------- the router, the residual norm, Muon
+
+namespace {
+
+constexpr int64_t kLim31 = static_cast<int64_t>(1) << 31;
+
+int check_route_desc(const mlpblk_route_desc *d) {
+    if (!d) return MLPBLK_EINVAL;
+    if (d->dtype != MLPBLK_BF16 && d->dtype != MLPBLK_FP32) return MLPBLK_ENOTSUP;
+    if (d->score != MLPBLK_ROUTE_SOFTMAX && d->score != MLPBLK_ROUTE_SIGMOID) return MLPBLK_ENOTSUP;
+    if (d->tokens < 0 || d->tokens >= kLim31 || d->experts < 1 || d->experts > 256 || d->top_k < 1 ||
+        d->top_k > MLPBLK_ROUTE_MAX_TOP_K)
+        return MLPBLK_EINVAL;
+    if (d->groups < 1 || d->groups > 64 || d->experts % d->groups != 0 || d->top_groups < 1 || d->top_groups > d->groups)
+        return MLPBLK_EINVAL;
+    if (d->top_k > d->top_groups * (d->experts / d->groups)) return MLPBLK_EINVAL;
+    if ((d->renorm != 0 && d->renorm != 1) || !isfinite(d->scale)) return MLPBLK_EINVAL;
+    return MLPBLK_OK;
+}
+
+int check_norm_desc(const mlpblk_norm_desc *d) {
+    if (!d) return MLPBLK_EINVAL;
+    if (d->dtype != MLPBLK_BF16 && d->dtype != MLPBLK_FP32) return MLPBLK_ENOTSUP;
+    if (d->tokens < 0 || d->tokens >= kLim31 || d->width < 1) return MLPBLK_EINVAL;
+    if (d->width > kNormMaxWidth) return MLPBLK_ENOTSUP;
+    if (!(d->eps >= 0.0f) || !isfinite(d->eps)) return MLPBLK_EINVAL;
+    if (d->block != 0 && d->block != 128) return MLPBLK_ENOTSUP;
+    return MLPBLK_OK;
+}
+
+int check_ortho_desc(const mlpblk_ortho_desc *d) {
+    if (!d) return MLPBLK_EINVAL;
+    if (d->dtype != MLPBLK_BF16 && d->dtype != MLPBLK_FP32) return MLPBLK_ENOTSUP;
+    if (d->rows < 1 || d->cols < 1 || d->rows > 131072 || d->cols > 131072 || d->batch < 1 || d->batch > 65535) return MLPBLK_EINVAL;
+    if (d->rows * d->cols >= (static_cast<int64_t>(1) << 40) / d->batch) return MLPBLK_EINVAL;
+    if (d->steps < 1 || d->steps > MLPBLK_ORTHO_MAX_STEPS || !(d->eps >= 0.0f) || !isfinite(d->eps)) return MLPBLK_EINVAL;
+    // (128-column tiles of the update: their count is an int)
+    if ((d->rows + 127) / 128 * ((d->cols + 127) / 128) * d->batch >= kLim31) return MLPBLK_EINVAL;
+    for (int i = 0; i < d->steps; ++i)
+        for (int j = 0; j < 3; ++j)
+            if (!isfinite(d->coefficients[i][j])) return MLPBLK_EINVAL;
+    return MLPBLK_OK;
+}
+
+// Workspace of an orthogonalisation: X twice (a step reads one and writes the other), its
+// low parts, G and P, P's diagonal's remainders, the norm's partial sums.
+struct OrthoLayout {
+    int64_t x[2], lo, g, p, diag, partial, total;
+};
+OrthoLayout ortho_layout(const mlpblk_ortho_desc *d) {
+    OrthoLayout l = {};
+    int64_t off = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t at = off;
+        off += align256(bytes);
+        return at;
+    };
+    const int64_t m = d->rows < d->cols ? d->rows : d->cols;
+    const int64_t x = d->rows * ortho_pitch(d->cols) * d->batch * 2, g = m * ortho_pitch(m) * d->batch * 2;
+    l.x[0] = take(x);
+    l.x[1] = take(x);
+    l.lo = take(x);
+    l.g = take(g);
+    l.p = take(g);
+    l.diag = take(m * d->batch * 4);
+    l.partial = take((d->batch > kOrthoNormParts ? d->batch : kOrthoNormParts) * static_cast<int64_t>(8));
+    l.total = off;
+    return l;
+}
+
+// The steps on `u`; the last X goes to o as bf16, or stays in the workspace (*x_out, times
+// *sx_out) where o is NULL.
+int orthogonalize_impl(const mlpblk_ortho_desc *d, const OrthoSource &u, void *o, void *workspace, const __half **x_out,
+                       float *sx_out, int sms, cudaStream_t s) {
+    const OrthoLayout l = ortho_layout(d);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    __half *x[2] = {reinterpret_cast<__half *>(ws + l.x[0]), reinterpret_cast<__half *>(ws + l.x[1])};
+    __half *lo = reinterpret_cast<__half *>(ws + l.lo), *g = reinterpret_cast<__half *>(ws + l.g), *p = reinterpret_cast<__half *>(ws + l.p);
+    float *diag = reinterpret_cast<float *>(ws + l.diag);
+    double *partial = reinterpret_cast<double *>(ws + l.partial);
+    const bool tall = d->rows > d->cols;
+    const int64_t n = tall ? d->rows : d->cols;
+    // X is kept times a power of two near sqrt(n): an orthogonal matrix's entries are near 1 then
+    const float sx = exp2f(roundf(0.5f * log2f(static_cast<float>(n))));
+    int parts = 0;
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_ORTHO_NORM, s, launch_ortho_norm(u, d->rows * d->cols, d->batch, partial, &parts, sms, s));
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_ORTHO_SCALE, s,
+                  launch_ortho_scale(u, d->rows, d->cols, d->batch, partial, parts, d->eps, sx, x[0], d->steps > 1 ? lo : nullptr, sms, s));
+    for (int i = 0; i < d->steps; ++i) {
+        const bool last = i + 1 == d->steps;
+        NsProduct q = {};
+        q.tall = tall;
+        q.rows = d->rows;
+        q.cols = d->cols;
+        q.batch = d->batch;
+        q.diag = diag;
+        q.a = d->coefficients[i][0];
+        q.b = d->coefficients[i][1];
+        q.c = d->coefficients[i][2];
+        q.op = kNsGram;
+        q.x = x[i & 1];
+        q.out = g;
+        q.alpha = 1.0f / (sx * sx);
+        MLPBLK_LAUNCH(MLPBLK_KERNEL_NS_GRAM, s, launch_ns_product(q, sms, s));
+        q.op = kNsSquare;
+        q.g = g;
+        q.out = p;
+        MLPBLK_LAUNCH(MLPBLK_KERNEL_NS_SQUARE, s, launch_ns_product(q, sms, s));
+        q.op = kNsUpdate;
+        q.g = p;
+        q.x_lo = i + 1 < d->steps ? lo : nullptr;
+        q.out = x[(i + 1) & 1];
+        q.out_lo = i + 2 < d->steps ? lo : nullptr;
+        q.o = last ? o : nullptr;
+        q.alpha = 1.0f / sx;
+        MLPBLK_LAUNCH(MLPBLK_KERNEL_NS_UPDATE, s, launch_ns_product(q, sms, s));
+    }
+    *x_out = x[d->steps & 1];
+    *sx_out = sx;
+    return MLPBLK_OK;
+}
+
+}  // namespace
+
+int mlpblk_moe_route(const mlpblk_route_desc *desc, const void *logits, const float *bias, int32_t *expert_idx,
+                     float *routing_weights, void *stream) {
+    MLPBLK_TRY(check_route_desc(desc));
+    if (desc->tokens == 0) return MLPBLK_OK;
+    if (!aligned16(logits) || !aligned16(expert_idx) || !aligned16(routing_weights) || (bias && !aligned16(bias))) return MLPBLK_EINVAL;
+    const int64_t n = desc->tokens * desc->top_k, row = desc->experts * element_bytes(desc->dtype);
+    if (!apart({Span(expert_idx, n, 4), Span(routing_weights, n, 4)}, {Span(logits, desc->tokens, row), Span(bias, desc->experts, 4)}))
+        return MLPBLK_EINVAL;
+    int sms = 0;
+    MLPBLK_TRY(device_sms(&sms));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_ROUTE, s, launch_route(*desc, logits, bias, expert_idx, routing_weights, s));
+    return MLPBLK_OK;
+}
+
+int mlpblk_moe_route_backward(const mlpblk_route_desc *desc, const void *logits, const int32_t *expert_idx,
+                              const float *d_routing_weights, void *d_logits, void *stream) {
+    MLPBLK_TRY(check_route_desc(desc));
+    if (desc->tokens == 0) return MLPBLK_OK;
+    if (!aligned16(logits) || !aligned16(expert_idx) || !aligned16(d_routing_weights) || !aligned16(d_logits)) return MLPBLK_EINVAL;
+    const int64_t n = desc->tokens * desc->top_k, row = desc->experts * element_bytes(desc->dtype);
+    if (!apart({Span(d_logits, desc->tokens, row)},
+               {Span(logits, desc->tokens, row), Span(expert_idx, n, 4), Span(d_routing_weights, n, 4)}))
+        return MLPBLK_EINVAL;
+    int sms = 0;
+    MLPBLK_TRY(device_sms(&sms));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_ROUTE_BWD, s, launch_route_bwd(*desc, logits, expert_idx, d_routing_weights, d_logits, s));
+    return MLPBLK_OK;
+}
+
+int mlpblk_add_rmsnorm(const mlpblk_norm_desc *desc, const void *x, const void *residual, const void *gamma,
+                       void *sum, void *n, void *codes, float *scales, float *rstd, void *stream) {
+    MLPBLK_TRY(check_norm_desc(desc));
+    if (desc->tokens == 0) return MLPBLK_OK;
+    if ((residual == nullptr) != (sum == nullptr) || (codes == nullptr) != (scales == nullptr) || (!n && !codes)) return MLPBLK_EINVAL;
+    if (!aligned16(x) || !aligned16(gamma)) return MLPBLK_EINVAL;
+    for (const void *p : {residual, static_cast<const void *>(sum), static_cast<const void *>(n), static_cast<const void *>(codes),
+                          static_cast<const void *>(scales), static_cast<const void *>(rstd)})
+        if (p && !aligned16(p)) return MLPBLK_EINVAL;
+    const int64_t T = desc->tokens, e = element_bytes(desc->dtype), row = desc->width * e;
+    const int64_t per = desc->block ? (desc->width + 127) / 128 : 1;
+    if (!apart({Span(sum, T, row), Span(n, T, row), Span(codes, T, desc->width), Span(scales, T * per, 4), Span(rstd, T, 4)},
+               {Span(x == sum ? nullptr : x, T, row), Span(residual == sum ? nullptr : residual, T, row), Span(gamma, desc->width, e)}))
+        return MLPBLK_EINVAL;
+    int sms = 0;
+    MLPBLK_TRY(device_sms(&sms));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_ADD_NORM, s,
+                  launch_add_rmsnorm(*desc, x, residual, gamma, sum, n, static_cast<uint8_t *>(codes), scales, rstd, sms, s));
+    return MLPBLK_OK;
+}
+
+size_t mlpblk_add_rmsnorm_workspace_size(const mlpblk_norm_desc *desc) {
+    if (check_norm_desc(desc) != MLPBLK_OK) return 0;
+    int64_t parts = desc->tokens < kNormMaxParts ? desc->tokens : kNormMaxParts;
+    if (parts < 1) parts = 1;
+    return static_cast<size_t>(parts * norm_part_pitch(desc->width) * 4);
+}
+
+int mlpblk_add_rmsnorm_backward(const mlpblk_norm_desc *desc, const void *dn, const void *d_sum, const void *sum,
+                                const float *rstd, const void *gamma, void *dx, float *dgamma, int32_t overwrite,
+                                void *workspace, size_t workspace_bytes, void *stream) {
+    MLPBLK_TRY(check_norm_desc(desc));
+    if ((overwrite != 0 && overwrite != 1) || !aligned16(dgamma)) return MLPBLK_EINVAL;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int sms = 0;
+    if (desc->tokens == 0) {
+        if (!overwrite) return MLPBLK_OK;
+        MLPBLK_TRY(device_sms(&sms));
+        MLPBLK_LAUNCH(MLPBLK_KERNEL_ADD_NORM_DG, s, launch_norm_dgamma(nullptr, 0, desc->width, dgamma, 1, s));
+        return MLPBLK_OK;
+    }
+    if (!aligned16(dn) || !aligned16(sum) || !aligned16(rstd) || !aligned16(gamma) || !aligned16(dx) || !aligned16(workspace) ||
+        (d_sum && !aligned16(d_sum)))
+        return MLPBLK_EINVAL;
+    const size_t need = mlpblk_add_rmsnorm_workspace_size(desc);
+    if (workspace_bytes < need) return MLPBLK_EWORKSPACE;
+    const int64_t T = desc->tokens, e = element_bytes(desc->dtype), row = desc->width * e;
+    if (!apart({Span(dx, T, row), Span(dgamma, desc->width, 4), Span(workspace, static_cast<int64_t>(need), 1)},
+               {Span(dn == dx ? nullptr : dn, T, row), Span(d_sum == dx ? nullptr : d_sum, T, row), Span(sum, T, row), Span(rstd, T, 4),
+                Span(gamma, desc->width, e)}))
+        return MLPBLK_EINVAL;
+    MLPBLK_TRY(device_sms(&sms));
+    float *part = static_cast<float *>(workspace);
+    int parts = 0;
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_ADD_NORM_BWD, s, launch_add_rmsnorm_bwd(*desc, dn, d_sum, sum, rstd, gamma, dx, part, &parts, sms, s));
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_ADD_NORM_DG, s, launch_norm_dgamma(part, parts, desc->width, dgamma, overwrite, s));
+    return MLPBLK_OK;
+}
+
+size_t mlpblk_orthogonalize_workspace_size(const mlpblk_ortho_desc *desc) {
+    if (check_ortho_desc(desc) != MLPBLK_OK) return 0;
+    return static_cast<size_t>(ortho_layout(desc).total);
+}
+
+int mlpblk_orthogonalize(const mlpblk_ortho_desc *desc, const void *u, void *o, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+    MLPBLK_TRY(check_ortho_desc(desc));
+    if (!aligned16(u) || !aligned16(o) || !aligned16(workspace)) return MLPBLK_EINVAL;
+    const int64_t need = ortho_layout(desc).total, n = desc->rows * desc->cols * desc->batch;
+    if (workspace_bytes < static_cast<size_t>(need)) return MLPBLK_EWORKSPACE;
+    if (!apart({Span(o, n, 2), Span(workspace, need, 1)}, {Span(u, n, element_bytes(desc->dtype))})) return MLPBLK_EINVAL;
+    int sms = 0;
+    MLPBLK_TRY(device_sms(&sms));
+    OrthoSource src = {};
+    src.u = u;
+    src.dtype = desc->dtype;
+    const __half *x;
+    float sx;
+    return orthogonalize_impl(desc, src, o, workspace, &x, &sx, sms, static_cast<cudaStream_t>(stream));
+}
+
+int mlpblk_muon_step(const mlpblk_ortho_desc *desc, const mlpblk_muon *hp, float *master, void *weight,
+                     const float *grad, float *momentum, const float *grad_scale, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+    MLPBLK_TRY(check_ortho_desc(desc));
+    if (!hp || !isfinite(hp->lr) || !isfinite(hp->weight_decay) || !isfinite(hp->scale) || !(hp->lr >= 0.0f) ||
+        !(hp->weight_decay >= 0.0f) || !(hp->momentum >= 0.0f && hp->momentum < 1.0f) || (hp->nesterov != 0 && hp->nesterov != 1))
+        return MLPBLK_EINVAL;
+    if (!aligned16(master) || !aligned16(grad) || !aligned16(momentum) || !aligned16(workspace) || (weight && !aligned16(weight)) ||
+        (grad_scale && (reinterpret_cast<uintptr_t>(grad_scale) & 3u)))
+        return MLPBLK_EINVAL;
+    const int64_t need = ortho_layout(desc).total, n = desc->rows * desc->cols * desc->batch;
+    if (workspace_bytes < static_cast<size_t>(need)) return MLPBLK_EWORKSPACE;
+    if (!apart({Span(master, n, 4), Span(momentum, n, 4), Span(weight, n, element_bytes(desc->dtype)), Span(workspace, need, 1)},
+               {Span(grad, n, 4), Span(grad_scale, 1, 4)}))
+        return MLPBLK_EINVAL;
+    int sms = 0;
+    MLPBLK_TRY(device_sms(&sms));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    OrthoSource src = {};
+    src.momentum = momentum;
+    src.grad = grad;
+    src.grad_scale = grad_scale;
+    src.beta = hp->momentum;
+    src.nesterov = hp->nesterov;
+    const __half *x;
+    float sx;
+    MLPBLK_TRY(orthogonalize_impl(desc, src, nullptr, workspace, &x, &sx, sms, s));
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_MUON_APPLY, s,
+                  launch_muon_apply(x, desc->rows, desc->cols, desc->batch, 1.0f - hp->lr * hp->weight_decay, hp->lr * hp->scale / sx,
+                                    master, weight, desc->dtype, sms, s));
+    return MLPBLK_OK;
+}
+
 int mlpblk_moe_backward(const mlpblk_moe_desc *desc, const void *dy, const void *x, const void *gamma,
                         const void *w1s, const void *w2s, const float *routing_weights, const void *saved, void *dx,
                         float *d_routing_weights, float *dgamma, float *dw1s, float *dw2s, void *workspace,
@@ -1655,7 +1926,9 @@ int mlpblk_last_error(void) {
     const int b = take_device_error_gemm_bwd();
     const int c = take_device_error_gemm_f8();
     const int f = take_device_error_gemm_f4();
+    const int n = take_device_error_gemm_ns();
     const int r = take_device_error_rowops();
+    if (n != MLPBLK_OK && a == MLPBLK_OK && b == MLPBLK_OK && c == MLPBLK_OK && f == MLPBLK_OK) return n;
     return a != MLPBLK_OK ? a : (b != MLPBLK_OK ? b : (c != MLPBLK_OK ? c : (f != MLPBLK_OK ? f : r)));
 }
 

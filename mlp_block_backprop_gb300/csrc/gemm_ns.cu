@@ -1,0 +1,867 @@
+// gemm_ns.cu -- the products of a Newton-Schulz step on the tensor cores (tcgen05.mma
+// kind::f16: fp16 operands, fp32 accumulator in TMEM):
+//
+//   G  = X X^T  (X wide)  or  X^T X  (X tall)
+//   P  = b G + c G G
+//   X' = a X + P X        or  a X + X P
+//
+// Nothing is transposed in memory: each operand is read K-major or MN-major as it lies,
+// and a tall X is worked on from its right.  G and P are symmetric: only tiles on and
+// above the diagonal are computed, the others are written as their mirror images.
+//
+// fp16, not bf16: the tensor cores run both at the same rate, and the values' range is
+// known (X's singular values stay below about 1.2, so X is kept times sqrt of its long
+// side, entries near 1; G and P, whose errors count against the identity's 1, as they are).
+// Rounding is 2^-11 instead of 2^-8, which the polynomial amplifies: on momentum with a few
+// strong directions the bf16 form is off by 1e-2 to 1e-1, this one by 1e-3 to 2e-3.  Two places get
+// more than fp16:
+//   - a X, which carries a weak direction (amplified by a = 3.4 a step) unchanged, takes X
+//     as the sum of two fp16 values in all but the last step;
+//   - P's diagonal, next to which its other entries are small, leaves what its rounding took
+//     in float32 (`diag`), and the update adds it to a.
+//
+// ns_small: one CTA, 128 x 128 tiles; K can be split over a cluster whose parts meet in
+//   distributed shared memory in rank order.
+// ns_pair: two CTAs on two SMs, 256 x 256 tiles (cta_group::2).
+// Bound by the tensor cores at large sizes, by launches and K's latency at small ones.
+#include <type_traits>
+
+#include "gemm_tc.cuh"
+#include "ortho.h"
+
+namespace mlpblk {
+
+namespace {
+
+constexpr int kNsK = 64;                // K values of a stage: 128 bytes
+
+struct NsArgs {
+    int op;
+    int rows, cols;                     // of D
+    int mt, nt;                         // tiles
+    int per;                            // tiles of one matrix (on and above the diagonal, or all)
+    int tiles;                          // of the batch
+    int kblocks;
+    int group_m;
+    int pitch;                          // elements of a row of out, aux
+    int64_t matrix;                     // elements of a matrix of out, aux
+    const __half *aux, *aux_lo;         // [rows][cols]: G (kNsSquare) or X (kNsUpdate)
+    float *diag;                        // [batch][diag_n]
+    int diag_n;
+    bool diag_col;                      // kNsUpdate: diag goes by column (tall)
+    __half *out, *out_lo;
+    uint16_t *o;                        // bf16 [batch][rows][cols]
+    float alpha, a, b, c;
+};
+
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn, bool b_mn) {
+    return (1u << 4)                                   // D format: f32 (A, B: f16 is code 0)
+           | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16)
+           | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// One lane of the warp, the same one each time: the issuing roles run their loops with the
+// whole warp, so that addresses and descriptors stay in uniform registers.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t p;
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  elect.sync _|p, 0xffffffff;\n"
+        "  selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
+__device__ __forceinline__ void mbar_expect_relaxed(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "  selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// mbar_wait for a barrier that other CTAs of the cluster arrive on.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (*abort) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            record_device_error(MLPBLK_ETIMEOUT);
+            return false;
+        }
+    }
+}
+
+// Before a producer leaves: waits (bounded) for the copies that it issued into the S stages,
+// the next of which would be `stage` in phase `phase`, so that none writes shared memory after
+// a run that gave up.
+__device__ __forceinline__ void await_copies(uint64_t *bars, int S, int stage, uint32_t phase) {
+    const uint64_t t0 = global_timer_ns();
+    for (int s = 0; s < S; ++s)
+        while (!mbar_try_wait(&bars[s], s < stage ? phase : phase ^ 1u) && global_timer_ns() - t0 <= kWaitLimitNs) {
+        }
+}
+
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void tma_load_4d(const CUtensorMap *map, uint64_t *bar, void *dst, int32_t c0, int32_t c1, int32_t c2,
+                                            int32_t c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d_pair(const CUtensorMap *map, uint32_t bar_cluster_addr, void *dst, int32_t c0,
+                                                 int32_t c1, int32_t c2, int32_t c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster_addr), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// ------------------------------------------------------------------- the work
+
+// One output tile: its matrix, origin, and whether its mirror image is written too.
+struct NsTile {
+    int batch, m0, n0;
+    bool mirror;
+};
+
+template <int TS, bool SYM>
+__device__ __forceinline__ NsTile ns_tile(const NsArgs &a, int t) {
+    NsTile w;
+    w.batch = t / a.per;
+    const int r = t - w.batch * a.per;
+    int mi, ni;
+    if (SYM) {
+        // column ni holds the tiles (0 .. ni, ni): ni (ni + 1) / 2 tiles lie before it
+        ni = static_cast<int>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
+        while (ni * (ni + 1) / 2 > r) --ni;
+        while ((ni + 1) * (ni + 2) / 2 <= r) ++ni;
+        mi = r - ni * (ni + 1) / 2;
+    } else {
+        raster_tile(r, a.mt, a.nt, a.group_m, mi, ni);
+    }
+    w.m0 = mi * TS;
+    w.n0 = ni * TS;
+    w.mirror = SYM && mi != ni;
+    return w;
+}
+
+// Loads of one operand's stage: 128 rows (or, MN-major, columns) from `row` on, K block kb.
+template <bool MN>
+__device__ __forceinline__ void load_operand(const CUtensorMap *map, uint64_t *bar, void *dst, int kb, int row, int batch) {
+    if (MN) tma_load_4d(map, bar, dst, 0, kb * kNsK, row / 64, batch);
+    else tma_load_3d(map, bar, dst, kb * kNsK, row, batch);
+}
+template <bool MN>
+__device__ __forceinline__ void load_operand_pair(const CUtensorMap *map, uint32_t bar, void *dst, int kb, int row, int batch) {
+    if (MN) tma_load_4d_pair(map, bar, dst, 0, kb * kNsK, row / 64, batch);
+    else tma_load_3d_pair(map, bar, dst, kb * kNsK, row, batch);
+}
+
+// Descriptor of an operand's stage, and its step for the next 16 values of K.
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(const void *s) {
+    return MN ? smem_desc_sw128(smem_u32(s), 64 * 128, 1024) : smem_desc_sw128(smem_u32(s), 16, 1024);
+}
+template <bool MN>
+constexpr uint64_t kOperandStep = MN ? (16 * 128) >> 4 : 32 >> 4;
+
+// ---------------------------------------------------------------- the epilogue
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+
+// What the epilogue of a row's CH columns reads besides the accumulator, loaded ahead of it.
+template <int OP, int CH>
+struct NsAux {
+    uint4 hi[OP == kNsGram ? 1 : CH / 8], lo[OP == kNsUpdate ? CH / 8 : 1];
+    float d;           // the row's diag (kNsUpdate, wide)
+};
+
+template <int OP, int CH>
+__device__ __forceinline__ void ns_load_aux(const NsArgs &a, const NsTile &w, int row, int col, NsAux<OP, CH> &x) {
+    if (OP == kNsGram) return;
+    const bool on = row < a.rows && col < a.cols;
+    const int64_t at = w.batch * a.matrix + static_cast<int64_t>(row) * a.pitch + col;
+#pragma unroll
+    for (int i = 0; i < CH / 8; ++i) {
+        x.hi[i] = on ? *reinterpret_cast<const uint4 *>(a.aux + at + 8 * i) : make_uint4(0, 0, 0, 0);
+        if (OP == kNsUpdate) x.lo[i] = on && a.aux_lo ? *reinterpret_cast<const uint4 *>(a.aux_lo + at + 8 * i) : make_uint4(0, 0, 0, 0);
+    }
+    if (OP == kNsUpdate) x.d = on && !a.diag_col ? a.diag[static_cast<int64_t>(w.batch) * a.diag_n + row] : 0.0f;
+}
+
+// CH columns from `col` on of the lane's row: the step's arithmetic and the stores.  The
+// whole warp calls it (the mirror image pairs neighbouring rows).  Columns up to the pitch
+// may be written: pads are nobody's.
+template <int OP, int CH>
+__device__ __forceinline__ void ns_finish(const NsArgs &a, const NsTile &w, int row, int col, const NsAux<OP, CH> &x, float (&v)[CH]) {
+    if (col >= a.cols) return;
+    const bool on = row < a.rows;
+    const int64_t at = w.batch * a.matrix + static_cast<int64_t>(row) * a.pitch + col;
+    if (OP == kNsGram) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) v[i] *= a.alpha;
+    } else {
+        const uint32_t *h = reinterpret_cast<const uint32_t *>(x.hi);
+        const uint32_t *l = reinterpret_cast<const uint32_t *>(x.lo);
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i) {
+            float2 p = unpack_half2(h[i]);
+            if (OP == kNsSquare) {
+                v[2 * i] = a.b * p.x + a.c * v[2 * i];
+                v[2 * i + 1] = a.b * p.y + a.c * v[2 * i + 1];
+            } else {
+                const float2 q = unpack_half2(l[i]);
+                float d0 = x.d, d1 = x.d;
+                if (a.diag_col) {
+                    const float *d = a.diag + static_cast<int64_t>(w.batch) * a.diag_n;
+                    d0 = col + 2 * i < a.cols ? __ldg(d + col + 2 * i) : 0.0f;
+                    d1 = col + 2 * i + 1 < a.cols ? __ldg(d + col + 2 * i + 1) : 0.0f;
+                }
+                v[2 * i] = (a.a + d0) * (p.x + q.x) + v[2 * i];
+                v[2 * i + 1] = (a.a + d1) * (p.y + q.y) + v[2 * i + 1];
+            }
+        }
+    }
+    if (OP == kNsUpdate && a.o) {
+        uint16_t *o = a.o + (static_cast<int64_t>(w.batch) * a.rows + row) * a.cols + col;
+        if (!on) return;
+        if (a.cols % 8 == 0) {
+#pragma unroll
+            for (int i = 0; i < CH / 8; ++i)
+                if (col + 8 * i < a.cols)
+                    *reinterpret_cast<uint4 *>(o + 8 * i) = make_uint4(
+                        pack_bf16x2(a.alpha * v[8 * i], a.alpha * v[8 * i + 1]), pack_bf16x2(a.alpha * v[8 * i + 2], a.alpha * v[8 * i + 3]),
+                        pack_bf16x2(a.alpha * v[8 * i + 4], a.alpha * v[8 * i + 5]), pack_bf16x2(a.alpha * v[8 * i + 6], a.alpha * v[8 * i + 7]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+                if (col + i < a.cols) o[i] = static_cast<uint16_t>(pack_bf16x2(a.alpha * v[i], 0.0f) & 0xFFFFu);
+        }
+        return;
+    }
+    uint32_t h[CH / 2];
+#pragma unroll
+    for (int i = 0; i < CH / 2; ++i) h[i] = pack_half2(v[2 * i], v[2 * i + 1]);
+    if (on) {
+#pragma unroll
+        for (int i = 0; i < CH / 8; ++i) *reinterpret_cast<uint4 *>(a.out + at + 8 * i) = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+        if (OP == kNsUpdate && a.out_lo) {
+            uint32_t l[CH / 2];
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) {
+                const float2 p = unpack_half2(h[i]);
+                l[i] = pack_half2(v[2 * i] - p.x, v[2 * i + 1] - p.y);
+            }
+#pragma unroll
+            for (int i = 0; i < CH / 8; ++i) *reinterpret_cast<uint4 *>(a.out_lo + at + 8 * i) = make_uint4(l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]);
+        }
+        if (OP == kNsSquare && row >= col && row < col + CH) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const float2 p = unpack_half2(h[i / 2]);
+                if (col + i == row) a.diag[static_cast<int64_t>(w.batch) * a.diag_n + row] = v[i] - (i & 1 ? p.y : p.x);
+            }
+        }
+    }
+    if (OP != kNsUpdate && w.mirror) {
+        // out[col + i][row]: lanes are neighbouring columns of the image; two lanes swap every
+        // other value, so that a store is a pair (rows behind a.rows are pads of the image's rows)
+        const int odd = row & 1;
+        __half *q = a.out + w.batch * a.matrix + static_cast<int64_t>(col + odd) * a.pitch + (row - odd);
+#pragma unroll
+        for (int i = 0; i < CH; i += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+            const uint32_t u = odd ? pack_half2(got, v[i + 1]) : pack_half2(v[i], got);
+            if (row - odd < a.rows && col + i + odd < a.cols) *reinterpret_cast<uint32_t *>(q) = u;
+            q += 2 * a.pitch;
+        }
+    }
+}
+
+// ------------------------------------------------------------------- ns_small
+
+template <bool SPLIT_>
+struct NsSmall {
+    static constexpr bool SPLIT = SPLIT_;
+    static constexpr int kEpiWarps = 8;             // two a lane quarter: 64 columns each
+    static constexpr int kThreads = 64 + 32 * kEpiWarps;
+    static constexpr int kOpBytes = 128 * 128;
+    static constexpr int kStageBytes = 2 * kOpBytes;
+    static constexpr int kDumpBytes = SPLIT ? 128 * 128 * 4 : 0;   // this CTA's part of the tile
+    static constexpr int kCtrlBytes = 1024;
+    static constexpr int kStages = (kSmemLimit - 1024 - kCtrlBytes - kDumpBytes) / kStageBytes;
+    static constexpr int kSmemBytes = 1024 + kCtrlBytes + kDumpBytes + kStages * kStageBytes;
+    static_assert(kStages >= 4, "pipeline");
+};
+
+template <class C, int OP, bool AMN, bool BMN>
+__global__ void __launch_bounds__(C::kThreads, 1)
+ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const NsArgs args) {
+    constexpr bool SYM = OP != kNsUpdate;
+    constexpr int S = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *a_s = smem, *b_s = a_s + S * C::kOpBytes;
+    float *dump = reinterpret_cast<float *>(b_s + S * C::kOpBytes);   // [column][row]
+    uint8_t *ctrl = reinterpret_cast<uint8_t *>(dump) + C::kDumpBytes;
+    uint64_t *full_bar = reinterpret_cast<uint64_t *>(ctrl);
+    uint64_t *empty_bar = full_bar + S;
+    uint64_t *accf_bar = empty_bar + S;
+    uint64_t *acce_bar = accf_bar + 2;
+    uint64_t *part_full = acce_bar + 2;   // every CTA of the cluster has its part in `dump`
+    uint64_t *part_empty = part_full + 1; // every CTA has read this CTA's part
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctrl + 512);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 516);
+
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int cs = C::SPLIT ? static_cast<int>(cluster_nctarank()) : 1;
+    const int rank = C::SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+    const int worker = static_cast<int>(blockIdx.x) / cs, workers = static_cast<int>(gridDim.x) / cs;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full_bar[s], 1);
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&accf_bar[b], 1);
+            mbar_init(&acce_bar[b], C::kEpiWarps);
+        }
+        mbar_init(part_full, cs);
+        mbar_init(part_empty, cs);
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 256);
+        tmem_relinquish_alloc_permit();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (cs > 1) cluster_sync();  // the peers' barriers exist before anyone arrives on them
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    griddep_launch_dependents();
+    int t = worker;
+    NsTile w = {};
+    if (t < args.tiles) w = ns_tile<128, SYM>(args, t);
+    auto next = [&]() {
+        t += workers;
+        if (t < args.tiles) w = ns_tile<128, SYM>(args, t);
+    };
+    const int k0 = args.kblocks * rank / cs, k1 = args.kblocks * (rank + 1) / cs;
+    griddep_wait();
+
+    if (warp == 0) {
+        const bool issue = elect_lane();
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (; ok && t < args.tiles; next()) {
+            for (int kb = k0; kb < k1; ++kb) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag));
+                if (!ok) break;
+                if (issue) {
+                    mbar_expect_relaxed(&full_bar[stage], C::kStageBytes);
+                    load_operand<AMN>(&tmA, &full_bar[stage], a_s + stage * C::kOpBytes, kb, w.m0, w.batch);
+                    load_operand<BMN>(&tmB, &full_bar[stage], b_s + stage * C::kOpBytes, kb, w.n0, w.batch);
+                }
+                __syncwarp();
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        await_copies(full_bar, S, stage, phase);
+        __syncwarp();
+    } else if (warp == 1) {
+        const bool issue = elect_lane();
+        const uint64_t a0 = operand_desc<AMN>(a_s), b0 = operand_desc<BMN>(b_s);
+        int stage = 0, it = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (; ok && t < args.tiles; next(), ++it) {
+            const int buf = it & 1;
+            ok = __all_sync(0xffffffffu, mbar_wait(&acce_bar[buf], ((it >> 1) & 1) ^ 1u, abort_flag));
+            if (!ok) break;
+            tc_fence_after_sync();
+            for (int kb = k0; kb < k1; ++kb) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort_flag));
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint64_t ad = a0 + stage * (C::kOpBytes >> 4), bd = b0 + stage * (C::kOpBytes >> 4);
+                if (issue) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        umma_bf16(tmem_base + buf * 128, ad + j * kOperandStep<AMN>, bd + j * kOperandStep<BMN>,
+                                  idesc_f16_f32(128, 128, AMN, BMN), (kb > k0 || j > 0) ? 1u : 0u);
+                    umma_commit(&empty_bar[stage]);
+                }
+                __syncwarp();
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) break;
+            if (issue) umma_commit(&accf_bar[buf]);
+            __syncwarp();
+        }
+        __syncwarp();
+    } else {
+        // A warp that gave up on a wait keeps walking (its waits then return at once), so that
+        // the barriers of the cluster's sum stay in step.
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        const int i = 32 * q + lane;
+        constexpr int kEpiThreads = 32 * C::kEpiWarps;
+        int it = 0;
+        for (; t < args.tiles; next(), ++it) {
+            const int row = w.m0 + i;
+            const bool some = k1 > k0;
+            const int buf = it & 1;
+            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * 128;
+            bool ok;
+            if (!C::SPLIT) {
+                NsAux<OP, 32> x[2];
+                ns_load_aux<OP, 32>(args, w, row, w.n0 + 64 * half, x[0]);
+                ns_load_aux<OP, 32>(args, w, row, w.n0 + 64 * half + 32, x[1]);
+                ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort_flag));
+                tc_fence_after_sync();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v[32];
+                    tmem_load_32cols(t_row + 64 * half + 32 * c, v);
+                    if (c == 1) {
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_relaxed(&acce_bar[buf]);
+                    }
+                    if (ok) ns_finish<OP, 32>(args, w, row, w.n0 + 64 * half + 32 * c, x[c], v);
+                }
+            } else {
+                ok = mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort_flag);
+                tc_fence_after_sync();
+                ok = mbar_wait_cluster(part_empty, (it & 1) ^ 1u, abort_flag) && ok;
+                ok = __all_sync(0xffffffffu, ok);
+                for (int c0 = half * 64; c0 < half * 64 + 64; c0 += 32) {
+                    float v[32];
+                    if (some && ok) {
+                        tmem_load_32cols(t_row + c0, v);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) dump[(c0 + j) * 128 + i] = v[j];
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_relaxed(&acce_bar[buf]);
+                named_barrier_sync(1, kEpiThreads);
+                if (threadIdx.x >= 64 && threadIdx.x < 64 + cs)
+                    mbar_arrive_cluster(mapa_shared(smem_u32(part_full), threadIdx.x - 64));
+                // this CTA finishes the columns [128 rank / cs, 128 (rank + 1) / cs), 16 at a time
+                const int width = 128 / cs, first = rank * width;
+                constexpr int CH = 16;
+                NsAux<OP, CH> x;
+                if (half * CH < width) ns_load_aux<OP, CH>(args, w, row, w.n0 + first + half * CH, x);
+                ok = mbar_wait_cluster(part_full, it & 1, abort_flag) && ok;
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) {
+                    for (int c0 = half * CH; c0 < width; c0 += 2 * CH) {
+                        float sum[CH];
+#pragma unroll
+                        for (int u = 0; u < CH; ++u) sum[u] = 0.0f;
+                        for (int r = 0; r < cs; ++r) {
+                            const uint32_t from = mapa_shared(smem_u32(dump + (first + c0) * 128 + i), r);
+                            float part[CH];
+#pragma unroll
+                            for (int u = 0; u < CH; ++u) part[u] = ld_cluster_f32(from + u * 512);
+#pragma unroll
+                            for (int u = 0; u < CH; ++u) sum[u] += part[u];
+                        }
+                        if (c0 != half * CH) ns_load_aux<OP, CH>(args, w, row, w.n0 + first + c0, x);
+                        ns_finish<OP, CH>(args, w, row, w.n0 + first + c0, x, sum);
+                    }
+                }
+                named_barrier_sync(1, kEpiThreads);
+                if (threadIdx.x >= 64 && threadIdx.x < 64 + cs)
+                    mbar_arrive_cluster(mapa_shared(smem_u32(part_empty), threadIdx.x - 64));
+            }
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (cs > 1) cluster_sync();  // no CTA leaves while its part may be read
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem_base, 256);
+    }
+}
+
+// -------------------------------------------------------------------- ns_pair
+
+struct NsPair {
+    static constexpr int kThreads = 320;            // producer, MMA, eight epilogue warps
+    static constexpr int kOpBytes = 128 * 128;      // 128 rows of A or B a CTA
+    static constexpr int kStageBytes = 2 * kOpBytes;
+    static constexpr int kCtrlBytes = 1024;
+    static constexpr int kStages = (kSmemLimit - 1024 - kCtrlBytes) / kStageBytes;
+    static constexpr int kSmemBytes = 1024 + kCtrlBytes + kStages * kStageBytes;
+};
+
+template <int OP, bool AMN, bool BMN>
+__global__ void __launch_bounds__(NsPair::kThreads, 1)
+ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const NsArgs args) {
+    using P = NsPair;
+    constexpr bool SYM = OP != kNsUpdate;
+    constexpr int S = P::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *a_s = smem, *b_s = a_s + S * P::kOpBytes;
+    uint8_t *ctrl = b_s + S * P::kOpBytes;
+    uint64_t *full_bar = reinterpret_cast<uint64_t *>(ctrl);
+    uint64_t *empty_bar = full_bar + S;
+    uint64_t *accf_bar = empty_bar + S;
+    uint64_t *acce_bar = accf_bar + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctrl + 512);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 516);
+
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int worker = static_cast<int>(blockIdx.x >> 1), workers = static_cast<int>(gridDim.x >> 1);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full_bar[s], 1);   // the leader's collects both CTAs' bytes
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&accf_bar[b], 1);
+            mbar_init(&acce_bar[b], 16);  // both CTAs' epilogue warps (the leader's barrier counts)
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+    }
+    cluster_sync();
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_alloc_permit_pair();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    griddep_launch_dependents();
+    int t = worker;
+    NsTile w = {};
+    if (t < args.tiles) w = ns_tile<256, SYM>(args, t);
+    auto next = [&]() {
+        t += workers;
+        if (t < args.tiles) w = ns_tile<256, SYM>(args, t);
+    };
+    griddep_wait();
+
+    if (warp == 0) {
+        const bool issue = elect_lane();
+        const uint32_t full0 = mapa_shared(smem_u32(&full_bar[0]), 0);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (; ok && t < args.tiles; next()) {
+            const int ar = w.m0 + static_cast<int>(rank) * 128, br = w.n0 + static_cast<int>(rank) * 128;
+            for (int kb = 0; kb < args.kblocks; ++kb) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag));
+                if (!ok) break;
+                if (issue) {
+                    uint8_t *da = a_s + stage * P::kOpBytes, *db = b_s + stage * P::kOpBytes;
+                    if (leader) {
+                        mbar_expect_relaxed(&full_bar[stage], 2 * P::kStageBytes);
+                        load_operand<AMN>(&tmA, &full_bar[stage], da, kb, ar, w.batch);
+                        load_operand<BMN>(&tmB, &full_bar[stage], db, kb, br, w.batch);
+                    } else {
+                        load_operand_pair<AMN>(&tmA, full0 + stage * 8, da, kb, ar, w.batch);
+                        load_operand_pair<BMN>(&tmB, full0 + stage * 8, db, kb, br, w.batch);
+                    }
+                }
+                __syncwarp();
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // the leader's barriers collect the other CTA's operands too, which leaves no earlier
+        if (leader) await_copies(full_bar, S, stage, phase);
+        __syncwarp();
+    } else if (warp == 1) {
+        if (leader) {
+            const bool issue = elect_lane();
+            const uint64_t a0 = operand_desc<AMN>(a_s), b0 = operand_desc<BMN>(b_s);
+            int stage = 0, it = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (; ok && t < args.tiles; t += workers, ++it) {
+                const int buf = it & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait(&acce_bar[buf], ((it >> 1) & 1) ^ 1u, abort_flag));
+                if (!ok) break;
+                tc_fence_after_sync();
+                for (int kb = 0; kb < args.kblocks; ++kb) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint64_t ad = a0 + stage * (P::kOpBytes >> 4), bd = b0 + stage * (P::kOpBytes >> 4);
+                    if (issue) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            umma_bf16_pair(tmem_base + buf * 256, ad + j * kOperandStep<AMN>, bd + j * kOperandStep<BMN>,
+                                           idesc_f16_f32(256, 256, AMN, BMN), (kb > 0 || j > 0) ? 1u : 0u);
+                        umma_commit_pair(&empty_bar[stage], 3);
+                    }
+                    __syncwarp();
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (issue) umma_commit_pair(&accf_bar[buf], 3);
+                __syncwarp();
+            }
+        }
+        __syncwarp();
+    } else {
+        // two warps a lane quarter: 128 columns each, 32 at a time
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t acce0 = mapa_shared(smem_u32(&acce_bar[0]), 0);
+        int it = 0;
+        for (; t < args.tiles; next(), ++it) {
+            const int row = w.m0 + static_cast<int>(rank) * 128 + 32 * q + lane;
+            const int buf = it & 1;
+            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * 256 + 128 * half;
+            const int col = w.n0 + 128 * half;
+            NsAux<OP, 32> x[2];
+            ns_load_aux<OP, 32>(args, w, row, col, x[0]);
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (c < 3) ns_load_aux<OP, 32>(args, w, row, col + 32 * (c + 1), x[(c + 1) & 1]);
+                float v[32];
+                tmem_load_32cols(t_row + 32 * c, v);
+                if (c == 3) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (leader) mbar_arrive_relaxed(&acce_bar[buf]);
+                        else mbar_arrive_cluster_relaxed(acce0 + buf * 8);
+                    }
+                }
+                ns_finish<OP, 32>(args, w, row, col + 32 * c, x[c & 1], v);
+            }
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the pair's MMAs may touch it
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// ------------------------------------------------------------------------ host
+
+// A batch of fp16 matrices [rows][cols], rows of `pitch` elements.  K-major: boxes of 64
+// columns x 128 rows.  MN-major: K runs over the rows; a box is 64 rows of two blocks of 64
+// columns (the map's third dimension walks the blocks, up to the pitch).
+bool ns_map(CUtensorMap *m, const __half *p, bool mn, int64_t rows, int64_t cols, int64_t pitch, int batch) {
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint64_t R = static_cast<cuuint64_t>(rows), line = static_cast<cuuint64_t>(pitch) * 2, B = static_cast<cuuint64_t>(batch);
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    if (mn) {
+        cuuint64_t dims[4] = {64, R, static_cast<cuuint64_t>(pitch / 64), B};
+        cuuint64_t strides[3] = {line, 128, R * line};
+        cuuint32_t box[4] = {64, kNsK, 2, 1};
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<__half *>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    }
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), R, B};
+    cuuint64_t strides[2] = {line, R * line};
+    cuuint32_t box[3] = {kNsK, 128, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half *>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Cluster size 1: no cluster attribute.
+template <class K>
+int launch_ns(K kernel, int threads, int smem, int grid, int cluster, const CUtensorMap &mA, const CUtensorMap &mB, const NsArgs &a,
+              int *attr_set, cudaStream_t s) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return MLPBLK_ECUDA;
+    if (!attr_set[dev]) {
+        const int rc = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+        if (rc != MLPBLK_OK) return rc;
+        attr_set[dev] = 1;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, mA, mB, a));
+}
+
+int64_t tiles_of(const NsArgs &a, int ts, bool sym) {
+    const int64_t mt = (a.rows + ts - 1) / ts, nt = (a.cols + ts - 1) / ts;
+    return sym ? mt * (mt + 1) / 2 : mt * nt;
+}
+
+template <int OP, bool AMN, bool BMN>
+int run_ns(NsArgs a, const CUtensorMap &mA, const CUtensorMap &mB, int batch, int sms, cudaStream_t s) {
+    constexpr bool SYM = OP != kNsUpdate;
+    const int64_t pair_tiles = tiles_of(a, 256, SYM) * batch, tiles = tiles_of(a, 128, SYM) * batch;
+    const int pairs = sms / 2;
+    if (tiles > INT32_MAX) return MLPBLK_EINVAL;
+    if (pairs >= 1 && 2 * pair_tiles >= pairs && a.rows > 128 && a.cols > 128) {
+        static int attr_set[64] = {0};
+        a.mt = (a.rows + 255) / 256;
+        a.nt = (a.cols + 255) / 256;
+        a.per = static_cast<int>(pair_tiles / batch);
+        a.tiles = static_cast<int>(pair_tiles);
+        a.group_m = 8;
+        const int workers = a.tiles < pairs ? a.tiles : pairs;
+        return launch_ns(ns_pair_kernel<OP, AMN, BMN>, NsPair::kThreads, NsPair::kSmemBytes, 2 * workers, 2, mA, mB, a, attr_set, s);
+    }
+    a.mt = (a.rows + 127) / 128;
+    a.nt = (a.cols + 127) / 128;
+    a.per = static_cast<int>(tiles / batch);
+    a.tiles = static_cast<int>(tiles);
+    a.group_m = 8;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= sms && a.kblocks >= 4 * split) split *= 2;
+    int workers = sms / split;
+    if (workers < 1) workers = 1;
+    if (a.tiles < workers) workers = a.tiles;
+    if (split > 1) {
+        static int attr_set[64] = {0};
+        return launch_ns(ns_small_kernel<NsSmall<true>, OP, AMN, BMN>, NsSmall<true>::kThreads, NsSmall<true>::kSmemBytes, workers * split,
+                         split, mA, mB, a, attr_set, s);
+    }
+    static int attr_set[64] = {0};
+    return launch_ns(ns_small_kernel<NsSmall<false>, OP, AMN, BMN>, NsSmall<false>::kThreads, NsSmall<false>::kSmemBytes, workers, 1, mA, mB,
+                     a, attr_set, s);
+}
+
+}  // namespace
+
+int launch_ns_product(const NsProduct &p, int sms, cudaStream_t s) {
+    const int64_t m = p.tall ? p.cols : p.rows;   // the short side
+    const int64_t x_pitch = ortho_pitch(p.cols), g_pitch = ortho_pitch(m);
+    NsArgs a = {};
+    a.op = p.op;
+    a.alpha = p.alpha;
+    a.a = p.a;
+    a.b = p.b;
+    a.c = p.c;
+    a.diag = p.diag;
+    a.diag_n = static_cast<int>(m);
+    a.diag_col = p.tall;
+    a.out = p.out;
+    a.out_lo = p.out_lo;
+    a.o = static_cast<uint16_t *>(p.o);
+    CUtensorMap mA, mB;
+    if (p.op == kNsUpdate) {
+        a.rows = static_cast<int>(p.rows);
+        a.cols = static_cast<int>(p.cols);
+        a.pitch = static_cast<int>(x_pitch);
+        a.matrix = p.rows * x_pitch;
+        a.aux = p.x;
+        a.aux_lo = p.x_lo;
+        a.kblocks = static_cast<int>((m + kNsK - 1) / kNsK);
+        if (p.tall) {
+            if (!ns_map(&mA, p.x, false, p.rows, p.cols, x_pitch, p.batch) || !ns_map(&mB, p.g, false, m, m, g_pitch, p.batch)) return MLPBLK_ECUDA;
+            return run_ns<kNsUpdate, false, false>(a, mA, mB, p.batch, sms, s);
+        }
+        if (!ns_map(&mA, p.g, false, m, m, g_pitch, p.batch) || !ns_map(&mB, p.x, true, p.rows, p.cols, x_pitch, p.batch)) return MLPBLK_ECUDA;
+        return run_ns<kNsUpdate, false, true>(a, mA, mB, p.batch, sms, s);
+    }
+    a.rows = a.cols = static_cast<int>(m);
+    a.pitch = static_cast<int>(g_pitch);
+    a.matrix = m * g_pitch;
+    if (p.op == kNsSquare) {
+        a.aux = p.g;
+        a.kblocks = static_cast<int>((m + kNsK - 1) / kNsK);
+        if (!ns_map(&mA, p.g, false, m, m, g_pitch, p.batch)) return MLPBLK_ECUDA;
+        return run_ns<kNsSquare, false, false>(a, mA, mA, p.batch, sms, s);
+    }
+    const int64_t n = p.tall ? p.rows : p.cols;
+    a.kblocks = static_cast<int>((n + kNsK - 1) / kNsK);
+    if (!ns_map(&mA, p.x, p.tall, p.rows, p.cols, x_pitch, p.batch)) return MLPBLK_ECUDA;
+    return p.tall ? run_ns<kNsGram, true, true>(a, mA, mA, p.batch, sms, s) : run_ns<kNsGram, false, false>(a, mA, mA, p.batch, sms, s);
+}
+
+int take_device_error_gemm_ns() {
+    int v = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof(int)) != cudaSuccess) return MLPBLK_ECUDA;
+    if (v != 0) cudaMemcpyToSymbol(g_device_error, &z, sizeof(int));
+    return v;
+}
+
+}  // namespace mlpblk

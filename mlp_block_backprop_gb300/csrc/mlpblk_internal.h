@@ -318,6 +318,18 @@ int launch_unpermute_bwd(const void *dy, const void *rows, const int *pos, const
                          const float *weights, int64_t T, int64_t width, int dtype, int k, int experts, int pad, int64_t R,
                          void *d_rows, float *d_weights, cudaStream_t s);
 
+// Host: the router (route.cu), and the residual sum with RMSNorm and E4M3 codes (norm.cu).
+int launch_route(const mlpblk_route_desc &d, const void *logits, const float *bias, int *ids, float *weights, cudaStream_t s);
+int launch_route_bwd(const mlpblk_route_desc &d, const void *logits, const int *ids, const float *dw, void *dl, cudaStream_t s);
+constexpr int64_t kNormMaxWidth = 16384;   // a row stays in the registers of 16 warps
+constexpr int kNormMaxParts = 1024;        // dgamma partial rows, at most
+inline int64_t norm_part_pitch(int64_t width) { return (width + 31) / 32 * 32; }
+int launch_add_rmsnorm(const mlpblk_norm_desc &d, const void *x, const void *residual, const void *gamma, void *sum, void *n,
+                       uint8_t *codes, float *scales, float *rstd, int sms, cudaStream_t s);
+int launch_add_rmsnorm_bwd(const mlpblk_norm_desc &d, const void *dn, const void *d_sum, const void *sum, const float *rstd,
+                           const void *gamma, void *dx, float *part, int *parts, int sms, cudaStream_t s);
+int launch_norm_dgamma(const float *part, int parts, int64_t width, float *dgamma, int overwrite, cudaStream_t s);
+
 // Host: fp32 CUDA-core GEMM path (simt_f32.cu).  Strides are in elements:
 // A(m,k) = A[m*sam + k*sak], B(n,k) = B[n*sbn + k*sbk], outputs row-major [M][N].
 struct SimtEpi {

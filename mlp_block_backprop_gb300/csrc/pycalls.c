@@ -45,12 +45,18 @@ CALL(fp4_dequantize, 5, a[0], a[1], a[2], a[3], a[4])
 CALL(fp4_matmul, 7, a[0], a[1], a[2], a[3], a[4], a[5], a[6])
 CALL(fp4_matmul_grouped, 9, a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8])
 CALL(fp4_wgrad_grouped, 8, a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7])
+CALL(moe_route, 6, a[0], a[1], a[2], a[3], a[4], a[5])
+CALL(moe_route_backward, 6, a[0], a[1], a[2], a[3], a[4], a[5])
+CALL(add_rmsnorm, 10, a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9])
+CALL(add_rmsnorm_backward, 12, a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], (int32_t)(intptr_t)a[8], a[9], (size_t)a[10], a[11])
+CALL(orthogonalize, 6, a[0], a[1], a[2], a[3], (size_t)a[4], a[5])
 
 #define ENTRY(name) {"mlpblk_" #name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {
     ENTRY(moe_sort), ENTRY(moe_permute), ENTRY(moe_permute_backward), ENTRY(moe_unpermute),
     ENTRY(moe_unpermute_backward), ENTRY(fp4_quantize), ENTRY(fp4_dequantize), ENTRY(fp4_matmul),
-    ENTRY(fp4_matmul_grouped), ENTRY(fp4_wgrad_grouped), {NULL, NULL, 0, NULL}};
+    ENTRY(fp4_matmul_grouped), ENTRY(fp4_wgrad_grouped),
+    ENTRY(moe_route), ENTRY(moe_route_backward), ENTRY(add_rmsnorm), ENTRY(add_rmsnorm_backward), ENTRY(orthogonalize), {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mlpblk_calls", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
