@@ -1715,7 +1715,7 @@ int mlpblk_moe_route(const mlpblk_route_desc *desc, const void *logits, const fl
     int sms = 0;
     MLPBLK_TRY(device_sms(&sms));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    MLPBLK_LAUNCH(MLPBLK_KERNEL_ROUTE, s, launch_route(*desc, logits, bias, expert_idx, routing_weights, s));
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_ROUTE, s, launch_route(*desc, logits, bias, expert_idx, routing_weights, sms, s));
     return MLPBLK_OK;
 }
 
@@ -1731,7 +1731,7 @@ int mlpblk_moe_route_backward(const mlpblk_route_desc *desc, const void *logits,
     int sms = 0;
     MLPBLK_TRY(device_sms(&sms));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    MLPBLK_LAUNCH(MLPBLK_KERNEL_ROUTE_BWD, s, launch_route_bwd(*desc, logits, expert_idx, d_routing_weights, d_logits, s));
+    MLPBLK_LAUNCH(MLPBLK_KERNEL_ROUTE_BWD, s, launch_route_bwd(*desc, logits, expert_idx, d_routing_weights, d_logits, sms, s));
     return MLPBLK_OK;
 }
 

@@ -319,8 +319,8 @@ int launch_unpermute_bwd(const void *dy, const void *rows, const int *pos, const
                          void *d_rows, float *d_weights, cudaStream_t s);
 
 // Host: the router (route.cu), and the residual sum with RMSNorm and E4M3 codes (norm.cu).
-int launch_route(const mlpblk_route_desc &d, const void *logits, const float *bias, int *ids, float *weights, cudaStream_t s);
-int launch_route_bwd(const mlpblk_route_desc &d, const void *logits, const int *ids, const float *dw, void *dl, cudaStream_t s);
+int launch_route(const mlpblk_route_desc &d, const void *logits, const float *bias, int *ids, float *weights, int sms, cudaStream_t s);
+int launch_route_bwd(const mlpblk_route_desc &d, const void *logits, const int *ids, const float *dw, void *dl, int sms, cudaStream_t s);
 constexpr int64_t kNormMaxWidth = 16384;   // a row stays in the registers of 16 warps
 constexpr int kNormMaxParts = 1024;        // dgamma partial rows, at most
 inline int64_t norm_part_pitch(int64_t width) { return (width + 31) / 32 * 32; }
