@@ -665,8 +665,8 @@ int mlpblk_moe_route_backward(const mlpblk_route_desc *desc, const void *logits,
  * sum is written where residual is given (and only then) and may be x or residual itself.
  * codes and scales are given together; n, codes and rstd may be NULL, n and codes not both.
  * The codes are those of the real number n / scale, rounded once.  A row that holds an
- * infinity or a NaN, or whose mean square exceeds float32, has a NaN rstd and NaN scales and
- * codes.
+ * infinity, a NaN or a magnitude of 2^60 or more has a NaN rstd and NaN scales and codes;
+ * squares below float32's range count as zero.
  *
  * mlpblk_add_rmsnorm_backward: with dn the gradient of n (as the codes stand for it:
  *   rounding passes it on) and d_sum that of sum (NULL: none),

@@ -10,15 +10,17 @@
 //
 //   g = dn gamma,  xh = s r:   dx = d_sum + r (g - xh mean(g xh)),   dgamma = sum_t dn xh
 //
-// One pass: a row stays in registers between its sums and its outputs.  max |s gamma| needs
-// no r, so both reductions of a row are one.  Bound by HBM (7 bytes an element forward
-// with a residual branch in bf16, 8 backward).
+// One pass: a row stays in registers between its sums and its outputs, and the next row is
+// already on its way.  max |s gamma| needs no r, so both reductions of a row are one.  Bound by HBM
+// (7 bytes an element forward with a residual branch in bf16, 8 backward), if the arithmetic
+// stays near 20 instructions an element.
 //
-// Codes are those of the real number n / scale: s gamma is exact (bf16), r and r / scale are
-// carried as sums of two floats (relative error about 2^-45), the product is rounded to odd
-// and only then to E4M3, so that no value is rounded twice.  Values half way between two
-// codes are common (a ratio of two short products), and a float32 quotient would send them
-// either way.
+// Codes are those of the real number n / scale, rounded once: values half way between two codes
+// are common (one in 1700 here: ratios of two short products), and which way they go is decided
+// by the 25th bit of the scale.  So s gamma is exact (bf16), the sum of squares, r and r / scale are carried as sums
+// of two floats (relative error below 2^-40), and where a float32 quotient comes within two
+// steps of a border the product is taken to 48 bits and rounded to odd before it is rounded
+// to E4M3.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -54,81 +56,119 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // How a lane holds its part of a warp's unit of a row: E values, which in the vector forms
-// lie next to each other and in the scalar form (rows of any length) 32 apart.
+// lie next to each other and in the scalar form (rows of any length) 32 apart.  Raw: as they
+// are loaded.
 template <class T_, bool VEC_>
 struct Lay {
     using T = T_;
     static constexpr bool VEC = VEC_;
-    static constexpr int E = VEC && sizeof(T) == 2 ? 8 : 4;
+    static constexpr bool kPacked = VEC && sizeof(T) == 2;
+    static constexpr int E = kPacked ? 8 : 4;
     static constexpr int kUnit = 32 * E;                 // values of a unit
     static constexpr int kBlockLanes = 128 / E;          // lanes that share a block of 128
-    static __device__ __forceinline__ int col(int unit, int lane, int i) {
-        return VEC ? unit * kUnit + lane * E + i : unit * kUnit + lane + 32 * i;
-    }
-    // E values from column col(unit, lane, 0) on; 0 behind the row's end
-    static __device__ __forceinline__ void load(const T *row, int unit, int lane, int width, float (&v)[E]) {
+    struct Raw {
+        uint32_t w[4];                                   // bf16 pairs, or a float (scalar bf16: its bits on top) each
+    };
+    // The column of a lane's value i in a unit whose first value is at `at` (first_col).
+    static __device__ __forceinline__ int first_col(int unit, int lane) { return unit * kUnit + (VEC ? lane * E : lane); }
+    static __device__ __forceinline__ int col(int at, int i) { return at + (VEC ? i : 32 * i); }
+    // The lane's part of a unit; 0 behind the row's end.
+    static __device__ __forceinline__ Raw load(const T *row, int at, int width) {
+        Raw r;
         if constexpr (VEC) {
-            const int c = unit * kUnit + lane * E;
-            if (c >= width) {
-#pragma unroll
-                for (int i = 0; i < E; ++i) v[i] = 0.0f;
-            } else if constexpr (sizeof(T) == 2) {
-                const uint4 a = *reinterpret_cast<const uint4 *>(row + c);
-                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[2 * i] = __uint_as_float(w[i] << 16);
-                    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-                }
-            } else {
-                const float4 a = *reinterpret_cast<const float4 *>(row + c);
-                v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            }
+            const uint4 a = at < width ? *reinterpret_cast<const uint4 *>(row + at) : make_uint4(0, 0, 0, 0);
+            r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
         } else {
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const int c = col(unit, lane, i);
-                v[i] = c < width ? static_cast<float>(row[c]) : 0.0f;
+                const int c = col(at, i);
+                if constexpr (sizeof(T) == 2) r.w[i] = c < width ? static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[c]) << 16 : 0u;
+                else r.w[i] = c < width ? __float_as_uint(row[c]) : 0u;
+            }
+        }
+        return r;
+    }
+    static __device__ __forceinline__ void store(T *row, int at, int width, const Raw &r) {
+        if constexpr (VEC) {
+            if (at < width) *reinterpret_cast<uint4 *>(row + at) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const int c = col(at, i);
+                if (c >= width) continue;
+                if constexpr (sizeof(T) == 2) reinterpret_cast<uint16_t *>(row)[c] = static_cast<uint16_t>(r.w[i] >> 16);
+                else row[c] = __uint_as_float(r.w[i]);
             }
         }
     }
-    static __device__ __forceinline__ void store(T *row, int unit, int lane, int width, const float (&v)[E]) {
-        if constexpr (VEC) {
-            const int c = unit * kUnit + lane * E;
-            if (c >= width) return;
-            if constexpr (sizeof(T) == 2)
-                *reinterpret_cast<uint4 *>(row + c) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-            else
-                *reinterpret_cast<float4 *>(row + c) = make_float4(v[0], v[1], v[2], v[3]);
+    static __device__ __forceinline__ void unpack(const Raw &r, float (&v)[E]) {
+        if constexpr (kPacked) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(r.w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const int c = col(unit, lane, i);
-                if (c < width) row[c] = static_cast<T>(v[i]);
-            }
+            for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r.w[i]);
         }
     }
-    static __device__ __forceinline__ void store_codes(uint8_t *row, int unit, int lane, int width, const uint32_t (&w)[E / 4]) {
+    // Rounded to the type.
+    static __device__ __forceinline__ Raw pack(const float (&v)[E]) {
+        Raw r;
+        if constexpr (kPacked) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r.w[i] = pack2(v[2 * i], v[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r.w[i] = sizeof(T) == 2 ? pack2(0.0f, v[i]) & 0xFFFF0000u : __float_as_uint(v[i]);
+        }
+        return r;
+    }
+    // a + b, rounded to the type.
+    static __device__ __forceinline__ Raw add(const Raw &a, const Raw &b) {
+        Raw r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kPacked) asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r.w[i]) : "r"(a.w[i]), "r"(b.w[i]));
+            else if constexpr (sizeof(T) == 2) r.w[i] = pack2(0.0f, __uint_as_float(a.w[i]) + __uint_as_float(b.w[i])) & 0xFFFF0000u;
+            else r.w[i] = __float_as_uint(__uint_as_float(a.w[i]) + __uint_as_float(b.w[i]));
+        }
+        return r;
+    }
+    // The largest magnitude of n units.
+    template <int N>
+    static __device__ __forceinline__ float largest(const Raw (&r)[N]) {
+        if constexpr (kPacked) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(r[u].w[i]));
+            return fmaxf(fabsf(__uint_as_float(m << 16)), fabsf(__uint_as_float(m & 0xFFFF0000u)));
+        } else {
+            float m = 0.0f;
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(__uint_as_float(r[u].w[i])));
+            return m;
+        }
+    }
+    static __device__ __forceinline__ void store_codes(uint8_t *row, int at, int width, const uint32_t (&w)[E / 4]) {
         if constexpr (VEC) {
-            const int c = unit * kUnit + lane * E;
-            if (c >= width) return;
-            if constexpr (E == 8) *reinterpret_cast<uint2 *>(row + c) = make_uint2(w[0], w[1]);
-            else *reinterpret_cast<uint32_t *>(row + c) = w[0];
+            if (at >= width) return;
+            if constexpr (E == 8) *reinterpret_cast<uint2 *>(row + at) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t *>(row + at) = w[0];
         } else {
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const int c = col(unit, lane, i);
+                const int c = col(at, i);
                 if (c < width) row[c] = static_cast<uint8_t>(w[0] >> (8 * i));
             }
         }
     }
 };
-
-// Rounded as the type keeps it.
-template <class T>
-__device__ __forceinline__ float rounded(float v) { return v; }
-template <>
-__device__ __forceinline__ float rounded<__nv_bfloat16>(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
 
 // hi + lo += v, without losing v's low bits (Knuth's two-sum).
 __device__ __forceinline__ void two_add(float &hi, float &lo, float v) {
@@ -148,12 +188,39 @@ struct Peak {
     }
 };
 
+// The sum of hi + lo over the warp's lanes (hi >= 0, lo small beside it), as two floats: in
+// fixed point below the largest lane's exponent, 25 bits and 24 more, which integers add
+// exactly (three reductions of the warp instead of five steps of two-sums).
+__device__ __forceinline__ void warp_sum(float &hi, float &lo) {
+    const float h = __fadd_rn(hi, lo), l = __fsub_rn(lo, __fsub_rn(h, hi));   // l within half an ulp of h
+    float most;
+    asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(most) : "f"(h));
+    // 2^(24 - exponent) brings every lane below 2^25
+    const uint32_t field = 278u - static_cast<uint32_t>(min(max(static_cast<int>(__float_as_uint(most) >> 23), 30), 254));
+    const float up = __uint_as_float(field << 23), down = __uint_as_float((254u - field) << 23);
+    const float x = h * up, whole = truncf(x);
+    const int high = static_cast<int>(whole), low = __float2int_rn(((x - whole) + l * up) * 0x1p24f);   // below 2^25
+    const int sum_high = __reduce_add_sync(0xffffffffu, high), sum_low = __reduce_add_sync(0xffffffffu, low);
+    const float top = static_cast<float>(sum_high);    // of 30 bits: what it rounds off goes below
+    const float rest = static_cast<float>(sum_high - static_cast<int>(top)) + static_cast<float>(sum_low) * 0x1p-24f;
+    hi = most < INFINITY ? top * down : NAN;
+    lo = rest * down;
+}
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ Peak warp_peak(Peak p, bool exact) {
+    const float h = warp_max(p.hi);
+    return {h, exact ? 0.0f : warp_max(p.hi == h ? p.lo : -INFINITY)};
+}
+
 // 1 / sqrt(mean + eps) from the row's sum of squares, as a sum of two floats: the
 // approximate root once refined (the residual 1 - m y^2 taken exactly).
-__device__ __forceinline__ void inverse_root(float hi, float lo, float width, float eps, float &rh, float &rl) {
-    const float q = __fdiv_rn(hi, width);
-    const float q1 = __fdiv_rn(__fmaf_rn(-q, width, hi) + lo, width);
-    float mh = q, ml = q1;
+__device__ __forceinline__ void inverse_root(float hi, float lo, float width, float inv_width, float eps, float &rh, float &rl) {
+    float mh = __fmul_rn(hi, inv_width);
+    float ml = (__fmaf_rn(-mh, width, hi) + lo) * inv_width;
     two_add(mh, ml, eps);
     const float y = rsqrtf(mh);
     const float y2 = __fmul_rn(y, y), y2l = __fmaf_rn(y, y, -y2);
@@ -165,18 +232,27 @@ __device__ __forceinline__ void inverse_root(float hi, float lo, float width, fl
     if (!(hi < INFINITY)) rh = NAN, rl = 0.0f;         // an infinity or a NaN in the row
 }
 
-// The scale of a block whose largest |s gamma| is p, and r / scale (times 1 / up) as two floats.
-// up is 2^64 where p is so small that r / scale would overflow, else 1.
+// The scale of a block whose largest |s gamma| is p, and r / scale as two floats.  up: where p is so
+// small that r / scale would overflow, the quotient is 2^-64 of it and up is 2^64; else 1.
 __device__ __forceinline__ float scale_of(const Peak &p, float rh, float rl, float &ch, float &cl, float &up) {
     const float t = __fmul_rn(rh, p.hi);
     const float tl = __fmaf_rn(rh, p.hi, -t) + rl * p.hi + rh * p.lo;
-    const float q = __fdiv_rn(t, 448.0f);
-    float scale = __fadd_rn(q, __fdiv_rn(__fmaf_rn(-q, 448.0f, t) + tl, 448.0f));
+    constexpr float k = 1.0f / 448.0f;
+    const float q = __fmul_rn(t, k);
+    float scale = __fadd_rn(q, (__fmaf_rn(-q, 448.0f, t) + tl) * k);
+    up = 1.0f;
+    if (p.hi > 0x1p-60f && scale > 0x1p-100f && scale < 0x1p100f) {
+        float y;
+        asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(scale));
+        ch = __fmul_rn(rh, y);
+        cl = (__fmaf_rn(-ch, scale, rh) + rl) * y;
+        return scale;
+    }
     if (!(p.hi < INFINITY)) scale = NAN;
     if (scale == 0.0f) scale = 1.0f;                   // a block of zeros
-    up = p.hi < 0x1p-60f ? 0x1p64f : 1.0f;
-    const float down = p.hi < 0x1p-60f ? 0x1p-64f : 1.0f;
-    const float a = rh * down;
+    const bool small = p.hi < 0x1p-60f;
+    up = small ? 0x1p64f : 1.0f;
+    const float down = small ? 0x1p-64f : 1.0f, a = rh * down;
     ch = __fdiv_rn(a, scale);
     cl = __fdiv_rn(__fmaf_rn(-ch, scale, a) + rl * down, scale);
     if (!(p.hi > 0.0f)) ch = cl = 0.0f;                // (r may be infinite there)
@@ -215,91 +291,111 @@ __device__ __forceinline__ void row_barrier(int slot, int warps) {
     else asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(32 * warps) : "memory");
 }
 
-template <class L, int N>
+// RES: a residual branch is added.
+template <class L, int N, bool RES>
 __global__ void __launch_bounds__(32 * kNormMaxWarps)
 add_rmsnorm_kernel(const NormArgs a) {
     using T = typename L::T;
+    using Raw = typename L::Raw;
     constexpr int E = L::E;
     constexpr bool kExact = sizeof(T) == 2;   // products of two values are exact in float32
+    constexpr bool kAhead = N <= 4;           // the next row is loaded while this one is worked on
     __shared__ float4 meet[2][kNormMaxWarps];
     griddep_enter();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int W = a.warps, slot = warp / W, w = warp % W;
     const int slots = static_cast<int>(blockDim.x >> 5) / W;
-    const float width = static_cast<float>(a.width);
-    float g[N][E];
+    const float width = static_cast<float>(a.width), inv_width = 1.0f / width;
+    Raw g[N], x[N], res[RES ? N : 1];
+    int c[N];                                 // the lane's first column of each unit
 #pragma unroll
-    for (int u = 0; u < N; ++u) L::load(static_cast<const T *>(a.gamma), w + u * W, lane, a.width, g[u]);
-    int phase = 0;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * slots + slot; t < a.T; t += static_cast<int64_t>(gridDim.x) * slots) {
+    for (int u = 0; u < N; ++u) c[u] = L::first_col(w + u * W, lane);
+#pragma unroll
+    for (int u = 0; u < N; ++u) g[u] = L::load(static_cast<const T *>(a.gamma), c[u], a.width);
+    auto fetch = [&](int64_t t) {
         const int64_t at = t * a.width;
-        float s[N][E];
 #pragma unroll
-        for (int u = 0; u < N; ++u) L::load(static_cast<const T *>(a.x) + at, w + u * W, lane, a.width, s[u]);
-        if (a.residual) {
-            float r[N][E];
-#pragma unroll
-            for (int u = 0; u < N; ++u) L::load(static_cast<const T *>(a.residual) + at, w + u * W, lane, a.width, r[u]);
+        for (int u = 0; u < N; ++u) {
+            x[u] = L::load(static_cast<const T *>(a.x) + at, c[u], a.width);
+            if (RES) res[u] = L::load(static_cast<const T *>(a.residual) + at, c[u], a.width);
+        }
+    };
+    int phase = 0;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * slots;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * slots + slot;
+    if (kAhead && t < a.T) fetch(t);
+    for (; t < a.T; t += step) {
+        const int64_t at = t * a.width;
+        if (!kAhead) fetch(t);
+        if (RES) {
 #pragma unroll
             for (int u = 0; u < N; ++u) {
-#pragma unroll
-                for (int i = 0; i < E; ++i) s[u][i] = rounded<T>(s[u][i] + r[u][i]);
-                L::store(static_cast<T *>(a.sum) + at, w + u * W, lane, a.width, s[u]);
+                x[u] = L::add(x[u], res[u]);
+                L::store(static_cast<T *>(a.sum) + at, c[u], a.width, x[u]);
             }
         }
-        float hi = 0.0f, lo = 0.0f;
+        // The squares of a lane are added on top of a power of two that no sum of them reaches: each
+        // addition then drops the same bits, and what it dropped is found exactly.
+        constexpr uint32_t kRoom = (N * E <= 4 ? 3u : N * E <= 8 ? 4u : N * E <= 16 ? 5u : N * E <= 32 ? 6u : 7u) << 23;
+        const float most = L::largest(x);
+        const float base = __uint_as_float(min((__float_as_uint(most * most) & 0x7F800000u) + kRoom, 0x7F800000u));
+        float hi = base, lo = 0.0f;
+        float v[N][E];                          // s gamma (bf16), or s
         Peak peak[N];
 #pragma unroll
         for (int u = 0; u < N; ++u) {
+            float gv[E];
+            L::unpack(x[u], v[u]);
+            L::unpack(g[u], gv);
             peak[u] = {0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const float q = __fmul_rn(s[u][i], s[u][i]), p = __fmul_rn(s[u][i], g[u][i]);
-                two_add(hi, lo, q);
+                const float s = v[u][i];
+                const float sum = __fmaf_rn(s, s, hi);
+                lo += __fmaf_rn(s, s, -__fsub_rn(sum, hi));
+                hi = sum;
+                const float p = __fmul_rn(s, gv[i]);
                 if (kExact) {
                     peak[u].hi = fmaxf(peak[u].hi, fabsf(p));
+                    v[u][i] = p;
                 } else {
-                    lo += __fmaf_rn(s[u][i], s[u][i], -q);
-                    const float pl = __fmaf_rn(s[u][i], g[u][i], -p);
+                    const float pl = __fmaf_rn(s, gv[i], -p);
                     peak[u].take(fabsf(p), p < 0.0f ? -pl : pl);
                 }
             }
         }
+        hi = __fsub_rn(hi, base);
+        if (kAhead && t + step < a.T) fetch(t + step);
         Peak top = peak[0];
 #pragma unroll
-        for (int u = 1; u < N; ++u) top.take(peak[u].hi, peak[u].lo);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float h = __shfl_xor_sync(0xffffffffu, hi, o), l = __shfl_xor_sync(0xffffffffu, lo, o);
-            two_add(hi, lo, h);
-            lo += l;
-            top.take(__shfl_xor_sync(0xffffffffu, top.hi, o), kExact ? 0.0f : __shfl_xor_sync(0xffffffffu, top.lo, o));
+        for (int u = 1; u < N; ++u) {
+            if (kExact) top.hi = fmaxf(top.hi, peak[u].hi);
+            else top.take(peak[u].hi, peak[u].lo);
         }
+        warp_sum(hi, lo);
+        top = warp_peak(top, kExact);
         if (W > 1) {
             // the buffer alternates, so one barrier a row is enough
             float4 *m = meet[phase] + slot * W;
             phase ^= 1;
             if (lane == 0) m[w] = make_float4(hi, lo, top.hi, top.lo);
             row_barrier(slot, W);
-            const float4 q = m[lane % W];
-            hi = q.x, lo = q.y, top = {q.z, q.w};
-            for (int o = 1; o < W; o <<= 1) {
-                const float h = __shfl_xor_sync(0xffffffffu, hi, o), l = __shfl_xor_sync(0xffffffffu, lo, o);
-                two_add(hi, lo, h);
-                lo += l;
-                top.take(__shfl_xor_sync(0xffffffffu, top.hi, o), kExact ? 0.0f : __shfl_xor_sync(0xffffffffu, top.lo, o));
-            }
+            const float4 q = lane < W ? m[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            hi = q.x, lo = q.y;
+            warp_sum(hi, lo);
+            top = warp_peak({q.z, q.w}, kExact);
         }
         float rh, rl;
-        inverse_root(hi, lo, width, a.eps, rh, rl);
+        inverse_root(hi, lo, width, inv_width, a.eps, rh, rl);
         if (a.rstd && w == 0 && lane == 0) a.rstd[t] = rh;
         if (a.n) {
 #pragma unroll
             for (int u = 0; u < N; ++u) {
-                float v[E];
+                float n[E], gv[E];
+                L::unpack(g[u], gv);
 #pragma unroll
-                for (int i = 0; i < E; ++i) v[i] = s[u][i] * g[u][i] * rh;
-                L::store(static_cast<T *>(a.n) + at, w + u * W, lane, a.width, v);
+                for (int i = 0; i < E; ++i) n[i] = (kExact ? v[u][i] : v[u][i] * gv[i]) * rh;
+                L::store(static_cast<T *>(a.n) + at, c[u], a.width, L::pack(n));
             }
         }
         if (a.codes) {
@@ -314,26 +410,38 @@ add_rmsnorm_kernel(const NormArgs a) {
                 if (unit * L::kUnit >= a.width) continue;
                 if (a.block) {
 #pragma unroll
-                    for (int o = 1; o < L::kBlockLanes; o <<= 1)
-                        peak[u].take(__shfl_xor_sync(0xffffffffu, peak[u].hi, o),
-                                     kExact ? 0.0f : __shfl_xor_sync(0xffffffffu, peak[u].lo, o));
+                    for (int o = 1; o < L::kBlockLanes; o <<= 1) {
+                        if (kExact) peak[u].hi = fmaxf(peak[u].hi, __shfl_xor_sync(0xffffffffu, peak[u].hi, o));
+                        else peak[u].take(__shfl_xor_sync(0xffffffffu, peak[u].hi, o), __shfl_xor_sync(0xffffffffu, peak[u].lo, o));
+                    }
                     const float scale = scale_of(peak[u], rh, rl, ch, cl, up);
                     const int b = unit * (L::kUnit / 128) + lane / L::kBlockLanes;
                     if (lane % L::kBlockLanes == 0 && b * 128 < a.width) a.scales[t * ((a.width + 127) / 128) + b] = scale;
                 }
+                float gv[E], q[E];
+                if (!kExact) L::unpack(g[u], gv);
+                // a border between two codes has its last 20 bits as 0x80000 (below 2^-6, E4M3's
+                // smallest normal, borders lie elsewhere): anything within two steps of one, or small, is near
+                uint32_t near = 0xFFFFFFFFu;
+                float least = INFINITY;
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    const float p = kExact ? v[u][i] : __fmul_rn(v[u][i], gv[i]);
+                    q[i] = __fmul_rn(p, ch);
+                    near = min(near, (__float_as_uint(q[i]) - 0x7FFFEu) & 0xFFFFFu);
+                    least = fminf(least, fabsf(q[i]));
+                }
+                if (near <= 4u || !(least >= 0x1p-6f) || up != 1.0f || ch != ch) {
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        const float p = kExact ? v[u][i] : __fmul_rn(v[u][i], gv[i]);
+                        q[i] = scaled_odd(p * up, kExact ? 0.0f : __fmaf_rn(v[u][i], gv[i], -p) * up, ch, cl);
+                    }
+                }
                 uint32_t codes[E / 4];
 #pragma unroll
-                for (int j = 0; j < E / 4; ++j) {
-                    float v[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x = s[u][4 * j + i], y = g[u][4 * j + i];
-                        const float p = __fmul_rn(x, y);
-                        v[i] = scaled_odd(p * up, kExact ? 0.0f : __fmaf_rn(x, y, -p) * up, ch, cl);
-                    }
-                    codes[j] = e4m3x2(v[0], v[1]) | e4m3x2(v[2], v[3]) << 16;
-                }
-                L::store_codes(a.codes + at, unit, lane, a.width, codes);
+                for (int j = 0; j < E / 4; ++j) codes[j] = e4m3x2(q[4 * j], q[4 * j + 1]) | e4m3x2(q[4 * j + 2], q[4 * j + 3]) << 16;
+                L::store_codes(a.codes + at, c[u], a.width, codes);
             }
         }
     }
@@ -344,7 +452,10 @@ template <class L, int N>
 __global__ void __launch_bounds__(32 * kNormMaxWarps)
 add_rmsnorm_bwd_kernel(const NormArgs a) {
     using T = typename L::T;
+    using Raw = typename L::Raw;
     constexpr int E = L::E;
+    constexpr bool kAhead = N <= 2;           // as in the forward
+    constexpr bool kKeep = N <= 4;            // a row stays in registers; else it is read again
     __shared__ float meet[2][kNormMaxWarps];
     extern __shared__ float shares[];         // [slots - 1][W * N * kUnit]: the other slots' dgamma
     griddep_enter();
@@ -352,29 +463,53 @@ add_rmsnorm_bwd_kernel(const NormArgs a) {
     const int W = a.warps, slot = warp / W, w = warp % W;
     const int slots = static_cast<int>(blockDim.x >> 5) / W;
     const float inv_width = 1.0f / static_cast<float>(a.width);
-    float g[N][E], acc[N][E];
+    Raw g[N], sr[N], dr[N], yr[N];
+    int c[N];                                 // the lane's first column of each unit
+#pragma unroll
+    for (int u = 0; u < N; ++u) c[u] = L::first_col(w + u * W, lane);
+    float acc[N][E], r_next = 0.0f;
 #pragma unroll
     for (int u = 0; u < N; ++u) {
-        L::load(static_cast<const T *>(a.gamma), w + u * W, lane, a.width, g[u]);
+        g[u] = L::load(static_cast<const T *>(a.gamma), c[u], a.width);
+        yr[u] = Raw{};
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[u][i] = 0.0f;
     }
-    int phase = 0;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * slots + slot; t < a.T; t += static_cast<int64_t>(gridDim.x) * slots) {
+    auto fetch_unit = [&](int64_t t, int u) {
         const int64_t at = t * a.width;
-        const float r = a.rstd_in[t];
-        float s[N][E], d[N][E], y[N][E];
+        sr[u] = L::load(static_cast<const T *>(a.x) + at, c[u], a.width);
+        dr[u] = L::load(static_cast<const T *>(a.dn) + at, c[u], a.width);
+        if (a.d_sum) yr[u] = L::load(static_cast<const T *>(a.d_sum) + at, c[u], a.width);
+    };
+    auto fetch = [&](int64_t t) {
+        r_next = a.rstd_in[t];
+        if constexpr (kKeep) {
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-            L::load(static_cast<const T *>(a.x) + at, w + u * W, lane, a.width, s[u]);
-            L::load(static_cast<const T *>(a.dn) + at, w + u * W, lane, a.width, d[u]);
-            if (a.d_sum) L::load(static_cast<const T *>(a.d_sum) + at, w + u * W, lane, a.width, y[u]);
+            for (int u = 0; u < N; ++u) fetch_unit(t, u);
         }
+    };
+    int phase = 0;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * slots;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * slots + slot;
+    if (kAhead && t < a.T) fetch(t);
+    for (; t < a.T; t += step) {
+        const int64_t at = t * a.width;
+        if (!kAhead) fetch(t);
+        const float r = r_next;
+        Raw s0[N], d0[N], y0[N];
         float dot = 0.0f;
 #pragma unroll
-        for (int u = 0; u < N; ++u)
+        for (int u = 0; u < N; ++u) {
+            if (!kKeep) fetch_unit(t, u);
+            s0[u] = sr[u], d0[u] = dr[u], y0[u] = yr[u];
+            float s[E], d[E], gv[E];
+            L::unpack(s0[u], s);
+            L::unpack(d0[u], d);
+            L::unpack(g[u], gv);
 #pragma unroll
-            for (int i = 0; i < E; ++i) dot += d[u][i] * g[u][i] * s[u][i];
+            for (int i = 0; i < E; ++i) dot += d[i] * gv[i] * s[i];
+        }
+        if (kAhead && t + step < a.T) fetch(t + step);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
         if (W > 1) {
@@ -385,17 +520,24 @@ add_rmsnorm_bwd_kernel(const NormArgs a) {
             dot = m[lane % W];
             for (int o = 1; o < W; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
         }
-        const float c = r * r * r * (dot * inv_width);
+        const float k = r * r * r * (dot * inv_width);
 #pragma unroll
         for (int u = 0; u < N; ++u) {
-            float v[E];
+            float s[E], d[E], y[E], gv[E], v[E];
+            if (!kKeep) {
+                fetch_unit(t, u);
+                s0[u] = sr[u], d0[u] = dr[u], y0[u] = yr[u];
+            }
+            L::unpack(s0[u], s);
+            L::unpack(d0[u], d);
+            L::unpack(y0[u], y);
+            L::unpack(g[u], gv);
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                v[i] = r * (d[u][i] * g[u][i]) - s[u][i] * c;
-                if (a.d_sum) v[i] += y[u][i];
-                acc[u][i] += d[u][i] * (s[u][i] * r);
+                v[i] = r * (d[i] * gv[i]) - s[i] * k + y[i];
+                acc[u][i] += d[i] * (s[i] * r);
             }
-            L::store(static_cast<T *>(a.dx) + at, w + u * W, lane, a.width, v);
+            L::store(static_cast<T *>(a.dx) + at, c[u], a.width, L::pack(v));
         }
     }
     // the CTA's partial row: slot 0's warps add the other slots' shares in order
@@ -404,7 +546,7 @@ add_rmsnorm_bwd_kernel(const NormArgs a) {
 #pragma unroll
         for (int u = 0; u < N; ++u)
 #pragma unroll
-            for (int i = 0; i < E; ++i) shares[(slot - 1) * stride + L::col(w + u * W, lane, i)] = acc[u][i];
+            for (int i = 0; i < E; ++i) shares[(slot - 1) * stride + L::col(c[u], i)] = acc[u][i];
     }
     if (slots > 1) __syncthreads();
     if (slot > 0) return;
@@ -413,10 +555,10 @@ add_rmsnorm_bwd_kernel(const NormArgs a) {
     for (int u = 0; u < N; ++u)
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            const int c = L::col(w + u * W, lane, i);
+            const int j = L::col(c[u], i);
             float v = acc[u][i];
-            for (int k = 1; k < slots; ++k) v += shares[(k - 1) * stride + c];
-            if (c < a.width) out[c] = v;
+            for (int k = 1; k < slots; ++k) v += shares[(k - 1) * stride + j];
+            if (j < a.width) out[j] = v;
         }
 }
 
@@ -442,15 +584,15 @@ norm_dgamma_kernel(const float *__restrict__ part, int parts, int pitch, int wid
     if (slice == 0 && c < width) dgamma[c] = overwrite ? red[0][lane] : dgamma[c] + red[0][lane];
 }
 
-// Warps of a row and units of a warp.  Many rows: four units a warp, so that a warp has
-// four 16-byte loads of each array in flight and a row meets in few warps.  Few rows (no more
-// than the SMs): as many warps as there are units.
+// Warps of a row and units of a warp.  Many rows: four units a warp forward, two backward (three arrays, and dgamma's
+// sums), so that with the next row on its way a warp has 64 KB an SM in flight and a row meets in few
+// warps.  Few rows (no more than the SMs): as many warps as there are units.
 struct NormShape {
     int warps, units;
 };
-NormShape norm_shape(int width, int unit, int64_t T, int sms) {
+NormShape norm_shape(int width, int unit, int64_t T, int sms, bool backward) {
     const int U = (width + unit - 1) / unit;
-    const int each = T <= sms ? 1 : 4;
+    const int each = T <= sms ? 1 : backward ? 2 : 4;
     NormShape s = {1, 0};
     while (s.warps < kNormMaxWarps && s.warps * each < U) s.warps *= 2;
     s.units = 1;
@@ -463,17 +605,16 @@ int run_norm(NormArgs a, bool backward, int sms, cudaStream_t s, int *parts) {
     const int threads = 32 * a.warps > kNormThreads ? 32 * a.warps : kNormThreads;
     const int slots = threads / (32 * a.warps);
     const size_t smem = backward ? static_cast<size_t>(slots - 1) * a.warps * N * L::kUnit * 4 : 0;
-    static int occ[2][5][64] = {};   // resident CTAs an SM, by direction, log2(warps) and device
+    void (*const kernel)(NormArgs) = backward ? add_rmsnorm_bwd_kernel<L, N> : (a.residual ? add_rmsnorm_kernel<L, N, true> : add_rmsnorm_kernel<L, N, false>);
+    static int occ[3][5][64] = {};   // resident CTAs an SM, by kernel, log2(warps) and device
     int dev = 0, lg = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) return MLPBLK_ECUDA;
     while ((1 << lg) < a.warps) ++lg;
-    int &o = occ[backward ? 1 : 0][lg][dev];
+    int &o = occ[backward ? 2 : (a.residual ? 1 : 0)][lg][dev];
     if (o == 0) {
         int n = 0;
-        const cudaError_t e = backward ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, add_rmsnorm_bwd_kernel<L, N>, threads, smem)
-                                       : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, add_rmsnorm_kernel<L, N>, threads, smem);
-        const int rc = cuda_status(e);
+        const int rc = cuda_status(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem));
         if (rc != MLPBLK_OK) return rc;
         o = n < 1 ? 1 : n;
     }
@@ -483,21 +624,22 @@ int run_norm(NormArgs a, bool backward, int sms, cudaStream_t s, int *parts) {
     if (backward) {
         if (grid > kNormMaxParts) grid = kNormMaxParts;
         *parts = static_cast<int>(grid);
-        return launch_pdl(add_rmsnorm_bwd_kernel<L, N>, dim3(static_cast<unsigned>(grid)), dim3(threads), smem, s, a);
     }
-    return launch_pdl(add_rmsnorm_kernel<L, N>, dim3(static_cast<unsigned>(grid)), dim3(threads), smem, s, a);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), smem, s, a);
 }
 
 template <class L>
 int run_norm_lay(NormArgs a, bool backward, int sms, cudaStream_t s, int *parts) {
-    const NormShape sh = norm_shape(a.width, L::kUnit, a.T, sms);
+    const NormShape sh = norm_shape(a.width, L::kUnit, a.T, sms, backward);
     a.warps = sh.warps;
     switch (sh.units) {
         case 1: return run_norm<L, 1>(a, backward, sms, s, parts);
         case 2: return run_norm<L, 2>(a, backward, sms, s, parts);
         case 4: return run_norm<L, 4>(a, backward, sms, s, parts);
-        default: return run_norm<L, 8>(a, backward, sms, s, parts);
+        default: break;
     }
+    if constexpr (L::E == 4) return run_norm<L, 8>(a, backward, sms, s, parts);   // (16 warps of 4 units of 256 are kNormMaxWidth)
+    return MLPBLK_EINVAL;
 }
 
 int run_norm_type(const NormArgs &a, int dtype, bool backward, int sms, cudaStream_t s, int *parts) {
