@@ -1625,9 +1625,10 @@ int check_ortho_desc(const mlpblk_ortho_desc *d) {
 }
 
 // Workspace of an orthogonalisation: X twice (a step reads one and writes the other), its
-// low parts, G and P, P's diagonal's remainders, the norm's partial sums.
+// low parts, four square matrices of the short side, the remainders of three diagonals, the
+// norm's partial sums.
 struct OrthoLayout {
-    int64_t x[2], lo, g, p, diag, partial, total;
+    int64_t x[2], lo, g[4], diag[3], partial, total;
 };
 OrthoLayout ortho_layout(const mlpblk_ortho_desc *d) {
     OrthoLayout l = {};
@@ -1642,9 +1643,8 @@ OrthoLayout ortho_layout(const mlpblk_ortho_desc *d) {
     l.x[0] = take(x);
     l.x[1] = take(x);
     l.lo = take(x);
-    l.g = take(g);
-    l.p = take(g);
-    l.diag = take(m * d->batch * 4);
+    for (int64_t &at : l.g) at = take(g);
+    for (int64_t &at : l.diag) at = take(m * d->batch * 4);
     l.partial = take((d->batch > kOrthoNormParts ? d->batch : kOrthoNormParts) * static_cast<int64_t>(8));
     l.total = off;
     return l;
@@ -1657,8 +1657,10 @@ int orthogonalize_impl(const mlpblk_ortho_desc *d, const OrthoSource &u, void *o
     const OrthoLayout l = ortho_layout(d);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     __half *x[2] = {reinterpret_cast<__half *>(ws + l.x[0]), reinterpret_cast<__half *>(ws + l.x[1])};
-    __half *lo = reinterpret_cast<__half *>(ws + l.lo), *g = reinterpret_cast<__half *>(ws + l.g), *p = reinterpret_cast<__half *>(ws + l.p);
-    float *diag = reinterpret_cast<float *>(ws + l.diag);
+    __half *lo = reinterpret_cast<__half *>(ws + l.lo), *g[4];
+    float *diag[3];
+    for (int i = 0; i < 4; ++i) g[i] = reinterpret_cast<__half *>(ws + l.g[i]);
+    for (int i = 0; i < 3; ++i) diag[i] = reinterpret_cast<float *>(ws + l.diag[i]);
     double *partial = reinterpret_cast<double *>(ws + l.partial);
     const bool tall = d->rows > d->cols;
     const int64_t n = tall ? d->rows : d->cols;
@@ -1668,36 +1670,78 @@ int orthogonalize_impl(const mlpblk_ortho_desc *d, const OrthoSource &u, void *o
     MLPBLK_LAUNCH(MLPBLK_KERNEL_ORTHO_NORM, s, launch_ortho_norm(u, d->rows * d->cols, d->batch, partial, &parts, sms, s));
     MLPBLK_LAUNCH(MLPBLK_KERNEL_ORTHO_SCALE, s,
                   launch_ortho_scale(u, d->rows, d->cols, d->batch, partial, parts, d->eps, sx, x[0], d->steps > 1 ? lo : nullptr, sms, s));
-    for (int i = 0; i < d->steps; ++i) {
-        const bool last = i + 1 == d->steps;
+    // Two steps at a time (csrc/gemm_ns.cu) save 3 m^2 (n - m) operations a matrix for one launch
+    // more: worth it from some 6 us of the tensor cores on.  Never the last step: its X is kept in
+    // one fp16 value, and G's errors would reach the result.
+    const int64_t m = tall ? d->cols : d->rows;
+    const bool two = m >= 512 && n >= 2 * m && 3.0 * d->batch * m * m * (n - m) >= 8e9;
+    int at = 0;   // which of x holds X
+    for (int i = 0; i < d->steps;) {
+        const bool pair = two && i + 2 < d->steps;
+        const float *c1 = d->coefficients[i], *c2 = d->coefficients[i + (pair ? 1 : 0)];
+        const int after = i + (pair ? 2 : 1);
+        const bool last = after == d->steps;
         NsProduct q = {};
         q.tall = tall;
         q.rows = d->rows;
         q.cols = d->cols;
         q.batch = d->batch;
-        q.diag = diag;
-        q.a = d->coefficients[i][0];
-        q.b = d->coefficients[i][1];
-        q.c = d->coefficients[i][2];
         q.op = kNsGram;
-        q.x = x[i & 1];
-        q.out = g;
+        q.x = x[at];
+        q.out = g[0];
         q.alpha = 1.0f / (sx * sx);
         MLPBLK_LAUNCH(MLPBLK_KERNEL_NS_GRAM, s, launch_ns_product(q, sms, s));
-        q.op = kNsSquare;
-        q.g = g;
-        q.out = p;
-        MLPBLK_LAUNCH(MLPBLK_KERNEL_NS_SQUARE, s, launch_ns_product(q, sms, s));
+        auto square = [&](const float *c, __half *to, float *rest) {
+            NsProduct r = q;
+            r.op = kNsSquare;
+            r.y = g[0];
+            r.b = c[1];
+            r.c = c[2];
+            r.out = to;
+            r.diag_out = rest;
+            return launch_ns_product(r, sms, s);
+        };
+        auto apply = [&](const __half *y, __half *to) {
+            NsProduct r = q;
+            r.op = kNsApply;
+            r.y = y;
+            r.p = g[1];
+            r.diag = diag[0];
+            r.a = c1[0];
+            r.out = to;
+            return launch_ns_product(r, sms, s);
+        };
+        MLPBLK_LAUNCH(MLPBLK_KERNEL_NS_SQUARE, s, square(c1, g[1], diag[0]));
+        if (pair) {
+            MLPBLK_LAUNCH(MLPBLK_KERNEL_NS_APPLY, s, apply(g[0], g[2]));
+            MLPBLK_LAUNCH(MLPBLK_KERNEL_NS_APPLY, s, apply(g[2], g[0]));
+            MLPBLK_LAUNCH(MLPBLK_KERNEL_NS_SQUARE, s, square(c2, g[3], diag[1]));
+            NsProduct r = q;
+            r.op = kNsJoin;
+            r.y = g[1];
+            r.p = g[3];
+            r.diag = diag[1];
+            r.diag2 = diag[0];
+            r.a = c2[0];
+            r.b = c1[0];
+            r.out = g[2];
+            r.diag_out = diag[2];
+            MLPBLK_LAUNCH(MLPBLK_KERNEL_NS_JOIN, s, launch_ns_product(r, sms, s));
+        }
         q.op = kNsUpdate;
-        q.g = p;
-        q.x_lo = i + 1 < d->steps ? lo : nullptr;
-        q.out = x[(i + 1) & 1];
-        q.out_lo = i + 2 < d->steps ? lo : nullptr;
+        q.p = g[pair ? 2 : 1];
+        q.diag = diag[pair ? 2 : 0];
+        q.a = pair ? c1[0] * c2[0] : c1[0];
+        q.x_lo = !last ? lo : nullptr;
+        q.out = x[at ^ 1];
+        q.out_lo = after + 1 < d->steps ? lo : nullptr;
         q.o = last ? o : nullptr;
         q.alpha = 1.0f / sx;
         MLPBLK_LAUNCH(MLPBLK_KERNEL_NS_UPDATE, s, launch_ns_product(q, sms, s));
+        i = after;
+        at ^= 1;
     }
-    *x_out = x[d->steps & 1];
+    *x_out = x[at];
     *sx_out = sx;
     return MLPBLK_OK;
 }

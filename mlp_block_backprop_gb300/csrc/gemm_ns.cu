@@ -5,6 +5,12 @@
 //   P  = b G + c G G
 //   X' = a X + P X        or  a X + X P
 //
+// and, where X's long side is at least twice the short one, two steps at a time with one product
+// on X for both: with the first step's P1, G becomes (a1 I + P1) G (a1 I + P1), its own P2 follows, and
+// X' = (a2 I + P2)(a1 I + P1) X = a1 a2 X + S X.  That trades a G and an update (3 m^2 n) for three
+// more products of the short side (m^3 each, half of them mirrored): 16384 x 4096 takes 28% fewer
+// operations.  G's own rounding errors then go through a second step, so it stays at two.
+//
 // Nothing is transposed in memory: each operand is read K-major or MN-major as it lies,
 // and a tall X is worked on from its right.  G and P are symmetric: only tiles on and
 // above the diagonal are computed, the others are written as their mirror images.
@@ -45,8 +51,9 @@ struct NsArgs {
     int group_m;
     int pitch;                          // elements of a row of out, aux
     int64_t matrix;                     // elements of a matrix of out, aux
-    const __half *aux, *aux_lo;         // [rows][cols]: G (kNsSquare) or X (kNsUpdate)
-    float *diag;                        // [batch][diag_n]
+    const __half *aux, *aux2;           // [rows][cols]: Y or X; X's low part (or NULL), or P (kNsJoin)
+    const float *diag, *diag2;          // [batch][diag_n]
+    float *diag_out;
     int diag_n;
     bool diag_col;                      // kNsUpdate: diag goes by column (tall)
     __half *out, *out_lo;
@@ -207,10 +214,14 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 __device__ __forceinline__ float2 unpack_half2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
 
 // What the epilogue of a row's CH columns reads besides the accumulator, loaded ahead of it.
+template <int OP>
+constexpr bool kNsTwo = OP == kNsUpdate || OP == kNsJoin;   // two tiles
+template <int OP>
+constexpr bool kNsScaled = OP == kNsUpdate || OP == kNsApply || OP == kNsJoin;   // (a + diag) times the first
 template <int OP, int CH>
 struct NsAux {
-    uint4 hi[OP == kNsGram ? 1 : CH / 8], lo[OP == kNsUpdate ? CH / 8 : 1];
-    float d;           // the row's diag (kNsUpdate, wide)
+    uint4 hi[OP == kNsGram ? 1 : CH / 8], lo[kNsTwo<OP> ? CH / 8 : 1];
+    float d;           // the row's diag (kNsScaled, but tall updates)
 };
 
 template <int OP, int CH>
@@ -221,9 +232,9 @@ __device__ __forceinline__ void ns_load_aux(const NsArgs &a, const NsTile &w, in
 #pragma unroll
     for (int i = 0; i < CH / 8; ++i) {
         x.hi[i] = on ? *reinterpret_cast<const uint4 *>(a.aux + at + 8 * i) : make_uint4(0, 0, 0, 0);
-        if (OP == kNsUpdate) x.lo[i] = on && a.aux_lo ? *reinterpret_cast<const uint4 *>(a.aux_lo + at + 8 * i) : make_uint4(0, 0, 0, 0);
+        if (kNsTwo<OP>) x.lo[i] = on && (OP == kNsJoin || a.aux2) ? *reinterpret_cast<const uint4 *>(a.aux2 + at + 8 * i) : make_uint4(0, 0, 0, 0);
     }
-    if (OP == kNsUpdate) x.d = on && !a.diag_col ? a.diag[static_cast<int64_t>(w.batch) * a.diag_n + row] : 0.0f;
+    if (kNsScaled<OP>) x.d = on && !a.diag_col ? a.diag[static_cast<int64_t>(w.batch) * a.diag_n + row] : 0.0f;
 }
 
 // CH columns from `col` on of the lane's row: the step's arithmetic and the stores.  The
@@ -242,10 +253,22 @@ __device__ __forceinline__ void ns_finish(const NsArgs &a, const NsTile &w, int 
         const uint32_t *l = reinterpret_cast<const uint32_t *>(x.lo);
 #pragma unroll
         for (int i = 0; i < CH / 2; ++i) {
-            float2 p = unpack_half2(h[i]);
+            const float2 p = unpack_half2(h[i]);
             if (OP == kNsSquare) {
                 v[2 * i] = a.b * p.x + a.c * v[2 * i];
                 v[2 * i + 1] = a.b * p.y + a.c * v[2 * i + 1];
+            } else if (OP == kNsApply) {
+                v[2 * i] = (a.a + x.d) * p.x + v[2 * i];
+                v[2 * i + 1] = (a.a + x.d) * p.y + v[2 * i + 1];
+            } else if (OP == kNsJoin) {
+                const float2 q = unpack_half2(l[i]);
+                const float *d2 = a.diag2 + static_cast<int64_t>(w.batch) * a.diag_n;
+                const int c0 = col + 2 * i, c1 = c0 + 1;
+                const float e0 = c0 < a.cols ? __ldg(d2 + c0) : 0.0f, e1 = c1 < a.cols ? __ldg(d2 + c1) : 0.0f;
+                v[2 * i] = (a.a + x.d) * p.x + (a.b + e0) * q.x + v[2 * i];
+                v[2 * i + 1] = (a.a + x.d) * p.y + (a.b + e1) * q.y + v[2 * i + 1];
+                if (c0 == row) v[2 * i] += (a.a + x.d) * e0 + a.b * x.d;
+                if (c1 == row) v[2 * i + 1] += (a.a + x.d) * e1 + a.b * x.d;
             } else {
                 const float2 q = unpack_half2(l[i]);
                 float d0 = x.d, d1 = x.d;
@@ -292,11 +315,11 @@ __device__ __forceinline__ void ns_finish(const NsArgs &a, const NsTile &w, int 
 #pragma unroll
             for (int i = 0; i < CH / 8; ++i) *reinterpret_cast<uint4 *>(a.out_lo + at + 8 * i) = make_uint4(l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]);
         }
-        if (OP == kNsSquare && row >= col && row < col + CH) {
+        if ((OP == kNsSquare || OP == kNsJoin) && row >= col && row < col + CH) {
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 const float2 p = unpack_half2(h[i / 2]);
-                if (col + i == row) a.diag[static_cast<int64_t>(w.batch) * a.diag_n + row] = v[i] - (i & 1 ? p.y : p.x);
+                if (col + i == row) a.diag_out[static_cast<int64_t>(w.batch) * a.diag_n + row] = v[i] - (i & 1 ? p.y : p.x);
             }
         }
     }
@@ -821,11 +844,13 @@ int launch_ns_product(const NsProduct &p, int sms, cudaStream_t s) {
     a.b = p.b;
     a.c = p.c;
     a.diag = p.diag;
+    a.diag2 = p.diag2;
+    a.diag_out = p.diag_out;
     a.diag_n = static_cast<int>(m);
-    a.diag_col = p.tall;
     a.out = p.out;
     a.out_lo = p.out_lo;
     a.o = static_cast<uint16_t *>(p.o);
+    a.kblocks = static_cast<int>((m + kNsK - 1) / kNsK);
     CUtensorMap mA, mB;
     if (p.op == kNsUpdate) {
         a.rows = static_cast<int>(p.rows);
@@ -833,28 +858,31 @@ int launch_ns_product(const NsProduct &p, int sms, cudaStream_t s) {
         a.pitch = static_cast<int>(x_pitch);
         a.matrix = p.rows * x_pitch;
         a.aux = p.x;
-        a.aux_lo = p.x_lo;
-        a.kblocks = static_cast<int>((m + kNsK - 1) / kNsK);
+        a.aux2 = p.x_lo;
+        a.diag_col = p.tall;
         if (p.tall) {
-            if (!ns_map(&mA, p.x, false, p.rows, p.cols, x_pitch, p.batch) || !ns_map(&mB, p.g, false, m, m, g_pitch, p.batch)) return MLPBLK_ECUDA;
+            if (!ns_map(&mA, p.x, false, p.rows, p.cols, x_pitch, p.batch) || !ns_map(&mB, p.p, false, m, m, g_pitch, p.batch)) return MLPBLK_ECUDA;
             return run_ns<kNsUpdate, false, false>(a, mA, mB, p.batch, sms, s);
         }
-        if (!ns_map(&mA, p.g, false, m, m, g_pitch, p.batch) || !ns_map(&mB, p.x, true, p.rows, p.cols, x_pitch, p.batch)) return MLPBLK_ECUDA;
+        if (!ns_map(&mA, p.p, false, m, m, g_pitch, p.batch) || !ns_map(&mB, p.x, true, p.rows, p.cols, x_pitch, p.batch)) return MLPBLK_ECUDA;
         return run_ns<kNsUpdate, false, true>(a, mA, mB, p.batch, sms, s);
     }
     a.rows = a.cols = static_cast<int>(m);
     a.pitch = static_cast<int>(g_pitch);
     a.matrix = m * g_pitch;
-    if (p.op == kNsSquare) {
-        a.aux = p.g;
-        a.kblocks = static_cast<int>((m + kNsK - 1) / kNsK);
-        if (!ns_map(&mA, p.g, false, m, m, g_pitch, p.batch)) return MLPBLK_ECUDA;
-        return run_ns<kNsSquare, false, false>(a, mA, mA, p.batch, sms, s);
+    if (p.op == kNsGram) {
+        const int64_t n = p.tall ? p.rows : p.cols;
+        a.kblocks = static_cast<int>((n + kNsK - 1) / kNsK);
+        if (!ns_map(&mA, p.x, p.tall, p.rows, p.cols, x_pitch, p.batch)) return MLPBLK_ECUDA;
+        return p.tall ? run_ns<kNsGram, true, true>(a, mA, mA, p.batch, sms, s) : run_ns<kNsGram, false, false>(a, mA, mA, p.batch, sms, s);
     }
-    const int64_t n = p.tall ? p.rows : p.cols;
-    a.kblocks = static_cast<int>((n + kNsK - 1) / kNsK);
-    if (!ns_map(&mA, p.x, p.tall, p.rows, p.cols, x_pitch, p.batch)) return MLPBLK_ECUDA;
-    return p.tall ? run_ns<kNsGram, true, true>(a, mA, mA, p.batch, sms, s) : run_ns<kNsGram, false, false>(a, mA, mA, p.batch, sms, s);
+    a.aux = p.y;
+    a.aux2 = p.p;
+    if (!ns_map(&mB, p.y, false, m, m, g_pitch, p.batch)) return MLPBLK_ECUDA;
+    if (p.op == kNsSquare) return run_ns<kNsSquare, false, false>(a, mB, mB, p.batch, sms, s);
+    if (!ns_map(&mA, p.p, false, m, m, g_pitch, p.batch)) return MLPBLK_ECUDA;
+    if (p.op == kNsApply) return run_ns<kNsApply, false, false>(a, mA, mB, p.batch, sms, s);
+    return run_ns<kNsJoin, false, false>(a, mA, mB, p.batch, sms, s);
 }
 
 int take_device_error_gemm_ns() {

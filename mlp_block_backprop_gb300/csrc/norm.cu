@@ -422,20 +422,26 @@ add_rmsnorm_kernel(const NormArgs a) {
                 if (!kExact) L::unpack(g[u], gv);
                 // a border between two codes has its last 20 bits as 0x80000 (below 2^-6, E4M3's
                 // smallest normal, borders lie elsewhere): anything within two steps of one, or small, is near
-                uint32_t near = 0xFFFFFFFFu;
-                float least = INFINITY;
+                // (four values share a look: 16384 x 4096 83 us; one 97, two 87, eight 89)
+                constexpr int kTogether = 4;
+                const bool odd = up != 1.0f || ch != ch;
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const float p = kExact ? v[u][i] : __fmul_rn(v[u][i], gv[i]);
-                    q[i] = __fmul_rn(p, ch);
-                    near = min(near, (__float_as_uint(q[i]) - 0x7FFFEu) & 0xFFFFFu);
-                    least = fminf(least, fabsf(q[i]));
-                }
-                if (near <= 4u || !(least >= 0x1p-6f) || up != 1.0f || ch != ch) {
+                for (int j = 0; j < E; j += kTogether) {
+                    uint32_t near = 0xFFFFFFFFu;
+                    float least = INFINITY;
 #pragma unroll
-                    for (int i = 0; i < E; ++i) {
+                    for (int i = j; i < j + kTogether; ++i) {
                         const float p = kExact ? v[u][i] : __fmul_rn(v[u][i], gv[i]);
-                        q[i] = scaled_odd(p * up, kExact ? 0.0f : __fmaf_rn(v[u][i], gv[i], -p) * up, ch, cl);
+                        q[i] = __fmul_rn(p, ch);
+                        near = min(near, (__float_as_uint(q[i]) - 0x7FFFEu) & 0xFFFFFu);
+                        least = fminf(least, fabsf(q[i]));
+                    }
+                    if (near <= 4u || !(least >= 0x1p-6f) || odd) {
+#pragma unroll
+                        for (int i = j; i < j + kTogether; ++i) {
+                            const float p = kExact ? v[u][i] : __fmul_rn(v[u][i], gv[i]);
+                            q[i] = scaled_odd(p * up, kExact ? 0.0f : __fmaf_rn(v[u][i], gv[i], -p) * up, ch, cl);
+                        }
                     }
                 }
                 uint32_t codes[E / 4];

@@ -14,21 +14,27 @@ constexpr int kOrthoNormParts = 1024;   // partial sums of squares, over the who
 inline int64_t ortho_pitch(int64_t cols) { return (cols + 63) / 64 * 64; }
 
 // Products of one step on a batch of matrices.  X is [rows, cols] (pitch elements a row);
-// G and P are square on the short side.
-//   kNsGram    G = alpha X X^T (rows <= cols) or alpha X^T X       symmetric
-//   kNsSquare  P = b G + c G G, diag = what rounding took from P's diagonal    symmetric
-//   kNsUpdate  X' = (a + diag) X + P X or X P;  o: alpha X' in bf16 instead
-enum NsOp : int { kNsGram = 0, kNsSquare = 1, kNsUpdate = 2 };
+// G, P and the other y are square on the short side and symmetric.
+//   kNsGram    out = alpha X X^T (rows <= cols) or alpha X^T X
+//   kNsSquare  out = b Y + c Y Y, diag_out = what rounding took from out's diagonal
+//   kNsApply   out = (a + diag) Y + P Y
+//   kNsJoin    out = (a + diag) Y + P Y + b P with Y's own remainders diag2: the polynomial of two
+//              steps, (a I + P) (b I + Y) less a b I; diag_out as above
+//   kNsUpdate  out = (a + diag) X + P X or X P;  o: alpha times it in bf16 instead
+// diag: the remainders of P's diagonal.
+enum NsOp : int { kNsGram = 0, kNsSquare = 1, kNsUpdate = 2, kNsApply = 3, kNsJoin = 4 };
 
 struct NsProduct {
     int op;
     bool tall;                 // rows > cols
     int64_t rows, cols;        // of X
     int batch;
-    const __half *x, *x_lo;    // kNsGram, kNsUpdate; x_lo NULL: none
-    const __half *g;           // kNsSquare: G; kNsUpdate: P
-    float *diag;               // [batch][short side], written by kNsSquare
-    __half *out, *out_lo;      // G, P or X'; out_lo NULL: none
+    const __half *x, *x_lo;    // kNsGram, kNsUpdate: X; x_lo NULL: none
+    const __half *y;           // kNsSquare, kNsApply, kNsJoin: Y
+    const __half *p;           // kNsApply, kNsJoin, kNsUpdate: P
+    const float *diag, *diag2; // [batch][short side]
+    float *diag_out;
+    __half *out, *out_lo;      // out_lo NULL: none
     void *o;                   // kNsUpdate: bf16 [batch][rows][cols] in place of out
     float alpha, a, b, c;
 };
