@@ -1644,7 +1644,7 @@ OrthoLayout ortho_layout(const mlpblk_ortho_desc *d) {
     l.x[1] = take(x);
     l.lo = take(x);
     for (int64_t &at : l.g) at = take(g);
-    for (int64_t &at : l.diag) at = take(m * d->batch * 4);
+    for (int64_t &at : l.diag) at = take(ortho_pitch(m) * d->batch * 4);
     l.partial = take((d->batch > kOrthoNormParts ? d->batch : kOrthoNormParts) * static_cast<int64_t>(8));
     l.total = off;
     return l;

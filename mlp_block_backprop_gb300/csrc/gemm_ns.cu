@@ -52,12 +52,13 @@ struct NsArgs {
     int pitch;                          // elements of a row of out, aux
     int64_t matrix;                     // elements of a matrix of out, aux
     const __half *aux, *aux2;           // [rows][cols]: Y or X; X's low part (or NULL), or P (kNsJoin)
-    const float *diag, *diag2;          // [batch][diag_n]
+    const float *diag, *diag2;          // [batch][diag_pitch]
     float *diag_out;
-    int diag_n;
+    int diag_pitch;                     // a multiple of 64
     bool diag_col;                      // kNsUpdate: diag goes by column (tall)
     __half *out, *out_lo;
     uint16_t *o;                        // bf16 [batch][rows][cols]
+    bool o_tma;                         // rows of o are whole 16-byte pieces
     float alpha, a, b, c;
 };
 
@@ -129,12 +130,6 @@ __device__ __forceinline__ uint32_t cluster_nctarank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
-}
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
-    return v;
 }
 
 __device__ __forceinline__ void tma_load_4d(const CUtensorMap *map, uint64_t *bar, void *dst, int32_t c0, int32_t c1, int32_t c2,
@@ -213,133 +208,191 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 __device__ __forceinline__ float2 unpack_half2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
 
-// What the epilogue of a row's CH columns reads besides the accumulator, loaded ahead of it.
+template <int OP>
+constexpr bool kNsOne = OP != kNsGram;                      // reads a tile besides the accumulator
 template <int OP>
 constexpr bool kNsTwo = OP == kNsUpdate || OP == kNsJoin;   // two tiles
 template <int OP>
 constexpr bool kNsScaled = OP == kNsUpdate || OP == kNsApply || OP == kNsJoin;   // (a + diag) times the first
-template <int OP, int CH>
-struct NsAux {
-    uint4 hi[OP == kNsGram ? 1 : CH / 8], lo[kNsTwo<OP> ? CH / 8 : 1];
-    float d;           // the row's diag (kNsScaled, but tall updates)
+
+// The step's arithmetic on a pair of columns (col, col + 1) of a row: v the accumulators, p and q the first and
+// second tile's values, d the row's diag, dc the columns' (tall updates, kNsJoin's diag2).
+template <int OP>
+__device__ __forceinline__ float2 ns_combine(const NsArgs &a, float2 v, float2 p, float2 q, float d, float2 dc, int row, int col) {
+    if (OP == kNsGram) return make_float2(a.alpha * v.x, a.alpha * v.y);
+    if (OP == kNsSquare) return make_float2(a.b * p.x + a.c * v.x, a.b * p.y + a.c * v.y);
+    if (OP == kNsApply) return make_float2((a.a + d) * p.x + v.x, (a.a + d) * p.y + v.y);
+    if (OP == kNsJoin) {
+        float2 r = make_float2((a.a + d) * p.x + (a.b + dc.x) * q.x + v.x, (a.a + d) * p.y + (a.b + dc.y) * q.y + v.y);
+        if (col == row) r.x += (a.a + d) * dc.x + a.b * d;
+        if (col + 1 == row) r.y += (a.a + d) * dc.y + a.b * d;
+        return r;
+    }
+    const float d0 = a.diag_col ? dc.x : d, d1 = a.diag_col ? dc.y : d;
+    return make_float2((a.a + d0) * (p.x + q.x) + v.x, (a.a + d1) * (p.y + q.y) + v.y);
+}
+
+// Tensor maps of the epilogue: chunks of 32 rows x 64 columns (128 bytes, swizzled) of what it reads and
+// writes, and of its mirror image (32 columns x 64 rows, as they lie).
+struct NsMaps {
+    CUtensorMap aux, aux2, out, out_lo, mirror;
 };
 
-template <int OP, int CH>
-__device__ __forceinline__ void ns_load_aux(const NsArgs &a, const NsTile &w, int row, int col, NsAux<OP, CH> &x) {
-    if (OP == kNsGram) return;
-    const bool on = row < a.rows && col < a.cols;
-    const int64_t at = w.batch * a.matrix + static_cast<int64_t>(row) * a.pitch + col;
-#pragma unroll
-    for (int i = 0; i < CH / 8; ++i) {
-        x.hi[i] = on ? *reinterpret_cast<const uint4 *>(a.aux + at + 8 * i) : make_uint4(0, 0, 0, 0);
-        if (kNsTwo<OP>) x.lo[i] = on && (OP == kNsJoin || a.aux2) ? *reinterpret_cast<const uint4 *>(a.aux2 + at + 8 * i) : make_uint4(0, 0, 0, 0);
-    }
-    if (kNsScaled<OP>) x.d = on && !a.diag_col ? a.diag[static_cast<int64_t>(w.batch) * a.diag_n + row] : 0.0f;
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int32_t c0, int32_t c1, int32_t c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
 }
 
-// CH columns from `col` on of the lane's row: the step's arithmetic and the stores.  The
-// whole warp calls it (the mirror image pairs neighbouring rows).  Columns up to the pitch
-// may be written: pads are nobody's.
-template <int OP, int CH>
-__device__ __forceinline__ void ns_finish(const NsArgs &a, const NsTile &w, int row, int col, const NsAux<OP, CH> &x, float (&v)[CH]) {
-    if (col >= a.cols) return;
-    const bool on = row < a.rows;
-    const int64_t at = w.batch * a.matrix + static_cast<int64_t>(row) * a.pitch + col;
-    if (OP == kNsGram) {
+constexpr int kNsChunkBytes = 32 * 128;
+constexpr int kNsStaging = 2 * kNsChunkBytes;   // a warp's: the first tile's chunk, in whose place the output is
+                                                // staged, and the second one's, or the output's low part, or the image
+
+// One warp's part of every tile: rows [row0, row0 + 32) of the CTA's, CHUNKS chunks of 64 columns from col0 on.
+// buf0, buf1: its staging; bar: the barrier of its loads; `loads`: how many it has waited for.
+template <int OP>
+struct NsEpilogue {
+    const NsArgs &a;
+    const NsMaps &maps;
+    uint8_t *buf0, *buf1;
+    uint64_t *bar;
+    volatile int *abort;
+    int lane;
+    uint32_t phase;
+
+    __device__ __forceinline__ bool on(const NsTile &, int row0, int col0) const { return row0 < a.rows && col0 < a.cols; }
+    __device__ __forceinline__ bool second() const { return OP == kNsJoin || (OP == kNsUpdate && a.aux2 != nullptr); }
+
+    // Asks for a chunk's tiles, once the stores from the same place have read it.
+    __device__ __forceinline__ void load(const NsTile &w, int row0, int col0) {
+        if (!kNsOne<OP> || !on(w, row0, col0)) return;
+        if (lane == 0) {
+            bulk_wait_group_read<0>();
+            mbar_expect_relaxed(bar, second() ? 2 * kNsChunkBytes : kNsChunkBytes);
+            tma_load_3d(&maps.aux, bar, buf0, col0, row0, w.batch);
+            if (second()) tma_load_3d(&maps.aux2, bar, buf1, col0, row0, w.batch);
+        }
+        __syncwarp();
+    }
+
+    // The chunk from its accumulators v (row `lane`, 64 columns).  The whole warp calls it.
+    __device__ __forceinline__ bool finish(const NsTile &w, int row0, int col0, float (&v)[64]) {
+        if (!on(w, row0, col0)) return true;
+        const int row = row0 + lane;
+        const uint32_t at0 = smem_u32(buf0) + lane * 128, at1 = smem_u32(buf1) + lane * 128;
+        const uint32_t sw = static_cast<uint32_t>(lane & 7);
+        if (kNsOne<OP>) {
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase, abort));
+            phase ^= 1u;
+            if (!ok) return false;
+        } else {
+            if (lane == 0) bulk_wait_group_read<0>();   // the staging is free again
+            __syncwarp();
+        }
+        const int64_t dat = static_cast<int64_t>(w.batch) * a.diag_pitch;
+        const float d = kNsScaled<OP> && !a.diag_col && row < a.rows ? a.diag[dat + row] : 0.0f;
+        const float *by_col = OP == kNsJoin ? a.diag2 : (OP == kNsUpdate && a.diag_col ? a.diag : nullptr);
+        const bool two = second();
 #pragma unroll
-        for (int i = 0; i < CH; ++i) v[i] *= a.alpha;
-    } else {
-        const uint32_t *h = reinterpret_cast<const uint32_t *>(x.hi);
-        const uint32_t *l = reinterpret_cast<const uint32_t *>(x.lo);
+        for (int j = 0; j < 8; ++j) {   // eight columns: 16 bytes of each tile
+            const uint32_t off = (static_cast<uint32_t>(j) ^ sw) << 4;
+            uint4 x = make_uint4(0, 0, 0, 0), y = make_uint4(0, 0, 0, 0);
+            if (kNsOne<OP>) x = ld_shared_v4(at0 + off);
+            if (kNsTwo<OP> && two) y = ld_shared_v4(at1 + off);
+            float4 c0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), c1 = c0;
+            if (kNsTwo<OP> && by_col) {   // (the pitch is a multiple of 64)
+                c0 = __ldg(reinterpret_cast<const float4 *>(by_col + dat + col0 + 8 * j));
+                c1 = __ldg(reinterpret_cast<const float4 *>(by_col + dat + col0 + 8 * j + 4));
+            }
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+            const float2 cs[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
 #pragma unroll
-        for (int i = 0; i < CH / 2; ++i) {
-            const float2 p = unpack_half2(h[i]);
-            if (OP == kNsSquare) {
-                v[2 * i] = a.b * p.x + a.c * v[2 * i];
-                v[2 * i + 1] = a.b * p.y + a.c * v[2 * i + 1];
-            } else if (OP == kNsApply) {
-                v[2 * i] = (a.a + x.d) * p.x + v[2 * i];
-                v[2 * i + 1] = (a.a + x.d) * p.y + v[2 * i + 1];
-            } else if (OP == kNsJoin) {
-                const float2 q = unpack_half2(l[i]);
-                const float *d2 = a.diag2 + static_cast<int64_t>(w.batch) * a.diag_n;
-                const int c0 = col + 2 * i, c1 = c0 + 1;
-                const float e0 = c0 < a.cols ? __ldg(d2 + c0) : 0.0f, e1 = c1 < a.cols ? __ldg(d2 + c1) : 0.0f;
-                v[2 * i] = (a.a + x.d) * p.x + (a.b + e0) * q.x + v[2 * i];
-                v[2 * i + 1] = (a.a + x.d) * p.y + (a.b + e1) * q.y + v[2 * i + 1];
-                if (c0 == row) v[2 * i] += (a.a + x.d) * e0 + a.b * x.d;
-                if (c1 == row) v[2 * i + 1] += (a.a + x.d) * e1 + a.b * x.d;
-            } else {
-                const float2 q = unpack_half2(l[i]);
-                float d0 = x.d, d1 = x.d;
-                if (a.diag_col) {
-                    const float *d = a.diag + static_cast<int64_t>(w.batch) * a.diag_n;
-                    d0 = col + 2 * i < a.cols ? __ldg(d + col + 2 * i) : 0.0f;
-                    d1 = col + 2 * i + 1 < a.cols ? __ldg(d + col + 2 * i + 1) : 0.0f;
-                }
-                v[2 * i] = (a.a + d0) * (p.x + q.x) + v[2 * i];
-                v[2 * i + 1] = (a.a + d1) * (p.y + q.y) + v[2 * i + 1];
+            for (int i = 0; i < 4; ++i) {
+                const int k = 8 * j + 2 * i;
+                const float2 r = ns_combine<OP>(a, make_float2(v[k], v[k + 1]), unpack_half2(xs[i]), unpack_half2(ys[i]), d, cs[i], row, col0 + k);
+                v[k] = r.x;
+                v[k + 1] = r.y;
             }
         }
-    }
-    if (OP == kNsUpdate && a.o) {
-        uint16_t *o = a.o + (static_cast<int64_t>(w.batch) * a.rows + row) * a.cols + col;
-        if (!on) return;
-        if (a.cols % 8 == 0) {
+        if (OP == kNsUpdate && a.o) {
 #pragma unroll
-            for (int i = 0; i < CH / 8; ++i)
-                if (col + 8 * i < a.cols)
-                    *reinterpret_cast<uint4 *>(o + 8 * i) = make_uint4(
-                        pack_bf16x2(a.alpha * v[8 * i], a.alpha * v[8 * i + 1]), pack_bf16x2(a.alpha * v[8 * i + 2], a.alpha * v[8 * i + 3]),
-                        pack_bf16x2(a.alpha * v[8 * i + 4], a.alpha * v[8 * i + 5]), pack_bf16x2(a.alpha * v[8 * i + 6], a.alpha * v[8 * i + 7]));
+            for (int j = 0; j < 8; ++j) {
+                const float *e = &v[8 * j];
+                st_shared_v4(at0 + ((static_cast<uint32_t>(j) ^ sw) << 4), pack_bf16x2(a.alpha * e[0], a.alpha * e[1]), pack_bf16x2(a.alpha * e[2], a.alpha * e[3]),
+                             pack_bf16x2(a.alpha * e[4], a.alpha * e[5]), pack_bf16x2(a.alpha * e[6], a.alpha * e[7]));
+            }
+            if (!a.o_tma) {
+                // rows of any length: a row a step, neighbouring lanes neighbouring columns
+                __syncwarp();
+                const int n_rows = min(32, a.rows - row0);
+                uint16_t *o = a.o + (static_cast<int64_t>(w.batch) * a.rows + row0) * a.cols + col0 + lane;
+                const bool in0 = col0 + lane < a.cols, in1 = col0 + lane + 32 < a.cols;
+                for (int r = 0; r < n_rows; ++r, o += a.cols) {
+                    const uint8_t *from = buf0 + r * 128;
+                    const int b0 = 2 * lane, b1 = b0 + 64;
+                    if (in0) o[0] = *reinterpret_cast<const uint16_t *>(from + ((((b0 >> 4) ^ (r & 7)) << 4) | (b0 & 15)));
+                    if (in1) o[32] = *reinterpret_cast<const uint16_t *>(from + ((((b1 >> 4) ^ (r & 7)) << 4) | (b1 & 15)));
+                }
+                __syncwarp();
+                return true;
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
-                if (col + i < a.cols) o[i] = static_cast<uint16_t>(pack_bf16x2(a.alpha * v[i], 0.0f) & 0xFFFFu);
-        }
-        return;
-    }
-    uint32_t h[CH / 2];
+            for (int j = 0; j < 8; ++j) {
+                const float *e = &v[8 * j];
+                const uint32_t off = (static_cast<uint32_t>(j) ^ sw) << 4;
+                const uint32_t h[4] = {pack_half2(e[0], e[1]), pack_half2(e[2], e[3]), pack_half2(e[4], e[5]), pack_half2(e[6], e[7])};
+                st_shared_v4(at0 + off, h[0], h[1], h[2], h[3]);
+                if (OP == kNsUpdate && a.out_lo) {
+                    uint32_t l[4];
 #pragma unroll
-    for (int i = 0; i < CH / 2; ++i) h[i] = pack_half2(v[2 * i], v[2 * i + 1]);
-    if (on) {
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 p = unpack_half2(h[i]);
+                        l[i] = pack_half2(e[2 * i] - p.x, e[2 * i + 1] - p.y);
+                    }
+                    st_shared_v4(at1 + off, l[0], l[1], l[2], l[3]);
+                }
+                if ((OP == kNsSquare || OP == kNsJoin) && row < a.rows && row >= col0 + 8 * j && row < col0 + 8 * j + 8) {
 #pragma unroll
-        for (int i = 0; i < CH / 8; ++i) *reinterpret_cast<uint4 *>(a.out + at + 8 * i) = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-        if (OP == kNsUpdate && a.out_lo) {
-            uint32_t l[CH / 2];
-#pragma unroll
-            for (int i = 0; i < CH / 2; ++i) {
-                const float2 p = unpack_half2(h[i]);
-                l[i] = pack_half2(v[2 * i] - p.x, v[2 * i + 1] - p.y);
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 p = unpack_half2(h[i / 2]);
+                        if (col0 + 8 * j + i == row) a.diag_out[dat + row] = e[i] - (i & 1 ? p.y : p.x);
+                    }
+                }
             }
+            if (OP != kNsUpdate && w.mirror) {
+                if (kNsTwo<OP>) __syncwarp();   // every lane has read its row of the second tile
+                // the image's row j holds this chunk's column j: 32 values, 64 bytes; two lanes swap every
+                // other value, so that a store is a pair
+                const int odd = lane & 1;
+                uint32_t to = smem_u32(buf1) + odd * 64 + (lane - odd) * 2;
 #pragma unroll
-            for (int i = 0; i < CH / 8; ++i) *reinterpret_cast<uint4 *>(a.out_lo + at + 8 * i) = make_uint4(l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]);
-        }
-        if ((OP == kNsSquare || OP == kNsJoin) && row >= col && row < col + CH) {
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const float2 p = unpack_half2(h[i / 2]);
-                if (col + i == row) a.diag_out[static_cast<int64_t>(w.batch) * a.diag_n + row] = v[i] - (i & 1 ? p.y : p.x);
+                for (int j = 0; j < 64; j += 2) {
+                    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+                    const uint32_t u = odd ? pack_half2(got, v[j + 1]) : pack_half2(v[j], got);
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(u) : "memory");
+                    to += 128;
+                }
             }
         }
-    }
-    if (OP != kNsUpdate && w.mirror) {
-        // out[col + i][row]: lanes are neighbouring columns of the image; two lanes swap every
-        // other value, so that a store is a pair (rows behind a.rows are pads of the image's rows)
-        const int odd = row & 1;
-        __half *q = a.out + w.batch * a.matrix + static_cast<int64_t>(col + odd) * a.pitch + (row - odd);
-#pragma unroll
-        for (int i = 0; i < CH; i += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-            const uint32_t u = odd ? pack_half2(got, v[i + 1]) : pack_half2(v[i], got);
-            if (row - odd < a.rows && col + i + odd < a.cols) *reinterpret_cast<uint32_t *>(q) = u;
-            q += 2 * a.pitch;
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(&maps.out, buf0, col0, row0, w.batch);
+            if (OP == kNsUpdate && a.out_lo && !a.o) tma_store_3d(&maps.out_lo, buf1, col0, row0, w.batch);
+            if (OP != kNsUpdate && w.mirror) tma_store_3d(&maps.mirror, buf1, row0, col0, w.batch);
+            bulk_commit_group();
         }
+        __syncwarp();
+        return true;
     }
-}
+};
 
 // ------------------------------------------------------------------- ns_small
 
+// SPLIT: K is split over a cluster; the parts meet in `dump`, and a CTA finishes some of the
+// tile's rows, 16 neighbouring threads a row, straight from and to global memory.  No mirror images there:
+// a split is for products that leave SMs idle, so every tile is computed.
 template <bool SPLIT_>
 struct NsSmall {
     static constexpr bool SPLIT = SPLIT_;
@@ -347,29 +400,84 @@ struct NsSmall {
     static constexpr int kThreads = 64 + 32 * kEpiWarps;
     static constexpr int kOpBytes = 128 * 128;
     static constexpr int kStageBytes = 2 * kOpBytes;
-    static constexpr int kDumpBytes = SPLIT ? 128 * 128 * 4 : 0;   // this CTA's part of the tile
+    static constexpr int kDumpPitch = 132;          // floats of a row: 16-byte accesses of eight rows meet in no bank
+    static constexpr int kDumpBytes = SPLIT ? 128 * kDumpPitch * 4 : kEpiWarps * kNsStaging;
     static constexpr int kCtrlBytes = 1024;
     static constexpr int kStages = (kSmemLimit - 1024 - kCtrlBytes - kDumpBytes) / kStageBytes;
     static constexpr int kSmemBytes = 1024 + kCtrlBytes + kDumpBytes + kStages * kStageBytes;
     static_assert(kStages >= 4, "pipeline");
 };
 
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+// Eight columns from col on of a row, whose sums are v: the split kernel's epilogue.
+template <int OP>
+__device__ __forceinline__ void ns_finish_eight(const NsArgs &a, const NsTile &w, int row, int col, const uint4 &x, const uint4 &y, float (&v)[8]) {
+    if (row >= a.rows || col >= a.cols) return;
+    const int64_t at = w.batch * a.matrix + static_cast<int64_t>(row) * a.pitch + col;
+    const int64_t dat = static_cast<int64_t>(w.batch) * a.diag_pitch;
+    const float d = kNsScaled<OP> && !a.diag_col ? a.diag[dat + row] : 0.0f;
+    const float *by_col = OP == kNsJoin ? a.diag2 : (OP == kNsUpdate && a.diag_col ? a.diag : nullptr);
+    float4 c0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), c1 = c0;
+    if (kNsTwo<OP> && by_col) {
+        c0 = __ldg(reinterpret_cast<const float4 *>(by_col + dat + col));
+        c1 = __ldg(reinterpret_cast<const float4 *>(by_col + dat + col + 4));
+    }
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    const float2 cs[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 r = ns_combine<OP>(a, make_float2(v[2 * i], v[2 * i + 1]), unpack_half2(xs[i]), unpack_half2(ys[i]), d, cs[i], row, col + 2 * i);
+        v[2 * i] = r.x;
+        v[2 * i + 1] = r.y;
+        h[i] = pack_half2(r.x, r.y);
+        const float2 p = unpack_half2(h[i]);
+        l[i] = pack_half2(r.x - p.x, r.y - p.y);
+        if (OP == kNsSquare || OP == kNsJoin) {
+            if (col + 2 * i == row) a.diag_out[dat + row] = r.x - p.x;
+            if (col + 2 * i + 1 == row) a.diag_out[dat + row] = r.y - p.y;
+        }
+    }
+    if (OP == kNsUpdate && a.o) {
+        uint16_t *o = a.o + (static_cast<int64_t>(w.batch) * a.rows + row) * a.cols + col;
+        if (a.o_tma) {
+            *reinterpret_cast<uint4 *>(o) = make_uint4(pack_bf16x2(a.alpha * v[0], a.alpha * v[1]), pack_bf16x2(a.alpha * v[2], a.alpha * v[3]),
+                                                       pack_bf16x2(a.alpha * v[4], a.alpha * v[5]), pack_bf16x2(a.alpha * v[6], a.alpha * v[7]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col + i < a.cols) o[i] = static_cast<uint16_t>(pack_bf16x2(a.alpha * v[i], 0.0f) & 0xFFFFu);
+        }
+        return;
+    }
+    // (the pitch is a multiple of 64: what lies behind the last column is nobody's)
+    *reinterpret_cast<uint4 *>(a.out + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    if (OP == kNsUpdate && a.out_lo) *reinterpret_cast<uint4 *>(a.out_lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
 template <class C, int OP, bool AMN, bool BMN>
 __global__ void __launch_bounds__(C::kThreads, 1)
-ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const NsArgs args) {
-    constexpr bool SYM = OP != kNsUpdate;
+ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const __grid_constant__ NsMaps maps, const NsArgs args) {
+    constexpr bool SYM = OP != kNsUpdate && !C::SPLIT;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *a_s = smem, *b_s = a_s + S * C::kOpBytes;
-    float *dump = reinterpret_cast<float *>(b_s + S * C::kOpBytes);   // [column][row]
-    uint8_t *ctrl = reinterpret_cast<uint8_t *>(dump) + C::kDumpBytes;
+    uint8_t *staging = b_s + S * C::kOpBytes;                // the epilogue warps' chunks, or
+    float *dump = reinterpret_cast<float *>(staging);        // [row][column], pitch kDumpPitch
+    uint8_t *ctrl = staging + C::kDumpBytes;
     uint64_t *full_bar = reinterpret_cast<uint64_t *>(ctrl);
     uint64_t *empty_bar = full_bar + S;
     uint64_t *accf_bar = empty_bar + S;
     uint64_t *acce_bar = accf_bar + 2;
     uint64_t *part_full = acce_bar + 2;   // every CTA of the cluster has its part in `dump`
     uint64_t *part_empty = part_full + 1; // every CTA has read this CTA's part
+    uint64_t *aux_bar = part_empty + 1;   // a warp's chunk has been loaded
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctrl + 512);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 516);
 
@@ -388,6 +496,7 @@ ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         }
         mbar_init(part_full, cs);
         mbar_init(part_empty, cs);
+        for (int b = 0; b < C::kEpiWarps; ++b) mbar_init(&aux_bar[b], 1);
         *abort_flag = 0;
         fence_barrier_init();
         prefetch_tensormap(&tmA);
@@ -470,86 +579,104 @@ ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             __syncwarp();
         }
         __syncwarp();
+    } else if constexpr (!C::SPLIT) {
+        const int q = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
+        uint8_t *st = staging + ew * kNsStaging;
+        NsEpilogue<OP> epi = {args, maps, st, st + kNsChunkBytes, &aux_bar[ew], abort_flag, lane, 0};
+        auto place = [&](const NsTile &x, int &row, int &col) { row = x.m0 + 32 * q, col = x.n0 + 64 * half; };
+        int it = 0, row, col;
+        if (t < args.tiles) {
+            place(w, row, col);
+            epi.load(w, row, col);
+        }
+        while (t < args.tiles) {
+            place(w, row, col);
+            const int buf = it & 1;
+            bool ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after_sync();
+            float v[64];
+            tmem_load_64cols(tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * 128 + 64 * half, *reinterpret_cast<float(*)[32]>(&v[0]),
+                             *reinterpret_cast<float(*)[32]>(&v[32]));
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_relaxed(&acce_bar[buf]);
+            if (!epi.finish(w, row, col, v)) break;
+            next();
+            ++it;
+            if (t < args.tiles) {
+                place(w, row, col);
+                epi.load(w, row, col);
+            }
+        }
+        if (lane == 0) {
+            bulk_wait_group<0>();
+            if (*abort_flag) mbar_drain(&aux_bar[ew], epi.phase);   // a load may still be on its way
+        }
+        __syncwarp();
     } else {
         // A warp that gave up on a wait keeps walking (its waits then return at once), so that
         // the barriers of the cluster's sum stay in step.
         const int q = warp & 3, half = (warp - 2) >> 2;
-        const int i = 32 * q + lane;
+        const int i = 32 * q + lane, tid = static_cast<int>(threadIdx.x) - 64;
         constexpr int kEpiThreads = 32 * C::kEpiWarps;
+        const int rows = 128 / cs, first = rank * rows;      // this CTA's rows of the tile
         int it = 0;
         for (; t < args.tiles; next(), ++it) {
-            const int row = w.m0 + i;
             const bool some = k1 > k0;
             const int buf = it & 1;
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * 128;
-            bool ok;
-            if (!C::SPLIT) {
-                NsAux<OP, 32> x[2];
-                ns_load_aux<OP, 32>(args, w, row, w.n0 + 64 * half, x[0]);
-                ns_load_aux<OP, 32>(args, w, row, w.n0 + 64 * half + 32, x[1]);
-                ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort_flag));
-                tc_fence_after_sync();
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float v[32];
-                    tmem_load_32cols(t_row + 64 * half + 32 * c, v);
-                    if (c == 1) {
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_relaxed(&acce_bar[buf]);
-                    }
-                    if (ok) ns_finish<OP, 32>(args, w, row, w.n0 + 64 * half + 32 * c, x[c], v);
+            // the first rows' tiles, ahead of the sums
+            const int r0 = tid >> 4, c0 = (tid & 15) * 8;
+            uint4 x = make_uint4(0, 0, 0, 0), y = x;
+            auto fetch = [&](int r) {
+                const int row = w.m0 + first + r, col = w.n0 + c0;
+                if (kNsOne<OP> && row < args.rows && col < args.cols) {
+                    const int64_t at = w.batch * args.matrix + static_cast<int64_t>(row) * args.pitch + col;
+                    x = *reinterpret_cast<const uint4 *>(args.aux + at);
+                    if (kNsTwo<OP> && args.aux2) y = *reinterpret_cast<const uint4 *>(args.aux2 + at);
                 }
-            } else {
-                ok = mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort_flag);
-                tc_fence_after_sync();
-                ok = mbar_wait_cluster(part_empty, (it & 1) ^ 1u, abort_flag) && ok;
-                ok = __all_sync(0xffffffffu, ok);
-                for (int c0 = half * 64; c0 < half * 64 + 64; c0 += 32) {
-                    float v[32];
-                    if (some && ok) {
-                        tmem_load_32cols(t_row + c0, v);
-                    } else {
+            };
+            fetch(r0);
+            bool ok = mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort_flag);
+            tc_fence_after_sync();
+            ok = mbar_wait_cluster(part_empty, (it & 1) ^ 1u, abort_flag) && ok;
+            ok = __all_sync(0xffffffffu, ok);
+            for (int c = half * 64; c < half * 64 + 64; c += 32) {
+                float v[32];
+                if (some && ok) {
+                    tmem_load_32cols(tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * 128 + c, v);
+                } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) dump[(c0 + j) * 128 + i] = v[j];
+                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                 }
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_relaxed(&acce_bar[buf]);
-                named_barrier_sync(1, kEpiThreads);
-                if (threadIdx.x >= 64 && threadIdx.x < 64 + cs)
-                    mbar_arrive_cluster(mapa_shared(smem_u32(part_full), threadIdx.x - 64));
-                // this CTA finishes the columns [128 rank / cs, 128 (rank + 1) / cs), 16 at a time
-                const int width = 128 / cs, first = rank * width;
-                constexpr int CH = 16;
-                NsAux<OP, CH> x;
-                if (half * CH < width) ns_load_aux<OP, CH>(args, w, row, w.n0 + first + half * CH, x);
-                ok = mbar_wait_cluster(part_full, it & 1, abort_flag) && ok;
-                ok = __all_sync(0xffffffffu, ok);
-                if (ok) {
-                    for (int c0 = half * CH; c0 < width; c0 += 2 * CH) {
-                        float sum[CH];
 #pragma unroll
-                        for (int u = 0; u < CH; ++u) sum[u] = 0.0f;
-                        for (int r = 0; r < cs; ++r) {
-                            const uint32_t from = mapa_shared(smem_u32(dump + (first + c0) * 128 + i), r);
-                            float part[CH];
-#pragma unroll
-                            for (int u = 0; u < CH; ++u) part[u] = ld_cluster_f32(from + u * 512);
-#pragma unroll
-                            for (int u = 0; u < CH; ++u) sum[u] += part[u];
-                        }
-                        if (c0 != half * CH) ns_load_aux<OP, CH>(args, w, row, w.n0 + first + c0, x);
-                        ns_finish<OP, CH>(args, w, row, w.n0 + first + c0, x, sum);
-                    }
-                }
-                named_barrier_sync(1, kEpiThreads);
-                if (threadIdx.x >= 64 && threadIdx.x < 64 + cs)
-                    mbar_arrive_cluster(mapa_shared(smem_u32(part_empty), threadIdx.x - 64));
+                for (int j = 0; j < 32; j += 4)
+                    *reinterpret_cast<float4 *>(dump + i * C::kDumpPitch + c + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
             }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_relaxed(&acce_bar[buf]);
+            named_barrier_sync(1, kEpiThreads);
+            if (tid < cs) mbar_arrive_cluster(mapa_shared(smem_u32(part_full), tid));
+            ok = mbar_wait_cluster(part_full, it & 1, abort_flag) && ok;
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                for (int r = r0; r < rows; r += kEpiThreads / 16) {
+                    float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                    const uint32_t from = smem_u32(dump + (first + r) * C::kDumpPitch + c0);
+#pragma unroll 4
+                    for (int k = 0; k < cs; ++k) {
+                        const uint32_t at = mapa_shared(from, k);
+                        const float4 p = ld_cluster_v4(at), u = ld_cluster_v4(at + 16);
+                        sum[0] += p.x; sum[1] += p.y; sum[2] += p.z; sum[3] += p.w;
+                        sum[4] += u.x; sum[5] += u.y; sum[6] += u.z; sum[7] += u.w;
+                    }
+                    if (r != r0) fetch(r);
+                    ns_finish_eight<OP>(args, w, w.m0 + first + r, w.n0 + c0, x, y, sum);
+                }
+            }
+            named_barrier_sync(1, kEpiThreads);
+            if (tid < cs) mbar_arrive_cluster(mapa_shared(smem_u32(part_empty), tid));
         }
     }
 
@@ -569,24 +696,28 @@ struct NsPair {
     static constexpr int kOpBytes = 128 * 128;      // 128 rows of A or B a CTA
     static constexpr int kStageBytes = 2 * kOpBytes;
     static constexpr int kCtrlBytes = 1024;
-    static constexpr int kStages = (kSmemLimit - 1024 - kCtrlBytes) / kStageBytes;
-    static constexpr int kSmemBytes = 1024 + kCtrlBytes + kStages * kStageBytes;
+    static constexpr int kStagingBytes = 8 * kNsStaging;
+    static constexpr int kStages = (kSmemLimit - 1024 - kCtrlBytes - kStagingBytes) / kStageBytes;
+    static constexpr int kSmemBytes = 1024 + kCtrlBytes + kStagingBytes + kStages * kStageBytes;
+    static_assert(kStages >= 4, "pipeline");
 };
 
 template <int OP, bool AMN, bool BMN>
 __global__ void __launch_bounds__(NsPair::kThreads, 1)
-ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const NsArgs args) {
+ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const __grid_constant__ NsMaps maps, const NsArgs args) {
     using P = NsPair;
     constexpr bool SYM = OP != kNsUpdate;
     constexpr int S = P::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *a_s = smem, *b_s = a_s + S * P::kOpBytes;
-    uint8_t *ctrl = b_s + S * P::kOpBytes;
+    uint8_t *staging = b_s + S * P::kOpBytes;
+    uint8_t *ctrl = staging + P::kStagingBytes;
     uint64_t *full_bar = reinterpret_cast<uint64_t *>(ctrl);
     uint64_t *empty_bar = full_bar + S;
     uint64_t *accf_bar = empty_bar + S;
     uint64_t *acce_bar = accf_bar + 2;
+    uint64_t *aux_bar = acce_bar + 2;     // a warp's chunk has been loaded
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctrl + 512);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 516);
 
@@ -603,6 +734,7 @@ ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             mbar_init(&accf_bar[b], 1);
             mbar_init(&acce_bar[b], 16);  // both CTAs' epilogue warps (the leader's barrier counts)
         }
+        for (int b = 0; b < 8; ++b) mbar_init(&aux_bar[b], 1);
         *abort_flag = 0;
         fence_barrier_init();
         prefetch_tensormap(&tmA);
@@ -696,26 +828,29 @@ ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         }
         __syncwarp();
     } else {
-        // two warps a lane quarter: 128 columns each, 32 at a time
-        const int q = warp & 3, half = (warp - 2) >> 2;
+        // two warps a lane quarter: two chunks of 64 columns each
+        const int q = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
         const uint32_t acce0 = mapa_shared(smem_u32(&acce_bar[0]), 0);
-        int it = 0;
-        for (; t < args.tiles; next(), ++it) {
-            const int row = w.m0 + static_cast<int>(rank) * 128 + 32 * q + lane;
+        uint8_t *st = staging + ew * kNsStaging;
+        NsEpilogue<OP> epi = {args, maps, st, st + kNsChunkBytes, &aux_bar[ew], abort_flag, lane, 0};
+        auto place = [&](const NsTile &x, int &row, int &col) { row = x.m0 + static_cast<int>(rank) * 128 + 32 * q, col = x.n0 + 128 * half; };
+        int it = 0, row, col;
+        if (t < args.tiles) {
+            place(w, row, col);
+            epi.load(w, row, col);
+        }
+        while (t < args.tiles) {
+            place(w, row, col);
             const int buf = it & 1;
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * 256 + 128 * half;
-            const int col = w.n0 + 128 * half;
-            NsAux<OP, 32> x[2];
-            ns_load_aux<OP, 32>(args, w, row, col, x[0]);
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort_flag));
+            bool ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort_flag));
             if (!ok) break;
             tc_fence_after_sync();
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (c < 3) ns_load_aux<OP, 32>(args, w, row, col + 32 * (c + 1), x[(c + 1) & 1]);
-                float v[32];
-                tmem_load_32cols(t_row + 32 * c, v);
-                if (c == 3) {
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+                float v[64];
+                tmem_load_64cols(t_row + 64 * c, *reinterpret_cast<float(*)[32]>(&v[0]), *reinterpret_cast<float(*)[32]>(&v[32]));
+                if (c == 1) {
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) {
@@ -723,8 +858,21 @@ ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         else mbar_arrive_cluster_relaxed(acce0 + buf * 8);
                     }
                 }
-                ns_finish<OP, 32>(args, w, row, col + 32 * c, x[c & 1], v);
+                ok = epi.finish(w, row, col + 64 * c, v);
+                if (!ok) break;
+                if (c == 0) epi.load(w, row, col + 64);
             }
+            if (!ok) break;
+            next();
+            ++it;
+            if (t < args.tiles) {
+                place(w, row, col);
+                epi.load(w, row, col);
+            }
+        }
+        if (lane == 0) {
+            bulk_wait_group<0>();
+            if (*abort_flag) mbar_drain(&aux_bar[ew], epi.phase);   // a load may still be on its way
         }
         __syncwarp();
     }
@@ -762,10 +910,39 @@ bool ns_map(CUtensorMap *m, const __half *p, bool mn, int64_t rows, int64_t cols
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Boxes of `box_cols` x `box_rows` for the epilogue, of 16-bit values (fp16, or o's bf16).
+bool ns_chunk_map(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t pitch, int batch, uint32_t box_cols, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint64_t line = static_cast<cuuint64_t>(pitch) * 2;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
+    cuuint64_t strides[2] = {line, line * dims[1]};
+    cuuint32_t box[3] = {box_cols, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The maps that the epilogue of `a` uses.
+bool ns_epilogue_maps(NsMaps *m, const NsArgs &a, int batch) {
+    bool ok = true;
+    if (a.aux) ok &= ns_chunk_map(&m->aux, a.aux, a.rows, a.cols, a.pitch, batch, 64, 32);
+    if (a.aux2) ok &= ns_chunk_map(&m->aux2, a.aux2, a.rows, a.cols, a.pitch, batch, 64, 32);
+    if (a.o) {
+        if (a.o_tma) ok &= ns_chunk_map(&m->out, a.o, a.rows, a.cols, a.cols, batch, 64, 32);
+    } else {
+        ok &= ns_chunk_map(&m->out, a.out, a.rows, a.cols, a.pitch, batch, 64, 32);
+        if (a.out_lo) ok &= ns_chunk_map(&m->out_lo, a.out_lo, a.rows, a.cols, a.pitch, batch, 64, 32);
+    }
+    if (a.op != kNsUpdate) ok &= ns_chunk_map(&m->mirror, a.out, a.rows, a.cols, a.pitch, batch, 32, 64);
+    return ok;
+}
+
 // Cluster size 1: no cluster attribute.
 template <class K>
-int launch_ns(K kernel, int threads, int smem, int grid, int cluster, const CUtensorMap &mA, const CUtensorMap &mB, const NsArgs &a,
-              int *attr_set, cudaStream_t s) {
+int launch_ns(K kernel, int threads, int smem, int grid, int cluster, const CUtensorMap &mA, const CUtensorMap &mB, const NsMaps &maps,
+              const NsArgs &a, int *attr_set, cudaStream_t s) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) return MLPBLK_ECUDA;
@@ -788,7 +965,7 @@ int launch_ns(K kernel, int threads, int smem, int grid, int cluster, const CUte
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, mA, mB, a));
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, mA, mB, maps, a));
 }
 
 int64_t tiles_of(const NsArgs &a, int ts, bool sym) {
@@ -802,6 +979,7 @@ int run_ns(NsArgs a, const CUtensorMap &mA, const CUtensorMap &mB, int batch, in
     const int64_t pair_tiles = tiles_of(a, 256, SYM) * batch, tiles = tiles_of(a, 128, SYM) * batch;
     const int pairs = sms / 2;
     if (tiles > INT32_MAX) return MLPBLK_EINVAL;
+    NsMaps maps = {};
     if (pairs >= 1 && 2 * pair_tiles >= pairs && a.rows > 128 && a.cols > 128) {
         static int attr_set[64] = {0};
         a.mt = (a.rows + 255) / 256;
@@ -810,26 +988,28 @@ int run_ns(NsArgs a, const CUtensorMap &mA, const CUtensorMap &mB, int batch, in
         a.tiles = static_cast<int>(pair_tiles);
         a.group_m = 8;
         const int workers = a.tiles < pairs ? a.tiles : pairs;
-        return launch_ns(ns_pair_kernel<OP, AMN, BMN>, NsPair::kThreads, NsPair::kSmemBytes, 2 * workers, 2, mA, mB, a, attr_set, s);
+        if (!ns_epilogue_maps(&maps, a, batch)) return MLPBLK_ECUDA;
+        return launch_ns(ns_pair_kernel<OP, AMN, BMN>, NsPair::kThreads, NsPair::kSmemBytes, 2 * workers, 2, mA, mB, maps, a, attr_set, s);
     }
     a.mt = (a.rows + 127) / 128;
     a.nt = (a.cols + 127) / 128;
+    a.group_m = 8;
+    const int64_t every = static_cast<int64_t>(a.mt) * a.nt * batch;   // a split computes the images too
+    int split = 1;
+    while (split < 8 && every * split * 2 <= sms && a.kblocks >= 4 * split) split *= 2;
+    if (split > 1) {
+        a.per = a.mt * a.nt;
+        a.tiles = static_cast<int>(every);
+        static int attr_set[64] = {0};
+        return launch_ns(ns_small_kernel<NsSmall<true>, OP, AMN, BMN>, NsSmall<true>::kThreads, NsSmall<true>::kSmemBytes, a.tiles * split,
+                         split, mA, mB, maps, a, attr_set, s);
+    }
     a.per = static_cast<int>(tiles / batch);
     a.tiles = static_cast<int>(tiles);
-    a.group_m = 8;
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= sms && a.kblocks >= 4 * split) split *= 2;
-    int workers = sms / split;
-    if (workers < 1) workers = 1;
-    if (a.tiles < workers) workers = a.tiles;
-    if (split > 1) {
-        static int attr_set[64] = {0};
-        return launch_ns(ns_small_kernel<NsSmall<true>, OP, AMN, BMN>, NsSmall<true>::kThreads, NsSmall<true>::kSmemBytes, workers * split,
-                         split, mA, mB, a, attr_set, s);
-    }
+    if (!ns_epilogue_maps(&maps, a, batch)) return MLPBLK_ECUDA;
     static int attr_set[64] = {0};
-    return launch_ns(ns_small_kernel<NsSmall<false>, OP, AMN, BMN>, NsSmall<false>::kThreads, NsSmall<false>::kSmemBytes, workers, 1, mA, mB,
-                     a, attr_set, s);
+    return launch_ns(ns_small_kernel<NsSmall<false>, OP, AMN, BMN>, NsSmall<false>::kThreads, NsSmall<false>::kSmemBytes, a.tiles < sms ? a.tiles : sms, 1,
+                     mA, mB, maps, a, attr_set, s);
 }
 
 }  // namespace
@@ -846,10 +1026,11 @@ int launch_ns_product(const NsProduct &p, int sms, cudaStream_t s) {
     a.diag = p.diag;
     a.diag2 = p.diag2;
     a.diag_out = p.diag_out;
-    a.diag_n = static_cast<int>(m);
+    a.diag_pitch = static_cast<int>(g_pitch);
     a.out = p.out;
     a.out_lo = p.out_lo;
     a.o = static_cast<uint16_t *>(p.o);
+    a.o_tma = p.cols % 8 == 0;
     a.kblocks = static_cast<int>((m + kNsK - 1) / kNsK);
     CUtensorMap mA, mB;
     if (p.op == kNsUpdate) {
@@ -877,7 +1058,7 @@ int launch_ns_product(const NsProduct &p, int sms, cudaStream_t s) {
         return p.tall ? run_ns<kNsGram, true, true>(a, mA, mA, p.batch, sms, s) : run_ns<kNsGram, false, false>(a, mA, mA, p.batch, sms, s);
     }
     a.aux = p.y;
-    a.aux2 = p.p;
+    if (p.op == kNsJoin) a.aux2 = p.p;
     if (!ns_map(&mB, p.y, false, m, m, g_pitch, p.batch)) return MLPBLK_ECUDA;
     if (p.op == kNsSquare) return run_ns<kNsSquare, false, false>(a, mB, mB, p.batch, sms, s);
     if (!ns_map(&mA, p.p, false, m, m, g_pitch, p.batch)) return MLPBLK_ECUDA;

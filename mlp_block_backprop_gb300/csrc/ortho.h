@@ -32,7 +32,7 @@ struct NsProduct {
     const __half *x, *x_lo;    // kNsGram, kNsUpdate: X; x_lo NULL: none
     const __half *y;           // kNsSquare, kNsApply, kNsJoin: Y
     const __half *p;           // kNsApply, kNsJoin, kNsUpdate: P
-    const float *diag, *diag2; // [batch][short side]
+    const float *diag, *diag2; // [batch][ortho_pitch(short side)]
     float *diag_out;
     __half *out, *out_lo;      // out_lo NULL: none
     void *o;                   // kNsUpdate: bf16 [batch][rows][cols] in place of out
