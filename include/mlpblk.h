@@ -872,6 +872,7 @@ int mlpblk_rmsnorm_backward_noalloc(const mlpblk_desc *desc, const void *x, cons
 #define MLPBLK_KERNEL_MUON_APPLY     43  /* master, weight                            */
 #define MLPBLK_KERNEL_NS_APPLY       44  /* Y = a Y + P Y (two steps at a time)       */
 #define MLPBLK_KERNEL_NS_JOIN        45  /* the polynomial of two steps               */
+#define MLPBLK_KERNEL_NS_STEPS       46  /* every step of small matrices              */
 
 /*
  * mlpblk_trace_begin: from now on, launch i of this library records

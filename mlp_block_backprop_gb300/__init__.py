@@ -74,7 +74,7 @@ KERNEL_NAMES = {1: "fold_gamma", 2: "gemm_fwd_w1", 3: "gemm_fwd_w2", 4: "gemm_dg
                 30: "fp4_quant", 31: "fp4_dequant", 32: "fp4_gemm", 33: "route", 34: "route_bwd",
                 35: "add_norm", 36: "add_norm_bwd", 37: "add_norm_dgamma", 38: "ortho_norm", 39: "ortho_scale",
                 40: "ns_gram", 41: "ns_square", 42: "ns_update", 43: "muon_apply",
-                44: "ns_apply", 45: "ns_join"}
+                44: "ns_apply", 45: "ns_join", 46: "ns_steps"}
 
 
 class MlpBlkError(RuntimeError):

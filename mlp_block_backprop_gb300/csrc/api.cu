@@ -1670,6 +1670,26 @@ int orthogonalize_impl(const mlpblk_ortho_desc *d, const OrthoSource &u, void *o
     MLPBLK_LAUNCH(MLPBLK_KERNEL_ORTHO_NORM, s, launch_ortho_norm(u, d->rows * d->cols, d->batch, partial, &parts, sms, s));
     MLPBLK_LAUNCH(MLPBLK_KERNEL_ORTHO_SCALE, s,
                   launch_ortho_scale(u, d->rows, d->cols, d->batch, partial, parts, d->eps, sx, x[0], d->steps > 1 ? lo : nullptr, sms, s));
+    if (ns_fused_fits(d->rows, d->cols, d->batch, sms)) {
+        NsFusedProblem q = {};
+        q.rows = d->rows;
+        q.cols = d->cols;
+        q.batch = d->batch;
+        q.steps = d->steps;
+        q.x[0] = x[0];
+        q.x[1] = x[1];
+        q.lo = lo;
+        q.g = g[0];
+        q.p = g[1];
+        q.diag = diag[0];
+        q.o = o;
+        q.sx = sx;
+        q.coefficients = d->coefficients;
+        MLPBLK_LAUNCH(MLPBLK_KERNEL_NS_STEPS, s, launch_ns_fused(q, s));
+        *x_out = x[d->steps & 1];
+        *sx_out = sx;
+        return MLPBLK_OK;
+    }
     // Two steps at a time (csrc/gemm_ns.cu) save 3 m^2 (n - m) operations a matrix for one launch
     // more: worth it from some 6 us of the tensor cores on.  Never the last step: its X is kept in
     // one fp16 value, and G's errors would reach the result.

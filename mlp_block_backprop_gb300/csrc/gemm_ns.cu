@@ -237,6 +237,11 @@ __device__ __forceinline__ float2 ns_combine(const NsArgs &a, float2 v, float2 p
 struct NsMaps {
     CUtensorMap aux, aux2, out, out_lo, mirror;
 };
+struct NsMapRefs {
+    const CUtensorMap *aux, *aux2, *out, *out_lo, *mirror;
+    __device__ __forceinline__ NsMapRefs() {}
+    __device__ __forceinline__ NsMapRefs(const NsMaps &m) : aux(&m.aux), aux2(&m.aux2), out(&m.out), out_lo(&m.out_lo), mirror(&m.mirror) {}
+};
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int32_t c0, int32_t c1, int32_t c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
@@ -253,7 +258,7 @@ constexpr int kNsStaging = 2 * kNsChunkBytes;   // a warp's: the first tile's ch
 template <int OP>
 struct NsEpilogue {
     const NsArgs &a;
-    const NsMaps &maps;
+    const NsMapRefs maps;
     uint8_t *buf0, *buf1;
     uint64_t *bar;
     volatile int *abort;
@@ -269,8 +274,8 @@ struct NsEpilogue {
         if (lane == 0) {
             bulk_wait_group_read<0>();
             mbar_expect_relaxed(bar, second() ? 2 * kNsChunkBytes : kNsChunkBytes);
-            tma_load_3d(&maps.aux, bar, buf0, col0, row0, w.batch);
-            if (second()) tma_load_3d(&maps.aux2, bar, buf1, col0, row0, w.batch);
+            tma_load_3d(maps.aux, bar, buf0, col0, row0, w.batch);
+            if (second()) tma_load_3d(maps.aux2, bar, buf1, col0, row0, w.batch);
         }
         __syncwarp();
     }
@@ -290,7 +295,7 @@ struct NsEpilogue {
             __syncwarp();
         }
         const int64_t dat = static_cast<int64_t>(w.batch) * a.diag_pitch;
-        const float d = kNsScaled<OP> && !a.diag_col && row < a.rows ? a.diag[dat + row] : 0.0f;
+        const float d = kNsScaled<OP> && !a.diag_col && row < a.rows ? __ldcg(a.diag + dat + row) : 0.0f;
         const float *by_col = OP == kNsJoin ? a.diag2 : (OP == kNsUpdate && a.diag_col ? a.diag : nullptr);
         const bool two = second();
 #pragma unroll
@@ -301,8 +306,8 @@ struct NsEpilogue {
             if (kNsTwo<OP> && two) y = ld_shared_v4(at1 + off);
             float4 c0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), c1 = c0;
             if (kNsTwo<OP> && by_col) {   // (the pitch is a multiple of 64)
-                c0 = __ldg(reinterpret_cast<const float4 *>(by_col + dat + col0 + 8 * j));
-                c1 = __ldg(reinterpret_cast<const float4 *>(by_col + dat + col0 + 8 * j + 4));
+                c0 = __ldcg(reinterpret_cast<const float4 *>(by_col + dat + col0 + 8 * j));
+                c1 = __ldcg(reinterpret_cast<const float4 *>(by_col + dat + col0 + 8 * j + 4));
             }
             const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
             const float2 cs[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
@@ -378,9 +383,9 @@ struct NsEpilogue {
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
-            tma_store_3d(&maps.out, buf0, col0, row0, w.batch);
-            if (OP == kNsUpdate && a.out_lo && !a.o) tma_store_3d(&maps.out_lo, buf1, col0, row0, w.batch);
-            if (OP != kNsUpdate && w.mirror) tma_store_3d(&maps.mirror, buf1, row0, col0, w.batch);
+            tma_store_3d(maps.out, buf0, col0, row0, w.batch);
+            if (OP == kNsUpdate && a.out_lo && !a.o) tma_store_3d(maps.out_lo, buf1, col0, row0, w.batch);
+            if (OP != kNsUpdate && w.mirror) tma_store_3d(maps.mirror, buf1, row0, col0, w.batch);
             bulk_commit_group();
         }
         __syncwarp();
@@ -420,12 +425,12 @@ __device__ __forceinline__ void ns_finish_eight(const NsArgs &a, const NsTile &w
     if (row >= a.rows || col >= a.cols) return;
     const int64_t at = w.batch * a.matrix + static_cast<int64_t>(row) * a.pitch + col;
     const int64_t dat = static_cast<int64_t>(w.batch) * a.diag_pitch;
-    const float d = kNsScaled<OP> && !a.diag_col ? a.diag[dat + row] : 0.0f;
+    const float d = kNsScaled<OP> && !a.diag_col ? __ldcg(a.diag + dat + row) : 0.0f;
     const float *by_col = OP == kNsJoin ? a.diag2 : (OP == kNsUpdate && a.diag_col ? a.diag : nullptr);
     float4 c0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), c1 = c0;
     if (kNsTwo<OP> && by_col) {
-        c0 = __ldg(reinterpret_cast<const float4 *>(by_col + dat + col));
-        c1 = __ldg(reinterpret_cast<const float4 *>(by_col + dat + col + 4));
+        c0 = __ldcg(reinterpret_cast<const float4 *>(by_col + dat + col));
+        c1 = __ldcg(reinterpret_cast<const float4 *>(by_col + dat + col + 4));
     }
     const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
     const float2 cs[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
@@ -582,7 +587,7 @@ ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     } else if constexpr (!C::SPLIT) {
         const int q = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
         uint8_t *st = staging + ew * kNsStaging;
-        NsEpilogue<OP> epi = {args, maps, st, st + kNsChunkBytes, &aux_bar[ew], abort_flag, lane, 0};
+        NsEpilogue<OP> epi = {args, NsMapRefs(maps), st, st + kNsChunkBytes, &aux_bar[ew], abort_flag, lane, 0};
         auto place = [&](const NsTile &x, int &row, int &col) { row = x.m0 + 32 * q, col = x.n0 + 64 * half; };
         int it = 0, row, col;
         if (t < args.tiles) {
@@ -832,7 +837,7 @@ ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const int q = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
         const uint32_t acce0 = mapa_shared(smem_u32(&acce_bar[0]), 0);
         uint8_t *st = staging + ew * kNsStaging;
-        NsEpilogue<OP> epi = {args, maps, st, st + kNsChunkBytes, &aux_bar[ew], abort_flag, lane, 0};
+        NsEpilogue<OP> epi = {args, NsMapRefs(maps), st, st + kNsChunkBytes, &aux_bar[ew], abort_flag, lane, 0};
         auto place = [&](const NsTile &x, int &row, int &col) { row = x.m0 + static_cast<int>(rank) * 128 + 32 * q, col = x.n0 + 128 * half; };
         int it = 0, row, col;
         if (t < args.tiles) {
@@ -883,6 +888,257 @@ ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// ------------------------------------------------------------------- ns_fused
+
+// All steps of a small matrix in one launch: a cluster of up to eight CTAs a matrix, whose products
+// follow one another between cluster barriers instead of launches (256 x 256, five steps: FIGURE).
+// A product's tiles are dealt out to the CTAs; between products everything goes through L2, by
+// the copies of the asynchronous proxy on both sides (but the diagonal's remainders).
+struct NsFusedArgs {
+    int m, rows, cols;                 // the short side; X
+    int x_pitch, g_pitch;
+    int steps;
+    float *diag;
+    uint16_t *o;                       // NULL: the last X stays in x[steps & 1]
+    float sx;
+    float coef[MLPBLK_ORTHO_MAX_STEPS][3];
+};
+// Operands (K-major, MN-major) and chunks of the epilogue.
+struct NsFusedMaps {
+    CUtensorMap x_k[2], x_mn[2], g, p;
+    CUtensorMap x_chunk[2], lo_chunk, g_chunk, p_chunk, o_chunk;
+};
+
+constexpr int kFusedCtas = 8;          // of a cluster, at most
+
+struct NsFused {
+    using C = NsSmall<false>;
+    uint8_t *a_s, *b_s, *staging;
+    uint64_t *full_bar, *empty_bar, *accf_bar, *acce_bar, *aux_bar;
+    volatile int *abort;
+    uint32_t tmem;
+    int warp, lane, rank, ctas;
+    int stage = 0, it = 0;             // of this warp's role, through all products
+    uint32_t phase = 0;                // an epilogue warp: of its loads
+
+    // One product of the cluster.
+    template <int OP, bool AMN, bool BMN>
+    __device__ __forceinline__ void product(const CUtensorMap *mA, const CUtensorMap *mB, const NsMapRefs &maps, const NsArgs &a, int batch) {
+        constexpr int S = C::kStages;
+        const int tiles = a.mt * a.nt;
+        int t = rank;
+        auto tile = [&]() {
+            NsTile w = {};
+            w.batch = batch;
+            w.m0 = t % a.mt * 128;
+            w.n0 = t / a.mt * 128;
+            return w;
+        };
+        if (warp == 0) {
+            const bool issue = elect_lane();
+            if (issue) fence_proxy_async_global();
+            bool ok = true;
+            for (; ok && t < tiles; t += ctas) {
+                const NsTile w = tile();
+                for (int kb = 0; kb < a.kblocks; ++kb) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1u, abort));
+                    if (!ok) break;
+                    if (issue) {
+                        mbar_expect_relaxed(&full_bar[stage], C::kStageBytes);
+                        load_operand<AMN>(mA, &full_bar[stage], a_s + stage * C::kOpBytes, kb, w.m0, batch);
+                        load_operand<BMN>(mB, &full_bar[stage], b_s + stage * C::kOpBytes, kb, w.n0, batch);
+                    }
+                    __syncwarp();
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        } else if (warp == 1) {
+            const bool issue = elect_lane();
+            const uint64_t a0 = operand_desc<AMN>(a_s), b0 = operand_desc<BMN>(b_s);
+            bool ok = true;
+            for (; ok && t < tiles; t += ctas, ++it) {
+                const int buf = it & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait(&acce_bar[buf], ((it >> 1) & 1) ^ 1u, abort));
+                if (!ok) break;
+                tc_fence_after_sync();
+                for (int kb = 0; kb < a.kblocks; ++kb) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint64_t ad = a0 + stage * (C::kOpBytes >> 4), bd = b0 + stage * (C::kOpBytes >> 4);
+                    if (issue) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            umma_bf16(tmem + buf * 128, ad + j * kOperandStep<AMN>, bd + j * kOperandStep<BMN>,
+                                      idesc_f16_f32(128, 128, AMN, BMN), (kb > 0 || j > 0) ? 1u : 0u);
+                        umma_commit(&empty_bar[stage]);
+                    }
+                    __syncwarp();
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (issue) umma_commit(&accf_bar[buf]);
+                __syncwarp();
+            }
+        } else {
+            const int q = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
+            uint8_t *st = staging + ew * kNsStaging;
+            NsEpilogue<OP> epi = {a, maps, st, st + kNsChunkBytes, &aux_bar[ew], abort, lane, phase};
+            if (lane == 0) fence_proxy_async_global();
+            if (t < tiles) epi.load(tile(), t % a.mt * 128 + 32 * q, t / a.mt * 128 + 64 * half);
+            while (t < tiles) {
+                const NsTile w = tile();
+                const int buf = it & 1;
+                const bool ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort));
+                if (!ok) break;
+                tc_fence_after_sync();
+                float v[64];
+                tmem_load_64cols(tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * 128 + 64 * half, *reinterpret_cast<float(*)[32]>(&v[0]),
+                                 *reinterpret_cast<float(*)[32]>(&v[32]));
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_relaxed(&acce_bar[buf]);
+                if (!epi.finish(w, w.m0 + 32 * q, w.n0 + 64 * half, v)) break;
+                t += ctas;
+                ++it;
+                if (t < tiles) epi.load(tile(), t % a.mt * 128 + 32 * q, t / a.mt * 128 + 64 * half);
+            }
+            if (lane == 0) {
+                bulk_wait_group<0>();
+                if (*abort) mbar_drain(&aux_bar[ew], epi.phase);   // a load may still be on its way
+                fence_proxy_async_global();
+            }
+            __syncwarp();
+            phase = epi.phase;
+        }
+        cluster_sync();
+    }
+};
+
+template <bool TALL>
+__global__ void __launch_bounds__(NsSmall<false>::kThreads, 1)
+ns_fused_kernel(const __grid_constant__ NsFusedMaps maps, const __grid_constant__ NsFusedArgs args) {
+    using C = NsSmall<false>;
+    constexpr int S = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    NsFused f;
+    f.a_s = smem;
+    f.b_s = f.a_s + S * C::kOpBytes;
+    f.staging = f.b_s + S * C::kOpBytes;
+    uint8_t *ctrl = f.staging + C::kDumpBytes;
+    f.full_bar = reinterpret_cast<uint64_t *>(ctrl);
+    f.empty_bar = f.full_bar + S;
+    f.accf_bar = f.empty_bar + S;
+    f.acce_bar = f.accf_bar + 2;
+    f.aux_bar = f.acce_bar + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctrl + 512);
+    f.abort = reinterpret_cast<volatile int *>(ctrl + 516);
+    f.warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    f.lane = threadIdx.x & 31;
+    f.rank = static_cast<int>(cluster_ctarank());
+    f.ctas = static_cast<int>(cluster_nctarank());
+    const int batch = static_cast<int>(blockIdx.x) / f.ctas;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&f.full_bar[s], 1);
+            mbar_init(&f.empty_bar[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&f.accf_bar[b], 1);
+            mbar_init(&f.acce_bar[b], C::kEpiWarps);
+        }
+        for (int b = 0; b < C::kEpiWarps; ++b) mbar_init(&f.aux_bar[b], 1);
+        *f.abort = 0;
+        fence_barrier_init();
+        for (int i = 0; i < 2; ++i) {
+            prefetch_tensormap(&maps.x_k[i]);
+            prefetch_tensormap(&maps.x_mn[i]);
+            prefetch_tensormap(&maps.x_chunk[i]);
+        }
+        prefetch_tensormap(&maps.g);
+        prefetch_tensormap(&maps.p);
+        prefetch_tensormap(&maps.g_chunk);
+        prefetch_tensormap(&maps.p_chunk);
+        prefetch_tensormap(&maps.lo_chunk);
+    }
+    if (f.warp == 1) {
+        tmem_alloc(tmem_slot, 256);
+        tmem_relinquish_alloc_permit();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    f.tmem = *tmem_slot;
+    griddep_launch_dependents();
+    griddep_wait();
+
+    NsArgs sq = {};                    // G and P
+    sq.rows = sq.cols = args.m;
+    sq.mt = sq.nt = (args.m + 127) / 128;
+    sq.diag_pitch = args.g_pitch;
+    sq.diag = sq.diag_out = args.diag;
+    sq.alpha = 1.0f / (args.sx * args.sx);
+    NsArgs up = {};                    // X
+    up.rows = args.rows;
+    up.cols = args.cols;
+    up.mt = (args.rows + 127) / 128;
+    up.nt = (args.cols + 127) / 128;
+    up.diag_pitch = args.g_pitch;
+    up.diag = args.diag;
+    up.diag_col = TALL;
+    up.o_tma = args.cols % 8 == 0;
+    up.alpha = 1.0f / args.sx;
+    const int n_blocks = ((TALL ? args.rows : args.cols) + kNsK - 1) / kNsK, m_blocks = (args.m + kNsK - 1) / kNsK;
+    // (what is set but not read by an epilogue only has to be there)
+    NsMapRefs to_g, to_p, to_x;
+    to_g.aux = to_g.aux2 = to_g.out_lo = to_g.mirror = nullptr;
+    to_g.out = &maps.g_chunk;
+    to_p = to_g;
+    to_p.aux = &maps.g_chunk;
+    to_p.out = &maps.p_chunk;
+    to_x = to_g;
+    to_x.aux2 = to_x.out_lo = &maps.lo_chunk;
+    __half *const some = reinterpret_cast<__half *>(args.diag);
+#pragma unroll 1
+    for (int i = 0; i < args.steps; ++i) {
+        const int from = i & 1;
+        sq.kblocks = n_blocks;
+        if (TALL) f.product<kNsGram, true, true>(&maps.x_mn[from], &maps.x_mn[from], to_g, sq, batch);
+        else f.product<kNsGram, false, false>(&maps.x_k[from], &maps.x_k[from], to_g, sq, batch);
+        sq.kblocks = m_blocks;
+        sq.b = args.coef[i][1];
+        sq.c = args.coef[i][2];
+        f.product<kNsSquare, false, false>(&maps.g, &maps.g, to_p, sq, batch);
+        const bool last = i + 1 == args.steps;
+        up.kblocks = m_blocks;
+        up.a = args.coef[i][0];
+        up.aux2 = last ? nullptr : some;                  // there are low parts (the map says where)
+        up.out_lo = i + 2 < args.steps ? some : nullptr;
+        up.o = last ? args.o : nullptr;
+        to_x.aux = &maps.x_chunk[from];
+        to_x.out = up.o ? &maps.o_chunk : &maps.x_chunk[from ^ 1];
+        if (TALL) f.product<kNsUpdate, false, false>(&maps.x_k[from], &maps.p, to_x, up, batch);
+        else f.product<kNsUpdate, false, true>(&maps.p, &maps.x_mn[from], to_x, up, batch);
+    }
+    if (f.warp == 0) {
+        await_copies(f.full_bar, S, f.stage, f.phase);
+        __syncwarp();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (f.warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(f.tmem, 256);
     }
 }
 
@@ -980,7 +1236,12 @@ int run_ns(NsArgs a, const CUtensorMap &mA, const CUtensorMap &mB, int batch, in
     const int pairs = sms / 2;
     if (tiles > INT32_MAX) return MLPBLK_EINVAL;
     NsMaps maps = {};
-    if (pairs >= 1 && 2 * pair_tiles >= pairs && a.rows > 128 && a.cols > 128) {
+    // Rounds of tiles, each with its stages of K and the part of its epilogue that nothing hides
+    // (us, measured: 8 x 1024 x 2048, 4096 x 16384): a pair's 256 x 256 tile 0.3 a stage and 3.6, a
+    // CTA's 128 x 128 one 0.22 and 2.2.  (X X^T of 8 x 1024 x 2048: 80 pair tiles on 76 pairs 31 us, 288
+    // small ones 23; X' 40 and 45.)
+    const int64_t pair_rounds = pairs >= 1 ? (pair_tiles + pairs - 1) / pairs : 0, rounds = (tiles + sms - 1) / sms;
+    if (pairs >= 1 && pair_rounds * (0.3 * a.kblocks + 3.6) < rounds * (0.22 * a.kblocks + 2.2)) {
         static int attr_set[64] = {0};
         a.mt = (a.rows + 255) / 256;
         a.nt = (a.cols + 255) / 256;
@@ -995,8 +1256,15 @@ int run_ns(NsArgs a, const CUtensorMap &mA, const CUtensorMap &mB, int batch, in
     a.nt = (a.cols + 127) / 128;
     a.group_m = 8;
     const int64_t every = static_cast<int64_t>(a.mt) * a.nt * batch;   // a split computes the images too
+    // K is split where that saves more than the cluster's sum costs: a stage takes 0.155 us with
+    // few CTAs at work, the sum some 5.5 and 0.3 a part (X X^T of 256 x 8192: 27.2 us whole, 22.4, 17.9 and 18.0
+    // in two, four and eight; of 512 x 2048: 13.0, 14.3, 14.3, 25.6).
     int split = 1;
-    while (split < 8 && every * split * 2 <= sms && a.kblocks >= 4 * split) split *= 2;
+    double best = 0.155 * a.kblocks;
+    for (int k = 2; k <= 8; k *= 2) {
+        const double cost = 0.155 * a.kblocks / k + 5.5 + 0.3 * k;
+        if (every * k <= sms && a.kblocks >= 2 * k && cost < best) best = cost, split = k;
+    }
     if (split > 1) {
         a.per = a.mt * a.nt;
         a.tiles = static_cast<int>(every);
@@ -1064,6 +1332,72 @@ int launch_ns_product(const NsProduct &p, int sms, cudaStream_t s) {
     if (!ns_map(&mA, p.p, false, m, m, g_pitch, p.batch)) return MLPBLK_ECUDA;
     if (p.op == kNsApply) return run_ns<kNsApply, false, false>(a, mA, mB, p.batch, sms, s);
     return run_ns<kNsJoin, false, false>(a, mA, mB, p.batch, sms, s);
+}
+
+// CTAs of a matrix: one a tile of X, up to eight.
+static int ns_fused_ctas(int64_t rows, int64_t cols) {
+    const int64_t tiles = (rows + 127) / 128 * ((cols + 127) / 128);
+    int c = 1;
+    while (c < kFusedCtas && c < tiles) c *= 2;
+    return c;
+}
+
+// One launch where a product is short beside a launch, and all matrices run at once.
+bool ns_fused_fits(int64_t rows, int64_t cols, int batch, int sms) {
+    const int64_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
+    return m <= 256 && n <= 2048 && static_cast<int64_t>(batch) * ns_fused_ctas(rows, cols) <= sms;
+}
+
+int launch_ns_fused(const NsFusedProblem &p, cudaStream_t s) {
+    const bool tall = p.rows > p.cols;
+    const int64_t m = tall ? p.cols : p.rows, x_pitch = ortho_pitch(p.cols), g_pitch = ortho_pitch(m);
+    NsFusedArgs a = {};
+    a.m = static_cast<int>(m);
+    a.rows = static_cast<int>(p.rows);
+    a.cols = static_cast<int>(p.cols);
+    a.x_pitch = static_cast<int>(x_pitch);
+    a.g_pitch = static_cast<int>(g_pitch);
+    a.steps = p.steps;
+    a.diag = p.diag;
+    a.o = static_cast<uint16_t *>(p.o);
+    a.sx = p.sx;
+    for (int i = 0; i < p.steps; ++i)
+        for (int j = 0; j < 3; ++j) a.coef[i][j] = p.coefficients[i][j];
+    NsFusedMaps maps = {};
+    bool ok = ns_map(&maps.g, p.g, false, m, m, g_pitch, p.batch) && ns_map(&maps.p, p.p, false, m, m, g_pitch, p.batch) &&
+              ns_chunk_map(&maps.g_chunk, p.g, m, m, g_pitch, p.batch, 64, 32) && ns_chunk_map(&maps.p_chunk, p.p, m, m, g_pitch, p.batch, 64, 32) &&
+              ns_chunk_map(&maps.lo_chunk, p.lo, p.rows, p.cols, x_pitch, p.batch, 64, 32);
+    if (p.o && p.cols % 8 == 0) ok = ok && ns_chunk_map(&maps.o_chunk, p.o, p.rows, p.cols, p.cols, p.batch, 64, 32);
+    for (int i = 0; i < 2; ++i)
+        ok = ok && ns_map(&maps.x_k[i], p.x[i], false, p.rows, p.cols, x_pitch, p.batch) && ns_map(&maps.x_mn[i], p.x[i], true, p.rows, p.cols, x_pitch, p.batch) &&
+             ns_chunk_map(&maps.x_chunk[i], p.x[i], p.rows, p.cols, x_pitch, p.batch, 64, 32);
+    if (!ok) return MLPBLK_ECUDA;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return MLPBLK_ECUDA;
+    static int attr_set[2][64] = {};
+    void (*const kernel)(NsFusedMaps, NsFusedArgs) = tall ? ns_fused_kernel<true> : ns_fused_kernel<false>;
+    if (!attr_set[tall][dev]) {
+        const int rc = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NsSmall<false>::kSmemBytes));
+        if (rc != MLPBLK_OK) return rc;
+        attr_set[tall][dev] = 1;
+    }
+    cudaLaunchConfig_t cfg = {};
+    const int ctas = ns_fused_ctas(p.rows, p.cols);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.batch * ctas));
+    cfg.blockDim = dim3(NsSmall<false>::kThreads);
+    cfg.dynamicSmemBytes = NsSmall<false>::kSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, maps, a));
 }
 
 int take_device_error_gemm_ns() {

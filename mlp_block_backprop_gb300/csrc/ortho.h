@@ -40,6 +40,19 @@ struct NsProduct {
 };
 
 int launch_ns_product(const NsProduct &p, int sms, cudaStream_t s);
+
+// All steps of small matrices in one launch, from x[0]; the last X in x[steps & 1], or o.
+struct NsFusedProblem {
+    int64_t rows, cols;
+    int batch, steps;
+    __half *x[2], *lo, *g, *p;
+    float *diag;
+    void *o;
+    float sx;
+    const float (*coefficients)[3];
+};
+bool ns_fused_fits(int64_t rows, int64_t cols, int batch, int sms);
+int launch_ns_fused(const NsFusedProblem &p, cudaStream_t s);
 int take_device_error_gemm_ns();
 
 // Where a step's input comes from: a matrix, or momentum and gradient.
