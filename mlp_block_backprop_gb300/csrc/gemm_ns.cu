@@ -894,7 +894,7 @@ ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 // ------------------------------------------------------------------- ns_fused
 
 // All steps of a small matrix in one launch: a cluster of up to eight CTAs a matrix, whose products
-// follow one another between cluster barriers instead of launches (256 x 256, five steps: FIGURE).
+// follow one another between cluster barriers instead of launches (256 x 256, five steps: 81 -> 68 us).
 // A product's tiles are dealt out to the CTAs; between products everything goes through L2, by
 // the copies of the asynchronous proxy on both sides (but the diagonal's remainders).
 struct NsFusedArgs {
@@ -1342,10 +1342,11 @@ static int ns_fused_ctas(int64_t rows, int64_t cols) {
     return c;
 }
 
-// One launch where a product is short beside a launch, and all matrices run at once.
+// One launch where a product is short beside a launch, and all matrices run at once (us, one launch and
+// several: 256 x 256 68 and 81, 256 x 1024 87 and 93, 250 x 2000 122 and 108, 16 of 256 x 256 77 and 87).
 bool ns_fused_fits(int64_t rows, int64_t cols, int batch, int sms) {
     const int64_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
-    return m <= 256 && n <= 2048 && static_cast<int64_t>(batch) * ns_fused_ctas(rows, cols) <= sms;
+    return m <= 256 && n <= 1024 && static_cast<int64_t>(batch) * ns_fused_ctas(rows, cols) <= sms;
 }
 
 int launch_ns_fused(const NsFusedProblem &p, cudaStream_t s) {

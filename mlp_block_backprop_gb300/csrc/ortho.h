@@ -8,7 +8,7 @@
 
 namespace mlpblk {
 
-constexpr int kOrthoNormParts = 1024;   // partial sums of squares, over the whole batch, at most
+constexpr int kOrthoNormParts = 2048;   // partial sums of squares, over the whole batch, at most
 
 // Elements of a row of a workspace matrix: whole 128-byte lines of fp16.
 inline int64_t ortho_pitch(int64_t cols) { return (cols + 63) / 64 * 64; }
