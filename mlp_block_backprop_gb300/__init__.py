@@ -1243,13 +1243,21 @@ class AddRmsNorm(_Kept):
                 _codes(codes, where, e, dev)
             codes = codes.data_ptr()
         if scales is not None:
-            scales = _operand(scales, where, "scales", t.float32, self._s, dev)
+            if scales.dtype is not t.float32 or scales.numel() < self._s or scales.get_device() != dev or not scales.is_contiguous():
+                _operand(scales, where, "scales", t.float32, self._s, dev)
+            scales = scales.data_ptr()
         if n is not None:
-            n = _operand(n, where, "n", dt, e, dev)
+            if n.dtype is not dt or n.numel() < e or n.get_device() != dev or not n.is_contiguous():
+                _operand(n, where, "n", dt, e, dev)
+            n = n.data_ptr()
         if residual is not None:
-            residual = _operand(residual, where, "residual", dt, e, dev)
+            if residual.dtype is not dt or residual.numel() < e or residual.get_device() != dev or not residual.is_contiguous():
+                _operand(residual, where, "residual", dt, e, dev)
+            residual = residual.data_ptr()
         if sum is not None:
-            sum = _operand(sum, where, "sum", dt, e, dev)
+            if sum.dtype is not dt or sum.numel() < e or sum.get_device() != dev or not sum.is_contiguous():
+                _operand(sum, where, "sum", dt, e, dev)
+            sum = sum.data_ptr()
         rc = _calls.add_rmsnorm(self._d, x.data_ptr(), residual, gamma.data_ptr(), sum, n, codes, scales, self._at[0],
                                 t.raw_stream(dev) if stream is None else _stream(stream))
         if rc:
