@@ -230,7 +230,8 @@ __device__ __noinline__ void route_exactly(const RouteArgs &a, const T *row, boo
     for (int i = 0; i < chunks; ++i) {
         const int e = 32 * i + lane;
         const float l = e < a.E ? logit_of(to_float(row[e])) : -INFINITY;
-        const bool in = l > -INFINITY && (regroup || (keys[e] > -INFINITY && keys[e] >= least));
+        const bool open = l > -INFINITY && !(a.bias && !(a.bias[e] > -INFINITY));
+        const bool in = open && (regroup || (keys[e] > -INFINITY && keys[e] >= least));
         const unsigned votes = __ballot_sync(all, in);
         if (in) list[n + __popc(votes & ((1u << lane) - 1u))] = e;
         n += __popc(votes);
@@ -402,7 +403,8 @@ route_kernel(const RouteArgs a) {
     float bias[kRouteV];
     if (KEYED) {
 #pragma unroll
-        for (int i = 0; i < kRouteV; ++i) bias[i] = !by_logit && e0 + i < a.E ? __ldg(a.bias + e0 + i) : 0.0f;
+        for (int i = 0; i < kRouteV; ++i)           // (NaN becomes -inf: a NaN among the keys would win no round)
+            bias[i] = !by_logit && e0 + i < a.E ? fmaxf(__ldg(a.bias + e0 + i), -INFINITY) : 0.0f;
     }
     unsigned again = 0, regroup = 0;                // tokens of the warp to select again, and their groups too
 
@@ -471,7 +473,7 @@ route_kernel(const RouteArgs a) {
                 }
                 next = lanes_max<L>(mark);
                 const float slack = near_cut(last, next, most);
-                const bool doubt = next > -INFINITY && last - next <= slack;
+                const bool doubt = next > -INFINITY && last < INFINITY && last - next <= slack;
                 if (__any_sync(all, doubt)) {
                     float copy[kRouteV];
 #pragma unroll
@@ -512,7 +514,7 @@ route_kernel(const RouteArgs a) {
                 }
                 last = -lanes_max<L>(-last);
                 next = lanes_max<L>(next);
-                close = next > -INFINITY && last - next <= near_cut(last, next, most);
+                close = next > -INFINITY && last < INFINITY && last - next <= near_cut(last, next, most);
 #pragma unroll
                 for (int i = 0; i < kRouteV; ++i) {
                     if (by_logit) key[i] = l[i];
@@ -581,31 +583,38 @@ route_kernel(const RouteArgs a) {
     __syncwarp();
     if (KEYED) {
         if (!by_logit) {
-            // Neighbours that float32 cannot tell apart, and that are not the same numbers: two
-            // keys and, of the softmax, what the common sum does to the scores' difference (at the cut the other
-            // one stands for everything below it, so for the largest score).
+            // Neighbours that float32 cannot tell apart: near, or the same numbers (equal then, in order of
+            // their experts).  What float32 may be off: two keys and, of the softmax, what the common sum
+            // does to the scores' difference (at the cut the other one stands for everything below it, so
+            // for the largest score).
+            enum : int { kApart = 0, kNear = 1, kSame = 2 };
+            auto reach = [&](int n, float x, float y) {
+                return (a.sigmoid ? 8.0f : 22.0f) * kHalf * w.most[n] + 2.0f * kHalf * (fabsf(x) + fabsf(y));
+            };
             bool any = false;
             for (int i = lane; i < N * a.k; i += 32) {
                 const int n = over(i, a.by_k), r = i - n * a.k;
                 const int e = w.won[n][r], f = w.won[n][r + 1];
-                bool near = false;
+                int state = kApart;
                 if (f >= 0 && t0 + n < a.T) {
                     const float ke = w.top[n][r], kf = w.top[n][r + 1];
-                    const float off = (a.sigmoid ? 8.0f : 22.0f) * kHalf * w.most[n] + 2.0f * kHalf * (fabsf(ke) + fabsf(kf));
-                    if (ke - kf <= off) {
+                    if (ke < INFINITY && ke - kf <= reach(n, ke, kf)) {
                         const T *row = rows + (t0 + n) * a.E;
-                        near = logit_of(to_float(row[e])) != logit_of(to_float(row[f])) || __ldg(a.bias + e) != __ldg(a.bias + f);
+                        state = logit_of(to_float(row[e])) != logit_of(to_float(row[f])) || __ldg(a.bias + e) != __ldg(a.bias + f) ? kNear : kSame;
                     }
                 }
-                w.lane[n][r] = near;                // (the winners' lanes have been used)
-                any |= near;
+                w.lane[n][r] = state;               // (the winners' lanes have been used)
+                any |= state == kNear || (state == kSame && r + 1 == a.k);
             }
             if (__any_sync(all, any)) {
                 __syncwarp();
+                unsigned cut = 0;                   // tokens whose cut goes through experts of the same numbers
                 for (int i = lane; i < N * a.k; i += 32) {
                     const int n = over(i, a.by_k), r = i - n * a.k;
-                    if (!w.lane[n][r]) continue;
-                    if (!a.sigmoid || r + 1 == a.k || (r > 0 && w.lane[n][r - 1]) || w.lane[n][r + 1]) {
+                    const int state = w.lane[n][r];
+                    if (state == kSame && r + 1 == a.k) cut |= 1u << n;
+                    if (state != kNear) continue;
+                    if (!a.sigmoid || r + 1 == a.k || (r > 0 && w.lane[n][r - 1] != kApart) || w.lane[n][r + 1] != kApart) {
                         again |= 1u << n;           // more than two, or what was not selected
                         continue;
                     }
@@ -615,6 +624,16 @@ route_kernel(const RouteArgs a) {
                     if (y > x || (y == x && f < e)) {
                         w.won[n][r] = f;
                         w.won[n][r + 1] = e;
+                    }
+                }
+                // behind those, there may be others that are near
+                for (cut = __reduce_or_sync(all, cut); cut != 0; cut &= cut - 1) {
+                    const int n = __ffs(cut) - 1, e = w.won[n][a.k];
+                    const T *row = rows + (t0 + n) * a.E;
+                    const float ke = w.top[n][a.k], l = logit_of(to_float(row[e])), b = __ldg(a.bias + e);
+                    for (int f = lane; f < a.E; f += 32) {
+                        const float kf = w.keys[n][f];
+                        if (fabsf(kf - ke) <= reach(n, ke, ke) && (logit_of(to_float(row[f])) != l || __ldg(a.bias + f) != b)) again |= 1u << n;
                     }
                 }
             }
@@ -813,7 +832,7 @@ route_bwd_kernel(const RouteArgs a) {
 template <class T, int L>
 int run_route(const RouteArgs &a, bool backward, int sms, cudaStream_t s) {
     constexpr int kSide = 32 / L, kWarps = kRouteThreads / 32;
-        constexpr int kMany = kSide < 2 ? 2 : kSide, kManyBack = kSide < 8 ? 8 : kSide;
+    constexpr int kMany = kSide < 2 ? 2 : kSide, kManyBack = kSide < 8 ? 8 : kSide;
     const bool many = a.T >= static_cast<int64_t>(sms) * 64 * kSide;
     const int n = kWarps * (many ? (backward ? kManyBack : kMany) : kSide);   // tokens of a CTA
     const dim3 grid(static_cast<unsigned>((a.T + n - 1) / n)), block(kRouteThreads);

@@ -40,7 +40,8 @@ def route(logits, top_k, score="softmax", bias=None, groups=1, top_groups=None, 
     ids, weights = np.full((T, top_k), -1, dtype=np.int32), np.zeros((T, top_k))
     for t in range(T):
         s, l = scores(logits[t], score), _row(logits[t])
-        key = np.where(l > -np.inf, s if bias is None else s + np.asarray(bias, dtype=np.float64), -np.inf)
+        b = np.zeros(E) if bias is None else np.asarray(bias, dtype=np.float64)
+        key = np.where((l > -np.inf) & (b > -np.inf), s + b, -np.inf)
         rank = l if bias is None else key          # without a bias the logits decide
         if top_groups < groups:
             per = E // groups

@@ -117,6 +117,28 @@ def test_route_and_gradient(mb, case, dtype, biased, kind):
     assert np.all(err <= 4 * tol * mag + half * np.abs(ref) + floor), (err - 4 * tol * mag - half * np.abs(ref)).max()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("case", [c for c in CASES if c[1] > 1])
+def test_biases_that_are_not_finite(mb, case, dtype):
+    """-inf and NaN close an expert to selection, +inf puts it first; more of each than are selected.
+    The others' biases are zero, so that many keys are equal, and equal in float32 alone."""
+    import torch
+    T, E, k, score, groups, top_groups, renorm, scale = case
+    rng = np.random.default_rng(T + E)
+    for kind in ("plain", "ties", "near", "far"):
+        dev, l = _logits(rng, T, E, kind, dtype)
+        for values in ((), (np.inf,), (-np.inf, np.nan), (np.inf, -np.inf, np.nan)):
+            bias = np.zeros(E, dtype=np.float32)
+            for i, v in enumerate(values):
+                bias[rng.random(E) < (0.15 if np.isposinf(v) and kind == "plain" else 0.5)] = v
+            ids = torch.full((T, k), 77, dtype=torch.int32, device="cuda")
+            w = torch.full((T, k), 77.0, device="cuda")
+            mb.MoeRouter(T, E, k, score, groups, top_groups, renorm, scale, dtype).route(dev, ids, w, bias=torch.from_numpy(bias).cuda())
+            ref_ids, ref_w = route.route(l, k, score, bias, groups, top_groups, renorm, scale)
+            np.testing.assert_array_equal(ids.cpu().numpy(), ref_ids)
+            np.testing.assert_allclose(to_np(w), ref_w, rtol=_tol(l, E, k), atol=2.0 ** -126 * (1 if not renorm else 1e20))
+
+
 def test_gradient_against_differences(mb):
     """d_logits on central differences of L = sum dw w in float32 steps that keep the selection."""
     import torch
