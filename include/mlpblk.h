@@ -616,7 +616,8 @@ int mlpblk_fp4_product_kernel(const mlpblk_fp4_matmul_desc *desc, int form, int 
  * A logit of -infinity or NaN closes its expert to the token; +infinity counts as the largest
  * finite value.  A row whose experts are all closed selects nothing.  The order is that of
  * the scores in float64 (without a bias, of the logits), whatever the arithmetic here:
- * float32 keys that are too close to call are computed again.  bias values are finite.
+ * float32 keys that are too close to call are computed again.  A bias of -infinity or NaN
+ * closes its expert to selection, whose share of the softmax stays; one of +infinity puts it first.
  *
  * mlpblk_moe_route_backward: d_logits[T,E] (written) from d_routing_weights[T,k], for the
  * ids of the same logits, held fixed ("Hard Top-K Has No Ordinary Derivative").  Ids outside
@@ -664,9 +665,10 @@ int mlpblk_moe_route_backward(const mlpblk_route_desc *desc, const void *logits,
  *   codes = E4M3(n / scale), nearest even                         [T, width], a byte each
  * sum is written where residual is given (and only then) and may be x or residual itself.
  * codes and scales are given together; n, codes and rstd may be NULL, n and codes not both.
- * The codes are those of the real number n / scale, rounded once.  A row that holds an
- * infinity, a NaN or a magnitude of 2^60 or more has a NaN rstd and NaN scales and codes;
- * squares below float32's range count as zero.
+ * The codes are those of the real number n / scale, rounded once (where the products
+ * sum * gamma are in float32's normal range: smaller ones are rounded to it, one beyond it makes its scale
+ * and that scale's codes NaN).  A row that holds an infinity, a NaN or a magnitude of 2^60 or more
+ * has a NaN rstd and NaN scales and codes; squares below float32's range count as zero.
  *
  * mlpblk_add_rmsnorm_backward: with dn the gradient of n (as the codes stand for it:
  *   rounding passes it on) and d_sum that of sum (NULL: none),
@@ -721,7 +723,9 @@ int mlpblk_add_rmsnorm_backward(const mlpblk_norm_desc *desc, const void *dn, co
  * Precision: products of fp16 values, whose range X's scaling fits, with float32 sums; a X
  * takes X as two fp16 values in all but the last step.  With Muon's coefficients
  * (3.4445, -4.7750, 2.0315), five steps, the result is within 3e-3 of the formula's in the
- * Frobenius norm (before o's rounding to bf16).  The polynomials must keep |X|'s singular values below 16.  A NaN or an
+ * Frobenius norm (before o's rounding to bf16).  The matrices b G + c G^2 are fp16 too: every singular
+ * value s on the way must keep |b s^2 + c s^4| and, of two neighbouring steps, |a a'| below 60000
+ * (with those coefficients s < 13).  A NaN or an
  * infinity in u makes its matrix NaN.  Sums have a fixed order.
  *
  * mlpblk_orthogonalize_workspace_size: bytes of scratch for both; 0 for an invalid

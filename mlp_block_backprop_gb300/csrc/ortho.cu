@@ -177,7 +177,7 @@ ortho_scale_kernel(const ScaleArgs a) {
             if (d > 0.0 && d < INFINITY) frexp(d, &e);
             e = min(max(e, -120), 120);
             factor[0] = ldexpf(1.0f, -e);
-            factor[1] = static_cast<float>(static_cast<double>(a.sx) / ldexp(d, -e));
+            factor[1] = d == 0.0 ? 0.0f : static_cast<float>(static_cast<double>(a.sx) / ldexp(d, -e));   // (eps = 0 and a matrix of zeros)
         }
     }
     __syncthreads();

@@ -188,6 +188,30 @@ def test_values_at_the_edges(mb, dtype, block):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("block", [0, 128])
+def test_products_beyond_the_range(mb, dtype, block):
+    """sum * gamma overflows in one column: its scale is NaN, rstd is not."""
+    import torch
+    T, d = 5, 300
+    rng = np.random.default_rng(6)
+    x, gamma = _t(rng.normal(0, 1, (T, d)), dtype), _t(np.ones(d), dtype)
+    x[3, 200], gamma[200] = 2.0 ** 20, 2.0 ** 110
+    op = mb.AddRmsNorm(T, d, 1e-6, dtype, block)
+    per = 3 if block else 1
+    codes, scales = torch.empty(T, d, dtype=torch.uint8, device="cuda"), torch.empty(T, per, device="cuda")
+    op.forward(x, gamma, codes, scales)
+    _, ref_codes, ref_scales, ref_r = norm.forward(to_np(x), to_np(gamma), 1e-6, block)
+    np.testing.assert_allclose(to_np(op.rstd), ref_r, rtol=2.0 ** -23)
+    bad = np.zeros((T, per), dtype=bool)
+    bad[3, 1 if block else 0] = True
+    got = to_np(codes.view(torch.float8_e4m3fn))
+    wide = np.repeat(bad, 128 if block else d, axis=1)[:, :d]
+    assert np.isnan(to_np(scales)[bad]).all() and np.isnan(got[wide]).all()
+    np.testing.assert_array_equal(to_np(scales)[~bad], ref_scales.astype(np.float64)[~bad])
+    np.testing.assert_array_equal(got[~wide], ref_codes[~wide])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_sum_in_place(mb, dtype):
     """The residual stream updated where it lies, and x likewise."""
     import torch

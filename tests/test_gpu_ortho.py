@@ -116,6 +116,35 @@ def test_steps_of_their_own_coefficients(mb, shape, steps):
     assert _rel(o, _exact(u, coef)) <= NS + HALF
 
 
+@pytest.mark.parametrize("steps", [2, 3, 4, 5, 6])
+@pytest.mark.parametrize("shape", [(1, 1001, 4100), (1, 4500, 1024), (3, 700, 3001), (4, 2900, 650)])
+def test_two_steps_with_one_product(mb, shape, steps):
+    """Long sides of at least twice the short one, enough work: two steps share a product on X."""
+    import torch
+    b, r, c = shape
+    gen = torch.Generator(device="cuda").manual_seed(steps)
+    for kind in ("flat", "mixed", "low"):
+        u = torch.stack([_matrix(gen, r, c, kind, "bf16") for _ in range(b)])
+        o = torch.empty(b, r, c, dtype=torch.bfloat16, device="cuda")
+        op = mb.Orthogonalizer(r, c, batch=b, steps=steps, dtype="bf16")
+        op._ws.fill_(0xFF)
+        with mb.KernelTrace(64) as trace:
+            op.orthogonalize(u, o)
+            torch.cuda.synchronize()
+        names = [n for n, _ in trace.durations()]
+        assert names.count("ns_join") == (steps - 1) // 2
+        for i in range(b):
+            assert _rel(o[i], _exact(u[i], (muon.COEFFICIENTS,) * steps)) <= NS + HALF
+
+
+def test_zeros_without_eps(mb):
+    import torch
+    for shape in ((40, 70), (1300, 300)):
+        u, o = torch.zeros(shape, device="cuda"), torch.full(shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        mb.Orthogonalizer(*shape, eps=0.0).orthogonalize(u, o)
+        assert not o.any()
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1e-20, 1e-3, 1e10, 1e25, 1e36])
 def test_size_of_u_does_not_matter(mb, scale):
     """Squares leave float32's range long before the values do."""
