@@ -158,7 +158,7 @@ struct NsTile {
     bool mirror;
 };
 
-template <int TS, bool SYM>
+template <int TM, int TN, bool SYM>
 __device__ __forceinline__ NsTile ns_tile(const NsArgs &a, int t) {
     NsTile w;
     w.batch = t / a.per;
@@ -173,17 +173,20 @@ __device__ __forceinline__ NsTile ns_tile(const NsArgs &a, int t) {
     } else {
         raster_tile(r, a.mt, a.nt, a.group_m, mi, ni);
     }
-    w.m0 = mi * TS;
-    w.n0 = ni * TS;
+    w.m0 = mi * TM;
+    w.n0 = ni * TN;
     w.mirror = SYM && mi != ni;
     return w;
 }
 
-// Loads of one operand's stage: 128 rows (or, MN-major, columns) from `row` on, K block kb.
-template <bool MN>
-__device__ __forceinline__ void load_operand(const CUtensorMap *map, uint64_t *bar, void *dst, int kb, int row, int batch) {
-    if (MN) tma_load_4d(map, bar, dst, 0, kb * kNsK, row / 64, batch);
-    else tma_load_3d(map, bar, dst, kb * kNsK, row, batch);
+// Loads of one operand's stage: ROWS rows (or, MN-major, columns) from `row` on, K block kb, in boxes of BOX.
+template <bool MN, int ROWS = 128, int BOX = 128>
+__device__ __forceinline__ void load_operand(const CUtensorMap *map, uint64_t *bar, uint8_t *dst, int kb, int row, int batch) {
+#pragma unroll
+    for (int i = 0; i < ROWS; i += BOX, row += BOX, dst += BOX * 128) {
+        if (MN) tma_load_4d(map, bar, dst, 0, kb * kNsK, row / 64, batch);
+        else tma_load_3d(map, bar, dst, kb * kNsK, row, batch);
+    }
 }
 template <bool MN>
 __device__ __forceinline__ void load_operand_pair(const CUtensorMap *map, uint32_t bar, void *dst, int kb, int row, int batch) {
@@ -232,8 +235,8 @@ __device__ __forceinline__ float2 ns_combine(const NsArgs &a, float2 v, float2 p
     return make_float2((a.a + d0) * (p.x + q.x) + v.x, (a.a + d1) * (p.y + q.y) + v.y);
 }
 
-// Tensor maps of the epilogue: chunks of 32 rows x 64 columns (128 bytes, swizzled) of what it reads and
-// writes, and of its mirror image (32 columns x 64 rows, as they lie).
+// Tensor maps of the epilogue: chunks of 32 rows x 64 columns (128 bytes, swizzled) or 32 (64 bytes,
+// swizzled) of what it reads and writes, and of its mirror image (32 columns, as they lie).
 struct NsMaps {
     CUtensorMap aux, aux2, out, out_lo, mirror;
 };
@@ -253,10 +256,12 @@ constexpr int kNsChunkBytes = 32 * 128;
 constexpr int kNsStaging = 2 * kNsChunkBytes;   // a warp's: the first tile's chunk, in whose place the output is
                                                 // staged, and the second one's, or the output's low part, or the image
 
-// One warp's part of every tile: rows [row0, row0 + 32) of the CTA's, CHUNKS chunks of 64 columns from col0 on.
-// buf0, buf1: its staging; bar: the barrier of its loads; `loads`: how many it has waited for.
-template <int OP>
+// One warp's part of a tile: rows [row0, row0 + 32), chunks of CC columns (64 or 32) from col0 on.
+// buf0, buf1: its staging; bar, phase: the barrier of its loads.
+template <int OP, int CC = 64>
 struct NsEpilogue {
+    static constexpr int kBytes = 32 * CC * 2;      // of a chunk
+    static constexpr int kRow = CC * 2;
     const NsArgs &a;
     const NsMapRefs maps;
     uint8_t *buf0, *buf1;
@@ -268,24 +273,27 @@ struct NsEpilogue {
     __device__ __forceinline__ bool on(const NsTile &, int row0, int col0) const { return row0 < a.rows && col0 < a.cols; }
     __device__ __forceinline__ bool second() const { return OP == kNsJoin || (OP == kNsUpdate && a.aux2 != nullptr); }
 
+    // What the swizzle of a row's 16-byte pieces is: of 128-byte rows, or of 64-byte ones.
+    static __device__ __forceinline__ int swizzle(int row) { return CC == 64 ? row & 7 : row >> 1 & 3; }
+
     // Asks for a chunk's tiles, once the stores from the same place have read it.
     __device__ __forceinline__ void load(const NsTile &w, int row0, int col0) {
         if (!kNsOne<OP> || !on(w, row0, col0)) return;
         if (lane == 0) {
             bulk_wait_group_read<0>();
-            mbar_expect_relaxed(bar, second() ? 2 * kNsChunkBytes : kNsChunkBytes);
+            mbar_expect_relaxed(bar, second() ? 2 * kBytes : kBytes);
             tma_load_3d(maps.aux, bar, buf0, col0, row0, w.batch);
             if (second()) tma_load_3d(maps.aux2, bar, buf1, col0, row0, w.batch);
         }
         __syncwarp();
     }
 
-    // The chunk from its accumulators v (row `lane`, 64 columns).  The whole warp calls it.
-    __device__ __forceinline__ bool finish(const NsTile &w, int row0, int col0, float (&v)[64]) {
+    // The chunk from its accumulators v (row `lane`, CC columns).  The whole warp calls it.
+    __device__ __forceinline__ bool finish(const NsTile &w, int row0, int col0, float (&v)[CC]) {
         if (!on(w, row0, col0)) return true;
         const int row = row0 + lane;
-        const uint32_t at0 = smem_u32(buf0) + lane * 128, at1 = smem_u32(buf1) + lane * 128;
-        const uint32_t sw = static_cast<uint32_t>(lane & 7);
+        const uint32_t at0 = smem_u32(buf0) + lane * kRow, at1 = smem_u32(buf1) + lane * kRow;
+        const uint32_t sw = static_cast<uint32_t>(swizzle(lane));
         if (kNsOne<OP>) {
             const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase, abort));
             phase ^= 1u;
@@ -299,7 +307,7 @@ struct NsEpilogue {
         const float *by_col = OP == kNsJoin ? a.diag2 : (OP == kNsUpdate && a.diag_col ? a.diag : nullptr);
         const bool two = second();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {   // eight columns: 16 bytes of each tile
+        for (int j = 0; j < CC / 8; ++j) {   // eight columns: 16 bytes of each tile
             const uint32_t off = (static_cast<uint32_t>(j) ^ sw) << 4;
             uint4 x = make_uint4(0, 0, 0, 0), y = make_uint4(0, 0, 0, 0);
             if (kNsOne<OP>) x = ld_shared_v4(at0 + off);
@@ -319,9 +327,17 @@ struct NsEpilogue {
                 v[k + 1] = r.y;
             }
         }
+        if ((OP == kNsSquare || OP == kNsJoin) && row0 < col0 + CC && col0 < row0 + 32) {
+            // the chunk lies on the diagonal: what rounding takes from the lane's value there
+            const int at = row - col0;
+            float x = 0.0f;
+#pragma unroll
+            for (int k = 0; k < CC; ++k) x = k == at ? v[k] : x;
+            if (at >= 0 && at < CC && row < a.rows) a.diag_out[dat + row] = x - __half2float(__float2half_rn(x));
+        }
         if (OP == kNsUpdate && a.o) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < CC / 8; ++j) {
                 const float *e = &v[8 * j];
                 st_shared_v4(at0 + ((static_cast<uint32_t>(j) ^ sw) << 4), pack_bf16x2(a.alpha * e[0], a.alpha * e[1]), pack_bf16x2(a.alpha * e[2], a.alpha * e[3]),
                              pack_bf16x2(a.alpha * e[4], a.alpha * e[5]), pack_bf16x2(a.alpha * e[6], a.alpha * e[7]));
@@ -331,19 +347,19 @@ struct NsEpilogue {
                 __syncwarp();
                 const int n_rows = min(32, a.rows - row0);
                 uint16_t *o = a.o + (static_cast<int64_t>(w.batch) * a.rows + row0) * a.cols + col0 + lane;
-                const bool in0 = col0 + lane < a.cols, in1 = col0 + lane + 32 < a.cols;
+                const bool in0 = col0 + lane < a.cols, in1 = CC == 64 && col0 + lane + 32 < a.cols;
                 for (int r = 0; r < n_rows; ++r, o += a.cols) {
-                    const uint8_t *from = buf0 + r * 128;
+                    const uint8_t *from = buf0 + r * kRow;
                     const int b0 = 2 * lane, b1 = b0 + 64;
-                    if (in0) o[0] = *reinterpret_cast<const uint16_t *>(from + ((((b0 >> 4) ^ (r & 7)) << 4) | (b0 & 15)));
-                    if (in1) o[32] = *reinterpret_cast<const uint16_t *>(from + ((((b1 >> 4) ^ (r & 7)) << 4) | (b1 & 15)));
+                    if (in0) o[0] = *reinterpret_cast<const uint16_t *>(from + ((((b0 >> 4) ^ swizzle(r)) << 4) | (b0 & 15)));
+                    if (in1) o[32] = *reinterpret_cast<const uint16_t *>(from + ((((b1 >> 4) ^ swizzle(r)) << 4) | (b1 & 15)));
                 }
                 __syncwarp();
                 return true;
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < CC / 8; ++j) {
                 const float *e = &v[8 * j];
                 const uint32_t off = (static_cast<uint32_t>(j) ^ sw) << 4;
                 const uint32_t h[4] = {pack_half2(e[0], e[1]), pack_half2(e[2], e[3]), pack_half2(e[4], e[5]), pack_half2(e[6], e[7])};
@@ -357,13 +373,6 @@ struct NsEpilogue {
                     }
                     st_shared_v4(at1 + off, l[0], l[1], l[2], l[3]);
                 }
-                if ((OP == kNsSquare || OP == kNsJoin) && row < a.rows && row >= col0 + 8 * j && row < col0 + 8 * j + 8) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 p = unpack_half2(h[i / 2]);
-                        if (col0 + 8 * j + i == row) a.diag_out[dat + row] = e[i] - (i & 1 ? p.y : p.x);
-                    }
-                }
             }
             if (OP != kNsUpdate && w.mirror) {
                 if (kNsTwo<OP>) __syncwarp();   // every lane has read its row of the second tile
@@ -372,7 +381,7 @@ struct NsEpilogue {
                 const int odd = lane & 1;
                 uint32_t to = smem_u32(buf1) + odd * 64 + (lane - odd) * 2;
 #pragma unroll
-                for (int j = 0; j < 64; j += 2) {
+                for (int j = 0; j < CC; j += 2) {
                     const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
                     const uint32_t u = odd ? pack_half2(got, v[j + 1]) : pack_half2(v[j], got);
                     asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(u) : "memory");
@@ -393,22 +402,31 @@ struct NsEpilogue {
     }
 };
 
+// A warp's accumulators of 64 or 32 columns.
+__device__ __forceinline__ void ns_accumulators(uint32_t at, float (&v)[64]) {
+    tmem_load_64cols(at, *reinterpret_cast<float(*)[32]>(&v[0]), *reinterpret_cast<float(*)[32]>(&v[32]));
+}
+__device__ __forceinline__ void ns_accumulators(uint32_t at, float (&v)[32]) { tmem_load_32cols(at, v); }
+
 // ------------------------------------------------------------------- ns_small
 
 // SPLIT: K is split over a cluster; the parts meet in `dump`, and a CTA finishes some of the
 // tile's rows, 16 neighbouring threads a row, straight from and to global memory.  No mirror images there:
 // a split is for products that leave SMs idle, so every tile is computed.
-template <bool SPLIT_>
+template <bool SPLIT_, int BN_ = 128>
 struct NsSmall {
     static constexpr bool SPLIT = SPLIT_;
-    static constexpr int kEpiWarps = 8;             // two a lane quarter: 64 columns each
+    static constexpr int BN = BN_;                  // columns of a tile
+    static constexpr int kEpiWarps = 8;             // two a lane quarter: half of the columns each
+    static constexpr int kCols = BN / 2;            // a chunk's
     static constexpr int kThreads = 64 + 32 * kEpiWarps;
-    static constexpr int kOpBytes = 128 * 128;
-    static constexpr int kStageBytes = 2 * kOpBytes;
+    static constexpr int kABytes = 128 * 128, kBBytes = BN * 128;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static_assert(!SPLIT || BN == 128, "the cluster's sum");
     static constexpr int kDumpPitch = 132;          // floats of a row: 16-byte accesses of eight rows meet in no bank
     static constexpr int kDumpBytes = SPLIT ? 128 * kDumpPitch * 4 : kEpiWarps * kNsStaging;
     static constexpr int kCtrlBytes = 1024;
-    static constexpr int kStages = (kSmemLimit - 1024 - kCtrlBytes - kDumpBytes) / kStageBytes;
+    static constexpr int kFit = (kSmemLimit - 1024 - kCtrlBytes - kDumpBytes) / kStageBytes, kStages = kFit < 8 ? kFit : 8;
     static constexpr int kSmemBytes = 1024 + kCtrlBytes + kDumpBytes + kStages * kStageBytes;
     static_assert(kStages >= 4, "pipeline");
 };
@@ -468,12 +486,12 @@ __device__ __forceinline__ void ns_finish_eight(const NsArgs &a, const NsTile &w
 template <class C, int OP, bool AMN, bool BMN>
 __global__ void __launch_bounds__(C::kThreads, 1)
 ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const __grid_constant__ NsMaps maps, const NsArgs args) {
-    constexpr bool SYM = OP != kNsUpdate && !C::SPLIT;
-    constexpr int S = C::kStages;
+    constexpr bool SYM = OP != kNsUpdate && !C::SPLIT && C::BN == 128;
+    constexpr int S = C::kStages, BN = C::BN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t *a_s = smem, *b_s = a_s + S * C::kOpBytes;
-    uint8_t *staging = b_s + S * C::kOpBytes;                // the epilogue warps' chunks, or
+    uint8_t *a_s = smem, *b_s = a_s + S * C::kABytes;
+    uint8_t *staging = b_s + S * C::kBBytes;                 // the epilogue warps' chunks, or
     float *dump = reinterpret_cast<float *>(staging);        // [row][column], pitch kDumpPitch
     uint8_t *ctrl = staging + C::kDumpBytes;
     uint64_t *full_bar = reinterpret_cast<uint64_t *>(ctrl);
@@ -519,10 +537,10 @@ ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     griddep_launch_dependents();
     int t = worker;
     NsTile w = {};
-    if (t < args.tiles) w = ns_tile<128, SYM>(args, t);
+    if (t < args.tiles) w = ns_tile<128, BN, SYM>(args, t);
     auto next = [&]() {
         t += workers;
-        if (t < args.tiles) w = ns_tile<128, SYM>(args, t);
+        if (t < args.tiles) w = ns_tile<128, BN, SYM>(args, t);
     };
     const int k0 = args.kblocks * rank / cs, k1 = args.kblocks * (rank + 1) / cs;
     griddep_wait();
@@ -538,8 +556,8 @@ ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 if (!ok) break;
                 if (issue) {
                     mbar_expect_relaxed(&full_bar[stage], C::kStageBytes);
-                    load_operand<AMN>(&tmA, &full_bar[stage], a_s + stage * C::kOpBytes, kb, w.m0, w.batch);
-                    load_operand<BMN>(&tmB, &full_bar[stage], b_s + stage * C::kOpBytes, kb, w.n0, w.batch);
+                    load_operand<AMN, 128, BN>(&tmA, &full_bar[stage], a_s + stage * C::kABytes, kb, w.m0, w.batch);
+                    load_operand<BMN, BN, BN>(&tmB, &full_bar[stage], b_s + stage * C::kBBytes, kb, w.n0, w.batch);
                 }
                 __syncwarp();
                 if (++stage == S) {
@@ -565,12 +583,12 @@ ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort_flag));
                 if (!ok) break;
                 tc_fence_after_sync();
-                const uint64_t ad = a0 + stage * (C::kOpBytes >> 4), bd = b0 + stage * (C::kOpBytes >> 4);
+                const uint64_t ad = a0 + stage * (C::kABytes >> 4), bd = b0 + stage * (C::kBBytes >> 4);
                 if (issue) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        umma_bf16(tmem_base + buf * 128, ad + j * kOperandStep<AMN>, bd + j * kOperandStep<BMN>,
-                                  idesc_f16_f32(128, 128, AMN, BMN), (kb > k0 || j > 0) ? 1u : 0u);
+                        umma_bf16(tmem_base + buf * BN, ad + j * kOperandStep<AMN>, bd + j * kOperandStep<BMN>,
+                                  idesc_f16_f32(128, BN, AMN, BMN), (kb > k0 || j > 0) ? 1u : 0u);
                     umma_commit(&empty_bar[stage]);
                 }
                 __syncwarp();
@@ -587,8 +605,8 @@ ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     } else if constexpr (!C::SPLIT) {
         const int q = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
         uint8_t *st = staging + ew * kNsStaging;
-        NsEpilogue<OP> epi = {args, NsMapRefs(maps), st, st + kNsChunkBytes, &aux_bar[ew], abort_flag, lane, 0};
-        auto place = [&](const NsTile &x, int &row, int &col) { row = x.m0 + 32 * q, col = x.n0 + 64 * half; };
+        NsEpilogue<OP, C::kCols> epi = {args, NsMapRefs(maps), st, st + kNsChunkBytes, &aux_bar[ew], abort_flag, lane, 0};
+        auto place = [&](const NsTile &x, int &row, int &col) { row = x.m0 + 32 * q, col = x.n0 + C::kCols * half; };
         int it = 0, row, col;
         if (t < args.tiles) {
             place(w, row, col);
@@ -600,9 +618,8 @@ ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             bool ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort_flag));
             if (!ok) break;
             tc_fence_after_sync();
-            float v[64];
-            tmem_load_64cols(tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * 128 + 64 * half, *reinterpret_cast<float(*)[32]>(&v[0]),
-                             *reinterpret_cast<float(*)[32]>(&v[32]));
+            float v[C::kCols];
+            ns_accumulators(tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * BN + C::kCols * half, v);
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive_relaxed(&acce_bar[buf]);
@@ -757,10 +774,10 @@ ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     griddep_launch_dependents();
     int t = worker;
     NsTile w = {};
-    if (t < args.tiles) w = ns_tile<256, SYM>(args, t);
+    if (t < args.tiles) w = ns_tile<256, 256, SYM>(args, t);
     auto next = [&]() {
         t += workers;
-        if (t < args.tiles) w = ns_tile<256, SYM>(args, t);
+        if (t < args.tiles) w = ns_tile<256, 256, SYM>(args, t);
     };
     griddep_wait();
 
@@ -915,7 +932,7 @@ struct NsFusedMaps {
 constexpr int kFusedCtas = 8;          // of a cluster, at most
 
 struct NsFused {
-    using C = NsSmall<false>;
+    using C = NsSmall<false, 64>;
     uint8_t *a_s, *b_s, *staging;
     uint64_t *full_bar, *empty_bar, *accf_bar, *acce_bar, *aux_bar;
     volatile int *abort;
@@ -934,7 +951,7 @@ struct NsFused {
             NsTile w = {};
             w.batch = batch;
             w.m0 = t % a.mt * 128;
-            w.n0 = t / a.mt * 128;
+            w.n0 = t / a.mt * C::BN;
             return w;
         };
         if (warp == 0) {
@@ -948,8 +965,8 @@ struct NsFused {
                     if (!ok) break;
                     if (issue) {
                         mbar_expect_relaxed(&full_bar[stage], C::kStageBytes);
-                        load_operand<AMN>(mA, &full_bar[stage], a_s + stage * C::kOpBytes, kb, w.m0, batch);
-                        load_operand<BMN>(mB, &full_bar[stage], b_s + stage * C::kOpBytes, kb, w.n0, batch);
+                        load_operand<AMN, 128, C::BN>(mA, &full_bar[stage], a_s + stage * C::kABytes, kb, w.m0, batch);
+                        load_operand<BMN, C::BN, C::BN>(mB, &full_bar[stage], b_s + stage * C::kBBytes, kb, w.n0, batch);
                     }
                     __syncwarp();
                     if (++stage == S) {
@@ -971,12 +988,12 @@ struct NsFused {
                     ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort));
                     if (!ok) break;
                     tc_fence_after_sync();
-                    const uint64_t ad = a0 + stage * (C::kOpBytes >> 4), bd = b0 + stage * (C::kOpBytes >> 4);
+                    const uint64_t ad = a0 + stage * (C::kABytes >> 4), bd = b0 + stage * (C::kBBytes >> 4);
                     if (issue) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            umma_bf16(tmem + buf * 128, ad + j * kOperandStep<AMN>, bd + j * kOperandStep<BMN>,
-                                      idesc_f16_f32(128, 128, AMN, BMN), (kb > 0 || j > 0) ? 1u : 0u);
+                            umma_bf16(tmem + buf * C::BN, ad + j * kOperandStep<AMN>, bd + j * kOperandStep<BMN>,
+                                      idesc_f16_f32(128, C::BN, AMN, BMN), (kb > 0 || j > 0) ? 1u : 0u);
                         umma_commit(&empty_bar[stage]);
                     }
                     __syncwarp();
@@ -992,30 +1009,28 @@ struct NsFused {
         } else {
             const int q = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
             uint8_t *st = staging + ew * kNsStaging;
-            NsEpilogue<OP> epi = {a, maps, st, st + kNsChunkBytes, &aux_bar[ew], abort, lane, phase};
+            NsEpilogue<OP, C::kCols> epi = {a, maps, st, st + kNsChunkBytes, &aux_bar[ew], abort, lane, phase};
             if (lane == 0) fence_proxy_async_global();
-            if (t < tiles) epi.load(tile(), t % a.mt * 128 + 32 * q, t / a.mt * 128 + 64 * half);
+            if (t < tiles) epi.load(tile(), t % a.mt * 128 + 32 * q, t / a.mt * C::BN + C::kCols * half);
             while (t < tiles) {
                 const NsTile w = tile();
                 const int buf = it & 1;
                 const bool ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort));
                 if (!ok) break;
                 tc_fence_after_sync();
-                float v[64];
-                tmem_load_64cols(tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * 128 + 64 * half, *reinterpret_cast<float(*)[32]>(&v[0]),
-                                 *reinterpret_cast<float(*)[32]>(&v[32]));
+                float v[C::kCols];
+                ns_accumulators(tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * C::BN + C::kCols * half, v);
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_relaxed(&acce_bar[buf]);
-                if (!epi.finish(w, w.m0 + 32 * q, w.n0 + 64 * half, v)) break;
+                if (!epi.finish(w, w.m0 + 32 * q, w.n0 + C::kCols * half, v)) break;
                 t += ctas;
                 ++it;
-                if (t < tiles) epi.load(tile(), t % a.mt * 128 + 32 * q, t / a.mt * 128 + 64 * half);
+                if (t < tiles) epi.load(tile(), t % a.mt * 128 + 32 * q, t / a.mt * C::BN + C::kCols * half);
             }
             if (lane == 0) {
                 bulk_wait_group<0>();
                 if (*abort) mbar_drain(&aux_bar[ew], epi.phase);   // a load may still be on its way
-                fence_proxy_async_global();
             }
             __syncwarp();
             phase = epi.phase;
@@ -1025,16 +1040,16 @@ struct NsFused {
 };
 
 template <bool TALL>
-__global__ void __launch_bounds__(NsSmall<false>::kThreads, 1)
+__global__ void __launch_bounds__(NsFused::C::kThreads, 1)
 ns_fused_kernel(const __grid_constant__ NsFusedMaps maps, const __grid_constant__ NsFusedArgs args) {
-    using C = NsSmall<false>;
+    using C = NsSmall<false, 64>;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     NsFused f;
     f.a_s = smem;
-    f.b_s = f.a_s + S * C::kOpBytes;
-    f.staging = f.b_s + S * C::kOpBytes;
+    f.b_s = f.a_s + S * C::kABytes;
+    f.staging = f.b_s + S * C::kBBytes;
     uint8_t *ctrl = f.staging + C::kDumpBytes;
     f.full_bar = reinterpret_cast<uint64_t *>(ctrl);
     f.empty_bar = f.full_bar + S;
@@ -1084,7 +1099,8 @@ ns_fused_kernel(const __grid_constant__ NsFusedMaps maps, const __grid_constant_
 
     NsArgs sq = {};                    // G and P
     sq.rows = sq.cols = args.m;
-    sq.mt = sq.nt = (args.m + 127) / 128;
+    sq.mt = (args.m + 127) / 128;
+    sq.nt = (args.m + C::BN - 1) / C::BN;
     sq.diag_pitch = args.g_pitch;
     sq.diag = sq.diag_out = args.diag;
     sq.alpha = 1.0f / (args.sx * args.sx);
@@ -1092,7 +1108,7 @@ ns_fused_kernel(const __grid_constant__ NsFusedMaps maps, const __grid_constant_
     up.rows = args.rows;
     up.cols = args.cols;
     up.mt = (args.rows + 127) / 128;
-    up.nt = (args.cols + 127) / 128;
+    up.nt = (args.cols + C::BN - 1) / C::BN;
     up.diag_pitch = args.g_pitch;
     up.diag = args.diag;
     up.diag_col = TALL;
@@ -1145,9 +1161,9 @@ ns_fused_kernel(const __grid_constant__ NsFusedMaps maps, const __grid_constant_
 // ------------------------------------------------------------------------ host
 
 // A batch of fp16 matrices [rows][cols], rows of `pitch` elements.  K-major: boxes of 64
-// columns x 128 rows.  MN-major: K runs over the rows; a box is 64 rows of two blocks of 64
-// columns (the map's third dimension walks the blocks, up to the pitch).
-bool ns_map(CUtensorMap *m, const __half *p, bool mn, int64_t rows, int64_t cols, int64_t pitch, int batch) {
+// columns x 128 (or 64) rows.  MN-major: K runs over the rows; a box is 64 rows of two blocks (or
+// one) of 64 columns (the map's third dimension walks the blocks, up to the pitch).
+bool ns_map(CUtensorMap *m, const __half *p, bool mn, int64_t rows, int64_t cols, int64_t pitch, int batch, uint32_t box_rows = 128) {
     EncodeTiledFn fn = encode_tiled_fn();
     if (!fn) return false;
     const cuuint64_t R = static_cast<cuuint64_t>(rows), line = static_cast<cuuint64_t>(pitch) * 2, B = static_cast<cuuint64_t>(batch);
@@ -1155,19 +1171,20 @@ bool ns_map(CUtensorMap *m, const __half *p, bool mn, int64_t rows, int64_t cols
     if (mn) {
         cuuint64_t dims[4] = {64, R, static_cast<cuuint64_t>(pitch / 64), B};
         cuuint64_t strides[3] = {line, 128, R * line};
-        cuuint32_t box[4] = {64, kNsK, 2, 1};
+        cuuint32_t box[4] = {64, kNsK, box_rows / 64, 1};
         return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<__half *>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     }
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), R, B};
     cuuint64_t strides[2] = {line, R * line};
-    cuuint32_t box[3] = {kNsK, 128, 1};
+    cuuint32_t box[3] = {kNsK, box_rows, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half *>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Boxes of `box_cols` x `box_rows` for the epilogue, of 16-bit values (fp16, or o's bf16).
-bool ns_chunk_map(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t pitch, int batch, uint32_t box_cols, uint32_t box_rows) {
+// Boxes of `box_cols` (64 or 32) x `box_rows` for the epilogue, of 16-bit values (fp16, or o's bf16); a mirror
+// image's are not swizzled.
+bool ns_chunk_map(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t pitch, int batch, uint32_t box_cols, uint32_t box_rows, bool swizzle = true) {
     EncodeTiledFn fn = encode_tiled_fn();
     if (!fn) return false;
     const cuuint64_t line = static_cast<cuuint64_t>(pitch) * 2;
@@ -1176,22 +1193,22 @@ bool ns_chunk_map(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int
     cuuint32_t box[3] = {box_cols, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              swizzle ? (box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The maps that the epilogue of `a` uses.
-bool ns_epilogue_maps(NsMaps *m, const NsArgs &a, int batch) {
+// The maps that the epilogue of `a` uses, in chunks of `cols` columns.
+bool ns_epilogue_maps(NsMaps *m, const NsArgs &a, int batch, uint32_t cols = 64) {
     bool ok = true;
-    if (a.aux) ok &= ns_chunk_map(&m->aux, a.aux, a.rows, a.cols, a.pitch, batch, 64, 32);
-    if (a.aux2) ok &= ns_chunk_map(&m->aux2, a.aux2, a.rows, a.cols, a.pitch, batch, 64, 32);
+    if (a.aux) ok &= ns_chunk_map(&m->aux, a.aux, a.rows, a.cols, a.pitch, batch, cols, 32);
+    if (a.aux2) ok &= ns_chunk_map(&m->aux2, a.aux2, a.rows, a.cols, a.pitch, batch, cols, 32);
     if (a.o) {
-        if (a.o_tma) ok &= ns_chunk_map(&m->out, a.o, a.rows, a.cols, a.cols, batch, 64, 32);
+        if (a.o_tma) ok &= ns_chunk_map(&m->out, a.o, a.rows, a.cols, a.cols, batch, cols, 32);
     } else {
-        ok &= ns_chunk_map(&m->out, a.out, a.rows, a.cols, a.pitch, batch, 64, 32);
-        if (a.out_lo) ok &= ns_chunk_map(&m->out_lo, a.out_lo, a.rows, a.cols, a.pitch, batch, 64, 32);
+        ok &= ns_chunk_map(&m->out, a.out, a.rows, a.cols, a.pitch, batch, cols, 32);
+        if (a.out_lo) ok &= ns_chunk_map(&m->out_lo, a.out_lo, a.rows, a.cols, a.pitch, batch, cols, 32);
     }
-    if (a.op != kNsUpdate) ok &= ns_chunk_map(&m->mirror, a.out, a.rows, a.cols, a.pitch, batch, 32, 64);
+    if (a.op != kNsUpdate) ok &= ns_chunk_map(&m->mirror, a.out, a.rows, a.cols, a.pitch, batch, 32, 64, false);
     return ok;
 }
 
@@ -1229,13 +1246,23 @@ int64_t tiles_of(const NsArgs &a, int ts, bool sym) {
     return sym ? mt * (mt + 1) / 2 : mt * nt;
 }
 
+// One operand: a batch of matrices as they lie.
+struct NsOperand {
+    const __half *p;
+    int64_t rows, cols;
+};
+
 template <int OP, bool AMN, bool BMN>
-int run_ns(NsArgs a, const CUtensorMap &mA, const CUtensorMap &mB, int batch, int sms, cudaStream_t s) {
+int run_ns(NsArgs a, const NsOperand &A, const NsOperand &B, int batch, int sms, cudaStream_t s) {
     constexpr bool SYM = OP != kNsUpdate;
     const int64_t pair_tiles = tiles_of(a, 256, SYM) * batch, tiles = tiles_of(a, 128, SYM) * batch;
     const int pairs = sms / 2;
     if (tiles > INT32_MAX) return MLPBLK_EINVAL;
     NsMaps maps = {};
+    CUtensorMap mA, mB;
+    auto operands = [&](uint32_t box) {
+        return ns_map(&mA, A.p, AMN, A.rows, A.cols, ortho_pitch(A.cols), batch, box) && ns_map(&mB, B.p, BMN, B.rows, B.cols, ortho_pitch(B.cols), batch, box);
+    };
     // Rounds of tiles, each with its stages of K and the part of its epilogue that nothing hides
     // (us, measured: 8 x 1024 x 2048, 4096 x 16384): a pair's 256 x 256 tile 0.3 a stage and 3.6, a
     // CTA's 128 x 128 one 0.22 and 2.2.  (X X^T of 8 x 1024 x 2048: 80 pair tiles on 76 pairs 31 us, 288
@@ -1249,7 +1276,7 @@ int run_ns(NsArgs a, const CUtensorMap &mA, const CUtensorMap &mB, int batch, in
         a.tiles = static_cast<int>(pair_tiles);
         a.group_m = 8;
         const int workers = a.tiles < pairs ? a.tiles : pairs;
-        if (!ns_epilogue_maps(&maps, a, batch)) return MLPBLK_ECUDA;
+        if (!operands(128) || !ns_epilogue_maps(&maps, a, batch)) return MLPBLK_ECUDA;
         return launch_ns(ns_pair_kernel<OP, AMN, BMN>, NsPair::kThreads, NsPair::kSmemBytes, 2 * workers, 2, mA, mB, maps, a, attr_set, s);
     }
     a.mt = (a.rows + 127) / 128;
@@ -1268,13 +1295,25 @@ int run_ns(NsArgs a, const CUtensorMap &mA, const CUtensorMap &mB, int batch, in
     if (split > 1) {
         a.per = a.mt * a.nt;
         a.tiles = static_cast<int>(every);
+        if (!operands(128)) return MLPBLK_ECUDA;
         static int attr_set[64] = {0};
         return launch_ns(ns_small_kernel<NsSmall<true>, OP, AMN, BMN>, NsSmall<true>::kThreads, NsSmall<true>::kSmemBytes, a.tiles * split,
                          split, mA, mB, maps, a, attr_set, s);
     }
+    // Tiles of 64 columns where they fit in one round: half the MMAs and half the epilogue of each.
+    const int64_t halves = static_cast<int64_t>(a.mt) * ((a.cols + 63) / 64) * batch;
+    if (halves <= sms) {
+        using C = NsSmall<false, 64>;
+        a.nt = (a.cols + 63) / 64;
+        a.per = a.mt * a.nt;
+        a.tiles = static_cast<int>(halves);
+        if (!operands(64) || !ns_epilogue_maps(&maps, a, batch, C::kCols)) return MLPBLK_ECUDA;
+        static int attr_set[64] = {0};
+        return launch_ns(ns_small_kernel<C, OP, AMN, BMN>, C::kThreads, C::kSmemBytes, a.tiles, 1, mA, mB, maps, a, attr_set, s);
+    }
     a.per = static_cast<int>(tiles / batch);
     a.tiles = static_cast<int>(tiles);
-    if (!ns_epilogue_maps(&maps, a, batch)) return MLPBLK_ECUDA;
+    if (!operands(128) || !ns_epilogue_maps(&maps, a, batch)) return MLPBLK_ECUDA;
     static int attr_set[64] = {0};
     return launch_ns(ns_small_kernel<NsSmall<false>, OP, AMN, BMN>, NsSmall<false>::kThreads, NsSmall<false>::kSmemBytes, a.tiles < sms ? a.tiles : sms, 1,
                      mA, mB, maps, a, attr_set, s);
@@ -1300,7 +1339,7 @@ int launch_ns_product(const NsProduct &p, int sms, cudaStream_t s) {
     a.o = static_cast<uint16_t *>(p.o);
     a.o_tma = p.cols % 8 == 0;
     a.kblocks = static_cast<int>((m + kNsK - 1) / kNsK);
-    CUtensorMap mA, mB;
+    const NsOperand X = {p.x, p.rows, p.cols}, Y = {p.y, m, m}, P = {p.p, m, m};
     if (p.op == kNsUpdate) {
         a.rows = static_cast<int>(p.rows);
         a.cols = static_cast<int>(p.cols);
@@ -1309,12 +1348,7 @@ int launch_ns_product(const NsProduct &p, int sms, cudaStream_t s) {
         a.aux = p.x;
         a.aux2 = p.x_lo;
         a.diag_col = p.tall;
-        if (p.tall) {
-            if (!ns_map(&mA, p.x, false, p.rows, p.cols, x_pitch, p.batch) || !ns_map(&mB, p.p, false, m, m, g_pitch, p.batch)) return MLPBLK_ECUDA;
-            return run_ns<kNsUpdate, false, false>(a, mA, mB, p.batch, sms, s);
-        }
-        if (!ns_map(&mA, p.p, false, m, m, g_pitch, p.batch) || !ns_map(&mB, p.x, true, p.rows, p.cols, x_pitch, p.batch)) return MLPBLK_ECUDA;
-        return run_ns<kNsUpdate, false, true>(a, mA, mB, p.batch, sms, s);
+        return p.tall ? run_ns<kNsUpdate, false, false>(a, X, P, p.batch, sms, s) : run_ns<kNsUpdate, false, true>(a, P, X, p.batch, sms, s);
     }
     a.rows = a.cols = static_cast<int>(m);
     a.pitch = static_cast<int>(g_pitch);
@@ -1322,21 +1356,18 @@ int launch_ns_product(const NsProduct &p, int sms, cudaStream_t s) {
     if (p.op == kNsGram) {
         const int64_t n = p.tall ? p.rows : p.cols;
         a.kblocks = static_cast<int>((n + kNsK - 1) / kNsK);
-        if (!ns_map(&mA, p.x, p.tall, p.rows, p.cols, x_pitch, p.batch)) return MLPBLK_ECUDA;
-        return p.tall ? run_ns<kNsGram, true, true>(a, mA, mA, p.batch, sms, s) : run_ns<kNsGram, false, false>(a, mA, mA, p.batch, sms, s);
+        return p.tall ? run_ns<kNsGram, true, true>(a, X, X, p.batch, sms, s) : run_ns<kNsGram, false, false>(a, X, X, p.batch, sms, s);
     }
     a.aux = p.y;
     if (p.op == kNsJoin) a.aux2 = p.p;
-    if (!ns_map(&mB, p.y, false, m, m, g_pitch, p.batch)) return MLPBLK_ECUDA;
-    if (p.op == kNsSquare) return run_ns<kNsSquare, false, false>(a, mB, mB, p.batch, sms, s);
-    if (!ns_map(&mA, p.p, false, m, m, g_pitch, p.batch)) return MLPBLK_ECUDA;
-    if (p.op == kNsApply) return run_ns<kNsApply, false, false>(a, mA, mB, p.batch, sms, s);
-    return run_ns<kNsJoin, false, false>(a, mA, mB, p.batch, sms, s);
+    if (p.op == kNsSquare) return run_ns<kNsSquare, false, false>(a, Y, Y, p.batch, sms, s);
+    if (p.op == kNsApply) return run_ns<kNsApply, false, false>(a, P, Y, p.batch, sms, s);
+    return run_ns<kNsJoin, false, false>(a, P, Y, p.batch, sms, s);
 }
 
 // CTAs of a matrix: one a tile of X, up to eight.
 static int ns_fused_ctas(int64_t rows, int64_t cols) {
-    const int64_t tiles = (rows + 127) / 128 * ((cols + 127) / 128);
+    const int64_t tiles = (rows + 127) / 128 * ((cols + NsFused::C::BN - 1) / NsFused::C::BN);
     int c = 1;
     while (c < kFusedCtas && c < tiles) c *= 2;
     return c;
@@ -1365,13 +1396,13 @@ int launch_ns_fused(const NsFusedProblem &p, cudaStream_t s) {
     for (int i = 0; i < p.steps; ++i)
         for (int j = 0; j < 3; ++j) a.coef[i][j] = p.coefficients[i][j];
     NsFusedMaps maps = {};
-    bool ok = ns_map(&maps.g, p.g, false, m, m, g_pitch, p.batch) && ns_map(&maps.p, p.p, false, m, m, g_pitch, p.batch) &&
-              ns_chunk_map(&maps.g_chunk, p.g, m, m, g_pitch, p.batch, 64, 32) && ns_chunk_map(&maps.p_chunk, p.p, m, m, g_pitch, p.batch, 64, 32) &&
-              ns_chunk_map(&maps.lo_chunk, p.lo, p.rows, p.cols, x_pitch, p.batch, 64, 32);
-    if (p.o && p.cols % 8 == 0) ok = ok && ns_chunk_map(&maps.o_chunk, p.o, p.rows, p.cols, p.cols, p.batch, 64, 32);
+    bool ok = ns_map(&maps.g, p.g, false, m, m, g_pitch, p.batch, NsFused::C::BN) && ns_map(&maps.p, p.p, false, m, m, g_pitch, p.batch, NsFused::C::BN) &&
+              ns_chunk_map(&maps.g_chunk, p.g, m, m, g_pitch, p.batch, NsFused::C::kCols, 32) && ns_chunk_map(&maps.p_chunk, p.p, m, m, g_pitch, p.batch, NsFused::C::kCols, 32) &&
+              ns_chunk_map(&maps.lo_chunk, p.lo, p.rows, p.cols, x_pitch, p.batch, NsFused::C::kCols, 32);
+    if (p.o && p.cols % 8 == 0) ok = ok && ns_chunk_map(&maps.o_chunk, p.o, p.rows, p.cols, p.cols, p.batch, NsFused::C::kCols, 32);
     for (int i = 0; i < 2; ++i)
-        ok = ok && ns_map(&maps.x_k[i], p.x[i], false, p.rows, p.cols, x_pitch, p.batch) && ns_map(&maps.x_mn[i], p.x[i], true, p.rows, p.cols, x_pitch, p.batch) &&
-             ns_chunk_map(&maps.x_chunk[i], p.x[i], p.rows, p.cols, x_pitch, p.batch, 64, 32);
+        ok = ok && ns_map(&maps.x_k[i], p.x[i], false, p.rows, p.cols, x_pitch, p.batch, NsFused::C::BN) && ns_map(&maps.x_mn[i], p.x[i], true, p.rows, p.cols, x_pitch, p.batch, NsFused::C::BN) &&
+             ns_chunk_map(&maps.x_chunk[i], p.x[i], p.rows, p.cols, x_pitch, p.batch, NsFused::C::kCols, 32);
     if (!ok) return MLPBLK_ECUDA;
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1379,15 +1410,15 @@ int launch_ns_fused(const NsFusedProblem &p, cudaStream_t s) {
     static int attr_set[2][64] = {};
     void (*const kernel)(NsFusedMaps, NsFusedArgs) = tall ? ns_fused_kernel<true> : ns_fused_kernel<false>;
     if (!attr_set[tall][dev]) {
-        const int rc = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NsSmall<false>::kSmemBytes));
+        const int rc = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NsFused::C::kSmemBytes));
         if (rc != MLPBLK_OK) return rc;
         attr_set[tall][dev] = 1;
     }
     cudaLaunchConfig_t cfg = {};
     const int ctas = ns_fused_ctas(p.rows, p.cols);
     cfg.gridDim = dim3(static_cast<unsigned>(p.batch * ctas));
-    cfg.blockDim = dim3(NsSmall<false>::kThreads);
-    cfg.dynamicSmemBytes = NsSmall<false>::kSmemBytes;
+    cfg.blockDim = dim3(NsFused::C::kThreads);
+    cfg.dynamicSmemBytes = NsFused::C::kSmemBytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
