@@ -911,7 +911,7 @@ ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 // ------------------------------------------------------------------- ns_fused
 
 // All steps of a small matrix in one launch: a cluster of up to eight CTAs a matrix, whose products
-// follow one another between cluster barriers instead of launches (256 x 256, five steps: 81 -> 68 us).
+// follow one another between cluster barriers instead of launches (256 x 256, five steps: 51 us, 58 by launches).
 // A product's tiles are dealt out to the CTAs; between products everything goes through L2, by
 // the copies of the asynchronous proxy on both sides (but the diagonal's remainders).
 struct NsFusedArgs {
@@ -1373,11 +1373,13 @@ static int ns_fused_ctas(int64_t rows, int64_t cols) {
     return c;
 }
 
-// One launch where a product is short beside a launch, and all matrices run at once (us, one launch and
-// several: 256 x 256 68 and 81, 256 x 1024 87 and 93, 250 x 2000 122 and 108, 16 of 256 x 256 77 and 87).
+// One launch where a CTA has one tile of X and all matrices run at once; clusters of more than two
+// CTAs find room for some two thirds of the SMs (us, one launch and several: 256 x 256 51 and 58, 128 x 512
+// 50 and 56, 200 x 400 60 and 60, 250 x 1000 79 and 67; 12 of 256 x 256 54 and 61, 16 100 and 64).
 bool ns_fused_fits(int64_t rows, int64_t cols, int batch, int sms) {
-    const int64_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
-    return m <= 256 && n <= 1024 && static_cast<int64_t>(batch) * ns_fused_ctas(rows, cols) <= sms;
+    const int64_t tiles = (rows + 127) / 128 * ((cols + NsFused::C::BN - 1) / NsFused::C::BN);
+    const int64_t ctas = static_cast<int64_t>(batch) * ns_fused_ctas(rows, cols);
+    return tiles <= kFusedCtas && ctas <= (tiles <= 2 ? sms : sms * 2 / 3);
 }
 
 int launch_ns_fused(const NsFusedProblem &p, cudaStream_t s) {
