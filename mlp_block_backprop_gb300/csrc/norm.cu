@@ -282,7 +282,6 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-constexpr int kNormThreads = 128;      // of a CTA, at least
 constexpr int kNormMaxWarps = 16;      // of a row
 
 // Threads of row slot `slot` meet (its warps alone).
@@ -608,16 +607,20 @@ NormShape norm_shape(int width, int unit, int64_t T, int sms, bool backward) {
 
 template <class L, int N>
 int run_norm(NormArgs a, bool backward, int sms, cudaStream_t s, int *parts) {
-    const int threads = 32 * a.warps > kNormThreads ? 32 * a.warps : kNormThreads;
+    // Many rows: CTAs as large as they go (fewer partial rows of dgamma, and the rows of a CTA lie together:
+    // 16384 x 4096 forward 66 us with 512 threads, 72 with 128, backward 77 and 80; 4097 x 1001 float32 backward
+    // 13.3 and 14.2).  Few: 128 (300 x 1000 2.9 us, with 512 3.4), backward 256 (5.5; 128 6.1, 512 5.7).
+    const int least = a.T >= static_cast<int64_t>(sms) * 16 ? 32 * kNormMaxWarps : (backward ? 256 : 128);
+    const int threads = 32 * a.warps > least ? 32 * a.warps : least;
     const int slots = threads / (32 * a.warps);
     const size_t smem = backward ? static_cast<size_t>(slots - 1) * a.warps * N * L::kUnit * 4 : 0;
     void (*const kernel)(NormArgs) = backward ? add_rmsnorm_bwd_kernel<L, N> : (a.residual ? add_rmsnorm_kernel<L, N, true> : add_rmsnorm_kernel<L, N, false>);
-    static int occ[3][5][64] = {};   // resident CTAs an SM, by kernel, log2(warps) and device
+    static int occ[3][2][5][64] = {};   // resident CTAs an SM, by kernel, size, log2(warps) and device
     int dev = 0, lg = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) return MLPBLK_ECUDA;
     while ((1 << lg) < a.warps) ++lg;
-    int &o = occ[backward ? 2 : (a.residual ? 1 : 0)][lg][dev];
+    int &o = occ[backward ? 2 : (a.residual ? 1 : 0)][threads == 32 * kNormMaxWarps][lg][dev];
     if (o == 0) {
         int n = 0;
         const int rc = cuda_status(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem));
