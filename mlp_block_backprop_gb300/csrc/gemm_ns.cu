@@ -714,11 +714,13 @@ ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 // -------------------------------------------------------------------- ns_pair
 
 struct NsPair {
-    static constexpr int kThreads = 320;            // producer, MMA, eight epilogue warps
+    static constexpr int kEpiWarps = 16;            // four a lane quarter: 64 columns each, in two chunks
+    static constexpr int kCols = 32;                // of a chunk
+    static constexpr int kThreads = 64 + 32 * kEpiWarps;
     static constexpr int kOpBytes = 128 * 128;      // 128 rows of A or B a CTA
     static constexpr int kStageBytes = 2 * kOpBytes;
     static constexpr int kCtrlBytes = 1024;
-    static constexpr int kStagingBytes = 8 * kNsStaging;
+    static constexpr int kWarpStaging = 2 * 32 * kCols * 2, kStagingBytes = kEpiWarps * kWarpStaging;
     static constexpr int kStages = (kSmemLimit - 1024 - kCtrlBytes - kStagingBytes) / kStageBytes;
     static constexpr int kSmemBytes = 1024 + kCtrlBytes + kStagingBytes + kStages * kStageBytes;
     static_assert(kStages >= 4, "pipeline");
@@ -754,9 +756,9 @@ ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accf_bar[b], 1);
-            mbar_init(&acce_bar[b], 16);  // both CTAs' epilogue warps (the leader's barrier counts)
+            mbar_init(&acce_bar[b], 2 * P::kEpiWarps);  // both CTAs' epilogue warps (the leader's barrier counts)
         }
-        for (int b = 0; b < 8; ++b) mbar_init(&aux_bar[b], 1);
+        for (int b = 0; b < P::kEpiWarps; ++b) mbar_init(&aux_bar[b], 1);
         *abort_flag = 0;
         fence_barrier_init();
         prefetch_tensormap(&tmA);
@@ -850,12 +852,12 @@ ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         }
         __syncwarp();
     } else {
-        // two warps a lane quarter: two chunks of 64 columns each
-        const int q = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
+        const int q = warp & 3, part = (warp - 2) >> 2, ew = warp - 2;
+        constexpr int CC = P::kCols;
         const uint32_t acce0 = mapa_shared(smem_u32(&acce_bar[0]), 0);
-        uint8_t *st = staging + ew * kNsStaging;
-        NsEpilogue<OP> epi = {args, NsMapRefs(maps), st, st + kNsChunkBytes, &aux_bar[ew], abort_flag, lane, 0};
-        auto place = [&](const NsTile &x, int &row, int &col) { row = x.m0 + static_cast<int>(rank) * 128 + 32 * q, col = x.n0 + 128 * half; };
+        uint8_t *st = staging + ew * P::kWarpStaging;
+        NsEpilogue<OP, CC> epi = {args, NsMapRefs(maps), st, st + P::kWarpStaging / 2, &aux_bar[ew], abort_flag, lane, 0};
+        auto place = [&](const NsTile &x, int &row, int &col) { row = x.m0 + static_cast<int>(rank) * 128 + 32 * q, col = x.n0 + 64 * part; };
         int it = 0, row, col;
         if (t < args.tiles) {
             place(w, row, col);
@@ -864,14 +866,14 @@ ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         while (t < args.tiles) {
             place(w, row, col);
             const int buf = it & 1;
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * 256 + 128 * half;
+            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * 256 + 64 * part;
             bool ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort_flag));
             if (!ok) break;
             tc_fence_after_sync();
 #pragma unroll 1
             for (int c = 0; c < 2; ++c) {
-                float v[64];
-                tmem_load_64cols(t_row + 64 * c, *reinterpret_cast<float(*)[32]>(&v[0]), *reinterpret_cast<float(*)[32]>(&v[32]));
+                float v[CC];
+                ns_accumulators(t_row + CC * c, v);
                 if (c == 1) {
                     tc_fence_before_sync();
                     __syncwarp();
@@ -880,9 +882,9 @@ ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         else mbar_arrive_cluster_relaxed(acce0 + buf * 8);
                     }
                 }
-                ok = epi.finish(w, row, col + 64 * c, v);
+                ok = epi.finish(w, row, col + CC * c, v);
                 if (!ok) break;
-                if (c == 0) epi.load(w, row, col + 64);
+                if (c == 0) epi.load(w, row, col + CC);
             }
             if (!ok) break;
             next();
@@ -1208,7 +1210,7 @@ bool ns_epilogue_maps(NsMaps *m, const NsArgs &a, int batch, uint32_t cols = 64)
         ok &= ns_chunk_map(&m->out, a.out, a.rows, a.cols, a.pitch, batch, cols, 32);
         if (a.out_lo) ok &= ns_chunk_map(&m->out_lo, a.out_lo, a.rows, a.cols, a.pitch, batch, cols, 32);
     }
-    if (a.op != kNsUpdate) ok &= ns_chunk_map(&m->mirror, a.out, a.rows, a.cols, a.pitch, batch, 32, 64, false);
+    if (a.op != kNsUpdate) ok &= ns_chunk_map(&m->mirror, a.out, a.rows, a.cols, a.pitch, batch, 32, cols, false);
     return ok;
 }
 
@@ -1276,7 +1278,7 @@ int run_ns(NsArgs a, const NsOperand &A, const NsOperand &B, int batch, int sms,
         a.tiles = static_cast<int>(pair_tiles);
         a.group_m = 8;
         const int workers = a.tiles < pairs ? a.tiles : pairs;
-        if (!operands(128) || !ns_epilogue_maps(&maps, a, batch)) return MLPBLK_ECUDA;
+        if (!operands(128) || !ns_epilogue_maps(&maps, a, batch, NsPair::kCols)) return MLPBLK_ECUDA;
         return launch_ns(ns_pair_kernel<OP, AMN, BMN>, NsPair::kThreads, NsPair::kSmemBytes, 2 * workers, 2, mA, mB, maps, a, attr_set, s);
     }
     a.mt = (a.rows + 127) / 128;
