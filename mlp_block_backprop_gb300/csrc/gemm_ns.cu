@@ -1265,12 +1265,12 @@ int run_ns(NsArgs a, const NsOperand &A, const NsOperand &B, int batch, int sms,
     auto operands = [&](uint32_t box) {
         return ns_map(&mA, A.p, AMN, A.rows, A.cols, ortho_pitch(A.cols), batch, box) && ns_map(&mB, B.p, BMN, B.rows, B.cols, ortho_pitch(B.cols), batch, box);
     };
-    // Rounds of tiles, each with its stages of K and the part of its epilogue that nothing hides
-    // (us, measured: 8 x 1024 x 2048, 4096 x 16384): a pair's 256 x 256 tile 0.3 a stage and 3.6, a
-    // CTA's 128 x 128 one 0.22 and 2.2.  (X X^T of 8 x 1024 x 2048: 80 pair tiles on 76 pairs 31 us, 288
-    // small ones 23; X' 40 and 45.)
+    // Rounds of tiles, each with its stages of K and the part of its epilogue that nothing hides (us,
+    // measured): a pair's 256 x 256 tile 0.3 a stage and 2.4, and 4.5 for the clusters' start and last epilogue, a CTA's
+    // 128 x 128 one 0.22 and 2.2.  (X X^T of 8 x 1024 x 2048: 80 pair tiles on 76 pairs 31 us, 288
+    // small ones 23; X' 39 and 45.  16 x 512 x 512: 14 and 12; 3 x 1300 x 1300: 17 and 18, X' 27 and 23.)
     const int64_t pair_rounds = pairs >= 1 ? (pair_tiles + pairs - 1) / pairs : 0, rounds = (tiles + sms - 1) / sms;
-    if (pairs >= 1 && pair_rounds * (0.3 * a.kblocks + 3.6) < rounds * (0.22 * a.kblocks + 2.2)) {
+    if (pairs >= 1 && 4.5 + pair_rounds * (0.3 * a.kblocks + 2.4) < rounds * (0.22 * a.kblocks + 2.2)) {
         static int attr_set[64] = {0};
         a.mt = (a.rows + 255) / 256;
         a.nt = (a.cols + 255) / 256;
@@ -1302,7 +1302,8 @@ int run_ns(NsArgs a, const NsOperand &A, const NsOperand &B, int batch, int sms,
         return launch_ns(ns_small_kernel<NsSmall<true>, OP, AMN, BMN>, NsSmall<true>::kThreads, NsSmall<true>::kSmemBytes, a.tiles * split,
                          split, mA, mB, maps, a, attr_set, s);
     }
-    // Tiles of 64 columns where they fit in one round: half the MMAs and half the epilogue of each.
+    // Tiles of 64 columns where they fit in one round: half the MMAs and half the epilogue of each (five
+    // steps of 512 x 512 65 us, 97 by 128 columns; 250 x 2000 76 and 104).
     const int64_t halves = static_cast<int64_t>(a.mt) * ((a.cols + 63) / 64) * batch;
     if (halves <= sms) {
         using C = NsSmall<false, 64>;
