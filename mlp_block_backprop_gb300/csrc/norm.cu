@@ -591,13 +591,16 @@ norm_dgamma_kernel(const float *__restrict__ part, int parts, int pitch, int wid
 
 // Warps of a row and units of a warp.  Many rows: four units a warp forward, two backward (three arrays, and dgamma's
 // sums), so that with the next row on its way a warp has 64 KB an SM in flight and a row meets in few
-// warps.  Few rows (no more than the SMs): as many warps as there are units.
+// warps.  Few rows (no more than the SMs): as many warps as there are units, backward also for few values
+// (2000 x 777 9.3 us with one unit a warp, 10.6 with two; 4097 x 1001 float32, whose rows take twice the
+// instructions a value, 11.8 and 13.2; 4096 x 2048 20.7 and 19.7).
 struct NormShape {
     int warps, units;
 };
-NormShape norm_shape(int width, int unit, int64_t T, int sms, bool backward) {
+NormShape norm_shape(int width, int unit, bool vec, int64_t T, int sms, bool backward) {
     const int U = (width + unit - 1) / unit;
-    const int each = T <= sms ? 1 : backward ? 2 : 4;
+    const bool few = T <= sms || (backward && T * width <= (vec ? 2 : 8) << 20);
+    const int each = few ? 1 : backward ? 2 : 4;
     NormShape s = {1, 0};
     while (s.warps < kNormMaxWarps && s.warps * each < U) s.warps *= 2;
     s.units = 1;
@@ -608,9 +611,9 @@ NormShape norm_shape(int width, int unit, int64_t T, int sms, bool backward) {
 template <class L, int N>
 int run_norm(NormArgs a, bool backward, int sms, cudaStream_t s, int *parts) {
     // Many rows: CTAs as large as they go (fewer partial rows of dgamma, and the rows of a CTA lie together:
-    // 16384 x 4096 forward 66 us with 512 threads, 72 with 128, backward 77 and 80; 4097 x 1001 float32 backward
-    // 13.3 and 14.2).  Few: 128 (300 x 1000 2.9 us, with 512 3.4), backward 256 (5.5; 128 6.1, 512 5.7).
-    const int least = a.T >= static_cast<int64_t>(sms) * 16 ? 32 * kNormMaxWarps : (backward ? 256 : 128);
+    // 16384 x 4096 forward 66 us with 512 threads, 72 with 128, backward 77 and 80).  Few: 128 (300 x 1000
+    // forward 2.9 us, with 512 3.4; backward 512 there too: 300 x 4096 8.0 us, 8.1 with 128).
+    const int least = backward || a.T >= static_cast<int64_t>(sms) * 16 ? 32 * kNormMaxWarps : 128;
     const int threads = 32 * a.warps > least ? 32 * a.warps : least;
     const int slots = threads / (32 * a.warps);
     const size_t smem = backward ? static_cast<size_t>(slots - 1) * a.warps * N * L::kUnit * 4 : 0;
@@ -639,7 +642,7 @@ int run_norm(NormArgs a, bool backward, int sms, cudaStream_t s, int *parts) {
 
 template <class L>
 int run_norm_lay(NormArgs a, bool backward, int sms, cudaStream_t s, int *parts) {
-    const NormShape sh = norm_shape(a.width, L::kUnit, a.T, sms, backward);
+    const NormShape sh = norm_shape(a.width, L::kUnit, L::VEC, a.T, sms, backward);
     a.warps = sh.warps;
     switch (sh.units) {
         case 1: return run_norm<L, 1>(a, backward, sms, s, parts);
