@@ -72,11 +72,12 @@ struct Lay {
     // The column of a lane's value i in a unit whose first value is at `at` (first_col).
     static __device__ __forceinline__ int first_col(int unit, int lane) { return unit * kUnit + (VEC ? lane * E : lane); }
     static __device__ __forceinline__ int col(int at, int i) { return at + (VEC ? i : 32 * i); }
-    // The lane's part of a unit; 0 behind the row's end.
-    static __device__ __forceinline__ Raw load(const T *row, int at, int width) {
+    // The lane's part of a unit; 0 behind the row's end.  inside: it is known to have none there (the
+    // zeros' selects would be a move for each register and row).
+    static __device__ __forceinline__ Raw load(const T *row, int at, int width, bool inside = false) {
         Raw r;
         if constexpr (VEC) {
-            const uint4 a = at < width ? *reinterpret_cast<const uint4 *>(row + at) : make_uint4(0, 0, 0, 0);
+            const uint4 a = inside || at < width ? *reinterpret_cast<const uint4 *>(row + at) : make_uint4(0, 0, 0, 0);
             r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
         } else {
 #pragma unroll
@@ -311,13 +312,19 @@ add_rmsnorm_kernel(const NormArgs a) {
     for (int u = 0; u < N; ++u) c[u] = L::first_col(w + u * W, lane);
 #pragma unroll
     for (int u = 0; u < N; ++u) g[u] = L::load(static_cast<const T *>(a.gamma), c[u], a.width);
-    auto fetch = [&](int64_t t) {
+    auto fetch_row = [&](int64_t t, auto inside) {
         const int64_t at = t * a.width;
 #pragma unroll
         for (int u = 0; u < N; ++u) {
-            x[u] = L::load(static_cast<const T *>(a.x) + at, c[u], a.width);
-            if (RES) res[u] = L::load(static_cast<const T *>(a.residual) + at, c[u], a.width);
+            x[u] = L::load(static_cast<const T *>(a.x) + at, c[u], a.width, decltype(inside)::value);
+            if (RES) res[u] = L::load(static_cast<const T *>(a.residual) + at, c[u], a.width, decltype(inside)::value);
         }
+    };
+    // (two copies of the loads, not of the loop)
+    const bool whole = L::VEC && W * N * L::kUnit == a.width;
+    auto fetch = [&](int64_t t) {
+        if (whole) fetch_row(t, std::true_type{});
+        else fetch_row(t, std::false_type{});
     };
     int phase = 0;
     const int64_t step = static_cast<int64_t>(gridDim.x) * slots;
