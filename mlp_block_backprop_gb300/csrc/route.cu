@@ -812,8 +812,10 @@ route_bwd_kernel(const RouteArgs a) {
         out[4] = o1.x; out[5] = o1.y; out[6] = o1.z; out[7] = o1.w;
         if (softmax && n < tokens) {
             // s (ds - sum_j ds_j s_j): the first part stands in `out`
-            const float mean = a.renorm ? a.scale * w.dot[n] * (kRouteTiny / w.total[n]) : a.scale * w.dot[n];
-            if (mean != 0.0f) {
+            const float part = a.renorm ? kRouteTiny / w.total[n] : 1.0f, mean = a.scale * w.dot[n] * part;
+            // (renormalised it is mostly far below the roundings of dw - dot, and left out: 65536 tokens of
+            // 256 experts 34 us with it, 26 without; a NaN is not)
+            if (mean != 0.0f && !(part < 0x1p-60f && fabsf(mean) < INFINITY)) {
                 const float m = w.m[n], z = w.z[n];
                 float l[kRouteV];
                 load_logits(rows + (t0 + n) * a.E, e0, a.E, vec, l);
