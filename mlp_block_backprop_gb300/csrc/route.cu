@@ -28,10 +28,8 @@
 // the same logit with the same bias, the token is selected again in
 // float64.  So ids do not depend on how exp rounds.
 //
-// Bound by instruction issue and its latencies, not by HBM: 65536 tokens of 256 experts (33 MB of bf16
-// logits, 5 us of HBM; sigmoid, 8 groups, top-8) take 62 us, the gradient 20.  Two tokens a
-// warp there: one 86 us in all with the gradient's 20, two 74, four 80 (a warp's shared memory is then
-// twice as large).
+// Bound by instruction issue and its latencies (790 instructions a token), not by HBM: 65536 tokens of 256 experts
+// (33 MB of bf16 logits, 5 us of HBM; sigmoid, 8 groups, top-8) take 63 us, the gradient 15.
 #include <cuda_bf16.h>
 #include <float.h>
 
@@ -239,22 +237,29 @@ __device__ __noinline__ void route_exactly(const RouteArgs &a, const T *row, boo
     }
     m = lanes_max<32>(m);
     if (!(m > -INFINITY)) m = 0.0f;
-    double z = 0.0;
+    double inv_z = 0.0;
     if (!a.sigmoid) {
+        double z = 0.0;
 #pragma unroll 1
         for (int i = 0; i < chunks; ++i) {
             const int e = 32 * i + lane;
-            if (e < a.E) z += exact_exp(static_cast<double>(logit_of(to_float(row[e]))) - m);
+            if (e >= a.E) continue;
+            const double x = exact_exp(static_cast<double>(logit_of(to_float(row[e]))) - m);
+            z += x;
+            key[e] = __double_as_longlong(x);    // by expert, until the candidates' keys take the place
         }
-        z = lanes_sum<32>(z);
+        inv_z = 1.0 / lanes_sum<32>(z);
     }
     __syncwarp();
 #pragma unroll 1
-    for (int c = lane; c < n; c += 32) {
-        const int e = list[c];
-        key[c] = ordered(exact_key(a.sigmoid, to_float(row[e]), a.bias ? a.bias[e] : 0.0f, m, z));
+    for (int c0 = 0; c0 < n; c0 += 32) {
+        const int c = c0 + lane, e = c < n ? list[c] : 0;
+        const float bias = a.bias ? a.bias[e] : 0.0f;
+        const double x = a.sigmoid ? exact_key(true, to_float(row[e]), bias, 0.0f, 0.0) : __longlong_as_double(key[e]) * inv_z + bias;
+        __syncwarp();                            // (a candidate's place is not behind its expert's)
+        if (c < n) key[c] = ordered(x);
+        __syncwarp();
     }
-    __syncwarp();
     if (regroup) {
         // two best a group, in its run of the list; then the marks' order
         double *mark = w.exact.mark;
@@ -286,7 +291,22 @@ __device__ __noinline__ void route_exactly(const RouteArgs &a, const T *row, boo
         }
         __syncwarp();
     }
-    // rounds of the best; the list's order is the experts'
+    // the list's order is the experts'
+    if (n <= 32) {                               // a lane a candidate: each counts those before it
+        const int64_t mine = lane < n ? key[lane] : INT64_MIN;
+        int rank = 0;
+#pragma unroll 1
+        for (int c = 0; c < n; ++c) {
+            const int64_t y = __shfl_sync(all, mine, c);
+            rank += y > mine || (y == mine && c < lane);
+        }
+        const int live = __popc(__ballot_sync(all, mine > INT64_MIN));
+        if (mine > INT64_MIN && rank < a.k) won[rank] = list[lane];
+        if (lane >= live && lane < a.k) won[lane] = -1;
+        __syncwarp();
+        return;
+    }
+    // rounds of the best
 #pragma unroll 1
     for (int r = 0; r < a.k; ++r) {
         int64_t top = INT64_MIN;
@@ -609,18 +629,26 @@ route_kernel(const RouteArgs a) {
             if (__any_sync(all, any)) {
                 __syncwarp();
                 unsigned cut = 0;                   // tokens whose cut goes through experts of the same numbers
-                for (int i = lane; i < N * a.k; i += 32) {
-                    const int n = over(i, a.by_k), r = i - n * a.k;
-                    const int state = w.lane[n][r];
-                    if (state == kSame && r + 1 == a.k) cut |= 1u << n;
-                    if (state != kNear) continue;
-                    if (!a.sigmoid || r + 1 == a.k || (r > 0 && w.lane[n][r - 1] != kApart) || w.lane[n][r + 1] != kApart) {
-                        again |= 1u << n;           // more than two, or what was not selected
-                        continue;
-                    }
+                for (int i0 = 0; i0 < N * a.k; i0 += 32) {
+                    const int i = min(i0 + lane, N * a.k - 1), n = over(i, a.by_k), r = i - n * a.k;
+                    const bool end = r + 1 == a.k;
+                    const int state = i == i0 + lane ? w.lane[n][r] : kApart;
+                    if (state == kSame && end) cut |= 1u << n;
+                    // a pair by itself is settled here, its second key by the next lane
+                    const bool alone = a.sigmoid && !end && (r == 0 || w.lane[n][r - 1] == kApart) && w.lane[n][min(r + 1, a.k - 1)] == kApart;
+                    const bool pair = state == kNear && alone;
+                    if (state == kNear && !alone) again |= 1u << n;   // more than two, or what was not selected
+                    const unsigned pairs = __ballot_sync(all, pair);
+                    if (pairs == 0) continue;
                     const T *row = rows + (t0 + n) * a.E;
-                    const int e = w.won[n][r], f = w.won[n][r + 1];
-                    const double x = exact_key(true, to_float(row[e]), a.bias[e], 0.0f, 0.0), y = exact_key(true, to_float(row[f]), a.bias[f], 0.0f, 0.0);
+                    auto key_of = [&](int e) { return exact_key(true, to_float(row[e]), a.bias[e], 0.0f, 0.0); };
+                    const int e = w.won[n][r];
+                    double x = 0.0;
+                    if (pair || (pairs << 1 >> lane & 1u)) x = key_of(e);
+                    double y = __shfl_down_sync(all, x, 1);
+                    if (!pair) continue;
+                    const int f = w.won[n][r + 1];
+                    if (lane == 31) y = key_of(f);
                     if (y > x || (y == x && f < e)) {
                         w.won[n][r] = f;
                         w.won[n][r + 1] = e;
@@ -830,11 +858,12 @@ route_bwd_kernel(const RouteArgs a) {
 
 // Tokens a warp: as many as its lanes hold side by side, more where that still leaves the SMs full
 // of warps (the winners' part then fills the lanes; with few tokens it costs parallelism: 8 tokens
-// of 256 experts 3.6 us, and 8.3 with four a warp).
+// of 256 experts 3.6 us, and 8.3 with four a warp), and two steps of those where a step has one token or
+// two (65536 of 256 experts 63 us, one step 74, four 66; of 128 19.8, 23.5 and 23.6; of 60 20.3, two steps 24.4).
 template <class T, int L>
 int run_route(const RouteArgs &a, bool backward, int sms, cudaStream_t s) {
     constexpr int kSide = 32 / L, kWarps = kRouteThreads / 32;
-    constexpr int kMany = kSide < 2 ? 2 : kSide, kManyBack = kSide < 8 ? 8 : kSide;
+    constexpr int kMany = kSide <= 2 ? 2 * kSide : kSide, kManyBack = kSide < 8 ? 8 : kSide;
     const bool many = a.T >= static_cast<int64_t>(sms) * 64 * kSide;
     const int n = kWarps * (many ? (backward ? kManyBack : kMany) : kSide);   // tokens of a CTA
     const dim3 grid(static_cast<unsigned>((a.T + n - 1) / n)), block(kRouteThreads);
