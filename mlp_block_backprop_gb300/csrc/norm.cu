@@ -282,6 +282,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) { return e4m3x2(a, b) | e4m3x2(c, d) << 16; }
+
 constexpr int kNormMaxWarps = 16;      // of a row
 
 // Threads of row slot `slot` meet (its warps alone).
@@ -423,35 +425,28 @@ add_rmsnorm_kernel(const NormArgs a) {
                     const int b = unit * (L::kUnit / 128) + lane / L::kBlockLanes;
                     if (lane % L::kBlockLanes == 0 && b * 128 < a.width) a.scales[t * ((a.width + 127) / 128) + b] = scale;
                 }
-                float gv[E], q[E];
+                float gv[E];
                 if (!kExact) L::unpack(g[u], gv);
-                // a border between two codes has its last 20 bits as 0x80000 (below 2^-6, E4M3's
-                // smallest normal, borders lie elsewhere): anything within two steps of one, or small, is near
-                // (four values share a look: 16384 x 4096 83 us; one 97, two 87, eight 89)
-                constexpr int kTogether = 4;
-                const bool odd = up != 1.0f || ch != ch;
-#pragma unroll
-                for (int j = 0; j < E; j += kTogether) {
-                    uint32_t near = 0xFFFFFFFFu;
-                    float least = INFINITY;
-#pragma unroll
-                    for (int i = j; i < j + kTogether; ++i) {
-                        const float p = kExact ? v[u][i] : __fmul_rn(v[u][i], gv[i]);
-                        q[i] = __fmul_rn(p, ch);
-                        near = min(near, (__float_as_uint(q[i]) - 0x7FFFEu) & 0xFFFFFu);
-                        least = fminf(least, fabsf(q[i]));
-                    }
-                    if (near <= 4u || !(least >= 0x1p-6f) || odd) {
-#pragma unroll
-                        for (int i = j; i < j + kTogether; ++i) {
-                            const float p = kExact ? v[u][i] : __fmul_rn(v[u][i], gv[i]);
-                            q[i] = scaled_odd(p * up, kExact ? 0.0f : __fmaf_rn(v[u][i], gv[i], -p) * up, ch, cl);
-                        }
-                    }
-                }
+                // the codes at both ends of what a float32 quotient may be off: where they are the same, so is
+                // the exact one's (four values share a look)
+                constexpr float kOff = kExact ? 0x1p-22f : 0x1p-21f;
+                const float c_low = __fmul_rn(ch, 1.0f - kOff), c_high = __fmul_rn(ch, 1.0f + kOff);
                 uint32_t codes[E / 4];
 #pragma unroll
-                for (int j = 0; j < E / 4; ++j) codes[j] = e4m3x2(q[4 * j], q[4 * j + 1]) | e4m3x2(q[4 * j + 2], q[4 * j + 3]) << 16;
+                for (int j = 0; j < E / 4; ++j) {
+                    float p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[i] = kExact ? v[u][4 * j + i] : __fmul_rn(v[u][4 * j + i], gv[4 * j + i]);
+                    const uint32_t low = e4m3x4(p[0] * c_low, p[1] * c_low, p[2] * c_low, p[3] * c_low);
+                    codes[j] = e4m3x4(p[0] * c_high, p[1] * c_high, p[2] * c_high, p[3] * c_high);
+                    if (codes[j] != low || up != 1.0f) {
+                        float q[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            q[i] = scaled_odd(p[i] * up, kExact ? 0.0f : __fmaf_rn(v[u][4 * j + i], gv[4 * j + i], -p[i]) * up, ch, cl);
+                        codes[j] = e4m3x4(q[0], q[1], q[2], q[3]);
+                    }
+                }
                 L::store_codes(a.codes + at, c[u], a.width, codes);
             }
         }
