@@ -11,14 +11,15 @@
 //   g = dn gamma,  xh = s r:   dx = d_sum + r (g - xh mean(g xh)),   dgamma = sum_t dn xh
 //
 // One pass: a row stays in registers between its sums and its outputs, and the next row is
-// already on its way.  max |s gamma| needs no r, so both reductions of a row are one.  Forward bound by instruction
-// issue (34 an element; 16384 x 4096 bf16 with a residual branch 81 us, 5.8 TB/s of 7 bytes an element),
-// backward by HBM (88 us, 6.1 TB/s of 8).
+// already on its way.  max |s gamma| needs no r, so both reductions of a row are one.  Forward bound by HBM
+// where there is a residual branch (16384 x 4096 bf16 74 us, 6.4 TB/s of 7 bytes an element) and by instruction
+// issue without one (60 us), backward by HBM (90 us, 6.0 TB/s of 8 bytes).
+//
 // Codes are those of the real number n / scale, rounded once: values half way between two codes
 // are common (one in 1700 here: ratios of two short products), and which way they go is decided
 // by the 25th bit of the scale.  So s gamma is exact (bf16), the sum of squares, r and r / scale are carried as sums
-// of two floats (relative error below 2^-40), and where a float32 quotient comes within two
-// steps of a border the product is taken to 48 bits and rounded to odd before it is rounded
+// of two floats (relative error below 2^-40), and where a float32 quotient's error may reach a
+// border of two codes the product is taken to 48 bits and rounded to odd before it is rounded
 // to E4M3.
 #include <cuda_bf16.h>
 #include <math.h>
@@ -286,6 +287,15 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 
 constexpr int kNormMaxWarps = 16;      // of a row
 
+// The lowest log2(N) bits of i in the opposite order.
+template <int N>
+__device__ __forceinline__ int reversed(int i) {
+    int r = 0;
+#pragma unroll
+    for (int b = 1; b < N; b <<= 1) r = r << 1 | (i & b ? 1 : 0);
+    return r;
+}
+
 // Threads of row slot `slot` meet (its warps alone).
 __device__ __forceinline__ void row_barrier(int slot, int warps) {
     if (warps == 1) __syncwarp();
@@ -406,31 +416,51 @@ add_rmsnorm_kernel(const NormArgs a) {
             }
         }
         if (a.codes) {
-            float ch, cl, up;
+            float ch, cl, up;                 // by blocks: of the block whose scale the lane has found
+            constexpr int kGroup = L::kBlockLanes;
             if (!a.block) {
                 const float scale = scale_of(top, rh, rl, ch, cl, up);
                 if (w == 0 && lane == 0) a.scales[t] = scale;
+            } else {
+                // Each exchange halves the units that a lane goes on with, so that the lanes of a block end with
+                // one unit's maximum each, and find its scale (8192 x 8192: 94 us with every lane finding all).
+                Peak mine[N];
+#pragma unroll
+                for (int u = 0; u < N; ++u) mine[u] = peak[u];
+#pragma unroll
+                for (int o = 1, half = N / 2; o < kGroup; o <<= 1, half /= 2) {
+                    const bool upper = lane & o;
+#pragma unroll
+                    for (int u = 0; u < (half > 0 ? half : 1); ++u) {
+                        const Peak give = half > 0 && !upper ? mine[u + half] : mine[u];
+                        if (half > 0 && upper) mine[u] = mine[u + half];
+                        const float h = __shfl_xor_sync(0xffffffffu, give.hi, o);
+                        if (kExact) mine[u].hi = fmaxf(mine[u].hi, h);
+                        else mine[u].take(h, __shfl_xor_sync(0xffffffffu, give.lo, o));
+                    }
+                }
+                const float scale = scale_of(mine[0], rh, rl, ch, cl, up);
+                const int b = (w + reversed<N>(lane) * W) * (L::kUnit / 128) + lane / kGroup;
+                if (lane % kGroup < N && b * 128 < a.width) a.scales[t * ((a.width + 127) / 128) + b] = scale;
             }
+            const bool far = __any_sync(0xffffffffu, up != 1.0f);
 #pragma unroll
             for (int u = 0; u < N; ++u) {
                 const int unit = w + u * W;
                 if (unit * L::kUnit >= a.width) continue;
+                float cu = ch, cul = cl, uu = up;
                 if (a.block) {
-#pragma unroll
-                    for (int o = 1; o < L::kBlockLanes; o <<= 1) {
-                        if (kExact) peak[u].hi = fmaxf(peak[u].hi, __shfl_xor_sync(0xffffffffu, peak[u].hi, o));
-                        else peak[u].take(__shfl_xor_sync(0xffffffffu, peak[u].hi, o), __shfl_xor_sync(0xffffffffu, peak[u].lo, o));
-                    }
-                    const float scale = scale_of(peak[u], rh, rl, ch, cl, up);
-                    const int b = unit * (L::kUnit / 128) + lane / L::kBlockLanes;
-                    if (lane % L::kBlockLanes == 0 && b * 128 < a.width) a.scales[t * ((a.width + 127) / 128) + b] = scale;
+                    const int from = (lane & -kGroup) | reversed<N>(u);
+                    cu = __shfl_sync(0xffffffffu, ch, from);
+                    cul = __shfl_sync(0xffffffffu, cl, from);
+                    if (far) uu = __shfl_sync(0xffffffffu, up, from);
                 }
                 float gv[E];
                 if (!kExact) L::unpack(g[u], gv);
                 // the codes at both ends of what a float32 quotient may be off: where they are the same, so is
                 // the exact one's (four values share a look)
                 constexpr float kOff = kExact ? 0x1p-22f : 0x1p-21f;
-                const float c_low = __fmul_rn(ch, 1.0f - kOff), c_high = __fmul_rn(ch, 1.0f + kOff);
+                const float c_low = __fmul_rn(cu, 1.0f - kOff), c_high = __fmul_rn(cu, 1.0f + kOff);
                 uint32_t codes[E / 4];
 #pragma unroll
                 for (int j = 0; j < E / 4; ++j) {
@@ -439,11 +469,11 @@ add_rmsnorm_kernel(const NormArgs a) {
                     for (int i = 0; i < 4; ++i) p[i] = kExact ? v[u][4 * j + i] : __fmul_rn(v[u][4 * j + i], gv[4 * j + i]);
                     const uint32_t low = e4m3x4(p[0] * c_low, p[1] * c_low, p[2] * c_low, p[3] * c_low);
                     codes[j] = e4m3x4(p[0] * c_high, p[1] * c_high, p[2] * c_high, p[3] * c_high);
-                    if (codes[j] != low || up != 1.0f) {
+                    if (codes[j] != low || far) {
                         float q[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            q[i] = scaled_odd(p[i] * up, kExact ? 0.0f : __fmaf_rn(v[u][4 * j + i], gv[4 * j + i], -p[i]) * up, ch, cl);
+                            q[i] = scaled_odd(p[i] * uu, kExact ? 0.0f : __fmaf_rn(v[u][4 * j + i], gv[4 * j + i], -p[i]) * uu, cu, cul);
                         codes[j] = e4m3x4(q[0], q[1], q[2], q[3]);
                     }
                 }
