@@ -479,13 +479,14 @@ route_kernel(const RouteArgs a) {
                     join_two(first, second, x, y);
                 }
                 float mark = mark_of(first, second);
-                const int group = sub & -span;      // the group's first lane
+                // (the best mark's lowest group: no lane before the group's first has it)
+                const unsigned before = mine & ((1u << (lane0 + (sub & -span))) - 1u);
                 last = INFINITY;
                 for (int r = 0; r < a.top_groups; ++r) {
                     const float best = lanes_max<L>(mark);
-                    const int owner = __ffs(__ballot_sync(all, mark == best) & mine) - 1 - lane0;
+                    const unsigned votes = __ballot_sync(all, mark == best);
                     last = best;
-                    if ((owner & -span) == group) {
+                    if (mark == best && (votes & before) == 0) {
                         // (a group without an open expert may be kept too: it has nothing to select)
                         kept = 0xFFu;
                         mark = -INFINITY;
@@ -566,6 +567,7 @@ route_kernel(const RouteArgs a) {
     // The steps' rounds side by side: each waits for its maximum, not for the others'.
     const float *queue[kSteps];
     float head[kSteps];                             // the best of the lane's keys that are left
+    const unsigned before = mine & ((1u << lane) - 1u);
 #pragma unroll
     for (int step = 0; step < kSteps; ++step) {
         queue[step] = w.queue[step][lane];
@@ -577,10 +579,10 @@ route_kernel(const RouteArgs a) {
         for (int step = 0; step < kSteps; ++step) best[step] = lanes_max<L>(head[step]);
 #pragma unroll
         for (int step = 0; step < kSteps; ++step) {
-            const int owner = __ffs(__ballot_sync(all, head[step] == best[step]) & mine) - 1 - lane0;
-            if (sub == owner) {
+            const unsigned votes = __ballot_sync(all, head[step] == best[step]);
+            if (head[step] == best[step] && (votes & before) == 0) {   // the lowest lane that has it
                 w.top[step * kSide + seat][r] = best[step];
-                w.lane[step * kSide + seat][r] = owner;
+                w.lane[step * kSide + seat][r] = sub;
                 if (best[step] > -INFINITY) head[step] = *++queue[step];
             }
         }
