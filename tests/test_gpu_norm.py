@@ -263,3 +263,28 @@ def test_no_tokens(mb):
     assert bool((dg == 3).all())
     op.backward(e, e, gamma, e, dg, overwrite=True)
     assert not dg.any()
+
+
+@pytest.mark.parametrize("block", [0, 128])
+def test_offsets_beyond_32_bits(mb, block):
+    """2^32 values and more: the last rows against the oracle, and their gradient."""
+    import torch
+    T, d, last = (1 << 20) + 37, 4104, 6
+    x = torch.empty(T, d, dtype=torch.bfloat16, device="cuda").normal_()
+    gamma = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    per = (d + 127) // 128 if block else 1
+    codes, scales = torch.zeros(T, d, dtype=torch.uint8, device="cuda"), torch.zeros(T, per, device="cuda")
+    op = mb.AddRmsNorm(T, d, 1e-6, "bf16", block)
+    op.forward(x, gamma, codes, scales)
+    dx, dg = torch.zeros_like(x), torch.zeros(d, device="cuda")
+    op.backward(x, x, gamma, dx, dg, overwrite=True)
+    n = T - last
+    X = to_np(x[n:])
+    _, ref_codes, ref_scales, r = norm.forward(X, np.ones(d), 1e-6, block)
+    np.testing.assert_array_equal(to_np(scales[n:]).reshape(last, -1), ref_scales.astype(np.float64))
+    np.testing.assert_array_equal(to_np(codes[n:].view(torch.float8_e4m3fn)), ref_codes)
+    ref, _ = norm.backward(X, X, np.ones(d), r)
+    # dx = r x (1 - r^2 mean x^2) cancels to next to nothing: (d + 12) roundings of r x
+    assert np.all(np.abs(to_np(dx[n:]) - ref) <= 2.0 ** -8 * np.abs(ref) + (d + 12) * U * np.abs(X) * r[:, None])
+    # dgamma_k = sum_t x^2 r: T terms near 1, each CTA's share in order, then a tree
+    assert bool(((dg / T - 1).abs() < 0.01).all())

@@ -234,3 +234,15 @@ def test_capture_and_replay(mb):
     g.replay()
     torch.cuda.synchronize()
     assert _rel(o, _exact(u)) <= NS + HALF
+
+
+def test_offsets_beyond_32_bits(mb):
+    """A batch of more than 2^32 elements: its first and last matrices."""
+    import torch
+    b, r, c = 70, 8192, 7500
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    u = torch.empty(b, r, c, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    o = torch.zeros(b, r, c, dtype=torch.bfloat16, device="cuda")
+    mb.Orthogonalizer(r, c, batch=b, steps=2, dtype="bf16").orthogonalize(u, o)
+    for i in (0, b - 1):
+        assert _rel(o[i], _exact(u[i], (muon.COEFFICIENTS,) * 2)) <= NS + HALF

@@ -226,3 +226,25 @@ def test_capture_on_another_stream_and_replay(mb):
     ref_ids, ref_w = route.route(l, k, "sigmoid")
     np.testing.assert_array_equal(ids.cpu().numpy(), ref_ids)
     np.testing.assert_allclose(to_np(w), ref_w, rtol=_tol(l, E, k))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_offsets_beyond_32_bits(mb, score):
+    """2^32 logits and more: the last tokens as a batch of their own."""
+    import torch
+    E, k = 256, 4
+    T, last = (1 << 24) + 77, 100
+    l = torch.empty(T, E, dtype=torch.bfloat16, device="cuda").normal_()
+    bias = torch.randn(E, device="cuda") * 0.1
+    ids, w = torch.full((T, k), 77, dtype=torch.int32, device="cuda"), torch.full((T, k), 77.0, device="cuda")
+    mb.MoeRouter(T, E, k, score).route(l, ids, w, bias=bias)
+    dw, dl = torch.randn(T, k, device="cuda"), torch.full((T, E), 77.0, dtype=torch.bfloat16, device="cuda")
+    mb.MoeRouter(T, E, k, score, renorm=False).route_backward(l, ids, dw, dl)
+    n = T - last
+    tail = l[n:].clone()
+    ids2, w2, dl2 = torch.empty_like(ids[n:]), torch.empty_like(w[n:]), torch.empty_like(tail)
+    mb.MoeRouter(last, E, k, score).route(tail, ids2, w2, bias=bias)
+    mb.MoeRouter(last, E, k, score, renorm=False).route_backward(tail, ids2, dw[n:].clone(), dl2)
+    assert torch.equal(ids[n:], ids2) and torch.equal(w[n:], w2) and torch.equal(dl[n:], dl2)
+    ref_ids, _ = route.route(to_np(tail), k, score, to_np(bias))
+    np.testing.assert_array_equal(ids2.cpu().numpy(), ref_ids)
