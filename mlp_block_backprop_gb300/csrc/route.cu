@@ -29,7 +29,7 @@
 // float64.  So ids do not depend on how exp rounds.
 //
 // Bound by instruction issue and its latencies (790 instructions a token), not by HBM: 65536 tokens of 256 experts
-// (33 MB of bf16 logits, 5 us of HBM; sigmoid, 8 groups, top-8) take 60 us, the gradient 15.
+// (33 MB of bf16 logits, 5 us of HBM; sigmoid, 8 groups, top-8) take 60 us, the gradient 14.
 #include <cuda_bf16.h>
 #include <float.h>
 
@@ -861,11 +861,12 @@ route_bwd_kernel(const RouteArgs a) {
 // Tokens a warp: as many as its lanes hold side by side, more where that still leaves the SMs full
 // of warps (the winners' part then fills the lanes; with few tokens it costs parallelism: 8 tokens
 // of 256 experts 3.6 us, and 8.3 with four a warp), and two steps of those where a step has one token or
-// two (65536 of 256 experts 63 us, one step 74, four 66; of 128 19.8, 23.5 and 23.6; of 60 20.3, two steps 24.4).
+// two (65536 of 256 experts 63 us, one step 74, four 66; of 128 19.8, 23.5 and 23.6; of 60 20.3, two steps 24.4;
+// the gradient, at least four tokens a warp: 20000 tokens of 256 experts 6.1 us, two 6.6, eight 9.8; 65536 14.3, 17.6, 15.2).
 template <class T, int L>
 int run_route(const RouteArgs &a, bool backward, int sms, cudaStream_t s) {
     constexpr int kSide = 32 / L, kWarps = kRouteThreads / 32;
-    constexpr int kMany = kSide <= 2 ? 2 * kSide : kSide, kManyBack = kSide < 8 ? 8 : kSide;
+    constexpr int kMany = kSide <= 2 ? 2 * kSide : kSide, kManyBack = kSide < 4 ? 4 : kSide;
     const bool many = a.T >= static_cast<int64_t>(sms) * 64 * kSide;
     const int n = kWarps * (many ? (backward ? kManyBack : kMany) : kSide);   // tokens of a CTA
     const dim3 grid(static_cast<unsigned>((a.T + n - 1) / n)), block(kRouteThreads);
