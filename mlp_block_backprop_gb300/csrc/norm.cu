@@ -47,6 +47,7 @@ struct NormArgs {
     void *dx;
     float *part;
     int pitch;             // floats of a partial row
+    bool ask;              // rows are asked into L2 ahead of their loads
 };
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -546,6 +547,16 @@ add_rmsnorm_bwd_kernel(const NormArgs a) {
             for (int i = 0; i < E; ++i) dot += d[i] * gv[i] * s[i];
         }
         if (kAhead && t + step < a.T) fetch(t + step);
+        // The row after next is asked into L2 by three of its warps, an array each: what a warp has in flight
+        // in its registers is one row (16384 x 4096 bf16 92 -> 86 us, 8192 x 768, which L2 holds, 15.2 -> 16.2;
+        // with the warp's pointer kept over the loop the registers spill and nothing is won).
+        if (L::VEC && a.ask && w < 3 && lane == 0 && t + 2 * step < a.T) {
+            const void *src = w == 0 ? a.x : w == 1 ? a.dn : a.d_sum;
+            if (src)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const T *>(src) + (t + 2 * step) * a.width),
+                             "r"(a.width * static_cast<int>(sizeof(T)))
+                             : "memory");
+        }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
         if (W > 1) {
@@ -726,6 +737,7 @@ int launch_add_rmsnorm_bwd(const mlpblk_norm_desc &d, const void *dn, const void
     a.pitch = static_cast<int>(norm_part_pitch(d.width));
     a.T = d.tokens;
     a.width = static_cast<int>(d.width);
+    a.ask = d.tokens * d.width * (d.dtype == MLPBLK_BF16 ? 2 : 4) >= 24 << 20;   // two or three such arrays: more than half of L2
     return run_norm_type(a, d.dtype, true, sms, s, parts);
 }
 
