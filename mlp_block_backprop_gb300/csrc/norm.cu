@@ -13,7 +13,7 @@
 // One pass: a row stays in registers between its sums and its outputs, and the next row is
 // already on its way.  max |s gamma| needs no r, so both reductions of a row are one.  Forward bound by HBM
 // where there is a residual branch (16384 x 4096 bf16 74 us, 6.4 TB/s of 7 bytes an element) and by instruction
-// issue without one (60 us), backward by HBM (90 us, 6.0 TB/s of 8 bytes).
+// issue without one (60 us), backward by HBM (86 us, 6.2 TB/s of 8 bytes).
 //
 // Codes are those of the real number n / scale, rounded once: values half way between two codes
 // are common (one in 1700 here: ratios of two short products), and which way they go is decided
