@@ -1287,12 +1287,13 @@ int run_ns(NsArgs a, const NsOperand &A, const NsOperand &B, int batch, int sms,
     const int64_t every = static_cast<int64_t>(a.mt) * a.nt * batch;   // a split computes the images too
     // K is split where that saves more than the cluster's sum costs: a stage takes 0.155 us with
     // few CTAs at work, the sum some 5.5 and 0.3 a part (X X^T of 256 x 8192: 27.2 us whole, 22.4, 17.9 and 18.0
-    // in two, four and eight; of 512 x 2048: 13.0, 14.3, 14.3, 25.6).
+    // in two, four and eight; of 512 x 2048: 13.0, 14.3, 14.3, 25.6).  Clusters of eight find room on some two thirds
+    // of the SMs at once (500 x 16000, sixteen tiles: 31 us in eight, 19.5 in four).
     int split = 1;
     double best = 0.155 * a.kblocks;
     for (int k = 2; k <= 8; k *= 2) {
         const double cost = 0.155 * a.kblocks / k + 5.5 + 0.3 * k;
-        if (every * k <= sms && a.kblocks >= 2 * k && cost < best) best = cost, split = k;
+        if (every * k <= (k == 8 ? sms * 2 / 3 : sms * 5 / 6) && a.kblocks >= 2 * k && cost < best) best = cost, split = k;
     }
     if (split > 1) {
         a.per = a.mt * a.nt;
