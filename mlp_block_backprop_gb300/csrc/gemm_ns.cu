@@ -5,7 +5,7 @@
 //   P  = b G + c G G
 //   X' = a X + P X        or  a X + X P
 //
-// and, where X's long side is at least twice the short one, two steps at a time with one product
+// and, where X's long side is at least twice the short one (of 512 or more), two steps at a time with one product
 // on X for both: with the first step's P1, G becomes (a1 I + P1) G (a1 I + P1), its own P2 follows, and
 // X' = (a2 I + P2)(a1 I + P1) X = a1 a2 X + S X.  That trades a G and an update (3 m^2 n) for three
 // more products of the short side (m^3 each, half of them mirrored): 16384 x 4096 takes 28% fewer
@@ -26,10 +26,12 @@
 //   - P's diagonal, next to which its other entries are small, leaves what its rounding took
 //     in float32 (`diag`), and the update adds it to a.
 //
-// ns_small: one CTA, 128 x 128 tiles; K can be split over a cluster whose parts meet in
-//   distributed shared memory in rank order.
+// ns_small: one CTA, 128 x 128 tiles, or 128 x 64 where those fit one round of the SMs; K can be split over a
+//   cluster whose parts meet in distributed shared memory in rank order.
 // ns_pair: two CTAs on two SMs, 256 x 256 tiles (cta_group::2).
-// Bound by the tensor cores at large sizes, by launches and K's latency at small ones.
+// ns_fused: all steps of a small matrix in one launch of a cluster.
+// Bound by the tensor cores at large sizes (16384 x 4096: 508 of 512 clocks a stage of K), by the copies from L2 where
+// tiles are small, by launches and K's latency at the smallest.
 #include <type_traits>
 
 #include "gemm_tc.cuh"
