@@ -667,8 +667,10 @@ int mlpblk_moe_route_backward(const mlpblk_route_desc *desc, const void *logits,
  * codes and scales are given together; n, codes and rstd may be NULL, n and codes not both.
  * The codes are those of the real number n / scale, rounded once (where the products
  * sum * gamma are in float32's normal range: smaller ones are rounded to it, one beyond it makes its scale
- * and that scale's codes NaN).  A row that holds an infinity, a NaN or a magnitude of 2^60 or more
- * has a NaN rstd and NaN scales and codes; squares below float32's range count as zero.
+ * and that scale's codes NaN).  A row that holds an infinity or a NaN, or whose squares' sum leaves float32's range,
+ * has a NaN rstd and NaN scales and codes: no row of magnitudes below 2^56, possibly one with a
+ * larger magnitude, certainly one with 2^63 or more.  Squares below 2^-149 count as zero, and below 2^-126 they
+ * keep as many bits as float32 has there.
  *
  * mlpblk_add_rmsnorm_backward: with dn the gradient of n (as the codes stand for it:
  *   rounding passes it on) and d_sum that of sum (NULL: none),
