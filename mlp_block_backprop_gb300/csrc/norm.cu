@@ -554,7 +554,7 @@ add_rmsnorm_bwd_kernel(const NormArgs a) {
             L::unpack(d0[u], d);
             L::unpack(g[u], gv);
 #pragma unroll
-            for (int i = 0; i < E; ++i) dot += d[i] * gv[i] * s[i];
+            for (int i = 0; i < E; ++i) dot += d[i] * gv[i] * (s[i] * r);   // (g xh: rstd's powers alone leave float32's range)
         }
         if (kAhead && t + step < a.T) fetch(t + step);
         // The row after next is asked into L2 by three of its warps, an array each: what a warp has in flight
@@ -577,7 +577,7 @@ add_rmsnorm_bwd_kernel(const NormArgs a) {
             dot = m[lane % W];
             for (int o = 1; o < W; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
         }
-        const float k = r * r * r * (dot * inv_width);
+        const float mean = dot * inv_width;
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             float s[E], d[E], y[E], gv[E], v[E];
@@ -591,8 +591,9 @@ add_rmsnorm_bwd_kernel(const NormArgs a) {
             L::unpack(g[u], gv);
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                v[i] = r * (d[i] * gv[i]) - s[i] * k + y[i];
-                acc[u][i] += d[i] * (s[i] * r);
+                const float xh = s[i] * r;
+                v[i] = r * (d[i] * gv[i] - xh * mean) + y[i];
+                acc[u][i] += d[i] * xh;
             }
             L::store(static_cast<T *>(a.dx) + at, c[u], a.width, L::pack(v));
         }

@@ -30,6 +30,35 @@ def _t(a, dtype):
     return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).cuda().to(torch.bfloat16 if dtype == "bf16" else torch.float32)
 
 
+@pytest.mark.parametrize("eps", [1e-6, 0.0])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("width", [40, 1001, 1024, 4096, 16384])
+def test_gradients_of_large_and_small_rows(mb, width, dtype, eps):
+    """rstd from 1e-17 to 1e18: its cube leaves float32's range, the gradient does not."""
+    import torch
+    size = [1e12, 1e14, 1e15, 1e16, 1e17, 1.0] + ([1e-3] if eps else [1e-10, 1e-13, 1e-15, 1e-18])
+    T = len(size)
+    rng = np.random.default_rng(width)
+    # (magnitudes of at most 1.7 times the row's size: the sum of their squares stays in range)
+    s = _t(rng.uniform(-1.7, 1.7, (T, width)) * np.array(size)[:, None], dtype)
+    dn, gamma = _t(rng.normal(0, 1, (T, width)), dtype), _t(1 + rng.normal(0, 0.2, width), dtype)
+    op = mb.AddRmsNorm(T, width, eps, dtype)
+    op.forward(s, gamma, n=torch.empty_like(s))
+    S, N, G = to_np(s), to_np(dn), to_np(gamma)
+    r = to_np(op.rstd)
+    np.testing.assert_allclose(r, 1 / np.sqrt((S * S).mean(axis=1) + np.float64(np.float32(eps))), rtol=2.0 ** -23)
+    dx, dg = torch.full_like(s, float("nan")), torch.full((width,), float("nan"), device="cuda")
+    op.backward(dn, s, gamma, dx, dg, overwrite=True)
+    ref, ref_dg = norm.backward(N, S, G, r)
+    R = r[:, None]
+    dots = np.abs(N * G * S * R).mean(axis=1, keepdims=True)
+    half = 2.0 ** -8 if dtype == "bf16" else U
+    tol = half * np.abs(ref) + 8 * U * (np.abs(N * G) * R + np.abs(S) * R * R * dots) + (width + 3) * U * np.abs(S) * R * R * dots
+    err = np.abs(to_np(dx) - ref)
+    assert np.all(err <= tol), [(m, float((e / t).max())) for m, e, t in zip(size, err, tol)]
+    assert np.all(np.abs(to_np(dg) - ref_dg) <= (T + 4) * U * np.abs(N * S * R).sum(axis=0))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("block", [0, 128])
 def test_mean_squares_below_the_normal_range(mb, dtype, block):
