@@ -219,18 +219,9 @@ __device__ __forceinline__ Peak warp_peak(Peak p, bool exact) {
 }
 
 // 1 / sqrt(mean + eps) from the row's sum of squares, as a sum of two floats: the
-// approximate root once refined (the residual 1 - m y^2 taken exactly).  Where both are below 2^-80 they are
-// worked on times 2^60: 1 / mean would leave float32's range, and lo is not small beside hi there.
-__device__ __forceinline__ void inverse_root(float hi, float lo, float width, float inv_width, float eps, float &rh, float &rl) {
-    float back = 1.0f;
-    if (__fadd_rn(hi, eps) < 0x1p-80f) {
-        const float h = __fadd_rn(hi, lo);
-        lo = __fsub_rn(lo, __fsub_rn(h, hi)) * 0x1p60f;
-        hi = h * 0x1p60f;
-        eps *= 0x1p60f;
-        back = 0x1p30f;
-    }
-    float mh = __fmul_rn(hi, inv_width);
+// approximate root once refined (the residual 1 - m y^2 taken exactly).
+__device__ __forceinline__ void refined_root(float hi, float lo, float width, float inv_width, float eps, float &mh, float &rh, float &rl) {
+    mh = __fmul_rn(hi, inv_width);
     float ml = (__fmaf_rn(-mh, width, hi) + lo) * inv_width;
     two_add(mh, ml, eps);
     const float y = rsqrtf(mh);
@@ -239,8 +230,17 @@ __device__ __forceinline__ void inverse_root(float hi, float lo, float width, fl
     const float c = y * (0.5f * e + 0.375f * e * e);
     rh = __fadd_rn(y, c);
     rl = c - __fsub_rn(rh, y);
-    rh *= back, rl *= back;
-    if (mh == 0.0f) rh = y, rl = 0.0f;                 // eps = 0 and a row of zeros: infinite
+}
+__device__ __forceinline__ void inverse_root(float hi, float lo, float width, float inv_width, float eps, float &rh, float &rl) {
+    float mh;
+    refined_root(hi, lo, width, inv_width, eps, mh, rh, rl);
+    if (mh < 0x1p-80f) {
+        // once more times 2^60: 1 / mean leaves float32's range, and lo is not small beside hi
+        const float h = __fadd_rn(hi, lo);
+        refined_root(h * 0x1p60f, __fsub_rn(lo, __fsub_rn(h, hi)) * 0x1p60f, width, inv_width, eps * 0x1p60f, mh, rh, rl);
+        rh *= 0x1p30f, rl *= 0x1p30f;
+        if (mh == 0.0f) rh = INFINITY, rl = 0.0f;      // eps = 0 and a row of zeros
+    }
     if (!(hi < INFINITY)) rh = NAN, rl = 0.0f;         // an infinity or a NaN in the row
 }
 
