@@ -313,6 +313,22 @@ __device__ __forceinline__ void row_barrier(int slot, int warps) {
     else asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(32 * warps) : "memory");
 }
 
+// n of a row in which s gamma leaves float32's range, from s once more: s r gamma need not leave it.
+// (A call: inside the loop over the rows its registers cost the codes 3%.)
+template <class L>
+__device__ __noinline__ void norm_again(const NormArgs &a, const typename L::T *row, int64_t at, int w, float rh) {
+    using T = typename L::T;
+    constexpr int E = L::E;
+    for (int c = L::first_col(w, threadIdx.x & 31); c < a.width; c += a.warps * L::kUnit) {
+        float n[E], g[E];
+        L::unpack(L::load(row + at, c, a.width), n);
+        L::unpack(L::load(static_cast<const T *>(a.gamma), c, a.width), g);
+#pragma unroll
+        for (int i = 0; i < E; ++i) n[i] = (n[i] * rh) * g[i];
+        L::store(static_cast<T *>(a.n) + at, c, a.width, L::pack(n));
+    }
+}
+
 // RES: a residual branch is added.
 template <class L, int N, bool RES>
 __global__ void __launch_bounds__(32 * kNormMaxWarps)
@@ -425,6 +441,7 @@ add_rmsnorm_kernel(const NormArgs a) {
                 for (int i = 0; i < E; ++i) n[i] = (kExact ? v[u][i] : v[u][i] * gv[i]) * rh;
                 L::store(static_cast<T *>(a.n) + at, c[u], a.width, L::pack(n));
             }
+            if (!(top.hi < INFINITY)) norm_again<L>(a, static_cast<const T *>(RES ? a.sum : a.x), at, w, rh);
         }
         if (a.codes) {
             float ch, cl, up;                 // by blocks: of the block whose scale the lane has found

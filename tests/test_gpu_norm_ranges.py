@@ -77,3 +77,22 @@ def test_mean_squares_below_the_normal_range(mb, dtype, block):
     np.testing.assert_allclose(to_np(n), ref_n, rtol=3 * U + (2.0 ** -8 if dtype == "bf16" else U))
     np.testing.assert_array_equal(to_np(scales), ref_scales.astype(np.float64))
     np.testing.assert_array_equal(to_np(codes), ref_codes)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("with_res", [True, False])
+@pytest.mark.parametrize("width", [300, 1024, 5000])
+def test_n_where_the_products_of_sum_and_gamma_overflow(mb, width, with_res, dtype):
+    """sum * gamma is 2^130, n = sum * rstd * gamma is not: n is the formula's."""
+    import torch
+    T = 400
+    rng = np.random.default_rng(6)
+    x, gamma = rng.normal(0, 1, (T, width)), 1 + rng.normal(0, 0.2, width)
+    x[3, 200], x[-1, 200], gamma[200] = 2.0 ** 20, -2.0 ** 22, 2.0 ** 110
+    res = rng.normal(0, 1, (T, width)) if with_res else None
+    x, gamma = _t(x, dtype), _t(gamma, dtype)
+    s = torch.empty_like(x) if with_res else None
+    op, n = mb.AddRmsNorm(T, width, 1e-6, dtype), torch.empty_like(x)
+    op.forward(x, gamma, n=n, residual=_t(res, dtype) if with_res else None, sum=s)
+    ref, _, _, _ = norm.forward(to_np(s if with_res else x), to_np(gamma), 1e-6)
+    np.testing.assert_allclose(to_np(n), ref, rtol=3 * U + (2.0 ** -8 if dtype == "bf16" else U), atol=1e-37)
