@@ -670,7 +670,7 @@ int mlpblk_moe_route_backward(const mlpblk_route_desc *desc, const void *logits,
  * and that scale's codes NaN).  A row that holds an infinity or a NaN, or whose squares' sum leaves float32's range,
  * has a NaN rstd and NaN scales and codes: no row of magnitudes below 2^56, possibly one with a
  * larger magnitude, certainly one with 2^63 or more.  Squares below 2^-149 count as zero, and below 2^-126 they
- * keep as many bits as float32 has there.
+ * keep as many bits as float32 has there.  A gamma that is NaN or infinite makes the scales over it NaN, and those scales' codes.
  *
  * mlpblk_add_rmsnorm_backward: with dn the gradient of n (as the codes stand for it:
  *   rounding passes it on) and d_sum that of sum (NULL: none),

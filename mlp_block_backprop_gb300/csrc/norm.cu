@@ -179,14 +179,21 @@ __device__ __forceinline__ void two_add(float &hi, float &lo, float v) {
     hi = s;
 }
 
+// The larger one; NaN if one of them is (fmaxf drops it).  Units with such a gamma marked ahead of the loop over the
+// rows, instead: 8192 x 8192 by blocks 93 us, with this 87.
+__device__ __forceinline__ float larger(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // A product as it orders: the float32 product and, in float32 tensors, its rounding error
-// (bf16 products are exact).
+// (bf16 products are exact).  A NaN stays: it is gamma's, and then the scale's.
 struct Peak {
     float hi, lo;
     __device__ __forceinline__ void take(float h, float l) {
-        const bool more = h > hi || (h == hi && l > lo);
-        hi = more ? h : hi;
-        lo = more ? l : lo;
+        lo = h > hi || (h == hi && l > lo) ? l : lo;
+        hi = larger(hi, h);
     }
 };
 
@@ -210,7 +217,7 @@ __device__ __forceinline__ void warp_sum(float &hi, float &lo) {
 }
 __device__ __forceinline__ float warp_max(float v) {
     float r;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
 __device__ __forceinline__ Peak warp_peak(Peak p, bool exact) {
@@ -400,7 +407,7 @@ add_rmsnorm_kernel(const NormArgs a) {
                 hi = sum;
                 const float p = __fmul_rn(s, gv[i]);
                 if (kExact) {
-                    peak[u].hi = fmaxf(peak[u].hi, fabsf(p));
+                    peak[u].hi = larger(peak[u].hi, fabsf(p));
                     v[u][i] = p;
                 } else {
                     const float pl = __fmaf_rn(s, gv[i], -p);
@@ -413,7 +420,7 @@ add_rmsnorm_kernel(const NormArgs a) {
         Peak top = peak[0];
 #pragma unroll
         for (int u = 1; u < N; ++u) {
-            if (kExact) top.hi = fmaxf(top.hi, peak[u].hi);
+            if (kExact) top.hi = larger(top.hi, peak[u].hi);
             else top.take(peak[u].hi, peak[u].lo);
         }
         warp_sum(hi, lo);
@@ -463,7 +470,7 @@ add_rmsnorm_kernel(const NormArgs a) {
                         const Peak give = half > 0 && !upper ? mine[u + half] : mine[u];
                         if (half > 0 && upper) mine[u] = mine[u + half];
                         const float h = __shfl_xor_sync(0xffffffffu, give.hi, o);
-                        if (kExact) mine[u].hi = fmaxf(mine[u].hi, h);
+                        if (kExact) mine[u].hi = larger(mine[u].hi, h);
                         else mine[u].take(h, __shfl_xor_sync(0xffffffffu, give.lo, o));
                     }
                 }

@@ -96,3 +96,29 @@ def test_n_where_the_products_of_sum_and_gamma_overflow(mb, width, with_res, dty
     op.forward(x, gamma, n=n, residual=_t(res, dtype) if with_res else None, sum=s)
     ref, _, _, _ = norm.forward(to_np(s if with_res else x), to_np(gamma), 1e-6)
     np.testing.assert_allclose(to_np(n), ref, rtol=3 * U + (2.0 ** -8 if dtype == "bf16" else U), atol=1e-37)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("block", [0, 128])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_gamma_that_is_not_finite(mb, dtype, block, value):
+    """max |n| over a NaN or an infinity: the scale of its block (or row) and that scale's codes are NaN, the others are not."""
+    import torch
+    for T, d, at in ((5, 300, 200), (700, 1024, 1023), (3, 129, 0), (40, 1001, 640)):
+        rng = np.random.default_rng(d)
+        x, gamma = _t(rng.normal(0, 1, (T, d)), dtype), _t(1 + rng.normal(0, 0.2, d), dtype)
+        gamma[at] = value
+        per = (d + 127) // 128 if block else 1
+        op = mb.AddRmsNorm(T, d, 1e-6, dtype, block)
+        codes, scales = torch.empty(T, d, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(T, per, device="cuda")
+        op.forward(x, gamma, codes, scales)
+        fine = to_np(gamma)
+        fine[at] = 1.0
+        _, ref_codes, ref_scales, ref_r = norm.forward(to_np(x), fine, 1e-6, block)
+        np.testing.assert_allclose(to_np(op.rstd), ref_r, rtol=2.0 ** -23)
+        bad = np.zeros(per, dtype=bool)
+        bad[at // 128 if block else 0] = True
+        wide = np.repeat(bad, 128 if block else d)[:d]
+        assert np.isnan(to_np(scales)[:, bad]).all() and np.isnan(to_np(codes)[:, wide]).all()
+        np.testing.assert_array_equal(to_np(scales)[:, ~bad], ref_scales.astype(np.float64)[:, ~bad])
+        np.testing.assert_array_equal(to_np(codes)[:, ~wide], ref_codes[:, ~wide])
