@@ -274,7 +274,7 @@ __device__ __forceinline__ float scale_of(const Peak &p, float rh, float rl, flo
     const float down = small ? 0x1p-64f : 1.0f, a = rh * down;
     ch = __fdiv_rn(a, scale);
     cl = __fdiv_rn(__fmaf_rn(-ch, scale, a) + rl * down, scale);
-    if (!(p.hi > 0.0f)) ch = cl = 0.0f;                // (r may be infinite there)
+    if (!(p.hi > 0.0f)) ch = cl = 0.0f, up = 1.0f;     // zeros, or behind the row's end: codes of 0 (r may be infinite there)
     if (scale != scale) ch = cl = NAN;
     return scale;
 }

@@ -122,3 +122,25 @@ def test_gamma_that_is_not_finite(mb, dtype, block, value):
         assert np.isnan(to_np(scales)[:, bad]).all() and np.isnan(to_np(codes)[:, wide]).all()
         np.testing.assert_array_equal(to_np(scales)[:, ~bad], ref_scales.astype(np.float64)[:, ~bad])
         np.testing.assert_array_equal(to_np(codes)[:, ~wide], ref_codes[:, ~wide])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("width", [200, 1536, 5120])
+def test_blocks_of_zeros_among_others(mb, width, dtype):
+    """Blocks of zeros (also negative ones) and of values below 2^-60 beside ordinary ones, and widths whose last units lie
+    behind the row's end: scales of 1 and codes of zero with the values' signs."""
+    import torch
+    T = 700
+    rng = np.random.default_rng(width)
+    x = rng.normal(0, 1, (T, width))
+    for t in range(T):
+        b = rng.integers(0, (width + 127) // 128)
+        x[t, 128 * b:128 * (b + 1)] = (0.0, -0.0, 1e-25, 2.0 ** -100)[t % 4]
+    x, gamma = _t(x, dtype), _t(1 + rng.normal(0, 0.2, width), dtype)
+    op = mb.AddRmsNorm(T, width, 1e-6, dtype, 128)
+    codes, scales = torch.empty(T, width, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(T, (width + 127) // 128, device="cuda")
+    op.forward(x, gamma, codes, scales)
+    _, ref_codes, ref_scales, _ = norm.forward(to_np(x), to_np(gamma), 1e-6, 128)
+    np.testing.assert_array_equal(to_np(scales), ref_scales.astype(np.float64))
+    np.testing.assert_array_equal(to_np(codes), ref_codes)
+    np.testing.assert_array_equal(np.signbit(to_np(codes)), np.signbit(to_np(x)))
