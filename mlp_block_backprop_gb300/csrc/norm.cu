@@ -581,11 +581,13 @@ add_rmsnorm_bwd_kernel(const NormArgs a) {
             for (int i = 0; i < E; ++i) dot += d[i] * gv[i] * (s[i] * r);   // (g xh: rstd's powers alone leave float32's range)
         }
         if (kAhead && t + step < a.T) fetch(t + step);
-        // The row after next is asked into L2 by three of its warps, an array each: what a warp has in flight
+        // The row after next is asked into L2, by a lane each of its first three warps or, of fewer, by the first warp's
+        // first three lanes: what a warp has in flight
         // in its registers is one row (16384 x 4096 bf16 92 -> 86 us, 8192 x 768, which L2 holds, 15.2 -> 16.2;
         // with the warp's pointer kept over the loop the registers spill and nothing is won).
-        if (L::VEC && a.ask && w < 3 && lane == 0 && t + 2 * step < a.T) {
-            const void *src = w == 0 ? a.x : w == 1 ? a.dn : a.d_sum;
+        const int array = W > 2 ? w + 3 * lane : lane + 3 * w;
+        if (L::VEC && a.ask && array < 3 && t + 2 * step < a.T) {
+            const void *src = array == 0 ? a.x : array == 1 ? a.dn : a.d_sum;
             if (src)
                 asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const T *>(src) + (t + 2 * step) * a.width),
                              "r"(a.width * static_cast<int>(sizeof(T)))

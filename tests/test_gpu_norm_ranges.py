@@ -144,3 +144,25 @@ def test_blocks_of_zeros_among_others(mb, width, dtype):
     np.testing.assert_array_equal(to_np(scales), ref_scales.astype(np.float64))
     np.testing.assert_array_equal(to_np(codes), ref_codes)
     np.testing.assert_array_equal(np.signbit(to_np(codes)), np.signbit(to_np(x)))
+
+
+@pytest.mark.parametrize("shape", [(52000, 256), (30001, 512), (15000, 1000), (13000, 1024)])
+def test_gradients_of_many_rows_of_few_warps(mb, shape):
+    """Rows of one, two and four warps, whose arrays are asked into L2 ahead: every row's gradient, with and without d_sum."""
+    import torch
+    T, d = shape
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    rand = lambda *n: torch.randn(*n, device="cuda", generator=gen)
+    s, dn, ds, gamma = (t.to(torch.bfloat16) for t in (rand(T, d), rand(T, d), rand(T, d), 1 + 0.2 * rand(d)))
+    op = mb.AddRmsNorm(T, d)
+    op.forward(s, gamma, n=torch.empty_like(s))
+    S, N, G, r = s.double(), dn.double(), gamma.double(), op.rstd.double()[:, None]
+    xh, g = S * r, N * G
+    ref = r * (g - xh * (g * xh).mean(dim=1, keepdim=True))
+    mag = (g.abs() + xh.abs() * (g * xh).abs().mean(dim=1, keepdim=True)) * r
+    for d_sum in (ds, None):
+        dx, dg = torch.full_like(s, float("nan")), torch.full((d,), float("nan"), device="cuda")
+        op.backward(dn, s, gamma, dx, dg, d_sum=d_sum, overwrite=True)
+        want = ref if d_sum is None else ref + ds.double()
+        assert bool(((dx.double() - want).abs() <= 2.0 ** -8 * want.abs() + (d + 11) * U * (mag + ds.double().abs())).all())
+        assert bool(((dg.double() - (N * xh).sum(0)).abs() <= (T + 4) * U * (N * xh).abs().sum(0)).all())
