@@ -328,26 +328,34 @@ __device__ __noinline__ void route_exactly(const RouteArgs &a, const T *row, boo
     }
 }
 
-// How far two marks may be off together: two keys each, and their sums.
-__device__ __forceinline__ float near_cut(float last, float next, float most) {
-    return 16.0f * kHalf * most + 4.0f * kHalf * (fabsf(last) + fabsf(next));
+// What the roundings of the scores may move between two keys (between two marks twice that), given the
+// largest score: 2 x 3.4 u of it (route_kernel says whence), and of the softmax 20 u of the scores' difference for the
+// common sum (12 additions, its terms' own errors and the quotient).
+__device__ __forceinline__ float score_slack(bool sigmoid, float most) { return (sigmoid ? 8.0f : 28.0f) * kHalf * most; }
+
+// How far a mark may be off by the roundings of its keys' sums with the bias, its own and that of a bound mark -+ off: 3 u of
+// the keys' magnitudes, which are more than the mark's where the keys have opposite signs.  Infinite ones are exact.
+__device__ __forceinline__ float mark_off(float first, float second, float mark) {
+    if (!(fabsf(mark) < INFINITY)) return 0.0f;
+    return 5.0f * kHalf * fabsf(first) + (second > -INFINITY ? 5.0f * kHalf * fabsf(second) : 0.0f);
 }
 
 // Groups of whole lanes whose marks lie too near the cut: settles which of them stay, in float64, from the
-// experts that may be their two best.  A token belongs to L lanes, a group to `span` of them; mark,
-// second, kept: the group's; last, next: the least mark that is kept, the best that is not; returns whether the
-// lane's group stays.  The whole warp calls it; tokens that are not `close` keep what they have.
+// experts that may be their two best.  A token belongs to L lanes, a group to `span` of them; mark, off,
+// second, kept: the group's; low, high: the least bound mark - off that is kept, the largest mark + off that is not; returns
+// whether the lane's group stays.  The whole warp calls it; tokens that are not `close` keep what they have.
 template <class T, int L>
-__device__ __noinline__ bool settle_groups(const RouteArgs &a, const T *row, const float *key, float second, float mark, bool kept,
-                                           float last, float next, float slack, bool close, int span) {
+__device__ __noinline__ bool settle_groups(const RouteArgs &a, const T *row, const float *key, float second, float mark, float off, bool kept,
+                                           float low, float high, float slack, bool close, int span) {
     const unsigned all = 0xffffffffu;
     const int sub = threadIdx.x % L, e0 = sub * kRouteV, lane0 = threadIdx.x % 32 / L * L;
     const unsigned mine = L == 32 ? all : ((1u << (L % 32)) - 1u) << lane0;
-    const bool doubt = close && mark > -INFINITY && (kept ? mark <= next + slack : mark >= last - slack);
+    const bool doubt = close && mark > -INFINITY && (kept ? mark - off <= high + slack : mark + off >= low - slack);
+    const float least = second - (slack + 4.0f * kHalf * fabsf(second));   // of the keys that may be second best
     uint32_t which = 0;
 #pragma unroll 1
     for (int i = 0; i < kRouteV; ++i)
-        if (doubt && key[i] > -INFINITY && key[i] >= second - slack) which |= 1u << i;
+        if (doubt && key[i] > -INFINITY && key[i] >= least) which |= 1u << i;
     float m = -INFINITY;
     double z = 0.0;
     if (!a.sigmoid) {
@@ -453,8 +461,8 @@ route_kernel(const RouteArgs a) {
         // Keys, and how far they may be off (u = 2^-24).  Sigmoid: ex2.approx 4 u of e and its
         // argument |x| u, both times s (1 - s) (1/4 at most; |x| s (1 - s) 0.23 at most), 1 + e u, the
         // reciprocal 2 u: 3.3 u.  Softmax: exp 2 u, its argument |l - m| u times s / max s (1/e at
-        // most), the product u: 3.4 u of the largest score, and a sum of 13 roundings that
-        // moves all scores alike.  The sum with the bias u of the key.
+        // most), the product u: 3.4 u of the largest score, and a sum whose roundings
+        // move all scores alike (score_slack).  The sum with the bias u of the key.
         const float most = a.sigmoid ? 1.0f : inv_z;
         if (KEYED) {
 #pragma unroll
@@ -469,7 +477,8 @@ route_kernel(const RouteArgs a) {
         bool close = false;
         if (grouped) {
             uint32_t kept = 0;                      // of the lane's eight, those in kept groups
-            float last, next;                       // the least mark that is kept, the best that is not
+            float low, high;                        // bounds of the least mark that is kept, of the best that is not
+            const float slack = 2.0f * score_slack(a.sigmoid, most);
             if (whole) {
                 float first = fmaxf(key[0], key[1]), second = fminf(key[0], key[1]);
 #pragma unroll
@@ -478,28 +487,27 @@ route_kernel(const RouteArgs a) {
                     const float x = __shfl_xor_sync(all, first, o), y = __shfl_xor_sync(all, second, o);
                     join_two(first, second, x, y);
                 }
-                float mark = mark_of(first, second);
+                const float own = mark_of(first, second), off = mark_off(first, second, own);
+                float mark = own;
                 // (the best mark's lowest group: no lane before the group's first has it)
                 const unsigned before = mine & ((1u << (lane0 + (sub & -span))) - 1u);
-                last = INFINITY;
                 for (int r = 0; r < a.top_groups; ++r) {
                     const float best = lanes_max<L>(mark);
                     const unsigned votes = __ballot_sync(all, mark == best);
-                    last = best;
                     if (mark == best && (votes & before) == 0) {
                         // (a group without an open expert may be kept too: it has nothing to select)
                         kept = 0xFFu;
                         mark = -INFINITY;
                     }
                 }
-                next = lanes_max<L>(mark);
-                const float slack = near_cut(last, next, most);
-                const bool doubt = next > -INFINITY && last < INFINITY && last - next <= slack;
+                low = -lanes_max<L>(kept != 0 ? off - own : -INFINITY);
+                high = lanes_max<L>(kept != 0 ? -INFINITY : own + off);
+                const bool doubt = high > -INFINITY && low < INFINITY && low - high <= slack;
                 if (__any_sync(all, doubt)) {
                     float copy[kRouteV];
 #pragma unroll
                     for (int i = 0; i < kRouteV; ++i) copy[i] = key[i];
-                    kept = settle_groups<T, L>(a, rows + t * a.E, copy, second, mark_of(first, second), kept != 0, last, next, slack, doubt, span) ? 0xFFu : 0u;
+                    kept = settle_groups<T, L>(a, rows + t * a.E, copy, second, own, off, kept != 0, low, high, slack, doubt, span) ? 0xFFu : 0u;
                 }
                 if (by_logit) {
 #pragma unroll
@@ -517,25 +525,27 @@ route_kernel(const RouteArgs a) {
                 for (int g = sub; g < a.groups; g += L) {
                     float first = -INFINITY, second = -INFINITY;
                     for (int i = 0; i < a.per; ++i) join_two(first, second, keys[g * a.per + i], -INFINITY);
-                    marks[g * a.per] = mark_of(first, second);   // (no other lane reads this group)
+                    const float own = mark_of(first, second);
+                    marks[g * a.per] = own;         // (no other lane reads this group)
+                    if (a.per > 1) marks[g * a.per + 1] = mark_off(first, second, own);
                 }
                 __syncwarp();
                 // each lane settles some groups; a vote tells all of them
-                last = INFINITY, next = -INFINITY;
+                low = INFINITY, high = -INFINITY;
                 uint64_t groups = 0;
                 for (int g0 = 0; g0 < a.groups; g0 += L) {
                     const int g = g0 + sub;
                     const bool on = g < a.groups && group_kept(marks, a.per, a.groups, a.top_groups, g);
                     if (g < a.groups) {
-                        const float x = marks[g * a.per];
-                        if (on) last = fminf(last, x);
-                        else next = fmaxf(next, x);
+                        const float x = marks[g * a.per], off = a.per > 1 ? marks[g * a.per + 1] : mark_off(x, -INFINITY, x);
+                        if (on) low = fminf(low, x - off);
+                        else high = fmaxf(high, x + off);
                     }
                     groups |= static_cast<uint64_t>((__ballot_sync(all, on) & mine) >> lane0) << g0;
                 }
-                last = -lanes_max<L>(-last);
-                next = lanes_max<L>(next);
-                close = next > -INFINITY && last < INFINITY && last - next <= near_cut(last, next, most);
+                low = -lanes_max<L>(-low);
+                high = lanes_max<L>(high);
+                close = high > -INFINITY && low < INFINITY && low - high <= slack;
 #pragma unroll
                 for (int i = 0; i < kRouteV; ++i) {
                     if (by_logit) key[i] = l[i];
@@ -608,10 +618,10 @@ route_kernel(const RouteArgs a) {
             // Neighbours that float32 cannot tell apart: near, or the same numbers (equal then, in order of
             // their experts).  What float32 may be off: two keys and, of the softmax, what the common sum
             // does to the scores' difference (at the cut the other one stands for everything below it, so
-            // for the largest score).
+            // for the largest score); u of each key for its sum with the bias.
             enum : int { kApart = 0, kNear = 1, kSame = 2 };
             auto reach = [&](int n, float x, float y) {
-                return (a.sigmoid ? 8.0f : 22.0f) * kHalf * w.most[n] + 2.0f * kHalf * (fabsf(x) + fabsf(y));
+                return score_slack(a.sigmoid, w.most[n]) + 2.0f * kHalf * (fabsf(x) + fabsf(y));
             };
             bool any = false;
             for (int i = lane; i < N * a.k; i += 32) {

@@ -1,0 +1,62 @@
+"""The router where float32 keys do not tell groups or experts apart, and gradients beside slots that select
+nothing, against float64, GB300 only.  Ids are compared exactly; no tolerances but where stated."""
+
+import numpy as np
+import pytest
+
+from oracle import route
+from helpers import to_np
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mb():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import mlp_block_backprop_gb300 as mb
+    yield mb
+    assert mb.mlpblk_last_error() == mb.MLPBLK_OK
+
+
+def _select(l, k, score, bias, groups, top_groups):
+    """oracle.route's ids for rows of finite logits and biases, all rows at once."""
+    l = l.astype(np.float64)
+    T, E = l.shape
+    if score == "sigmoid":
+        s = 1.0 / (1.0 + np.exp(-l))
+    else:
+        e = np.exp(l - l.max(axis=1, keepdims=True))
+        s = e / e.sum(axis=1, keepdims=True)
+    key = s + bias.astype(np.float64)
+    by = key.reshape(T, groups, E // groups)
+    best = np.sort(by, axis=2)[:, :, -2:]
+    marks = best.sum(axis=2)
+    keep = np.argsort(-marks, axis=1, kind="stable")[:, :top_groups]
+    kept = np.zeros((T, groups), dtype=bool)
+    np.put_along_axis(kept, keep, True, axis=1)
+    return np.argsort(-np.where(np.repeat(kept, E // groups, axis=1), key, -np.inf), axis=1, kind="stable")[:, :k].astype(np.int32)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("shape", [(256, 8, 4), (240, 10, 4), (48, 12, 5), (16, 8, 3)])
+@pytest.mark.parametrize("size", [0.0, 1.0, 10.0, 100.0, 1e4])
+def test_groups_whose_keys_cancel_in_their_marks(mb, shape, score, size):
+    """A bias of +size on one expert of each group and -size on the others: marks near zero, whose keys'
+    roundings are of +size's."""
+    import torch
+    E, groups, top_groups = shape
+    T, k, per = 65536, 4, E // groups
+    rng = np.random.default_rng(E)
+    l = rng.normal(0, 0.1, (T, E)).astype(np.float32)
+    bias = np.full((groups, per), -size, dtype=np.float32)
+    bias[np.arange(groups), rng.integers(0, per, groups)] = size
+    bias = bias.ravel()
+    ids, w = torch.full((T, k), 77, dtype=torch.int32, device="cuda"), torch.full((T, k), 77.0, device="cuda")
+    mb.MoeRouter(T, E, k, score, groups, top_groups, dtype="f32").route(torch.from_numpy(l).cuda(), ids, w, bias=torch.from_numpy(bias).cuda())
+    ref = _select(l, k, score, bias, groups, top_groups)
+    wrong = np.nonzero((ids.cpu().numpy() != ref).any(axis=1))[0]
+    assert len(wrong) == 0, (len(wrong), wrong[:4], ids.cpu().numpy()[wrong[:4]], ref[wrong[:4]])
+    some = slice(0, 40)
+    np.testing.assert_array_equal(route.route(l[some], k, score, bias, groups, top_groups)[0], ref[some])
