@@ -151,10 +151,10 @@ __device__ __forceinline__ void join_two(double &first, double &second, double a
     second = second < b ? b : second;
     second = second < low ? low : second;
 }
-// A group's mark from its two best keys: -inf where it has no open expert.
+// A group's mark from its two best keys, half their sum (which may leave float32's range): -inf where it has no open expert.
 template <class F>
 __device__ __forceinline__ F mark_of(F first, F second) {
-    return second > -INFINITY ? first + second : first;
+    return second > -INFINITY ? F(0.5) * first + F(0.5) * second : F(0.5) * first;
 }
 
 // Is group g among the best?  marks in shared memory, `stride` apart; ties to the lower group.
@@ -328,16 +328,16 @@ __device__ __noinline__ void route_exactly(const RouteArgs &a, const T *row, boo
     }
 }
 
-// What the roundings of the scores may move between two keys (between two marks twice that), given the
+// What the roundings of the scores may move between two keys (or two marks, half the sum of two keys each), given the
 // largest score: 2 x 3.4 u of it (route_kernel says whence), and of the softmax 20 u of the scores' difference for the
 // common sum (12 additions, its terms' own errors and the quotient).
 __device__ __forceinline__ float score_slack(bool sigmoid, float most) { return (sigmoid ? 8.0f : 28.0f) * kHalf * most; }
 
 // How far a mark may be off by the roundings of its keys' sums with the bias, its own and that of a bound mark -+ off: 3 u of
-// the keys' magnitudes, which are more than the mark's where the keys have opposite signs.  Infinite ones are exact.
+// half the keys' magnitudes, which are more than the mark's where the keys have opposite signs.  Infinite ones are exact.
 __device__ __forceinline__ float mark_off(float first, float second, float mark) {
     if (!(fabsf(mark) < INFINITY)) return 0.0f;
-    return 5.0f * kHalf * fabsf(first) + (second > -INFINITY ? 5.0f * kHalf * fabsf(second) : 0.0f);
+    return 2.5f * kHalf * fabsf(first) + (second > -INFINITY ? 2.5f * kHalf * fabsf(second) : 0.0f);
 }
 
 // Groups of whole lanes whose marks lie too near the cut: settles which of them stay, in float64, from the
@@ -478,7 +478,7 @@ route_kernel(const RouteArgs a) {
         if (grouped) {
             uint32_t kept = 0;                      // of the lane's eight, those in kept groups
             float low, high;                        // bounds of the least mark that is kept, of the best that is not
-            const float slack = 2.0f * score_slack(a.sigmoid, most);
+            const float slack = score_slack(a.sigmoid, most);
             if (whole) {
                 float first = fmaxf(key[0], key[1]), second = fminf(key[0], key[1]);
 #pragma unroll

@@ -60,3 +60,19 @@ def test_groups_whose_keys_cancel_in_their_marks(mb, shape, score, size):
     assert len(wrong) == 0, (len(wrong), wrong[:4], ids.cpu().numpy()[wrong[:4]], ref[wrong[:4]])
     some = slice(0, 40)
     np.testing.assert_array_equal(route.route(l[some], k, score, bias, groups, top_groups)[0], ref[some])
+
+
+@pytest.mark.parametrize("shape", [(256, 8, 4), (240, 10, 4), (24, 12, 5)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_marks_beyond_the_range_of_float32(mb, shape, sign):
+    """Biases of which two overflow when added: the marks order all the same."""
+    import torch
+    E, groups, top_groups = shape
+    T, k = 300, 4
+    rng = np.random.default_rng(groups)
+    l = rng.normal(0, 1, (T, E)).astype(np.float32)
+    bias = (sign * rng.uniform(1.8e38, 3.4e38, E)).astype(np.float32)
+    ids, w = torch.full((T, k), 77, dtype=torch.int32, device="cuda"), torch.full((T, k), 77.0, device="cuda")
+    mb.MoeRouter(T, E, k, "sigmoid", groups, top_groups, dtype="f32").route(torch.from_numpy(l).cuda(), ids, w, bias=torch.from_numpy(bias).cuda())
+    ref, _ = route.route(l, k, "sigmoid", bias, groups, top_groups)
+    np.testing.assert_array_equal(ids.cpu().numpy(), ref)
