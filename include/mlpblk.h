@@ -621,7 +621,7 @@ int mlpblk_fp4_product_kernel(const mlpblk_fp4_matmul_desc *desc, int form, int 
  *
  * mlpblk_moe_route_backward: d_logits[T,E] (written) from d_routing_weights[T,k], for the
  * ids of the same logits, held fixed ("Hard Top-K Has No Ordinary Derivative").  Ids outside
- * 0 .. E-1 and closed experts have no gradient.  The bias has none.
+ * 0 .. E-1 and closed experts have no gradient, and their d_routing_weights no part in the others'.  The bias has none.
  *
  * logits and d_logits [T,E] are in desc->dtype, the rest float32 and int32; scores, sums and
  * quotients are float32, their order fixed.  Limits: tokens < 2^31, experts 1..256, top_k

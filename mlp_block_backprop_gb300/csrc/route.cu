@@ -801,7 +801,7 @@ route_bwd_kernel(const RouteArgs a) {
         w.id[n][r] = e;
         w.s[n][r] = s;
         w.slope[n][r] = slope;
-        w.w[n][r] = a.dw[t0 * a.k + i];
+        w.w[n][r] = e >= 0 ? a.dw[t0 * a.k + i] : 0.0f;   // (what stands beside no expert may be NaN)
     }
     __syncwarp();
     // sum_i s_i and sum_i dw_i s_i

@@ -76,3 +76,33 @@ def test_marks_beyond_the_range_of_float32(mb, shape, sign):
     mb.MoeRouter(T, E, k, "sigmoid", groups, top_groups, dtype="f32").route(torch.from_numpy(l).cuda(), ids, w, bias=torch.from_numpy(bias).cuda())
     ref, _ = route.route(l, k, "sigmoid", bias, groups, top_groups)
     np.testing.assert_array_equal(ids.cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_weights_beside_no_expert_have_no_part_in_the_gradient(mb, score, renorm, dtype):
+    """d_routing_weights of slots without an expert (id -1, or an expert that is closed) may hold anything."""
+    import torch
+    T, E, k = 200, 40, 6
+    rng = np.random.default_rng(1)
+    l = rng.normal(0, 1, (T, E))
+    l[rng.random((T, E)) < 0.9] = -np.inf                  # four open experts on average, six slots
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    dev = torch.from_numpy(l.astype(np.float32)).to(dt).cuda()
+    op = mb.MoeRouter(T, E, k, score, renorm=renorm, dtype=dtype)
+    ids, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    op.route(dev, ids, w)
+    none = ids < 0
+    assert bool(none.any()) and bool((~none).any())
+    ids[:, 5] = torch.where(none[:, 5] & (dev[:, 7] == -float("inf")), 7, ids[:, 5])   # a closed expert's id
+    dw = torch.from_numpy(rng.normal(0, 1, (T, k)).astype(np.float32)).cuda()
+    want, got = torch.empty_like(dev), torch.empty_like(dev)
+    op.route_backward(dev, ids, torch.where(none, 0.0, dw), want)
+    assert bool(want.isfinite().all())
+    for junk in (float("nan"), float("inf"), 3e38):
+        op.route_backward(dev, ids, torch.where(none, junk, dw), got)
+        assert torch.equal(got, want), junk
+    ref = route.backward(to_np(dev), ids.cpu().numpy(), to_np(torch.where(none, 0.0, dw)), score, renorm)
+    # (E + 12 roundings of 2^-24 of terms below 8, and half a step of the type)
+    assert np.all(np.abs(to_np(want) - ref) <= (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * np.abs(ref) + (E + 12) * 8 * 2.0 ** -24)
