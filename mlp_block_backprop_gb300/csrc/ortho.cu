@@ -91,8 +91,9 @@ __device__ __forceinline__ void source(const OrthoSource &u, float gs, int64_t a
     }
 }
 
-// Squares of any size (Blue's three accumulators): a piece whose largest value is beyond 2^60 or below
-// 2^-40 is scaled by a power of two before it is squared.
+// Squares of any size (Blue's three accumulators): a piece whose largest value is beyond 2^40 or below
+// 2^-40 is scaled by a power of two before it is squared.  A thread adds up to 2^23 pieces of eight: below 2^106 in
+// `mid`, 2^122 in `big`.
 struct Squares {
     float big, mid, small;   // times 2^-160, 1, 2^160
 };
@@ -100,7 +101,7 @@ __device__ __forceinline__ void add_squares(Squares &q, const float (&v)[kPiece]
     float m = fabsf(v[0]), s = 0.0f;
 #pragma unroll
     for (int i = 1; i < kPiece; ++i) m = fmaxf(m, fabsf(v[i]));
-    if (m >= 0x1p-40f && m <= 0x1p60f) {
+    if (m >= 0x1p-40f && m <= 0x1p40f) {
 #pragma unroll
         for (int i = 0; i < kPiece; ++i) s = __fmaf_rn(v[i], v[i], s);
         q.mid += s;

@@ -1,0 +1,103 @@
+"""How near the orthogonalised updates come to the formula before they are rounded to bf16 (through
+muon_step's float32 masters), by kind of input and by size, GB300 only.
+
+The bounds are the documented ones, Frobenius norm of the error over that of the formula's result: 3e-3 where the
+entries round independently and the short side is 64 or more, 6e-3 from 12 on, 2e-2 below; and 2e-2 at any size where
+they round alike (few entries that are not zero, multiples of a permutation, rows that are nearly equal).  They come from
+a model in float64 that rounds to fp16 where the kernels do: 2.0e-3 (64), 4.8e-3 (12), 11.3e-3 (2) and, over all 2 x 2
+diagonals, 1.61e-2 at the worst of its inputs; a constant with noise of 1e-3 of it, 700 x 8000, two steps at a time 3.9e-3
+(one at a time 2.0e-3), of 1e-5, 512 x 16000, 11.4e-3 and 4.4e-3.
+"""
+
+import pytest
+
+from oracle import muon
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mb():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import mlp_block_backprop_gb300 as mb
+    yield mb
+    assert mb.mlpblk_last_error() == mb.MLPBLK_OK
+
+
+def _exact(u, steps=5, eps=1e-7):
+    """The oracle's formula in float64 on the GPU."""
+    x = u.double()
+    x = x / (x.square().sum().sqrt() + eps)
+    tall = x.shape[0] > x.shape[1]
+    if tall:
+        x = x.T
+    a, b, c = muon.COEFFICIENTS
+    for _ in range(steps):
+        g = x @ x.T
+        x = a * x + (b * g + c * (g @ g)) @ x
+    return x.T if tall else x
+
+
+def _unrounded(mb, u, steps=5, eps=1e-7):
+    """X as float32: a master of zeros minus lr scale X, lr = 1, scale = -1, from a momentum that is u."""
+    import torch
+    w, m = torch.zeros_like(u), torch.zeros_like(u)
+    b, r, c = u.shape
+    op = mb.Orthogonalizer(r, c, batch=b, steps=steps, eps=eps)
+    op._ws.fill_(0xFF)
+    op.muon_step(w, u, m, 1.0, beta=0.0, scale=-1.0, nesterov=False)
+    assert torch.equal(m, u)
+    return w
+
+
+def _rel(a, b):
+    return float((a.double() - b).norm()) / float(b.norm())
+
+
+def _matrix(gen, r, c, kind):
+    import torch
+    rand = lambda *n: torch.randn(*n, device="cuda", generator=gen)
+    if kind == "flat":
+        return rand(r, c)
+    if kind == "low":
+        return rand(r, 3) @ rand(3, c)
+    if kind == "ones":
+        return 1 + 1e-3 * rand(r, c)
+    if kind == "mixed":
+        k = min(16, r, c)
+        return 0.01 * rand(r, c) * (r ** 0.5 + c ** 0.5) / 2 + (rand(r, k) / torch.arange(1, k + 1, device="cuda")) @ rand(k, c)
+    if kind == "orthogonal":
+        q = torch.linalg.qr(rand(max(r, c), min(r, c)))[0]
+        return (q if r >= c else q.T).contiguous()
+    if kind == "identity":
+        return torch.eye(r, c, device="cuda")
+    if kind == "sparse":
+        return rand(r, c) * (torch.rand(r, c, device="cuda", generator=gen) < 0.1) + torch.eye(r, c, device="cuda")
+    e = float(kind[len("entry"):])          # one entry of 1, noise of size e elsewhere
+    u = e * rand(r, c)
+    u[r // 2, c // 3] = 1.0
+    return u
+
+
+ALIKE = ("identity", "sparse", "ones", "entry0", "entry1e-7")
+
+
+def _bound(r, c, kind):
+    m = min(r, c)
+    return 2e-2 if kind in ALIKE or m < 12 else (6e-3 if m < 64 else 3e-3)
+
+
+@pytest.mark.parametrize("shape", [(460, 256, 512), (3, 8192, 4096)])
+@pytest.mark.parametrize("size", [1.15e18, 3e36, 2.0 ** -41, 2.0 ** -39, 2.0 ** 41])
+def test_norms_of_many_large_values(mb, shape, size):
+    """Every entry of one magnitude, some 40 and more pieces of eight a thread: the squares' sums stay in float32's range."""
+    import torch
+    b, r, c = shape
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    u = (torch.randint(0, 2, (b, r, c), device="cuda", generator=gen) * 2 - 1).float() * size
+    x = _unrounded(mb, u, steps=1, eps=0.0)
+    for i in (0, b - 1):
+        v = u[i] / size                                    # (the formula has no size: eps is 0)
+        assert _rel(x[i], _exact(v, 1, 0.0)) <= 3e-3
