@@ -724,8 +724,13 @@ int mlpblk_add_rmsnorm_backward(const mlpblk_norm_desc *desc, const void *dn, co
  *
  * Precision: products of fp16 values, whose range X's scaling fits, with float32 sums; a X
  * takes X as two fp16 values in all but the last step.  With Muon's coefficients
- * (3.4445, -4.7750, 2.0315), five steps, the result is within 3e-3 of the formula's in the
- * Frobenius norm (before o's rounding to bf16).  The matrices b G + c G^2 are fp16 too: every singular
+ * (3.4445, -4.7750, 2.0315), five steps, the error against the formula, in the Frobenius norm and before o's rounding to
+ * bf16 (X in muon_step), is
+ *   up to 3e-3 where u's entries round independently (noise, low rank, strong directions or a large entry over noise) and
+ *   its short side is 64 or more, mostly 1e-3 to 2e-3; up to 6e-3 for short sides from 12 on, up to 2e-2 below;
+ *   up to 2e-2 at any size where they round alike: few entries that are not zero, multiples of the identity or of a
+ *   permutation (mostly 1e-3 to 5e-3), a constant or nearly equal rows over noise of 1e-3 of them or less.
+ * The matrices b G + c G^2 are fp16 too: every singular
  * value s on the way must keep |b s^2 + c s^4| and, of two neighbouring steps, |a a'| below 60000
  * (with those coefficients s < 13).  A NaN or an
  * infinity in u makes its matrix NaN.  Sums have a fixed order.

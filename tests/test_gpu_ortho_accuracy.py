@@ -89,6 +89,21 @@ def _bound(r, c, kind):
     return 2e-2 if kind in ALIKE or m < 12 else (6e-3 if m < 64 else 3e-3)
 
 
+@pytest.mark.parametrize("kind", ["flat", "low", "ones", "mixed", "orthogonal", "identity", "sparse", "entry0", "entry1e-7", "entry1e-6", "entry1e-2"])
+def test_one_step_at_a_time(mb, kind):
+    import torch
+    for r, c in ((2, 2), (2, 3), (4, 1000), (2, 5000), (8, 8), (12, 13), (16, 16), (24, 24), (32, 32), (35, 35), (63, 200), (64, 64), (96, 96), (353, 353),
+                 (1000, 70), (256, 4000), (512, 512), (512, 4000), (700, 900), (1024, 1024)):
+        gen = torch.Generator(device="cuda").manual_seed(r + c)
+        if kind == "low" and min(r, c) < 4:
+            continue
+        n = 16 if r * c < 5000 else 2
+        u = torch.stack([_matrix(gen, r, c, kind) for _ in range(n)])
+        x = _unrounded(mb, u)
+        errors = [_rel(x[i], _exact(u[i])) for i in range(n)]
+        assert max(errors) <= _bound(r, c, kind), (r, c, max(errors))
+
+
 @pytest.mark.parametrize("shape", [(460, 256, 512), (3, 8192, 4096)])
 @pytest.mark.parametrize("size", [1.15e18, 3e36, 2.0 ** -41, 2.0 ** -39, 2.0 ** 41])
 def test_norms_of_many_large_values(mb, shape, size):
