@@ -1693,8 +1693,9 @@ int orthogonalize_impl(const mlpblk_ortho_desc *d, const OrthoSource &u, void *o
     // Two steps at a time (csrc/gemm_ns.cu) save 3 m^2 (n - m) operations a matrix for one launch
     // more: worth it from some 6 us of the tensor cores on, or where G has few tiles and a long K
     // (640 x 5000: 135 -> 121 us).  Never the last step: its X is kept in one fp16 value, and G's errors would reach
-    // the result.  Nor a short side below 512, over which G's errors average less (one large entry among 256 x 4000 small ones: off by
-    // 3.9e-3 instead of 1.6e-3, at 512 1.5e-3).
+    // the result.  Nor a short side below 512: the joined polynomial's diagonal meets X's low part and its other entries do
+    // not, which a dense strong direction of few rows feels (three directions in 64 x 4000: off by 6.0e-3, one step at a
+    // time 1.1e-3; in 256 x 4000 2.3e-3 and 1.1e-3, in 512 x 4000 1.6e-3 and 1.1e-3).
     const int64_t m = tall ? d->cols : d->rows;
     const bool two = m >= 512 && ((n >= 2 * m && 3.0 * d->batch * m * m * (n - m) >= 8e9) || n >= 2048 + 4 * m);
     int at = 0;   // which of x holds X

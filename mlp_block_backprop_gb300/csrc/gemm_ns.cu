@@ -9,7 +9,10 @@
 // on X for both: with the first step's P1, G becomes (a1 I + P1) G (a1 I + P1), its own P2 follows, and
 // X' = (a2 I + P2)(a1 I + P1) X = a1 a2 X + S X.  That trades a G and an update (3 m^2 n) for three
 // more products of the short side (m^3 each, half of them mirrored): 16384 x 4096 takes 28% fewer
-// operations.  G's own rounding errors then go through a second step, so it stays at two.
+// operations.  G's own rounding errors then go through a second step, so it stays at two.  S cancels most of a1 a2 X on
+// strong directions (-11 of 12), so what S X leaves out of X's low part counts eleven times: S's diagonal is kept out of
+// the product, whole and in float32, and meets both parts of X with a1 a2 (one entry in 512 x 2560: off by 4.7e-3 with
+// the diagonal in S, 1.2e-3 so; Gaussian 1.6e-3 and 0.7e-3).
 //
 // Nothing is transposed in memory: each operand is read K-major or MN-major as it lies,
 // and a tall X is worked on from its right.  G and P are symmetric: only tiles on and
@@ -330,12 +333,15 @@ struct NsEpilogue {
             }
         }
         if ((OP == kNsSquare || OP == kNsJoin) && row0 < col0 + CC && col0 < row0 + 32) {
-            // the chunk lies on the diagonal: what rounding takes from the lane's value there
+            // the chunk lies on the diagonal: what rounding takes from the lane's value there (kNsJoin: all of it)
             const int at = row - col0;
             float x = 0.0f;
 #pragma unroll
-            for (int k = 0; k < CC; ++k) x = k == at ? v[k] : x;
-            if (at >= 0 && at < CC && row < a.rows) a.diag_out[dat + row] = x - __half2float(__float2half_rn(x));
+            for (int k = 0; k < CC; ++k) {
+                x = k == at ? v[k] : x;
+                if (OP == kNsJoin) v[k] = k == at ? 0.0f : v[k];
+            }
+            if (at >= 0 && at < CC && row < a.rows) a.diag_out[dat + row] = OP == kNsJoin ? x : x - __half2float(__float2half_rn(x));
         }
         if (OP == kNsUpdate && a.o) {
 #pragma unroll
@@ -460,7 +466,8 @@ __device__ __forceinline__ void ns_finish_eight(const NsArgs &a, const NsTile &w
         const float2 r = ns_combine<OP>(a, make_float2(v[2 * i], v[2 * i + 1]), unpack_half2(xs[i]), unpack_half2(ys[i]), d, cs[i], row, col + 2 * i);
         v[2 * i] = r.x;
         v[2 * i + 1] = r.y;
-        h[i] = pack_half2(r.x, r.y);
+        const bool d0 = OP == kNsJoin && col + 2 * i == row, d1 = OP == kNsJoin && col + 2 * i + 1 == row;
+        h[i] = pack_half2(d0 ? 0.0f : r.x, d1 ? 0.0f : r.y);
         const float2 p = unpack_half2(h[i]);
         l[i] = pack_half2(r.x - p.x, r.y - p.y);
         if (OP == kNsSquare || OP == kNsJoin) {

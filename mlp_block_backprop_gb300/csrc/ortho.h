@@ -19,9 +19,9 @@ inline int64_t ortho_pitch(int64_t cols) { return (cols + 63) / 64 * 64; }
 //   kNsSquare  out = b Y + c Y Y, diag_out = what rounding took from out's diagonal
 //   kNsApply   out = (a + diag) Y + P Y
 //   kNsJoin    out = (a + diag) Y + P Y + b P with Y's own remainders diag2: the polynomial of two
-//              steps, (a I + P) (b I + Y) less a b I; diag_out as above
+//              steps, (a I + P) (b I + Y) less a b I; its diagonal goes to diag_out whole, and is zero in out
 //   kNsUpdate  out = (a + diag) X + P X or X P;  o: alpha times it in bf16 instead
-// diag: the remainders of P's diagonal.
+// diag: the remainders of P's diagonal (after kNsJoin, the diagonal).
 enum NsOp : int { kNsGram = 0, kNsSquare = 1, kNsUpdate = 2, kNsApply = 3, kNsJoin = 4 };
 
 struct NsProduct {

@@ -104,6 +104,35 @@ def test_one_step_at_a_time(mb, kind):
         assert max(errors) <= _bound(r, c, kind), (r, c, max(errors))
 
 
+@pytest.mark.parametrize("kind", ["flat", "low", "ones", "mixed", "orthogonal", "identity", "entry0", "entry1e-7", "entry1e-6", "entry1e-4", "entry1e-2"])
+def test_two_steps_with_one_product(mb, kind):
+    """3e-3 for all of these but nearly equal rows (2e-2): one entry is off by 1.2e-3 in the model, identities of these
+    sizes by 1.2e-3 at most."""
+    import torch
+    for r, c in ((512, 2560), (2560, 512), (512, 4100), (1024, 4096), (4500, 1024), (700, 8000)):
+        gen = torch.Generator(device="cuda").manual_seed(r + c)
+        # (enough work for the rule on sizes: several matrices of a short side of 512)
+        n = 5 if min(r, c) <= 700 else 2
+        u = torch.stack([_matrix(gen, r, c, kind) for _ in range(n)])
+        with mb.KernelTrace(64) as trace:
+            x = _unrounded(mb, u)
+            torch.cuda.synchronize()
+        assert [name for name, _ in trace.durations()].count("ns_join") == 2
+        errors = [_rel(x[i], _exact(u[i])) for i in (0, n - 1)]
+        assert max(errors) <= (2e-2 if kind == "ones" else 3e-3), (r, c, errors)
+
+
+@pytest.mark.parametrize("steps", [3, 4, 6])
+def test_two_steps_with_one_product_of_one_large_entry(mb, steps):
+    import torch
+    for r, c in ((512, 4100), (4500, 1024)):
+        gen = torch.Generator(device="cuda").manual_seed(steps)
+        for kind in ("entry0", "entry1e-7", "entry1e-6"):
+            u = torch.stack([_matrix(gen, r, c, kind) for _ in range(3)])
+            x = _unrounded(mb, u, steps)
+            assert _rel(x[1], _exact(u[1], steps)) <= 3e-3, (r, c, kind)
+
+
 @pytest.mark.parametrize("shape", [(460, 256, 512), (3, 8192, 4096)])
 @pytest.mark.parametrize("size", [1.15e18, 3e36, 2.0 ** -41, 2.0 ** -39, 2.0 ** 41])
 def test_norms_of_many_large_values(mb, shape, size):
