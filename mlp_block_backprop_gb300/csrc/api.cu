@@ -1614,10 +1614,8 @@ int check_ortho_desc(const mlpblk_ortho_desc *d) {
     if (!d) return MLPBLK_EINVAL;
     if (d->dtype != MLPBLK_BF16 && d->dtype != MLPBLK_FP32) return MLPBLK_ENOTSUP;
     if (d->rows < 1 || d->cols < 1 || d->rows > 131072 || d->cols > 131072 || d->batch < 1 || d->batch > 65535) return MLPBLK_EINVAL;
-    if (d->rows * d->cols >= (static_cast<int64_t>(1) << 40) / d->batch) return MLPBLK_EINVAL;
+    if (d->rows * d->cols * d->batch >= static_cast<int64_t>(1) << 40) return MLPBLK_EINVAL;
     if (d->steps < 1 || d->steps > MLPBLK_ORTHO_MAX_STEPS || !(d->eps >= 0.0f) || !isfinite(d->eps)) return MLPBLK_EINVAL;
-    // (128-column tiles of the update: their count is an int)
-    if ((d->rows + 127) / 128 * ((d->cols + 127) / 128) * d->batch >= kLim31) return MLPBLK_EINVAL;
     for (int i = 0; i < d->steps; ++i)
         for (int j = 0; j < 3; ++j)
             if (!isfinite(d->coefficients[i][j])) return MLPBLK_EINVAL;

@@ -1,0 +1,21 @@
+"""Descriptors at the documented limits, and what the classes raise for those beyond: no GPU."""
+
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def mb():
+    import mlp_block_backprop_gb300 as mb
+    return mb
+
+
+def test_batches_of_just_below_two_to_the_forty_elements(mb):
+    """129648 x 130473 x 65 = 2^40 - 16 elements are taken; one matrix more is not."""
+    d = mb.make_ortho_desc(129648, 130473, batch=65)
+    assert 129648 * 130473 * 65 < 1 << 40
+    assert mb.mlpblk_orthogonalize_workspace_size(d) > 6 * ((1 << 40) - 16)      # three X in fp16
+    assert mb.mlpblk_orthogonalize_workspace_size(mb.make_ortho_desc(129648, 130473, batch=66)) == 0
+    assert mb.mlpblk_orthogonalize_workspace_size(mb.make_ortho_desc(131072, 131072, batch=64)) == 0
+    assert mb.mlpblk_orthogonalize_workspace_size(mb.make_ortho_desc(131072, 131071, batch=64)) > 0
