@@ -1211,8 +1211,8 @@ class AddRmsNorm(_Kept):
         import torch
         self.desc = make_norm_desc(tokens, width, eps, dtype, block)
         size = mlpblk_add_rmsnorm_workspace_size(self.desc)
-        if size == 0:
-            raise MlpBlkError(MLPBLK_EINVAL, "mlpblk_add_rmsnorm_workspace_size")
+        if size == 0:   # (a call without tensors tells why)
+            raise MlpBlkError(lib.mlpblk_add_rmsnorm(ctypes.byref(self.desc), *[None] * 9) or MLPBLK_EINVAL, "AddRmsNorm")
         self._rstd = torch.zeros(tokens, dtype=torch.float32, device=device)
         self._ws = torch.empty(size, dtype=torch.uint8, device=device)
         self._dev = self._ws.get_device()
@@ -1333,8 +1333,8 @@ class Orthogonalizer(_Kept):
         import torch
         self.desc = make_ortho_desc(rows, cols, batch, steps, coefficients, eps, dtype)
         size = mlpblk_orthogonalize_workspace_size(self.desc)
-        if size == 0:
-            raise MlpBlkError(MLPBLK_EINVAL, "mlpblk_orthogonalize_workspace_size")
+        if size == 0:   # (a call without tensors tells why)
+            raise MlpBlkError(lib.mlpblk_orthogonalize(ctypes.byref(self.desc), None, None, None, 0, None) or MLPBLK_EINVAL, "Orthogonalizer")
         self._ws = torch.empty(size, dtype=torch.uint8, device=device)
         self._dev = self._ws.get_device()
         self._d = ctypes.addressof(self.desc)
