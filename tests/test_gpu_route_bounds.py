@@ -106,3 +106,24 @@ def test_weights_beside_no_expert_have_no_part_in_the_gradient(mb, score, renorm
     ref = route.backward(to_np(dev), ids.cpu().numpy(), to_np(torch.where(none, 0.0, dw)), score, renorm)
     # (E + 12 roundings of 2^-24 of terms below 8, and half a step of the type)
     assert np.all(np.abs(to_np(want) - ref) <= (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * np.abs(ref) + (E + 12) * 8 * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [5, 40, 200])
+def test_gradient_of_an_expert_named_twice(mb, E, score, renorm, dtype):
+    """Ids of a caller's own, some experts in two slots and more: each slot adds its share."""
+    import torch
+    T, k = 70, 5
+    rng = np.random.default_rng(E)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    dev = torch.from_numpy(rng.normal(0, 1, (T, E)).astype(np.float32)).to(dt).cuda()
+    ids = rng.integers(0, min(E, 4), (T, k)).astype(np.int32)
+    dw = rng.normal(0, 1, (T, k)).astype(np.float32)
+    got = torch.full_like(dev, float("nan"))
+    mb.MoeRouter(T, E, k, score, renorm=renorm, dtype=dtype).route_backward(dev, torch.from_numpy(ids).cuda(), torch.from_numpy(dw).cuda(), got)
+    ref = route.backward(to_np(dev), ids, dw, score, renorm)
+    # terms: |dw| and their mean, at most 5 slots of them, over S >= s of the expert: below 64; E + 12 roundings of 2^-24, and
+    # half a step of the type
+    assert np.all(np.abs(to_np(got) - ref) <= (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * np.abs(ref) + (E + 12) * 64 * 2.0 ** -24)
