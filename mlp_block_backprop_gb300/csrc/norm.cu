@@ -238,15 +238,19 @@ __device__ __forceinline__ void refined_root(float hi, float lo, float width, fl
     rh = __fadd_rn(y, c);
     rl = c - __fsub_rn(rh, y);
 }
+// The same of a mean below 2^-80, times 2^60: 1 / mean leaves float32's range, and lo is not small beside hi.
+__device__ __noinline__ float2 tiny_root(float hi, float lo, float width, float inv_width, float eps) {
+    float mh, rh, rl;
+    const float h = __fadd_rn(hi, lo);
+    refined_root(h * 0x1p60f, __fsub_rn(lo, __fsub_rn(h, hi)) * 0x1p60f, width, inv_width, eps * 0x1p60f, mh, rh, rl);
+    return mh == 0.0f ? make_float2(INFINITY, 0.0f) : make_float2(rh * 0x1p30f, rl * 0x1p30f);   // (eps = 0 and a row of zeros)
+}
 __device__ __forceinline__ void inverse_root(float hi, float lo, float width, float inv_width, float eps, float &rh, float &rl) {
     float mh;
     refined_root(hi, lo, width, inv_width, eps, mh, rh, rl);
     if (mh < 0x1p-80f) {
-        // once more times 2^60: 1 / mean leaves float32's range, and lo is not small beside hi
-        const float h = __fadd_rn(hi, lo);
-        refined_root(h * 0x1p60f, __fsub_rn(lo, __fsub_rn(h, hi)) * 0x1p60f, width, inv_width, eps * 0x1p60f, mh, rh, rl);
-        rh *= 0x1p30f, rl *= 0x1p30f;
-        if (mh == 0.0f) rh = INFINITY, rl = 0.0f;      // eps = 0 and a row of zeros
+        const float2 r = tiny_root(hi, lo, width, inv_width, eps);
+        rh = r.x, rl = r.y;
     }
     if (!(hi < INFINITY)) rh = NAN, rl = 0.0f;         // an infinity or a NaN in the row
 }
