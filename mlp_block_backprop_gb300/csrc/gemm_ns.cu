@@ -418,8 +418,8 @@ __device__ __forceinline__ void ns_accumulators(uint32_t at, float (&v)[32]) { t
 
 // ------------------------------------------------------------------- ns_small
 
-// SPLIT: K is split over a cluster; the parts meet in `dump`, and a CTA finishes some of the
-// tile's rows, 16 neighbouring threads a row, straight from and to global memory.  No mirror images there:
+// SPLIT (G alone): K is split over a cluster; the parts meet in `dump`, and a CTA finishes some of the
+// tile's rows, 16 neighbouring threads a row, straight to global memory.  No mirror images there:
 // a split is for products that leave SMs idle, so every tile is computed.
 template <bool SPLIT_, int BN_ = 128>
 struct NsSmall {
@@ -445,51 +445,13 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t cluster_addr) {
     return v;
 }
 
-// Eight columns from col on of a row, whose sums are v: the split kernel's epilogue.
-template <int OP>
-__device__ __forceinline__ void ns_finish_eight(const NsArgs &a, const NsTile &w, int row, int col, const uint4 &x, const uint4 &y, float (&v)[8]) {
+// Eight columns from col on of a row of G, whose sums are v: the split kernel's epilogue.
+__device__ __forceinline__ void ns_finish_eight(const NsArgs &a, const NsTile &w, int row, int col, const float (&v)[8]) {
     if (row >= a.rows || col >= a.cols) return;
-    const int64_t at = w.batch * a.matrix + static_cast<int64_t>(row) * a.pitch + col;
-    const int64_t dat = static_cast<int64_t>(w.batch) * a.diag_pitch;
-    const float d = kNsScaled<OP> && !a.diag_col ? __ldcg(a.diag + dat + row) : 0.0f;
-    const float *by_col = OP == kNsJoin ? a.diag2 : (OP == kNsUpdate && a.diag_col ? a.diag : nullptr);
-    float4 c0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), c1 = c0;
-    if (kNsTwo<OP> && by_col) {
-        c0 = __ldcg(reinterpret_cast<const float4 *>(by_col + dat + col));
-        c1 = __ldcg(reinterpret_cast<const float4 *>(by_col + dat + col + 4));
-    }
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-    const float2 cs[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 r = ns_combine<OP>(a, make_float2(v[2 * i], v[2 * i + 1]), unpack_half2(xs[i]), unpack_half2(ys[i]), d, cs[i], row, col + 2 * i);
-        v[2 * i] = r.x;
-        v[2 * i + 1] = r.y;
-        const bool d0 = OP == kNsJoin && col + 2 * i == row, d1 = OP == kNsJoin && col + 2 * i + 1 == row;
-        h[i] = pack_half2(d0 ? 0.0f : r.x, d1 ? 0.0f : r.y);
-        const float2 p = unpack_half2(h[i]);
-        l[i] = pack_half2(r.x - p.x, r.y - p.y);
-        if (OP == kNsSquare || OP == kNsJoin) {
-            if (col + 2 * i == row) a.diag_out[dat + row] = r.x - p.x;
-            if (col + 2 * i + 1 == row) a.diag_out[dat + row] = r.y - p.y;
-        }
-    }
-    if (OP == kNsUpdate && a.o) {
-        uint16_t *o = a.o + (static_cast<int64_t>(w.batch) * a.rows + row) * a.cols + col;
-        if (a.o_tma) {
-            *reinterpret_cast<uint4 *>(o) = make_uint4(pack_bf16x2(a.alpha * v[0], a.alpha * v[1]), pack_bf16x2(a.alpha * v[2], a.alpha * v[3]),
-                                                       pack_bf16x2(a.alpha * v[4], a.alpha * v[5]), pack_bf16x2(a.alpha * v[6], a.alpha * v[7]));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (col + i < a.cols) o[i] = static_cast<uint16_t>(pack_bf16x2(a.alpha * v[i], 0.0f) & 0xFFFFu);
-        }
-        return;
-    }
     // (the pitch is a multiple of 64: what lies behind the last column is nobody's)
-    *reinterpret_cast<uint4 *>(a.out + at) = make_uint4(h[0], h[1], h[2], h[3]);
-    if (OP == kNsUpdate && a.out_lo) *reinterpret_cast<uint4 *>(a.out_lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+    *reinterpret_cast<uint4 *>(a.out + w.batch * a.matrix + static_cast<int64_t>(row) * a.pitch + col) =
+        make_uint4(pack_half2(a.alpha * v[0], a.alpha * v[1]), pack_half2(a.alpha * v[2], a.alpha * v[3]), pack_half2(a.alpha * v[4], a.alpha * v[5]),
+                   pack_half2(a.alpha * v[6], a.alpha * v[7]));
 }
 
 template <class C, int OP, bool AMN, bool BMN>
@@ -497,6 +459,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const __grid_constant__ NsMaps maps, const NsArgs args) {
     constexpr bool SYM = OP != kNsUpdate && !C::SPLIT && C::BN == 128;
     constexpr int S = C::kStages, BN = C::BN;
+    static_assert(!C::SPLIT || OP == kNsGram, "the cluster's sum");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *a_s = smem, *b_s = a_s + S * C::kABytes;
@@ -656,18 +619,7 @@ ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         for (; t < args.tiles; next(), ++it) {
             const bool some = k1 > k0;
             const int buf = it & 1;
-            // the first rows' tiles, ahead of the sums
             const int r0 = tid >> 4, c0 = (tid & 15) * 8;
-            uint4 x = make_uint4(0, 0, 0, 0), y = x;
-            auto fetch = [&](int r) {
-                const int row = w.m0 + first + r, col = w.n0 + c0;
-                if (kNsOne<OP> && row < args.rows && col < args.cols) {
-                    const int64_t at = w.batch * args.matrix + static_cast<int64_t>(row) * args.pitch + col;
-                    x = *reinterpret_cast<const uint4 *>(args.aux + at);
-                    if (kNsTwo<OP> && args.aux2) y = *reinterpret_cast<const uint4 *>(args.aux2 + at);
-                }
-            };
-            fetch(r0);
             bool ok = mbar_wait(&accf_bar[buf], (it >> 1) & 1, abort_flag);
             tc_fence_after_sync();
             ok = mbar_wait_cluster(part_empty, (it & 1) ^ 1u, abort_flag) && ok;
@@ -702,8 +654,7 @@ ns_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         sum[0] += p.x; sum[1] += p.y; sum[2] += p.z; sum[3] += p.w;
                         sum[4] += u.x; sum[5] += u.y; sum[6] += u.z; sum[7] += u.w;
                     }
-                    if (r != r0) fetch(r);
-                    ns_finish_eight<OP>(args, w, w.m0 + first + r, w.n0 + c0, x, y, sum);
+                    ns_finish_eight(args, w, w.m0 + first + r, w.n0 + c0, sum);
                 }
             }
             named_barrier_sync(1, kEpiThreads);
@@ -1293,24 +1244,27 @@ int run_ns(NsArgs a, const NsOperand &A, const NsOperand &B, int batch, int sms,
     a.mt = (a.rows + 127) / 128;
     a.nt = (a.cols + 127) / 128;
     a.group_m = 8;
-    const int64_t every = static_cast<int64_t>(a.mt) * a.nt * batch;   // a split computes the images too
-    // K is split where that saves more than the cluster's sum costs: a stage takes 0.155 us with
-    // few CTAs at work, the sum some 5.5 and 0.3 a part (X X^T of 256 x 8192: 27.2 us whole, 22.4, 17.9 and 18.0
-    // in two, four and eight; of 512 x 2048: 13.0, 14.3, 14.3, 25.6).  Clusters of eight find room on some two thirds
-    // of the SMs at once (500 x 16000, sixteen tiles: 31 us in eight, 19.5 in four).
-    int split = 1;
-    double best = 0.155 * a.kblocks;
-    for (int k = 2; k <= 8; k *= 2) {
-        const double cost = 0.155 * a.kblocks / k + 5.5 + 0.3 * k;
-        if (every * k <= (k == 8 ? sms * 2 / 3 : sms * 5 / 6) && a.kblocks >= 2 * k && cost < best) best = cost, split = k;
-    }
-    if (split > 1) {
-        a.per = a.mt * a.nt;
-        a.tiles = static_cast<int>(every);
-        if (!operands(128)) return MLPBLK_ECUDA;
-        static int attr_set[64] = {0};
-        return launch_ns(ns_small_kernel<NsSmall<true>, OP, AMN, BMN>, NsSmall<true>::kThreads, NsSmall<true>::kSmemBytes, a.tiles * split,
-                         split, mA, mB, maps, a, attr_set, s);
+    if constexpr (OP == kNsGram) {
+        const int64_t every = static_cast<int64_t>(a.mt) * a.nt * batch;   // a split computes the images too
+        // K is split where that saves more than the cluster's sum costs: a stage takes 0.155 us with
+        // few CTAs at work, the sum some 5.5 and 0.3 a part (X X^T of 256 x 8192: 27.2 us whole, 22.4, 17.9 and 18.0
+        // in two, four and eight; of 512 x 2048: 13.0, 14.3, 14.3, 25.6).  Clusters of eight find room on some two thirds
+        // of the SMs at once (500 x 16000, sixteen tiles: 31 us in eight, 19.5 in four).  The other products' K is the
+        // short side: where it has the 58 stages that this takes, there are hundreds of tiles.
+        int split = 1;
+        double best = 0.155 * a.kblocks;
+        for (int k = 2; k <= 8; k *= 2) {
+            const double cost = 0.155 * a.kblocks / k + 5.5 + 0.3 * k;
+            if (every * k <= (k == 8 ? sms * 2 / 3 : sms * 5 / 6) && a.kblocks >= 2 * k && cost < best) best = cost, split = k;
+        }
+        if (split > 1) {
+            a.per = a.mt * a.nt;
+            a.tiles = static_cast<int>(every);
+            if (!operands(128)) return MLPBLK_ECUDA;
+            static int attr_set[64] = {0};
+            return launch_ns(ns_small_kernel<NsSmall<true>, OP, AMN, BMN>, NsSmall<true>::kThreads, NsSmall<true>::kSmemBytes, a.tiles * split,
+                             split, mA, mB, maps, a, attr_set, s);
+        }
     }
     // Tiles of 64 columns where they fit in one round: half the MMAs and half the epilogue of each (five
     // steps of 512 x 512 65 us, 97 by 128 columns; 250 x 2000 76 and 104).
