@@ -614,7 +614,7 @@ int mlpblk_fp4_product_kernel(const mlpblk_fp4_matmul_desc *desc, int form, int 
  *   routing_weights[t,j] = scale * s, or with desc->renorm scale * s / (sum_j s + 1e-20); 0
  *                          beside -1
  * A logit of -infinity or NaN closes its expert to the token; +infinity counts as the largest
- * finite value.  A row whose experts are all closed selects nothing.  The order is that of
+ * finite float32 (of bf16 logits, too).  A row whose experts are all closed selects nothing.  The order is that of
  * the scores in float64 (without a bias, of the logits), whatever the arithmetic here:
  * float32 keys that are too close to call are computed again.  A bias of -infinity or NaN
  * closes its expert to selection, whose share of the softmax stays; one of +infinity puts it first.

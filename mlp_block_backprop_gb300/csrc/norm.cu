@@ -13,7 +13,10 @@
 // One pass: a row stays in registers between its sums and its outputs, and the next row is
 // already on its way.  max |s gamma| needs no r, so both reductions of a row are one.  Forward bound by HBM
 // where there is a residual branch (16384 x 4096 bf16 74 us, 6.4 TB/s of 7 bytes an element) and by instruction
-// issue without one (60 us), backward by HBM (86 us, 6.2 TB/s of 8 bytes).
+// issue without one (61 us), backward by HBM (84 us, 6.4 TB/s of 8 bytes).
+//
+// Order of the gradient's products: r alone may be 2^-60 or, with a small eps, 2^60 and more, and its square or cube
+// leaves float32's range; s r and the products with it do not.
 //
 // Codes are those of the real number n / scale, rounded once: values half way between two codes
 // are common (one in 1700 here: ratios of two short products), and which way they go is decided
