@@ -537,7 +537,7 @@ route_kernel(const RouteArgs a) {
                     const int g = g0 + sub;
                     const bool on = g < a.groups && group_kept(marks, a.per, a.groups, a.top_groups, g);
                     if (g < a.groups) {
-                        const float x = marks[g * a.per], off = a.per > 1 ? marks[g * a.per + 1] : mark_off(x, -INFINITY, x);
+                        const float x = marks[g * a.per], off = a.per > 1 ? marks[g * a.per + 1] : mark_off(2.0f * x, -INFINITY, x);
                         if (on) low = fminf(low, x - off);
                         else high = fmaxf(high, x + off);
                     }

@@ -127,3 +127,20 @@ def test_gradient_of_an_expert_named_twice(mb, E, score, renorm, dtype):
     # terms: |dw| and their mean, at most 5 slots of them, over S >= s of the expert: below 64; E + 12 roundings of 2^-24, and
     # half a step of the type
     assert np.all(np.abs(to_np(got) - ref) <= (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * np.abs(ref) + (E + 12) * 64 * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,top_groups", [(16, 5), (64, 10), (9, 4)])
+@pytest.mark.parametrize("size", [0.0, 10.0, 1e4])
+def test_groups_of_one_expert(mb, E, top_groups, size, score):
+    """A mark is half its only key; a common bias of `size` leaves the scores their last bits."""
+    import torch
+    T, k = 20000, 4
+    rng = np.random.default_rng(E)
+    l = rng.normal(0, 0.1, (T, E)).astype(np.float32)
+    bias = np.full(E, size, dtype=np.float32)
+    ids, w = torch.full((T, k), 77, dtype=torch.int32, device="cuda"), torch.full((T, k), 77.0, device="cuda")
+    mb.MoeRouter(T, E, k, score, E, top_groups, dtype="f32").route(torch.from_numpy(l).cuda(), ids, w, bias=torch.from_numpy(bias).cuda())
+    # (the k best of the best groups are the k best)
+    ref = _select(l, k, score, bias, 1, 1)
+    np.testing.assert_array_equal(ids.cpu().numpy(), ref)
