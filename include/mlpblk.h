@@ -728,8 +728,9 @@ int mlpblk_add_rmsnorm_backward(const mlpblk_norm_desc *desc, const void *dn, co
  * bf16 (X in muon_step), is
  *   up to 3e-3 where u's entries round independently (noise, low rank, strong directions or a large entry over noise) and
  *   its short side is 64 or more, mostly 1e-3 to 2e-3; up to 6e-3 for short sides from 12 on, up to 2e-2 below;
- *   up to 2e-2 at any size where they round alike: few entries that are not zero, multiples of the identity or of a
- *   permutation (mostly 1e-3 to 5e-3), a constant or nearly equal rows over noise of 1e-3 of them or less.
+ *   up to 2e-2 at any size where roundings agree: few entries that are not zero, an orthogonal u (dense ones 1e-3 to 4e-3,
+ *   multiples of the identity or of a permutation mostly 1e-3 to 5e-3), a constant or nearly equal rows over noise of 1e-3
+ *   of them or less.
  * The matrices b G + c G^2 are fp16 too: every singular
  * value s on the way must keep |b s^2 + c s^4| and, of two neighbouring steps, |a a'| below 60000
  * (with those coefficients s < 13).  A NaN or an
